@@ -20,6 +20,8 @@ GDN_F32, GDN_BF16, GDN_F16 = 0, 1, 2
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_ARG", 2: "GDN_ERR_SLOT", 3: "GDN_ERR_DUP_SLOT",
           4: "GDN_ERR_DTYPE", 5: "GDN_ERR_SIZE", 6: "GDN_ERR_UNSUPPORTED", 7: "GDN_ERR_CUDA"}
 DEVERR_SLOT, DEVERR_SEQ, DEVERR_COUNT, DEVERR_TIMEOUT = 1, 2, 4, 8
+DEVERR_PAGE, DEVERR_VALUE = 16, 32
+GDN_KV_I8, GDN_KV_E4M3 = 0, 1
 TEST_DECODE_WAIT_TIMEOUT = 1
 
 EXPORTED = ("gdn_pool_state_bytes", "gdn_pool_conv_bytes", "gdn_pool_create", "gdn_pool_reset",
@@ -30,6 +32,8 @@ EXPORTED = ("gdn_pool_state_bytes", "gdn_pool_conv_bytes", "gdn_pool_create", "g
             "gdn_in_proj",
             "gdn_prefill_chunked", "gdn_prefill_recurrent", "gdn_spec_verify",
             "gdn_spec_verify_deferred", "gdn_prefill_chunked_noalloc", "gdn_prefill_chunked_ckpt",
+            "gdn_kv_code_bytes", "gdn_kv_scale_bytes", "gdn_kv_create", "gdn_kv_destroy",
+            "gdn_kv_get_error", "gdn_kv_append", "gdn_kv_read", "gdn_kv_attend",
             "gdn_status_string",
             "gdn_last_error_message")
 
@@ -54,6 +58,14 @@ class gdn_qkv(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("g", ctypes.c_void_p), ("beta", ctypes.c_void_p),
                 ("ld_qk", ctypes.c_int64), ("ld_v", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class gdn_kv_desc(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("h_q", ctypes.c_int32),
+                ("h_kv", ctypes.c_int32), ("d", ctypes.c_int32), ("code", ctypes.c_int),
+                ("host_checks", ctypes.c_int32)]
 
 
 _lib = None
@@ -100,6 +112,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                              ctypes.c_float, vp]),
         "gdn_prefill_chunked_ckpt": (st, [vp, i32, vp, vp, i32, i32, i32, P(gdn_qkv), vp, st,
                                           ctypes.c_float, vp, i32, i32, vp]),
+        "gdn_kv_code_bytes": (ctypes.c_size_t, [P(gdn_kv_desc)]),
+        "gdn_kv_scale_bytes": (ctypes.c_size_t, [P(gdn_kv_desc)]),
+        "gdn_kv_create": (st, [P(gdn_kv_desc), vp, vp, ctypes.c_size_t, vp, vp, ctypes.c_size_t,
+                               vp, P(vp)]),
+        "gdn_kv_destroy": (st, [vp]),
+        "gdn_kv_get_error": (st, [vp, P(ctypes.c_uint32)]),
+        "gdn_kv_append": (st, [vp, i32, vp, vp, vp, i32, i32, i32, vp, i64, vp, i64, st, vp]),
+        "gdn_kv_read": (st, [vp, i32, vp, vp, vp, i32, i32, i32, vp, i64, vp, i64, st, vp]),
+        "gdn_kv_attend": (st, [vp, i32, vp, vp, vp, i32, i32, i32, i32, vp, i64, st, vp, i64, st,
+                               ctypes.c_float, vp]),
         "gdn_status_string": (ctypes.c_char_p, [st]),
         "gdn_last_error_message": (ctypes.c_char_p, []),
     }
@@ -461,4 +483,163 @@ def gdn_prefill_chunked_ckpt(pool: Pool, layer: int, slot_ids: torch.Tensor,
         slot_ids.numel(), q.shape[0], max_seqlen, ctypes.byref(inp), _ptr(o), _dt(o), scale,
         _idx(ckpt_slots.contiguous(), "ckpt_slots"), ckpt_slots.shape[1], ckpt_every,
         _stream(stream)))
+    return o
+
+
+# ------------------------------------------------------- 8-bit paged KV cache
+
+_KV_CODES = {torch.int8: GDN_KV_I8, torch.float8_e4m3fn: GDN_KV_E4M3}
+
+
+class KVCache:
+    """A handle on an 8-bit paged KV cache plus the torch tensors that hold it:
+    k, v [n_layers, n_pages, h_kv, page_tokens, d] codes (int8 or
+    float8_e4m3fn), k_scale, v_scale [n_layers, n_pages, h_kv] float32 powers
+    of two (value = code * scale) and page_table [n_slots, max_pages] int32,
+    which the caller fills with page ids.  See gdn.h for the layout's rules."""
+
+    def __init__(self, k, v, k_scale, v_scale, page_table, h_q, host_checks=True):
+        if k.dtype not in _KV_CODES:
+            raise GDNError(4, f"unsupported code type {k.dtype}")
+        if k.dim() != 5 or v.shape != k.shape or v.dtype != k.dtype:
+            raise GDNError(5, "k and v must share one shape [n_layers, n_pages, h_kv, "
+                              "page_tokens, d] and type")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.dtype != torch.float32 or t.shape != k.shape[:3]:
+                raise GDNError(5, f"{name} must be float32 {tuple(k.shape[:3])}")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2:
+            raise GDNError(1, "page_table must be int32 [n_slots, max_pages]")
+        for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale),
+                        ("page_table", page_table)):
+            if not t.is_contiguous() or t.device != k.device:
+                raise GDNError(1, f"{name} must be contiguous and on k's device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_table = page_table
+        self.desc = gdn_kv_desc(k.shape[0], page_table.shape[0], k.shape[1], page_table.shape[1],
+                                k.shape[3], h_q, k.shape[2], k.shape[4], _KV_CODES[k.dtype],
+                                1 if host_checks else 0)
+        self.handle = gdn_kv_create(self.desc, k, v, k_scale, v_scale, page_table)
+
+    @classmethod
+    def empty(cls, n_layers, n_slots, n_pages, max_pages, page_tokens, h_q, h_kv, d,
+              code=torch.int8, host_checks=True, device="cuda"):
+        """A cache in new memory.  The page table starts at -1 (no page)."""
+        shape = (n_layers, n_pages, h_kv, page_tokens, d)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(code) for _ in range(2))
+        ks, vs = (torch.zeros(shape[:3], device=device) for _ in range(2))
+        table = torch.full((n_slots, max_pages), -1, dtype=torch.int32, device=device)
+        return cls(k, v, ks, vs, table, h_q, host_checks)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            gdn_kv_destroy(self)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def gdn_kv_code_bytes(desc: gdn_kv_desc) -> int:
+    return load_library().gdn_kv_code_bytes(ctypes.byref(desc))
+
+
+def gdn_kv_scale_bytes(desc: gdn_kv_desc) -> int:
+    return load_library().gdn_kv_scale_bytes(ctypes.byref(desc))
+
+
+def gdn_kv_create(desc: gdn_kv_desc, k, v, k_scale, v_scale, page_table):
+    out = ctypes.c_void_p()
+    _check(load_library().gdn_kv_create(
+        ctypes.byref(desc), _ptr(k), _ptr(v), k.numel() * k.element_size(), _ptr(k_scale),
+        _ptr(v_scale), k_scale.numel() * 4, _ptr(page_table), ctypes.byref(out)))
+    return out
+
+
+def gdn_kv_destroy(kv: KVCache):
+    _check(load_library().gdn_kv_destroy(kv.handle))
+
+
+def gdn_kv_get_error(kv: KVCache) -> int:
+    err = ctypes.c_uint32(0)
+    _check(load_library().gdn_kv_get_error(kv.handle, ctypes.byref(err)))
+    return err.value
+
+
+def _kv_index(slot_ids, starts, cu_seqlens, tokens, name):
+    n = slot_ids.numel()
+    if starts.numel() != n or (n + 1 != cu_seqlens.numel() if cu_seqlens is not None
+                               else tokens != n):
+        raise GDNError(5, f"{name} must have an entry per slot id, cu_seqlens one more "
+                          "(without it: one token per slot)")
+    return (_idx(slot_ids, "slot_ids"), _idx(starts, name), _idx(cu_seqlens, "cu_seqlens"), n,
+            tokens)
+
+
+def _kv_rows(kv, slot_ids, pos, k, v, cu_seqlens, max_seqlen):
+    d = kv.desc
+    some = k if k is not None else v
+    if some is None:
+        raise GDNError(1, "k and v are both None")
+    if k is not None and v is not None and (k.dtype != v.dtype or k.shape[0] != v.shape[0]):
+        raise GDNError(4, "k and v must share one dtype and token count")
+    tokens = some.shape[0]
+    idx = _kv_index(slot_ids, pos, cu_seqlens, tokens, "pos")
+    ld_k = 0 if k is None else _token_rows(k, d.h_kv, d.d, "k")
+    ld_v = 0 if v is None else _token_rows(v, d.h_kv, d.d, "v")
+    if tokens <= 1:  # the stride of a single row says nothing
+        ld_k = ld_v = 0
+    if max_seqlen <= 0:
+        max_seqlen = 1 if cu_seqlens is None else tokens
+    return (*idx, max_seqlen, _ptr(k), ld_k, _ptr(v), ld_v, _dt(some))
+
+
+def gdn_kv_append(kv: KVCache, layer: int, slot_ids: torch.Tensor, pos: torch.Tensor,
+                  k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                  max_seqlen: int = 0, stream=None):
+    """Quantise k, v [tokens, h_kv, d] (float32 or bf16; the token stride may
+    exceed h_kv * d) into positions pos[i], pos[i] + 1, ... of slot slot_ids[i]."""
+    if k is None or v is None:
+        raise GDNError(1, "k and v are both needed")
+    _check(load_library().gdn_kv_append(
+        kv.handle, layer, *_kv_rows(kv, slot_ids, pos, k, v, cu_seqlens, max_seqlen),
+        _stream(stream)))
+
+
+def gdn_kv_read(kv: KVCache, layer: int, slot_ids: torch.Tensor, pos: torch.Tensor,
+                k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+                cu_seqlens: Optional[torch.Tensor] = None, max_seqlen: int = 0, stream=None):
+    """Read cached tokens back as values into k, v [tokens, h_kv, d] (either may be None)."""
+    _check(load_library().gdn_kv_read(
+        kv.handle, layer, *_kv_rows(kv, slot_ids, pos, k, v, cu_seqlens, max_seqlen),
+        _stream(stream)))
+    return k, v
+
+
+def gdn_kv_attend(kv: KVCache, layer: int, slot_ids: torch.Tensor, kv_lens: torch.Tensor,
+                  q: torch.Tensor, o: Optional[torch.Tensor] = None,
+                  cu_seqlens: Optional[torch.Tensor] = None, max_seqlen: int = 0,
+                  max_kv_len: int = 0, scale: Optional[float] = None, stream=None):
+    """Causal attention of q [tokens, h_q, d] over the slots' cached tokens;
+    kv_lens counts the query tokens themselves (append them first).  o
+    [tokens, h_q, d] (default: q's type); scale defaults to d ** -0.5."""
+    d = kv.desc
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if o.shape != q.shape:
+        raise GDNError(5, f"o must have q's shape {tuple(q.shape)}")
+    tokens = q.shape[0]
+    idx = _kv_index(slot_ids, kv_lens, cu_seqlens, tokens, "kv_lens")
+    ld_q, ld_o = _token_rows(q, d.h_q, d.d, "q"), _token_rows(o, d.h_q, d.d, "o")
+    if tokens <= 1:
+        ld_q = ld_o = 0
+    if max_seqlen <= 0:
+        max_seqlen = 1 if cu_seqlens is None else tokens
+    if max_kv_len <= 0:
+        max_kv_len = d.max_pages * d.page_tokens
+    _check(load_library().gdn_kv_attend(
+        kv.handle, layer, *idx, max_seqlen, max_kv_len, _ptr(q), ld_q, _dt(q), _ptr(o), ld_o,
+        _dt(o), d.d ** -0.5 if scale is None else scale, _stream(stream)))
     return o

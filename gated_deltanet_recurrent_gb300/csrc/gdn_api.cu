@@ -202,6 +202,10 @@ bool encode_state_map(gdn_pool *p) {
 
 }  // namespace
 
+namespace gdn {
+void set_last_message(const char *msg) { g_last_msg = msg; }
+}  // namespace gdn
+
 extern "C" {
 
 const char *gdn_status_string(gdn_status s) {

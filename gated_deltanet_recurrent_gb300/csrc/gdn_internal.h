@@ -181,4 +181,48 @@ cudaError_t launch_prefill(const PoolView &p, int layer, const SeqIndex &seq, co
                            void *o, gdn_dtype o_dtype, float scale, void *work,
                            cudaStream_t s);
 
+// ---- 8-bit paged KV cache ----
+struct KVView {
+  uint8_t *k, *v;              // codes [n_layers][n_pages][h_kv][page_tokens][d]
+  float *k_scale, *v_scale;    // [n_layers][n_pages][h_kv]
+  const int32_t *table;        // [n_slots][max_pages]
+  unsigned int *err;
+  int n_layers, n_slots, n_pages, max_pages, page_tokens, page_log2, h_q, h_kv, d;
+  gdn_kv_code code;
+  GDN_HD int64_t capacity() const { return (int64_t)max_pages * page_tokens; }
+  // index of the scale of (layer, page, head); times page_tokens * d: of its first code
+  GDN_HD int64_t block(int layer, int page, int head) const {
+    return ((int64_t)layer * n_pages + page) * h_kv + head;
+  }
+};
+
+// Token rows of the new keys and values (const in append, written in read).
+struct KVRows {
+  void *k, *v;
+  int64_t ld_k, ld_v;          // resolved (never 0)
+  gdn_dtype dtype;
+};
+
+cudaError_t launch_kv_append(const KVView &c, int layer, const SeqIndex &seq, const int32_t *pos,
+                             int max_seqlen, const KVRows &rows, cudaStream_t s);
+cudaError_t launch_kv_read(const KVView &c, int layer, const SeqIndex &seq, const int32_t *pos,
+                           int max_seqlen, const KVRows &rows, cudaStream_t s);
+
+struct KVAttendArgs {
+  SeqIndex seq;
+  const int32_t *kv_lens;
+  int max_seqlen, max_kv_len;  // hints (>= 1)
+  const void *q;
+  void *o;
+  int64_t ld_q, ld_o;          // resolved (never 0)
+  gdn_dtype q_dtype, o_dtype;
+  float scale;
+};
+
+cudaError_t launch_kv_attend(const KVView &c, int layer, const KVAttendArgs &a, int sm_count,
+                             cudaMemPool_t work_pool, cudaStream_t s);
+
+// Detail text of the last failure on this host thread (gdn_last_error_message).
+void set_last_message(const char *msg);
+
 }  // namespace gdn

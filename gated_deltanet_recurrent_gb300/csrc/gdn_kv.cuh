@@ -1,0 +1,82 @@
+// Device helpers of the 8-bit KV cache: scales that are powers of two, and
+// codes (int8, or e4m3 floats) to and from float32 and binary16.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "gdn_common.cuh"
+
+namespace gdn {
+namespace kv {
+
+template <int CODE>
+struct Code;  // top code, exponent range of the scale, conversions
+
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // -126..127
+
+// binary16 pairs of two e4m3 codes (exact)
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+
+template <>
+struct Code<GDN_KV_I8> {
+  static constexpr int kMaxExp = 120;
+  // the least e with amax <= 127 * 2^e, in [-100, 120]; amax is finite and >= 0.  With
+  // amax = 1.f * 2^(E-127), 127 * 2^(E-133) = 1.984375 * 2^(E-127) covers it unless 1.f is larger.
+  static __device__ __forceinline__ int exponent(float amax) {
+    const uint32_t b = __float_as_uint(amax);
+    const int e = (int)(b >> 23) - 133 + ((b & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+    return min(max(e, -100), kMaxExp);
+  }
+  // y is not NaN
+  static __device__ __forceinline__ uint32_t encode(float y) {
+    return (uint32_t)__float2int_rn(fminf(fmaxf(y, -127.f), 127.f)) & 0xffu;
+  }
+  static __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    return encode(a) | encode(b) << 8 | encode(c) << 16 | encode(d) << 24;
+  }
+  static __device__ __forceinline__ float4 decode4(uint32_t w) {
+    return make_float4((float)(int8_t)(w & 0xff), (float)(int8_t)(w >> 8 & 0xff),
+                       (float)(int8_t)(w >> 16 & 0xff), (float)(int8_t)(w >> 24));
+  }
+};
+
+template <>
+struct Code<GDN_KV_E4M3> {
+  static constexpr int kMaxExp = 118;
+  // the least e with amax <= 448 * 2^e = 1.75 * 2^(e+8), in [-100, 118]
+  static __device__ __forceinline__ int exponent(float amax) {
+    const uint32_t b = __float_as_uint(amax);
+    const int e = (int)(b >> 23) - 135 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return min(max(e, -100), kMaxExp);
+  }
+  static __device__ __forceinline__ uint32_t encode2(float a, float b) {
+    uint16_t r;  // the second operand is the low byte
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    return encode2(a, b) | encode2(c, d) << 16;
+  }
+  static __device__ __forceinline__ float4 decode4(uint32_t w) {
+    const uint32_t lo = e4m3x2_to_half2((uint16_t)(w & 0xffff)), hi = e4m3x2_to_half2((uint16_t)(w >> 16));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+};
+
+// The exponent of a stored scale: a power of two in the codes' range.  Anything
+// else, as in a page that was never written, is brought into it; what is no
+// positive finite number counts as the smallest.
+template <int CODE>
+__device__ __forceinline__ int scale_exponent(float s) {
+  const int e = (int)(__float_as_uint(s) >> 23) - 127;  // sign bit set: e > 128
+  return e >= 128 ? -100 : min(max(e, -100), Code<CODE>::kMaxExp);
+}
+
+}  // namespace kv
+}  // namespace gdn

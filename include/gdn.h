@@ -78,6 +78,10 @@ typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_F16 = 2 } gdn_dtype;
 #define GDN_DEVERR_COUNT 4u  /* an advance/accept_len outside [0, length] was clamped */
 #define GDN_DEVERR_TIMEOUT 8u /* a bounded wait on an asynchronous copy gave up; outputs of
                                  that CTA are missing (never expected; reported, not hung) */
+#define GDN_DEVERR_PAGE 16u  /* a page table entry in use is outside [0, n_pages): its tokens were
+                                neither written nor read, and are masked in gdn_kv_attend */
+#define GDN_DEVERR_VALUE 32u /* a non-finite key or value was appended: an infinity was stored as
+                                the largest code of its sign, a NaN as zero */
 
 /* Shape of every GDN layer in the pool.  Supported: dk in {16, 32, 64, 128},
  * dv a multiple of 4 (<= 4096), h_v a multiple of h_k, 2 <= conv_k <= 8,
@@ -398,6 +402,119 @@ gdn_status gdn_prefill_chunked_noalloc(gdn_pool *pool, int32_t layer, const int3
                                        int32_t total_tokens, int32_t max_seqlen,
                                        const gdn_qkv *in, void *o, gdn_dtype o_dtype, float scale,
                                        gdn_stream stream);
+
+/* ---- 8-bit paged KV cache ----
+ *
+ * The attention layers that stand between the recurrent ones keep the keys
+ * and values of every token; this is their per-request memory, indexed by the
+ * same slot ids as the pool (the source pages describe hybrid models but no
+ * KV cache; this part has no counterpart on them).  Memory is pages of
+ * page_tokens tokens.  A page holds, per layer, KV head and side (K or V), a
+ * block of 8-bit codes and one float32 scale, a power of two:
+ *     value = code * scale,
+ *   k_codes, v_codes  [n_layers][n_pages][h_kv][page_tokens][d]  one byte each
+ *   k_scale, v_scale  [n_layers][n_pages][h_kv]                  float32
+ *   page_table        [n_slots][max_pages]                       int32
+ * Token position p of a slot is row p % page_tokens of page
+ * page_table[slot][p / page_tokens], in every layer.  All five are plain
+ * caller memory: the caller hands out pages by writing the page table (on the
+ * stream, before the calls that use it), may let slots share pages that none
+ * of them appends to, and keeps each slot's length itself.  Nothing has to be
+ * cleared before use.
+ *
+ * The scale of a block is 2^e with the least e such that every finite
+ * magnitude in it is <= top * 2^e, top = 127 (GDN_KV_I8) or 448
+ * (GDN_KV_E4M3), -100 <= e <= 120 (I8) or 118 (E4M3); larger magnitudes are
+ * stored as the top code.  A code is value / scale rounded to nearest even.
+ * Powers of two make value / scale, code * scale and a change of scale exact
+ * up to that one rounding, in float32 and in bf16. */
+typedef enum { GDN_KV_I8 = 0, GDN_KV_E4M3 = 1 } gdn_kv_code;
+
+/* Supported: d in {64, 128, 256}, page_tokens in {16, 32, 64, 128}, h_q a
+ * multiple of h_kv. */
+typedef struct {
+  int32_t n_layers;
+  int32_t n_slots;
+  int32_t n_pages;      /* pages of the cache; a page id is valid in every layer */
+  int32_t max_pages;    /* page table entries per slot: a slot holds max_pages * page_tokens tokens */
+  int32_t page_tokens;
+  int32_t h_q;          /* query heads; query head h reads KV head h / (h_q / h_kv) */
+  int32_t h_kv;
+  int32_t d;            /* head dim of queries, keys and values */
+  gdn_kv_code code;
+  int32_t host_checks;  /* nonzero: validate index arrays on the host (syncs), as for a pool */
+} gdn_kv_desc;
+
+typedef struct gdn_kv gdn_kv;
+
+/* Bytes of k_codes (v_codes the same), and of k_scale (v_scale the same). */
+size_t gdn_kv_code_bytes(const gdn_kv_desc *desc);
+size_t gdn_kv_scale_bytes(const gdn_kv_desc *desc);
+
+/* Wrap caller memory (codes 16-byte aligned, scales and table 4-byte).  The
+ * handle allocates an error word and owns a stream-ordered memory pool for
+ * the workspace of gdn_kv_attend, kept for reuse until gdn_kv_destroy.  Every
+ * compute call below is asynchronous on its stream.  Calls on different
+ * streams may overlap if none appends to a page that another reads or
+ * appends to. */
+gdn_status gdn_kv_create(const gdn_kv_desc *desc, void *k_codes, void *v_codes,
+                         size_t code_bytes, float *k_scale, float *v_scale, size_t scale_bytes,
+                         const int32_t *page_table, gdn_kv **out);
+/* Releases the handle (caller memory is left alone); synchronises the device
+ * first.  NULL is a no-op. */
+gdn_status gdn_kv_destroy(gdn_kv *kv);
+/* As gdn_pool_get_error: waits for the device, returns and clears the word. */
+gdn_status gdn_kv_get_error(gdn_kv *kv, uint32_t *dev_err);
+
+/* Quantise new tokens into the cache.  Sequence i is tokens cu_seqlens[i] ..
+ * cu_seqlens[i+1]-1 of k and v (cu_seqlens == NULL: one token each) and goes
+ * to positions pos[i], pos[i] + 1, ... of slot slot_ids[i].  A page entered
+ * at its first row starts anew; a page entered further in keeps the rows
+ * before the entry: its scale becomes the larger of its own and the new
+ * tokens', and where that is larger the kept codes are rescaled (rounded to
+ * nearest even again).  So a sequence may be appended in pieces, and rejected
+ * drafts are overwritten by appending at their position again (the scale does
+ * not shrink until the page is entered at its first row).  Rows after the
+ * last new token keep no meaning.
+ * k, v: [total_tokens][h_kv][d] in dtype (GDN_F32 or GDN_BF16), token strides
+ * ld_k, ld_v elements (0: h_kv * d); rows 16-byte aligned.  pos: [n_seqs].
+ * max_seqlen as for gdn_conv_silu.  A sequence whose range does not fit
+ * [0, max_pages * page_tokens) is skipped (GDN_DEVERR_SEQ). */
+gdn_status gdn_kv_append(gdn_kv *kv, int32_t layer, const int32_t *slot_ids, const int32_t *pos,
+                         const int32_t *cu_seqlens, int32_t n_seqs, int32_t total_tokens,
+                         int32_t max_seqlen, const void *k, int64_t ld_k, const void *v,
+                         int64_t ld_v, gdn_dtype dtype, gdn_stream stream);
+
+/* Read cached tokens back as values: the same arguments, with k and v written
+ * (either may be NULL).  Exact in both dtypes. */
+gdn_status gdn_kv_read(gdn_kv *kv, int32_t layer, const int32_t *slot_ids, const int32_t *pos,
+                       const int32_t *cu_seqlens, int32_t n_seqs, int32_t total_tokens,
+                       int32_t max_seqlen, void *k, int64_t ld_k, void *v, int64_t ld_v,
+                       gdn_dtype dtype, gdn_stream stream);
+
+/* Causal grouped-query attention over the cache.  Sequence i holds
+ * kv_lens[i] tokens, of which its query tokens (cu_seqlens as above) are the
+ * last: with len of them, query token t sits at position
+ * p = kv_lens[i] - len + t and
+ *     o[t][h] = sum_{j <= p} w_j v_j,   w = softmax_j(scale * q[t][h] . k_j),
+ * over the cached positions j of KV head h / (h_q / h_kv).  One token a slot
+ * is a decode step, a few are drafts, many a (piece of a) prompt; append the
+ * tokens first.  A query with nothing to attend (p < 0, or all its pages
+ * invalid) gets zeros.
+ * q: [total_tokens][h_q][d] in q_dtype, o the same shape in o_dtype (GDN_F32
+ * or GDN_BF16), token strides ld_q, ld_o elements (0: h_q * d), rows 16-byte
+ * aligned; scale is finite.  Scores, softmax statistics and sums are float32;
+ * the products run on the tensor cores on the codes (exact in binary16) and
+ * on queries and weights rounded to binary16 (bf16 q: the query exactly, up
+ * to 2^-25 of its row's largest element; the weight to 2^-11), or split into
+ * two binary16 parts each (float32 q: to 2^-22).
+ * max_seqlen, max_kv_len: upper bounds of the query and cache lengths, used
+ * only to choose the kernel and size its grid (any value >= 1 is correct). */
+gdn_status gdn_kv_attend(gdn_kv *kv, int32_t layer, const int32_t *slot_ids,
+                         const int32_t *kv_lens, const int32_t *cu_seqlens, int32_t n_seqs,
+                         int32_t total_tokens, int32_t max_seqlen, int32_t max_kv_len,
+                         const void *q, int64_t ld_q, gdn_dtype q_dtype, void *o, int64_t ld_o,
+                         gdn_dtype o_dtype, float scale, gdn_stream stream);
 
 /* Human-readable name of a status, and the detail of the last failure on
  * this host thread (empty string if none). */

@@ -130,3 +130,58 @@ def test_gated_rmsnorm_argument_checks(lib, args, status):
     st = lib.gdn_gated_rmsnorm(a["rows"], a["d"], a["o"], a["o_dtype"], a["z"], a["z_dtype"],
                                a["w"], a["eps"], a["y"], a["y_dtype"], None)
     assert abi.STATUS[st] == status
+
+
+def _kv_desc(**kw):
+    d = dict(n_layers=2, n_slots=5, n_pages=7, max_pages=4, page_tokens=32, h_q=8, h_kv=2, d=64,
+             code=abi.GDN_KV_I8, host_checks=0)
+    d.update(kw)
+    return abi.gdn_kv_desc(**d)
+
+
+def test_kv_byte_sizes(lib):
+    assert abi.gdn_kv_code_bytes(_kv_desc()) == 2 * 7 * 2 * 32 * 64
+    assert abi.gdn_kv_scale_bytes(_kv_desc()) == 2 * 7 * 2 * 4
+    big = _kv_desc(n_layers=16, n_pages=100000, h_kv=8, page_tokens=128, d=256)
+    assert abi.gdn_kv_code_bytes(big) == 16 * 100000 * 8 * 128 * 256
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n_pages=0), "GDN_ERR_ARG"),
+    (dict(h_q=7), "GDN_ERR_ARG"),
+    (dict(d=96), "GDN_ERR_UNSUPPORTED"),
+    (dict(page_tokens=24), "GDN_ERR_UNSUPPORTED"),
+    (dict(max_pages=2 ** 31 - 1), "GDN_ERR_UNSUPPORTED"),
+    (dict(n_slots=70000), "GDN_ERR_UNSUPPORTED"),
+    (dict(code=2), "GDN_ERR_DTYPE"),
+])
+def test_kv_create_rejects_bad_shapes(lib, kw, status):
+    out = ctypes.c_void_p()
+    st = lib.gdn_kv_create(ctypes.byref(_kv_desc(**kw)), 0x1000, 0x2000, 1 << 50, 0x3000, 0x4000,
+                           1 << 50, 0x5000, ctypes.byref(out))
+    assert abi.STATUS[st] == status
+    assert out.value is None and lib.gdn_last_error_message().decode()
+
+
+def test_kv_create_rejects_null_small_and_misaligned(lib):
+    def create(k=0x1000, v=0x2000, cb=1 << 50, ks=0x3000, vs=0x4000, sb=1 << 50, t=0x5000,
+               desc=_kv_desc()):
+        out = ctypes.c_void_p()
+        return abi.STATUS[lib.gdn_kv_create(ctypes.byref(desc) if desc else None, k, v, cb, ks, vs,
+                                            sb, t, ctypes.byref(out))]
+    assert create(desc=None) == "GDN_ERR_ARG"
+    assert create(k=None) == create(vs=None) == create(t=None) == "GDN_ERR_ARG"
+    assert create(v=0x2008) == create(ks=0x3002) == "GDN_ERR_ARG"
+    assert create(cb=100) == create(sb=100) == "GDN_ERR_SIZE"
+
+
+def test_kv_calls_on_a_null_handle_fail_cleanly(lib):
+    assert abi.STATUS[lib.gdn_kv_append(None, 0, None, None, None, 1, 1, 1, None, 0, None, 0,
+                                        abi.GDN_BF16, None)] == "GDN_ERR_ARG"
+    assert abi.STATUS[lib.gdn_kv_read(None, 0, None, None, None, 1, 1, 1, None, 0, None, 0,
+                                      abi.GDN_BF16, None)] == "GDN_ERR_ARG"
+    assert abi.STATUS[lib.gdn_kv_attend(None, 0, None, None, None, 1, 1, 1, 1, None, 0,
+                                        abi.GDN_BF16, None, 0, abi.GDN_BF16, 1.0, None)] == \
+        "GDN_ERR_ARG"
+    assert abi.STATUS[lib.gdn_kv_get_error(None, None)] == "GDN_ERR_ARG"
+    assert lib.gdn_kv_destroy(None) == 0
