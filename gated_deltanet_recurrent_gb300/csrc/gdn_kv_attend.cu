@@ -1,127 +1,707 @@
-// Causal grouped-query attention over the 8-bit KV cache, in its plain form:
-// a warp per (query token, query head) walks the cached positions in order
-// with the running maximum and sum of the softmax, d / 32 elements of the
-// query, the key and the accumulator per lane.
+// Causal grouped-query attention over the 8-bit KV cache: single tokens,
+// drafts, and every call in float32 (the long bf16 calls go to
+// gdn_kv_prompt.cu).
+//
+// Mathematics.  With value codes c_j, V scale 2^e_j and scores x_j = scale *
+// log2(e) * q.k_j, the output is
+//     o = sum_j 2^(x_j + e_j - M) c_j / sum_j 2^(x_j - M)
+// for any M.  M follows the running maximum of y_j = x_j + e_j, so the weights
+// 2^(y_j - M) that multiply the codes are well scaled whatever the V scales
+// are, and can be rounded to binary16; the codes are exact in binary16.  The
+// denominator sums 2^(y_j - M) * 2^-e_j in float32.  M is raised only when some
+// y_j exceeds it by more than 8, which saves most of the reductions and
+// rescalings, and the weights are lifted by 2^7: they reach 2^15 at most, and
+// keep binary16's full precision down to 2^-21 of the weight at M.  Queries are scaled by a
+// power of two per row to lie in [1, 2) at their largest and rounded to
+// binary16 (exact for bf16), or split into two binary16 parts (float32).
+//
+// Work.  HBM-bound: each KV head's codes are read once for all its query rows.
+// A unit is 8 * NT query rows (tokens x the query heads of one KV head) of one
+// sequence against its whole context, in tiles of 64 tokens, 16 per warp:
+//   S^T (16 tokens x 8 rows) = K Q^T and O^T (d x 8 rows) += V^T P^T by
+//   mma.sync m16n8k16, which wants the small side as N = 8: the query rows of
+//   a decode step fill it, where a 128-row tcgen05 tile would be 1/16 full.
+// K and V go from global memory straight to registers in the layout of the A
+// operand: which token is which k index, and which d which row, is free as long
+// as both operands agree, so every load is 16 contiguous bytes of a row, and V
+// needs no transposition beyond one byte permutation that the conversion to
+// binary16 does anyway.  The next tile's loads are issued as soon as their
+// registers are free.
+//
+// Split.  All tiles of all units form one line that is cut into equal pieces,
+// one per CTA of a single wave, whatever the mix of lengths (the lengths are on
+// the device; every CTA sums them itself).  A unit that is cut leaves partial
+// sums in a workspace, which a second, programmatically dependent kernel joins.
 #include "gdn_kv.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 16 * kWarps;      // tokens
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f, kLift = 7.f;
 
-template <int CODE, int D, typename TQ, typename TO>
-__global__ void __launch_bounds__(32 * kWarps)
-    attend_plain_kernel(KVView c, int layer, KVAttendArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, i = blockIdx.y;
-  const bool report = blockIdx.x + threadIdx.x == 0;
-  const int slot = a.seq.slot_ids[i];
-  if (slot < 0 || slot >= c.n_slots) {
-    if (report) raise_error(c.err, GDN_DEVERR_SLOT);
-    return;
-  }
-  int lo = i, len = 1;
+// A unit that is cut starts in CTA c and ends in CTA c + parts - 1.
+struct CutUnit {
+  int seq, unit, parts, pad;
+};
+
+template <int D, int NT>
+struct SplitCfg {
+  static constexpr int kRows = 8 * NT;
+  // CTAs per SM that the register budget is set for
+  static constexpr int kCtas = D == 64 ? (NT == 1 ? 5 : 4) : D == 128 ? (NT == 1 ? 4 : 3)
+                                                                      : (NT == 1 ? 3 : 2);
+  static constexpr int kPartFloats = kRows * (D + 2);  // O, then M, then L
+  static constexpr int kOutStride = D + 4;             // floats; spreads the rows over the banks
+};
+
+// What one sequence asks for.
+struct SeqWork {
+  int slot, tok0, len, kv_len;
+  int row_tiles, tiles;   // row tiles per KV head; token tiles per unit
+  int64_t weight;         // tiles of all its units; 0: nothing (or a bad entry)
+};
+
+__device__ __forceinline__ SeqWork seq_work(const KVView &c, const KVAttendArgs &a, int i,
+                                            int rows_per_unit, bool report) {
+  SeqWork w;
+  w.weight = 0;
+  w.slot = a.seq.slot_ids[i];
+  w.kv_len = a.kv_lens[i];
+  w.tok0 = i;
+  int hi = i + 1;
   if (a.seq.cu_seqlens != nullptr) {
-    lo = a.seq.cu_seqlens[i];
-    const int hi = a.seq.cu_seqlens[i + 1];
-    if (lo < 0 || hi < lo || hi > a.seq.total_tokens) {
-      if (report) raise_error(c.err, GDN_DEVERR_SEQ);
-      return;
-    }
-    len = hi - lo;
+    w.tok0 = a.seq.cu_seqlens[i];
+    hi = a.seq.cu_seqlens[i + 1];
   }
-  const int kv_len = a.kv_lens[i];
-  if (kv_len < 0 || kv_len > c.capacity()) {
+  w.len = hi - w.tok0;
+  if (w.slot < 0 || w.slot >= c.n_slots) {
+    if (report) raise_error(c.err, GDN_DEVERR_SLOT);
+    return w;
+  }
+  if (w.tok0 < 0 || hi < w.tok0 || hi > a.seq.total_tokens || w.kv_len < 0 ||
+      w.kv_len > c.capacity()) {
     if (report) raise_error(c.err, GDN_DEVERR_SEQ);
-    return;
+    return w;
   }
-  const int64_t rows = (int64_t)len * c.h_q;
-  for (int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); r < rows;
-       r += (int64_t)gridDim.x * kWarps) {
-    const int t = (int)(r / c.h_q), h = (int)(r % c.h_q), hk = h / (c.h_q / c.h_kv);
-    const TQ *q = static_cast<const TQ *>(a.q) + (int64_t)(lo + t) * a.ld_q + (int64_t)h * D;
-    float qv[E], o[E], m = -INFINITY, l = 0.f;
+  const int64_t rows = (int64_t)w.len * (c.h_q / c.h_kv);
+  w.row_tiles = (int)((rows + rows_per_unit - 1) / rows_per_unit);
+  w.tiles = w.kv_len > 0 ? (w.kv_len + kTile - 1) / kTile : 1;
+  w.weight = (int64_t)c.h_kv * w.row_tiles * w.tiles;
+  return w;
+}
+
+// Sum over the CTA; every thread receives it.
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *buf) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      qv[e] = Elem<TQ>::load1(q + lane * E + e) * a.scale;
-      o[e] = 0.f;
-    }
-    const int last = kv_len - len + t;
-    for (int j = 0; j <= last; ++j) {
-      const int id = c.table[(int64_t)slot * c.max_pages + (j >> c.page_log2)];
-      if (id < 0 || id >= c.n_pages) {
-        raise_error(c.err, GDN_DEVERR_PAGE);
-        continue;
-      }
-      const int64_t blk = c.block(layer, id, hk);
-      const int64_t at =
-          ((blk << c.page_log2) + (j & (c.page_tokens - 1))) * D + lane * E;
-      float kx[E < 4 ? 4 : E], vx[E < 4 ? 4 : E];
-      if (E == 2) {
-        const float4 x = kv::Code<CODE>::decode4(*reinterpret_cast<const uint16_t *>(c.k + at));
-        const float4 y = kv::Code<CODE>::decode4(*reinterpret_cast<const uint16_t *>(c.v + at));
-        kx[0] = x.x, kx[1] = x.y, vx[0] = y.x, vx[1] = y.y;
-      } else {
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+  __syncthreads();
+  int64_t s = 0;
 #pragma unroll
-        for (int e = 0; e + 3 < E; e += 4) {
-          const float4 x =
-              kv::Code<CODE>::decode4(*reinterpret_cast<const uint32_t *>(c.k + at + e));
-          const float4 y =
-              kv::Code<CODE>::decode4(*reinterpret_cast<const uint32_t *>(c.v + at + e));
-          kx[e] = x.x, kx[e + 1] = x.y, kx[e + 2] = x.z, kx[e + 3] = x.w;
-          vx[e] = y.x, vx[e + 1] = y.y, vx[e + 2] = y.z, vx[e + 3] = y.w;
-        }
-      }
-      float s = 0.f;
+  for (int w = 0; w < kWarps; ++w) s += buf[w];
+  __syncthreads();
+  return s;
+}
+
+__device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Streamed loads: each code is used once per CTA.
+__device__ __forceinline__ void ldg16(uint32_t *w, const uint8_t *p) {
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "l"(p));
+}
+__device__ __forceinline__ void ldg8(uint32_t *w, const uint8_t *p) {
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+}
+
+// Conversions of packed codes to binary16 pairs.  k_pairs: the four codes of a
+// word as two pairs; byte b of the word is element place(b) of the four.  v_pairs: byte b of two tokens' words as pair b.
+template <int CODE>
+struct Pairs;
+
+template <>
+struct Pairs<GDN_KV_I8> {
+  // the pairs are bytes (0, 2) and (1, 3): byte 0..3 is element 0, 2, 1, 3
+  static __device__ __forceinline__ int place(int byte) { return (byte & 1) * 2 + (byte >> 1); }
+  // 0x6400 | (code + 128) is 1152 + code in binary16; exact
+  static __device__ __forceinline__ uint32_t widen(uint32_t bytes) {
+    uint32_t x = (bytes & 0x00ff00ffu) ^ 0x64806480u, y;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x64806480u));
+    return y;
+  }
+  static __device__ __forceinline__ void k_pairs(uint32_t w, uint32_t &p, uint32_t &q) {
+    p = widen(w);
+    q = widen(w >> 8);
+  }
+  static __device__ __forceinline__ void v_pairs(uint32_t w0, uint32_t w1, uint32_t *p) {
+    const uint32_t a = __byte_perm(w0, w1, 0x5410), b = __byte_perm(w0, w1, 0x7632);
+    p[0] = widen(a);
+    p[1] = widen(a >> 8);
+    p[2] = widen(b);
+    p[3] = widen(b >> 8);
+  }
+};
+
+template <>
+struct Pairs<GDN_KV_E4M3> {
+  static __device__ __forceinline__ int place(int byte) { return byte; }
+  static __device__ __forceinline__ void split(uint32_t w, uint32_t &p, uint32_t &q) {
+    p = kv::e4m3x2_to_half2((uint16_t)(w & 0xffffu));
+    q = kv::e4m3x2_to_half2((uint16_t)(w >> 16));
+  }
+  static __device__ __forceinline__ void k_pairs(uint32_t w, uint32_t &p, uint32_t &q) {
+    split(w, p, q);
+  }
+  static __device__ __forceinline__ void v_pairs(uint32_t w0, uint32_t w1, uint32_t *p) {
+    split(__byte_perm(w0, w1, 0x5140), p[0], p[1]);
+    split(__byte_perm(w0, w1, 0x7362), p[2], p[3]);
+  }
+};
+
+// One 16-token step of a warp: where its codes are, and their scales.
+struct Step {
+  int64_t row;        // first row of the step in the code arrays (times D: bytes)
+  float k_scale;
+  int v_exp;
+  bool valid;         // the page id is in range
+};
+
+template <int CODE>
+__device__ __forceinline__ Step make_step(const KVView &c, int layer, int head, int id, int tok) {
+  Step s;
+  s.valid = id >= 0 && id < c.n_pages;
+  if (!s.valid) raise_error(c.err, GDN_DEVERR_PAGE);
+  const int64_t blk = c.block(layer, s.valid ? id : 0, head);  // any page; its tokens are masked
+  s.row = (blk << c.page_log2) + (tok & (c.page_tokens - 1));
+  s.k_scale = c.k_scale[blk];
+  s.v_exp = kv::scale_exponent<CODE>(c.v_scale[blk]);
+  return s;
+}
+
+template <int D>
+__device__ __forceinline__ void load_k(uint32_t (*w)[2][4], const uint8_t *k, int64_t row, int g,
+                                       int t) {
+  const uint8_t *p = k + (row + g) * D + 16 * t;
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += qv[e] * kx[e];
-      s = group_sum<32>(s) * c.k_scale[blk];
-      const float mn = fmaxf(m, s), keep = expf(m - mn), p = expf(s - mn);
-      m = mn;
-      l = l * keep + p;
-      const float pv = p * c.v_scale[blk];
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * keep + pv * vx[e];
-    }
-    TO *dst = static_cast<TO *>(a.o) + (int64_t)(lo + t) * a.ld_o + (int64_t)h * D + lane * E;
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-    for (int e = 0; e < E; ++e) Elem<TO>::store1(dst + e, o[e] * inv);
+  for (int seg = 0; seg < D / 64; ++seg) {
+    ldg16(w[seg][0], p + 64 * seg);
+    ldg16(w[seg][1], p + 64 * seg + 8 * D);
   }
 }
 
-template <int CODE, int D, typename TQ>
-cudaError_t launch_t(const KVView &c, int layer, const KVAttendArgs &a, cudaStream_t s) {
-  const int64_t rows = (int64_t)a.max_seqlen * c.h_q;
-  int64_t bx = (rows + kWarps - 1) / kWarps;
-  if (bx > 65535) bx = 65535;
-  const dim3 grid((unsigned)bx, (unsigned)a.seq.n_seqs);
+// tokens 2t, 2t + 1, 2t + 8, 2t + 9; d from 16 g (+ 128 i), for D = 64 from 8 g
+template <int D>
+__device__ __forceinline__ void load_v(uint32_t (*w)[D / 32], const uint8_t *v, int64_t row, int g,
+                                       int t) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const uint8_t *p = v + (row + 2 * t + (x & 1) + 8 * (x >> 1)) * D;
+    if constexpr (D == 64) {
+      ldg8(w[x], p + 8 * g);
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 128; ++i) ldg16(w[x] + 4 * i, p + 128 * i + 16 * g);
+    }
+  }
+}
+
+// d of byte 0 of word j of a lane's V words
+template <int D>
+__device__ __forceinline__ int v_dim(int g, int j) {
+  return D == 64 ? 8 * g + 4 * j : 128 * (j / 4) + 16 * g + 4 * (j % 4);
+}
+
+__device__ __forceinline__ void put_row4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void put_row4(bf16 *p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
+                                             *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// o = O / L of one row's four elements; a row without weights is zero
+__device__ __forceinline__ void put_out(const KVView &c, const KVAttendArgs &a, const SeqWork &w,
+                                        int head, int row, int d, float4 x, float l) {
+  const int group = c.h_q / c.h_kv;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t at = (int64_t)(w.tok0 + row / group) * a.ld_o +
+                     (int64_t)(head * group + row % group) * c.d + d;
   if (a.o_dtype == GDN_F32)
-    attend_plain_kernel<CODE, D, TQ, float><<<grid, 32 * kWarps, 0, s>>>(c, layer, a);
+    put_row4(static_cast<float *>(a.o) + at, scale4(inv, x));
   else
-    attend_plain_kernel<CODE, D, TQ, bf16><<<grid, 32 * kWarps, 0, s>>>(c, layer, a);
-  return cudaGetLastError();
+    put_row4(static_cast<bf16 *>(a.o) + at, scale4(inv, x));
+}
+
+template <int CODE, int D, int NT, typename TQ>
+__global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
+    attend_split_kernel(const KVView c, const int layer, const KVAttendArgs a, const int min_tiles,
+                        float *__restrict__ part, CutUnit *__restrict__ cut) {
+  using Cfg = SplitCfg<D, NT>;
+  constexpr int R = Cfg::kRows;
+  constexpr int PARTS = sizeof(TQ) == 4 ? 2 : 1;   // binary16 parts of queries and weights
+  constexpr int SEGS = D / 64, VW = D / 32, MT = D / 16;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __half *sQ = reinterpret_cast<__half *>(smem);                     // [PARTS][NT][SEGS][2][32][8]
+  float *sO = reinterpret_cast<float *>(smem + PARTS * R * D * 2);   // [kWarps][R][kOutStride]
+  __shared__ float sM[kWarps][R], sL[kWarps][R], sA[R];
+  __shared__ int sLim[R];
+  __shared__ int64_t s_buf[kWarps], s_found_off;
+  __shared__ int s_found;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int n = a.seq.n_seqs, cta = blockIdx.x;
+  const int group = c.h_q / c.h_kv;
+
+  // ---- this CTA's piece of the line of tiles ----
+  int64_t mine = 0;
+  for (int i = tid; i < n; i += kThreads) mine += seq_work(c, a, i, R, cta == 0).weight;
+  const int64_t total = block_sum(mine, s_buf);
+  const int64_t wanted = (total + min_tiles - 1) / min_tiles;
+  const int64_t ctas = wanted < gridDim.x ? wanted : gridDim.x;
+  if (tid == 0) cut[cta].parts = 0;
+  if (cta >= ctas) return;
+  const int64_t begin = cta * total / ctas, end = (cta + 1) * total / ctas;
+  if (tid == 0) s_found = -1;
+  int64_t before = 0;
+  for (int base = 0; base < n; base += kThreads) {
+    const int64_t w = base + tid < n ? seq_work(c, a, base + tid, R, false).weight : 0;
+    int64_t x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_buf[warp] = x;
+    __syncthreads();
+    int64_t from = before + x - w;
+    for (int k = 0; k < warp; ++k) from += s_buf[k];
+    if (w > 0 && from <= begin && begin < from + w) {
+      s_found = base + tid;
+      s_found_off = begin - from;
+    }
+    for (int k = 0; k < kWarps; ++k) before += s_buf[k];
+    __syncthreads();
+    if (s_found >= 0) break;
+  }
+
+  int seq = s_found;
+  if (seq < 0) return;  // (only if the lengths changed under the kernel)
+  SeqWork w = seq_work(c, a, seq, R, false);
+  int unit = (int)(s_found_off / w.tiles), tile = (int)(s_found_off % w.tiles);
+  for (int64_t at = begin; at < end;) {
+    if (unit == c.h_kv * w.row_tiles) {  // the next sequence that has work
+      do {
+        if (++seq >= n) return;
+        w = seq_work(c, a, seq, R, false);
+      } while (w.weight == 0);
+      unit = 0;
+    }
+    const int n_here = (int)min((int64_t)(w.tiles - tile), end - at);
+    const int head = unit / w.row_tiles, row0 = (unit % w.row_tiles) * R;
+    const int rows = min(R, (int)min((int64_t)w.len * group - row0, (int64_t)R));
+
+    // ---- queries: scaled to [1, 2) by a power of two, binary16, in the B layout ----
+    constexpr int E = D / 32;
+    for (int r = warp; r < R; r += kWarps) {
+      const int row = row0 + min(r, rows - 1);  // rows past the end repeat the last, unused
+      const int tok = row / group;
+      const TQ *q = static_cast<const TQ *>(a.q) + (int64_t)(w.tok0 + tok) * a.ld_q +
+                    (int64_t)(head * group + row % group) * D + lane * E;
+      float x[E];
+      if constexpr (E == 2) {
+        x[0] = Elem<TQ>::load1(q);
+        x[1] = Elem<TQ>::load1(q + 1);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const float4 f = Elem<TQ>::load4(q + e);
+          x[e] = f.x, x[e + 1] = f.y, x[e + 2] = f.z, x[e + 3] = f.w;
+        }
+      }
+      float m = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(x[e]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      int ex = (int)(__float_as_uint(m) >> 23) - 127;
+      ex = ex > 126 || m == 0.f ? 0 : max(ex, -126);
+      const float inv = a.scale < 0.f ? -kv::pow2f(-ex) : kv::pow2f(-ex);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int d = lane * E + e;
+        const int j = (d & 12) + Pairs<CODE>::place(d & 3);  // place within the lane's 16
+        const int dst = ((((r >> 3) * SEGS + d / 64) * 2 + (j >> 3)) * 32 + (r & 7) * 4 +
+                         (d % 64) / 16) * 8 + (j & 7);
+        const float y = x[e] * inv;
+        const __half hi = __float2half_rn(y);
+        sQ[dst] = hi;
+        if constexpr (PARTS == 2) sQ[NT * 8 * D + dst] = __float2half_rn(y - __half2float(hi));
+      }
+      if (lane == 0) {
+        sA[r] = fabsf(a.scale) * kLog2e * kv::pow2f(ex);
+        sLim[r] = w.kv_len - w.len + tok + 1;
+      }
+    }
+    __syncthreads();
+
+    // ---- the tiles ----
+    float o[MT][NT][4], M[NT][2], Ms[NT][2], L[NT][2], qa[NT][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        M[x][y] = -INFINITY;
+        Ms[x][y] = L[x][y] = 0.f;
+        qa[x][y] = sA[8 * x + 2 * t + y];
+        lim[x][y] = sLim[8 * x + 2 * t + y];
+      }
+#pragma unroll
+    for (int x = 0; x < MT; ++x)
+#pragma unroll
+      for (int y = 0; y < NT; ++y)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) o[x][y][z] = 0.f;
+    const int lim_min = sLim[0];  // positions before it are open to every row
+    const int last = min((tile + n_here) * kTile, sLim[R - 1]);
+    const int32_t *table = c.table + (int64_t)w.slot * c.max_pages;
+    int tok = tile * kTile + 16 * warp;
+    uint32_t kw[SEGS][2][4], vw[4][VW];
+    Step st;
+    int next_id = 0;
+    if (tok < last) {
+      st = make_step<CODE>(c, layer, head, table[tok >> c.page_log2], tok);
+      load_k<D>(kw, c.k, st.row, g, t);
+      load_v<D>(vw, c.v, st.row, g, t);
+      if (tok + kTile < last) next_id = table[(tok + kTile) >> c.page_log2];
+    }
+    for (; tok < last; tok += kTile) {
+      // S^T = K Q^T
+      float s[NT][4];
+#pragma unroll
+      for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+#pragma unroll
+      for (int seg = 0; seg < SEGS; ++seg)
+#pragma unroll
+        for (int j2 = 0; j2 < 2; ++j2) {
+          uint32_t a0[4], a1[4];
+          Pairs<CODE>::k_pairs(kw[seg][0][2 * j2], a0[0], a0[2]);
+          Pairs<CODE>::k_pairs(kw[seg][1][2 * j2], a0[1], a0[3]);
+          Pairs<CODE>::k_pairs(kw[seg][0][2 * j2 + 1], a1[0], a1[2]);
+          Pairs<CODE>::k_pairs(kw[seg][1][2 * j2 + 1], a1[1], a1[3]);
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+              const uint4 b = *reinterpret_cast<const uint4 *>(
+                  sQ + (size_t)((((p * NT + x) * SEGS + seg) * 2 + j2) * 32 + lane) * 8);
+              mma16816(s[x], a0, b.x, b.y);
+              mma16816(s[x], a1, b.z, b.w);
+            }
+        }
+      const Step cur = st;
+      if (tok + kTile < last) {
+        st = make_step<CODE>(c, layer, head, next_id, tok + kTile);
+        load_k<D>(kw, c.k, st.row, g, t);
+        if (tok + 2 * kTile < last) next_id = table[(tok + 2 * kTile) >> c.page_log2];
+      }
+
+      // weights
+      const float e = (float)cur.v_exp, unscale = kv::pow2f(-cur.v_exp);
+      const bool masked = tok + 16 > lim_min || !cur.valid;
+      bool raise = false;
+      float peak[NT][2];
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float f = qa[x][y] * cur.k_scale;
+          s[x][y] = fmaf(s[x][y], f, e);
+          s[x][2 + y] = fmaf(s[x][2 + y], f, e);
+          if (masked) {
+            if (!cur.valid || tok + g >= lim[x][y]) s[x][y] = -INFINITY;
+            if (!cur.valid || tok + g + 8 >= lim[x][y]) s[x][2 + y] = -INFINITY;
+          }
+          peak[x][y] = fmaxf(s[x][y], s[x][2 + y]);
+          raise |= peak[x][y] > M[x][y] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float m = peak[x][y];
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            m = fmaxf(m, M[x][y]);
+            const float f = m == -INFINITY ? 1.f : fast_exp2(M[x][y] - m);
+            M[x][y] = m;
+            Ms[x][y] = m == -INFINITY ? 0.f : m - kLift;
+            L[x][y] *= f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              o[i][x][y] *= f;
+              o[i][x][2 + y] *= f;
+            }
+          }
+      }
+      uint32_t pb[PARTS][NT][2];
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        float p[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) p[y] = fast_exp2(s[x][y] - Ms[x][y & 1]);
+        L[x][0] = fmaf(p[0] + p[2], unscale, L[x][0]);
+        L[x][1] = fmaf(p[1] + p[3], unscale, L[x][1]);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t h = half2_bits(p[2 * y], p[2 * y + 1]);
+          pb[0][x][y] = transpose8(h);
+          if constexpr (PARTS == 2) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            pb[1][x][y] = transpose8(half2_bits(p[2 * y] - f.x, p[2 * y + 1] - f.y));
+          }
+        }
+      }
+      if (tok + 16 > w.kv_len || !cur.valid) {  // what lies there is no code of this sequence
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (!cur.valid || tok + 2 * t + (x & 1) + 8 * (x >> 1) >= w.kv_len)
+#pragma unroll
+            for (int j = 0; j < VW; ++j) vw[x][j] = 0;
+      }
+
+      // O^T += V^T P^T
+#pragma unroll
+      for (int j = 0; j < VW; ++j) {
+        uint32_t lo[4], hi[4];
+        Pairs<CODE>::v_pairs(vw[0][j], vw[1][j], lo);
+        Pairs<CODE>::v_pairs(vw[2][j], vw[3][j], hi);
+        const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]};
+        const uint32_t a1[4] = {lo[2], lo[3], hi[2], hi[3]};
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+          for (int x = 0; x < NT; ++x) {
+            mma16816(o[2 * j][x], a0, pb[p][x][0], pb[p][x][1]);
+            mma16816(o[2 * j + 1][x], a1, pb[p][x][0], pb[p][x][1]);
+          }
+      }
+      if (tok + kTile < last) load_v<D>(vw, c.v, st.row, g, t);
+    }
+
+    // ---- join the warps ----
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float l = L[x][y];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        const int r = 8 * x + 2 * t + y;
+        if (g == 0) {
+          sM[warp][r] = M[x][y];
+          sL[warp][r] = l;
+        }
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+          *reinterpret_cast<float4 *>(sO + (size_t)(warp * R + r) * Cfg::kOutStride +
+                                      v_dim<D>(g, j)) =
+              make_float4(o[2 * j][x][y], o[2 * j][x][2 + y], o[2 * j + 1][x][y],
+                          o[2 * j + 1][x][2 + y]);
+      }
+    __syncthreads();
+    const bool whole = tile == 0 && n_here == w.tiles;
+    float *my_part = part + (size_t)(2 * cta + (tile == 0 ? 1 : 0)) * Cfg::kPartFloats;
+    for (int x = tid; x < rows * (D / 4); x += kThreads) {
+      const int r = x / (D / 4), d = 4 * (x % (D / 4));
+      float m = sM[0][r];
+#pragma unroll
+      for (int k = 1; k < kWarps; ++k) m = fmaxf(m, sM[k][r]);
+      float l = 0.f;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float f = sM[k][r] == -INFINITY ? (sL[k][r] == 0.f ? 0.f : 1.f)
+                                              : fast_exp2(sM[k][r] - m);
+        l += f * sL[k][r];
+        sum = axpby4(1.f, sum, f,
+                     *reinterpret_cast<const float4 *>(sO + (size_t)(k * R + r) * Cfg::kOutStride +
+                                                       d));
+      }
+      if (whole) {
+        put_out(c, a, w, head, row0 + r, d, sum, l);
+      } else {
+        *reinterpret_cast<float4 *>(my_part + r * D + d) = sum;
+        if (d == 0) {
+          my_part[R * D + r] = m;
+          my_part[R * D + R + r] = l;
+        }
+      }
+    }
+    if (tid == 0 && !whole && tile == 0) {
+      // the CTA whose piece holds this unit's last tile
+      const int64_t end_cta = ((at + w.tiles) * ctas + total - 1) / total;
+      cut[cta] = CutUnit{seq, unit, (int)(end_cta - cta), 0};
+    }
+    __syncthreads();
+    at += n_here;
+    tile = 0;
+    ++unit;
+  }
+}
+
+// Joins the parts of the unit that was cut at the end of CTA blockIdx.x: a warp
+// per query row and 128 elements of it, four parts at a time.
+constexpr int kJoinWarps = 8;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    attend_join_kernel(const KVView c, const KVAttendArgs a, const float *__restrict__ part,
+                       const CutUnit *__restrict__ cut) {
+  using Cfg = SplitCfg<D, NT>;
+  constexpr int R = Cfg::kRows;
+  constexpr int COLS = D / 4;               // float4 columns of a row
+  constexpr int ACROSS = 32 * kJoinWarps / COLS;  // threads of one column: they share the parts
+  __shared__ float4 s_sum[32 * kJoinWarps];
+  __shared__ float s_l[ACROSS];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const CutUnit u = cut[blockIdx.x];
+  if (u.parts == 0) return;
+  const SeqWork w = seq_work(c, a, u.seq, R, false);
+  const int head = u.unit / w.row_tiles, r = blockIdx.y;
+  const int row = (u.unit % w.row_tiles) * R + r;
+  if (row >= (int64_t)w.len * (c.h_q / c.h_kv)) return;
+  const int col = threadIdx.x % COLS, lane = threadIdx.x / COLS;
+  // part 0 is the second partial sum of CTA blockIdx.x, part p the first of CTA blockIdx.x + p
+  auto at = [&](int p) {
+    return part + (size_t)(2 * (blockIdx.x + p) + (p == 0 ? 1 : 0)) * Cfg::kPartFloats;
+  };
+  float m = -INFINITY;
+  for (int p = 0; p < u.parts; ++p) m = fmaxf(m, at(p)[R * D + r]);
+  float l = 0.f;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = lane; p < u.parts; p += ACROSS) {
+    const float *x = at(p);
+    const float pm = x[R * D + r], pl = x[R * D + R + r];
+    const float f = pm == -INFINITY ? (pl == 0.f ? 0.f : 1.f) : fast_exp2(pm - m);
+    l += f * pl;
+    sum = axpby4(1.f, sum, f, *reinterpret_cast<const float4 *>(x + r * D + 4 * col));
+  }
+  s_sum[threadIdx.x] = sum;
+  if (col == 0) s_l[lane] = l;
+  __syncthreads();
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 1; k < ACROSS; ++k) {
+      sum = axpby4(1.f, sum, 1.f, s_sum[k * COLS + col]);
+      l += s_l[k];
+    }
+    put_out(c, a, w, head, row, 4 * col, sum, l);
+  }
+}
+
+template <int CODE, int D, int NT, typename TQ>
+cudaError_t launch_split(const KVView &c, int layer, const KVAttendArgs &a, int sm_count,
+                         cudaMemPool_t work_pool, cudaStream_t s) {
+  using Cfg = SplitCfg<D, NT>;
+  constexpr int kParts = sizeof(TQ) == 4 ? 2 : 1;
+  constexpr int kMinTiles = 1;
+  constexpr int kSmem = kParts * Cfg::kRows * D * 2 +
+                        kWarps * Cfg::kRows * Cfg::kOutStride * (int)sizeof(float);
+  auto kernel = attend_split_kernel<CODE, D, NT, TQ>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  // one wave, or fewer CTAs where the hints say that there are fewer tiles
+  const int64_t rows = (int64_t)a.max_seqlen * (c.h_q / c.h_kv);
+  const double tiles = (double)a.seq.n_seqs * c.h_kv * ((rows + Cfg::kRows - 1) / Cfg::kRows) *
+                       (a.max_kv_len / kTile + 1);
+  int64_t grid = (int64_t)sm_count * Cfg::kCtas;
+  if (tiles / kMinTiles < (double)grid) grid = (int64_t)(tiles / kMinTiles) + 1;
+  const size_t part_bytes = (size_t)grid * 2 * Cfg::kPartFloats * sizeof(float);
+  void *work = nullptr;
+  e = cudaMallocFromPoolAsync(&work, part_bytes + grid * sizeof(CutUnit), work_pool, s);
+  if (e != cudaSuccess) return e;
+  float *part = static_cast<float *>(work);
+  CutUnit *cut = reinterpret_cast<CutUnit *>(static_cast<char *>(work) + part_bytes);
+  kernel<<<(unsigned)grid, kThreads, kSmem, s>>>(c, layer, a, kMinTiles, part, cut);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, Cfg::kRows);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attend_join_kernel<D, NT>, c, a,
+                           static_cast<const float *>(part), static_cast<const CutUnit *>(cut));
+  }
+  const cudaError_t ef = cudaFreeAsync(work, s);
+  return e != cudaSuccess ? e : ef;
+}
+
+template <int CODE, int D, int NT>
+cudaError_t by_type(const KVView &c, int layer, const KVAttendArgs &a, int sms, cudaMemPool_t pool,
+                    cudaStream_t s) {
+  return a.q_dtype == GDN_F32 ? launch_split<CODE, D, NT, float>(c, layer, a, sms, pool, s)
+                              : launch_split<CODE, D, NT, bf16>(c, layer, a, sms, pool, s);
 }
 
 template <int CODE, int D>
-cudaError_t by_type(const KVView &c, int layer, const KVAttendArgs &a, cudaStream_t s) {
-  return a.q_dtype == GDN_F32 ? launch_t<CODE, D, float>(c, layer, a, s)
-                              : launch_t<CODE, D, bf16>(c, layer, a, s);
+cudaError_t by_rows(const KVView &c, int layer, const KVAttendArgs &a, int sms, cudaMemPool_t pool,
+                    cudaStream_t s) {
+  // eight query rows per unit where a slot has no more, else sixteen
+  return (int64_t)a.max_seqlen * (c.h_q / c.h_kv) <= 8
+             ? by_type<CODE, D, 1>(c, layer, a, sms, pool, s)
+             : by_type<CODE, D, 2>(c, layer, a, sms, pool, s);
 }
 
 template <int CODE>
-cudaError_t by_dim(const KVView &c, int layer, const KVAttendArgs &a, cudaStream_t s) {
-  return c.d == 64 ? by_type<CODE, 64>(c, layer, a, s)
-                   : (c.d == 128 ? by_type<CODE, 128>(c, layer, a, s)
-                                 : by_type<CODE, 256>(c, layer, a, s));
+cudaError_t by_dim(const KVView &c, int layer, const KVAttendArgs &a, int sms, cudaMemPool_t pool,
+                   cudaStream_t s) {
+  return c.d == 64    ? by_rows<CODE, 64>(c, layer, a, sms, pool, s)
+         : c.d == 128 ? by_rows<CODE, 128>(c, layer, a, sms, pool, s)
+                      : by_rows<CODE, 256>(c, layer, a, sms, pool, s);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_attend(const KVView &c, int layer, const KVAttendArgs &a, int sm_count,
                              cudaMemPool_t work_pool, cudaStream_t s) {
-  return c.code == GDN_KV_I8 ? by_dim<GDN_KV_I8>(c, layer, a, s)
-                             : by_dim<GDN_KV_E4M3>(c, layer, a, s);
+  return c.code == GDN_KV_I8 ? by_dim<GDN_KV_I8>(c, layer, a, sm_count, work_pool, s)
+                             : by_dim<GDN_KV_E4M3>(c, layer, a, sm_count, work_pool, s);
 }
 
 }  // namespace gdn
