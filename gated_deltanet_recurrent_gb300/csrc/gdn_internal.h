@@ -14,6 +14,8 @@
 #define GDN_HD inline
 #endif
 
+struct CUtensorMap_st;  // CUtensorMap (cuda.h)
+
 namespace gdn {
 
 constexpr float kL2Eps = 1e-6f;
@@ -219,8 +221,17 @@ struct KVAttendArgs {
   float scale;
 };
 
-cudaError_t launch_kv_attend(const KVView &c, int layer, const KVAttendArgs &a, int sm_count,
-                             cudaMemPool_t work_pool, cudaStream_t s);
+// What a cache handle keeps for the attention's launches: tensor maps of the
+// codes viewed as [blocks][page_tokens][d] bytes, with boxes of 16 rows x
+// min(d, 128) bytes in the 128-byte swizzle (d = 64: 64-byte).
+struct KVHost {
+  const CUtensorMap_st *k_map, *v_map;
+  int sm_count;
+  cudaMemPool_t work_pool;
+};
+
+cudaError_t launch_kv_attend(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
+                             cudaStream_t s);
 
 // Detail text of the last failure on this host thread (gdn_last_error_message).
 void set_last_message(const char *msg);

@@ -1,6 +1,8 @@
 // extern "C" entry points of the 8-bit paged KV cache: argument validation
 // (always), optional host-side validation of the index arrays and of the page
 // table entries in use, and the kernel launches.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -15,6 +17,7 @@ struct gdn_kv {
   gdn_kv_desc desc;
   int device;
   int sm_count;
+  alignas(64) CUtensorMap k_map, v_map;  // see gdn::KVHost
   cudaMemPool_t work_pool;  // stream-ordered attention workspaces (kept until destroy)
 };
 
@@ -60,6 +63,8 @@ gdn_status check_desc(const gdn_kv_desc *d) {
   if (d->n_slots > 65535) return fail(GDN_ERR_UNSUPPORTED, "n_slots=%d (max 65535)", d->n_slots);
   if (d->h_kv > 4096 || d->h_q / d->h_kv > 4096)
     return fail(GDN_ERR_UNSUPPORTED, "more than 4096 KV heads or query heads per KV head");
+  if ((int64_t)d->n_layers * d->n_pages > INT32_MAX / d->h_kv)
+    return fail(GDN_ERR_UNSUPPORTED, "n_layers * n_pages * h_kv must stay below 2^31");
   // positions and lengths are int32 throughout
   if ((int64_t)d->max_pages * d->page_tokens > INT32_MAX - 256)
     return fail(GDN_ERR_UNSUPPORTED, "max_pages * page_tokens must stay below 2^31 - 256");
@@ -87,6 +92,29 @@ gdn_status fetch(std::vector<int32_t> &dst, const int32_t *src, size_t n, cudaSt
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "copying index array to host");
   return GDN_OK;
+}
+
+// The codes of one side as [blocks][page_tokens][d] bytes.
+bool encode_codes(CUtensorMap *m, void *codes, const gdn_kv_desc &d) {
+  void *fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                       &q) != cudaSuccess ||
+      fn == nullptr || q != cudaDriverEntryPointSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  const cuuint64_t dim = (cuuint64_t)d.d, rows = (cuuint64_t)d.page_tokens;
+  cuuint64_t dims[3] = {dim, rows, (cuuint64_t)d.n_layers * d.n_pages * d.h_kv};
+  cuuint64_t strides[2] = {dim, dim * rows};
+  cuuint32_t box[3] = {(cuuint32_t)(d.d < 128 ? d.d : 128), 16, 1};
+  cuuint32_t elem[3] = {1, 1, 1};
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
+             m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, dims, strides, box, elem,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             d.d < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 
 // Arguments that the three calls share.  On GDN_OK with *empty set there is
@@ -231,6 +259,10 @@ gdn_status gdn_kv_create(const gdn_kv_desc *desc, void *k_codes, void *v_codes,
   c->desc = *desc;
   c->device = dev;
   c->sm_count = sm_count;
+  if (!encode_codes(&c->k_map, k_codes, *desc) || !encode_codes(&c->v_map, v_codes, *desc)) {
+    delete c;
+    return fail(GDN_ERR_CUDA, "encoding the tensor maps of the codes failed");
+  }
   unsigned int *err = nullptr;
   e = cudaMalloc(&err, sizeof(*err));
   if (e == cudaSuccess) {
@@ -374,7 +406,8 @@ gdn_status gdn_kv_attend(gdn_kv *c, int32_t layer, const int32_t *slot_ids,
   const gdn::KVAttendArgs a{seq,  kv_lens, max_seqlen < 1 ? 1 : max_seqlen,
                             max_kv_len < 1 ? 1 : max_kv_len, q, o, ld_q, ld_o, q_dtype, o_dtype,
                             scale};
-  const cudaError_t e = gdn::launch_kv_attend(c->view, layer, a, c->sm_count, c->work_pool, s);
+  const gdn::KVHost h{&c->k_map, &c->v_map, c->sm_count, c->work_pool};
+  const cudaError_t e = gdn::launch_kv_attend(c->view, layer, a, h, s);
   if (e != cudaSuccess) return cuda_fail(e, "KV attention launch");
   return ok();
 }

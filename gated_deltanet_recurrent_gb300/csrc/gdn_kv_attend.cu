@@ -21,17 +21,21 @@
 //   S^T (16 tokens x 8 rows) = K Q^T and O^T (d x 8 rows) += V^T P^T by
 //   mma.sync m16n8k16, which wants the small side as N = 8: the query rows of
 //   a decode step fill it, where a 128-row tcgen05 tile would be 1/16 full.
-// K and V go from global memory straight to registers in the layout of the A
-// operand: which token is which k index, and which d which row, is free as long
-// as both operands agree, so every load is 16 contiguous bytes of a row, and V
-// needs no transposition beyond one byte permutation that the conversion to
-// binary16 does anyway.  The next tile's loads are issued as soon as their
-// registers are free.
+// Each warp has its own ring of 16-token stages that one lane fills with tensor
+// copies (16 rows of 128 bytes, 128-byte swizzle), so what is in flight takes no
+// registers and no warp waits for another.  Which token is which k index, and
+// which d which row, is free as long as both operands agree: the A operands of
+// both products are 16-byte (d = 64: 8-byte) shared-memory reads of rows as they
+// lie, and V needs no transposition beyond one byte permutation that the
+// conversion to binary16 does anyway.  Row r of the products is token perm(r),
+// an order in which these reads meet no bank twice under the swizzle.
 //
 // Split.  All tiles of all units form one line that is cut into equal pieces,
 // one per CTA of a single wave, whatever the mix of lengths (the lengths are on
 // the device; every CTA sums them itself).  A unit that is cut leaves partial
 // sums in a workspace, which a second, programmatically dependent kernel joins.
+#include <cuda.h>
+
 #include "gdn_kv.cuh"
 
 namespace gdn {
@@ -48,14 +52,22 @@ struct CutUnit {
   int seq, unit, parts, pad;
 };
 
-template <int D, int NT>
+template <int D, int NT, int PARTS>
 struct SplitCfg {
   static constexpr int kRows = 8 * NT;
   // CTAs per SM that the register budget is set for
   static constexpr int kCtas = D == 64 ? (NT == 1 ? 5 : 4) : D == 128 ? (NT == 1 ? 4 : 3)
                                                                       : (NT == 1 ? 3 : 2);
+  // stages of a warp's ring: what fits in an SM's shared memory with kCtas CTAs
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? (NT == 1 ? 3 : 4)
+                                                        : (NT == 1 ? 2 : PARTS == 1 ? 3 : 2);
+  static constexpr int kStage = 2 * 16 * D;            // bytes: K, then V
   static constexpr int kPartFloats = kRows * (D + 2);  // O, then M, then L
   static constexpr int kOutStride = D + 4;             // floats; spreads the rows over the banks
+  // the rings, and after the last tile the warps' sums in their place
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kSums = kWarps * kRows * kOutStride * 4;
+  static constexpr int kSmem = (kRing > kSums ? kRing : kSums) + PARTS * kRows * D * 2 + 1024;
 };
 
 // What one sequence asks for.
@@ -94,17 +106,25 @@ __device__ __forceinline__ SeqWork seq_work(const KVView &c, const KVAttendArgs 
   return w;
 }
 
-// Sum over the CTA; every thread receives it.
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *buf) {
+// Exclusive prefix sum over the CTA's threads, and the total.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *buf, int64_t *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t own = x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) buf[warp] = x;
   __syncthreads();
-  int64_t s = 0;
+  int64_t from = x - own, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) s += buf[w];
-  __syncthreads();
-  return s;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) from += buf[w];
+    all += buf[w];
+  }
+  *total = all;
+  return from;
 }
 
 __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
@@ -131,14 +151,14 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// Streamed loads: each code is used once per CTA.
-__device__ __forceinline__ void ldg16(uint32_t *w, const uint8_t *p) {
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "l"(p));
-}
-__device__ __forceinline__ void ldg8(uint32_t *w, const uint8_t *p) {
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+// 16 rows of 128 (d = 64: 64) bytes: bytes x.. of rows `row`.. of block `blk`
+__device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *m, int x, int row, int blk,
+                                         uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(row), "r"(blk), "r"(smem_addr(bar))
+      : "memory");
 }
 
 // Conversions of packed codes to binary16 pairs.  k_pairs: the four codes of a
@@ -185,49 +205,28 @@ struct Pairs<GDN_KV_E4M3> {
   }
 };
 
-// One 16-token step of a warp: where its codes are, and their scales.
-struct Step {
-  int64_t row;        // first row of the step in the code arrays (times D: bytes)
-  float k_scale;
-  int v_exp;
-  bool valid;         // the page id is in range
-};
+// Token of product row (or k index) r of a 16-token step.
+__device__ __forceinline__ int perm(int r) { return (r & 8) | (r & 1 ? (r & 7) ^ 4 : r & 7); }
 
-template <int CODE>
-__device__ __forceinline__ Step make_step(const KVView &c, int layer, int head, int id, int tok) {
-  Step s;
-  s.valid = id >= 0 && id < c.n_pages;
-  if (!s.valid) raise_error(c.err, GDN_DEVERR_PAGE);
-  const int64_t blk = c.block(layer, s.valid ? id : 0, head);  // any page; its tokens are masked
-  s.row = (blk << c.page_log2) + (tok & (c.page_tokens - 1));
-  s.k_scale = c.k_scale[blk];
-  s.v_exp = kv::scale_exponent<CODE>(c.v_scale[blk]);
-  return s;
+// Byte offset of 16-byte chunk x of row `row` in a stage's K or V half, as the
+// tensor copy swizzles it.
+template <int D>
+__device__ __forceinline__ int chunk_at(int row, int x) {
+  if constexpr (D == 64) return row * 64 + ((x ^ (row >> 1 & 3)) << 4);
+  return (x >> 3) * 2048 + row * 128 + (((x & 7) ^ (row & 7)) << 4);
 }
 
+// V words of token `row`: d from 16 g (+ 128 i), for D = 64 from 8 g
 template <int D>
-__device__ __forceinline__ void load_k(uint32_t (*w)[2][4], const uint8_t *k, int64_t row, int g,
-                                       int t) {
-  const uint8_t *p = k + (row + g) * D + 16 * t;
+__device__ __forceinline__ void load_v(uint32_t *w, const unsigned char *v, int row, int g) {
+  if constexpr (D == 64) {
+    const uint2 x = *reinterpret_cast<const uint2 *>(v + chunk_at<D>(row, g >> 1) + 8 * (g & 1));
+    w[0] = x.x, w[1] = x.y;
+  } else {
 #pragma unroll
-  for (int seg = 0; seg < D / 64; ++seg) {
-    ldg16(w[seg][0], p + 64 * seg);
-    ldg16(w[seg][1], p + 64 * seg + 8 * D);
-  }
-}
-
-// tokens 2t, 2t + 1, 2t + 8, 2t + 9; d from 16 g (+ 128 i), for D = 64 from 8 g
-template <int D>
-__device__ __forceinline__ void load_v(uint32_t (*w)[D / 32], const uint8_t *v, int64_t row, int g,
-                                       int t) {
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    const uint8_t *p = v + (row + 2 * t + (x & 1) + 8 * (x >> 1)) * D;
-    if constexpr (D == 64) {
-      ldg8(w[x], p + 8 * g);
-    } else {
-#pragma unroll
-      for (int i = 0; i < D / 128; ++i) ldg16(w[x] + 4 * i, p + 128 * i + 16 * g);
+    for (int i = 0; i < D / 128; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(v + chunk_at<D>(row, 8 * i + g));
+      w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
     }
   }
 }
@@ -259,62 +258,68 @@ __device__ __forceinline__ void put_out(const KVView &c, const KVAttendArgs &a, 
 }
 
 template <int CODE, int D, int NT, typename TQ>
-__global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
-    attend_split_kernel(const KVView c, const int layer, const KVAttendArgs a, const int min_tiles,
-                        float *__restrict__ part, CutUnit *__restrict__ cut) {
-  using Cfg = SplitCfg<D, NT>;
-  constexpr int R = Cfg::kRows;
-  constexpr int PARTS = sizeof(TQ) == 4 ? 2 : 1;   // binary16 parts of queries and weights
+__global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 : 1>::kCtas)
+    attend_split_kernel(const __grid_constant__ CUtensorMap k_map,
+                        const __grid_constant__ CUtensorMap v_map, const KVView c, const int layer,
+                        const KVAttendArgs a, const int min_tiles, float *__restrict__ part,
+                        CutUnit *__restrict__ cut) {
+  constexpr int PARTS = sizeof(TQ) == 4 ? 2 : 1;  // binary16 parts of queries and weights
+  using Cfg = SplitCfg<D, NT, PARTS>;
+  constexpr int R = Cfg::kRows, S = Cfg::kStages;
   constexpr int SEGS = D / 64, VW = D / 32, MT = D / 16;
-  extern __shared__ __align__(16) unsigned char smem[];
-  __half *sQ = reinterpret_cast<__half *>(smem);                     // [PARTS][NT][SEGS][2][32][8]
-  float *sO = reinterpret_cast<float *>(smem + PARTS * R * D * 2);   // [kWarps][R][kOutStride]
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float *sO = reinterpret_cast<float *>(smem);  // [kWarps][R][kOutStride], after the rings
+  __half *sQ = reinterpret_cast<__half *>(      // [PARTS][NT][SEGS][2][32][8]
+      smem + (Cfg::kRing > Cfg::kSums ? Cfg::kRing : Cfg::kSums));
   __shared__ float sM[kWarps][R], sL[kWarps][R], sA[R];
-  __shared__ int sLim[R];
   __shared__ int64_t s_buf[kWarps], s_found_off;
   __shared__ int s_found;
+  __shared__ __align__(8) uint64_t s_full[kWarps][S];
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int n = a.seq.n_seqs, cta = blockIdx.x;
   const int group = c.h_q / c.h_kv;
+  unsigned char *ring = smem + warp * S * Cfg::kStage;
+  uint64_t *full = s_full[warp];
+  if (lane == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(&full[i], 1);
+    mbar_fence_init();
+  }
 
   // ---- this CTA's piece of the line of tiles ----
-  int64_t mine = 0;
-  for (int i = tid; i < n; i += kThreads) mine += seq_work(c, a, i, R, cta == 0).weight;
-  const int64_t total = block_sum(mine, s_buf);
+  if (tid == 0) {
+    cut[cta].parts = 0;
+    s_found = -1;
+  }
+  const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
+  int64_t mine = 0, total;
+  for (int i = i0; i < i1; ++i) mine += seq_work(c, a, i, R, cta == 0).weight;
+  int64_t from = block_scan(mine, s_buf, &total);
   const int64_t wanted = (total + min_tiles - 1) / min_tiles;
   const int64_t ctas = wanted < gridDim.x ? wanted : gridDim.x;
-  if (tid == 0) cut[cta].parts = 0;
   if (cta >= ctas) return;
   const int64_t begin = cta * total / ctas, end = (cta + 1) * total / ctas;
-  if (tid == 0) s_found = -1;
-  int64_t before = 0;
-  for (int base = 0; base < n; base += kThreads) {
-    const int64_t w = base + tid < n ? seq_work(c, a, base + tid, R, false).weight : 0;
-    int64_t x = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+  if (from <= begin && begin < from + mine)
+    for (int i = i0; i < i1; ++i) {
+      const int64_t x = seq_work(c, a, i, R, false).weight;
+      if (from <= begin && begin < from + x) {
+        s_found = i;
+        s_found_off = begin - from;
+      }
+      from += x;
     }
-    if (lane == 31) s_buf[warp] = x;
-    __syncthreads();
-    int64_t from = before + x - w;
-    for (int k = 0; k < warp; ++k) from += s_buf[k];
-    if (w > 0 && from <= begin && begin < from + w) {
-      s_found = base + tid;
-      s_found_off = begin - from;
-    }
-    for (int k = 0; k < kWarps; ++k) before += s_buf[k];
-    __syncthreads();
-    if (s_found >= 0) break;
-  }
+  __syncthreads();
 
   int seq = s_found;
   if (seq < 0) return;  // (only if the lengths changed under the kernel)
   SeqWork w = seq_work(c, a, seq, R, false);
+  if (w.weight == 0) return;
   int unit = (int)(s_found_off / w.tiles), tile = (int)(s_found_off % w.tiles);
+  uint32_t used = 0;  // stages that this warp has filled so far
+  bool ok = true;
   for (int64_t at = begin; at < end;) {
     if (unit == c.h_kv * w.row_tiles) {  // the next sequence that has work
       do {
@@ -325,14 +330,44 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
     }
     const int n_here = (int)min((int64_t)(w.tiles - tile), end - at);
     const int head = unit / w.row_tiles, row0 = (unit % w.row_tiles) * R;
-    const int rows = min(R, (int)min((int64_t)w.len * group - row0, (int64_t)R));
+    const int rows = (int)min((int64_t)w.len * group - row0, (int64_t)R);
+    const int pos0 = w.kv_len - w.len + 1;            // positions open to token 0
+    const int lim_min = pos0 + row0 / group;          // ... to every row of the unit
+    const int last = min((tile + n_here) * kTile, pos0 + (row0 + rows - 1) / group);
+    const int32_t *table = c.table + (int64_t)w.slot * c.max_pages;
+    const int tok0 = tile * kTile + 16 * warp;
+    const int steps = tok0 < last ? (last - tok0 + kTile - 1) / kTile : 0;
+
+    // A step's page (any page, if the id is bad: its tokens are masked).
+    auto page_id = [&](int i) { return table[(tok0 + i * kTile) >> c.page_log2]; };
+    auto fill = [&](int i, int id) {
+      const uint32_t u = used + i;
+      if (lane == 0) {
+        const bool bad = id < 0 || id >= c.n_pages;
+        if (bad) raise_error(c.err, GDN_DEVERR_PAGE);
+        const int blk = (int)c.block(layer, bad ? 0 : id, head);
+        const int row = (tok0 + i * kTile) & (c.page_tokens - 1);
+        unsigned char *dst = ring + (u % S) * Cfg::kStage;
+        uint64_t *bar = &full[u % S];
+        mbar_arrive_expect_tx(bar, Cfg::kStage);
+#pragma unroll
+        for (int x = 0; x < D; x += 128) tma_rows(dst + 16 * x, &k_map, x, row, blk, bar);
+#pragma unroll
+        for (int x = 0; x < D; x += 128) tma_rows(dst + 16 * D + 16 * x, &v_map, x, row, blk, bar);
+      }
+    };
+    int ids[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) ids[i] = i < steps ? page_id(i) : 0;
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (i < steps) fill(i, ids[i]);
 
     // ---- queries: scaled to [1, 2) by a power of two, binary16, in the B layout ----
     constexpr int E = D / 32;
     for (int r = warp; r < R; r += kWarps) {
       const int row = row0 + min(r, rows - 1);  // rows past the end repeat the last, unused
-      const int tok = row / group;
-      const TQ *q = static_cast<const TQ *>(a.q) + (int64_t)(w.tok0 + tok) * a.ld_q +
+      const TQ *q = static_cast<const TQ *>(a.q) + (int64_t)(w.tok0 + row / group) * a.ld_q +
                     (int64_t)(head * group + row % group) * D + lane * E;
       float x[E];
       if constexpr (E == 2) {
@@ -364,10 +399,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
         sQ[dst] = hi;
         if constexpr (PARTS == 2) sQ[NT * 8 * D + dst] = __float2half_rn(y - __half2float(hi));
       }
-      if (lane == 0) {
-        sA[r] = fabsf(a.scale) * kLog2e * kv::pow2f(ex);
-        sLim[r] = w.kv_len - w.len + tok + 1;
-      }
+      if (lane == 0) sA[r] = fabsf(a.scale) * kLog2e * kv::pow2f(ex);
     }
     __syncthreads();
 
@@ -381,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
         M[x][y] = -INFINITY;
         Ms[x][y] = L[x][y] = 0.f;
         qa[x][y] = sA[8 * x + 2 * t + y];
-        lim[x][y] = sLim[8 * x + 2 * t + y];
+        lim[x][y] = pos0 + (row0 + min(8 * x + 2 * t + y, rows - 1)) / group;
       }
 #pragma unroll
     for (int x = 0; x < MT; ++x)
@@ -389,33 +421,52 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
       for (int y = 0; y < NT; ++y)
 #pragma unroll
         for (int z = 0; z < 4; ++z) o[x][y][z] = 0.f;
-    const int lim_min = sLim[0];  // positions before it are open to every row
-    const int last = min((tile + n_here) * kTile, sLim[R - 1]);
-    const int32_t *table = c.table + (int64_t)w.slot * c.max_pages;
-    int tok = tile * kTile + 16 * warp;
-    uint32_t kw[SEGS][2][4], vw[4][VW];
-    Step st;
-    int next_id = 0;
-    if (tok < last) {
-      st = make_step<CODE>(c, layer, head, table[tok >> c.page_log2], tok);
-      load_k<D>(kw, c.k, st.row, g, t);
-      load_v<D>(vw, c.v, st.row, g, t);
-      if (tok + kTile < last) next_id = table[(tok + kTile) >> c.page_log2];
-    }
-    for (; tok < last; tok += kTile) {
+    // scales of the next step, loaded a step ahead
+    float next_k = 0.f, next_v = 0.f;
+    auto scales = [&](int id) {
+      const int64_t blk = c.block(layer, id < 0 || id >= c.n_pages ? 0 : id, head);
+      next_k = c.k_scale[blk];
+      next_v = c.v_scale[blk];
+    };
+    if (steps > 0) scales(ids[0]);
+    int ahead = S < steps ? page_id(S) : 0;  // page of step i + S
+    for (int i = 0; i < steps && ok; ++i) {
+      const uint32_t u = used + i;
+      const int tok = tok0 + i * kTile;
+      const unsigned char *sK = ring + (u % S) * Cfg::kStage, *sV = sK + 16 * D;
+      const bool valid = ids[0] >= 0 && ids[0] < c.n_pages;
+      const float k_scale = next_k;
+      const int v_exp = kv::scale_exponent<CODE>(next_v);
+#pragma unroll
+      for (int x = 0; x + 1 < S; ++x) ids[x] = ids[x + 1];
+      ids[S - 1] = ahead;
+      if (i + 1 < steps) scales(ids[0]);
+      if (i + S + 1 < steps) ahead = page_id(i + S + 1);
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[u % S], (u / S) & 1));
+      if (!ok) {  // report it, and give the copies in flight (with limits again) time to land
+        if (lane == 0) raise_error(c.err, GDN_DEVERR_TIMEOUT);
+        for (int x = i + 1; x < min(steps, i + S); ++x)
+          mbar_wait_bounded(&full[(used + x) % S], ((used + x) / S) & 1);
+        break;
+      }
+
       // S^T = K Q^T
       float s[NT][4];
 #pragma unroll
       for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
 #pragma unroll
-      for (int seg = 0; seg < SEGS; ++seg)
+      for (int seg = 0; seg < SEGS; ++seg) {
+        const uint4 k0 = *reinterpret_cast<const uint4 *>(sK + chunk_at<D>(perm(g), 4 * seg + t));
+        const uint4 k1 =
+            *reinterpret_cast<const uint4 *>(sK + chunk_at<D>(perm(g + 8), 4 * seg + t));
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int j2 = 0; j2 < 2; ++j2) {
           uint32_t a0[4], a1[4];
-          Pairs<CODE>::k_pairs(kw[seg][0][2 * j2], a0[0], a0[2]);
-          Pairs<CODE>::k_pairs(kw[seg][1][2 * j2], a0[1], a0[3]);
-          Pairs<CODE>::k_pairs(kw[seg][0][2 * j2 + 1], a1[0], a1[2]);
-          Pairs<CODE>::k_pairs(kw[seg][1][2 * j2 + 1], a1[1], a1[3]);
+          Pairs<CODE>::k_pairs(w0[2 * j2], a0[0], a0[2]);
+          Pairs<CODE>::k_pairs(w1[2 * j2], a0[1], a0[3]);
+          Pairs<CODE>::k_pairs(w0[2 * j2 + 1], a1[0], a1[2]);
+          Pairs<CODE>::k_pairs(w1[2 * j2 + 1], a1[1], a1[3]);
 #pragma unroll
           for (int p = 0; p < PARTS; ++p)
 #pragma unroll
@@ -426,28 +477,23 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
               mma16816(s[x], a1, b.z, b.w);
             }
         }
-      const Step cur = st;
-      if (tok + kTile < last) {
-        st = make_step<CODE>(c, layer, head, next_id, tok + kTile);
-        load_k<D>(kw, c.k, st.row, g, t);
-        if (tok + 2 * kTile < last) next_id = table[(tok + 2 * kTile) >> c.page_log2];
       }
 
       // weights
-      const float e = (float)cur.v_exp, unscale = kv::pow2f(-cur.v_exp);
-      const bool masked = tok + 16 > lim_min || !cur.valid;
+      const float e = (float)v_exp, unscale = kv::pow2f(-v_exp);
+      const bool masked = tok + 16 > lim_min || !valid;
       bool raise = false;
       float peak[NT][2];
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float f = qa[x][y] * cur.k_scale;
+          const float f = qa[x][y] * k_scale;
           s[x][y] = fmaf(s[x][y], f, e);
           s[x][2 + y] = fmaf(s[x][2 + y], f, e);
           if (masked) {
-            if (!cur.valid || tok + g >= lim[x][y]) s[x][y] = -INFINITY;
-            if (!cur.valid || tok + g + 8 >= lim[x][y]) s[x][2 + y] = -INFINITY;
+            if (!valid || tok + perm(g) >= lim[x][y]) s[x][y] = -INFINITY;
+            if (!valid || tok + perm(g + 8) >= lim[x][y]) s[x][2 + y] = -INFINITY;
           }
           peak[x][y] = fmaxf(s[x][y], s[x][2 + y]);
           raise |= peak[x][y] > M[x][y] + kSlack;
@@ -467,9 +513,9 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
             Ms[x][y] = m == -INFINITY ? 0.f : m - kLift;
             L[x][y] *= f;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              o[i][x][y] *= f;
-              o[i][x][2 + y] *= f;
+            for (int j = 0; j < MT; ++j) {
+              o[j][x][y] *= f;
+              o[j][x][2 + y] *= f;
             }
           }
       }
@@ -491,15 +537,19 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
           }
         }
       }
-      if (tok + 16 > w.kv_len || !cur.valid) {  // what lies there is no code of this sequence
+
+      // O^T += V^T P^T
+      uint32_t vw[4][VW];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        load_v<D>(vw[x], sV, perm(2 * t + (x & 1) + 8 * (x >> 1)), g);
+      if (tok + 16 > w.kv_len || !valid) {  // what lies there is no code of this sequence
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          if (!cur.valid || tok + 2 * t + (x & 1) + 8 * (x >> 1) >= w.kv_len)
+          if (!valid || tok + perm(2 * t + (x & 1) + 8 * (x >> 1)) >= w.kv_len)
 #pragma unroll
             for (int j = 0; j < VW; ++j) vw[x][j] = 0;
       }
-
-      // O^T += V^T P^T
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
         uint32_t lo[4], hi[4];
@@ -515,8 +565,13 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
             mma16816(o[2 * j + 1][x], a1, pb[p][x][0], pb[p][x][1]);
           }
       }
-      if (tok + kTile < last) load_v<D>(vw, c.v, st.row, g, t);
+      __syncwarp();  // the stage has been read by every lane
+      if (i + S < steps) fill(i + S, ids[S - 1]);
     }
+    // the rings are free after this: the sums take their place
+    ok = __syncthreads_and(ok);
+    if (!ok) return;
+    used += steps;
 
     // ---- join the warps ----
 #pragma unroll
@@ -572,6 +627,8 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
       const int64_t end_cta = ((at + w.tiles) * ctas + total - 1) / total;
       cut[cta] = CutUnit{seq, unit, (int)(end_cta - cta), 0};
     }
+    // the next unit's copies (async proxy) overwrite what was written here
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     at += n_here;
     tile = 0;
@@ -579,86 +636,104 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT>::kCtas)
   }
 }
 
-// Joins the parts of the unit that was cut at the end of CTA blockIdx.x: a warp
-// per query row and 128 elements of it, four parts at a time.
-constexpr int kJoinWarps = 8;
+// Joins the parts of the unit that was cut at the end of CTA blockIdx.x, one
+// query row per CTA.  All maxima and sums are loaded at once, then the threads
+// of a column take every ACROSS-th part, several loads in flight.
+constexpr int kJoinThreads = 256;
+constexpr int kMaxGrid = 2048;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kJoinWarps)
-    attend_join_kernel(const KVView c, const KVAttendArgs a, const float *__restrict__ part,
-                       const CutUnit *__restrict__ cut) {
-  using Cfg = SplitCfg<D, NT>;
+__global__ void __launch_bounds__(kJoinThreads)
+    attend_join_kernel(const KVView c, const KVAttendArgs a, const float *part,
+                       const CutUnit *cut) {
+  using Cfg = SplitCfg<D, NT, 1>;
   constexpr int R = Cfg::kRows;
-  constexpr int COLS = D / 4;               // float4 columns of a row
-  constexpr int ACROSS = 32 * kJoinWarps / COLS;  // threads of one column: they share the parts
-  __shared__ float4 s_sum[32 * kJoinWarps];
-  __shared__ float s_l[ACROSS];
+  constexpr int COLS = D / 4;                   // float4 columns of a row
+  constexpr int ACROSS = kJoinThreads / COLS;
+  __shared__ float4 s_sum[kJoinThreads];
+  __shared__ float s_f[kMaxGrid], s_red[2][kJoinThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const CutUnit u = cut[blockIdx.x];
   if (u.parts == 0) return;
   const SeqWork w = seq_work(c, a, u.seq, R, false);
+  if (w.weight == 0) return;
   const int head = u.unit / w.row_tiles, r = blockIdx.y;
-  const int row = (u.unit % w.row_tiles) * R + r;
+  const int64_t row = (int64_t)(u.unit % w.row_tiles) * R + r;
   if (row >= (int64_t)w.len * (c.h_q / c.h_kv)) return;
-  const int col = threadIdx.x % COLS, lane = threadIdx.x / COLS;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // part 0 is the second partial sum of CTA blockIdx.x, part p the first of CTA blockIdx.x + p
   auto at = [&](int p) {
     return part + (size_t)(2 * (blockIdx.x + p) + (p == 0 ? 1 : 0)) * Cfg::kPartFloats;
   };
   float m = -INFINITY;
-  for (int p = 0; p < u.parts; ++p) m = fmaxf(m, at(p)[R * D + r]);
-  float l = 0.f;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int p = lane; p < u.parts; p += ACROSS) {
-    const float *x = at(p);
-    const float pm = x[R * D + r], pl = x[R * D + R + r];
-    const float f = pm == -INFINITY ? (pl == 0.f ? 0.f : 1.f) : fast_exp2(pm - m);
-    l += f * pl;
-    sum = axpby4(1.f, sum, f, *reinterpret_cast<const float4 *>(x + r * D + 4 * col));
+  for (int p = tid; p < u.parts; p += kJoinThreads) {
+    s_f[p] = __ldcg(at(p) + R * D + r);
+    m = fmaxf(m, s_f[p]);
   }
-  s_sum[threadIdx.x] = sum;
-  if (col == 0) s_l[lane] = l;
-  __syncthreads();
-  if (lane == 0) {
 #pragma unroll
-    for (int k = 1; k < ACROSS; ++k) {
-      sum = axpby4(1.f, sum, 1.f, s_sum[k * COLS + col]);
-      l += s_l[k];
-    }
-    put_out(c, a, w, head, row, 4 * col, sum, l);
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) s_red[0][warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kJoinThreads / 32; ++k) m = fmaxf(m, s_red[0][k]);
+  float l = 0.f;
+  for (int p = tid; p < u.parts; p += kJoinThreads) {
+    const float pm = s_f[p], pl = __ldcg(at(p) + R * D + R + r);
+    const float f = pm == -INFINITY ? (pl == 0.f ? 0.f : 1.f) : fast_exp2(pm - m);
+    s_f[p] = f;
+    l += f * pl;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) s_red[1][warp] = l;
+  __syncthreads();
+  const int col = tid % COLS, share = tid / COLS;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int p = share; p < u.parts; p += ACROSS)
+    sum = axpby4(1.f, sum, s_f[p],
+                 __ldcg(reinterpret_cast<const float4 *>(at(p) + r * D + 4 * col)));
+  s_sum[tid] = sum;
+  __syncthreads();
+  if (share == 0) {
+#pragma unroll
+    for (int k = 1; k < ACROSS; ++k) sum = axpby4(1.f, sum, 1.f, s_sum[k * COLS + col]);
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinThreads / 32; ++k) l += s_red[1][k];
+    put_out(c, a, w, head, (int)row, 4 * col, sum, l);
   }
 }
 
 template <int CODE, int D, int NT, typename TQ>
-cudaError_t launch_split(const KVView &c, int layer, const KVAttendArgs &a, int sm_count,
-                         cudaMemPool_t work_pool, cudaStream_t s) {
-  using Cfg = SplitCfg<D, NT>;
-  constexpr int kParts = sizeof(TQ) == 4 ? 2 : 1;
+cudaError_t launch_split(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
+                         cudaStream_t s) {
+  using Cfg = SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 : 1>;
   constexpr int kMinTiles = 1;
-  constexpr int kSmem = kParts * Cfg::kRows * D * 2 +
-                        kWarps * Cfg::kRows * Cfg::kOutStride * (int)sizeof(float);
   auto kernel = attend_split_kernel<CODE, D, NT, TQ>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Cfg::kSmem);
   if (e != cudaSuccess) return e;
   // one wave, or fewer CTAs where the hints say that there are fewer tiles
   const int64_t rows = (int64_t)a.max_seqlen * (c.h_q / c.h_kv);
   const double tiles = (double)a.seq.n_seqs * c.h_kv * ((rows + Cfg::kRows - 1) / Cfg::kRows) *
                        (a.max_kv_len / kTile + 1);
-  int64_t grid = (int64_t)sm_count * Cfg::kCtas;
+  int64_t grid = (int64_t)h.sm_count * Cfg::kCtas;
+  if (grid > kMaxGrid) grid = kMaxGrid;
   if (tiles / kMinTiles < (double)grid) grid = (int64_t)(tiles / kMinTiles) + 1;
   const size_t part_bytes = (size_t)grid * 2 * Cfg::kPartFloats * sizeof(float);
   void *work = nullptr;
-  e = cudaMallocFromPoolAsync(&work, part_bytes + grid * sizeof(CutUnit), work_pool, s);
+  e = cudaMallocFromPoolAsync(&work, part_bytes + grid * sizeof(CutUnit), h.work_pool, s);
   if (e != cudaSuccess) return e;
   float *part = static_cast<float *>(work);
   CutUnit *cut = reinterpret_cast<CutUnit *>(static_cast<char *>(work) + part_bytes);
-  kernel<<<(unsigned)grid, kThreads, kSmem, s>>>(c, layer, a, kMinTiles, part, cut);
+  kernel<<<(unsigned)grid, kThreads, Cfg::kSmem, s>>>(*h.k_map, *h.v_map, c, layer, a, kMinTiles,
+                                                      part, cut);
   e = cudaGetLastError();
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, Cfg::kRows);
-    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -673,35 +748,35 @@ cudaError_t launch_split(const KVView &c, int layer, const KVAttendArgs &a, int 
 }
 
 template <int CODE, int D, int NT>
-cudaError_t by_type(const KVView &c, int layer, const KVAttendArgs &a, int sms, cudaMemPool_t pool,
+cudaError_t by_type(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
                     cudaStream_t s) {
-  return a.q_dtype == GDN_F32 ? launch_split<CODE, D, NT, float>(c, layer, a, sms, pool, s)
-                              : launch_split<CODE, D, NT, bf16>(c, layer, a, sms, pool, s);
+  return a.q_dtype == GDN_F32 ? launch_split<CODE, D, NT, float>(c, layer, a, h, s)
+                              : launch_split<CODE, D, NT, bf16>(c, layer, a, h, s);
 }
 
 template <int CODE, int D>
-cudaError_t by_rows(const KVView &c, int layer, const KVAttendArgs &a, int sms, cudaMemPool_t pool,
+cudaError_t by_rows(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
                     cudaStream_t s) {
   // eight query rows per unit where a slot has no more, else sixteen
   return (int64_t)a.max_seqlen * (c.h_q / c.h_kv) <= 8
-             ? by_type<CODE, D, 1>(c, layer, a, sms, pool, s)
-             : by_type<CODE, D, 2>(c, layer, a, sms, pool, s);
+             ? by_type<CODE, D, 1>(c, layer, a, h, s)
+             : by_type<CODE, D, 2>(c, layer, a, h, s);
 }
 
 template <int CODE>
-cudaError_t by_dim(const KVView &c, int layer, const KVAttendArgs &a, int sms, cudaMemPool_t pool,
+cudaError_t by_dim(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
                    cudaStream_t s) {
-  return c.d == 64    ? by_rows<CODE, 64>(c, layer, a, sms, pool, s)
-         : c.d == 128 ? by_rows<CODE, 128>(c, layer, a, sms, pool, s)
-                      : by_rows<CODE, 256>(c, layer, a, sms, pool, s);
+  return c.d == 64    ? by_rows<CODE, 64>(c, layer, a, h, s)
+         : c.d == 128 ? by_rows<CODE, 128>(c, layer, a, h, s)
+                      : by_rows<CODE, 256>(c, layer, a, h, s);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attend(const KVView &c, int layer, const KVAttendArgs &a, int sm_count,
-                             cudaMemPool_t work_pool, cudaStream_t s) {
-  return c.code == GDN_KV_I8 ? by_dim<GDN_KV_I8>(c, layer, a, sm_count, work_pool, s)
-                             : by_dim<GDN_KV_E4M3>(c, layer, a, sm_count, work_pool, s);
+cudaError_t launch_kv_attend(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
+                             cudaStream_t s) {
+  return c.code == GDN_KV_I8 ? by_dim<GDN_KV_I8>(c, layer, a, h, s)
+                             : by_dim<GDN_KV_E4M3>(c, layer, a, h, s);
 }
 
 }  // namespace gdn
