@@ -568,14 +568,42 @@ def gdn_kv_get_error(kv: KVCache) -> int:
     return err.value
 
 
+# A decode step's calls are a few microseconds long: the checks below read each
+# attribute once, and the stream comes as a raw handle.
+
+def _kv_stream(stream, t: torch.Tensor) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+_KV_DTYPES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
+
+
+def _kv_dtype(t: torch.Tensor) -> int:
+    code = _KV_DTYPES.get(t.dtype)
+    if code is None:
+        raise GDNError(4, f"unsupported dtype {t.dtype}")
+    return code
+
+
 def _kv_index(slot_ids, starts, cu_seqlens, tokens, name):
+    """Pointers of the index arrays, and the number of sequences."""
     n = slot_ids.numel()
-    if starts.numel() != n or (n + 1 != cu_seqlens.numel() if cu_seqlens is not None
-                               else tokens != n):
-        raise GDNError(5, f"{name} must have an entry per slot id, cu_seqlens one more "
-                          "(without it: one token per slot)")
-    return (_idx(slot_ids, "slot_ids"), _idx(starts, name), _idx(cu_seqlens, "cu_seqlens"), n,
-            tokens)
+    if slot_ids.dtype != torch.int32 or starts.dtype != torch.int32 or \
+            not slot_ids.is_contiguous() or not starts.is_contiguous():
+        raise GDNError(1, f"slot_ids and {name} must be contiguous int32 tensors")
+    if starts.numel() != n:
+        raise GDNError(5, f"{name} must have an entry per slot id")
+    if cu_seqlens is None:
+        if tokens != n:
+            raise GDNError(5, "without cu_seqlens there is one token per slot")
+        return slot_ids.data_ptr(), starts.data_ptr(), None, n
+    if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous():
+        raise GDNError(1, "cu_seqlens must be a contiguous int32 tensor")
+    if cu_seqlens.numel() != n + 1:
+        raise GDNError(5, "cu_seqlens must have one entry more than slot_ids")
+    return slot_ids.data_ptr(), starts.data_ptr(), cu_seqlens.data_ptr(), n
 
 
 def _kv_rows(kv, slot_ids, pos, k, v, cu_seqlens, max_seqlen):
@@ -586,14 +614,15 @@ def _kv_rows(kv, slot_ids, pos, k, v, cu_seqlens, max_seqlen):
     if k is not None and v is not None and (k.dtype != v.dtype or k.shape[0] != v.shape[0]):
         raise GDNError(4, "k and v must share one dtype and token count")
     tokens = some.shape[0]
-    idx = _kv_index(slot_ids, pos, cu_seqlens, tokens, "pos")
+    slots, starts, cu, n = _kv_index(slot_ids, pos, cu_seqlens, tokens, "pos")
     ld_k = 0 if k is None else _token_rows(k, d.h_kv, d.d, "k")
     ld_v = 0 if v is None else _token_rows(v, d.h_kv, d.d, "v")
     if tokens <= 1:  # the stride of a single row says nothing
         ld_k = ld_v = 0
     if max_seqlen <= 0:
         max_seqlen = 1 if cu_seqlens is None else tokens
-    return (*idx, max_seqlen, _ptr(k), ld_k, _ptr(v), ld_v, _dt(some))
+    return (slots, starts, cu, n, tokens, max_seqlen, None if k is None else k.data_ptr(), ld_k,
+            None if v is None else v.data_ptr(), ld_v, _kv_dtype(some))
 
 
 def gdn_kv_append(kv: KVCache, layer: int, slot_ids: torch.Tensor, pos: torch.Tensor,
@@ -603,18 +632,22 @@ def gdn_kv_append(kv: KVCache, layer: int, slot_ids: torch.Tensor, pos: torch.Te
     exceed h_kv * d) into positions pos[i], pos[i] + 1, ... of slot slot_ids[i]."""
     if k is None or v is None:
         raise GDNError(1, "k and v are both needed")
-    _check(load_library().gdn_kv_append(
+    status = _lib.gdn_kv_append(
         kv.handle, layer, *_kv_rows(kv, slot_ids, pos, k, v, cu_seqlens, max_seqlen),
-        _stream(stream)))
+        _kv_stream(stream, slot_ids))
+    if status:
+        _check(status)
 
 
 def gdn_kv_read(kv: KVCache, layer: int, slot_ids: torch.Tensor, pos: torch.Tensor,
                 k: Optional[torch.Tensor], v: Optional[torch.Tensor],
                 cu_seqlens: Optional[torch.Tensor] = None, max_seqlen: int = 0, stream=None):
     """Read cached tokens back as values into k, v [tokens, h_kv, d] (either may be None)."""
-    _check(load_library().gdn_kv_read(
+    status = _lib.gdn_kv_read(
         kv.handle, layer, *_kv_rows(kv, slot_ids, pos, k, v, cu_seqlens, max_seqlen),
-        _stream(stream)))
+        _kv_stream(stream, slot_ids))
+    if status:
+        _check(status)
     return k, v
 
 
@@ -631,7 +664,7 @@ def gdn_kv_attend(kv: KVCache, layer: int, slot_ids: torch.Tensor, kv_lens: torc
     if o.shape != q.shape:
         raise GDNError(5, f"o must have q's shape {tuple(q.shape)}")
     tokens = q.shape[0]
-    idx = _kv_index(slot_ids, kv_lens, cu_seqlens, tokens, "kv_lens")
+    slots, starts, cu, n = _kv_index(slot_ids, kv_lens, cu_seqlens, tokens, "kv_lens")
     ld_q, ld_o = _token_rows(q, d.h_q, d.d, "q"), _token_rows(o, d.h_q, d.d, "o")
     if tokens <= 1:
         ld_q = ld_o = 0
@@ -639,7 +672,10 @@ def gdn_kv_attend(kv: KVCache, layer: int, slot_ids: torch.Tensor, kv_lens: torc
         max_seqlen = 1 if cu_seqlens is None else tokens
     if max_kv_len <= 0:
         max_kv_len = d.max_pages * d.page_tokens
-    _check(load_library().gdn_kv_attend(
-        kv.handle, layer, *idx, max_seqlen, max_kv_len, _ptr(q), ld_q, _dt(q), _ptr(o), ld_o,
-        _dt(o), d.d ** -0.5 if scale is None else scale, _stream(stream)))
+    status = _lib.gdn_kv_attend(
+        kv.handle, layer, slots, starts, cu, n, tokens, max_seqlen, max_kv_len, q.data_ptr(), ld_q,
+        _kv_dtype(q), o.data_ptr(), ld_o, _kv_dtype(o), d.d ** -0.5 if scale is None else scale,
+        _kv_stream(stream, slot_ids))
+    if status:
+        _check(status)
     return o

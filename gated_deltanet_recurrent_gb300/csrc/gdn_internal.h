@@ -227,11 +227,34 @@ struct KVAttendArgs {
 struct KVHost {
   const CUtensorMap_st *k_map, *v_map;
   int sm_count;
-  cudaMemPool_t work_pool;
+  int device;
+  struct KVWork *work;
+};
+
+// Attention workspaces: one per stream that the handle has been used on (a
+// stream's calls are in order, so they can share it), kept until the handle is
+// destroyed.  A call that is being captured into a graph, or comes on yet
+// another stream than kStreams, gets memory that is freed on the stream after
+// it.  A kept workspace costs no allocation between the kernels of successive
+// calls: with one, their launches do not overlap (1 us of 4 for an empty pair).
+struct KVWork {
+  static constexpr int kStreams = 16;
+  cudaMemPool_t pool;
+  struct {
+    unsigned long long stream;  // cudaStreamGetId: never given twice
+    void *mem;
+    size_t bytes;
+  } kept[kStreams];
+  int n;
+  cudaError_t get(size_t bytes, cudaStream_t s, void **mem, bool *temporary);
 };
 
 cudaError_t launch_kv_attend(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
                              cudaStream_t s);
+
+// bf16 queries with many rows per KV head, on the tcgen05 tensor cores
+cudaError_t launch_kv_attend_prompt(const KVView &c, int layer, const KVAttendArgs &a,
+                                    const KVHost &h, cudaStream_t s);
 
 // Detail text of the last failure on this host thread (gdn_last_error_message).
 void set_last_message(const char *msg);

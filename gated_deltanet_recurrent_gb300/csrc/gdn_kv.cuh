@@ -4,10 +4,53 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "gdn_common.cuh"
 
 namespace gdn {
 namespace kv {
+
+// Launch as a programmatic dependent of the kernel before it on the stream: it
+// may become resident early, and waits (dependent_wait) before it touches
+// global memory until every earlier kernel is complete and visible.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s,
+                   A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// Let the next kernel of the stream be set up (it waits for this one itself),
+// and wait for those before this one.
+__device__ __forceinline__ void dependents_may_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void dependent_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Allow `kernel` `smem` bytes of dynamic shared memory, on its first launch on a
+// device (`seen`: the kernel's own, a bit per device; the call costs a launch a
+// good part of a microsecond).
+template <typename K>
+cudaError_t allow_smem(K kernel, int smem, int device, std::atomic<uint64_t> &seen) {
+  const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
+  if (seen.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) seen.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 template <int CODE>
 struct Code;  // top code, exponent range of the scale, conversions

@@ -18,8 +18,46 @@ struct gdn_kv {
   int device;
   int sm_count;
   alignas(64) CUtensorMap k_map, v_map;  // see gdn::KVHost
-  cudaMemPool_t work_pool;  // stream-ordered attention workspaces (kept until destroy)
+  gdn::KVWork work;
 };
+
+namespace gdn {
+
+cudaError_t KVWork::get(size_t bytes, cudaStream_t s, void **mem, bool *temporary) {
+  *temporary = true;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  cudaError_t e = cudaStreamIsCapturing(s, &capture);
+  if (e != cudaSuccess) return e;
+  if (capture == cudaStreamCaptureStatusNone) {
+    if ((e = cudaStreamGetId(s, &id)) != cudaSuccess) return e;
+    int i = 0;
+    while (i < n && kept[i].stream != id) ++i;
+    if (i < n && kept[i].bytes >= bytes) {
+      *temporary = false;
+      *mem = kept[i].mem;
+      return cudaSuccess;
+    }
+    if (i < kStreams) {  // a new stream, or a larger call than before
+      void *fresh = nullptr;
+      e = cudaMallocFromPoolAsync(&fresh, bytes, pool, s);
+      if (e != cudaSuccess) return e;
+      if (i < n) {
+        e = cudaFreeAsync(kept[i].mem, s);
+        if (e != cudaSuccess) return e;
+      } else {
+        ++n;
+      }
+      kept[i] = {id, fresh, bytes};
+      *temporary = false;
+      *mem = fresh;
+      return cudaSuccess;
+    }
+  }
+  return cudaMallocFromPoolAsync(mem, bytes, pool, s);
+}
+
+}  // namespace gdn
 
 namespace {
 
@@ -259,6 +297,7 @@ gdn_status gdn_kv_create(const gdn_kv_desc *desc, void *k_codes, void *v_codes,
   c->desc = *desc;
   c->device = dev;
   c->sm_count = sm_count;
+  c->work.n = 0;
   if (!encode_codes(&c->k_map, k_codes, *desc) || !encode_codes(&c->v_map, v_codes, *desc)) {
     delete c;
     return fail(GDN_ERR_CUDA, "encoding the tensor maps of the codes failed");
@@ -278,11 +317,11 @@ gdn_status gdn_kv_create(const gdn_kv_desc *desc, void *k_codes, void *v_codes,
   props.allocType = cudaMemAllocationTypePinned;
   props.location.type = cudaMemLocationTypeDevice;
   props.location.id = dev;
-  e = cudaMemPoolCreate(&c->work_pool, &props);
+  e = cudaMemPoolCreate(&c->work.pool, &props);
   if (e == cudaSuccess) {
     uint64_t keep = UINT64_MAX;  // keep freed workspace for the next call
-    e = cudaMemPoolSetAttribute(c->work_pool, cudaMemPoolAttrReleaseThreshold, &keep);
-    if (e != cudaSuccess) cudaMemPoolDestroy(c->work_pool);
+    e = cudaMemPoolSetAttribute(c->work.pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    if (e != cudaSuccess) cudaMemPoolDestroy(c->work.pool);
   }
   if (e != cudaSuccess) {
     cudaFree(err);
@@ -303,7 +342,11 @@ gdn_status gdn_kv_destroy(gdn_kv *c) {
   if (!c) return ok();
   const cudaError_t e = cudaDeviceSynchronize();
   cudaError_t e2 = cudaFree(c->view.err);
-  const cudaError_t e3 = cudaMemPoolDestroy(c->work_pool);
+  for (int i = 0; i < c->work.n; ++i) {
+    const cudaError_t ew = cudaFree(c->work.kept[i].mem);
+    if (e2 == cudaSuccess) e2 = ew;
+  }
+  const cudaError_t e3 = cudaMemPoolDestroy(c->work.pool);
   if (e2 == cudaSuccess) e2 = e3;
   delete c;
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
@@ -406,7 +449,7 @@ gdn_status gdn_kv_attend(gdn_kv *c, int32_t layer, const int32_t *slot_ids,
   const gdn::KVAttendArgs a{seq,  kv_lens, max_seqlen < 1 ? 1 : max_seqlen,
                             max_kv_len < 1 ? 1 : max_kv_len, q, o, ld_q, ld_o, q_dtype, o_dtype,
                             scale};
-  const gdn::KVHost h{&c->k_map, &c->v_map, c->sm_count, c->work_pool};
+  const gdn::KVHost h{&c->k_map, &c->v_map, c->sm_count, c->device, &c->work};
   const cudaError_t e = gdn::launch_kv_attend(c->view, layer, a, h, s);
   if (e != cudaSuccess) return cuda_fail(e, "KV attention launch");
   return ok();

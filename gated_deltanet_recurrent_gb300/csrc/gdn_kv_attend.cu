@@ -47,9 +47,9 @@ constexpr int kTile = 16 * kWarps;      // tokens
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f, kLift = 7.f;
 
-// A unit that is cut starts in CTA c and ends in CTA c + parts - 1.
+// A unit that is cut starts in CTA c and ends in CTA c + parts - 1 (parts 0: none does).
 struct CutUnit {
-  int seq, unit, parts, pad;
+  int parts, tok0, head, row0, rows, pad[3];
 };
 
 template <int D, int NT, int PARTS>
@@ -58,6 +58,15 @@ struct SplitCfg {
   // CTAs per SM that the register budget is set for
   static constexpr int kCtas = D == 64 ? (NT == 1 ? 5 : 4) : D == 128 ? (NT == 1 ? 4 : 3)
                                                                       : (NT == 1 ? 3 : 2);
+  // What a unit's start costs a CTA (its queries, its first page ids and codes), in tiles:
+  // the line of tiles is cut as if each unit had so many more (where there are many tiles per
+  // CTA; else every CTA should have as few as possible).  Measured on 64 contexts up to 8192,
+  // d = 256: a second unit takes a CTA 5 us, a tile 2.4 us.
+  static constexpr int kEntry = 512 / D;
+  // Shares of an SM's CTAs.  The warps that came first are issued first: with equal shares
+  // the three CTAs of d = 256 (NT = 1) end after 44, 47.5 and 53 us.
+  static constexpr int kShare(int order) { return D == 256 && NT == 1 ? 13 - order : 1; }
+  static constexpr int kSkewed = D == 256 && NT == 1;
   // stages of a warp's ring: what fits in an SM's shared memory with kCtas CTAs
   static constexpr int kStages = D == 64 ? 4 : D == 128 ? (NT == 1 ? 3 : 4)
                                                         : (NT == 1 ? 2 : PARTS == 1 ? 3 : 2);
@@ -74,11 +83,11 @@ struct SplitCfg {
 struct SeqWork {
   int slot, tok0, len, kv_len;
   int row_tiles, tiles;   // row tiles per KV head; token tiles per unit
-  int64_t weight;         // tiles of all its units; 0: nothing (or a bad entry)
+  int64_t weight;         // length of all its units; 0: nothing (or a bad entry)
 };
 
 __device__ __forceinline__ SeqWork seq_work(const KVView &c, const KVAttendArgs &a, int i,
-                                            int rows_per_unit, bool report) {
+                                            int rows_per_unit, int entry, bool report) {
   SeqWork w;
   w.weight = 0;
   w.slot = a.seq.slot_ids[i];
@@ -102,7 +111,7 @@ __device__ __forceinline__ SeqWork seq_work(const KVView &c, const KVAttendArgs 
   const int64_t rows = (int64_t)w.len * (c.h_q / c.h_kv);
   w.row_tiles = (int)((rows + rows_per_unit - 1) / rows_per_unit);
   w.tiles = w.kv_len > 0 ? (w.kv_len + kTile - 1) / kTile : 1;
-  w.weight = (int64_t)c.h_kv * w.row_tiles * w.tiles;
+  w.weight = (int64_t)c.h_kv * w.row_tiles * (w.tiles + entry);
   return w;
 }
 
@@ -126,6 +135,44 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *buf, int64_t *
   *total = all;
   return from;
 }
+
+// a * b / c, in 32 bits where they are enough
+__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
+  const int64_t x = a * b;
+  return x >> 32 == 0 ? (int64_t)((uint32_t)x / (uint32_t)c) : x / c;
+}
+
+// How the line of tiles is cut: segments (one, or one for each order of a CTA
+// on its SM, by share), each into equal pieces.
+template <typename Cfg>
+struct Cut {
+  int64_t total;
+  int per, segments;  // CTAs of a segment
+  __device__ __forceinline__ int64_t segment(int o) const {
+    if (segments == 1) return o ? total : 0;
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < Cfg::kCtas; ++i) {
+      if (i < o) before += Cfg::kShare(i);
+      all += Cfg::kShare(i);
+    }
+    return total * before / all;
+  }
+  // first tile of CTA i's piece
+  __device__ __forceinline__ int64_t begin(int i) const {
+    const int o = i / per;
+    const int64_t from = segment(o);
+    return o == segments ? from : from + mul_div(segment(o + 1) - from, i - o * per, per);
+  }
+  // the CTA whose piece holds tile x
+  __device__ __forceinline__ int owner(int64_t x) const {
+    int o = 0;
+    while (o + 1 < segments && segment(o + 1) <= x) ++o;
+    const int64_t from = segment(o), len = segment(o + 1) - from;
+    return o * per + (int)mul_div(x - from + 1, per, len) -
+           ((x - from + 1) * per % len == 0 ? 1 : 0);
+  }
+};
 
 __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -245,11 +292,11 @@ __device__ __forceinline__ void put_row4(bf16 *p, float4 v) {
 }
 
 // o = O / L of one row's four elements; a row without weights is zero
-__device__ __forceinline__ void put_out(const KVView &c, const KVAttendArgs &a, const SeqWork &w,
-                                        int head, int row, int d, float4 x, float l) {
+__device__ __forceinline__ void put_out(const KVView &c, const KVAttendArgs &a, int tok0, int head,
+                                        int row, int d, float4 x, float l) {
   const int group = c.h_q / c.h_kv;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t at = (int64_t)(w.tok0 + row / group) * a.ld_o +
+  const int64_t at = (int64_t)(tok0 + row / group) * a.ld_o +
                      (int64_t)(head * group + row % group) * c.d + d;
   if (a.o_dtype == GDN_F32)
     put_row4(static_cast<float *>(a.o) + at, scale4(inv, x));
@@ -261,7 +308,8 @@ template <int CODE, int D, int NT, typename TQ>
 __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 : 1>::kCtas)
     attend_split_kernel(const __grid_constant__ CUtensorMap k_map,
                         const __grid_constant__ CUtensorMap v_map, const KVView c, const int layer,
-                        const KVAttendArgs a, const int min_tiles, float *__restrict__ part,
+                        const KVAttendArgs a, const int entry, const bool full_grid,
+                        float *__restrict__ part,
                         CutUnit *__restrict__ cut) {
   constexpr int PARTS = sizeof(TQ) == 4 ? 2 : 1;  // binary16 parts of queries and weights
   using Cfg = SplitCfg<D, NT, PARTS>;
@@ -278,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
   __shared__ int s_found;
   __shared__ __align__(8) uint64_t s_full[kWarps][S];
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  kv::dependents_may_launch();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int n = a.seq.n_seqs, cta = blockIdx.x;
   const int group = c.h_q / c.h_kv;
@@ -290,21 +338,22 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
   }
 
   // ---- this CTA's piece of the line of tiles ----
-  if (tid == 0) {
-    cut[cta].parts = 0;
-    s_found = -1;
-  }
+  if (tid == 0) s_found = -1;
+  kv::dependent_wait();
+  if (tid == 0) cut[cta].parts = 0;
   const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
   int64_t mine = 0, total;
-  for (int i = i0; i < i1; ++i) mine += seq_work(c, a, i, R, cta == 0).weight;
+  for (int i = i0; i < i1; ++i) mine += seq_work(c, a, i, R, entry, cta == 0).weight;
   int64_t from = block_scan(mine, s_buf, &total);
-  const int64_t wanted = (total + min_tiles - 1) / min_tiles;
-  const int64_t ctas = wanted < gridDim.x ? wanted : gridDim.x;
+  const int ctas = (int)min(total, (int64_t)gridDim.x);
   if (cta >= ctas) return;
-  const int64_t begin = cta * total / ctas, end = (cta + 1) * total / ctas;
+  // (a full grid has sm_count * kCtas CTAs; CTA i is the (i / sm_count)-th of its SM)
+  const bool skewed = Cfg::kSkewed && full_grid && ctas == (int)gridDim.x && total >= 4 * ctas;
+  const Cut<Cfg> cuts{total, skewed ? ctas / Cfg::kCtas : ctas, skewed ? Cfg::kCtas : 1};
+  const int64_t begin = cuts.begin(cta), end = cuts.begin(cta + 1);
   if (from <= begin && begin < from + mine)
     for (int i = i0; i < i1; ++i) {
-      const int64_t x = seq_work(c, a, i, R, false).weight;
+      const int64_t x = seq_work(c, a, i, R, entry, false).weight;
       if (from <= begin && begin < from + x) {
         s_found = i;
         s_found_off = begin - from;
@@ -315,20 +364,32 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
 
   int seq = s_found;
   if (seq < 0) return;  // (only if the lengths changed under the kernel)
-  SeqWork w = seq_work(c, a, seq, R, false);
+  SeqWork w = seq_work(c, a, seq, R, entry, false);
   if (w.weight == 0) return;
-  int unit = (int)(s_found_off / w.tiles), tile = (int)(s_found_off % w.tiles);
-  uint32_t used = 0;  // stages that this warp has filled so far
+  int unit, place;  // place: in the unit, its entry first
+  {
+    const int64_t off = s_found_off;
+    const int len = w.tiles + entry;
+    unit = (int)(off >> 32 == 0 ? (uint32_t)off / (uint32_t)len : off / len);
+    place = (int)(off - (int64_t)unit * len);
+  }
+  int at_stage = 0;      // the ring's next stage, and the phase of its barrier
+  uint32_t phase = 0;
   bool ok = true;
   for (int64_t at = begin; at < end;) {
     if (unit == c.h_kv * w.row_tiles) {  // the next sequence that has work
       do {
         if (++seq >= n) return;
-        w = seq_work(c, a, seq, R, false);
+        w = seq_work(c, a, seq, R, entry, false);
       } while (w.weight == 0);
       unit = 0;
     }
-    const int n_here = (int)min((int64_t)(w.tiles - tile), end - at);
+    const int64_t unit_end = at + w.tiles + entry - place;
+    const int tile = max(place - entry, 0);
+    const int n_here = (int)(min(unit_end, end) - at) + place - entry - tile;
+    at = min(unit_end, end);
+    place = 0;
+    if (n_here <= 0) continue;  // the piece ends within the unit's entry
     const int head = unit / w.row_tiles, row0 = (unit % w.row_tiles) * R;
     const int rows = (int)min((int64_t)w.len * group - row0, (int64_t)R);
     const int pos0 = w.kv_len - w.len + 1;            // positions open to token 0
@@ -338,30 +399,33 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
     const int tok0 = tile * kTile + 16 * warp;
     const int steps = tok0 < last ? (last - tok0 + kTile - 1) / kTile : 0;
 
-    // A step's page (any page, if the id is bad: its tokens are masked).
-    auto page_id = [&](int i) { return table[(tok0 + i * kTile) >> c.page_log2]; };
-    auto fill = [&](int i, int id) {
-      const uint32_t u = used + i;
+    // A step's block of codes, or -1 (reported) if its page id is bad: block 0 is read in its
+    // place, and its tokens are masked.
+    const int blk0 = layer * c.n_pages * c.h_kv + head;
+    auto block_of = [&](int i) {
+      const int id = table[(tok0 + i * kTile) >> c.page_log2];
+      return (uint32_t)id < (uint32_t)c.n_pages ? id * c.h_kv + blk0 : -1;
+    };
+    auto fill = [&](int i, int blk, int stage) {
       if (lane == 0) {
-        const bool bad = id < 0 || id >= c.n_pages;
-        if (bad) raise_error(c.err, GDN_DEVERR_PAGE);
-        const int blk = (int)c.block(layer, bad ? 0 : id, head);
+        if (blk < 0) raise_error(c.err, GDN_DEVERR_PAGE);
         const int row = (tok0 + i * kTile) & (c.page_tokens - 1);
-        unsigned char *dst = ring + (u % S) * Cfg::kStage;
-        uint64_t *bar = &full[u % S];
+        unsigned char *dst = ring + stage * Cfg::kStage;
+        uint64_t *bar = &full[stage];
         mbar_arrive_expect_tx(bar, Cfg::kStage);
 #pragma unroll
-        for (int x = 0; x < D; x += 128) tma_rows(dst + 16 * x, &k_map, x, row, blk, bar);
+        for (int x = 0; x < D; x += 128) tma_rows(dst + 16 * x, &k_map, x, row, max(blk, 0), bar);
 #pragma unroll
-        for (int x = 0; x < D; x += 128) tma_rows(dst + 16 * D + 16 * x, &v_map, x, row, blk, bar);
+        for (int x = 0; x < D; x += 128)
+          tma_rows(dst + 16 * D + 16 * x, &v_map, x, row, max(blk, 0), bar);
       }
     };
     int ids[S];
 #pragma unroll
-    for (int i = 0; i < S; ++i) ids[i] = i < steps ? page_id(i) : 0;
+    for (int i = 0; i < S; ++i) ids[i] = i < steps ? block_of(i) : -1;
 #pragma unroll
     for (int i = 0; i < S; ++i)
-      if (i < steps) fill(i, ids[i]);
+      if (i < steps) fill(i, ids[i], at_stage + i < S ? at_stage + i : at_stage + i - S);
 
     // ---- queries: scaled to [1, 2) by a power of two, binary16, in the B layout ----
     constexpr int E = D / 32;
@@ -423,30 +487,40 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
         for (int z = 0; z < 4; ++z) o[x][y][z] = 0.f;
     // scales of the next step, loaded a step ahead
     float next_k = 0.f, next_v = 0.f;
-    auto scales = [&](int id) {
-      const int64_t blk = c.block(layer, id < 0 || id >= c.n_pages ? 0 : id, head);
-      next_k = c.k_scale[blk];
-      next_v = c.v_scale[blk];
+    auto scales = [&](int blk) {
+      next_k = c.k_scale[max(blk, 0)];
+      next_v = c.v_scale[max(blk, 0)];
     };
     if (steps > 0) scales(ids[0]);
-    int ahead = S < steps ? page_id(S) : 0;  // page of step i + S
+    int ahead = S < steps ? block_of(S) : -1;  // block of step i + S
     for (int i = 0; i < steps && ok; ++i) {
-      const uint32_t u = used + i;
-      const int tok = tok0 + i * kTile;
-      const unsigned char *sK = ring + (u % S) * Cfg::kStage, *sV = sK + 16 * D;
-      const bool valid = ids[0] >= 0 && ids[0] < c.n_pages;
+      const int tok = tok0 + i * kTile, stage = at_stage;
+      const unsigned char *sK = ring + stage * Cfg::kStage, *sV = sK + 16 * D;
+      const bool valid = ids[0] >= 0;
       const float k_scale = next_k;
-      const int v_exp = kv::scale_exponent<CODE>(next_v);
+      // the V scale is 2^e: e, and 2^-e (a block that only stands in for a bad page: 1)
+      const uint32_t v_bits = valid ? __float_as_uint(next_v) & 0x7f800000u : 0x3f800000u;
+      const float e = (float)((int)(v_bits >> 23) - 127);
+      const float unscale = __uint_as_float(0x7f000000u - v_bits);
 #pragma unroll
       for (int x = 0; x + 1 < S; ++x) ids[x] = ids[x + 1];
       ids[S - 1] = ahead;
       if (i + 1 < steps) scales(ids[0]);
-      if (i + S + 1 < steps) ahead = page_id(i + S + 1);
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[u % S], (u / S) & 1));
+      if (i + S + 1 < steps) ahead = block_of(i + S + 1);
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase));
+      if (++at_stage == S) {
+        at_stage = 0;
+        phase ^= 1;
+      }
       if (!ok) {  // report it, and give the copies in flight (with limits again) time to land
         if (lane == 0) raise_error(c.err, GDN_DEVERR_TIMEOUT);
-        for (int x = i + 1; x < min(steps, i + S); ++x)
-          mbar_wait_bounded(&full[(used + x) % S], ((used + x) / S) & 1);
+        for (int x = i + 1; x < min(steps, i + S); ++x) {
+          mbar_wait_bounded(&full[at_stage], phase);
+          if (++at_stage == S) {
+            at_stage = 0;
+            phase ^= 1;
+          }
+        }
         break;
       }
 
@@ -478,9 +552,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
             }
         }
       }
-
       // weights
-      const float e = (float)v_exp, unscale = kv::pow2f(-v_exp);
       const bool masked = tok + 16 > lim_min || !valid;
       bool raise = false;
       float peak[NT][2];
@@ -566,12 +638,11 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
           }
       }
       __syncwarp();  // the stage has been read by every lane
-      if (i + S < steps) fill(i + S, ids[S - 1]);
+      if (i + S < steps) fill(i + S, ids[S - 1], stage);
     }
     // the rings are free after this: the sums take their place
     ok = __syncthreads_and(ok);
     if (!ok) return;
-    used += steps;
 
     // ---- join the warps ----
 #pragma unroll
@@ -594,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
                           o[2 * j + 1][x][2 + y]);
       }
     __syncthreads();
-    const bool whole = tile == 0 && n_here == w.tiles;
+    const bool whole = n_here == w.tiles;
     float *my_part = part + (size_t)(2 * cta + (tile == 0 ? 1 : 0)) * Cfg::kPartFloats;
     for (int x = tid; x < rows * (D / 4); x += kThreads) {
       const int r = x / (D / 4), d = 4 * (x % (D / 4));
@@ -613,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
                                                        d));
       }
       if (whole) {
-        put_out(c, a, w, head, row0 + r, d, sum, l);
+        put_out(c, a, w.tok0, head, row0 + r, d, sum, l);
       } else {
         *reinterpret_cast<float4 *>(my_part + r * D + d) = sum;
         if (d == 0) {
@@ -622,23 +693,18 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
         }
       }
     }
-    if (tid == 0 && !whole && tile == 0) {
-      // the CTA whose piece holds this unit's last tile
-      const int64_t end_cta = ((at + w.tiles) * ctas + total - 1) / total;
-      cut[cta] = CutUnit{seq, unit, (int)(end_cta - cta), 0};
-    }
+    if (tid == 0 && !whole && tile == 0)
+      cut[cta] = CutUnit{cuts.owner(unit_end - 1) - cta + 1, w.tok0, head, row0, rows, {0, 0, 0}};
     // the next unit's copies (async proxy) overwrite what was written here
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
-    at += n_here;
-    tile = 0;
     ++unit;
   }
 }
 
 // Joins the parts of the unit that was cut at the end of CTA blockIdx.x, one
-// query row per CTA.  All maxima and sums are loaded at once, then the threads
-// of a column take every ACROSS-th part, several loads in flight.
+// query row per CTA.  Maxima and sums of all parts, and the first outputs, are
+// loaded at once: what counts is how few loads wait for one another.
 constexpr int kJoinThreads = 256;
 constexpr int kMaxGrid = 2048;
 
@@ -649,26 +715,34 @@ __global__ void __launch_bounds__(kJoinThreads)
   using Cfg = SplitCfg<D, NT, 1>;
   constexpr int R = Cfg::kRows;
   constexpr int COLS = D / 4;                   // float4 columns of a row
-  constexpr int ACROSS = kJoinThreads / COLS;
+  constexpr int ACROSS = kJoinThreads / COLS;   // threads of a column share the parts
+  constexpr int FIRST = 4;                      // outputs that a thread loads ahead
   __shared__ float4 s_sum[kJoinThreads];
   __shared__ float s_f[kMaxGrid], s_red[2][kJoinThreads / 32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  kv::dependents_may_launch();
+  kv::dependent_wait();
   const CutUnit u = cut[blockIdx.x];
-  if (u.parts == 0) return;
-  const SeqWork w = seq_work(c, a, u.seq, R, false);
-  if (w.weight == 0) return;
-  const int head = u.unit / w.row_tiles, r = blockIdx.y;
-  const int64_t row = (int64_t)(u.unit % w.row_tiles) * R + r;
-  if (row >= (int64_t)w.len * (c.h_q / c.h_kv)) return;
+  const int r = blockIdx.y;
+  if (u.parts == 0 || r >= u.rows) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int col = tid % COLS, share = tid / COLS;
   // part 0 is the second partial sum of CTA blockIdx.x, part p the first of CTA blockIdx.x + p
   auto at = [&](int p) {
     return part + (size_t)(2 * (blockIdx.x + p) + (p == 0 ? 1 : 0)) * Cfg::kPartFloats;
   };
-  float m = -INFINITY;
+  auto out = [&](int p) {
+    return __ldcg(reinterpret_cast<const float4 *>(at(p) + r * D + 4 * col));
+  };
+  float4 first[FIRST];
+#pragma unroll
+  for (int x = 0; x < FIRST; ++x)
+    if (share + x * ACROSS < u.parts) first[x] = out(share + x * ACROSS);
+  float m = -INFINITY, own_m = -INFINITY, own_l = 0.f;
   for (int p = tid; p < u.parts; p += kJoinThreads) {
-    s_f[p] = __ldcg(at(p) + R * D + r);
-    m = fmaxf(m, s_f[p]);
+    own_m = __ldcg(at(p) + R * D + r);
+    own_l = __ldcg(at(p) + R * D + R + r);
+    s_f[p] = own_m;
+    m = fmaxf(m, own_m);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -678,7 +752,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int k = 0; k < kJoinThreads / 32; ++k) m = fmaxf(m, s_red[0][k]);
   float l = 0.f;
   for (int p = tid; p < u.parts; p += kJoinThreads) {
-    const float pm = s_f[p], pl = __ldcg(at(p) + R * D + R + r);
+    const float pm = s_f[p];
+    const float pl = u.parts <= kJoinThreads ? own_l : __ldcg(at(p) + R * D + R + r);
     const float f = pm == -INFINITY ? (pl == 0.f ? 0.f : 1.f) : fast_exp2(pm - m);
     s_f[p] = f;
     l += f * pl;
@@ -687,12 +762,13 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if (lane == 0) s_red[1][warp] = l;
   __syncthreads();
-  const int col = tid % COLS, share = tid / COLS;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int x = 0; x < FIRST; ++x)
+    if (share + x * ACROSS < u.parts) sum = axpby4(1.f, sum, s_f[share + x * ACROSS], first[x]);
 #pragma unroll 8
-  for (int p = share; p < u.parts; p += ACROSS)
-    sum = axpby4(1.f, sum, s_f[p],
-                 __ldcg(reinterpret_cast<const float4 *>(at(p) + r * D + 4 * col)));
+  for (int p = share + FIRST * ACROSS; p < u.parts; p += ACROSS)
+    sum = axpby4(1.f, sum, s_f[p], out(p));
   s_sum[tid] = sum;
   __syncthreads();
   if (share == 0) {
@@ -701,7 +777,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     l = 0.f;
 #pragma unroll
     for (int k = 0; k < kJoinThreads / 32; ++k) l += s_red[1][k];
-    put_out(c, a, w, head, (int)row, 4 * col, sum, l);
+    put_out(c, a, u.tok0, u.head, u.row0 + r, 4 * col, sum, l);
   }
 }
 
@@ -709,41 +785,30 @@ template <int CODE, int D, int NT, typename TQ>
 cudaError_t launch_split(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
                          cudaStream_t s) {
   using Cfg = SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 : 1>;
-  constexpr int kMinTiles = 1;
   auto kernel = attend_split_kernel<CODE, D, NT, TQ>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg::kSmem);
+  static std::atomic<uint64_t> seen{0};
+  cudaError_t e = kv::allow_smem(kernel, Cfg::kSmem, h.device, seen);
   if (e != cudaSuccess) return e;
   // one wave, or fewer CTAs where the hints say that there are fewer tiles
   const int64_t rows = (int64_t)a.max_seqlen * (c.h_q / c.h_kv);
   const double tiles = (double)a.seq.n_seqs * c.h_kv * ((rows + Cfg::kRows - 1) / Cfg::kRows) *
                        (a.max_kv_len / kTile + 1);
-  int64_t grid = (int64_t)h.sm_count * Cfg::kCtas;
-  if (grid > kMaxGrid) grid = kMaxGrid;
-  if (tiles / kMinTiles < (double)grid) grid = (int64_t)(tiles / kMinTiles) + 1;
+  const int64_t most = (int64_t)h.sm_count * Cfg::kCtas;
+  const int64_t grid = tiles < (double)most ? (int64_t)tiles : most < kMaxGrid ? most : kMaxGrid;
+  const int entry = tiles >= 8. * (double)most ? Cfg::kEntry : 0;
   const size_t part_bytes = (size_t)grid * 2 * Cfg::kPartFloats * sizeof(float);
   void *work = nullptr;
-  e = cudaMallocFromPoolAsync(&work, part_bytes + grid * sizeof(CutUnit), h.work_pool, s);
+  bool temporary;
+  e = h.work->get(part_bytes + grid * sizeof(CutUnit), s, &work, &temporary);
   if (e != cudaSuccess) return e;
   float *part = static_cast<float *>(work);
   CutUnit *cut = reinterpret_cast<CutUnit *>(static_cast<char *>(work) + part_bytes);
-  kernel<<<(unsigned)grid, kThreads, Cfg::kSmem, s>>>(*h.k_map, *h.v_map, c, layer, a, kMinTiles,
-                                                      part, cut);
-  e = cudaGetLastError();
-  if (e == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, Cfg::kRows);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attend_join_kernel<D, NT>, c, a,
-                           static_cast<const float *>(part), static_cast<const CutUnit *>(cut));
-  }
-  const cudaError_t ef = cudaFreeAsync(work, s);
+  e = kv::launch(kernel, dim3((unsigned)grid), kThreads, Cfg::kSmem, s, *h.k_map, *h.v_map, c,
+                 layer, a, entry, grid == most, part, cut);
+  if (e == cudaSuccess)
+    e = kv::launch(attend_join_kernel<D, NT>, dim3((unsigned)grid, Cfg::kRows), kJoinThreads, 0, s,
+                   c, a, static_cast<const float *>(part), static_cast<const CutUnit *>(cut));
+  const cudaError_t ef = temporary ? cudaFreeAsync(work, s) : cudaSuccess;
   return e != cudaSuccess ? e : ef;
 }
 
@@ -775,6 +840,15 @@ cudaError_t by_dim(const KVView &c, int layer, const KVAttendArgs &a, const KVHo
 
 cudaError_t launch_kv_attend(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
                              cudaStream_t s) {
+  // bf16 calls with more than 32 query rows per KV head go to the tcgen05 kernel, unless the
+  // whole call is small: its units take longer to set up, and it has fewer of them.  Sequences
+  // x KV heads x 16-row tiles x context, split / tcgen05 in us: 16 x 9 x 128 = 18 K 22 / 29,
+  // 16 x 5 x 512 = 41 K 28 / 26, 64 x 3 x 512 = 98 K 31 / 25, 16 x 5 x 8192 = 655 K 82 / 51;
+  // with 24 and 20 rows, 128 x 2 x 8192 217 / 228 and 512 x 2 x 8192 486 / 596.
+  const int64_t rows = (int64_t)a.max_seqlen * (c.h_q / c.h_kv);
+  if (a.q_dtype == GDN_BF16 && rows > 32 &&
+      (double)a.seq.n_seqs * c.h_kv * ((rows + 15) / 16) * a.max_kv_len >= 65536.)
+    return launch_kv_attend_prompt(c, layer, a, h, s);
   return c.code == GDN_KV_I8 ? by_dim<GDN_KV_I8>(c, layer, a, h, s)
                              : by_dim<GDN_KV_E4M3>(c, layer, a, h, s);
 }

@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(512)
     append_tile_kernel(KVView c, int layer, SeqIndex seq, const int32_t *__restrict__ pos,
                        KVRows rows) {
   __shared__ float s_max[16];
+  kv::dependents_may_launch();
+  kv::dependent_wait();
   const int head = blockIdx.y >> 1, side = blockIdx.y & 1;
   const int tid = threadIdx.x, nt = blockDim.x;
   int slot, tok0, len, first;
@@ -182,6 +184,8 @@ template <typename T, int CODE>
 __global__ void __launch_bounds__(32 * kAppendWarps)
     append_warp_kernel(KVView c, int layer, SeqIndex seq, const int32_t *__restrict__ pos,
                        KVRows rows) {
+  kv::dependents_may_launch();
+  kv::dependent_wait();
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   const int per_seq = 2 * c.h_kv;
@@ -253,6 +257,8 @@ __device__ __forceinline__ void put4<bf16>(bf16 *p, float4 v) {
 template <typename T, int CODE>
 __global__ void __launch_bounds__(kReadThreads)
     read_kernel(KVView c, int layer, SeqIndex seq, const int32_t *__restrict__ pos, KVRows rows) {
+  kv::dependents_may_launch();
+  kv::dependent_wait();
   const int side = blockIdx.y;
   if ((side ? rows.v : rows.k) == nullptr) return;
   int slot, tok0, len, first;
@@ -289,18 +295,16 @@ cudaError_t append_t(const KVView &c, int layer, const SeqIndex &seq, const int3
                      int max_seqlen, const KVRows &rows, cudaStream_t s) {
   if (max_seqlen <= 8) {
     const int64_t units = (int64_t)seq.n_seqs * 2 * c.h_kv;
-    append_warp_kernel<T, CODE>
-        <<<(unsigned)((units + kAppendWarps - 1) / kAppendWarps), 32 * kAppendWarps, 0, s>>>(
-            c, layer, seq, pos, rows);
-    return cudaGetLastError();
+    return kv::launch(append_warp_kernel<T, CODE>,
+                      dim3((unsigned)((units + kAppendWarps - 1) / kAppendWarps)),
+                      32 * kAppendWarps, 0, s, c, layer, seq, pos, rows);
   }
   const int threads = c.page_tokens * c.d / (8 * kVec) < 32 ? 32 : c.page_tokens * c.d / (8 * kVec);
   // an unaligned range of max_seqlen tokens touches one page more than an aligned one
   const int64_t pages = ((int64_t)max_seqlen + c.page_tokens - 2) / c.page_tokens + 1;
   dim3 grid((unsigned)(pages < c.max_pages ? pages : c.max_pages), (unsigned)(2 * c.h_kv),
             (unsigned)seq.n_seqs);
-  append_tile_kernel<T, CODE><<<grid, threads, 0, s>>>(c, layer, seq, pos, rows);
-  return cudaGetLastError();
+  return kv::launch(append_tile_kernel<T, CODE>, grid, threads, 0, s, c, layer, seq, pos, rows);
 }
 
 template <typename T, int CODE>
@@ -309,9 +313,8 @@ cudaError_t read_t(const KVView &c, int layer, const SeqIndex &seq, const int32_
   const int64_t work = (int64_t)max_seqlen * c.h_kv * (c.d / 16);
   int64_t bx = (work + kReadThreads - 1) / kReadThreads;
   if (bx > 65535) bx = 65535;
-  read_kernel<T, CODE><<<dim3((unsigned)bx, 2, (unsigned)seq.n_seqs), kReadThreads, 0, s>>>(
-      c, layer, seq, pos, rows);
-  return cudaGetLastError();
+  return kv::launch(read_kernel<T, CODE>, dim3((unsigned)bx, 2, (unsigned)seq.n_seqs),
+                    kReadThreads, 0, s, c, layer, seq, pos, rows);
 }
 
 }  // namespace

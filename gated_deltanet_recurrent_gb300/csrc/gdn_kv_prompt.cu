@@ -1,0 +1,908 @@
+// Causal grouped-query attention over the 8-bit KV cache on the 5th-generation
+// tensor cores: bf16 calls with many query rows per KV head (prompts, and
+// drafts of wide groups).  Mathematics, scaling and masking are those of
+// gdn_kv_attend.cu; this file is about feeding tcgen05.
+//
+// A unit is 128 * MT query rows (token-major, the query heads of one KV head
+// side by side) of one sequence and KV head; KV tiles have 128 tokens.  Per
+// tile and 128 rows: S = Q K^T (128 x 128, operands in shared memory), softmax
+// weights P back into S's TMEM columns as binary16, O += P V (P from TMEM, V in
+// shared memory as an MN-major operand, so it needs no transposition).
+//
+// Roles, joined by mbarriers:
+//   softmax    4 * MT warps, one thread per query row: S from TMEM, running
+//              maximum and sum, P to TMEM; raises the maximum (and rescales O in
+//              TMEM) only when it must, which after a few tiles is rare
+//   converters CW warps: 16 codes per load, to binary16 (exact), into a ring of
+//              slots of 128 tokens x min(d, 128) in the 128-byte swizzle, K and
+//              V slots in the order of the MMAs; their loads run PF slots ahead
+//   MMA        one thread; MT = 2: the two row tiles alternate, so one's softmax
+//              runs under the other's products; MT = 1: S is double-buffered
+//              and S of the next tile is computed under the softmax of this one
+//   pages      one warp: page ids and scales of the coming tiles
+//
+// What bounds it: per tile and 128 rows the tensor pipe needs d * 8 cycles (4096
+// products a cycle), shared memory d * 6 for the operands plus the converted
+// codes' writes, d * 4 / MT (128 bytes a cycle).  MT = 2 halves the conversion
+// per row; d = 256 has room in TMEM (O 256 columns, two S) for MT = 1 only.
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "gdn_kv.cuh"
+#include "gdn_tc.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kBN = 128;                 // tokens of a KV tile
+constexpr int kGroups = kBN / 16;        // page-aligned token groups of a tile
+constexpr int kInfo = 8;                 // tiles of page info in flight
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f, kLift = 7.f;
+
+template <int D, int MT>
+struct PromptCfg {
+  static constexpr int kRows = 128 * MT;
+  static constexpr int DC = D < 128 ? D : 128;          // d range of a slot
+  static constexpr int kHalves = D / DC;                // slots of a K or V tile
+  static constexpr int kSlot = kBN * DC * 2;            // bytes
+  static constexpr int kSlots = 4;
+  static constexpr int kQTile = 128 * D * 2;
+  static constexpr int kConvWarps = MT == 2 ? 4 : 8;
+  static constexpr int kConvTeams = MT == 2 ? 1 : 2;    // teams take the slots in turn
+  static constexpr int kPrefetch = 2;                   // of a team's own slots
+  static constexpr int kThreads = 512;  // warps 12..15: MMA, pages, two idle
+  // registers per thread of each role; with 512 threads a launch has 128 each, and the
+  // shares' sum may not exceed that: MT = 2: 256 * 168 + 128 * 112 + 128 * 64 = 65,536;
+  // MT = 1: 128 * 184 + 256 * 112 + 128 * 64 = 60,416
+  static constexpr int kSoftRegs = MT == 2 ? 168 : 184;
+  static constexpr int kConvRegs = 112;
+  static constexpr int kMiscRegs = 64;
+  static constexpr int kSmem = MT * kQTile + kSlots * kSlot + 1024;
+  // TMEM columns: S (MT tiles, or two buffers), then O
+  static constexpr int kO = 2 * kBN;
+  static constexpr int kTmem = kO + MT * D <= 256 ? 256 : 512;
+  static constexpr int kPartFloats = kRows * (D + 2);
+};
+
+struct Unit {
+  int slot, tok0, len, kv_len, head, row0, rows;
+  int tiles, begin, end;  // KV tiles in all, and this split's
+};
+
+// f16 operands, f32 accumulator; B MN-major if `mn`
+__host__ __device__ constexpr uint32_t idesc_f16(int n, bool mn) {
+  return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Shared-memory operands in the 128-byte swizzle: 128-byte rows of 64 elements,
+// 8-row atoms (SBO 1024).  K-major (K and Q: rows are tokens or queries) or
+// MN-major (V: rows are tokens, the K index; panels of 64 d are 16 KiB apart,
+// LBO).  The low word takes the address; steps add to it.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) {
+  return saddr >> 4 | (lbo >> 4) << 16;
+}
+__device__ __forceinline__ uint64_t desc(uint32_t low) {
+  return (uint64_t)kDescHigh << 32 | low;
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// (a0, a1) * b + c and (a0, a1) + (b0, b1) on register pairs
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
+      "mov.b64 z, {%5, %5};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+// one lane of the warp (all 32 call it), in a form that keeps the warp's code uniform
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 32 columns of this thread's TMEM lane; the caller waits
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Four codes of a word as two binary16 pairs.  Along d, element j of four sits
+// at place(j); queries are laid out the same way and outputs are read back so.
+template <int CODE>
+struct Widen;
+template <>
+struct Widen<GDN_KV_I8> {
+  static __host__ __device__ constexpr int place(int j) { return (j & 1) * 2 + (j >> 1); }
+  static __device__ __forceinline__ uint32_t one(uint32_t bytes) {
+    uint32_t y;
+    asm("sub.rn.f16x2 %0, %1, %2;"
+        : "=r"(y)
+        : "r"((bytes & 0x00ff00ffu) ^ 0x64806480u), "r"(0x64806480u));
+    return y;
+  }
+  static __device__ __forceinline__ void four(uint32_t w, uint32_t &a, uint32_t &b) {
+    a = one(w);
+    b = one(w >> 8);
+  }
+};
+template <>
+struct Widen<GDN_KV_E4M3> {
+  static __host__ __device__ constexpr int place(int j) { return j; }
+  static __device__ __forceinline__ void four(uint32_t w, uint32_t &a, uint32_t &b) {
+    a = kv::e4m3x2_to_half2((uint16_t)(w & 0xffffu));
+    b = kv::e4m3x2_to_half2((uint16_t)(w >> 16));
+  }
+};
+
+// Unit `u` (row tile, from the heaviest) of sequence i and KV head `head`, and
+// the tiles of split `split` of `splits`.  False: there is none.
+__device__ __forceinline__ bool find_unit(const KVView &c, const KVAttendArgs &a, int i, int head,
+                                          int64_t u, int rows_per_unit, int split, int splits,
+                                          bool report, Unit *w) {
+  const int group = c.h_q / c.h_kv;
+  w->slot = a.seq.slot_ids[i];
+  w->kv_len = a.kv_lens[i];
+  w->tok0 = i;
+  int hi = i + 1;
+  if (a.seq.cu_seqlens != nullptr) {
+    w->tok0 = a.seq.cu_seqlens[i];
+    hi = a.seq.cu_seqlens[i + 1];
+  }
+  w->len = hi - w->tok0;
+  if (w->slot < 0 || w->slot >= c.n_slots) {
+    if (report) raise_error(c.err, GDN_DEVERR_SLOT);
+    return false;
+  }
+  if (w->tok0 < 0 || hi < w->tok0 || hi > a.seq.total_tokens || w->kv_len < 0 ||
+      w->kv_len > c.capacity()) {
+    if (report) raise_error(c.err, GDN_DEVERR_SEQ);
+    return false;
+  }
+  const int64_t all = (int64_t)w->len * group;
+  const int64_t units = (all + rows_per_unit - 1) / rows_per_unit;
+  if (u >= units) return false;
+  w->head = head;
+  w->row0 = (int)((units - 1 - u) * rows_per_unit);
+  w->rows = (int)min(all - w->row0, (int64_t)rows_per_unit);
+  const int lim = w->kv_len - w->len + 1 + (w->row0 + w->rows - 1) / group;
+  w->tiles = lim > 0 ? (lim + kBN - 1) / kBN : 0;
+  w->begin = (int)((int64_t)w->tiles * split / splits);
+  w->end = (int)((int64_t)w->tiles * (split + 1) / splits);
+  return true;
+}
+
+__device__ __forceinline__ void put8(float *p, const float *v) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void put8(bf16 *p, const float *v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int CODE, int D, int MT>
+__global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
+    attend_prompt_kernel(const KVView c, const int layer, const KVAttendArgs a, const int splits,
+                         const int hinted_units, float *__restrict__ part) {
+  using Cfg = PromptCfg<D, MT>;
+  constexpr int R = Cfg::kRows, NS = Cfg::kSlots, H = Cfg::kHalves, CW = Cfg::kConvWarps;
+  constexpr int TEAMS = Cfg::kConvTeams;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char *sQ = smem;                             // [MT][D / 64][128 rows][128 bytes]
+  unsigned char *sKV = smem + MT * Cfg::kQTile;         // [NS][DC / 64][128 tokens][128 bytes]
+  __shared__ __align__(8) uint64_t slot_full[NS], slot_empty[NS], info_full[kInfo],
+      info_empty[kInfo], s_full[2], p_full[MT], pv_done[MT], q_full, drain;
+  __shared__ int s_blk[kInfo][kGroups], s_plain[kInfo];
+  __shared__ float s_ks[kInfo][kGroups], s_ve[kInfo][kGroups], s_un[kInfo][kGroups];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_abort;
+
+  kv::dependents_may_launch();
+  kv::dependent_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // blocks are ordered by row tile, the heaviest of every sequence and head first
+  const int heads = a.seq.n_seqs * c.h_kv, z = blockIdx.x % heads, split = blockIdx.y;
+  const int i = z / c.h_kv, head = z % c.h_kv, group = c.h_q / c.h_kv;
+  const int64_t u0 = blockIdx.x / heads;
+  Unit w;
+  if (!find_unit(c, a, i, head, u0, R, 0, 1, tid + split + (int)u0 == 0, &w)) return;
+  constexpr int kConv = 4 * MT, kMma = kConv + CW, kPages = kMma + 1;
+  static_assert(kMma == 12, "four warpgroups: softmax and converters, then MMA and pages");
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(&slot_full[i], CW / TEAMS), mbar_init(&slot_empty[i], 1);
+    for (int i = 0; i < kInfo; ++i)
+      mbar_init(&info_full[i], 1),
+          mbar_init(&info_empty[i], 2 * H * (CW / TEAMS) + 4 * MT);  // its slots' loads, softmax
+    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1);
+    for (int i = 0; i < MT; ++i) mbar_init(&p_full[i], 4), mbar_init(&pv_done[i], 1);
+    mbar_init(&q_full, 4 * MT);
+    mbar_init(&drain, 1);
+    s_abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == kMma) tc::tmem_alloc(&tmem_slot, Cfg::kTmem);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  volatile int *abort_flag = &s_abort;
+  // A wait that gives up ends the kernel's work: every role stops at its next wait.
+  auto wait = [&](uint64_t *bar, uint32_t phase) {
+    if (mbar_wait_bounded(bar, phase & 1) && !*abort_flag) return true;
+    if (*abort_flag == 0) raise_error(c.err, GDN_DEVERR_TIMEOUT);
+    *abort_flag = 1;
+    return false;
+  };
+  auto warp_wait = [&](uint64_t *bar, uint32_t phase) {
+    return __all_sync(0xffffffffu, wait(bar, phase));
+  };
+
+  uint32_t slots = 0;  // slots used by earlier units
+  uint32_t done = 0;   // tiles of earlier units
+  uint32_t units = 0;  // earlier units with tiles
+  bool ok = true;
+  // Every role walks the same units: one, or, where there are more than the
+  // hint says, several, of which the later ones are not split.
+  auto each_unit = [&](auto role) {
+    for (int64_t u = u0; ok && find_unit(c, a, i, head, u, R, u < hinted_units ? split : 0,
+                                         u < hinted_units ? splits : 1, false, &w);
+         u += hinted_units) {
+      if (u >= hinted_units && split > 0) break;
+      const int T = w.end - w.begin;
+      role(u, T);
+      slots += 2 * H * T;
+      done += T;
+      units += T > 0;
+    }
+  };
+
+  if (warp < kConv) {
+    set_regs_up<Cfg::kSoftRegs>();
+    each_unit([&](const int64_t u, const int T) {
+      // ---- softmax: one thread per query row ----
+      const int mt = warp >> 2;
+      const int row = 128 * mt + 32 * (warp & 3) + lane;  // in the unit
+      const int grow = w.row0 + min(row, w.rows - 1);     // rows past the end repeat the last
+      const int lim = w.kv_len - w.len + 1 + grow / group;
+      float qa = 0.f;  // scale * log2(e) * the query's power of two
+      if (T > 0) {
+        constexpr int E = D / 32;
+        const int row_w = w.row0 + 128 * mt + 32 * (warp & 3);
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r) {
+          const int gr = min(row_w + r, w.row0 + w.rows - 1);
+          const bf16 *q = static_cast<const bf16 *>(a.q) + (int64_t)(w.tok0 + gr / group) * a.ld_q +
+                          (int64_t)(head * group + gr % group) * D + lane * E;
+          float x[E];
+          if constexpr (E == 2) {
+            x[0] = Elem<bf16>::load1(q);
+            x[1] = Elem<bf16>::load1(q + 1);
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+              const float4 f = Elem<bf16>::load4(q + e);
+              x[e] = f.x, x[e + 1] = f.y, x[e + 2] = f.z, x[e + 3] = f.w;
+            }
+          }
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(x[e]));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          int ex = (int)(__float_as_uint(m) >> 23) - 127;
+          ex = ex > 126 || m == 0.f ? 0 : max(ex, -126);
+          const float inv = a.scale < 0.f ? -kv::pow2f(-ex) : kv::pow2f(-ex);
+          const int srow = 32 * (warp & 3) + r;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int d = lane * E + e, p = (d & ~3) + Widen<CODE>::place(d & 3);
+            *reinterpret_cast<__half *>(sQ + mt * Cfg::kQTile + (p >> 6) * 16384 + srow * 128 +
+                                        (((p >> 3 & 7) ^ (srow & 7)) << 4) + (p & 7) * 2) =
+                __float2half_rn(x[e] * inv);
+          }
+          if (r == lane) qa = fabsf(a.scale) * kLog2e * kv::pow2f(ex);
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full);
+      }
+      const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+      const uint32_t tO = tmem + lanes + Cfg::kO + mt * D;
+      float M = -INFINITY, Ms = 0.f, L = 0.f;
+      for (int j = 0; j < T && ok; ++j) {
+        const uint32_t n = done + j, buf = MT == 2 ? mt : n & 1;
+        const uint32_t tS = tmem + lanes + buf * kBN;
+        const int info = n % kInfo;
+        if (!warp_wait(&info_full[info], n / kInfo) ||
+            !warp_wait(&s_full[buf], MT == 2 ? n : n >> 1)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const int open = lim - (w.begin + j) * kBN;  // columns that this row may see
+        const bool masked = __any_sync(0xffffffffu, open < kBN);
+        // largest y of the tile; `hide`: some lane has columns that it may not see
+        auto find_peak = [&](auto hide) {
+          float peak = -INFINITY;
+          uint32_t s[2][32];
+          tmem_ld32_async(tS, s[0]);
+#pragma unroll
+          for (int h = 0; h < kBN / 32; ++h) {
+            tmem_ld_wait();
+            if (h + 1 < kBN / 32) tmem_ld32_async(tS + 32 * (h + 1), s[(h + 1) & 1]);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t *v = s[h & 1] + 16 * b;
+              const float f = qa * s_ks[info][2 * h + b], e = s_ve[info][2 * h + b];
+              float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+              for (int x = 0; x < 16; x += 2) {
+                const float a0 = __uint_as_float(v[x]), a1 = __uint_as_float(v[x + 1]);
+                if (!hide.value || 32 * h + 16 * b + x < open) m0 = fmaxf(m0, a0);
+                if (!hide.value || 32 * h + 16 * b + x + 1 < open) m1 = fmaxf(m1, a1);
+              }
+              m0 = fmaxf(m0, m1);
+              // (a row without columns: -inf times 0 would be NaN, which fmaxf drops)
+              peak = fmaxf(peak, fmaf(m0, f, e));
+            }
+          }
+          return peak;
+        };
+        const float peak = masked ? find_peak(std::true_type{}) : find_peak(std::false_type{});
+        bool seen = j == 0;  // pv_done of the tile before this one (each phase is waited for)
+        if (__any_sync(0xffffffffu, peak > M + kSlack)) {
+          const float m = fmaxf(M, peak);
+          const float f = m == -INFINITY ? 1.f : fast_exp2(M - m);
+          M = m;
+          Ms = m == -INFINITY ? 0.f : m - kLift;
+          L *= f;
+          if (j > 0) {  // O holds the tiles before this one
+            if (!warp_wait(&pv_done[mt], n - 1)) {
+              ok = false;
+              break;
+            }
+            seen = true;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+              uint32_t o[32];
+              tmem_ld32_async(tO + x, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_st16(tO + x, o);
+              tmem_st16(tO + x + 16, o + 16);
+            }
+          }
+        }
+        // weights; P's columns follow those of S that have been read
+        auto weigh = [&](auto hide) {
+          uint32_t s[2][32];
+          tmem_ld32_async(tS, s[0]);
+#pragma unroll
+          for (int h = 0; h < kBN / 32; ++h) {
+            uint32_t p[16];
+            tmem_ld_wait();
+            if (h + 1 < kBN / 32) tmem_ld32_async(tS + 32 * (h + 1), s[(h + 1) & 1]);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t *v = s[h & 1] + 16 * b;
+              const float f = qa * s_ks[info][2 * h + b], e = s_ve[info][2 * h + b] - Ms;
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int x = 0; x < 16; x += 2) {
+                float2 y =
+                    fma2(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), f, e);
+                if (hide.value) {
+                  if (32 * h + 16 * b + x >= open) y.x = -INFINITY;
+                  if (32 * h + 16 * b + x + 1 >= open) y.y = -INFINITY;
+                }
+                y.x = fast_exp2(y.x);
+                y.y = fast_exp2(y.y);
+                sum = add2(sum, y);
+                p[8 * b + x / 2] = half2_bits(y.x, y.y);
+              }
+              L = fmaf(sum.x + sum.y, s_un[info][2 * h + b], L);
+            }
+            tmem_st16(tS + 16 * h, p);
+          }
+        };
+        if (masked)
+          weigh(std::true_type{});
+        else
+          weigh(std::false_type{});
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        if (!seen && !warp_wait(&pv_done[mt], n - 1)) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&p_full[mt]);
+          mbar_arrive(&info_empty[info]);
+        }
+      }
+      // ---- outputs ----
+      if (ok && T > 0 && !warp_wait(&pv_done[mt], done + T - 1)) ok = false;
+      if (ok) {
+        tc::fence_after_sync();
+        const bool live = row < w.rows;
+        const bool whole = splits == 1 || u >= hinted_units;
+        const int64_t at = (int64_t)(w.tok0 + grow / group) * a.ld_o +
+                           (int64_t)(head * group + grow % group) * D;
+        float *mine = part;
+        if (!whole) {
+          mine += ((int64_t)blockIdx.x * splits + split) * Cfg::kPartFloats;
+          if (live) {
+            mine[R * D + row] = M;
+            mine[R * D + R + row] = L;
+          }
+          mine += (int64_t)row * D;
+        }
+        const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+#pragma unroll 1
+        for (int x = 0; x < D; x += 32) {
+          uint32_t o[32];
+          float v[32];
+          if (T > 0) {
+            tmem_ld32_async(tO + x, o);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int y = 0; y < 32; ++y)
+            v[y] = T > 0 ? __uint_as_float(o[(y & ~3) + Widen<CODE>::place(y & 3)]) * inv : 0.f;
+          if (live) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) {
+              if (!whole)
+                put8(mine + x + y, v + y);
+              else if (a.o_dtype == GDN_F32)
+                put8(static_cast<float *>(a.o) + at + x + y, v + y);
+              else
+                put8(static_cast<bf16 *>(a.o) + at + x + y, v + y);
+            }
+          }
+        }
+        tc::fence_before_sync();
+      }
+    });
+  } else if (warp < kMma) {
+    set_regs_down<Cfg::kConvRegs>();
+    each_unit([&](const int64_t, const int T) {
+      // ---- converters ----
+      constexpr int DC = Cfg::DC, COLS = DC / 16;
+      constexpr int PASS = 32 * CW / TEAMS / COLS;  // rows that a team covers at once
+      constexpr int VPS = kBN / PASS;               // loads per thread and slot
+      constexpr int PF = Cfg::kPrefetch;
+      const int team = (warp - kConv) / (CW / TEAMS);
+      const int ct = tid - 32 * (kConv + team * (CW / TEAMS));
+      // d = 64: 4 lanes to a row; else lanes 0-3 and 8-11 share a row, 4-7 and 12-15 the next:
+      // eight consecutive lanes write all eight 16-byte columns of the swizzled rows
+      const int col = DC == 64 ? ct & 3 : (ct & 3) | (ct >> 1 & 4);
+      const int row = DC == 64 ? ct >> 2 : (ct >> 2 & 1) | (ct >> 3 & ~1);
+      const int page_bytes = D << c.page_log2;
+      const int n_slots = 2 * H * T;
+      // slot x: its tile, side and half, in the order of the MMAs
+      auto place = [&](int x, int *tile, int *side, int *half) {
+        const int y = x / H;
+        *half = x % H;
+        if (MT == 2) {  // K0 V0 K1 V1 ...
+          *tile = y >> 1;
+          *side = y & 1;
+        } else if (y == 0 || T == 1) {  // K0, K1 V0, K2 V1, ... V(T-1)
+          *tile = 0;
+          *side = y;
+        } else if (y == 2 * T - 1) {
+          *tile = T - 1;
+          *side = 1;
+        } else {
+          *side = (y + 1) & 1;
+          *tile = *side ? (y >> 1) - 1 : (y + 1) >> 1;
+        }
+      };
+      uint4 code[PF][VPS];
+      auto load = [&](int x, uint4 *dst) {
+        int tile, side, half;
+        place(x, &tile, &side, &half);
+        const uint32_t n = done + tile;
+        const int info = n % kInfo;
+        if (!warp_wait(&info_full[info], n / kInfo)) return false;
+        const uint8_t *base = (side ? c.v : c.k) + half * DC + 16 * col;
+        auto fetch = [&](int v, int blk) {
+          const int r = v * PASS + row;
+          const uint8_t *p = base + (int64_t)blk * page_bytes + (r & (c.page_tokens - 1)) * D;
+          asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(dst[v].x), "=r"(dst[v].y), "=r"(dst[v].z), "=r"(dst[v].w)
+                       : "l"(p));
+        };
+        if (s_plain[info]) {  // nothing to leave out: loads without a branch between them
+          int blk[VPS];
+#pragma unroll
+          for (int v = 0; v < VPS; ++v) blk[v] = s_blk[info][(v * PASS + row) >> 4];
+#pragma unroll
+          for (int v = 0; v < VPS; ++v) fetch(v, blk[v]);
+        } else {
+#pragma unroll
+          for (int v = 0; v < VPS; ++v) {
+            const int r = v * PASS + row, blk = s_blk[info][r >> 4];
+            dst[v] = make_uint4(0, 0, 0, 0);  // past the end, or no page: the code of zero
+            if (blk >= 0 && (w.begin + tile) * kBN + r < w.kv_len) fetch(v, blk);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&info_empty[info]);
+        return true;
+      };
+#pragma unroll
+      for (int y = 0; y < PF; ++y)
+        if (ok && team + y * TEAMS < n_slots) ok = load(team + y * TEAMS, code[y]);
+      for (int x0 = team; x0 < n_slots && ok; x0 += PF * TEAMS) {
+#pragma unroll
+        for (int y = 0; y < PF; ++y) {
+          const int x = x0 + y * TEAMS;
+          if (x >= n_slots || !ok) break;
+          const uint32_t n = slots + x;
+          if (n >= NS && !warp_wait(&slot_empty[n % NS], n / NS - 1)) {
+            ok = false;
+            break;
+          }
+          unsigned char *dst = sKV + (n % NS) * Cfg::kSlot + (col >> 2) * 16384;
+#pragma unroll
+          for (int v = 0; v < VPS; ++v) {
+            const int r = v * PASS + row;
+            uint32_t h[8];
+            Widen<CODE>::four(code[y][v].x, h[0], h[1]);
+            Widen<CODE>::four(code[y][v].y, h[2], h[3]);
+            Widen<CODE>::four(code[y][v].z, h[4], h[5]);
+            Widen<CODE>::four(code[y][v].w, h[6], h[7]);
+            unsigned char *q = dst + r * 128;
+            const int k = 2 * (col & 3);
+            *reinterpret_cast<uint4 *>(q + ((k ^ (r & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(q + (((k + 1) ^ (r & 7)) << 4)) =
+                make_uint4(h[4], h[5], h[6], h[7]);
+          }
+          tc::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&slot_full[n % NS]);
+          if (x + PF * TEAMS < n_slots) ok = load(x + PF * TEAMS, code[y]);
+        }
+      }
+    });
+  } else if (warp == kMma) {
+    set_regs_down<Cfg::kMiscRegs>();
+    each_unit([&](const int64_t, const int T) {
+      // ---- MMA ----
+      // The whole warp takes every branch and wait; one elected lane issues.  (Issued
+      // from a branch on the lane number, an MMA took 160 cycles under busy softmax
+      // warps instead of 70.)
+      if (T > 0) {
+        constexpr uint32_t id_qk = idesc_f16(kBN, false);
+        constexpr uint32_t id_pv = idesc_f16(Cfg::DC, true);
+        const bool issue = elect_one();
+        uint32_t at = slots;  // next slot
+        auto next_slot = [&]() {
+          const bool got = warp_wait(&slot_full[at % NS], at / NS);
+          tc::fence_after_sync();
+          return got;
+        };
+        const uint32_t q_low = desc_low(smem_addr(sQ), 16);
+        const uint32_t k_low = desc_low(smem_addr(sKV), 16);
+        const uint32_t v_low = desc_low(smem_addr(sKV), 16384);
+        // S (+)= Q K^T of one slot; `then`: what to commit to
+        auto qk = [&](uint32_t slot, int half, int mt, int buf, uint64_t *then, uint64_t *free) {
+          const uint32_t q = q_low + (mt * Cfg::kQTile + half * (Cfg::DC / 64) * 16384) / 16;
+          const uint32_t k = k_low + (slot % NS) * (Cfg::kSlot / 16);
+          if (issue) {
+#pragma unroll
+            for (int x = 0; x < Cfg::DC / 16; ++x) {
+              const uint32_t off = ((x >> 2) * 16384 + (x & 3) * 32) / 16;
+              tc::mma_ss_f16(tmem + buf * kBN, desc(q + off), desc(k + off), id_qk, half + x > 0);
+            }
+            if (then) tc::mma_commit(then);
+            if (free) tc::mma_commit(free);
+          }
+          __syncwarp();
+        };
+        // O (+)= P V of one slot
+        auto pv = [&](uint32_t slot, int half, int mt, int buf, bool first, uint64_t *then,
+                      uint64_t *free) {
+          const uint32_t v = v_low + (slot % NS) * (Cfg::kSlot / 16);
+          if (issue) {
+#pragma unroll
+            for (int x = 0; x < kBN / 16; ++x)
+              tc::mma_ts_f16(tmem + Cfg::kO + mt * D + half * Cfg::DC, tmem + buf * kBN + 8 * x,
+                             desc(v + x * 128), id_pv, !first || x > 0);
+            if (then) tc::mma_commit(then);
+            if (free) tc::mma_commit(free);
+          }
+          __syncwarp();
+        };
+        auto p_ready = [&](int mt, int j) {
+          const bool got = warp_wait(&p_full[mt], done + j);
+          tc::fence_after_sync();
+          return got;
+        };
+        auto run = [&]() {
+          if (!warp_wait(&q_full, units)) return false;
+          tc::fence_after_sync();
+          if constexpr (MT == 2) {
+            if (!next_slot()) return false;
+            qk(at, 0, 0, 0, &s_full[0], nullptr);
+            qk(at, 0, 1, 1, &s_full[1], &slot_empty[at % NS]);
+            ++at;
+            for (int j = 0; j < T; ++j) {  // `at`: V of tile j, then K of the next
+              if (!next_slot() || !p_ready(0, j)) return false;
+              pv(at, 0, 0, 0, j == 0, &pv_done[0], nullptr);
+              if (j + 1 < T) {
+                ++at;
+                if (!next_slot()) return false;
+                qk(at, 0, 0, 0, &s_full[0], nullptr);
+                --at;
+              }
+              if (!p_ready(1, j)) return false;
+              pv(at, 0, 1, 1, j == 0, &pv_done[1], &slot_empty[at % NS]);
+              ++at;
+              if (j + 1 < T) {
+                qk(at, 0, 1, 1, &s_full[1], &slot_empty[at % NS]);
+                ++at;
+              }
+            }
+          } else {
+            for (int j = -1; j < T; ++j) {
+              if (j + 1 < T) {
+                const uint32_t n = done + j + 1;
+                for (int h = 0; h < H; ++h, ++at) {
+                  if (!next_slot()) return false;
+                  qk(at, h, 0, n & 1, h == H - 1 ? &s_full[n & 1] : nullptr, &slot_empty[at % NS]);
+                }
+              }
+              if (j >= 0) {
+                if (!p_ready(0, j)) return false;
+                for (int h = 0; h < H; ++h, ++at) {
+                  if (!next_slot()) return false;
+                  pv(at, h, 0, (done + j) & 1, j == 0, h == H - 1 ? &pv_done[0] : nullptr,
+                     &slot_empty[at % NS]);
+                }
+              }
+            }
+          }
+          return true;
+        };
+        ok = run();
+        if (!ok) {  // the MMAs in flight finish before TMEM is freed
+          if (issue) tc::mma_commit(&drain);
+          mbar_wait_bounded(&drain, 0);
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    });
+  } else if (warp == kPages) {
+    set_regs_down<Cfg::kMiscRegs>();
+    each_unit([&](const int64_t, const int T) {
+      // ---- page ids and scales, four tiles at a time ----
+      const int32_t *table = c.table + (int64_t)w.slot * c.max_pages;
+      for (int j0 = 0; j0 < T && ok; j0 += 4) {
+        const int j = j0 + (lane >> 3), gr = lane & 7;
+        const int tok = (w.begin + j) * kBN + 16 * gr;
+        int blk = -1;
+        float ks = 0.f, ve = -INFINITY, un = 0.f;
+        if (j < T && tok < w.kv_len) {
+          const int id = table[tok >> c.page_log2];
+          if (id >= 0 && id < c.n_pages) {
+            blk = (int)c.block(layer, id, head);
+            ks = c.k_scale[blk];
+            const int e = kv::scale_exponent<CODE>(c.v_scale[blk]);
+            ve = (float)e;
+            un = kv::pow2f(-e);
+          } else {
+            raise_error(c.err, GDN_DEVERR_PAGE);
+          }
+        }
+        for (int x = 0; x < 4 && j0 + x < T && ok; ++x) {
+          const uint32_t n = done + j0 + x;
+          const int info = n % kInfo;
+          if (n >= kInfo) ok = warp_wait(&info_empty[info], n / kInfo - 1);
+          if (!ok) break;
+          const bool plain =
+              __all_sync(0xffffffffu, (lane >> 3) != x || (blk >= 0 && tok + 16 <= w.kv_len));
+          if ((lane >> 3) == x) {
+            s_plain[info] = plain;
+            s_blk[info][gr] = blk;
+            s_ks[info][gr] = ks;
+            s_ve[info][gr] = ve;
+            s_un[info][gr] = un;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&info_full[info]);
+        }
+      }
+    });
+  } else {
+    set_regs_down<Cfg::kMiscRegs>();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMma) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, Cfg::kTmem);
+  }
+}
+
+// Joins the splits of a unit: a CTA per (unit, sequence and head) and four rows.
+constexpr int kJoinRows = 4;
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kJoinRows * D / 4)
+    attend_prompt_join_kernel(const KVView c, const KVAttendArgs a, const int splits,
+                              const float *part) {
+  using Cfg = PromptCfg<D, MT>;
+  constexpr int R = Cfg::kRows;
+  kv::dependents_may_launch();
+  kv::dependent_wait();
+  const int heads = a.seq.n_seqs * c.h_kv, z = blockIdx.x % heads;
+  Unit w;
+  if (!find_unit(c, a, z / c.h_kv, z % c.h_kv, blockIdx.x / heads, R, 0, 1, false, &w)) return;
+  const int row = blockIdx.y * kJoinRows + threadIdx.x / (D / 4);
+  const int d = 4 * (threadIdx.x % (D / 4));
+  if (row >= w.rows) return;
+  const float *base = part + (int64_t)blockIdx.x * splits * Cfg::kPartFloats;
+  float m = -INFINITY, l = 0.f;
+  for (int s = 0; s < splits; ++s)
+    m = fmaxf(m, __ldcg(base + (int64_t)s * Cfg::kPartFloats + R * D + row));
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float *p = base + (int64_t)s * Cfg::kPartFloats;
+    const float pm = __ldcg(p + R * D + row), pl = __ldcg(p + R * D + R + row);
+    const float f = pm == -INFINITY ? (pl == 0.f ? 0.f : 1.f) : fast_exp2(pm - m);
+    l += f * pl;
+    sum = axpby4(1.f, sum, f, __ldcg(reinterpret_cast<const float4 *>(p + (int64_t)row * D + d)));
+  }
+  const int group = c.h_q / c.h_kv, grow = w.row0 + row;
+  const int64_t at = (int64_t)(w.tok0 + grow / group) * a.ld_o +
+                     (int64_t)(w.head * group + grow % group) * D + d;
+  const float4 v = scale4(l == 0.f ? 0.f : 1.f / l, sum);
+  if (a.o_dtype == GDN_F32) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at) = v;
+  } else {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2 *>(static_cast<bf16 *>(a.o) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+  }
+}
+
+template <int CODE, int D, int MT>
+cudaError_t launch_prompt(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
+                          cudaStream_t s) {
+  using Cfg = PromptCfg<D, MT>;
+  auto kernel = attend_prompt_kernel<CODE, D, MT>;
+  static std::atomic<uint64_t> seen{0};
+  cudaError_t e = kv::allow_smem(kernel, Cfg::kSmem, h.device, seen);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)a.max_seqlen * (c.h_q / c.h_kv);
+  const int64_t z = (int64_t)a.seq.n_seqs * c.h_kv;
+  int64_t units = (rows + Cfg::kRows - 1) / Cfg::kRows;
+  if (units * z > INT32_MAX) units = INT32_MAX / z;
+  // too few units for the GPU: cut each one's context
+  const int64_t tiles = a.max_kv_len / kBN + 1;
+  int64_t splits = 1;
+  if (units * z < h.sm_count) {
+    splits = h.sm_count / (units * z);
+    if (splits > tiles) splits = tiles;
+    if (splits > 64) splits = 64;
+  }
+  void *work = nullptr;
+  bool temporary = false;
+  if (splits > 1) {
+    e = h.work->get((size_t)z * units * splits * Cfg::kPartFloats * sizeof(float), s, &work,
+                    &temporary);
+    if (e != cudaSuccess) return e;
+  }
+  e = kv::launch(kernel, dim3((unsigned)(units * z), (unsigned)splits), Cfg::kThreads, Cfg::kSmem,
+                 s, c, layer, a, (int)splits, (int)units, static_cast<float *>(work));
+  if (splits > 1) {
+    if (e == cudaSuccess)
+      e = kv::launch(attend_prompt_join_kernel<D, MT>,
+                     dim3((unsigned)(units * z), Cfg::kRows / kJoinRows), kJoinRows * D / 4, 0, s,
+                     c, a, (int)splits, static_cast<const float *>(work));
+    const cudaError_t ef = temporary ? cudaFreeAsync(work, s) : cudaSuccess;
+    if (e == cudaSuccess) e = ef;
+  }
+  return e;
+}
+
+template <int CODE>
+cudaError_t by_dim(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
+                   cudaStream_t s) {
+  const bool one = (int64_t)a.max_seqlen * (c.h_q / c.h_kv) <= 128;
+  if (c.d == 256) return launch_prompt<CODE, 256, 1>(c, layer, a, h, s);
+  if (c.d == 128)
+    return one ? launch_prompt<CODE, 128, 1>(c, layer, a, h, s)
+               : launch_prompt<CODE, 128, 2>(c, layer, a, h, s);
+  return one ? launch_prompt<CODE, 64, 1>(c, layer, a, h, s)
+             : launch_prompt<CODE, 64, 2>(c, layer, a, h, s);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attend_prompt(const KVView &c, int layer, const KVAttendArgs &a,
+                                    const KVHost &h, cudaStream_t s) {
+  return c.code == GDN_KV_I8 ? by_dim<GDN_KV_I8>(c, layer, a, h, s)
+                             : by_dim<GDN_KV_E4M3>(c, layer, a, h, s);
+}
+
+}  // namespace gdn

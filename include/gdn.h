@@ -452,11 +452,12 @@ size_t gdn_kv_code_bytes(const gdn_kv_desc *desc);
 size_t gdn_kv_scale_bytes(const gdn_kv_desc *desc);
 
 /* Wrap caller memory (codes 16-byte aligned, scales and table 4-byte).  The
- * handle allocates an error word and owns a stream-ordered memory pool for
- * the workspace of gdn_kv_attend, kept for reuse until gdn_kv_destroy.  Every
- * compute call below is asynchronous on its stream.  Calls on different
- * streams may overlap if none appends to a page that another reads or
- * appends to. */
+ * handle allocates an error word and owns a memory pool from which
+ * gdn_kv_attend takes a workspace for each stream that it is called on (some
+ * ten MiB; kept for reuse until gdn_kv_destroy).  Every compute call below is
+ * asynchronous on its stream.  Calls on different streams may overlap if none
+ * appends to a page that another reads or appends to; calls from several host
+ * threads on one handle must be serialised by the caller. */
 gdn_status gdn_kv_create(const gdn_kv_desc *desc, void *k_codes, void *v_codes,
                          size_t code_bytes, float *k_scale, float *v_scale, size_t scale_bytes,
                          const int32_t *page_table, gdn_kv **out);
@@ -506,8 +507,9 @@ gdn_status gdn_kv_read(gdn_kv *kv, int32_t layer, const int32_t *slot_ids, const
  * aligned; scale is finite.  Scores, softmax statistics and sums are float32;
  * the products run on the tensor cores on the codes (exact in binary16) and
  * on queries and weights rounded to binary16 (bf16 q: the query exactly, up
- * to 2^-25 of its row's largest element; the weight to 2^-11), or split into
- * two binary16 parts each (float32 q: to 2^-22).
+ * to 2^-25 of its row's largest element; the weight to 2^-11, or to 2^-32 of
+ * the row's largest weight x V scale where that is more), or split into two
+ * binary16 parts each (float32 q: to 2^-22, with the same smallest step).
  * max_seqlen, max_kv_len: upper bounds of the query and cache lengths, used
  * only to choose the kernel and size its grid (any value >= 1 is correct). */
 gdn_status gdn_kv_attend(gdn_kv *kv, int32_t layer, const int32_t *slot_ids,

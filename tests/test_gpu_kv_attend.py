@@ -307,6 +307,43 @@ def test_long_context_and_many_slots():
     assert_close(got, want, mag, "bf16", "bf16")
 
 
+@pytest.mark.parametrize("code", ["i8", "e4m3"])
+@pytest.mark.parametrize("h_q,h_kv,d", [(16, 2, 256), (8, 2, 128), (28, 4, 128), (12, 4, 64)])
+def test_weights_far_below_the_largest(code, h_q, h_kv, d):
+    """The tensor-core kernel (the length hints choose it) on scores up to 100
+    apart and V scales 2^-30 apart.  Weights are rounded to 2^-11, or to a step
+    of 2^-24 under a largest weight of at least 2^7: the contribution of a
+    position is off by at most 2^-32 of the largest y = weight * V scale of its
+    row, times its code, of at most top.  So, beside the usual relative part,
+    err <= positions * 2^-32 * max_j(w_j s_j) * top."""
+    rng = np.random.default_rng(20)
+    length, n, page, top = 300, 40, 16, 127 if code == "i8" else 448
+    kv, ref = make(code, page, h_kv, d, 1, 20, h_q=h_q, seed=4)
+    k, v = rows(rng, length, h_kv, d, "bf16", 0), rows(rng, length, h_kv, d, "bf16", 0)
+    q = queries(rng, n, h_q, d, "bf16")
+    k[:16] = 0
+    k[5] = q[-1].reshape(h_kv, -1, d)[:, 0] * 2
+    v[:16] *= 2.0 ** -30
+    v[64:128] = 0
+    append(kv, ref, 0, [0], [0], [length], k, v, "bf16")
+    scale = 100.0 / (2 * d)
+    want, mag = ref.attend(0, [0], [length], [n], q, scale)
+    got = run(kv, 0, [0], [length], [n], q, "bf16", "f32", scale, max_seqlen=2000,
+              max_kv_len=40000)
+    group = h_q // h_kv
+    keys = np.repeat(ref.values(0, 0, "k", 0, length), group, 1)
+    s = np.einsum("thd,jhd->thj", q.astype(np.float64), keys) * scale
+    s[np.arange(length)[None, None] > np.arange(length - n, length)[:, None, None] + 0 * s] = -np.inf
+    w = np.exp(s - s.max(-1, keepdims=True))
+    w /= w.sum(-1, keepdims=True)
+    pages = ref.table[0, np.arange(length) // page]
+    v_scale = np.repeat(ref.scale["v"][0, pages], group, 1)            # [length, h_q]
+    peak = (w * v_scale.T[None]).max(-1)
+    lim = 5.5e-4 * mag + length * 2.0 ** -32 * top * peak[..., None]
+    err = np.abs(host(got) - want)
+    assert (err <= lim).all(), (float((err / lim).max()), int((err > lim).sum()))
+
+
 def test_zero_tokens_and_the_same_answer_twice():
     rng = np.random.default_rng(19)
     kv, _ = filled(rng, "i8", 16, 4, 2, 64, [500, 3])
