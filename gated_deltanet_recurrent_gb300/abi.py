@@ -515,6 +515,7 @@ class KVCache:
                 raise GDNError(1, f"{name} must be contiguous and on k's device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.page_table = page_table
+        self.h_q, self.h_kv, self.d = h_q, k.shape[2], k.shape[4]
         self.desc = gdn_kv_desc(k.shape[0], page_table.shape[0], k.shape[1], page_table.shape[1],
                                 k.shape[3], h_q, k.shape[2], k.shape[4], _KV_CODES[k.dtype],
                                 1 if host_checks else 0)
@@ -589,9 +590,10 @@ def _kv_dtype(t: torch.Tensor) -> int:
 
 def _kv_index(slot_ids, starts, cu_seqlens, tokens, name):
     """Pointers of the index arrays, and the number of sequences."""
+    i32 = torch.int32
     n = slot_ids.numel()
-    if slot_ids.dtype != torch.int32 or starts.dtype != torch.int32 or \
-            not slot_ids.is_contiguous() or not starts.is_contiguous():
+    if slot_ids.dtype != i32 or starts.dtype != i32 or not slot_ids.is_contiguous() or \
+            not starts.is_contiguous():
         raise GDNError(1, f"slot_ids and {name} must be contiguous int32 tensors")
     if starts.numel() != n:
         raise GDNError(5, f"{name} must have an entry per slot id")
@@ -599,30 +601,47 @@ def _kv_index(slot_ids, starts, cu_seqlens, tokens, name):
         if tokens != n:
             raise GDNError(5, "without cu_seqlens there is one token per slot")
         return slot_ids.data_ptr(), starts.data_ptr(), None, n
-    if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous():
+    if cu_seqlens.dtype != i32 or not cu_seqlens.is_contiguous():
         raise GDNError(1, "cu_seqlens must be a contiguous int32 tensor")
     if cu_seqlens.numel() != n + 1:
         raise GDNError(5, "cu_seqlens must have one entry more than slot_ids")
     return slot_ids.data_ptr(), starts.data_ptr(), cu_seqlens.data_ptr(), n
 
 
+def _kv_token_rows(shape, stride, heads, dim, name):
+    """Token stride of [tokens, heads, dim] rows whose heads are packed (0: one row, whose
+    stride says nothing)."""
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise GDNError(5, f"{name} must be [tokens, {heads}, {dim}], got {tuple(shape)}")
+    if stride[2] != 1 or stride[1] != dim:
+        raise GDNError(1, f"{name}: heads must be packed (strides {stride})")
+    return stride[0] if shape[0] > 1 else 0
+
+
 def _kv_rows(kv, slot_ids, pos, k, v, cu_seqlens, max_seqlen):
-    d = kv.desc
-    some = k if k is not None else v
-    if some is None:
-        raise GDNError(1, "k and v are both None")
-    if k is not None and v is not None and (k.dtype != v.dtype or k.shape[0] != v.shape[0]):
-        raise GDNError(4, "k and v must share one dtype and token count")
-    tokens = some.shape[0]
+    k_ptr = v_ptr = None
+    ld_k = ld_v = 0
+    tokens = dtype = None
+    if k is not None:
+        shape = k.shape
+        tokens, dtype = shape[0], k.dtype
+        ld_k = _kv_token_rows(shape, k.stride(), kv.h_kv, kv.d, "k")
+        k_ptr = k.data_ptr()
+    if v is not None:
+        shape = v.shape
+        if tokens is None:
+            tokens, dtype = shape[0], v.dtype
+        elif shape[0] != tokens or v.dtype != dtype:
+            raise GDNError(4, "k and v must share one dtype and token count")
+        ld_v = _kv_token_rows(shape, v.stride(), kv.h_kv, kv.d, "v")
+        v_ptr = v.data_ptr()
+    code = _KV_DTYPES.get(dtype)
+    if code is None:
+        raise GDNError(1 if dtype is None else 4, f"k or v of float32 or bf16 needed, got {dtype}")
     slots, starts, cu, n = _kv_index(slot_ids, pos, cu_seqlens, tokens, "pos")
-    ld_k = 0 if k is None else _token_rows(k, d.h_kv, d.d, "k")
-    ld_v = 0 if v is None else _token_rows(v, d.h_kv, d.d, "v")
-    if tokens <= 1:  # the stride of a single row says nothing
-        ld_k = ld_v = 0
     if max_seqlen <= 0:
-        max_seqlen = 1 if cu_seqlens is None else tokens
-    return (slots, starts, cu, n, tokens, max_seqlen, None if k is None else k.data_ptr(), ld_k,
-            None if v is None else v.data_ptr(), ld_v, _kv_dtype(some))
+        max_seqlen = 1 if cu is None else tokens
+    return slots, starts, cu, n, tokens, max_seqlen, k_ptr, ld_k, v_ptr, ld_v, code
 
 
 def gdn_kv_append(kv: KVCache, layer: int, slot_ids: torch.Tensor, pos: torch.Tensor,
@@ -658,23 +677,22 @@ def gdn_kv_attend(kv: KVCache, layer: int, slot_ids: torch.Tensor, kv_lens: torc
     """Causal attention of q [tokens, h_q, d] over the slots' cached tokens;
     kv_lens counts the query tokens themselves (append them first).  o
     [tokens, h_q, d] (default: q's type); scale defaults to d ** -0.5."""
-    d = kv.desc
     if o is None:
         o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if o.shape != q.shape:
-        raise GDNError(5, f"o must have q's shape {tuple(q.shape)}")
-    tokens = q.shape[0]
+    shape = q.shape
+    if o.shape != shape:
+        raise GDNError(5, f"o must have q's shape {tuple(shape)}")
+    ld_q = _kv_token_rows(shape, q.stride(), kv.h_q, kv.d, "q")
+    ld_o = _kv_token_rows(shape, o.stride(), kv.h_q, kv.d, "o")
+    tokens = shape[0]
     slots, starts, cu, n = _kv_index(slot_ids, kv_lens, cu_seqlens, tokens, "kv_lens")
-    ld_q, ld_o = _token_rows(q, d.h_q, d.d, "q"), _token_rows(o, d.h_q, d.d, "o")
-    if tokens <= 1:
-        ld_q = ld_o = 0
     if max_seqlen <= 0:
-        max_seqlen = 1 if cu_seqlens is None else tokens
+        max_seqlen = 1 if cu is None else tokens
     if max_kv_len <= 0:
-        max_kv_len = d.max_pages * d.page_tokens
+        max_kv_len = kv.desc.max_pages * kv.desc.page_tokens
     status = _lib.gdn_kv_attend(
         kv.handle, layer, slots, starts, cu, n, tokens, max_seqlen, max_kv_len, q.data_ptr(), ld_q,
-        _kv_dtype(q), o.data_ptr(), ld_o, _kv_dtype(o), d.d ** -0.5 if scale is None else scale,
+        _kv_dtype(q), o.data_ptr(), ld_o, _kv_dtype(o), kv.d ** -0.5 if scale is None else scale,
         _kv_stream(stream, slot_ids))
     if status:
         _check(status)

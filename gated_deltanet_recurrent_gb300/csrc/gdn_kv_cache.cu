@@ -7,7 +7,7 @@
 // exact.  Both kernels are HBM-bound: the new rows are read once, one byte is
 // written per element.
 //   tile kernel (prompts): one CTA per block; the block's new rows stay in
-//     registers (64 elements per thread) between the maximum and the codes.
+//     registers (32 per thread) between the maximum and the codes.
 //   warp kernel (single tokens and drafts): one warp per (sequence, head,
 //     side), which walks its pages in order; there is little to read, so what
 //     counts is the chain of dependent loads (slot -> page -> scale) and the
@@ -20,28 +20,26 @@ namespace gdn {
 namespace {
 
 // Token range and first position of sequence i; false: nothing to do (an
-// error bit is set where the entry is bad; `report`: this thread reports).
+// error bit is set where the entry is bad; `report`: this thread reports).  All
+// loads are issued before the first check.
 __device__ __forceinline__ bool kv_sequence(const KVView &c, const SeqIndex &seq,
                                             const int32_t *pos, int i, bool report, int *slot,
                                             int *tok0, int *len, int *first) {
   *slot = seq.slot_ids[i];
+  *first = pos[i];
+  *tok0 = i;
+  int hi = i + 1;
+  if (seq.cu_seqlens != nullptr) {
+    *tok0 = seq.cu_seqlens[i];
+    hi = seq.cu_seqlens[i + 1];
+  }
+  *len = hi - *tok0;
   if (*slot < 0 || *slot >= c.n_slots) {
     if (report) raise_error(c.err, GDN_DEVERR_SLOT);
     return false;
   }
-  *tok0 = i;
-  *len = 1;
-  if (seq.cu_seqlens != nullptr) {
-    *tok0 = seq.cu_seqlens[i];
-    const int hi = seq.cu_seqlens[i + 1];
-    if (*tok0 < 0 || hi < *tok0 || hi > seq.total_tokens) {
-      if (report) raise_error(c.err, GDN_DEVERR_SEQ);
-      return false;
-    }
-    *len = hi - *tok0;
-  }
-  *first = pos[i];
-  if (*first < 0 || (int64_t)*first + *len > c.capacity()) {
+  if (*tok0 < 0 || hi < *tok0 || hi > seq.total_tokens || *first < 0 ||
+      (int64_t)*first + *len > c.capacity()) {
     if (report) raise_error(c.err, GDN_DEVERR_SEQ);
     return false;
   }
@@ -56,37 +54,70 @@ __device__ __forceinline__ int kv_page(const KVView &c, int slot, int index, boo
   return -1;
 }
 
-// Eight consecutive elements of a row (16-byte aligned), NaN as zero; *odd is
-// set where one is not finite.
+// 16 bytes of a row, as they lie: 4 or 8 elements.  A lane's neighbours take the
+// next ones, so that loads, codes and values all go in whole sectors.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float *x, bool *odd) {
-  const float4 a = Elem<T>::load4(p), b = Elem<T>::load4(p + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+constexpr int kElems = 16 / sizeof(T);
+
+// Largest magnitude as float32 bits, which order like the magnitudes: infinities
+// (0x7f800000) above the finite ones, NaN above those.
+template <typename T>
+__device__ __forceinline__ uint32_t max_bits(uint4 r, uint32_t m) {
+  if constexpr (sizeof(T) == 4) {
+    m = max(max(m, r.x & 0x7fffffffu), max(r.y & 0x7fffffffu, r.z & 0x7fffffffu));
+    return max(m, r.w & 0x7fffffffu);
+  } else {
+    const uint32_t x = __vmaxu2(__vmaxu2(r.x & 0x7fff7fffu, r.y & 0x7fff7fffu),
+                                __vmaxu2(r.z & 0x7fff7fffu, r.w & 0x7fff7fffu));
+    return max(m, max(x << 16, x & 0x7fff0000u));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void widen(uint4 r, float *x) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (!(fabsf(x[j]) <= 3.402823466e38f)) {
-      *odd = true;
-      if (x[j] != x[j]) x[j] = 0.f;
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(T) == 4) {
+      x[j] = __uint_as_float(w[j]);
+    } else {
+      x[2 * j] = __uint_as_float(w[j] << 16);
+      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
     }
   }
 }
 
-__device__ __forceinline__ float finite_max8(const float *x, float m) {
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// The same over the finite elements only (for blocks that hold others).
+template <typename T>
+__device__ __forceinline__ uint32_t finite_max_bits(uint4 r, uint32_t m) {
+  float x[kElems<T>];
+  widen<T>(r, x);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float a = fabsf(x[j]);
-    if (a <= 3.402823466e38f) m = fmaxf(m, a);
+  for (int j = 0; j < kElems<T>; ++j) {
+    const uint32_t b = __float_as_uint(x[j]) & 0x7fffffffu;
+    if (b < kInfBits) m = max(m, b);
   }
   return m;
 }
 
-template <int CODE>
-__device__ __forceinline__ void store8(uint8_t *p, const float *x, float inv) {
+// The codes of 16 bytes of elements; `odd`: NaN may be among them, and is stored as zero.
+template <int CODE, typename T>
+__device__ __forceinline__ void store_codes(uint8_t *p, uint4 r, float inv, bool odd) {
   using C = kv::Code<CODE>;
-  *reinterpret_cast<uint2 *>(p) =
-      make_uint2(C::encode4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                 C::encode4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+  float x[kElems<T>];
+  widen<T>(r, x);
+#pragma unroll
+  for (int j = 0; j < kElems<T>; ++j) {
+    x[j] *= inv;
+    if (odd && x[j] != x[j]) x[j] = 0.f;
+  }
+  const uint32_t lo = C::encode4(x[0], x[1], x[2], x[3]);
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<uint32_t *>(p) = lo;
+  else
+    *reinterpret_cast<uint2 *>(p) = make_uint2(lo, C::encode4(x[4], x[5], x[6], x[7]));
 }
 
 // codes [0, bytes) of a block times `ratio` (a power of two below one)
@@ -105,15 +136,15 @@ __device__ __forceinline__ void rescale(uint8_t *block, int bytes, float ratio, 
   }
 }
 
-// ---- prompts: a CTA of max(32, page_tokens * d / 64) threads per block ----
+// ---- prompts: a CTA per block, with the block's elements in its registers ----
 
-constexpr int kVec = 8;  // vectors of 8 elements per thread
+constexpr int kVec = 8;  // 16-byte vectors per thread
 
 template <typename T, int CODE>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(sizeof(T) == 2 ? 512 : 1024, sizeof(T) == 2 ? 2 : 1)
     append_tile_kernel(KVView c, int layer, SeqIndex seq, const int32_t *__restrict__ pos,
                        KVRows rows) {
-  __shared__ float s_max[16];
+  __shared__ uint32_t s_max[2][32];
   kv::dependents_may_launch();
   kv::dependent_wait();
   const int head = blockIdx.y >> 1, side = blockIdx.y & 1;
@@ -125,41 +156,59 @@ __global__ void __launch_bounds__(512)
   const int page0 = first >> c.page_log2, page1 = (first + len - 1) >> c.page_log2;
   const int64_t ld = side ? rows.ld_v : rows.ld_k;
   const T *src = static_cast<const T *>(side ? rows.v : rows.k) + (int64_t)head * c.d;
-  const int d8 = c.d >> 3;
+  // vectors of a row, a power of two
+  const int dv_log2 = 31 - __clz(c.d / kElems<T>), dv = 1 << dv_log2;
+  // the largest of the CTA's `m`
+  auto reduce = [&](uint32_t m, int buf) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (nt > 32) {
+      if ((tid & 31) == 0) s_max[buf][tid >> 5] = m;
+      __syncthreads();
+      m = __reduce_max_sync(0xffffffffu, (tid & 31) < (nt >> 5) ? s_max[buf][tid & 31] : 0u);
+    }
+    return m;
+  };
   // the grid's x covers max_seqlen; a sequence that is longer than that takes more rounds
   for (int pg = page0 + blockIdx.x; pg <= page1; pg += gridDim.x) {
-    const int id = kv_page(c, slot, pg, blockIdx.y + tid == 0);
-    if (id < 0) continue;
     const int start = pg << c.page_log2;
     const int off = pg == page0 ? first - start : 0;
     const int end = min(c.page_tokens, first + len - start);
     const T *base = src + (int64_t)(tok0 + start + off - first) * ld;
-    const int nv = (end - off) * d8;
-    float x[kVec][8];
-    bool odd = false;
-    float m = 0.f;
+    const int nv = (end - off) * dv;
+    auto vec = [&](int v) {
+      return *reinterpret_cast<const uint4 *>(base + (int64_t)(v >> dv_log2) * ld +
+                                              (v & (dv - 1)) * kElems<T>);
+    };
+    // the elements are on their way before the page id and the scale are asked for
+    uint4 x[kVec];
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const int v = i * nt + tid;
-      if (v < nv) {
-        load8<T>(base + (int64_t)(v / d8) * ld + (v % d8) * 8, x[i], &odd);
-        m = finite_max8(x[i], m);
-      }
+      if (v < nv) x[i] = vec(v);
     }
-    if (odd) raise_error(c.err, GDN_DEVERR_VALUE);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (nt > 32) {
-      if ((tid & 31) == 0) s_max[tid >> 5] = m;
-      __syncthreads();
-      for (int w = 0; w < nt >> 5; ++w) m = fmaxf(m, s_max[w]);
-    }
+    const int id = kv_page(c, slot, pg, blockIdx.y + tid == 0);
+    if (id < 0) continue;
     const int64_t blk = c.block(layer, id, head);
     uint8_t *codes = (side ? c.v : c.k) + (blk << c.page_log2) * c.d;
     float *scale = (side ? c.v_scale : c.k_scale) + blk;
-    int e = kv::Code<CODE>::exponent(m);
+    const float was = off > 0 ? *scale : 0.f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (i * nt + tid < nv) m = max_bits<T>(x[i], m);
+    m = reduce(m, 0);
+    const bool odd = m >= kInfBits;
+    if (odd) {
+      if (tid == 0) raise_error(c.err, GDN_DEVERR_VALUE);
+      m = 0;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (i * nt + tid < nv) m = finite_max_bits<T>(x[i], m);
+      m = reduce(m, 1);
+    }
+    int e = kv::Code<CODE>::exponent(__uint_as_float(m));
     if (off > 0) {
-      const int old = kv::scale_exponent<CODE>(*scale);
+      const int old = kv::scale_exponent<CODE>(was);
       if (e > old)
         rescale<CODE>(codes, off * c.d, kv::pow2f(max(old - e, -126)), tid, nt);
       else
@@ -169,7 +218,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const int v = i * nt + tid;
-      if (v < nv) store8<CODE>(codes + (int64_t)off * c.d + v * 8, x[i], inv);
+      if (v < nv) store_codes<CODE, T>(codes + off * c.d + v * kElems<T>, x[i], inv, odd);
     }
     __syncthreads();  // every thread has read the old scale and s_max
     if (tid == 0) *scale = kv::pow2f(e);
@@ -196,11 +245,19 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   if (!kv_sequence(c, seq, pos, i, r + lane == 0, &slot, &tok0, &len, &first)) return;
   const int64_t ld = side ? rows.ld_v : rows.ld_k;
   const T *src = static_cast<const T *>(side ? rows.v : rows.k) + (int64_t)head * c.d;
-  const int d8 = c.d >> 3;
+  const int dv_log2 = 31 - __clz(c.d / kElems<T>), dv = 1 << dv_log2;
   for (int done = 0; done < len;) {
     const int at = first + done, off = at & (c.page_tokens - 1);
     const int take = min(len - done, c.page_tokens - off);
     const T *base = src + (int64_t)(tok0 + done) * ld;
+    const int nv = take * dv;
+    auto vec = [&](int v) {
+      return *reinterpret_cast<const uint4 *>(base + (int64_t)(v >> dv_log2) * ld +
+                                              (v & (dv - 1)) * kElems<T>);
+    };
+    // a token's elements (one vector per lane) are on their way before the page id is asked for
+    uint4 x;
+    if (lane < nv) x = vec(lane);
     const int id = kv_page(c, slot, at >> c.page_log2, r + lane == 0);
     done += take;
     if (id < 0) continue;
@@ -208,18 +265,18 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
     uint8_t *codes = (side ? c.v : c.k) + (blk << c.page_log2) * c.d;
     float *scale = (side ? c.v_scale : c.k_scale) + blk;
     const float was = off > 0 ? *scale : 0.f;
-    const int nv = take * d8;
-    float x[8];
-    bool odd = false;
-    float m = 0.f;
-    for (int v = lane; v < nv; v += 32) {
-      load8<T>(base + (int64_t)(v / d8) * ld + (v % d8) * 8, x, &odd);
-      m = finite_max8(x, m);
+    uint32_t m = 0;
+    if (lane < nv) m = max_bits<T>(x, m);
+    for (int v = lane + 32; v < nv; v += 32) m = max_bits<T>(vec(v), m);
+    m = __reduce_max_sync(0xffffffffu, m);
+    const bool odd = m >= kInfBits;
+    if (odd) {
+      if (lane == 0) raise_error(c.err, GDN_DEVERR_VALUE);
+      m = 0;
+      for (int v = lane; v < nv; v += 32) m = finite_max_bits<T>(vec(v), m);
+      m = __reduce_max_sync(0xffffffffu, m);
     }
-    if (odd) raise_error(c.err, GDN_DEVERR_VALUE);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    int e = kv::Code<CODE>::exponent(m);
+    int e = kv::Code<CODE>::exponent(__uint_as_float(m));
     if (off > 0) {
       const int old = kv::scale_exponent<CODE>(was);
       if (e > old)
@@ -228,31 +285,21 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
         e = old;
     }
     const float inv = kv::pow2f(-e);
-    for (int v = lane; v < nv; v += 32) {
-      if (nv > 32) load8<T>(base + (int64_t)(v / d8) * ld + (v % d8) * 8, x, &odd);
-      store8<CODE>(codes + (int64_t)off * c.d + v * 8, x, inv);
-    }
+    if (lane < nv) store_codes<CODE, T>(codes + off * c.d + lane * kElems<T>, x, inv, odd);
+    for (int v = lane + 32; v < nv; v += 32)
+      store_codes<CODE, T>(codes + off * c.d + v * kElems<T>, vec(v), inv, odd);
     __syncwarp();  // every lane has read the old scale
     if (lane == 0) *scale = kv::pow2f(e);
   }
 }
 
-// ---- read back: a thread per 16 codes ----
+// ---- read back ----
+//
+// A thread writes 16 bytes of each of kReadItems places; the page ids of all of
+// them are asked for at once, then the codes and scales of all.
 
 constexpr int kReadThreads = 256;
-
-template <typename T>
-__device__ __forceinline__ void put4(T *p, float4 v);
-template <>
-__device__ __forceinline__ void put4<float>(float *p, float4 v) {
-  *reinterpret_cast<float4 *>(p) = v;
-}
-template <>
-__device__ __forceinline__ void put4<bf16>(bf16 *p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
-                                             *reinterpret_cast<const uint32_t *>(&b));
-}
+constexpr int kReadItems = 4;
 
 template <typename T, int CODE>
 __global__ void __launch_bounds__(kReadThreads)
@@ -269,24 +316,55 @@ __global__ void __launch_bounds__(kReadThreads)
   const float *scale = side ? c.v_scale : c.k_scale;
   T *out = static_cast<T *>(side ? rows.v : rows.k);
   const int64_t ld = side ? rows.ld_v : rows.ld_k;
-  const int d16 = c.d >> 4, per_token = c.h_kv * d16;
+  constexpr int E = kElems<T>;
+  const int dv_log2 = 31 - __clz(c.d / E), per_token = c.h_kv << dv_log2;
   const int64_t total = (int64_t)len * per_token;
-  for (int64_t u = (int64_t)blockIdx.x * kReadThreads + threadIdx.x; u < total;
-       u += (int64_t)gridDim.x * kReadThreads) {
-    const int t = (int)(u / per_token), r = (int)(u % per_token);
-    const int head = r / d16, j = r % d16, at = first + t;
-    const int id = kv_page(c, slot, at >> c.page_log2, true);
-    if (id < 0) continue;
-    const int64_t blk = c.block(layer, id, head);
-    const int row = at & (c.page_tokens - 1);
-    const uint4 w = *reinterpret_cast<const uint4 *>(
-        codes + ((blk << c.page_log2) + row) * c.d + 16 * j);
-    const float f = scale[blk];
-    T *dst = out + (int64_t)(tok0 + t) * ld + (int64_t)head * c.d + 16 * j;
-    put4<T>(dst, scale4(f, kv::Code<CODE>::decode4(w.x)));
-    put4<T>(dst + 4, scale4(f, kv::Code<CODE>::decode4(w.y)));
-    put4<T>(dst + 8, scale4(f, kv::Code<CODE>::decode4(w.z)));
-    put4<T>(dst + 12, scale4(f, kv::Code<CODE>::decode4(w.w)));
+  for (int64_t u0 = (int64_t)blockIdx.x * (kReadThreads * kReadItems) + threadIdx.x; u0 < total;
+       u0 += (int64_t)gridDim.x * (kReadThreads * kReadItems)) {
+    int t[kReadItems], r[kReadItems], id[kReadItems];
+#pragma unroll
+    for (int x = 0; x < kReadItems; ++x) {
+      const int64_t u = u0 + x * kReadThreads;
+      id[x] = -1;
+      if (u < total) {
+        t[x] = u >> 32 == 0 ? (int)((uint32_t)u / (uint32_t)per_token) : (int)(u / per_token);
+        r[x] = (int)(u - (int64_t)t[x] * per_token);
+        id[x] = kv_page(c, slot, (first + t[x]) >> c.page_log2, true);
+      }
+    }
+    uint32_t w[kReadItems][E / 4];
+    float f[kReadItems];
+#pragma unroll
+    for (int x = 0; x < kReadItems; ++x)
+      if (id[x] >= 0) {
+        const int head = r[x] >> dv_log2, row = (first + t[x]) & (c.page_tokens - 1);
+        const int64_t blk = c.block(layer, id[x], head);
+        const uint8_t *p = codes + ((blk << c.page_log2) + row) * c.d +
+                           E * (r[x] - (head << dv_log2));
+        if constexpr (E == 4) {
+          w[x][0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+          const uint2 two = *reinterpret_cast<const uint2 *>(p);
+          w[x][0] = two.x, w[x][E / 4 - 1] = two.y;
+        }
+        f[x] = scale[blk];
+      }
+#pragma unroll
+    for (int x = 0; x < kReadItems; ++x)
+      if (id[x] >= 0) {
+        T *dst = out + (int64_t)(tok0 + t[x]) * ld + (int64_t)E * r[x];
+        const float4 a = scale4(f[x], kv::Code<CODE>::decode4(w[x][0]));
+        if constexpr (E == 4) {
+          *reinterpret_cast<float4 *>(dst) = a;
+        } else {
+          const float4 b = scale4(f[x], kv::Code<CODE>::decode4(w[x][E / 4 - 1]));
+          const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(a.x, a.y),
+                                       __floats2bfloat162_rn(a.z, a.w),
+                                       __floats2bfloat162_rn(b.x, b.y),
+                                       __floats2bfloat162_rn(b.z, b.w)};
+          *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(h);
+        }
+      }
   }
 }
 
@@ -299,7 +377,7 @@ cudaError_t append_t(const KVView &c, int layer, const SeqIndex &seq, const int3
                       dim3((unsigned)((units + kAppendWarps - 1) / kAppendWarps)),
                       32 * kAppendWarps, 0, s, c, layer, seq, pos, rows);
   }
-  const int threads = c.page_tokens * c.d / (8 * kVec) < 32 ? 32 : c.page_tokens * c.d / (8 * kVec);
+  const int vecs = c.page_tokens * c.d / (kElems<T> * kVec), threads = vecs < 32 ? 32 : vecs;
   // an unaligned range of max_seqlen tokens touches one page more than an aligned one
   const int64_t pages = ((int64_t)max_seqlen + c.page_tokens - 2) / c.page_tokens + 1;
   dim3 grid((unsigned)(pages < c.max_pages ? pages : c.max_pages), (unsigned)(2 * c.h_kv),
@@ -310,8 +388,8 @@ cudaError_t append_t(const KVView &c, int layer, const SeqIndex &seq, const int3
 template <typename T, int CODE>
 cudaError_t read_t(const KVView &c, int layer, const SeqIndex &seq, const int32_t *pos,
                    int max_seqlen, const KVRows &rows, cudaStream_t s) {
-  const int64_t work = (int64_t)max_seqlen * c.h_kv * (c.d / 16);
-  int64_t bx = (work + kReadThreads - 1) / kReadThreads;
+  const int64_t work = (int64_t)max_seqlen * c.h_kv * (c.d / kElems<T>);
+  int64_t bx = (work + kReadThreads * kReadItems - 1) / (kReadThreads * kReadItems);
   if (bx > 65535) bx = 65535;
   return kv::launch(read_kernel<T, CODE>, dim3((unsigned)bx, 2, (unsigned)seq.n_seqs),
                     kReadThreads, 0, s, c, layer, seq, pos, rows);
