@@ -393,10 +393,15 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
         tc::fence_after_sync();
         const int open = lim - (w.begin + j) * kBN;  // columns that this row may see
         const bool masked = __any_sync(0xffffffffu, open < kBN);
-        // largest y of the tile; `hide`: some lane has columns that it may not see
-        auto find_peak = [&](auto hide) {
-          float peak = -INFINITY;
+        // One pass over S: weights under the present reference, their sum (in units of the
+        // denominator) and the largest exponent, as far above the reference as it is.  `hide`:
+        // some lane has columns that it may not see.
+        uint32_t p[kBN / 2];
+        float sum, peak;
+        auto weigh = [&](auto hide) {
           uint32_t s[2][32];
+          sum = 0.f;
+          peak = -INFINITY;
           tmem_ld32_async(tS, s[0]);
 #pragma unroll
           for (int h = 0; h < kBN / 32; ++h) {
@@ -405,31 +410,40 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               const uint32_t *v = s[h & 1] + 16 * b;
-              const float f = qa * s_ks[info][2 * h + b], e = s_ve[info][2 * h + b];
-              float m0 = -INFINITY, m1 = -INFINITY;
+              const float f = qa * s_ks[info][2 * h + b], e = s_ve[info][2 * h + b] - Ms;
+              float2 part = make_float2(0.f, 0.f);
 #pragma unroll
               for (int x = 0; x < 16; x += 2) {
-                const float a0 = __uint_as_float(v[x]), a1 = __uint_as_float(v[x + 1]);
-                if (!hide.value || 32 * h + 16 * b + x < open) m0 = fmaxf(m0, a0);
-                if (!hide.value || 32 * h + 16 * b + x + 1 < open) m1 = fmaxf(m1, a1);
+                float2 y =
+                    fma2(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), f, e);
+                if (hide.value) {
+                  if (32 * h + 16 * b + x >= open) y.x = -INFINITY;
+                  if (32 * h + 16 * b + x + 1 >= open) y.y = -INFINITY;
+                }
+                peak = fmaxf(fmaxf(y.x, y.y), peak);
+                y.x = fast_exp2(y.x);
+                y.y = fast_exp2(y.y);
+                part = add2(part, y);
+                p[16 * h + 8 * b + x / 2] = half2_bits(y.x, y.y);
               }
-              m0 = fmaxf(m0, m1);
-              // (a row without columns: -inf times 0 would be NaN, which fmaxf drops)
-              peak = fmaxf(peak, fmaf(m0, f, e));
+              sum = fmaf(part.x + part.y, s_un[info][2 * h + b], sum);
             }
           }
-          return peak;
         };
-        const float peak = masked ? find_peak(std::true_type{}) : find_peak(std::false_type{});
-        bool seen = j == 0;  // pv_done of the tile before this one (each phase is waited for)
-        if (__any_sync(0xffffffffu, peak > M + kSlack)) {
-          const float m = fmaxf(M, peak);
+        if (masked)
+          weigh(std::true_type{});
+        else
+          weigh(std::false_type{});
+        bool seen = MT == 2 || j == 0;  // pv_done of the tile before this one: with MT = 2 its
+                                        // product came before this tile's S
+        if (__any_sync(0xffffffffu, peak > (M == -INFINITY ? -INFINITY : kSlack + kLift))) {
+          const float m = fmaxf(M, peak + Ms);
           const float f = m == -INFINITY ? 1.f : fast_exp2(M - m);
           M = m;
           Ms = m == -INFINITY ? 0.f : m - kLift;
           L *= f;
           if (j > 0) {  // O holds the tiles before this one
-            if (!warp_wait(&pv_done[mt], n - 1)) {
+            if (!seen && !warp_wait(&pv_done[mt], n - 1)) {
               ok = false;
               break;
             }
@@ -446,43 +460,14 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
               tmem_st16(tO + x + 16, o + 16);
             }
           }
+          if (masked)
+            weigh(std::true_type{});
+          else
+            weigh(std::false_type{});
         }
-        // weights; P's columns follow those of S that have been read
-        auto weigh = [&](auto hide) {
-          uint32_t s[2][32];
-          tmem_ld32_async(tS, s[0]);
+        L += sum;
 #pragma unroll
-          for (int h = 0; h < kBN / 32; ++h) {
-            uint32_t p[16];
-            tmem_ld_wait();
-            if (h + 1 < kBN / 32) tmem_ld32_async(tS + 32 * (h + 1), s[(h + 1) & 1]);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const uint32_t *v = s[h & 1] + 16 * b;
-              const float f = qa * s_ks[info][2 * h + b], e = s_ve[info][2 * h + b] - Ms;
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int x = 0; x < 16; x += 2) {
-                float2 y =
-                    fma2(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), f, e);
-                if (hide.value) {
-                  if (32 * h + 16 * b + x >= open) y.x = -INFINITY;
-                  if (32 * h + 16 * b + x + 1 >= open) y.y = -INFINITY;
-                }
-                y.x = fast_exp2(y.x);
-                y.y = fast_exp2(y.y);
-                sum = add2(sum, y);
-                p[8 * b + x / 2] = half2_bits(y.x, y.y);
-              }
-              L = fmaf(sum.x + sum.y, s_un[info][2 * h + b], L);
-            }
-            tmem_st16(tS + 16 * h, p);
-          }
-        };
-        if (masked)
-          weigh(std::true_type{});
-        else
-          weigh(std::false_type{});
+        for (int x = 0; x < kBN / 2; x += 16) tmem_st16(tS + x, p + x);
         tc::tmem_st_wait();
         tc::fence_before_sync();
         if (!seen && !warp_wait(&pv_done[mt], n - 1)) {
