@@ -375,14 +375,14 @@ cudaError_t append_t(const KVView &c, int layer, const SeqIndex &seq, const int3
     const int64_t units = (int64_t)seq.n_seqs * 2 * c.h_kv;
     return kv::launch(append_warp_kernel<T, CODE>,
                       dim3((unsigned)((units + kAppendWarps - 1) / kAppendWarps)),
-                      32 * kAppendWarps, 0, s, c, layer, seq, pos, rows);
+                      32 * kAppendWarps, 0, s, 1, c, layer, seq, pos, rows);
   }
   const int vecs = c.page_tokens * c.d / (kElems<T> * kVec), threads = vecs < 32 ? 32 : vecs;
   // an unaligned range of max_seqlen tokens touches one page more than an aligned one
   const int64_t pages = ((int64_t)max_seqlen + c.page_tokens - 2) / c.page_tokens + 1;
   dim3 grid((unsigned)(pages < c.max_pages ? pages : c.max_pages), (unsigned)(2 * c.h_kv),
             (unsigned)seq.n_seqs);
-  return kv::launch(append_tile_kernel<T, CODE>, grid, threads, 0, s, c, layer, seq, pos, rows);
+  return kv::launch(append_tile_kernel<T, CODE>, grid, threads, 0, s, 1, c, layer, seq, pos, rows);
 }
 
 template <typename T, int CODE>
@@ -392,7 +392,7 @@ cudaError_t read_t(const KVView &c, int layer, const SeqIndex &seq, const int32_
   int64_t bx = (work + kReadThreads * kReadItems - 1) / (kReadThreads * kReadItems);
   if (bx > 65535) bx = 65535;
   return kv::launch(read_kernel<T, CODE>, dim3((unsigned)bx, 2, (unsigned)seq.n_seqs),
-                    kReadThreads, 0, s, c, layer, seq, pos, rows);
+                    kReadThreads, 0, s, 1, c, layer, seq, pos, rows);
 }
 
 }  // namespace

@@ -41,13 +41,17 @@ constexpr int kInfo = 8;                 // tiles of page info in flight
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f, kLift = 7.f;
 
-template <int D, int MT>
+template <int D, int MT, bool PAIR>
 struct PromptCfg {
-  static constexpr int kRows = 128 * MT;
-  static constexpr int DC = D < 128 ? D : 128;          // d range of a slot
-  static constexpr int kHalves = D / DC;                // slots of a K or V tile
-  static constexpr int kSlot = kBN * DC * 2;            // bytes
-  static constexpr int kSlots = 4;
+  static constexpr int kCtas = PAIR ? 2 : 1;            // that share a unit
+  static constexpr int kRows = 128 * MT * kCtas;        // of a unit
+  // A slot holds a K or V tile's codes for one MMA group: alone, 128 tokens x min(d, 128); in
+  // a pair, this CTA's half of the operand, 64 tokens x d of K or 128 tokens x d / 2 of V.
+  static constexpr int DC = D < 128 ? D : 128;
+  static constexpr int kHalves = PAIR ? 1 : D / DC;     // slots of a K or V tile
+  static constexpr int kSlot = PAIR ? 128 * D : kBN * DC * 2;  // bytes
+  static constexpr int kKPanel = PAIR ? 8192 : 16384;   // bytes of a slot's 64 d (K), 64 d (V)
+  static constexpr int kSlots = PAIR && D == 128 ? 6 : 4;
   static constexpr int kQTile = 128 * D * 2;
   static constexpr int kConvWarps = MT == 2 ? 4 : 8;
   static constexpr int kConvTeams = MT == 2 ? 1 : 2;    // teams take the slots in turn
@@ -62,7 +66,7 @@ struct PromptCfg {
   static constexpr int kSmem = MT * kQTile + kSlots * kSlot + 1024;
   // TMEM columns: S (MT tiles, or two buffers), then O
   static constexpr int kO = 2 * kBN;
-  static constexpr int kTmem = kO + MT * D <= 256 ? 256 : 512;
+  static constexpr int kTmem = 512;
   static constexpr int kPartFloats = kRows * (D + 2);
 };
 
@@ -72,8 +76,99 @@ struct Unit {
 };
 
 // f16 operands, f32 accumulator; B MN-major if `mn`
-__host__ __device__ constexpr uint32_t idesc_f16(int n, bool mn) {
-  return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool mn) {
+  return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(m >> 4) << 24);
+}
+
+// ---- what differs between a CTA alone and a pair (cluster of two, cta_group::2) ----
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// arrive on CTA 0's barrier of the pair
+__device__ __forceinline__ void arrive_leader(uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity) {
+  for (uint32_t it = 0; it < (1u << 20); ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                       uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(accumulate)
+        : "memory");
+  else
+    tc::mma_ss_f16(d, a, b, id, accumulate);
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                       uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(accumulate)
+        : "memory");
+  else
+    tc::mma_ts_f16(d, a, b, id, accumulate);
+}
+// arrive on `bar` (of both CTAs of a pair) when the MMAs issued so far are done
+template <bool PAIR>
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    tc::mma_commit(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(slot)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tc::tmem_alloc(slot, cols);
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols)
+                 : "memory");
+  else
+    tc::tmem_dealloc(taddr, cols);
 }
 
 // Shared-memory operands in the 128-byte swizzle: 128-byte rows of 64 elements,
@@ -250,18 +345,18 @@ __device__ __forceinline__ void put8(bf16 *p, const float *v) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int CODE, int D, int MT>
-__global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
+template <int CODE, int D, int MT, bool PAIR>
+__global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
     attend_prompt_kernel(const KVView c, const int layer, const KVAttendArgs a, const int splits,
                          const int hinted_units, float *__restrict__ part) {
-  using Cfg = PromptCfg<D, MT>;
+  using Cfg = PromptCfg<D, MT, PAIR>;
   constexpr int R = Cfg::kRows, NS = Cfg::kSlots, H = Cfg::kHalves, CW = Cfg::kConvWarps;
   constexpr int TEAMS = Cfg::kConvTeams;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char *sQ = smem;                             // [MT][D / 64][128 rows][128 bytes]
-  unsigned char *sKV = smem + MT * Cfg::kQTile;         // [NS][DC / 64][128 tokens][128 bytes]
+  unsigned char *sKV = smem + MT * Cfg::kQTile;         // [NS] slots, 128-byte rows of 64 d
   __shared__ __align__(8) uint64_t slot_full[NS], slot_empty[NS], info_full[kInfo],
       info_empty[kInfo], s_full[2], p_full[MT], pv_done[MT], q_full, drain;
   __shared__ int s_blk[kInfo][kGroups], s_plain[kInfo];
@@ -273,37 +368,49 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
   kv::dependent_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // blocks are ordered by row tile, the heaviest of every sequence and head first
-  const int heads = a.seq.n_seqs * c.h_kv, z = blockIdx.x % heads, split = blockIdx.y;
+  const int block = blockIdx.x / Cfg::kCtas, rank = PAIR ? (int)cluster_rank() : 0;
+  const int heads = a.seq.n_seqs * c.h_kv, z = block % heads, split = blockIdx.y;
   const int i = z / c.h_kv, head = z % c.h_kv, group = c.h_q / c.h_kv;
-  const int64_t u0 = blockIdx.x / heads;
+  const int64_t u0 = block / heads;
   Unit w;
-  if (!find_unit(c, a, i, head, u0, R, 0, 1, tid + split + (int)u0 == 0, &w)) return;
+  if (!find_unit(c, a, i, head, u0, R, 0, 1, tid + split + rank + (int)u0 == 0, &w)) return;
   constexpr int kConv = 4 * MT, kMma = kConv + CW, kPages = kMma + 1;
   static_assert(kMma == 12, "four warpgroups: softmax and converters, then MMA and pages");
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&slot_full[i], CW / TEAMS), mbar_init(&slot_empty[i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&slot_full[i], CW / TEAMS * Cfg::kCtas), mbar_init(&slot_empty[i], 1);
     for (int i = 0; i < kInfo; ++i)
       mbar_init(&info_full[i], 1),
           mbar_init(&info_empty[i], 2 * H * (CW / TEAMS) + 4 * MT);  // its slots' loads, softmax
     for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1);
-    for (int i = 0; i < MT; ++i) mbar_init(&p_full[i], 4), mbar_init(&pv_done[i], 1);
-    mbar_init(&q_full, 4 * MT);
+    for (int i = 0; i < MT; ++i) mbar_init(&p_full[i], 4 * Cfg::kCtas), mbar_init(&pv_done[i], 1);
+    mbar_init(&q_full, 4 * MT * Cfg::kCtas);
     mbar_init(&drain, 1);
     s_abort = 0;
     mbar_fence_init();
   }
-  if (warp == kMma) tc::tmem_alloc(&tmem_slot, Cfg::kTmem);
+  if (warp == kMma) tmem_alloc<PAIR>(&tmem_slot, Cfg::kTmem);
   tc::fence_before_sync();
-  __syncthreads();
+  if constexpr (PAIR)
+    cluster_sync();
+  else
+    __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
   volatile int *abort_flag = &s_abort;
   // A wait that gives up ends the kernel's work: every role stops at its next wait.
   auto wait = [&](uint64_t *bar, uint32_t phase) {
-    if (mbar_wait_bounded(bar, phase & 1) && !*abort_flag) return true;
+    if ((PAIR ? wait_cluster(bar, phase & 1) : mbar_wait_bounded(bar, phase & 1)) && !*abort_flag)
+      return true;
     if (*abort_flag == 0) raise_error(c.err, GDN_DEVERR_TIMEOUT);
     *abort_flag = 1;
     return false;
+  };
+  // slot_full, q_full and p_full are waited for by the MMA warp, which is CTA 0's in a pair
+  auto arrive_mma = [&](uint64_t *bar) {
+    if constexpr (PAIR)
+      arrive_leader(bar);
+    else
+      mbar_arrive(bar);
   };
   auto warp_wait = [&](uint64_t *bar, uint32_t phase) {
     return __all_sync(0xffffffffu, wait(bar, phase));
@@ -333,13 +440,14 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
     each_unit([&](const int64_t u, const int T) {
       // ---- softmax: one thread per query row ----
       const int mt = warp >> 2;
-      const int row = 128 * mt + 32 * (warp & 3) + lane;  // in the unit
+      const int tile_row = 128 * (mt * Cfg::kCtas + rank) + 32 * (warp & 3);
+      const int row = tile_row + lane;                    // in the unit
       const int grow = w.row0 + min(row, w.rows - 1);     // rows past the end repeat the last
       const int lim = w.kv_len - w.len + 1 + grow / group;
       float qa = 0.f;  // scale * log2(e) * the query's power of two
       if (T > 0) {
         constexpr int E = D / 32;
-        const int row_w = w.row0 + 128 * mt + 32 * (warp & 3);
+        const int row_w = w.row0 + tile_row;
 #pragma unroll 4
         for (int r = 0; r < 32; ++r) {
           const int gr = min(row_w + r, w.row0 + w.rows - 1);
@@ -376,7 +484,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
         }
         tc::fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full);
+        if (lane == 0) arrive_mma(&q_full);
       }
       const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
       const uint32_t tO = tmem + lanes + Cfg::kO + mt * D;
@@ -476,7 +584,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&p_full[mt]);
+          arrive_mma(&p_full[mt]);
           mbar_arrive(&info_empty[info]);
         }
       }
@@ -490,7 +598,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
                            (int64_t)(head * group + grow % group) * D;
         float *mine = part;
         if (!whole) {
-          mine += ((int64_t)blockIdx.x * splits + split) * Cfg::kPartFloats;
+          mine += ((int64_t)block * splits + split) * Cfg::kPartFloats;
           if (live) {
             mine[R * D + row] = M;
             mine[R * D + R + row] = L;
@@ -528,16 +636,37 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
     set_regs_down<Cfg::kConvRegs>();
     each_unit([&](const int64_t, const int T) {
       // ---- converters ----
-      constexpr int DC = Cfg::DC, COLS = DC / 16;
-      constexpr int PASS = 32 * CW / TEAMS / COLS;  // rows that a team covers at once
-      constexpr int VPS = kBN / PASS;               // loads per thread and slot
+      constexpr int kTeam = 32 * CW / TEAMS;
+      constexpr int VPS = Cfg::kSlot / 32 / kTeam;  // loads (of 16 codes) per thread and slot
       constexpr int PF = Cfg::kPrefetch;
       const int team = (warp - kConv) / (CW / TEAMS);
       const int ct = tid - 32 * (kConv + team * (CW / TEAMS));
-      // d = 64: 4 lanes to a row; else lanes 0-3 and 8-11 share a row, 4-7 and 12-15 the next:
-      // eight consecutive lanes write all eight 16-byte columns of the swizzled rows
-      const int col = DC == 64 ? ct & 3 : (ct & 3) | (ct >> 1 & 4);
-      const int row = DC == 64 ? ct >> 2 : (ct >> 2 & 1) | (ct >> 3 & ~1);
+      // Place of a thread's load v in a slot of 4 or 8 columns of 16 codes: with 4, 4 lanes to
+      // a row; with 8, lanes 0-3 and 8-11 share a row, 4-7 and 12-15 the next.  Either way
+      // eight consecutive lanes write all eight 16-byte columns of the swizzled rows.
+      auto place4 = [&](int v, int *row, int *col) {
+        *row = v * (kTeam / 4) + (ct >> 2);
+        *col = ct & 3;
+      };
+      auto place8 = [&](int v, int *row, int *col) {
+        *row = v * (kTeam / 8) + ((ct >> 2 & 1) | (ct >> 3 & ~1));
+        *col = (ct & 3) | (ct >> 1 & 4);
+      };
+      auto in_slot = [&](int side, int v, int *row, int *col) {
+        if constexpr (!PAIR) {
+          if constexpr (D == 64)
+            place4(v, row, col);
+          else
+            place8(v, row, col);
+        } else if (side == 0) {  // 64 tokens, d / 16 columns, by eights
+          place8(D == 256 ? v % (VPS / 2) : v, row, col);
+          if (D == 256 && v >= VPS / 2) *col += 8;
+        } else if constexpr (D == 256) {
+          place8(v, row, col);
+        } else {
+          place4(v, row, col);
+        }
+      };
       const int page_bytes = D << c.page_log2;
       const int n_slots = 2 * H * T;
       // slot x: its tile, side and half, in the order of the MMAs
@@ -565,10 +694,13 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
         const uint32_t n = done + tile;
         const int info = n % kInfo;
         if (!warp_wait(&info_full[info], n / kInfo)) return false;
-        const uint8_t *base = (side ? c.v : c.k) + half * DC + 16 * col;
-        auto fetch = [&](int v, int blk) {
-          const int r = v * PASS + row;
-          const uint8_t *p = base + (int64_t)blk * page_bytes + (r & (c.page_tokens - 1)) * D;
+        // of a pair, this CTA takes half of K's tokens and half of V's d
+        const int tok0 = PAIR && side == 0 ? rank * 64 : 0;
+        const uint8_t *base =
+            (side ? c.v : c.k) + (PAIR ? (side ? rank * (D / 2) : 0) : half * Cfg::DC);
+        auto fetch = [&](int v, int r, int col, int blk) {
+          const uint8_t *p =
+              base + (int64_t)blk * page_bytes + (r & (c.page_tokens - 1)) * D + 16 * col;
           asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                        : "=r"(dst[v].x), "=r"(dst[v].y), "=r"(dst[v].z), "=r"(dst[v].w)
                        : "l"(p));
@@ -576,15 +708,26 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
         if (s_plain[info]) {  // nothing to leave out: loads without a branch between them
           int blk[VPS];
 #pragma unroll
-          for (int v = 0; v < VPS; ++v) blk[v] = s_blk[info][(v * PASS + row) >> 4];
+          for (int v = 0; v < VPS; ++v) {
+            int r, col;
+            in_slot(side, v, &r, &col);
+            blk[v] = s_blk[info][(tok0 + r) >> 4];
+          }
 #pragma unroll
-          for (int v = 0; v < VPS; ++v) fetch(v, blk[v]);
+          for (int v = 0; v < VPS; ++v) {
+            int r, col;
+            in_slot(side, v, &r, &col);
+            fetch(v, tok0 + r, col, blk[v]);
+          }
         } else {
 #pragma unroll
           for (int v = 0; v < VPS; ++v) {
-            const int r = v * PASS + row, blk = s_blk[info][r >> 4];
+            int r, col;
+            in_slot(side, v, &r, &col);
+            const int blk = s_blk[info][(tok0 + r) >> 4];
             dst[v] = make_uint4(0, 0, 0, 0);  // past the end, or no page: the code of zero
-            if (blk >= 0 && (w.begin + tile) * kBN + r < w.kv_len) fetch(v, blk);
+            if (blk >= 0 && (w.begin + tile) * kBN + tok0 + r < w.kv_len)
+              fetch(v, tok0 + r, col, blk);
           }
         }
         __syncwarp();
@@ -604,16 +747,20 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
             ok = false;
             break;
           }
-          unsigned char *dst = sKV + (n % NS) * Cfg::kSlot + (col >> 2) * 16384;
+          int tile, side, half;
+          place(x, &tile, &side, &half);
+          const int panel = side ? 16384 : Cfg::kKPanel;
+          unsigned char *dst = sKV + (n % NS) * Cfg::kSlot;
 #pragma unroll
           for (int v = 0; v < VPS; ++v) {
-            const int r = v * PASS + row;
+            int r, col;
+            in_slot(side, v, &r, &col);
             uint32_t h[8];
             Widen<CODE>::four(code[y][v].x, h[0], h[1]);
             Widen<CODE>::four(code[y][v].y, h[2], h[3]);
             Widen<CODE>::four(code[y][v].z, h[4], h[5]);
             Widen<CODE>::four(code[y][v].w, h[6], h[7]);
-            unsigned char *q = dst + r * 128;
+            unsigned char *q = dst + (col >> 2) * panel + r * 128;
             const int k = 2 * (col & 3);
             *reinterpret_cast<uint4 *>(q + ((k ^ (r & 7)) << 4)) =
                 make_uint4(h[0], h[1], h[2], h[3]);
@@ -622,7 +769,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
           }
           tc::fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&slot_full[n % NS]);
+          if (lane == 0) arrive_mma(&slot_full[n % NS]);
           if (x + PF * TEAMS < n_slots) ok = load(x + PF * TEAMS, code[y]);
         }
       }
@@ -634,9 +781,10 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
       // The whole warp takes every branch and wait; one elected lane issues.  (Issued
       // from a branch on the lane number, an MMA took 160 cycles under busy softmax
       // warps instead of 70.)
-      if (T > 0) {
-        constexpr uint32_t id_qk = idesc_f16(kBN, false);
-        constexpr uint32_t id_pv = idesc_f16(Cfg::DC, true);
+      if (T > 0 && rank == 0) {
+        constexpr int kM = 128 * Cfg::kCtas;
+        constexpr uint32_t id_qk = idesc_f16(kM, kBN, false);
+        constexpr uint32_t id_pv = idesc_f16(kM, PAIR ? D : Cfg::DC, true);
         const bool issue = elect_one();
         uint32_t at = slots;  // next slot
         auto next_slot = [&]() {
@@ -653,12 +801,12 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
           const uint32_t k = k_low + (slot % NS) * (Cfg::kSlot / 16);
           if (issue) {
 #pragma unroll
-            for (int x = 0; x < Cfg::DC / 16; ++x) {
-              const uint32_t off = ((x >> 2) * 16384 + (x & 3) * 32) / 16;
-              tc::mma_ss_f16(tmem + buf * kBN, desc(q + off), desc(k + off), id_qk, half + x > 0);
-            }
-            if (then) tc::mma_commit(then);
-            if (free) tc::mma_commit(free);
+            for (int x = 0; x < D / H / 16; ++x)
+              mma_ss<PAIR>(tmem + buf * kBN, desc(q + ((x >> 2) * 16384 + (x & 3) * 32) / 16),
+                           desc(k + ((x >> 2) * Cfg::kKPanel + (x & 3) * 32) / 16), id_qk,
+                           half + x > 0);
+            if (then) mma_commit<PAIR>(then);
+            if (free) mma_commit<PAIR>(free);
           }
           __syncwarp();
         };
@@ -669,10 +817,10 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
           if (issue) {
 #pragma unroll
             for (int x = 0; x < kBN / 16; ++x)
-              tc::mma_ts_f16(tmem + Cfg::kO + mt * D + half * Cfg::DC, tmem + buf * kBN + 8 * x,
-                             desc(v + x * 128), id_pv, !first || x > 0);
-            if (then) tc::mma_commit(then);
-            if (free) tc::mma_commit(free);
+              mma_ts<PAIR>(tmem + Cfg::kO + mt * D + half * Cfg::DC, tmem + buf * kBN + 8 * x,
+                           desc(v + x * 128), id_pv, !first || x > 0);
+            if (then) mma_commit<PAIR>(then);
+            if (free) mma_commit<PAIR>(free);
           }
           __syncwarp();
         };
@@ -729,7 +877,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
         };
         ok = run();
         if (!ok) {  // the MMAs in flight finish before TMEM is freed
-          if (issue) tc::mma_commit(&drain);
+          if (issue) mma_commit<PAIR>(&drain);
           mbar_wait_bounded(&drain, 0);
         }
       }
@@ -779,23 +927,26 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::kThreads, 1)
   } else {
     set_regs_down<Cfg::kMiscRegs>();
   }
+  __syncwarp();
   tc::fence_before_sync();
-  __syncthreads();
+  if constexpr (PAIR)
+    cluster_sync();  // no CTA leaves while the other's arrivals or MMAs may still reach it
+  else
+    __syncthreads();
   if (warp == kMma) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, Cfg::kTmem);
+    tmem_dealloc<PAIR>(tmem, Cfg::kTmem);
   }
 }
 
 // Joins the splits of a unit: a CTA per (unit, sequence and head) and four rows.
 constexpr int kJoinRows = 4;
 
-template <int D, int MT>
+template <int D, int R>
 __global__ void __launch_bounds__(kJoinRows * D / 4)
     attend_prompt_join_kernel(const KVView c, const KVAttendArgs a, const int splits,
                               const float *part) {
-  using Cfg = PromptCfg<D, MT>;
-  constexpr int R = Cfg::kRows;
+  constexpr int kPartFloats = R * (D + 2);
   kv::dependents_may_launch();
   kv::dependent_wait();
   const int heads = a.seq.n_seqs * c.h_kv, z = blockIdx.x % heads;
@@ -804,14 +955,14 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
   const int row = blockIdx.y * kJoinRows + threadIdx.x / (D / 4);
   const int d = 4 * (threadIdx.x % (D / 4));
   if (row >= w.rows) return;
-  const float *base = part + (int64_t)blockIdx.x * splits * Cfg::kPartFloats;
+  const float *base = part + (int64_t)blockIdx.x * splits * kPartFloats;
   float m = -INFINITY, l = 0.f;
   for (int s = 0; s < splits; ++s)
-    m = fmaxf(m, __ldcg(base + (int64_t)s * Cfg::kPartFloats + R * D + row));
+    m = fmaxf(m, __ldcg(base + (int64_t)s * kPartFloats + R * D + row));
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = 0; s < splits; ++s) {
-    const float *p = base + (int64_t)s * Cfg::kPartFloats;
+    const float *p = base + (int64_t)s * kPartFloats;
     const float pm = __ldcg(p + R * D + row), pl = __ldcg(p + R * D + R + row);
     const float f = pm == -INFINITY ? (pl == 0.f ? 0.f : 1.f) : fast_exp2(pm - m);
     l += f * pl;
@@ -830,23 +981,23 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
   }
 }
 
-template <int CODE, int D, int MT>
+template <int CODE, int D, int MT, bool PAIR>
 cudaError_t launch_prompt(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
                           cudaStream_t s) {
-  using Cfg = PromptCfg<D, MT>;
-  auto kernel = attend_prompt_kernel<CODE, D, MT>;
+  using Cfg = PromptCfg<D, MT, PAIR>;
+  auto kernel = attend_prompt_kernel<CODE, D, MT, PAIR>;
   static std::atomic<uint64_t> seen{0};
   cudaError_t e = kv::allow_smem(kernel, Cfg::kSmem, h.device, seen);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.max_seqlen * (c.h_q / c.h_kv);
   const int64_t z = (int64_t)a.seq.n_seqs * c.h_kv;
   int64_t units = (rows + Cfg::kRows - 1) / Cfg::kRows;
-  if (units * z > INT32_MAX) units = INT32_MAX / z;
+  if (units * z > INT32_MAX / Cfg::kCtas) units = INT32_MAX / Cfg::kCtas / z;
   // too few units for the GPU: cut each one's context
-  const int64_t tiles = a.max_kv_len / kBN + 1;
+  const int64_t tiles = a.max_kv_len / kBN + 1, room = h.sm_count / Cfg::kCtas;
   int64_t splits = 1;
-  if (units * z < h.sm_count) {
-    splits = h.sm_count / (units * z);
+  if (units * z < room) {
+    splits = room / (units * z);
     if (splits > tiles) splits = tiles;
     if (splits > 64) splits = 64;
   }
@@ -857,13 +1008,14 @@ cudaError_t launch_prompt(const KVView &c, int layer, const KVAttendArgs &a, con
                     &temporary);
     if (e != cudaSuccess) return e;
   }
-  e = kv::launch(kernel, dim3((unsigned)(units * z), (unsigned)splits), Cfg::kThreads, Cfg::kSmem,
-                 s, c, layer, a, (int)splits, (int)units, static_cast<float *>(work));
+  e = kv::launch(kernel, dim3((unsigned)(units * z * Cfg::kCtas), (unsigned)splits), Cfg::kThreads,
+                 Cfg::kSmem, s, Cfg::kCtas, c, layer, a, (int)splits, (int)units,
+                 static_cast<float *>(work));
   if (splits > 1) {
     if (e == cudaSuccess)
-      e = kv::launch(attend_prompt_join_kernel<D, MT>,
+      e = kv::launch(attend_prompt_join_kernel<D, Cfg::kRows>,
                      dim3((unsigned)(units * z), Cfg::kRows / kJoinRows), kJoinRows * D / 4, 0, s,
-                     c, a, (int)splits, static_cast<const float *>(work));
+                     1, c, a, (int)splits, static_cast<const float *>(work));
     const cudaError_t ef = temporary ? cudaFreeAsync(work, s) : cudaSuccess;
     if (e == cudaSuccess) e = ef;
   }
@@ -873,13 +1025,16 @@ cudaError_t launch_prompt(const KVView &c, int layer, const KVAttendArgs &a, con
 template <int CODE>
 cudaError_t by_dim(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
                    cudaStream_t s) {
-  const bool one = (int64_t)a.max_seqlen * (c.h_q / c.h_kv) <= 128;
-  if (c.d == 256) return launch_prompt<CODE, 256, 1>(c, layer, a, h, s);
+  const int64_t rows = (int64_t)a.max_seqlen * (c.h_q / c.h_kv);
+  if (c.d == 256)
+    return rows <= 128 ? launch_prompt<CODE, 256, 1, false>(c, layer, a, h, s)
+                       : launch_prompt<CODE, 256, 1, true>(c, layer, a, h, s);
   if (c.d == 128)
-    return one ? launch_prompt<CODE, 128, 1>(c, layer, a, h, s)
-               : launch_prompt<CODE, 128, 2>(c, layer, a, h, s);
-  return one ? launch_prompt<CODE, 64, 1>(c, layer, a, h, s)
-             : launch_prompt<CODE, 64, 2>(c, layer, a, h, s);
+    return rows <= 128   ? launch_prompt<CODE, 128, 1, false>(c, layer, a, h, s)
+           : rows <= 256 ? launch_prompt<CODE, 128, 2, false>(c, layer, a, h, s)
+                         : launch_prompt<CODE, 128, 2, true>(c, layer, a, h, s);
+  return rows <= 128 ? launch_prompt<CODE, 64, 1, false>(c, layer, a, h, s)
+                     : launch_prompt<CODE, 64, 2, false>(c, layer, a, h, s);
 }
 
 }  // namespace
