@@ -92,28 +92,16 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// arrive on CTA 0's barrier of the pair
+// Arrive on CTA 0's barrier of the pair.  What the arrival stands for lies in this CTA's
+// own shared memory or TMEM and is complete before it (proxy fence, or the wait for TMEM
+// stores), so the default scope will do: a cluster-scope release also waits for the
+// global loads in flight, 1000 cycles for each slot.
 __device__ __forceinline__ void arrive_leader(uint64_t *bar) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar))
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar))
       : "memory");
 }
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity) {
-  for (uint32_t it = 0; it < (1u << 20); ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
-  return false;
-}
-
 template <bool PAIR>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
                                        uint32_t accumulate) {
@@ -399,8 +387,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
   volatile int *abort_flag = &s_abort;
   // A wait that gives up ends the kernel's work: every role stops at its next wait.
   auto wait = [&](uint64_t *bar, uint32_t phase) {
-    if ((PAIR ? wait_cluster(bar, phase & 1) : mbar_wait_bounded(bar, phase & 1)) && !*abort_flag)
-      return true;
+    if (mbar_wait_bounded(bar, phase & 1) && !*abort_flag) return true;
     if (*abort_flag == 0) raise_error(c.err, GDN_DEVERR_TIMEOUT);
     *abort_flag = 1;
     return false;
@@ -705,14 +692,18 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
                        : "=r"(dst[v].x), "=r"(dst[v].y), "=r"(dst[v].z), "=r"(dst[v].w)
                        : "l"(p));
         };
-        if (s_plain[info]) {  // nothing to leave out: loads without a branch between them
-          int blk[VPS];
+        const bool plain = s_plain[info] != 0;  // nothing of the tile to leave out
+        int blk[VPS];
 #pragma unroll
-          for (int v = 0; v < VPS; ++v) {
-            int r, col;
-            in_slot(side, v, &r, &col);
-            blk[v] = s_blk[info][(tok0 + r) >> 4];
-          }
+        for (int v = 0; v < VPS; ++v) {
+          int r, col;
+          in_slot(side, v, &r, &col);
+          blk[v] = s_blk[info][(tok0 + r) >> 4];
+        }
+        // (the arrival comes before the loads: it would wait for them)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&info_empty[info]);
+        if (plain) {  // loads without a branch between them
 #pragma unroll
           for (int v = 0; v < VPS; ++v) {
             int r, col;
@@ -724,14 +715,11 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
           for (int v = 0; v < VPS; ++v) {
             int r, col;
             in_slot(side, v, &r, &col);
-            const int blk = s_blk[info][(tok0 + r) >> 4];
             dst[v] = make_uint4(0, 0, 0, 0);  // past the end, or no page: the code of zero
-            if (blk >= 0 && (w.begin + tile) * kBN + tok0 + r < w.kv_len)
-              fetch(v, tok0 + r, col, blk);
+            if (blk[v] >= 0 && (w.begin + tile) * kBN + tok0 + r < w.kv_len)
+              fetch(v, tok0 + r, col, blk[v]);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&info_empty[info]);
         return true;
       };
 #pragma unroll
