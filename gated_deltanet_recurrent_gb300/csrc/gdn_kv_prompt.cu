@@ -433,41 +433,81 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
       const int lim = w.kv_len - w.len + 1 + grow / group;
       float qa = 0.f;  // scale * log2(e) * the query's power of two
       if (T > 0) {
-        constexpr int E = D / 32;
-        const int row_w = w.row0 + tile_row;
-#pragma unroll 4
-        for (int r = 0; r < 32; ++r) {
-          const int gr = min(row_w + r, w.row0 + w.rows - 1);
-          const bf16 *q = static_cast<const bf16 *>(a.q) + (int64_t)(w.tok0 + gr / group) * a.ld_q +
-                          (int64_t)(head * group + gr % group) * D + lane * E;
-          float x[E];
-          if constexpr (E == 2) {
-            x[0] = Elem<bf16>::load1(q);
-            x[1] = Elem<bf16>::load1(q + 1);
-          } else {
+        // a lane takes E consecutive elements of each row; the next eight rows are on their
+        // way while eight are scaled and stored
+        constexpr int E = D / 32, kBatch = 8;
+        const int row_w = w.row0 + tile_row, last_row = w.row0 + w.rows - 1;
+        uint32_t raw[2][kBatch][E / 2];
+        auto load_rows = [&](int r0, uint32_t (*x)[E / 2]) {
 #pragma unroll
-            for (int e = 0; e < E; e += 4) {
-              const float4 f = Elem<bf16>::load4(q + e);
-              x[e] = f.x, x[e + 1] = f.y, x[e + 2] = f.z, x[e + 3] = f.w;
+          for (int r = 0; r < kBatch; ++r) {
+            const int gr = min(row_w + r0 + r, last_row);
+            const bf16 *q = static_cast<const bf16 *>(a.q) +
+                            (int64_t)(w.tok0 + gr / group) * a.ld_q +
+                            (int64_t)(head * group + gr % group) * D + lane * E;
+            if constexpr (E == 8) {
+              const uint4 v = *reinterpret_cast<const uint4 *>(q);
+              x[r][0] = v.x, x[r][1] = v.y, x[r][2] = v.z, x[r][3] = v.w;
+            } else if constexpr (E == 4) {
+              const uint2 v = *reinterpret_cast<const uint2 *>(q);
+              x[r][0] = v.x, x[r][1] = v.y;
+            } else {
+              x[r][0] = *reinterpret_cast<const uint32_t *>(q);
             }
           }
-          float m = 0.f;
+        };
+        load_rows(0, raw[0]);
 #pragma unroll
-          for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(x[e]));
+        for (int r0 = 0; r0 < 32; r0 += kBatch) {
+          if (r0 + kBatch < 32) load_rows(r0 + kBatch, raw[(r0 / kBatch + 1) & 1]);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          int ex = (int)(__float_as_uint(m) >> 23) - 127;
-          ex = ex > 126 || m == 0.f ? 0 : max(ex, -126);
-          const float inv = a.scale < 0.f ? -kv::pow2f(-ex) : kv::pow2f(-ex);
-          const int srow = 32 * (warp & 3) + r;
+          for (int r = 0; r < kBatch; ++r) {
+            const uint32_t *x = raw[(r0 / kBatch) & 1][r];
+            uint32_t m = 0;  // magnitudes of bf16 order like their bits; NaN is left out
+            float f[E];
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int d = lane * E + e, p = (d & ~3) + Widen<CODE>::place(d & 3);
-            *reinterpret_cast<__half *>(sQ + mt * Cfg::kQTile + (p >> 6) * 16384 + srow * 128 +
-                                        (((p >> 3 & 7) ^ (srow & 7)) << 4) + (p & 7) * 2) =
-                __float2half_rn(x[e] * inv);
+            for (int e = 0; e < E; e += 2) {
+              f[e] = __uint_as_float(x[e / 2] << 16);
+              f[e + 1] = __uint_as_float(x[e / 2] & 0xffff0000u);
+              const uint32_t lo = __float_as_uint(f[e]) & 0x7fffffffu;
+              const uint32_t hi = __float_as_uint(f[e + 1]) & 0x7fffffffu;
+              if (lo <= 0x7f800000u) m = max(m, lo);
+              if (hi <= 0x7f800000u) m = max(m, hi);
+            }
+            m = __reduce_max_sync(0xffffffffu, m);
+            int ex = (int)(m >> 23) - 127;
+            ex = ex > 126 || m == 0 ? 0 : max(ex, -126);
+            const float inv = a.scale < 0.f ? -kv::pow2f(-ex) : kv::pow2f(-ex);
+            const int srow = 32 * (warp & 3) + r0 + r;
+            unsigned char *dst = sQ + mt * Cfg::kQTile + srow * 128;
+            // element d is at place p of its row: panel p / 64, swizzled 16-byte chunk
+            auto at = [&](int p) {
+              return dst + (p >> 6) * 16384 + (((p >> 3 & 7) ^ (srow & 7)) << 4) + (p & 7) * 2;
+            };
+            if constexpr (E == 2) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int d = lane * 2 + e;
+                *reinterpret_cast<__half *>(at((d & ~3) + Widen<CODE>::place(d & 3))) =
+                    __float2half_rn(f[e] * inv);
+              }
+            } else {
+              uint32_t h[E / 2];
+#pragma unroll
+              for (int e = 0; e < E; e += 4) {
+                float y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[Widen<CODE>::place(j)] = f[e + j] * inv;
+                h[e / 2] = half2_bits(y[0], y[1]);
+                h[e / 2 + 1] = half2_bits(y[2], y[3]);
+              }
+              if constexpr (E == 8)
+                *reinterpret_cast<uint4 *>(at(lane * 8)) = make_uint4(h[0], h[1], h[2], h[3]);
+              else
+                *reinterpret_cast<uint2 *>(at(lane * 4)) = make_uint2(h[0], h[1]);
+            }
+            if (r0 + r == lane) qa = fabsf(a.scale) * kLog2e * kv::pow2f(ex);
           }
-          if (r == lane) qa = fabsf(a.scale) * kLog2e * kv::pow2f(ex);
         }
         tc::fence_async_smem();
         __syncwarp();
