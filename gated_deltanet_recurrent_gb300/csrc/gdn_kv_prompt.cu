@@ -15,7 +15,7 @@
 //              TMEM) only when it must, which after a few tiles is rare
 //   converters CW warps: 16 codes per load, to binary16 (exact), into a ring of
 //              slots of 128 tokens x min(d, 128) in the 128-byte swizzle, K and
-//              V slots in the order of the MMAs; their loads run PF slots ahead
+//              V slots in the order of the MMAs, in two teams that take turns
 //   MMA        one thread; MT = 2: the two row tiles alternate, so one's softmax
 //              runs under the other's products; MT = 1: S is double-buffered
 //              and S of the next tile is computed under the softmax of this one
@@ -54,8 +54,11 @@ struct PromptCfg {
   static constexpr int kSlots = PAIR && D == 128 ? 6 : 4;
   static constexpr int kQTile = 128 * D * 2;
   static constexpr int kConvWarps = MT == 2 ? 4 : 8;
-  static constexpr int kConvTeams = MT == 2 ? 1 : 2;    // teams take the slots in turn
-  static constexpr int kPrefetch = 2;                   // of a team's own slots
+  // Teams take the slots in turn, each loading its next slot's codes as soon as it has
+  // converted one.  Two teams with one slot ahead: 707 us for 8 prompt pieces (d = 256) and
+  // 482 for a prompt of 8192 (d = 128); one team 888 and 500, four teams 886 and 571; with two
+  // slots ahead the codes do not fit in the registers (815, 672).
+  static constexpr int kConvTeams = 2;
   static constexpr int kThreads = 512;  // warps 12..15: MMA, pages, two idle
   // registers per thread of each role; with 512 threads a launch has 128 each, and the
   // shares' sum may not exceed that: MT = 2: 256 * 168 + 128 * 112 + 128 * 64 = 65,536;
@@ -336,7 +339,7 @@ __device__ __forceinline__ void put8(bf16 *p, const float *v) {
 template <int CODE, int D, int MT, bool PAIR>
 __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
     attend_prompt_kernel(const KVView c, const int layer, const KVAttendArgs a, const int splits,
-                         const int hinted_units, float *__restrict__ part) {
+                         const int hinted_units, const int *order, float *__restrict__ part) {
   using Cfg = PromptCfg<D, MT, PAIR>;
   constexpr int R = Cfg::kRows, NS = Cfg::kSlots, H = Cfg::kHalves, CW = Cfg::kConvWarps;
   constexpr int TEAMS = Cfg::kConvTeams;
@@ -355,11 +358,13 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
   kv::dependents_may_launch();
   kv::dependent_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // blocks are ordered by row tile, the heaviest of every sequence and head first
+  // blocks take the units of the list, or else by row tile, the heaviest of every sequence and
+  // head first
   const int block = blockIdx.x / Cfg::kCtas, rank = PAIR ? (int)cluster_rank() : 0;
-  const int heads = a.seq.n_seqs * c.h_kv, z = block % heads, split = blockIdx.y;
+  const int place0 = order ? __ldcg(order + block) : block;
+  const int heads = a.seq.n_seqs * c.h_kv, z = place0 % heads, split = blockIdx.y;
   const int i = z / c.h_kv, head = z % c.h_kv, group = c.h_q / c.h_kv;
-  const int64_t u0 = block / heads;
+  const int64_t u0 = place0 / heads;
   Unit w;
   if (!find_unit(c, a, i, head, u0, R, 0, 1, tid + split + rank + (int)u0 == 0, &w)) return;
   constexpr int kConv = 4 * MT, kMma = kConv + CW, kPages = kMma + 1;
@@ -535,8 +540,8 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
         float sum, peak;
         auto weigh = [&](auto hide) {
           uint32_t s[2][32];
+          float top[2] = {-INFINITY, -INFINITY};
           sum = 0.f;
-          peak = -INFINITY;
           tmem_ld32_async(tS, s[0]);
 #pragma unroll
           for (int h = 0; h < kBN / 32; ++h) {
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
                   if (32 * h + 16 * b + x >= open) y.x = -INFINITY;
                   if (32 * h + 16 * b + x + 1 >= open) y.y = -INFINITY;
                 }
-                peak = fmaxf(fmaxf(y.x, y.y), peak);
+                top[b] = fmaxf(fmaxf(y.x, y.y), top[b]);
                 y.x = fast_exp2(y.x);
                 y.y = fast_exp2(y.y);
                 part = add2(part, y);
@@ -564,6 +569,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
               sum = fmaf(part.x + part.y, s_un[info][2 * h + b], sum);
             }
           }
+          peak = fmaxf(top[0], top[1]);
         };
         if (masked)
           weigh(std::true_type{});
@@ -665,7 +671,6 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
       // ---- converters ----
       constexpr int kTeam = 32 * CW / TEAMS;
       constexpr int VPS = Cfg::kSlot / 32 / kTeam;  // loads (of 16 codes) per thread and slot
-      constexpr int PF = Cfg::kPrefetch;
       const int team = (warp - kConv) / (CW / TEAMS);
       const int ct = tid - 32 * (kConv + team * (CW / TEAMS));
       // Place of a thread's load v in a slot of 4 or 8 columns of 16 codes: with 4, 4 lanes to
@@ -714,7 +719,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
           *tile = *side ? (y >> 1) - 1 : (y + 1) >> 1;
         }
       };
-      uint4 code[PF][VPS];
+      uint4 code[VPS];
       auto load = [&](int x, uint4 *dst) {
         int tile, side, half;
         place(x, &tile, &side, &half);
@@ -762,44 +767,37 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
         }
         return true;
       };
-#pragma unroll
-      for (int y = 0; y < PF; ++y)
-        if (ok && team + y * TEAMS < n_slots) ok = load(team + y * TEAMS, code[y]);
-      for (int x0 = team; x0 < n_slots && ok; x0 += PF * TEAMS) {
-#pragma unroll
-        for (int y = 0; y < PF; ++y) {
-          const int x = x0 + y * TEAMS;
-          if (x >= n_slots || !ok) break;
-          const uint32_t n = slots + x;
-          if (n >= NS && !warp_wait(&slot_empty[n % NS], n / NS - 1)) {
-            ok = false;
-            break;
-          }
-          int tile, side, half;
-          place(x, &tile, &side, &half);
-          const int panel = side ? 16384 : Cfg::kKPanel;
-          unsigned char *dst = sKV + (n % NS) * Cfg::kSlot;
-#pragma unroll
-          for (int v = 0; v < VPS; ++v) {
-            int r, col;
-            in_slot(side, v, &r, &col);
-            uint32_t h[8];
-            Widen<CODE>::four(code[y][v].x, h[0], h[1]);
-            Widen<CODE>::four(code[y][v].y, h[2], h[3]);
-            Widen<CODE>::four(code[y][v].z, h[4], h[5]);
-            Widen<CODE>::four(code[y][v].w, h[6], h[7]);
-            unsigned char *q = dst + (col >> 2) * panel + r * 128;
-            const int k = 2 * (col & 3);
-            *reinterpret_cast<uint4 *>(q + ((k ^ (r & 7)) << 4)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(q + (((k + 1) ^ (r & 7)) << 4)) =
-                make_uint4(h[4], h[5], h[6], h[7]);
-          }
-          tc::fence_async_smem();
-          __syncwarp();
-          if (lane == 0) arrive_mma(&slot_full[n % NS]);
-          if (x + PF * TEAMS < n_slots) ok = load(x + PF * TEAMS, code[y]);
+      if (team < n_slots) ok = load(team, code);
+      for (int x = team; x < n_slots && ok; x += TEAMS) {
+        const uint32_t n = slots + x;
+        if (n >= NS && !warp_wait(&slot_empty[n % NS], n / NS - 1)) {
+          ok = false;
+          break;
         }
+        int tile, side, half;
+        place(x, &tile, &side, &half);
+        const int panel = side ? 16384 : Cfg::kKPanel;
+        unsigned char *dst = sKV + (n % NS) * Cfg::kSlot;
+#pragma unroll
+        for (int v = 0; v < VPS; ++v) {
+          int r, col;
+          in_slot(side, v, &r, &col);
+          uint32_t h[8];
+          Widen<CODE>::four(code[v].x, h[0], h[1]);
+          Widen<CODE>::four(code[v].y, h[2], h[3]);
+          Widen<CODE>::four(code[v].z, h[4], h[5]);
+          Widen<CODE>::four(code[v].w, h[6], h[7]);
+          unsigned char *q = dst + (col >> 2) * panel + r * 128;
+          const int k = 2 * (col & 3);
+          *reinterpret_cast<uint4 *>(q + ((k ^ (r & 7)) << 4)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4 *>(q + (((k + 1) ^ (r & 7)) << 4)) =
+              make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_mma(&slot_full[n % NS]);
+        if (x + TEAMS < n_slots) ok = load(x + TEAMS, code);
       }
     });
   } else if (warp == kMma) {
@@ -967,6 +965,49 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
   }
 }
 
+// The units by weight, the heaviest first, so that the last CTAs to end have little to do
+// (for several sequences in more than one wave: a sequence's units weigh what its context
+// does).  One CTA: a histogram over the tile counts, and a scatter; units of equal weight
+// come in any order, which no result depends on.
+constexpr int kOrderThreads = 1024;
+constexpr int kOrderMost = 65536;  // units
+
+template <int R>
+__global__ void __launch_bounds__(kOrderThreads)
+    order_units_kernel(const KVView c, const KVAttendArgs a, const int units, const int shift,
+                       int *order) {
+  __shared__ int bins[kOrderThreads], sums[32];
+  kv::dependents_may_launch();
+  kv::dependent_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int heads = a.seq.n_seqs * c.h_kv, total = units * heads;
+  // place `v`: row tile v / heads of sequence and head v % heads; bin 0 is the heaviest
+  auto bin = [&](int v) {
+    Unit w;
+    const int z = v % heads;
+    if (!find_unit(c, a, z / c.h_kv, z % c.h_kv, v / heads, R, 0, 1, false, &w))
+      return kOrderThreads - 1;
+    return max(kOrderThreads - 2 - (w.tiles >> shift), 0);
+  };
+  bins[tid] = 0;
+  __syncthreads();
+  for (int v = tid; v < total; v += kOrderThreads) atomicAdd(&bins[bin(v)], 1);
+  __syncthreads();
+  const int own = bins[tid];
+  int x = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  for (int k = 0; k < warp; ++k) x += sums[k];
+  bins[tid] = x - own;  // where the bin begins
+  __syncthreads();
+  for (int v = tid; v < total; v += kOrderThreads) order[atomicAdd(&bins[bin(v)], 1)] = v;
+}
+
 // Joins the splits of a unit: a CTA per (unit, sequence and head) and four rows.
 constexpr int kJoinRows = 4;
 
@@ -1029,25 +1070,34 @@ cudaError_t launch_prompt(const KVView &c, int layer, const KVAttendArgs &a, con
     if (splits > tiles) splits = tiles;
     if (splits > 64) splits = 64;
   }
+  const bool sort = a.seq.n_seqs > 1 && units * z > room && units * z <= kOrderMost;
   void *work = nullptr;
   bool temporary = false;
-  if (splits > 1) {
-    e = h.work->get((size_t)z * units * splits * Cfg::kPartFloats * sizeof(float), s, &work,
-                    &temporary);
+  if (splits > 1 || sort) {
+    const size_t bytes = sort ? (size_t)units * z * sizeof(int)
+                              : (size_t)z * units * splits * Cfg::kPartFloats * sizeof(float);
+    e = h.work->get(bytes, s, &work, &temporary);
     if (e != cudaSuccess) return e;
+  }
+  if (sort) {
+    int shift = 0;
+    while ((tiles >> shift) > kOrderThreads - 2) ++shift;
+    e = kv::launch(order_units_kernel<Cfg::kRows>, dim3(1), kOrderThreads, 0, s, 1, c, a,
+                   (int)units, shift, static_cast<int *>(work));
+    if (e != cudaSuccess) {
+      if (temporary) cudaFreeAsync(work, s);
+      return e;
+    }
   }
   e = kv::launch(kernel, dim3((unsigned)(units * z * Cfg::kCtas), (unsigned)splits), Cfg::kThreads,
                  Cfg::kSmem, s, Cfg::kCtas, c, layer, a, (int)splits, (int)units,
-                 static_cast<float *>(work));
-  if (splits > 1) {
-    if (e == cudaSuccess)
-      e = kv::launch(attend_prompt_join_kernel<D, Cfg::kRows>,
-                     dim3((unsigned)(units * z), Cfg::kRows / kJoinRows), kJoinRows * D / 4, 0, s,
-                     1, c, a, (int)splits, static_cast<const float *>(work));
-    const cudaError_t ef = temporary ? cudaFreeAsync(work, s) : cudaSuccess;
-    if (e == cudaSuccess) e = ef;
-  }
-  return e;
+                 sort ? static_cast<const int *>(work) : nullptr, static_cast<float *>(work));
+  if (splits > 1 && e == cudaSuccess)
+    e = kv::launch(attend_prompt_join_kernel<D, Cfg::kRows>,
+                   dim3((unsigned)(units * z), Cfg::kRows / kJoinRows), kJoinRows * D / 4, 0, s, 1,
+                   c, a, (int)splits, static_cast<const float *>(work));
+  const cudaError_t ef = temporary ? cudaFreeAsync(work, s) : cudaSuccess;
+  return e != cudaSuccess ? e : ef;
 }
 
 template <int CODE>
