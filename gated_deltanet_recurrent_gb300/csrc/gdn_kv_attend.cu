@@ -840,14 +840,19 @@ cudaError_t by_dim(const KVView &c, int layer, const KVAttendArgs &a, const KVHo
 
 cudaError_t launch_kv_attend(const KVView &c, int layer, const KVAttendArgs &a, const KVHost &h,
                              cudaStream_t s) {
-  // bf16 calls with more than 32 query rows per KV head go to the tcgen05 kernel, unless the
-  // whole call is small: its units take longer to set up, and it has fewer of them.  Sequences
-  // x KV heads x 16-row tiles x context, split / tcgen05 in us: 16 x 9 x 128 = 18 K 22 / 29,
-  // 16 x 5 x 512 = 41 K 28 / 26, 64 x 3 x 512 = 98 K 31 / 25, 16 x 5 x 8192 = 655 K 82 / 51;
-  // with 24 and 20 rows, 128 x 2 x 8192 217 / 228 and 512 x 2 x 8192 486 / 596.
+  // The tcgen05 kernel takes bf16 calls with more than 16 query rows per KV head, but not the
+  // small ones (its units take longer to set up) and, up to 32 rows, neither those with few
+  // units, which it cannot spread as well, nor those with more than a wave of them, of whose
+  // 128-row tiles it uses a quarter.  Measured, split / tcgen05 in us, as sequences x KV heads,
+  // rows, context:
+  //   2 x 136 x 512 15 / 23     8 x 36 x 2048 20 / 20      8 x 72 x 2048 30 / 27
+  //   8 x 132 x 2048 30 / 26    16 x 264 x 2048 76 / 39    64 x 68 x 8192 161 / 70
+  //   2 x 24 x 8192 22 / 29     32 x 27 x 2048 27 / 19     64 x 20 x 2048 34 / 28
+  //   128 x 24 x 8192 212 / 222   192 x 20 x 2048 67 / 77  512 x 20 x 512 56 / 73
   const int64_t rows = (int64_t)a.max_seqlen * (c.h_q / c.h_kv);
-  if (a.q_dtype == GDN_BF16 && rows > 32 &&
-      (double)a.seq.n_seqs * c.h_kv * ((rows + 15) / 16) * a.max_kv_len >= 65536.)
+  const int64_t heads = (int64_t)a.seq.n_seqs * c.h_kv;
+  if (a.q_dtype == GDN_BF16 && (rows > 32 || (rows > 16 && heads >= 16 && heads <= h.sm_count)) &&
+      (double)heads * ((rows + 15) / 16) * a.max_kv_len > 32768.)
     return launch_kv_attend_prompt(c, layer, a, h, s);
   return c.code == GDN_KV_I8 ? by_dim<GDN_KV_I8>(c, layer, a, h, s)
                              : by_dim<GDN_KV_E4M3>(c, layer, a, h, s);

@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
   Unit w;
   if (!find_unit(c, a, i, head, u0, R, 0, 1, tid + split + rank + (int)u0 == 0, &w)) return;
   constexpr int kConv = 4 * MT, kMma = kConv + CW, kPages = kMma + 1;
+  static_assert(TEAMS <= NS, "a team's wait for a free slot counts on the earlier teams' slots");
   static_assert(kMma == 12, "four warpgroups: softmax and converters, then MMA and pages");
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(&slot_full[i], CW / TEAMS * Cfg::kCtas), mbar_init(&slot_empty[i], 1);
@@ -1067,8 +1068,9 @@ cudaError_t launch_prompt(const KVView &c, int layer, const KVAttendArgs &a, con
   int64_t splits = 1;
   if (units * z < room) {
     splits = room / (units * z);
-    if (splits > tiles) splits = tiles;
+    if (splits > tiles / 3) splits = tiles / 3;
     if (splits > 64) splits = 64;
+    if (splits < 1) splits = 1;
   }
   const bool sort = a.seq.n_seqs > 1 && units * z > room && units * z <= kOrderMost;
   void *work = nullptr;
