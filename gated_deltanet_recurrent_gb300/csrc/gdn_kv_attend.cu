@@ -9,11 +9,13 @@
 // 2^(y_j - M) that multiply the codes are well scaled whatever the V scales
 // are, and can be rounded to binary16; the codes are exact in binary16.  The
 // denominator sums 2^(y_j - M) * 2^-e_j in float32.  M is raised only when some
-// y_j exceeds it by more than 8, which saves most of the reductions and
-// rescalings, and the weights are lifted by 2^7: they reach 2^15 at most, and
-// keep binary16's full precision down to 2^-21 of the weight at M.  Queries are scaled by a
-// power of two per row to lie in [1, 2) at their largest and rounded to
-// binary16 (exact for bf16), or split into two binary16 parts (float32).
+// y_j exceeds it by more than 7, which saves most of the reductions and
+// rescalings; it is a whole number, so that y_j - M, from one fused multiply-add,
+// is rounded at its own size and not at that of y_j.  The weights are lifted by
+// 2^8: the largest is between 2^7 and 2^15, and those down to 2^-21 of it keep
+// binary16's full precision.  Queries are scaled by a power of two per row to lie
+// in [1, 2) at their largest and rounded to binary16 (exact for bf16), or split
+// into two binary16 parts (float32).
 //
 // Work.  HBM-bound: each KV head's codes are read once for all its query rows.
 // A unit is 8 * NT query rows (tokens x the query heads of one KV head) of one
@@ -45,7 +47,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;      // tokens
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.f, kLift = 7.f;
+constexpr float kSlack = 7.f, kLift = 8.f;
 
 // A unit that is cut starts in CTA c and ends in CTA c + parts - 1 (parts 0: none does).
 struct CutUnit {
@@ -475,7 +477,8 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         M[x][y] = -INFINITY;
-        Ms[x][y] = L[x][y] = 0.f;
+        Ms[x][y] = -1e30f;  // any exponent is above it: the first positions raise M
+        L[x][y] = 0.f;
         qa[x][y] = sA[8 * x + 2 * t + y];
         lim[x][y] = pos0 + (row0 + min(8 * x + 2 * t + y, rows - 1)) / group;
       }
@@ -530,6 +533,8 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
       for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
 #pragma unroll
       for (int seg = 0; seg < SEGS; ++seg) {
+        // (float32 queries: the products' own sums are short, and joined by rounded additions)
+        float part_s[PARTS == 2 ? NT : 1][4] = {};
         const uint4 k0 = *reinterpret_cast<const uint4 *>(sK + chunk_at<D>(perm(g), 4 * seg + t));
         const uint4 k1 =
             *reinterpret_cast<const uint4 *>(sK + chunk_at<D>(perm(g + 8), 4 * seg + t));
@@ -547,48 +552,60 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
             for (int x = 0; x < NT; ++x) {
               const uint4 b = *reinterpret_cast<const uint4 *>(
                   sQ + (size_t)((((p * NT + x) * SEGS + seg) * 2 + j2) * 32 + lane) * 8);
-              mma16816(s[x], a0, b.x, b.y);
-              mma16816(s[x], a1, b.z, b.w);
+              float *sum = PARTS == 2 ? part_s[x] : s[x];
+              mma16816(sum, a0, b.x, b.y);
+              mma16816(sum, a1, b.z, b.w);
             }
         }
+        if constexpr (PARTS == 2)
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) s[x][y] += part_s[x][y];
       }
       // weights
       const bool masked = tok + 16 > lim_min || !valid;
+      float f[NT][2], y[NT][4];  // y: exponents of the weights
+      auto exponents = [&](int x, int k, float shift) {
+        y[x][k] = fmaf(s[x][k], f[x][k], shift);
+        y[x][2 + k] = fmaf(s[x][2 + k], f[x][k], shift);
+        if (masked) {
+          if (!valid || tok + perm(g) >= lim[x][k]) y[x][k] = -INFINITY;
+          if (!valid || tok + perm(g + 8) >= lim[x][k]) y[x][2 + k] = -INFINITY;
+        }
+      };
       bool raise = false;
-      float peak[NT][2];
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float f = qa[x][y] * k_scale;
-          s[x][y] = fmaf(s[x][y], f, e);
-          s[x][2 + y] = fmaf(s[x][2 + y], f, e);
-          if (masked) {
-            if (!valid || tok + perm(g) >= lim[x][y]) s[x][y] = -INFINITY;
-            if (!valid || tok + perm(g + 8) >= lim[x][y]) s[x][2 + y] = -INFINITY;
-          }
-          peak[x][y] = fmaxf(s[x][y], s[x][2 + y]);
-          raise |= peak[x][y] > M[x][y] + kSlack;
+        for (int k = 0; k < 2; ++k) {
+          f[x][k] = qa[x][k] * k_scale;
+          exponents(x, k, e - Ms[x][k]);
+          raise |= fmaxf(y[x][k], y[x][2 + k]) > kSlack + kLift;
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float m = peak[x][y];
+          for (int k = 0; k < 2; ++k) {
+            exponents(x, k, e);
+            float m = fmaxf(y[x][k], y[x][2 + k]);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1)
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            m = fmaxf(m, M[x][y]);
-            const float f = m == -INFINITY ? 1.f : fast_exp2(M[x][y] - m);
-            M[x][y] = m;
-            Ms[x][y] = m == -INFINITY ? 0.f : m - kLift;
-            L[x][y] *= f;
+            m = fmaxf(ceilf(m), M[x][k]);
+            if (m != -INFINITY) {
+              const float keep = fast_exp2(M[x][k] - m);
+              M[x][k] = m;
+              Ms[x][k] = m - kLift;
+              L[x][k] *= keep;
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-              o[j][x][y] *= f;
-              o[j][x][2 + y] *= f;
+              for (int j = 0; j < MT; ++j) {
+                o[j][x][k] *= keep;
+                o[j][x][2 + k] *= keep;
+              }
             }
+            exponents(x, k, e - Ms[x][k]);
           }
       }
       uint32_t pb[PARTS][NT][2];
@@ -596,16 +613,16 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
       for (int x = 0; x < NT; ++x) {
         float p[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) p[y] = fast_exp2(s[x][y] - Ms[x][y & 1]);
+        for (int k = 0; k < 4; ++k) p[k] = fast_exp2(y[x][k]);
         L[x][0] = fmaf(p[0] + p[2], unscale, L[x][0]);
         L[x][1] = fmaf(p[1] + p[3], unscale, L[x][1]);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t h = half2_bits(p[2 * y], p[2 * y + 1]);
-          pb[0][x][y] = transpose8(h);
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t h = half2_bits(p[2 * k], p[2 * k + 1]);
+          pb[0][x][k] = transpose8(h);
           if constexpr (PARTS == 2) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            pb[1][x][y] = transpose8(half2_bits(p[2 * y] - f.x, p[2 * y + 1] - f.y));
+            const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            pb[1][x][k] = transpose8(half2_bits(p[2 * k] - r.x, p[2 * k + 1] - r.y));
           }
         }
       }
@@ -630,12 +647,23 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
         const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]};
         const uint32_t a1[4] = {lo[2], lo[3], hi[2], hi[3]};
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p)
+        for (int x = 0; x < NT; ++x) {
+          if constexpr (PARTS == 1) {
+            mma16816(o[2 * j][x], a0, pb[0][x][0], pb[0][x][1]);
+            mma16816(o[2 * j + 1][x], a1, pb[0][x][0], pb[0][x][1]);
+          } else {
+            float u[4] = {}, v[4] = {};
+            mma16816(u, a0, pb[1][x][0], pb[1][x][1]);
+            mma16816(v, a1, pb[1][x][0], pb[1][x][1]);
+            mma16816(u, a0, pb[0][x][0], pb[0][x][1]);
+            mma16816(v, a1, pb[0][x][0], pb[0][x][1]);
 #pragma unroll
-          for (int x = 0; x < NT; ++x) {
-            mma16816(o[2 * j][x], a0, pb[p][x][0], pb[p][x][1]);
-            mma16816(o[2 * j + 1][x], a1, pb[p][x][0], pb[p][x][1]);
+            for (int k = 0; k < 4; ++k) {
+              o[2 * j][x][k] += u[k];
+              o[2 * j + 1][x][k] += v[k];
+            }
           }
+        }
       }
       __syncwarp();  // the stage has been read by every lane
       if (i + S < steps) fill(i + S, ids[S - 1], stage);

@@ -39,7 +39,7 @@ constexpr int kBN = 128;                 // tokens of a KV tile
 constexpr int kGroups = kBN / 16;        // page-aligned token groups of a tile
 constexpr int kInfo = 8;                 // tiles of page info in flight
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.f, kLift = 7.f;
+constexpr float kSlack = 7.f, kLift = 8.f;
 
 template <int D, int MT, bool PAIR>
 struct PromptCfg {
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
         bool seen = MT == 2 || j == 0;  // pv_done of the tile before this one: with MT = 2 its
                                         // product came before this tile's S
         if (__any_sync(0xffffffffu, peak > (M == -INFINITY ? -INFINITY : kSlack + kLift))) {
-          const float m = fmaxf(M, peak + Ms);
+          const float m = fmaxf(M, ceilf(peak + Ms));
           const float f = m == -INFINITY ? 1.f : fast_exp2(M - m);
           M = m;
           Ms = m == -INFINITY ? 0.f : m - kLift;
