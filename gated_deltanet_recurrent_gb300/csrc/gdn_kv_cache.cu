@@ -13,7 +13,11 @@
 //     counts is the chain of dependent loads (slot -> page -> scale) and the
 //     number of warps that hide it.  The rows are read twice, the second time
 //     from L1.
-// A page is written by one sequence of a call, so no two units meet.
+// A page is written by one sequence of a call, so no two units meet.  Measured,
+// append and read-back together: 8192 float32 tokens of 8 x 128 (168 MB) 42 us,
+// 4.0 TB/s; 8 pieces of up to 2048 bf16 tokens of 2 x 256 (59 MB) 20 us, of
+// which a third is the chain of loads at each kernel's start.  Below some MB a
+// call costs what its launches do.
 #include "gdn_kv.cuh"
 
 namespace gdn {

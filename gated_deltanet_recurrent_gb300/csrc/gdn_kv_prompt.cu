@@ -14,17 +14,25 @@
 //              maximum and sum, P to TMEM; raises the maximum (and rescales O in
 //              TMEM) only when it must, which after a few tiles is rare
 //   converters CW warps: 16 codes per load, to binary16 (exact), into a ring of
-//              slots of 128 tokens x min(d, 128) in the 128-byte swizzle, K and
-//              V slots in the order of the MMAs, in two teams that take turns
-//   MMA        one thread; MT = 2: the two row tiles alternate, so one's softmax
+//              slots in the 128-byte swizzle, K and V slots in the order of the
+//              MMAs, in two teams that take turns
+//   MMA        one warp, one elected lane issues; MT = 2: the two row tiles alternate, so one's softmax
 //              runs under the other's products; MT = 1: S is double-buffered
 //              and S of the next tile is computed under the softmax of this one
 //   pages      one warp: page ids and scales of the coming tiles
 //
 // What bounds it: per tile and 128 rows the tensor pipe needs d * 8 cycles (4096
-// products a cycle), shared memory d * 6 for the operands plus the converted
-// codes' writes, d * 4 / MT (128 bytes a cycle).  MT = 2 halves the conversion
-// per row; d = 256 has room in TMEM (O 256 columns, two S) for MT = 1 only.
+// products a cycle).  Shared memory (128 bytes a cycle) needs d * 6 for the
+// operands, d * 4 / MT for the converted codes' writes and d * 2 / MT for their
+// loads through L1: alone, more than the tensor pipe.  So long prompts run in
+// pairs of CTAs (cta_group::2, 256-row products): each CTA converts and holds
+// half of every K and V operand, which halves all but the queries' part (8 pieces
+// of up to 2048 tokens, 16 x 2 heads, d = 256: 1422 -> 969 us when this came).
+// MT = 2 halves the conversion per row; d = 256 has room in TMEM (O 256 columns,
+// two S) for MT = 1 only.  Measured: those pieces 631 us (1210 TFLOP/s, tensor
+// pipe 51 % active); a prompt of 8192, 32 x 8 heads, d = 128, 485 us (1135
+// TFLOP/s, 48 %).  What is left is the softmax's latency between the two
+// products of a tile (1550 of 3300 cycles), and 6 us of setup per unit.
 #include <cuda.h>
 
 #include <type_traits>
