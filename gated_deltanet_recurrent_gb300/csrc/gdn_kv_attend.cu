@@ -839,9 +839,13 @@ cudaError_t launch_split(const KVView &c, int layer, const KVAttendArgs &a, cons
   CutUnit *cut = reinterpret_cast<CutUnit *>(static_cast<char *>(work) + part_bytes);
   e = kv::launch(kernel, dim3((unsigned)grid), kThreads, Cfg::kSmem, s, 1, *h.k_map, *h.v_map, c,
                  layer, a, entry, grid == most, part, cut);
+  // (one token per slot: a unit has exactly the rows of its group)
+  const unsigned used = a.seq.cu_seqlens == nullptr && c.h_q / c.h_kv < Cfg::kRows
+                            ? (unsigned)(c.h_q / c.h_kv)
+                            : (unsigned)Cfg::kRows;
   if (e == cudaSuccess)
-    e = kv::launch(attend_join_kernel<D, NT>, dim3((unsigned)grid, Cfg::kRows), kJoinThreads, 0, s, 1,
-                   c, a, static_cast<const float *>(part), static_cast<const CutUnit *>(cut));
+    e = kv::launch(attend_join_kernel<D, NT>, dim3((unsigned)grid, used), kJoinThreads, 0, s, 1, c,
+                   a, static_cast<const float *>(part), static_cast<const CutUnit *>(cut));
   const cudaError_t ef = temporary ? cudaFreeAsync(work, s) : cudaSuccess;
   return e != cudaSuccess ? e : ef;
 }
