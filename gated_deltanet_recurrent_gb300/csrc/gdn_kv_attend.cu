@@ -828,7 +828,12 @@ cudaError_t launch_split(const KVView &c, int layer, const KVAttendArgs &a, cons
   const double tiles = (double)a.seq.n_seqs * c.h_kv * ((rows + Cfg::kRows - 1) / Cfg::kRows) *
                        (a.max_kv_len / kTile + 1);
   const int64_t most = (int64_t)h.sm_count * Cfg::kCtas;
-  const int64_t grid = tiles < (double)most ? (int64_t)tiles : most < kMaxGrid ? most : kMaxGrid;
+  // A CTA per tile where there are fewer tiles than that; two tiles where a context has more
+  // than 64, as its join would get long (1 x 2 heads, 8192 tokens: 15.1 us with one tile a CTA,
+  // 13.1 with two, 14.2 with three; 777 tokens: 9.5, 13.9, 14.6).
+  const int least = a.max_kv_len > 64 * kTile ? 2 : 1;
+  const int64_t full = most < kMaxGrid ? most : kMaxGrid;
+  const int64_t grid = tiles < (double)full * least ? ((int64_t)tiles + least - 1) / least : full;
   const int entry = tiles >= 8. * (double)most ? Cfg::kEntry : 0;
   const size_t part_bytes = (size_t)grid * 2 * Cfg::kPartFloats * sizeof(float);
   void *work = nullptr;
