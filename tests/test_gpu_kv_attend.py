@@ -344,6 +344,26 @@ def test_weights_far_below_the_largest(code, h_q, h_kv, d):
     assert (err <= lim).all(), (float((err / lim).max()), int((err > lim).sum()))
 
 
+@pytest.mark.parametrize("code", ["i8", "e4m3"])
+@pytest.mark.parametrize("h_q,h_kv,d,hint", [(16, 2, 256, 5), (16, 2, 256, 40), (32, 8, 128, 20),
+                                             (32, 8, 128, 40), (8, 2, 128, 80), (12, 4, 64, 40),
+                                             (12, 4, 64, 60)])
+def test_more_rows_than_the_hint_says(code, h_q, h_kv, d, hint):
+    """The hints choose the tensor-core kernel in each of its forms, for fewer
+    query tokens than there are: its CTAs take several units one after another."""
+    rng = np.random.default_rng(hint + d)
+    lens, kv_lens = [300, 0, 129, 1, 37], [301, 5, 700, 64, 37]
+    kv, ref = filled(rng, code, 32, h_q, h_kv, d, kv_lens)
+    q = queries(rng, sum(lens), h_q, d, "bf16")
+    slots = list(range(5))
+    want, mag = ref.attend(0, slots, kv_lens, lens, q, d ** -0.5)
+    for kv_hint in (40000, 700):
+        got = run(kv, 0, slots, kv_lens, lens, q, "bf16", "bf16", d ** -0.5, max_seqlen=hint,
+                  max_kv_len=kv_hint)
+        assert_close(got, want, mag, "bf16", "bf16", kv_hint)
+    assert abi.gdn_kv_get_error(kv) == 0
+
+
 def test_zero_tokens_and_the_same_answer_twice():
     rng = np.random.default_rng(19)
     kv, _ = filled(rng, "i8", 16, 4, 2, 64, [500, 3])
