@@ -364,6 +364,74 @@ def test_more_rows_than_the_hint_says(code, h_q, h_kv, d, hint):
     assert abi.gdn_kv_get_error(kv) == 0
 
 
+# hints that choose the tensor-core kernel whatever the call's size; a call of 200 tokens a slot
+# takes pairs of CTAs (d = 128, 256), one of 40 tokens or fewer a CTA alone
+FORMS = [(16, 2, 256, 200), (16, 2, 256, 9), (32, 8, 128, 200), (32, 8, 128, 40), (32, 8, 128, 20),
+         (12, 4, 64, 200), (12, 4, 64, 20)]
+
+
+@pytest.mark.parametrize("h_q,h_kv,d,hint", FORMS)
+def test_tensor_core_kernel_at_its_edges(h_q, h_kv, d, hint):
+    """Queries without positions, an invalid page, queries that are not finite,
+    scales of any sign, strided rows: each for the other kernel too, above."""
+    rng = np.random.default_rng(d + hint)
+    force = dict(max_seqlen=hint, max_kv_len=200000)
+    n = min(hint, 50)
+    kv, ref = filled(rng, "e4m3", 16, h_q, h_kv, d, [2, 0, 200, 333])
+    lens, kv_lens, slots = [n, n, n, n], [2, 0, 200, 333], [0, 1, 2, 3]
+    q = queries(rng, 4 * n, h_q, d, "bf16")
+    for scale in (d ** -0.5, -0.1, 0.0):
+        o = run(kv, 0, slots, kv_lens, lens, q, "bf16", "f32", scale, **force)
+        assert (host(o)[:n - 2] == 0).all() and (host(o)[n:2 * n] == 0).all()
+        for slot, lo, m in ((0, n - 2, 2), (2, 2 * n, n), (3, 3 * n, n)):
+            k, v = (ref.values(0, slot, s, 0, kv_lens[slot]) for s in "kv")
+            want, mag = attend_values(q[lo:lo + m].astype(np.float64), k, v, scale)
+            assert_close(o[lo:lo + m], want, mag, "bf16", "f32", (slot, scale))
+    assert abi.gdn_kv_get_error(kv) == 0
+    # a page in the middle that is none
+    kv.page_table[2, 4] = kv.desc.n_pages
+    k, v = (ref.values(0, 2, s, 0, 200) for s in "kv")
+    want, mag = attend_values(q[:n].astype(np.float64), k, v, 0.1, np.arange(200) // 16 == 4)
+    assert_close(run(kv, 0, [2], [200], [n], q[:n], "bf16", "f32", 0.1, **force), want, mag,
+                 "bf16", "f32")
+    assert abi.gdn_kv_get_error(kv) == abi.DEVERR_PAGE
+    # queries that are not finite, in rows of their own
+    bad = q[:n].copy()
+    bad[0, 1, 5], bad[n - 1, h_q - 1, 0] = np.nan, np.inf
+    k, v = (ref.values(0, 3, s, 0, 333) for s in "kv")
+    want, mag = attend_values(q[:n].astype(np.float64), k, v, 0.1)
+    wide = torch.zeros(n, h_q + 3, d, device="cuda", dtype=torch.bfloat16)
+    out = torch.full((n, h_q + 2, d), 7.0, device="cuda")
+    wide[:, 1:h_q + 1] = dev(bad, "bf16")
+    abi.gdn_kv_attend(kv, 0, dev_i32([3]), dev_i32([333]), wide[:, 1:h_q + 1], out[:, 2:],
+                      cu_seqlens=cum([n]), scale=0.1, **force)
+    hit = np.zeros((n, h_q), dtype=bool)
+    hit[0, 1] = hit[n - 1, h_q - 1] = True
+    got = out[:, 2:]
+    assert np.isnan(host(got)[hit]).all() and (out[:, :2] == 7).all()
+    keep = torch.from_numpy(~hit).cuda()
+    assert_close(got[keep], want[~hit], mag[~hit], "bf16", "f32")
+
+
+@pytest.mark.parametrize("hint", [9, 200])
+def test_tensor_core_kernel_offsets_past_32_bits(hint):
+    rng = np.random.default_rng(21)
+    h, d, page, n_pages, n = 4, 256, 128, 18000, 9
+    kv = abi.KVCache.empty(2, 1, n_pages, 3, page, 32, h, d, torch.int8, host_checks=False)
+    table = np.array([[n_pages - 1, n_pages - 7, 11]])
+    kv.page_table.copy_(torch.from_numpy(table.astype(np.int32)))
+    k, v = rows(rng, 300, h, d, "bf16"), rows(rng, 300, h, d, "bf16")
+    abi.gdn_kv_append(kv, 1, dev_i32([0]), dev_i32([0]), dev(k, "bf16"), dev(v, "bf16"),
+                      cu_seqlens=cum([300]))
+    from oracle.kv_oracle import KVOracle
+    ref = KVOracle(1, 3, h, page, d, "i8", np.array([[0, 1, 2]]))
+    ref.append(0, [0], [0], [300], k, v)
+    q = queries(rng, n, 32, d, "bf16")
+    want, mag = ref.attend(0, [0], [300], [n], q, 1 / 16)
+    o = run(kv, 1, [0], [300], [n], q, "bf16", "f32", 1 / 16, max_seqlen=hint, max_kv_len=200000)
+    assert_close(o, want, mag, "bf16", "f32")
+
+
 def test_zero_tokens_and_the_same_answer_twice():
     rng = np.random.default_rng(19)
     kv, _ = filled(rng, "i8", 16, 4, 2, 64, [500, 3])
