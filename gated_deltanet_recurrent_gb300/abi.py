@@ -615,7 +615,11 @@ def _kv_token_rows(shape, stride, heads, dim, name):
         raise GDNError(5, f"{name} must be [tokens, {heads}, {dim}], got {tuple(shape)}")
     if stride[2] != 1 or stride[1] != dim:
         raise GDNError(1, f"{name}: heads must be packed (strides {stride})")
-    return stride[0] if shape[0] > 1 else 0
+    if shape[0] <= 1:
+        return 0
+    if stride[0] < heads * dim:  # an expanded row (stride 0) is not the library's "packed" (0)
+        raise GDNError(1, f"{name}: token stride {stride[0]} smaller than a token")
+    return stride[0]
 
 
 def _kv_rows(kv, slot_ids, pos, k, v, cu_seqlens, max_seqlen):
