@@ -165,13 +165,24 @@ def _idx(t: Optional[torch.Tensor], name: str):
     return _ptr(t)
 
 
+def _row_stride(t: torch.Tensor, width: int, name: str) -> int:
+    """Stride of t's rows of `width` elements: that width for one row or none, whose stride says
+    nothing.  Rows that overlap are refused, as those expanded from one (stride 0, which the
+    library takes for packed)."""
+    if t.shape[0] <= 1:
+        return width
+    if t.stride(0) < width:
+        raise GDNError(1, f"{name}: row stride {t.stride(0)} smaller than a row of {width}")
+    return t.stride(0)
+
+
 def _token_rows(t: torch.Tensor, heads: int, dim: int, name: str) -> int:
     """Token stride (elements) of a [tokens, heads, dim] view whose heads are packed."""
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
         raise GDNError(5, f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
     if t.stride(2) != 1 or t.stride(1) != dim:
         raise GDNError(1, f"{name}: heads must be packed (strides {t.stride()})")
-    return t.stride(0)
+    return _row_stride(t, heads * dim, name)
 
 
 def _qkv(pool: "Pool", q, k, v, g, beta) -> gdn_qkv:
@@ -301,8 +312,9 @@ def gdn_conv_silu(pool: Pool, layer: int, slot_ids: torch.Tensor, x: torch.Tenso
         max_seqlen = x.shape[0]
     _check(load_library().gdn_conv_silu(
         pool.handle, layer, _idx(slot_ids, "slot_ids"), _idx(cu_seqlens, "cu_seqlens"), n,
-        x.shape[0], max_seqlen, _ptr(x), x.stride(0), _dt(x), _ptr(w), _ptr(bias), _ptr(y),
-        0 if y is None else y.stride(0), _idx(advance, "advance"), _stream(stream)))
+        x.shape[0], max_seqlen, _ptr(x), _row_stride(x, x.shape[1], "x"), _dt(x), _ptr(w),
+        _ptr(bias), _ptr(y), 0 if y is None else _row_stride(y, y.shape[1], "y"),
+        _idx(advance, "advance"), _stream(stream)))
     return y
 
 
@@ -335,8 +347,9 @@ def gdn_decode_step_conv(pool: Pool, layer: int, slot_ids: torch.Tensor, x: torc
     if len(dts) != 1:
         raise GDNError(4, "x, y, g and beta must share one dtype")
     _check(load_library().gdn_decode_step_conv(
-        pool.handle, layer, _idx(slot_ids, "slot_ids"), n, _ptr(x), x.stride(0), _ptr(w),
-        _ptr(bias), _ptr(y), y.stride(0), _ptr(g), _ptr(beta), dts.pop(), _ptr(o), _dt(o), scale,
+        pool.handle, layer, _idx(slot_ids, "slot_ids"), n, _ptr(x),
+        _row_stride(x, x.shape[1], "x"), _ptr(w), _ptr(bias), _ptr(y),
+        _row_stride(y, y.shape[1], "y"), _ptr(g), _ptr(beta), dts.pop(), _ptr(o), _dt(o), scale,
         _stream(stream)))
     return o
 
@@ -365,8 +378,9 @@ def gdn_in_proj(pool: Pool, x: torch.Tensor, w: torch.Tensor,
     if y.dim() != 2 or y.stride(1) != 1 or tuple(y.shape) != (x.shape[0], w.shape[0]):
         raise GDNError(1, "y must be [tokens, n_out] with a unit column stride")
     _check(load_library().gdn_in_proj(pool.handle, x.shape[0], x.shape[1], w.shape[0], _ptr(x),
-                                      x.stride(0), _ptr(w), w.stride(0), _ptr(y), y.stride(0),
-                                      _dt(y), _stream(stream)))
+                                      _row_stride(x, x.shape[1], "x"), _ptr(w),
+                                      _row_stride(w, w.shape[1], "w"), _ptr(y),
+                                      _row_stride(y, y.shape[1], "y"), _dt(y), _stream(stream)))
     return y
 
 
