@@ -125,5 +125,40 @@ __device__ __forceinline__ int scale_exponent(float s) {
   return e >= 128 ? -100 : min(max(e, -100), Code<CODE>::kMaxExp);
 }
 
+// ---- the softmax's two sums, whose terms may lie further apart than float32 reaches ----
+//
+// The numerator follows y = x + e (score plus V exponent), the denominator sums 2^(x - M) beside
+// it.  Terms of y far below M vanish from the numerator rightly, but a page of small (or all-zero)
+// values can have the scores that matter.  So
+//   - where a page's exponent is more than kFar below the largest so far, its terms of the
+//     denominator come from x - M itself: 2^(y - M) could vanish before 2^-e brings it back;
+//   - M is also raised for x + kLowExp, so that no 2^(x - M) is above 2^(15 - kLowExp) and the
+//     sum of a whole context stays finite.  The numerator's weights of pages below kLowExp are then
+//     up to 2^16 smaller than they could be;
+//   - what is carried over to a larger M is scaled in two steps.
+constexpr int kLowExp = -84;
+constexpr int kFar = 90;
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// a * 2^n, n from 127 down to -252 (or -inf): 2^n alone is zero below -126
+__device__ __forceinline__ float lower(float a, float n) {
+  return a * fast_exp2(fmaxf(n, -126.f)) * fast_exp2(fminf(n + 126.f, 0.f));
+}
+
+// A part's sum of the denominator (reference m) under the reference `top` of all parts.  (A part
+// without a reference has no weights, or, of a query that is not finite, NaN.)
+__device__ __forceinline__ float join_sum(float l, float m, float top) {
+  return m == -INFINITY ? l : lower(l, m - top);
+}
+// The factor of its numerator.
+__device__ __forceinline__ float join_factor(float l, float m, float top) {
+  return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : fast_exp2(m - top);
+}
+
 }  // namespace kv
 }  // namespace gdn

@@ -8,7 +8,8 @@
 // for any M.  M follows the running maximum of y_j = x_j + e_j, so the weights
 // 2^(y_j - M) that multiply the codes are well scaled whatever the V scales
 // are, and can be rounded to binary16; the codes are exact in binary16.  The
-// denominator sums 2^(y_j - M) * 2^-e_j in float32.  M is raised only when some
+// denominator sums 2^(y_j - M) * 2^-e_j in float32 (pages whose e lies far from
+// the others' are treated apart, see gdn_kv.cuh).  M is raised only when some
 // y_j exceeds it by more than 7, which saves most of the reductions and
 // rescalings; it is a whole number, so that y_j - M, from one fused multiply-add,
 // is rounded at its own size and not at that of y_j.  The weights are lifted by
@@ -55,6 +56,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;      // tokens
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 7.f, kLift = 8.f;
+constexpr int kHigh = 50;  // V exponents of ordinary pages: from kHigh - kFar up to this
 
 // A unit that is cut starts in CTA c and ends in CTA c + parts - 1 (parts 0: none does).
 struct CutUnit {
@@ -163,11 +165,7 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+using kv::fast_exp2;
 
 // 16 rows of 128 (d = 64: 64) bytes: bytes x.. of rows `row`.. of block `blk`
 __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *m, int x, int row, int blk,
@@ -457,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
       for (int y = 0; y < NT; ++y)
 #pragma unroll
         for (int z = 0; z < 4; ++z) o[x][y][z] = 0.f;
+    uint32_t odd_low = (uint32_t)(127 + kHigh - kv::kFar) << 23;
     // scales of the next step, loaded a step ahead
     float next_k = 0.f, next_v = 0.f;
     auto scales = [&](int blk) {
@@ -473,7 +472,10 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
       // the V scale is 2^e: e, and 2^-e (a block that only stands in for a bad page: 1)
       const uint32_t v_bits = valid ? __float_as_uint(next_v) & 0x7f800000u : 0x3f800000u;
       const float e = (float)((int)(v_bits >> 23) - 127);
-      const float unscale = __uint_as_float(0x7f000000u - v_bits);
+      // Exponents that lie far from the others' (see gdn_kv.cuh): none do while all are from
+      // kHigh - kFar to kHigh; a larger one moves the lower end.  Their terms of L are added apart.
+      const bool odd = v_bits < odd_low || v_bits > (uint32_t)(127 + kHigh) << 23;
+      float unscale = __uint_as_float(0x7f000000u - v_bits);
 #pragma unroll
       for (int x = 0; x + 1 < S; ++x) ids[x] = ids[x + 1];
       ids[S - 1] = ahead;
@@ -543,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
           if (!valid || tok + perm(g + 8) >= lim[x][k]) y[x][2 + k] = -INFINITY;
         }
       };
-      bool raise = false;
+      bool raise = odd;
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -558,16 +560,16 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             exponents(x, k, e);
-            float m = fmaxf(y[x][k], y[x][2 + k]);
+            float m = fmaxf(y[x][k], y[x][2 + k]) + fmaxf(kv::kLowExp - e, 0.f);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1)
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
             m = fmaxf(ceilf(m), M[x][k]);
             if (m != -INFINITY) {
               const float keep = fast_exp2(M[x][k] - m);
+              L[x][k] = kv::lower(L[x][k], M[x][k] - m);
               M[x][k] = m;
               Ms[x][k] = m - kLift;
-              L[x][k] *= keep;
 #pragma unroll
               for (int j = 0; j < MT; ++j) {
                 o[j][x][k] *= keep;
@@ -575,7 +577,16 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
               }
             }
             exponents(x, k, e - Ms[x][k]);
+            if (odd) {
+#pragma unroll
+              for (int z = k; z < 4; z += 2)
+                if (y[x][z] != -INFINITY)
+                  L[x][k] += kv::lower(1.f, fmaf(s[x][z], f[x][k], -Ms[x][k]));
+            }
           }
+        if (odd) unscale = 0.f;
+        constexpr uint32_t kSpan = (uint32_t)kv::kFar << 23;
+        odd_low = max(odd_low, max(v_bits, kSpan) - kSpan);
       }
       uint32_t pb[PARTS][NT][2];
 #pragma unroll
@@ -673,9 +684,8 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
-        const float f = sM[k][r] == -INFINITY ? (sL[k][r] == 0.f ? 0.f : 1.f)
-                                              : fast_exp2(sM[k][r] - m);
-        l += f * sL[k][r];
+        const float f = kv::join_factor(sL[k][r], sM[k][r], m);
+        l += kv::join_sum(sL[k][r], sM[k][r], m);
         sum = axpby4(1.f, sum, f,
                      *reinterpret_cast<const float4 *>(sO + (size_t)(k * R + r) * Cfg::kOutStride +
                                                        d));
@@ -751,9 +761,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int p = tid; p < u.parts; p += kJoinThreads) {
     const float pm = s_f[p];
     const float pl = u.parts <= kJoinThreads ? own_l : __ldcg(at(p) + R * D + R + r);
-    const float f = pm == -INFINITY ? (pl == 0.f ? 0.f : 1.f) : fast_exp2(pm - m);
-    s_f[p] = f;
-    l += f * pl;
+    s_f[p] = kv::join_factor(pl, pm, m);
+    l += kv::join_sum(pl, pm, m);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);

@@ -182,11 +182,7 @@ __device__ __forceinline__ uint64_t desc(uint32_t low) {
   return (uint64_t)kDescHigh << 32 | low;
 }
 
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+using kv::fast_exp2;
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -344,6 +340,32 @@ __device__ __forceinline__ void put8(bf16 *p, const float *v) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A row's part of a tile with V exponents far from the others (see gdn_kv.cuh): the sum of its
+// weights, in units of the denominator, from x - M itself; and the largest exponent, with no V
+// exponent below kLowExp.  A function of its own, and reached from where the maximum is raised: 8
+// prompt pieces (d = 256) take 612 us, a prompt of 8192 (d = 128) 490; inlined there 640 and 481,
+// before the common pass over S 652 and 528.
+__device__ __noinline__ float2 weigh_apart(uint32_t tS, int open, float qa, float Ms,
+                                           const float *ks, const float *ve) {
+  float sum = 0.f, peak = -INFINITY;
+#pragma unroll 1
+  for (int h = 0; h < kBN; h += 32) {
+    uint32_t v[32];
+    tmem_ld32_async(tS + h, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int x = 0; x < 32; ++x) {
+      const float e = ve[(h + x) / 16];
+      if (h + x < open && e != -INFINITY) {
+        const float z = fmaf(__uint_as_float(v[x]), qa * ks[(h + x) / 16], -Ms);
+        sum += kv::lower(1.f, z);
+        peak = fmaxf(peak, z + fmaxf(e, (float)kv::kLowExp));
+      }
+    }
+  }
+  return make_float2(sum, peak);
+}
+
 template <int CODE, int D, int MT, bool PAIR>
 __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
     attend_prompt_kernel(const KVView c, const int layer, const KVAttendArgs a, const int splits,
@@ -358,7 +380,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
   unsigned char *sKV = smem + MT * Cfg::kQTile;         // [NS] slots, 128-byte rows of 64 d
   __shared__ __align__(8) uint64_t slot_full[NS], slot_empty[NS], info_full[kInfo],
       info_empty[kInfo], s_full[2], p_full[MT], pv_done[MT], q_full, drain;
-  __shared__ int s_blk[kInfo][kGroups], s_plain[kInfo];
+  __shared__ int s_blk[kInfo][kGroups], s_plain[kInfo], s_odd[kInfo];
   __shared__ float s_ks[kInfo][kGroups], s_ve[kInfo][kGroups], s_un[kInfo][kGroups];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
@@ -534,8 +556,12 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
         const uint32_t n = done + j, buf = MT == 2 ? mt : n & 1;
         const uint32_t tS = tmem + lanes + buf * kBN;
         const int info = n % kInfo;
-        if (!warp_wait(&info_full[info], n / kInfo) ||
-            !warp_wait(&s_full[buf], MT == 2 ? n : n >> 1)) {
+        if (!warp_wait(&info_full[info], n / kInfo)) {
+          ok = false;
+          break;
+        }
+        const bool odd = s_odd[info] != 0;  // some V exponents far from the others
+        if (!warp_wait(&s_full[buf], MT == 2 ? n : n >> 1)) {
           ok = false;
           break;
         }
@@ -580,18 +606,31 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
           }
           peak = fmaxf(top[0], top[1]);
         };
-        if (masked)
-          weigh(std::true_type{});
-        else
-          weigh(std::false_type{});
         bool seen = MT == 2 || j == 0;  // pv_done of the tile before this one: with MT = 2 its
                                         // product came before this tile's S
-        if (__any_sync(0xffffffffu, peak > (M == -INFINITY ? -INFINITY : kSlack + kLift))) {
+        float apart = 0.f;
+        bool todo = odd;
+        for (int raises = 0;;) {  // again after the reference was raised (once, or twice if odd)
+          if (masked)
+            weigh(std::true_type{});
+          else
+            weigh(std::false_type{});
+          const float limit = M == -INFINITY ? -INFINITY : kSlack + kLift;
+          bool raise = __any_sync(0xffffffffu, peak > limit) && raises < (odd ? 2 : 1);
+          if (!raise && !todo) break;
+          if (odd) {
+            const float2 x = weigh_apart(tS, open, qa, Ms, s_ks[info], s_ve[info]);
+            apart = x.x;
+            peak = fmaxf(peak, x.y);
+            todo = raise = __any_sync(0xffffffffu, peak > limit) && raises < 2;
+            if (!raise) continue;  // (for the weights, which are not kept over this)
+          }
+          ++raises;
           const float m = fmaxf(M, ceilf(peak + Ms));
           const float f = m == -INFINITY ? 1.f : fast_exp2(M - m);
+          if (m != -INFINITY) L = kv::lower(L, M - m);
           M = m;
           Ms = m == -INFINITY ? 0.f : m - kLift;
-          L *= f;
           if (j > 0) {  // O holds the tiles before this one
             if (!seen && !warp_wait(&pv_done[mt], n - 1)) {
               ok = false;
@@ -610,14 +649,11 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
               tmem_st16(tO + x + 16, o + 16);
             }
           }
-          if (masked)
-            weigh(std::true_type{});
-          else
-            weigh(std::false_type{});
         }
-        L += sum;
+        if (!ok) break;
 #pragma unroll
         for (int x = 0; x < kBN / 2; x += 16) tmem_st16(tS + x, p + x);
+        L += odd ? apart : sum;
         tc::tmem_st_wait();
         tc::fence_before_sync();
         if (!seen && !warp_wait(&pv_done[mt], n - 1)) {
@@ -923,23 +959,27 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
     each_unit([&](const int64_t, const int T) {
       // ---- page ids and scales, four tiles at a time ----
       const int32_t *table = c.table + (int64_t)w.slot * c.max_pages;
+      int e_max = kv::kLowExp;  // largest V exponent of the unit's tiles so far
       for (int j0 = 0; j0 < T && ok; j0 += 4) {
         const int j = j0 + (lane >> 3), gr = lane & 7;
         const int tok = (w.begin + j) * kBN + 16 * gr;
         int blk = -1;
         float ks = 0.f, ve = -INFINITY, un = 0.f;
+        int e = e_max;
         if (j < T && tok < w.kv_len) {
           const int id = table[tok >> c.page_log2];
           if (id >= 0 && id < c.n_pages) {
             blk = (int)c.block(layer, id, head);
             ks = c.k_scale[blk];
-            const int e = kv::scale_exponent<CODE>(c.v_scale[blk]);
+            e = kv::scale_exponent<CODE>(c.v_scale[blk]);
             ve = (float)e;
             un = kv::pow2f(-e);
           } else {
             raise_error(c.err, GDN_DEVERR_PAGE);
           }
         }
+        e_max = __reduce_max_sync(0xffffffffu, max(e, e_max));
+        const bool odd_group = blk >= 0 && e < max(kv::kLowExp, e_max - kv::kFar);
         for (int x = 0; x < 4 && j0 + x < T && ok; ++x) {
           const uint32_t n = done + j0 + x;
           const int info = n % kInfo;
@@ -947,8 +987,10 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
           if (!ok) break;
           const bool plain =
               __all_sync(0xffffffffu, (lane >> 3) != x || (blk >= 0 && tok + 16 <= w.kv_len));
+          const bool odd = __any_sync(0xffffffffu, (lane >> 3) == x && odd_group);
           if ((lane >> 3) == x) {
             s_plain[info] = plain;
+            s_odd[info] = odd;
             s_blk[info][gr] = blk;
             s_ks[info][gr] = ks;
             s_ve[info][gr] = ve;
@@ -1042,8 +1084,8 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
   for (int s = 0; s < splits; ++s) {
     const float *p = base + (int64_t)s * kPartFloats;
     const float pm = __ldcg(p + R * D + row), pl = __ldcg(p + R * D + R + row);
-    const float f = pm == -INFINITY ? (pl == 0.f ? 0.f : 1.f) : fast_exp2(pm - m);
-    l += f * pl;
+    const float f = kv::join_factor(pl, pm, m);
+    l += kv::join_sum(pl, pm, m);
     sum = axpby4(1.f, sum, f, __ldcg(reinterpret_cast<const float4 *>(p + (int64_t)row * D + d)));
   }
   const int group = c.h_q / c.h_kv, grow = w.row0 + row;

@@ -508,8 +508,10 @@ gdn_status gdn_kv_read(gdn_kv *kv, int32_t layer, const int32_t *slot_ids, const
  * the products run on the tensor cores on the codes (exact in binary16) and
  * on queries and weights rounded to binary16 (bf16 q: the query exactly, up
  * to 2^-25 of its row's largest element; the weight to 2^-11, or to 2^-32 of
- * the row's largest weight x V scale where that is more), or split into two
- * binary16 parts each (float32 q: to 2^-22, with the same smallest step).
+ * the row's largest weight x V scale where that is more, a scale counting as at
+ * least 2^-84), or split into two binary16 parts each (float32 q: to 2^-22, with
+ * the same smallest step).  The sum that normalises the weights takes them
+ * unrounded and holds for V scales of any spread.
  * max_seqlen, max_kv_len: upper bounds of the query and cache lengths, used
  * only to choose the kernel and size its grid (any value >= 1 is correct). */
 gdn_status gdn_kv_attend(gdn_kv *kv, int32_t layer, const int32_t *slot_ids,
