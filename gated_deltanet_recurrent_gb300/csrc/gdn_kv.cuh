@@ -125,6 +125,13 @@ __device__ __forceinline__ int scale_exponent(float s) {
   return e >= 128 ? -100 : min(max(e, -100), Code<CODE>::kMaxExp);
 }
 
+// The exponent that a query row is scaled down by, from that of its largest magnitude (128: not
+// finite).  Not all of it beyond 116: the row's factor scale * log2(e) * 2^ex has to be finite, and
+// binary16 holds the rest.
+__device__ __forceinline__ int query_exponent(int ex, bool zero) {
+  return ex > 127 || zero ? 0 : min(max(ex, -126), 116);
+}
+
 // ---- the softmax's two sums, whose terms may lie further apart than float32 reaches ----
 //
 // The numerator follows y = x + e (score plus V exponent), the denominator sums 2^(x - M) beside

@@ -15,8 +15,8 @@
 // is rounded at its own size and not at that of y_j.  The weights are lifted by
 // 2^8: the largest is between 2^7 and 2^15, and those down to 2^-21 of it keep
 // binary16's full precision.  Queries are scaled by a power of two per row to lie
-// in [1, 2) at their largest and rounded to binary16 (exact for bf16), or split
-// into two binary16 parts (float32).
+// in [1, 2) at their largest (rows from 2^117 on: up to 2^12) and rounded to binary16
+// (exact for bf16), or split into two binary16 parts (float32).
 //
 // Work.  HBM-bound: each KV head's codes are read once for all its query rows.
 // A unit is 8 * NT query rows (tokens x the query heads of one KV head) of one
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
     for (int i = 0; i < S; ++i)
       if (i < steps) fill(i, ids[i], at_stage + i < S ? at_stage + i : at_stage + i - S);
 
-    // ---- queries: scaled to [1, 2) by a power of two, binary16, in the B layout ----
+    // ---- queries: scaled by a power of two, binary16, in the B layout ----
     constexpr int E = D / 32;
     for (int r = warp; r < R; r += kWarps) {
       const int row = row0 + min(r, rows - 1);  // rows past the end repeat the last, unused
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       int ex = (int)(__float_as_uint(m) >> 23) - 127;
-      ex = ex > 126 || m == 0.f ? 0 : max(ex, -126);
+      ex = kv::query_exponent(ex, m == 0.f);
       const float inv = a.scale < 0.f ? -kv::pow2f(-ex) : kv::pow2f(-ex);
 #pragma unroll
       for (int e = 0; e < E; ++e) {

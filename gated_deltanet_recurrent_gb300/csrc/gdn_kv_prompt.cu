@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
             }
             m = __reduce_max_sync(0xffffffffu, m);
             int ex = (int)(m >> 23) - 127;
-            ex = ex > 126 || m == 0 ? 0 : max(ex, -126);
+            ex = kv::query_exponent(ex, m == 0);
             const float inv = a.scale < 0.f ? -kv::pow2f(-ex) : kv::pow2f(-ex);
             const int srow = 32 * (warp & 3) + r0 + r;
             unsigned char *dst = sQ + mt * Cfg::kQTile + srow * 128;

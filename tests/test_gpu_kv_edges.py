@@ -1,5 +1,5 @@
-"""gdn_kv_attend at the edges of its range: value scales far apart.
-Tolerances are those of test_gpu_kv_attend.py."""
+"""gdn_kv_attend at the edges of its range: value scales far apart, queries of
+the largest magnitudes.  Tolerances are those of test_gpu_kv_attend.py."""
 import numpy as np
 import pytest
 import torch
@@ -129,3 +129,23 @@ def test_many_value_tokens_of_zero(code, tensor_core):
               max_seqlen=n, max_kv_len=length)
     for i in (0, 1, n_seqs // 2, n_seqs - 1):
         assert_close(got[i * n:(i + 1) * n], want, mag, "bf16", "f32", i)
+
+
+@pytest.mark.parametrize("shape,q_dtype,tensor_core", SIDES)
+def test_queries_of_the_largest_magnitudes(shape, q_dtype, tensor_core):
+    """Finite queries up to the largest float, whose scores are ordinary."""
+    h_q, h_kv, d, n = shape
+    rng = np.random.default_rng(d + 3)
+    kv, ref = make("i8", 16, h_kv, d, 1, 8, h_q=h_q)
+    k = synth.cast(rows(rng, 100, h_kv, d, "bf16", 0) * np.float32(2.0 ** -90), "bf16")
+    v = rows(rng, 100, h_kv, d, "bf16", 0)
+    append(kv, ref, 0, [0], [0], [100], k, v, "bf16")
+    for e in (115, 125, 126, 127):
+        q = rng.uniform(-1.98, 1.98, (n, h_q, d)) * 2.0 ** e
+        q[:, :, 0] = 1.98 * 2.0 ** e
+        q = synth.cast(q, q_dtype)
+        assert np.isfinite(q).all()
+        scale = 2.0 ** (90 - e) / d ** 0.5
+        want, mag = ref.attend(0, [0], [100], [n], q, scale)
+        got = call(kv, [0], [100], [n], q, q_dtype, scale, tensor_core)
+        assert_close(got, want, mag, q_dtype, "f32", e)
