@@ -23,6 +23,7 @@ DEVERR_SLOT, DEVERR_SEQ, DEVERR_COUNT, DEVERR_TIMEOUT = 1, 2, 4, 8
 DEVERR_PAGE, DEVERR_VALUE = 16, 32
 GDN_KV_I8, GDN_KV_E4M3 = 0, 1
 TEST_DECODE_WAIT_TIMEOUT = 1
+TEST_KV_WAIT_TIMEOUT = 1
 
 EXPORTED = ("gdn_pool_state_bytes", "gdn_pool_conv_bytes", "gdn_pool_create", "gdn_pool_reset",
             "gdn_pool_copy",
@@ -33,7 +34,8 @@ EXPORTED = ("gdn_pool_state_bytes", "gdn_pool_conv_bytes", "gdn_pool_create", "g
             "gdn_prefill_chunked", "gdn_prefill_recurrent", "gdn_spec_verify",
             "gdn_spec_verify_deferred", "gdn_prefill_chunked_noalloc", "gdn_prefill_chunked_ckpt",
             "gdn_kv_code_bytes", "gdn_kv_scale_bytes", "gdn_kv_create", "gdn_kv_destroy",
-            "gdn_kv_get_error", "gdn_kv_append", "gdn_kv_read", "gdn_kv_attend",
+            "gdn_kv_get_error", "gdn_kv_set_test_flags", "gdn_kv_append", "gdn_kv_read",
+            "gdn_kv_attend",
             "gdn_status_string",
             "gdn_last_error_message")
 
@@ -118,6 +120,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                vp, P(vp)]),
         "gdn_kv_destroy": (st, [vp]),
         "gdn_kv_get_error": (st, [vp, P(ctypes.c_uint32)]),
+        "gdn_kv_set_test_flags": (st, [vp, ctypes.c_uint32]),
         "gdn_kv_append": (st, [vp, i32, vp, vp, vp, i32, i32, i32, vp, i64, vp, i64, st, vp]),
         "gdn_kv_read": (st, [vp, i32, vp, vp, vp, i32, i32, i32, vp, i64, vp, i64, st, vp]),
         "gdn_kv_attend": (st, [vp, i32, vp, vp, vp, i32, i32, i32, i32, vp, i64, st, vp, i64, st,
@@ -581,6 +584,11 @@ def gdn_kv_get_error(kv: KVCache) -> int:
     err = ctypes.c_uint32(0)
     _check(load_library().gdn_kv_get_error(kv.handle, ctypes.byref(err)))
     return err.value
+
+
+def gdn_kv_set_test_flags(kv: KVCache, flags: int):
+    """Test hook of the C ABI (see gdn.h); 0 restores normal operation."""
+    _check(load_library().gdn_kv_set_test_flags(kv.handle, flags))
 
 
 # A decode step's calls are a few microseconds long: the checks below read each

@@ -191,6 +191,7 @@ struct KVView {
   unsigned int *err;
   int n_layers, n_slots, n_pages, max_pages, page_tokens, page_log2, h_q, h_kv, d;
   gdn_kv_code code;
+  uint32_t test_flags;         // GDN_TEST_KV_* bits (gdn_kv_set_test_flags); 0 in normal use
   GDN_HD int64_t capacity() const { return (int64_t)max_pages * page_tokens; }
   // index of the scale of (layer, page, head); times page_tokens * d: of its first code
   GDN_HD int64_t block(int layer, int page, int head) const {

@@ -157,6 +157,9 @@ __device__ __forceinline__ float lower(float a, float n) {
   return a * fast_exp2(fmaxf(n, -126.f)) * fast_exp2(fminf(n + 126.f, 0.f));
 }
 
+// The reference of a part that was not computed (those that were have a number or -inf).
+__device__ __forceinline__ float no_result() { return __int_as_float(0x7fffffff); }
+
 // A part's sum of the denominator (reference m) under the reference `top` of all parts.  (A part
 // without a reference has no weights, or, of a query that is not finite, NaN.)
 __device__ __forceinline__ float join_sum(float l, float m, float top) {

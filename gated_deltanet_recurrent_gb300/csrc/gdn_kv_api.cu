@@ -333,7 +333,7 @@ gdn_status gdn_kv_create(const gdn_kv_desc *desc, void *k_codes, void *v_codes,
   c->view = gdn::KVView{static_cast<uint8_t *>(k_codes), static_cast<uint8_t *>(v_codes), k_scale,
                         v_scale, page_table, err, desc->n_layers, desc->n_slots, desc->n_pages,
                         desc->max_pages, desc->page_tokens, log2, desc->h_q, desc->h_kv, desc->d,
-                        desc->code};
+                        desc->code, 0};
   *out = c;
   return ok();
 }
@@ -363,6 +363,14 @@ gdn_status gdn_kv_get_error(gdn_kv *c, uint32_t *dev_err) {
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
   *dev_err = h;
+  return ok();
+}
+
+gdn_status gdn_kv_set_test_flags(gdn_kv *c, uint32_t flags) {
+  if (!c) return fail(GDN_ERR_ARG, "kv is NULL");
+  if (flags & ~(uint32_t)GDN_TEST_KV_WAIT_TIMEOUT)
+    return fail(GDN_ERR_ARG, "unknown test flags 0x%x", flags);
+  c->view.test_flags = flags;
   return ok();
 }
 

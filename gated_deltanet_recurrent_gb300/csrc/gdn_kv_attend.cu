@@ -304,6 +304,9 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
   if (lane == 0) {
     for (int i = 0; i < S; ++i) mbar_init(&full[i], 1);
     mbar_fence_init();
+    // (test hook: the first copy's barrier waits for 16 bytes that no one sends)
+    if ((c.test_flags & GDN_TEST_KV_WAIT_TIMEOUT) && warp == 0 && (cta & 1))
+      mbar_expect_tx(&full[0], 16);
   }
 
   // ---- this CTA's piece of the line of tiles ----
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
   int at_stage = 0;      // the ring's next stage, and the phase of its barrier
   uint32_t phase = 0;
   bool ok = true;
-  for (int64_t at = begin; at < end;) {
+  for (int64_t at = begin; at < end && ok;) {
     if (unit == c.h_kv * w.row_tiles) {  // the next sequence that has work
       do {
         if (++seq >= n) return;
@@ -650,7 +653,6 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
     }
     // the rings are free after this: the sums take their place
     ok = __syncthreads_and(ok);
-    if (!ok) return;
 
     // ---- join the warps ----
 #pragma unroll
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
         for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
         const int r = 8 * x + 2 * t + y;
         if (g == 0) {
-          sM[warp][r] = M[x][y];
+          sM[warp][r] = ok ? M[x][y] : kv::no_result();  // (of every warp: the join finds it)
           sL[warp][r] = l;
         }
 #pragma unroll
@@ -691,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, sizeof(TQ) == 4 ? 2 
                                                        d));
       }
       if (whole) {
-        put_out(c, a, w.tok0, head, row0 + r, d, sum, l);
+        if (ok) put_out(c, a, w.tok0, head, row0 + r, d, sum, l);
       } else {
         *reinterpret_cast<float4 *>(my_part + r * D + d) = sum;
         if (d == 0) {
@@ -745,18 +747,24 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int x = 0; x < FIRST; ++x)
     if (share + x * ACROSS < u.parts) first[x] = out(share + x * ACROSS);
   float m = -INFINITY, own_m = -INFINITY, own_l = 0.f;
+  bool missing = false;
   for (int p = tid; p < u.parts; p += kJoinThreads) {
     own_m = __ldcg(at(p) + R * D + r);
     own_l = __ldcg(at(p) + R * D + R + r);
     s_f[p] = own_m;
+    missing |= own_m != own_m;
     m = fmaxf(m, own_m);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) s_red[0][warp] = m;
+  missing = __any_sync(0xffffffffu, missing);
+  if (lane == 0) s_red[0][warp] = missing ? kv::no_result() : m;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kJoinThreads / 32; ++k) m = fmaxf(m, s_red[0][k]);
+  for (int k = 0; k < kJoinThreads / 32; ++k) {
+    missing |= s_red[0][k] != s_red[0][k];
+    m = fmaxf(m, s_red[0][k]);
+  }
   float l = 0.f;
   for (int p = tid; p < u.parts; p += kJoinThreads) {
     const float pm = s_f[p];
@@ -777,7 +785,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     sum = axpby4(1.f, sum, s_f[p], out(p));
   s_sum[tid] = sum;
   __syncthreads();
-  if (share == 0) {
+  if (share == 0 && !missing) {  // (where some part gave up the row stays as it was)
 #pragma unroll
     for (int k = 1; k < ACROSS; ++k) sum = axpby4(1.f, sum, 1.f, s_sum[k * COLS + col]);
     l = 0.f;

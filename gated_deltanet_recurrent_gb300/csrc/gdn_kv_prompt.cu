@@ -401,7 +401,12 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
   static_assert(TEAMS <= NS, "a team's wait for a free slot counts on the earlier teams' slots");
   static_assert(kMma == 12, "four warpgroups: softmax and converters, then MMA and pages");
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&slot_full[i], CW / TEAMS * Cfg::kCtas), mbar_init(&slot_empty[i], 1);
+    // (test hook: the first slot waits for an arrival that never comes)
+    const int extra =
+        (c.test_flags & GDN_TEST_KV_WAIT_TIMEOUT) && ((block + blockIdx.y) & 1) ? 1 : 0;
+    for (int i = 0; i < NS; ++i)
+      mbar_init(&slot_full[i], CW / TEAMS * Cfg::kCtas + (i == 0 ? extra : 0)),
+          mbar_init(&slot_empty[i], 1);
     for (int i = 0; i < kInfo; ++i)
       mbar_init(&info_full[i], 1),
           mbar_init(&info_empty[i], 2 * H * (CW / TEAMS) + 4 * MT);  // its slots' loads, softmax
@@ -668,15 +673,16 @@ __global__ void __launch_bounds__(PromptCfg<D, MT, PAIR>::kThreads, 1)
       }
       // ---- outputs ----
       if (ok && T > 0 && !warp_wait(&pv_done[mt], done + T - 1)) ok = false;
-      if (ok) {
+      const bool live = row < w.rows;
+      const bool whole = splits == 1 || u >= hinted_units;
+      float *mine = whole ? part : part + ((int64_t)block * splits + split) * Cfg::kPartFloats;
+      if (!ok) {  // the join finds this and writes nothing
+        if (!whole && live) mine[R * D + row] = kv::no_result();
+      } else {
         tc::fence_after_sync();
-        const bool live = row < w.rows;
-        const bool whole = splits == 1 || u >= hinted_units;
         const int64_t at = (int64_t)(w.tok0 + grow / group) * a.ld_o +
                            (int64_t)(head * group + grow % group) * D;
-        float *mine = part;
         if (!whole) {
-          mine += ((int64_t)block * splits + split) * Cfg::kPartFloats;
           if (live) {
             mine[R * D + row] = M;
             mine[R * D + R + row] = L;
@@ -1077,8 +1083,13 @@ __global__ void __launch_bounds__(kJoinRows * D / 4)
   if (row >= w.rows) return;
   const float *base = part + (int64_t)blockIdx.x * splits * kPartFloats;
   float m = -INFINITY, l = 0.f;
-  for (int s = 0; s < splits; ++s)
-    m = fmaxf(m, __ldcg(base + (int64_t)s * kPartFloats + R * D + row));
+  bool missing = false;
+  for (int s = 0; s < splits; ++s) {
+    const float pm = __ldcg(base + (int64_t)s * kPartFloats + R * D + row);
+    missing |= pm != pm;
+    m = fmaxf(m, pm);
+  }
+  if (missing) return;  // some part gave up: the row stays as it was
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = 0; s < splits; ++s) {

@@ -467,6 +467,14 @@ gdn_status gdn_kv_destroy(gdn_kv *kv);
 /* As gdn_pool_get_error: waits for the device, returns and clears the word. */
 gdn_status gdn_kv_get_error(gdn_kv *kv, uint32_t *dev_err);
 
+/* Test hook (0 in normal use; other bits are GDN_ERR_ARG).  With
+ * GDN_TEST_KV_WAIT_TIMEOUT set, every other CTA of gdn_kv_attend's kernels has a
+ * barrier that waits for more than it gets: its bounded wait runs out (a second or
+ * two), it sets GDN_DEVERR_TIMEOUT and exits with no copy or product in flight,
+ * and the query rows that it had a part in keep what o held. */
+#define GDN_TEST_KV_WAIT_TIMEOUT 1u
+gdn_status gdn_kv_set_test_flags(gdn_kv *kv, uint32_t flags);
+
 /* Quantise new tokens into the cache.  Sequence i is tokens cu_seqlens[i] ..
  * cu_seqlens[i+1]-1 of k and v (cu_seqlens == NULL: one token each) and goes
  * to positions pos[i], pos[i] + 1, ... of slot slot_ids[i].  A page entered

@@ -55,3 +55,10 @@ def test_the_stride_of_a_single_row_says_nothing():
     assert abi._kv_token_rows(row.shape, (0, 64, 1), 2, 64, "k") == 0
     assert abi._kv_token_rows((0, 2, 64), (128, 64, 1), 2, 64, "k") == 0
     assert abi._kv_token_rows((3, 2, 64), (384, 64, 1), 2, 64, "k") == 384
+
+
+def test_unknown_test_flags_fail_cleanly():
+    from gated_deltanet_recurrent_gb300 import build
+    build.build()
+    lib = abi.load_library()
+    assert abi.STATUS[lib.gdn_kv_set_test_flags(None, 1)] == "GDN_ERR_ARG"
