@@ -80,6 +80,22 @@ gdn_status cuda_fail(cudaError_t e, const char *what) {
   return fail(GDN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+// The handle's device is the current one within the scope, whichever the caller has.
+struct OnDevice {
+  int before = -1;
+  cudaError_t status;
+  explicit OnDevice(int device) {
+    status = cudaGetDevice(&before);
+    if (status == cudaSuccess && before != device)
+      status = cudaSetDevice(device);
+    else
+      before = -1;
+  }
+  ~OnDevice() {
+    if (before >= 0) cudaSetDevice(before);
+  }
+};
+
 bool dtype_ok(gdn_dtype d) { return d == GDN_F32 || d == GDN_BF16; }
 size_t dtype_size(gdn_dtype d) { return d == GDN_F32 ? 4 : 2; }
 
@@ -340,7 +356,9 @@ gdn_status gdn_kv_create(const gdn_kv_desc *desc, void *k_codes, void *v_codes,
 
 gdn_status gdn_kv_destroy(gdn_kv *c) {
   if (!c) return ok();
-  const cudaError_t e = cudaDeviceSynchronize();
+  const OnDevice here(c->device);
+  cudaError_t e = cudaDeviceSynchronize();
+  if (here.status != cudaSuccess) e = here.status;
   cudaError_t e2 = cudaFree(c->view.err);
   for (int i = 0; i < c->work.n; ++i) {
     const cudaError_t ew = cudaFree(c->work.kept[i].mem);
@@ -357,7 +375,9 @@ gdn_status gdn_kv_destroy(gdn_kv *c) {
 gdn_status gdn_kv_get_error(gdn_kv *c, uint32_t *dev_err) {
   if (!c || !dev_err) return fail(GDN_ERR_ARG, "kv and dev_err must be non-NULL");
   unsigned int h = 0;
-  cudaError_t e = cudaDeviceSynchronize();
+  const OnDevice here(c->device);
+  cudaError_t e = here.status;
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(&h, c->view.err, sizeof(h), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess) e = cudaMemset(c->view.err, 0, sizeof(h));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();

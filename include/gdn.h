@@ -461,8 +461,8 @@ size_t gdn_kv_scale_bytes(const gdn_kv_desc *desc);
 gdn_status gdn_kv_create(const gdn_kv_desc *desc, void *k_codes, void *v_codes,
                          size_t code_bytes, float *k_scale, float *v_scale, size_t scale_bytes,
                          const int32_t *page_table, gdn_kv **out);
-/* Releases the handle (caller memory is left alone); synchronises the device
- * first.  NULL is a no-op. */
+/* Releases the handle (caller memory is left alone); synchronises its device
+ * first, whichever is current.  NULL is a no-op. */
 gdn_status gdn_kv_destroy(gdn_kv *kv);
 /* As gdn_pool_get_error: waits for the device, returns and clears the word. */
 gdn_status gdn_kv_get_error(gdn_kv *kv, uint32_t *dev_err);
