@@ -39,18 +39,21 @@ cudaError_t KVWork::get(size_t bytes, cudaStream_t s, void **mem, bool *temporar
       return cudaSuccess;
     }
     if (i < kStreams) {  // a new stream, or a larger call than before
-      void *fresh = nullptr;
-      e = cudaMallocFromPoolAsync(&fresh, bytes, pool, s);
-      if (e != cudaSuccess) return e;
-      if (i < n) {
+      // (a call that fails leaves the place as it is, or empty: nothing is lost)
+      if (i < n && kept[i].mem) {
         e = cudaFreeAsync(kept[i].mem, s);
         if (e != cudaSuccess) return e;
-      } else {
-        ++n;
       }
-      kept[i] = {id, fresh, bytes};
+      kept[i] = {id, nullptr, 0};
+      if (i == n) ++n;
+      e = cudaMallocFromPoolAsync(&kept[i].mem, bytes, pool, s);
+      if (e != cudaSuccess) {
+        kept[i].mem = nullptr;
+        return e;
+      }
+      kept[i].bytes = bytes;
       *temporary = false;
-      *mem = fresh;
+      *mem = kept[i].mem;
       return cudaSuccess;
     }
   }

@@ -39,7 +39,7 @@ static cudaError_t alloc(const char *name, void **p, size_t n) {
 }
 static cudaError_t release(const char *name, void *p) {
   const cudaError_t e = call(name);
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && p) {
     if (!live.erase(p)) abort();
     free(p);
   }

@@ -65,3 +65,23 @@ def test_the_error_word_is_read_on_its_own_device(lib):
     lib.cudaGetDevice(ctypes.byref(device))
     assert device.value == 2
     assert lib.gdn_kv_destroy(kv) == 0
+
+
+def test_a_workspace_that_grows_loses_no_memory_when_a_call_fails(lib):
+    kv = create(lib)
+    lib.fake_workspace_bytes(100)
+    assert attend(lib, kv, stream=1) == 0
+    lib.fake_workspace_bytes(200)
+    for name in (b"free_async", b"pool_malloc"):
+        lib.fake_fail(name)
+        assert abi.STATUS[attend(lib, kv, stream=1)] == "GDN_ERR_CUDA"
+    lib.fake_fail(b"")
+    before = lib.fake_live()
+    assert attend(lib, kv, stream=1) == 0
+    assert lib.fake_live() == before + 1     # (the failed growth had given the old one back)
+    lib.fake_reset()
+    for n in (200, 150, 10):                 # what is there serves smaller calls
+        lib.fake_workspace_bytes(n)
+        assert attend(lib, kv, stream=1) == 0
+    assert lib.fake_calls() == b""
+    assert lib.gdn_kv_destroy(kv) == 0
