@@ -214,7 +214,8 @@ cudaError_t launch_kv_read(const KVView &c, int layer, const SeqIndex &seq, cons
 struct KVAttendArgs {
   SeqIndex seq;
   const int32_t *kv_lens;
-  int max_seqlen, max_kv_len;  // hints (>= 1)
+  int max_seqlen, max_kv_len;  // the caller's bounds (>= 1), cut to what the call can hold
+  int kv_hint;                 // max_kv_len as the caller gave it: chooses the kernel only
   const void *q;
   void *o;
   int64_t ld_q, ld_o;          // resolved (never 0)

@@ -200,6 +200,12 @@ gdn_status check_call(const gdn_kv *c, int32_t layer, const int32_t *slot_ids,
   return GDN_OK;
 }
 
+// The caller's bound of the sequences' lengths, no larger than the call allows.
+int32_t bound_seqlen(int32_t max_seqlen, const int32_t *cu_seqlens, int32_t total_tokens) {
+  const int32_t most = cu_seqlens ? total_tokens : 1;
+  return max_seqlen < 1 ? 1 : max_seqlen < most ? max_seqlen : most;
+}
+
 // Token rows: a stride of at least `width` elements, 16-byte aligned rows.
 gdn_status check_rows(const void *p, int64_t *ld, int64_t width, gdn_dtype dt, const char *name) {
   if (*ld == 0) *ld = width;
@@ -419,8 +425,8 @@ gdn_status gdn_kv_append(gdn_kv *c, int32_t layer, const int32_t *slot_ids, cons
        (st = check_device_ptr(v, "v"))))
     return st;
   const gdn::KVRows rows{const_cast<void *>(k), const_cast<void *>(v), ld_k, ld_v, dtype};
-  const cudaError_t e = gdn::launch_kv_append(c->view, layer, seq, pos,
-                                              max_seqlen < 1 ? 1 : max_seqlen, rows, s);
+  max_seqlen = bound_seqlen(max_seqlen, cu_seqlens, total_tokens);
+  const cudaError_t e = gdn::launch_kv_append(c->view, layer, seq, pos, max_seqlen, rows, s);
   if (e != cudaSuccess) return cuda_fail(e, "KV append launch");
   return ok();
 }
@@ -447,8 +453,8 @@ gdn_status gdn_kv_read(gdn_kv *c, int32_t layer, const int32_t *slot_ids, const 
        (v && (st = check_device_ptr(v, "v")))))
     return st;
   const gdn::KVRows rows{k, v, ld_k, ld_v, dtype};
-  const cudaError_t e = gdn::launch_kv_read(c->view, layer, seq, pos,
-                                            max_seqlen < 1 ? 1 : max_seqlen, rows, s);
+  max_seqlen = bound_seqlen(max_seqlen, cu_seqlens, total_tokens);
+  const cudaError_t e = gdn::launch_kv_read(c->view, layer, seq, pos, max_seqlen, rows, s);
   if (e != cudaSuccess) return cuda_fail(e, "KV read launch");
   return ok();
 }
@@ -477,9 +483,11 @@ gdn_status gdn_kv_attend(gdn_kv *c, int32_t layer, const int32_t *slot_ids,
       ((st = check_index(c, seq, kv_lens, true, false, s)) || (st = check_device_ptr(q, "q")) ||
        (st = check_device_ptr(o, "o"))))
     return st;
-  const gdn::KVAttendArgs a{seq,  kv_lens, max_seqlen < 1 ? 1 : max_seqlen,
-                            max_kv_len < 1 ? 1 : max_kv_len, q, o, ld_q, ld_o, q_dtype, o_dtype,
-                            scale};
+  const int64_t capacity = c->view.capacity();
+  const int32_t hint = max_kv_len < 1 ? 1 : max_kv_len;
+  const gdn::KVAttendArgs a{seq,  kv_lens, bound_seqlen(max_seqlen, cu_seqlens, total_tokens),
+                            hint < capacity ? hint : (int)capacity, hint, q, o, ld_q, ld_o,
+                            q_dtype, o_dtype, scale};
   const gdn::KVHost h{&c->k_map, &c->v_map, c->sm_count, c->device, &c->work};
   const cudaError_t e = gdn::launch_kv_attend(c->view, layer, a, h, s);
   if (e != cudaSuccess) return cuda_fail(e, "KV attention launch");

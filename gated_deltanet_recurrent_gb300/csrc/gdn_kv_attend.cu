@@ -877,7 +877,7 @@ cudaError_t launch_kv_attend(const KVView &c, int layer, const KVAttendArgs &a, 
   const int64_t rows = (int64_t)a.max_seqlen * (c.h_q / c.h_kv);
   const int64_t heads = (int64_t)a.seq.n_seqs * c.h_kv;
   if (a.q_dtype == GDN_BF16 && (rows > 32 || (rows > 16 && heads >= 16 && heads <= h.sm_count)) &&
-      (double)heads * ((rows + 15) / 16) * a.max_kv_len > 32768.)
+      (double)heads * ((rows + 15) / 16) * a.kv_hint > 32768.)
     return launch_kv_attend_prompt(c, layer, a, h, s);
   return c.code == GDN_KV_I8 ? by_dim<GDN_KV_I8>(c, layer, a, h, s)
                              : by_dim<GDN_KV_E4M3>(c, layer, a, h, s);

@@ -521,7 +521,9 @@ gdn_status gdn_kv_read(gdn_kv *kv, int32_t layer, const int32_t *slot_ids, const
  * the same smallest step).  The sum that normalises the weights takes them
  * unrounded and holds for V scales of any spread.
  * max_seqlen, max_kv_len: upper bounds of the query and cache lengths, used
- * only to choose the kernel and size its grid (any value >= 1 is correct). */
+ * only to choose the kernel and size its grid (any value >= 1 is correct).  The
+ * grid is sized for no more than total_tokens (without cu_seqlens: one token)
+ * and max_pages * page_tokens. */
 gdn_status gdn_kv_attend(gdn_kv *kv, int32_t layer, const int32_t *slot_ids,
                          const int32_t *kv_lens, const int32_t *cu_seqlens, int32_t n_seqs,
                          int32_t total_tokens, int32_t max_seqlen, int32_t max_kv_len,

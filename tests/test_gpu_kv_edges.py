@@ -1,12 +1,13 @@
 """gdn_kv_attend at the edges of its range: value scales far apart, queries of
-the largest magnitudes.  Tolerances are those of test_gpu_kv_attend.py."""
+the largest magnitudes, loose bounds.  Tolerances are those of test_gpu_kv_attend.py."""
 import numpy as np
 import pytest
 import torch
 
 from gated_deltanet_recurrent_gb300 import abi, synth
+from oracle.kv_oracle import KVOracle, attend_values
 from tests.gpu_util import dev, dev_i32, host, tdtype
-from tests.test_gpu_kv_attend import assert_close, queries, run
+from tests.test_gpu_kv_attend import assert_close, filled, queries, run
 from tests.test_gpu_kv_cache import append, cum, make, rows
 
 pytestmark = pytest.mark.gpu
@@ -149,3 +150,71 @@ def test_queries_of_the_largest_magnitudes(shape, q_dtype, tensor_core):
         want, mag = ref.attend(0, [0], [100], [n], q, scale)
         got = call(kv, [0], [100], [n], q, q_dtype, scale, tensor_core)
         assert_close(got, want, mag, q_dtype, "f32", e)
+
+
+@pytest.mark.parametrize("code", ["i8", "e4m3"])
+@pytest.mark.parametrize("h_q,h_kv,d,hint", [(16, 2, 256, 40), (32, 8, 128, 80), (8, 2, 128, 130)])
+def test_pairs_of_ctas_at_their_edges(code, h_q, h_kv, d, hint):
+    """The bound of the query tokens makes pairs of CTAs take a few rows: an
+    invalid page, queries that are not finite, more queries than positions."""
+    rng = np.random.default_rng(hint + 1)
+    kv, ref = filled(rng, code, 16, h_q, h_kv, d, [200, 2, 333])
+    n = 9
+    q = queries(rng, n, h_q, d, "bf16")
+    o = padded(kv, [1], [2], [n], q, "f32", 0.1, hint)
+    assert (host(o)[:n - 2] == 0).all()
+    want, mag = attend_values(q[n - 2:].astype(np.float64),
+                              *(ref.values(0, 1, s, 0, 2) for s in "kv"), 0.1)
+    assert_close(o[n - 2:], want, mag, "bf16", "f32")
+    bad = q.copy()
+    bad[0, 1, 5], bad[n - 1, h_q - 1, 0] = np.nan, np.inf
+    hit = np.zeros((n, h_q), dtype=bool)
+    hit[0, 1] = hit[n - 1, h_q - 1] = True
+    want, mag = ref.attend(0, [2], [333], [n], q, 0.1)
+    o = padded(kv, [2], [333], [n], bad, "f32", 0.1, hint)
+    assert np.isnan(host(o)[hit]).all()
+    assert_close(o[torch.from_numpy(~hit).cuda()], want[~hit], mag[~hit], "bf16", "f32")
+    assert abi.gdn_kv_get_error(kv) == 0
+    kv.page_table[0, 4] = -1
+    want, mag = attend_values(q.astype(np.float64), *(ref.values(0, 0, s, 0, 200) for s in "kv"),
+                              0.1, np.arange(200) // 16 == 4)
+    assert_close(padded(kv, [0], [200], [n], q, "f32", 0.1, hint), want, mag, "bf16", "f32")
+    assert abi.gdn_kv_get_error(kv) == abi.DEVERR_PAGE
+
+
+@pytest.mark.parametrize("h_q,h,d,page,n_pages,hint", [(32, 4, 256, 128, 18000, 40),
+                                                       (32, 8, 128, 64, 36000, 80)])
+def test_pairs_of_ctas_and_offsets_past_32_bits(h_q, h, d, page, n_pages, hint):
+    rng = np.random.default_rng(22)
+    kv = abi.KVCache.empty(2, 1, n_pages, 5, page, h_q, h, d, torch.int8, host_checks=False)
+    assert kv.k.numel() > 1 << 32
+    table = np.array([[n_pages - 1, n_pages - 7, 11, n_pages - 2, 12]])
+    kv.page_table.copy_(torch.from_numpy(table.astype(np.int32)))
+    k, v = rows(rng, 300, h, d, "bf16"), rows(rng, 300, h, d, "bf16")
+    abi.gdn_kv_append(kv, 1, dev_i32([0]), dev_i32([0]), dev(k, "bf16"), dev(v, "bf16"),
+                      cu_seqlens=cum([300]))
+    ref = KVOracle(1, 5, h, page, d, "i8", np.arange(5)[None])
+    ref.append(0, [0], [0], [300], k, v)
+    q = queries(rng, hint, h_q, d, "bf16")
+    want, mag = ref.attend(0, [0], [300], [hint], q, 1 / 16)
+    o = run(kv, 1, [0], [300], [hint], q, "bf16", "f32", 1 / 16, max_seqlen=hint,
+            max_kv_len=200000)
+    assert_close(o, want, mag, "bf16", "f32")
+
+
+def test_bounds_far_beyond_the_call():
+    """Every bound is correct, also the largest there is."""
+    rng = np.random.default_rng(23)
+    kv, ref = filled(rng, "i8", 16, 8, 2, 128, [100, 40])
+    huge = 2 ** 31 - 1
+    for lens in ([3, 2], [40, 25]):
+        q = queries(rng, sum(lens), 8, 128, "bf16")
+        want, mag = ref.attend(0, [0, 1], [100, 40], lens, q, 0.1)
+        got = run(kv, 0, [0, 1], [100, 40], lens, q, "bf16", "f32", 0.1, max_seqlen=huge,
+                  max_kv_len=huge)
+        assert_close(got, want, mag, "bf16", "f32")
+    back = torch.empty(90, 2, 128, device="cuda")
+    abi.gdn_kv_read(kv, 0, dev_i32([0, 1]), dev_i32([10, 40]), back, None, cu_seqlens=cum([90, 0]),
+                    max_seqlen=huge)
+    assert np.array_equal(host(back), ref.values(0, 0, "k", 10, 100))
+    assert abi.gdn_kv_get_error(kv) == 0

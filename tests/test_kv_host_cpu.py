@@ -85,3 +85,29 @@ def test_a_workspace_that_grows_loses_no_memory_when_a_call_fails(lib):
         assert attend(lib, kv, stream=1) == 0
     assert lib.fake_calls() == b""
     assert lib.gdn_kv_destroy(kv) == 0
+
+
+HUGE = 2 ** 31 - 1
+
+
+def test_loose_bounds_are_cut_to_what_a_call_can_hold(lib):
+    """A caller that captures a graph gives a loose bound: it must not size a
+    grid of two thousand million CTAs for a handful of tokens."""
+    kv = create(lib)
+    rows = (0x8000, 0, 0x9000, 0, abi.GDN_BF16, None)
+    for hint, want in ((HUGE, 50), (50, 50), (20, 20), (1, 1), (0, 1), (-5, 1)):
+        assert attend(lib, kv, cu=0xa000, n_seqs=3, tokens=50, max_seqlen=hint) == 0
+        assert lib.fake_max_seqlen() == want
+        for call in (lib.gdn_kv_append, lib.gdn_kv_read):
+            assert call(kv, 0, 0x6000, 0x7000, 0xa000, 3, 50, hint, *rows) == 0
+            assert lib.fake_rows_max_seqlen() == want
+    # one token each: no sequence is longer
+    assert attend(lib, kv, n_seqs=3, tokens=3, max_seqlen=HUGE) == 0
+    assert lib.fake_max_seqlen() == 1
+    assert lib.gdn_kv_append(kv, 0, 0x6000, 0x7000, None, 3, 3, HUGE, *rows) == 0
+    assert lib.fake_rows_max_seqlen() == 1
+    # a slot holds 2 pages of 16
+    for hint, want in ((HUGE, 32), (32, 32), (7, 7), (0, 1)):
+        assert attend(lib, kv, max_kv_len=hint) == 0
+        assert lib.fake_max_kv_len() == want
+    assert lib.gdn_kv_destroy(kv) == 0
