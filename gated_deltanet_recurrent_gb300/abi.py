@@ -183,7 +183,7 @@ def _token_rows(t: torch.Tensor, heads: int, dim: int, name: str) -> int:
     """Token stride (elements) of a [tokens, heads, dim] view whose heads are packed."""
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
         raise GDNError(5, f"{name} must be [tokens, {heads}, {dim}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 or t.stride(1) != dim:
+    if t.stride(2) != 1 or (t.stride(1) != dim and heads > 1):
         raise GDNError(1, f"{name}: heads must be packed (strides {t.stride()})")
     return _row_stride(t, heads * dim, name)
 
@@ -635,7 +635,7 @@ def _kv_token_rows(shape, stride, heads, dim, name):
     stride says nothing)."""
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise GDNError(5, f"{name} must be [tokens, {heads}, {dim}], got {tuple(shape)}")
-    if stride[2] != 1 or stride[1] != dim:
+    if stride[2] != 1 or (stride[1] != dim and heads > 1):
         raise GDNError(1, f"{name}: heads must be packed (strides {stride})")
     if shape[0] <= 1:
         return 0

@@ -57,6 +57,17 @@ def test_the_stride_of_a_single_row_says_nothing():
     assert abi._kv_token_rows((3, 2, 64), (384, 64, 1), 2, 64, "k") == 384
 
 
+def test_the_stride_of_a_single_head_says_nothing():
+    x = torch.zeros(5, 3, 64)[:, 1:2]                # packed rows' second head: strides 192, 64
+    assert abi._kv_token_rows(x.shape, x.stride(), 1, 64, "k") == 192
+    x = torch.zeros(1, 5, 64).transpose(0, 1)        # [5, 1, 64] of strides 64, 320
+    assert x.stride(1) == 320
+    assert abi._kv_token_rows(x.shape, x.stride(), 1, 64, "k") == 64
+    assert abi._token_rows(x, 1, 64, "q") == 64
+    with pytest.raises(abi.GDNError):
+        abi._kv_token_rows((5, 2, 64), (640, 320, 1), 2, 64, "k")
+
+
 def test_unknown_test_flags_fail_cleanly():
     from gated_deltanet_recurrent_gb300 import build
     build.build()
