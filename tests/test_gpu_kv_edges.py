@@ -1,5 +1,7 @@
 """gdn_kv_attend at the edges of its range: value scales far apart, queries of
-the largest magnitudes, loose bounds.  Tolerances are those of test_gpu_kv_attend.py."""
+the largest magnitudes, loose bounds, every form of the tensor-core kernel over
+long contexts, the unequal cut of large decode batches, and more streams than a
+handle keeps workspaces for.  Tolerances are those of test_gpu_kv_attend.py."""
 import numpy as np
 import pytest
 import torch
@@ -218,3 +220,74 @@ def test_bounds_far_beyond_the_call():
                     max_seqlen=huge)
     assert np.array_equal(host(back), ref.values(0, 0, "k", 10, 100))
     assert abi.gdn_kv_get_error(kv) == 0
+
+
+@pytest.mark.parametrize("code", ["i8", "e4m3"])
+@pytest.mark.parametrize("h_q,h_kv,d,n", FORMS)
+def test_tensor_core_kernel_over_long_contexts(code, h_q, h_kv, d, n):
+    """Enough sequences that no context is cut, of some 20 tiles each."""
+    rng = np.random.default_rng(n + d)
+    lens = [2500, 2311, 1100]
+    kv, ref = filled(rng, code, 64 if d == 64 else 128, h_q, h_kv, d, lens)
+    n_seqs = 160 // h_kv + 1
+    slots = [i % 3 for i in range(n_seqs)]
+    kv_lens = [int(rng.integers(max(n, lens[s] - 300), lens[s] + 1)) for s in slots]
+    q = queries(rng, n * n_seqs, h_q, d, "bf16")
+    o = run(kv, 0, slots, kv_lens, [n] * n_seqs, q, "bf16", "bf16", d ** -0.5, max_seqlen=n,
+            max_kv_len=2500)
+    for i in (0, 1, 2, n_seqs - 1):
+        part = q[i * n:(i + 1) * n]
+        want, mag = ref.attend(0, [slots[i]], [kv_lens[i]], [n], part, d ** -0.5)
+        assert_close(o[i * n:(i + 1) * n], want, mag, "bf16", "bf16", i)
+    # one of them alone: its context is cut into several CTAs' pieces
+    o = run(kv, 0, [0], [2500], [n], q[:n], "bf16", "f32", d ** -0.5, max_seqlen=n,
+            max_kv_len=5000)
+    want, mag = ref.attend(0, [0], [2500], [n], q[:n], d ** -0.5)
+    assert_close(o, want, mag, "bf16", "f32")
+    assert abi.gdn_kv_get_error(kv) == 0
+
+
+@pytest.mark.parametrize("code", ["i8", "e4m3"])
+@pytest.mark.parametrize("q_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("h_q,n_seqs", [(16, 45), (16, 64), (6, 200)])
+def test_decode_batches_in_unequal_pieces(code, q_dtype, h_q, n_seqs):
+    """d = 256, up to eight query heads per KV head, and more than four tiles
+    a CTA of a full grid: the pieces of the line of tiles differ in length by
+    the CTA's order on its SM, and units are cut where the orders meet.  Up to
+    8 tiles a CTA the line has no places for the units' starts, above it has."""
+    rng = np.random.default_rng(n_seqs)
+    lens = [2500, 2311, 2400, 2100, 2048, 2499, 1900, 2450]
+    kv, ref = filled(rng, code, 64, h_q, 2, 256, lens)
+    slots = [i % 8 for i in range(n_seqs)]
+    kv_lens = [int(rng.integers(1 if i % 9 == 7 else lens[s] * 3 // 4, lens[s] + 1))
+               for i, s in enumerate(slots)]
+    kv_lens[0] = 2500
+    ctas = 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    assert 2 * sum(-(-x // 64) for x in kv_lens) >= 4 * ctas
+    assert (n_seqs * 2 * (2500 // 64 + 1) >= 8 * ctas) == (n_seqs > 45)
+    q = queries(rng, n_seqs, h_q, 256, q_dtype)
+    got = run(kv, 0, slots, kv_lens, [1] * n_seqs, q, q_dtype, "f32", 1 / 16, max_kv_len=2500)
+    want, mag = ref.attend(0, slots, kv_lens, [1] * n_seqs, q, 1 / 16)
+    assert_close(got, want, mag, q_dtype, "f32")
+    assert abi.gdn_kv_get_error(kv) == 0
+
+
+def test_more_streams_than_kept_workspaces():
+    """A handle keeps workspaces for 16 streams; calls on others are as right."""
+    rng = np.random.default_rng(30)
+    kv, ref = filled(rng, "i8", 64, 8, 2, 128, [3000, 700])
+    for n in (1, 24):
+        q = queries(rng, 2 * n, 8, 128, "bf16")
+        want, mag = ref.attend(0, [0, 1], [3000, 700], [n, n], q, 0.1)
+        qd, slots, kv_lens, cu = dev(q, "bf16"), dev_i32([0, 1]), dev_i32([3000, 700]), cum([n, n])
+        streams, outs = [torch.cuda.Stream() for _ in range(20)], []
+        torch.cuda.synchronize()
+        for rep in range(3):
+            for s in streams:
+                with torch.cuda.stream(s):
+                    outs.append(abi.gdn_kv_attend(kv, 0, slots, kv_lens, qd, cu_seqlens=cu,
+                                                  max_seqlen=n, max_kv_len=3000, scale=0.1))
+        torch.cuda.synchronize()
+        for o in outs:
+            assert torch.equal(o, outs[0])
+        assert_close(outs[0], want, mag, "bf16", "bf16")
