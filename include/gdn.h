@@ -427,7 +427,15 @@ gdn_status gdn_prefill_chunked_noalloc(gdn_pool *pool, int32_t layer, const int3
  * (GDN_KV_E4M3), -100 <= e <= 120 (I8) or 118 (E4M3); larger magnitudes are
  * stored as the top code.  A code is value / scale rounded to nearest even.
  * Powers of two make value / scale, code * scale and a change of scale exact
- * up to that one rounding, in float32 and in bf16. */
+ * up to that one rounding, in float32 and in bf16.
+ *
+ * What that costs: a value is off by at most scale / 2 (I8; scale is up to twice
+ * amax / 127 of its page and head), or by 2^-4 of itself or 2^-10 scale (E4M3),
+ * in a page that grows by several appends by at most twice that.  One scale
+ * serves page_tokens * d elements: where a few channels are much larger than the
+ * others, their size sets the step of all int8 codes, and E4M3 is the better
+ * choice; without such channels int8 is about twice as close.  Small pages help
+ * int8 and do not matter to E4M3. */
 typedef enum { GDN_KV_I8 = 0, GDN_KV_E4M3 = 1 } gdn_kv_code;
 
 /* Supported: d in {64, 128, 256}, page_tokens in {16, 32, 64, 128}, h_q a
@@ -453,8 +461,10 @@ size_t gdn_kv_scale_bytes(const gdn_kv_desc *desc);
 
 /* Wrap caller memory (codes 16-byte aligned, scales and table 4-byte).  The
  * handle allocates an error word and owns a memory pool from which
- * gdn_kv_attend takes a workspace for each stream that it is called on (some
- * ten MiB; kept for reuse until gdn_kv_destroy).  Every compute call below is
+ * gdn_kv_attend takes a workspace for each of the first 16 streams that it is
+ * called on (some ten MiB; kept for reuse until gdn_kv_destroy).  The first call
+ * on a stream, a larger one than before, one that is being captured and every
+ * call on further streams allocate from that pool.  Every compute call below is
  * asynchronous on its stream.  Calls on different streams may overlap if none
  * appends to a page that another reads or appends to; calls from several host
  * threads on one handle must be serialised by the caller. */
