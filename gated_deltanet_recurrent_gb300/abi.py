@@ -511,7 +511,8 @@ _KV_CODES = {torch.int8: GDN_KV_I8, torch.float8_e4m3fn: GDN_KV_E4M3}
 class KVCache:
     """A handle on an 8-bit paged KV cache plus the torch tensors that hold it:
     k, v [n_layers, n_pages, h_kv, page_tokens, d] codes (int8 or
-    float8_e4m3fn), k_scale, v_scale [n_layers, n_pages, h_kv] float32 powers
+    float8_e4m3fn: the latter where a few channels of the keys are much larger
+    than the others), k_scale, v_scale [n_layers, n_pages, h_kv] float32 powers
     of two (value = code * scale) and page_table [n_slots, max_pages] int32,
     which the caller fills with page ids.  See gdn.h for the layout's rules."""
 
@@ -702,7 +703,9 @@ def gdn_kv_attend(kv: KVCache, layer: int, slot_ids: torch.Tensor, kv_lens: torc
                   max_kv_len: int = 0, scale: Optional[float] = None, stream=None):
     """Causal attention of q [tokens, h_q, d] over the slots' cached tokens;
     kv_lens counts the query tokens themselves (append them first).  o
-    [tokens, h_q, d] (default: q's type); scale defaults to d ** -0.5."""
+    [tokens, h_q, d] (default: q's type); scale defaults to d ** -0.5.  With
+    bf16 q the softmax weights are rounded to 2^-11, whichever type o has; with
+    float32 q they and q are held to 2^-22."""
     if o is None:
         o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     shape = q.shape

@@ -39,10 +39,13 @@
 // sums in a workspace, which a second, programmatically dependent kernel joins.
 //
 // Measured (6792 GB/s is a plain copy): 256 slots, 32 x 8 heads of 128, contexts
-// up to 8192, e4m3: 360 us, 6.4 TB/s; 64 slots, 16 x 2 heads of 256, int8: 66 us,
-// 4.7 TB/s, of which 15 us are the start, the units' starts and the join.  With
-// registers as the stages (no rings) the first took 395 us and the second 77.
-// d = 64 reaches 3.4 TB/s: there a step's fixed instructions outweigh its bytes.
+// up to 8192, e4m3: 360 us, 6.4 TB/s (float32 queries 398 us); 64 slots, 16 x 2
+// heads of 256, int8: 67 us, 4.6 TB/s, of which 15 us are the start, the units'
+// starts and the join (float32 77 us).  With registers as the stages (no rings)
+// the first took 395 us and the second 77.  d = 64 reaches 3.3 (int8) and 3.9
+// TB/s (e4m3): there a step's fixed instructions outweigh its bytes.  Float32
+// prompts run here too, 16 rows at a time: 2048 tokens of 32 x 8 x 128 take 472
+// us, 8192 take 6.4 ms, 86 TFLOP/s.
 #include <cuda.h>
 
 #include "gdn_kv.cuh"
@@ -72,7 +75,8 @@ struct SplitCfg {
   // What a unit's start costs a CTA (its queries, its first page ids and codes), in tiles:
   // the line of tiles is cut as if each unit had so many more (where there are many tiles per
   // CTA; else every CTA should have as few as possible).  Measured on 64 contexts up to 8192,
-  // d = 256: a second unit takes a CTA 5 us, a tile 2.4 us.
+  // d = 256: a second unit takes a CTA 5 us, a tile 2.4 us; for the other d the same bytes, not
+  // measured.
   static constexpr int kEntry = 512 / D;
   // Shares of an SM's CTAs.  The warps that came first are issued first: with equal shares
   // the three CTAs of d = 256 (NT = 1) end after 44, 47.5 and 53 us.

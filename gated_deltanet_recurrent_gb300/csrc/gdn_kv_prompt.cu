@@ -29,10 +29,13 @@
 // half of every K and V operand, which halves all but the queries' part (8 pieces
 // of up to 2048 tokens, 16 x 2 heads, d = 256: 1422 -> 969 us when this came).
 // MT = 2 halves the conversion per row; d = 256 has room in TMEM (O 256 columns,
-// two S) for MT = 1 only.  Measured: those pieces 631 us (1210 TFLOP/s, tensor
-// pipe 51 % active); a prompt of 8192, 32 x 8 heads, d = 128, 485 us (1135
+// two S) for MT = 1 only.  Measured: those pieces 619 us (1230 TFLOP/s, tensor
+// pipe 52 % active); a prompt of 8192, 32 x 8 heads, d = 128, 483 us (1140
 // TFLOP/s, 48 %).  What is left is the softmax's latency between the two
-// products of a tile (1550 of 3300 cycles), and 6 us of setup per unit.
+// products of a tile (1550 of 3300 cycles), and 6 us of setup per unit.  d = 64
+// has half the products for the same softmax: a prompt of 8192, 32 x 8 heads,
+// 501 us in int8, 470 in e4m3 (550 and 585 TFLOP/s), although the e4m3 form
+// spills 0.4 KB a thread.
 #include <cuda.h>
 
 #include <type_traits>

@@ -497,7 +497,8 @@ gdn_status gdn_kv_set_test_flags(gdn_kv *kv, uint32_t flags);
  * last new token keep no meaning.
  * k, v: [total_tokens][h_kv][d] in dtype (GDN_F32 or GDN_BF16), token strides
  * ld_k, ld_v elements (0: h_kv * d); rows 16-byte aligned.  pos: [n_seqs].
- * max_seqlen as for gdn_conv_silu.  A sequence whose range does not fit
+ * max_seqlen as for gdn_conv_silu.  The slots of a call must be distinct (host
+ * checks: GDN_ERR_DUP_SLOT).  A sequence whose range does not fit
  * [0, max_pages * page_tokens) is skipped (GDN_DEVERR_SEQ). */
 gdn_status gdn_kv_append(gdn_kv *kv, int32_t layer, const int32_t *slot_ids, const int32_t *pos,
                          const int32_t *cu_seqlens, int32_t n_seqs, int32_t total_tokens,
@@ -523,13 +524,13 @@ gdn_status gdn_kv_read(gdn_kv *kv, int32_t layer, const int32_t *slot_ids, const
  * q: [total_tokens][h_q][d] in q_dtype, o the same shape in o_dtype (GDN_F32
  * or GDN_BF16), token strides ld_q, ld_o elements (0: h_q * d), rows 16-byte
  * aligned; scale is finite.  Scores, softmax statistics and sums are float32;
- * the products run on the tensor cores on the codes (exact in binary16) and
- * on queries and weights rounded to binary16 (bf16 q: the query exactly, up
- * to 2^-25 of its row's largest element; the weight to 2^-11, or to 2^-32 of
- * the row's largest weight x V scale where that is more, a scale counting as at
- * least 2^-84), or split into two binary16 parts each (float32 q: to 2^-22, with
- * the same smallest step).  The sum that normalises the weights takes them
- * unrounded and holds for V scales of any spread.
+ * the products run on the tensor cores on the codes (exact in binary16) and on
+ * queries and weights rounded to binary16 (bf16 q: the query exactly, up to
+ * 2^-25 of its row's largest element; the weight, whichever type o has, to
+ * 2^-11, or to 2^-32 of the row's largest weight x V scale where that is more,
+ * a scale counting as at least 2^-84), or split into two binary16 parts each
+ * (float32 q: to 2^-22, with the same smallest step).  The sum that normalises
+ * the weights takes them unrounded and holds for V scales of any spread.
  * max_seqlen, max_kv_len: upper bounds of the query and cache lengths, used
  * only to choose the kernel and size its grid (any value >= 1 is correct).  The
  * grid is sized for no more than total_tokens (without cu_seqlens: one token)
