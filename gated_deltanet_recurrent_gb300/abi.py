@@ -22,6 +22,7 @@ STATUS = {0: "GDN_OK", 1: "GDN_ERR_ARG", 2: "GDN_ERR_SLOT", 3: "GDN_ERR_DUP_SLOT
 DEVERR_SLOT, DEVERR_SEQ, DEVERR_COUNT, DEVERR_TIMEOUT = 1, 2, 4, 8
 DEVERR_PAGE, DEVERR_VALUE = 16, 32
 GDN_KV_I8, GDN_KV_E4M3 = 0, 1
+GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
 TEST_DECODE_WAIT_TIMEOUT = 1
 TEST_KV_WAIT_TIMEOUT = 1
 
@@ -35,7 +36,8 @@ EXPORTED = ("gdn_pool_state_bytes", "gdn_pool_conv_bytes", "gdn_pool_create", "g
             "gdn_spec_verify_deferred", "gdn_prefill_chunked_noalloc", "gdn_prefill_chunked_ckpt",
             "gdn_kv_code_bytes", "gdn_kv_scale_bytes", "gdn_kv_create", "gdn_kv_destroy",
             "gdn_kv_get_error", "gdn_kv_set_test_flags", "gdn_kv_append", "gdn_kv_read",
-            "gdn_kv_attend",
+            "gdn_kv_attend", "gdn_kv_pages_grow", "gdn_kv_pages_trim",
+            "gdn_rope_create", "gdn_rope_destroy", "gdn_rope",
             "gdn_status_string",
             "gdn_last_error_message")
 
@@ -67,6 +69,19 @@ class gdn_kv_desc(ctypes.Structure):
                 ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("page_tokens", ctypes.c_int32), ("h_q", ctypes.c_int32),
                 ("h_kv", ctypes.c_int32), ("d", ctypes.c_int32), ("code", ctypes.c_int),
+                ("host_checks", ctypes.c_int32)]
+
+
+class gdn_kv_pages(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p)]
+
+
+class gdn_rope_desc(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("layout", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_int64), ("low_turns", ctypes.c_double),
+                ("high_turns", ctypes.c_double), ("out_scale", ctypes.c_float),
                 ("host_checks", ctypes.c_int32)]
 
 
@@ -125,6 +140,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "gdn_kv_read": (st, [vp, i32, vp, vp, vp, i32, i32, i32, vp, i64, vp, i64, st, vp]),
         "gdn_kv_attend": (st, [vp, i32, vp, vp, vp, i32, i32, i32, i32, vp, i64, st, vp, i64, st,
                                ctypes.c_float, vp]),
+        "gdn_kv_pages_grow": (st, [vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp]),
+        "gdn_kv_pages_trim": (st, [vp, vp, vp, vp, i32, vp]),
+        "gdn_rope_create": (st, [P(gdn_rope_desc), P(vp)]),
+        "gdn_rope_destroy": (st, [vp]),
+        "gdn_rope": (st, [vp, i32, vp, vp, i64, i32, vp, i64, i32, vp, i64, vp, i64, st, vp]),
         "gdn_status_string": (ctypes.c_char_p, [st]),
         "gdn_last_error_message": (ctypes.c_char_p, []),
     }
@@ -726,3 +746,176 @@ def gdn_kv_attend(kv: KVCache, layer: int, slot_ids: torch.Tensor, kv_lens: torc
     if status:
         _check(status)
     return o
+
+
+# ----------------------------------------- pages of the KV cache, on the GPU
+
+class KVPages:
+    """What the page calls keep beside the cache's page table: held [n_slots], free_pages
+    [n_pages] and n_free [1], int32 on the cache's device.  By default no slot holds a page
+    (the page table's entries are -1) and page 0 is the first to be given out."""
+
+    def __init__(self, kv: KVCache, held=None, free_pages=None, n_free=None):
+        d, device = kv.desc, kv.page_table.device
+        if (held is None) != (free_pages is None) or (held is None) != (n_free is None):
+            raise GDNError(1, "held, free_pages and n_free are given together")
+        if held is None:
+            held = torch.zeros(d.n_slots, dtype=torch.int32, device=device)
+            free_pages = torch.arange(d.n_pages - 1, -1, -1, dtype=torch.int32, device=device)
+            n_free = torch.full((1,), d.n_pages, dtype=torch.int32, device=device)
+        for name, t, size in (("held", held, d.n_slots), ("free_pages", free_pages, d.n_pages),
+                              ("n_free", n_free, 1)):
+            if t.dtype != torch.int32 or not t.is_contiguous() or t.device != device:
+                raise GDNError(1, f"{name} must be contiguous int32 on the cache's device")
+            if t.numel() != size:
+                raise GDNError(5, f"{name} must have {size} entries")
+        self.page_table, self.held, self.free_pages, self.n_free = \
+            kv.page_table, held, free_pages, n_free
+        self.desc = gdn_kv_pages(kv.page_table.data_ptr(), held.data_ptr(),
+                                 free_pages.data_ptr(), n_free.data_ptr())
+        self.desc_ptr = ctypes.addressof(self.desc)
+
+
+def _like(t, name, dtype, size, device):
+    """Pointer of an optional output array."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_contiguous() or t.device != device:
+        raise GDNError(1, f"{name} must be a contiguous {dtype} tensor on slot_ids' device")
+    if t.numel() != size:
+        raise GDNError(5, f"{name} must have {size} entries")
+    return t.data_ptr()
+
+
+def gdn_kv_pages_grow(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, pos: torch.Tensor,
+                      cu_seqlens: Optional[torch.Tensor] = None, total_tokens: int = -1,
+                      positions: Optional[torch.Tensor] = None,
+                      rows: Optional[torch.Tensor] = None,
+                      granted: Optional[torch.Tensor] = None, stream=None):
+    """Pages for the new tokens at pos[i], pos[i] + 1, ... of slot slot_ids[i] (one each, or
+    packed by cu_seqlens).  positions (int32), rows (int64): [total_tokens], where each token
+    goes; granted (int32): [n_seqs], 0 where the free pages did not suffice; each is written if
+    given.  total_tokens is needed where neither positions nor rows says it."""
+    n, device = slot_ids.numel(), slot_ids.device
+    tokens = rows.numel() if rows is not None else \
+        positions.numel() if positions is not None else total_tokens
+    if total_tokens not in (-1, tokens):
+        raise GDNError(5, f"total_tokens is {total_tokens}, the outputs hold {tokens}")
+    if tokens < 0:
+        if cu_seqlens is not None:
+            raise GDNError(1, "total_tokens is needed with cu_seqlens")
+        tokens = n
+    if device != pages.held.device or pos.device != device or \
+            (cu_seqlens is not None and cu_seqlens.device != device):
+        raise GDNError(1, "slot_ids, pos and cu_seqlens must be on the cache's device")
+    slots, starts, cu, n = _kv_index(slot_ids, pos, cu_seqlens, tokens, "pos")
+    status = _lib.gdn_kv_pages_grow(
+        kv.handle, pages.desc_ptr, slots, starts, cu, n, tokens,
+        _like(positions, "positions", torch.int32, tokens, device),
+        _like(rows, "rows", torch.int64, tokens, device),
+        _like(granted, "granted", torch.int32, n, device), _kv_stream(stream, slot_ids))
+    if status:
+        _check(status)
+
+
+def gdn_kv_pages_trim(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, lens: torch.Tensor,
+                      stream=None):
+    """Give back the pages that the first lens[i] tokens of slot slot_ids[i] do not use."""
+    n, device = slot_ids.numel(), slot_ids.device
+    if device != pages.held.device or lens.device != device:
+        raise GDNError(1, "slot_ids and lens must be on the cache's device")
+    slots, starts, _, n = _kv_index(slot_ids, lens, None, n, "lens")
+    status = _lib.gdn_kv_pages_trim(kv.handle, pages.desc_ptr, slots, starts, n,
+                                    _kv_stream(stream, slot_ids))
+    if status:
+        _check(status)
+
+
+# ------------------------------------------------------------ rotary positions
+
+_ROPE_LAYOUTS = {"half": GDN_ROPE_HALF, "interleaved": GDN_ROPE_INTERLEAVED}
+
+
+class Rope:
+    """A plan of rotary positions: heads of d elements whose first `rot` (default: all) are
+    turned, in pairs (j, j + rot/2) ("half") or (2j, 2j + 1) ("interleaved"), by position *
+    base ** (-2j / rot).  factor, original_len, low_turns and high_turns scale the frequencies
+    for long contexts and out_scale what is rotated: see gdn.h."""
+
+    def __init__(self, d, rot=None, layout="half", base=10000.0, factor=1.0, original_len=0,
+                 low_turns=1.0, high_turns=32.0, out_scale=1.0, host_checks=False):
+        if layout not in _ROPE_LAYOUTS:
+            raise GDNError(1, f"layout must be one of {sorted(_ROPE_LAYOUTS)}, got {layout!r}")
+        self.d, self.rot = d, d if rot is None else rot
+        self.desc = gdn_rope_desc(d, self.rot, _ROPE_LAYOUTS[layout], base, factor, original_len,
+                                  low_turns, high_turns, out_scale, 1 if host_checks else 0)
+        self.handle = gdn_rope_create(self.desc)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            gdn_rope_destroy(self)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def gdn_rope_create(desc: gdn_rope_desc):
+    out = ctypes.c_void_p()
+    _check(load_library().gdn_rope_create(ctypes.byref(desc), ctypes.byref(out)))
+    return out
+
+
+def gdn_rope_destroy(rope: Rope):
+    _check(load_library().gdn_rope_destroy(rope.handle))
+
+
+def _rope_rows(x, out, d, tokens, dtype, device, name):
+    """Pointer, token stride and heads of x [tokens, heads, d], and pointer and stride of out
+    (None: x itself)."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != tokens:
+        raise GDNError(5, f"{name} must be [{tokens}, heads, {d}], got {tuple(shape)}")
+    heads = shape[1]
+    ld = _kv_token_rows(shape, x.stride(), heads, d, name)
+    if out is None or out is x:
+        out, ld_out = x, ld
+    else:
+        if out.shape != shape:
+            raise GDNError(5, f"{name}_out must have {name}'s shape {tuple(shape)}")
+        ld_out = _kv_token_rows(shape, out.stride(), heads, d, f"{name}_out")
+    if x.dtype != dtype or out.dtype != dtype:
+        raise GDNError(4, "q, k and their outputs must share one dtype")
+    if x.device != device or out.device != device:
+        raise GDNError(1, f"{name} must be on the positions' device")
+    return x.data_ptr(), ld, heads, out.data_ptr(), ld_out
+
+
+def gdn_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor],
+             k: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+             k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotate q [tokens, h_q, d] and k [tokens, h_k, d] (float32 or bf16; either may be None; the
+    token stride may exceed heads * d) to positions [tokens] int32, into q_out and k_out, or in
+    place where these are not given.  Returns both."""
+    first = k if q is None else q
+    if first is None:
+        raise GDNError(1, "q or k is needed")
+    tokens, dtype, device = positions.numel(), first.dtype, positions.device
+    code = _kv_dtype(first)
+    if positions.dtype != torch.int32 or not positions.is_contiguous() or \
+            device.type != "cuda":
+        raise GDNError(1, "positions must be a contiguous int32 tensor on the GPU")
+    q_ptr = q_to = k_ptr = k_to = None
+    ld_q = h_q = ld_q_to = ld_k = h_k = ld_k_to = 0
+    if q is not None:
+        q_ptr, ld_q, h_q, q_to, ld_q_to = _rope_rows(q, q_out, rope.d, tokens, dtype, device, "q")
+    if k is not None:
+        k_ptr, ld_k, h_k, k_to, ld_k_to = _rope_rows(k, k_out, rope.d, tokens, dtype, device, "k")
+    status = _lib.gdn_rope(rope.handle, tokens, positions.data_ptr(), q_ptr, ld_q, h_q, k_ptr, ld_k,
+                           h_k, q_to, ld_q_to, k_to, ld_k_to, code, _kv_stream(stream, positions))
+    if status:
+        _check(status)
+    return q if q_out is None else q_out, k if k_out is None else k_out

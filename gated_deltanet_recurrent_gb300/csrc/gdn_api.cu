@@ -9,17 +9,7 @@
 #include <string>
 #include <vector>
 
-#include "gdn_internal.h"
-
-struct gdn_pool {
-  gdn::PoolView view;
-  gdn_pool_desc desc;
-  int device;
-  int sm_count;
-  bool has_tmap;
-  alignas(64) CUtensorMap tmap;  // the state as a [rows][dk] float32 tensor (TMA)
-  cudaMemPool_t work_pool;       // stream-ordered prefill workspaces (kept until destroy)
-};
+#include "gdn_handles.h"
 
 namespace {
 

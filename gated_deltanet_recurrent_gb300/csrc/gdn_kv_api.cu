@@ -3,23 +3,13 @@
 // table entries in use, and the kernel launches.
 #include <cuda.h>
 #include <cudaTypedefs.h>
-#include <stdarg.h>
-#include <stdio.h>
 
 #include <cmath>
 #include <new>
 #include <vector>
 
-#include "gdn_internal.h"
-
-struct gdn_kv {
-  gdn::KVView view;
-  gdn_kv_desc desc;
-  int device;
-  int sm_count;
-  alignas(64) CUtensorMap k_map, v_map;  // see gdn::KVHost
-  gdn::KVWork work;
-};
+#include "gdn_handles.h"
+#include "gdn_host.h"
 
 namespace gdn {
 
@@ -64,43 +54,7 @@ cudaError_t KVWork::get(size_t bytes, cudaStream_t s, void **mem, bool *temporar
 
 namespace {
 
-gdn_status fail(gdn_status s, const char *fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  gdn::set_last_message(buf);
-  return s;
-}
-
-gdn_status ok() {
-  gdn::set_last_message("");
-  return GDN_OK;
-}
-
-gdn_status cuda_fail(cudaError_t e, const char *what) {
-  return fail(GDN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-// The handle's device is the current one within the scope, whichever the caller has.
-struct OnDevice {
-  int before = -1;
-  cudaError_t status;
-  explicit OnDevice(int device) {
-    status = cudaGetDevice(&before);
-    if (status == cudaSuccess && before != device)
-      status = cudaSetDevice(device);
-    else
-      before = -1;
-  }
-  ~OnDevice() {
-    if (before >= 0) cudaSetDevice(before);
-  }
-};
-
-bool dtype_ok(gdn_dtype d) { return d == GDN_F32 || d == GDN_BF16; }
-size_t dtype_size(gdn_dtype d) { return d == GDN_F32 ? 4 : 2; }
+using namespace gdn::host;
 
 gdn_status check_desc(const gdn_kv_desc *d) {
   if (!d) return fail(GDN_ERR_ARG, "desc is NULL");
@@ -125,29 +79,6 @@ gdn_status check_desc(const gdn_kv_desc *d) {
   // positions and lengths are int32 throughout
   if ((int64_t)d->max_pages * d->page_tokens > INT32_MAX - 256)
     return fail(GDN_ERR_UNSUPPORTED, "max_pages * page_tokens must stay below 2^31 - 256");
-  return GDN_OK;
-}
-
-gdn_status check_device_ptr(const void *ptr, const char *name) {
-  cudaPointerAttributes attr;
-  if (cudaPointerGetAttributes(&attr, ptr) != cudaSuccess) {
-    cudaGetLastError();
-    return fail(GDN_ERR_ARG, "%s: cudaPointerGetAttributes failed", name);
-  }
-  if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged)
-    return fail(GDN_ERR_ARG, "%s is not device memory", name);
-  return GDN_OK;
-}
-
-gdn_status fetch(std::vector<int32_t> &dst, const int32_t *src, size_t n, cudaStream_t s,
-                 const char *name) {
-  dst.resize(n);
-  if (n == 0) return GDN_OK;
-  gdn_status st = check_device_ptr(src, name);
-  if (st != GDN_OK) return st;
-  cudaError_t e = cudaMemcpyAsync(dst.data(), src, n * sizeof(int32_t), cudaMemcpyDefault, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return cuda_fail(e, "copying index array to host");
   return GDN_OK;
 }
 
@@ -327,10 +258,10 @@ gdn_status gdn_kv_create(const gdn_kv_desc *desc, void *k_codes, void *v_codes,
     delete c;
     return fail(GDN_ERR_CUDA, "encoding the tensor maps of the codes failed");
   }
-  unsigned int *err = nullptr;
-  e = cudaMalloc(&err, sizeof(*err));
+  unsigned int *err = nullptr;  // the error word, and the page calls' ticket
+  e = cudaMalloc(&err, 2 * sizeof(*err));
   if (e == cudaSuccess) {
-    e = cudaMemset(err, 0, sizeof(*err));
+    e = cudaMemset(err, 0, 2 * sizeof(*err));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) cudaFree(err);
   }

@@ -541,6 +541,116 @@ gdn_status gdn_kv_attend(gdn_kv *kv, int32_t layer, const int32_t *slot_ids,
                          const void *q, int64_t ld_q, gdn_dtype q_dtype, void *o, int64_t ld_o,
                          gdn_dtype o_dtype, float scale, gdn_stream stream);
 
+/* ---- pages of the KV cache, handed out on the GPU ----
+ *
+ * The pages that no slot holds are a stack in device memory, and a count per
+ * slot says how many it holds: with them the page table can grow and shrink on
+ * the stream, by the lengths that are there, without the host knowing either.
+ *   page_table  [n_slots][max_pages]  the cache's own (the same address)
+ *   held        [n_slots]   the slot's pages: page_table[slot][0 .. held)
+ *   free_pages  [n_pages]   page ids; free_pages[0 .. *n_free) are free
+ *   n_free      [1]
+ * All four are plain caller memory, to be set before the first call: held 0, every
+ * page id once in free_pages, *n_free = n_pages (or fewer, with pages that
+ * the caller gave to slots itself counted in held).  The two calls below change
+ * them in the order of their stream; calls on different streams on one set must be
+ * ordered by the caller (events).  Pages that several slots share (a common
+ * prefix) are the caller's: trim those slots to no less than the shared pages, and
+ * take these out of table and held by itself. */
+typedef struct {
+  int32_t *page_table;
+  int32_t *held;
+  int32_t *free_pages;
+  int32_t *n_free;
+} gdn_kv_pages;
+
+/* Pages for new tokens, and where the tokens go.  Sequence i is tokens
+ * cu_seqlens[i] .. cu_seqlens[i+1]-1 (cu_seqlens == NULL: one token each) at
+ * positions pos[i], pos[i] + 1, ... of slot slot_ids[i], as in gdn_kv_append,
+ * which may follow on the stream.  With len tokens (len > 0) it needs
+ *     need = max(0, ceil((pos + len) / page_tokens) - held[slot])
+ * pages.  Sequences are served in their order: those with need 0 always, the
+ * others while the sum of all needs so far fits *n_free.  One that is served
+ * takes its pages from the end of free_pages, in order, into
+ * page_table[slot][held ...]; one that is not keeps what it has.
+ *   positions  [total_tokens] int32   position of each token in its slot
+ *   rows       [total_tokens] int64   its row of the cache, page * page_tokens +
+ *              pos % page_tokens (the same in every layer and head); -1 where the
+ *              sequence is not served or its page is invalid (GDN_DEVERR_PAGE)
+ *   granted    [n_seqs] int32         1: served, 0: not
+ * each of them NULL if not wanted.  Tokens before cu_seqlens[0], after the last
+ * sequence or of a malformed range are not written (where cu_seqlens decreases, it
+ * is not specified which of the tokens that two sequences claim are).  Skipped as
+ * never asked for, with granted 0, positions and rows -1: entries with a slot out of range or named twice in the call
+ * (GDN_DEVERR_SLOT), with a malformed token range or one that does not fit
+ * [0, max_pages * page_tokens) (GDN_DEVERR_SEQ), or whose held is outside
+ * [0, max_pages] (GDN_DEVERR_PAGE).  An impossible *n_free counts as 0
+ * (GDN_DEVERR_PAGE).  Needs no workspace; one launch. */
+gdn_status gdn_kv_pages_grow(gdn_kv *kv, const gdn_kv_pages *pages, const int32_t *slot_ids,
+                             const int32_t *pos, const int32_t *cu_seqlens, int32_t n_seqs,
+                             int32_t total_tokens, int32_t *positions, int64_t *rows,
+                             int32_t *granted, gdn_stream stream);
+
+/* Give back the pages that the first lens[i] tokens of slot slot_ids[i] do not
+ * use: 0 when a request ends, less than before when drafts were rejected.  Their
+ * table entries become -1.  The pages go to the end of free_pages such that a
+ * gdn_kv_pages_grow of the same sequences finds the same pages in the same
+ * places.  Skipped: as above, and negative lengths (GDN_DEVERR_SEQ).  A call after
+ * which more than n_pages pages were free changes nothing (GDN_DEVERR_PAGE). */
+gdn_status gdn_kv_pages_trim(gdn_kv *kv, const gdn_kv_pages *pages, const int32_t *slot_ids,
+                             const int32_t *lens, int32_t n_seqs, gdn_stream stream);
+
+/* ---- rotary positions ----
+ *
+ * The queries and keys of an attention layer carry their position as a rotation:
+ * in the first `rot` elements of each head (a part of it, or all), pair j of
+ * rot / 2 is turned by the angle p * theta_j at position p,
+ *     a' = s (a cos - b sin),   b' = s (b cos + a sin),
+ * with (a, b) = elements (j, j + rot/2) or (2j, 2j + 1).  The frequencies are
+ *     theta_j = base^(-2j / rot),
+ * and, to reach contexts longer than the model was trained on,
+ *   - divided by factor (original_len == 0; factor 1: as they are), or
+ *   - by their turns n_j = theta_j original_len / 2 pi within the original
+ *     length: theta_j (m + (1 - m) / factor), m = (n_j - low_turns) /
+ *     (high_turns - low_turns) cut to [0, 1]; fast pairs keep their frequency,
+ *     slow ones are stretched.
+ * s = out_scale multiplies what is rotated (1, or an attention temperature).
+ * Angles are reduced modulo a turn without loss: they are as good as theta_j in 64
+ * bits, off by |p| 2^-52 of a turn at most. */
+typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
+
+typedef struct {
+  int32_t d;             /* head dim: even, 2 .. 4096 */
+  int32_t rot;           /* elements that are rotated: even, 2 .. min(d, 512) */
+  gdn_rope_layout layout;
+  double base;
+  double factor;
+  int64_t original_len;
+  double low_turns, high_turns;
+  float out_scale;
+  int32_t host_checks;   /* nonzero: check that pointers are device-accessible */
+} gdn_rope_desc;
+
+typedef struct gdn_rope_plan gdn_rope_plan;
+
+/* The plan holds the frequencies, in host memory: it belongs to no device, and
+ * calls on it may run at once on any streams and from any threads. */
+gdn_status gdn_rope_create(const gdn_rope_desc *desc, gdn_rope_plan **out);
+gdn_status gdn_rope_destroy(gdn_rope_plan *plan);
+
+/* Rotate q [tokens][h_q][d] into q_out and k [tokens][h_k][d] into k_out, all in
+ * dtype (GDN_F32 or GDN_BF16; float32 inside, rounded once), token strides ld_*
+ * elements (0: packed).  positions: [tokens] int32, any values (negative ones turn
+ * back: the inverse, for out_scale 1, and the gradient's rotation).  In place where
+ * q_out == q (with the same stride); otherwise the rows must not overlap, and
+ * the elements behind `rot` are copied.  h_q or h_k may be 0 (its pointers are not
+ * looked at).  Pointers aligned to their elements; rows, heads and rot / 2 that are
+ * multiples of 16 bytes are fastest. */
+gdn_status gdn_rope(const gdn_rope_plan *plan, int32_t tokens, const int32_t *positions,
+                    const void *q, int64_t ld_q, int32_t h_q, const void *k, int64_t ld_k,
+                    int32_t h_k, void *q_out, int64_t ld_q_out, void *k_out, int64_t ld_k_out,
+                    gdn_dtype dtype, gdn_stream stream);
+
 /* Human-readable name of a status, and the detail of the last failure on
  * this host thread (empty string if none). */
 const char *gdn_status_string(gdn_status s);
