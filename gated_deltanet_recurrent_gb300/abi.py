@@ -20,7 +20,7 @@ GDN_F32, GDN_BF16, GDN_F16 = 0, 1, 2
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_ARG", 2: "GDN_ERR_SLOT", 3: "GDN_ERR_DUP_SLOT",
           4: "GDN_ERR_DTYPE", 5: "GDN_ERR_SIZE", 6: "GDN_ERR_UNSUPPORTED", 7: "GDN_ERR_CUDA"}
 DEVERR_SLOT, DEVERR_SEQ, DEVERR_COUNT, DEVERR_TIMEOUT = 1, 2, 4, 8
-DEVERR_PAGE, DEVERR_VALUE = 16, 32
+DEVERR_PAGE, DEVERR_VALUE, DEVERR_ADAPTER = 16, 32, 64
 GDN_KV_I8, GDN_KV_E4M3 = 0, 1
 GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
 TEST_DECODE_WAIT_TIMEOUT = 1
@@ -38,6 +38,7 @@ EXPORTED = ("gdn_pool_state_bytes", "gdn_pool_conv_bytes", "gdn_pool_create", "g
             "gdn_kv_get_error", "gdn_kv_set_test_flags", "gdn_kv_append", "gdn_kv_read",
             "gdn_kv_attend", "gdn_kv_pages_grow", "gdn_kv_pages_trim",
             "gdn_rope_create", "gdn_rope_destroy", "gdn_rope",
+            "gdn_adapters_create", "gdn_adapters_destroy", "gdn_in_proj_adapted",
             "gdn_status_string",
             "gdn_last_error_message")
 
@@ -82,6 +83,12 @@ class gdn_rope_desc(ctypes.Structure):
                 ("base", ctypes.c_double), ("factor", ctypes.c_double),
                 ("original_len", ctypes.c_int64), ("low_turns", ctypes.c_double),
                 ("high_turns", ctypes.c_double), ("out_scale", ctypes.c_float),
+                ("host_checks", ctypes.c_int32)]
+
+
+class gdn_adapters_desc(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("hidden", ctypes.c_int32), ("n_out", ctypes.c_int32),
                 ("host_checks", ctypes.c_int32)]
 
 
@@ -145,6 +152,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "gdn_rope_create": (st, [P(gdn_rope_desc), P(vp)]),
         "gdn_rope_destroy": (st, [vp]),
         "gdn_rope": (st, [vp, i32, vp, vp, i64, i32, vp, i64, i32, vp, i64, vp, i64, st, vp]),
+        "gdn_adapters_create": (st, [P(gdn_adapters_desc), vp, i64, vp, i64, vp, P(vp)]),
+        "gdn_adapters_destroy": (st, [vp]),
+        "gdn_in_proj_adapted": (st, [vp, vp, i64, vp, i64, vp, i64, vp, vp, i64, st, vp]),
         "gdn_status_string": (ctypes.c_char_p, [st]),
         "gdn_last_error_message": (ctypes.c_char_p, []),
     }
@@ -908,6 +918,8 @@ def gdn_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor],
     if positions.dtype != torch.int32 or not positions.is_contiguous() or \
             device.type != "cuda":
         raise GDNError(1, "positions must be a contiguous int32 tensor on the GPU")
+    if tokens == 0:
+        return q if q_out is None else q_out, k if k_out is None else k_out
     q_ptr = q_to = k_ptr = k_to = None
     ld_q = h_q = ld_q_to = ld_k = h_k = ld_k_to = 0
     if q is not None:
@@ -919,3 +931,104 @@ def gdn_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor],
     if status:
         _check(status)
     return q if q_out is None else q_out, k if k_out is None else k_out
+
+
+# ------------------------------------- low-rank adapters beside the projection
+
+class Adapters:
+    """The low-rank adapters of one projection: a [n, rank, hidden] and b [n, n_out, rank] bf16,
+    scale [n] float32 (default: ones), rank <= 128.  Rows start 16-byte aligned; those of one
+    adapter follow the other's.  The tensors may be rewritten between calls."""
+
+    def __init__(self, a, b, scale=None, host_checks=False):
+        if a.dtype != torch.bfloat16 or b.dtype != torch.bfloat16:
+            raise GDNError(4, "a and b must be bf16")
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise GDNError(5, "a must be [n, rank, hidden] and b [n, n_out, rank]")
+        n, self.rank, self.hidden = a.shape
+        self.n_out = b.shape[1]
+        if scale is None:
+            scale = torch.ones(n, dtype=torch.float32, device=a.device)
+        if scale.dtype != torch.float32 or scale.shape != (n,) or not scale.is_contiguous():
+            raise GDNError(1, f"scale must be contiguous float32 [{n}]")
+        if b.device != a.device or scale.device != a.device:
+            raise GDNError(1, "a, b and scale must be on one device")
+        lds = []
+        for name, t in (("a", a), ("b", b)):
+            rows, width = t.shape[1], t.shape[2]
+            ld = t.stride(1) if rows > 1 else t.stride(0) if n > 1 else width
+            if (width > 1 and t.stride(2) != 1) or ld < width or \
+                    (n > 1 and t.stride(0) != rows * ld):
+                raise GDNError(1, f"{name}: one row stride for all rows needed, and unit column "
+                                  f"stride (strides {t.stride()})")
+            lds.append(ld)
+        self.a, self.b, self.scale = a, b, scale
+        self.desc = gdn_adapters_desc(n, self.rank, self.hidden, self.n_out,
+                                      1 if host_checks else 0)
+        self.handle = gdn_adapters_create(self.desc, a, lds[0], b, lds[1], scale)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            gdn_adapters_destroy(self)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def gdn_adapters_create(desc: gdn_adapters_desc, a, ld_a, b, ld_b, scale):
+    out = ctypes.c_void_p()
+    _check(load_library().gdn_adapters_create(ctypes.byref(desc), _ptr(a), ld_a, _ptr(b), ld_b,
+                                              _ptr(scale), ctypes.byref(out)))
+    return out
+
+
+def gdn_adapters_destroy(adapters: Adapters):
+    _check(load_library().gdn_adapters_destroy(adapters.handle))
+
+
+def _proj_rows(t, rows, width, device, name):
+    """Row stride of t [rows, width] with unit column stride (0: one row or none)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] != width:
+        raise GDNError(5, f"{name} must be [{rows}, {width}], got {tuple(shape)}")
+    if t.device != device:
+        raise GDNError(1, f"{name} must be on the adapters' device")
+    if rows == 0:
+        return 0
+    if stride[1] != 1 and width > 1:
+        raise GDNError(1, f"{name} must have a unit column stride (strides {stride})")
+    if rows <= 1:
+        return 0
+    if stride[0] < width:  # an expanded row (stride 0) is not the library's "packed" (0)
+        raise GDNError(1, f"{name}: row stride {stride[0]} smaller than a row of {width}")
+    return stride[0]
+
+
+def gdn_in_proj_adapted(pool: Pool, adapters: Adapters, x: torch.Tensor, w: torch.Tensor,
+                        ids: torch.Tensor, y: Optional[torch.Tensor] = None, stream=None):
+    """y[t] = W x[t] + scale[a] B[a] (A[a] x[t]) with a = ids[t] (-1: none): x [tokens, hidden]
+    and w [n_out, hidden] bf16, ids [tokens] int32, y [tokens, n_out] float32 or bf16 (default
+    float32)."""
+    tokens, device = ids.numel(), adapters.a.device
+    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+        raise GDNError(4, "x and w must be bf16")
+    if ids.dtype != torch.int32 or not ids.is_contiguous() or ids.device != device:
+        raise GDNError(1, "ids must be a contiguous int32 tensor on the adapters' device")
+    ld_x = _proj_rows(x, tokens, adapters.hidden, device, "x")
+    ld_w = _proj_rows(w, adapters.n_out, adapters.hidden, device, "w")
+    if y is None:
+        y = torch.empty(tokens, adapters.n_out, dtype=torch.float32, device=device)
+    ld_y = _proj_rows(y, tokens, adapters.n_out, device, "y")
+    if tokens <= 1:  # the stride of a single row says nothing, and has to be aligned
+        ld_y = -(-adapters.n_out // 8) * 8
+        ld_x = -(-adapters.hidden // 8) * 8
+    status = _lib.gdn_in_proj_adapted(pool.handle, adapters.handle, tokens, x.data_ptr(), ld_x,
+                                      w.data_ptr(), ld_w, ids.data_ptr(), y.data_ptr(), ld_y,
+                                      _kv_dtype(y), _kv_stream(stream, ids))
+    if status:
+        _check(status)
+    return y

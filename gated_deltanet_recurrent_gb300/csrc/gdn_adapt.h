@@ -1,0 +1,25 @@
+// What the projection with adapters needs: shared by its entry point and its kernels.
+#pragma once
+
+#include "gdn_internal.h"
+
+namespace gdn {
+
+struct AdaptArgs {
+  const void *x, *w, *a, *b;  // bf16: x [tokens][hidden], w [n_out][hidden], a [n_adapters][rank]
+                              // [hidden], b [n_adapters][n_out][rank]
+  const float *scale;         // [n_adapters]
+  const int32_t *ids;         // [tokens]
+  void *y;                    // [tokens][n_out]
+  int64_t ld_x, ld_w, ld_a, ld_b, ld_y;
+  int tokens, hidden, n_out, rank, n_adapters;
+  gdn_dtype y_dtype;
+  float *h;                   // workspace
+  unsigned int *err;
+  int sm_count, device;
+};
+
+size_t adapt_workspace_bytes(const AdaptArgs &g);
+cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s);
+
+}  // namespace gdn

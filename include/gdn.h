@@ -82,6 +82,7 @@ typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_F16 = 2 } gdn_dtype;
                                 neither written nor read, and are masked in gdn_kv_attend */
 #define GDN_DEVERR_VALUE 32u /* a non-finite key or value was appended: an infinity was stored as
                                 the largest code of its sign, a NaN as zero */
+#define GDN_DEVERR_ADAPTER 64u /* a token's adapter is outside [-1, n_adapters): it got none */
 
 /* Shape of every GDN layer in the pool.  Supported: dk in {16, 32, 64, 128},
  * dv a multiple of 4 (<= 4096), h_v a multiple of h_k, 2 <= conv_k <= 8,
@@ -650,6 +651,52 @@ gdn_status gdn_rope(const gdn_rope_plan *plan, int32_t tokens, const int32_t *po
                     const void *q, int64_t ld_q, int32_t h_q, const void *k, int64_t ld_k,
                     int32_t h_k, void *q_out, int64_t ld_q_out, void *k_out, int64_t ld_k_out,
                     gdn_dtype dtype, gdn_stream stream);
+
+/* ---- low-rank adapters beside the input projection ----
+ *
+ * Requests of one batch that use differently tuned layers: each token t has the
+ * shared projection and, where it has an adapter a = ids[t], a low-rank one beside it,
+ *     y[t] = W x[t] + scale[a] B[a] (A[a] x[t]).
+ * The adapters of a layer are one handle on caller memory (which may be rewritten, on
+ * the stream, as adapters come and go; those of smaller rank are filled up with
+ * zeros):
+ *   a      [n_adapters][rank][hidden]   bf16, row stride ld_a elements (0: hidden)
+ *   b      [n_adapters][n_out][rank]    bf16, row stride ld_b elements (0: rank)
+ *   scale  [n_adapters]                 float32
+ * the rows of one adapter following those of the other.  Rows start 16-byte aligned
+ * (so ld_b is a multiple of 8).  1 <= rank <= 128. */
+typedef struct {
+  int32_t n_adapters;
+  int32_t rank;
+  int32_t hidden;
+  int32_t n_out;
+  int32_t host_checks;  /* nonzero: check pointers, and the ids on the host (syncs) */
+} gdn_adapters_desc;
+
+typedef struct gdn_adapters gdn_adapters;
+
+/* The handle owns a memory pool with a workspace for each of the first 16 streams that
+ * it is used on, as the KV cache does (tokens * rank * 12 bytes, at most). */
+gdn_status gdn_adapters_create(const gdn_adapters_desc *desc, const void *a, int64_t ld_a,
+                               const void *b, int64_t ld_b, const float *scale,
+                               gdn_adapters **out);
+/* Synchronises the handle's device first, whichever is current.  NULL is a no-op. */
+gdn_status gdn_adapters_destroy(gdn_adapters *adapters);
+
+/* gdn_in_proj with an adapter per token: x [tokens][hidden] and w [n_out][hidden] in
+ * bf16, y [tokens][n_out] in y_dtype, strides and alignment as there; ids: [tokens]
+ * int32, -1 for none.  Tokens of one adapter need not be neighbours (decode steps),
+ * but are fastest where they are (prompts).  The low side A x is summed in float32 and
+ * multiplied by scale; it enters the second product in two bf16 parts (to 2^-16 of
+ * itself) for bf16 y and in three (2^-24) for float32 y; y is rounded once.  An adapter
+ * with values that are not finite spoils its own tokens only.  An id outside
+ * [-1, n_adapters) counts as -1 (GDN_DEVERR_ADAPTER).  The pool supplies the error
+ * word.  tokens <= 2^20.  Calls from several host threads on one handle must be
+ * serialised by the caller. */
+gdn_status gdn_in_proj_adapted(gdn_pool *pool, gdn_adapters *adapters, int64_t tokens,
+                               const void *x, int64_t ld_x, const void *w, int64_t ld_w,
+                               const int32_t *ids, void *y, int64_t ld_y, gdn_dtype y_dtype,
+                               gdn_stream stream);
 
 /* Human-readable name of a status, and the detail of the last failure on
  * this host thread (empty string if none). */
