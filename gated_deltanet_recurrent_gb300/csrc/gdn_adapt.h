@@ -14,12 +14,17 @@ struct AdaptArgs {
   int64_t ld_x, ld_w, ld_a, ld_b, ld_y;
   int tokens, hidden, n_out, rank, n_adapters;
   gdn_dtype y_dtype;
-  float *h;                   // workspace
+  float *h;                   // workspace: [tokens][rank16] = scale * A x, zeros beyond rank
   unsigned int *err;
   int sm_count, device;
+  // the rank rounded up to the tensor cores' 16
+  GDN_HD int rank16() const { return (rank + 15) & ~15; }
 };
 
 size_t adapt_workspace_bytes(const AdaptArgs &g);
+// The low side, then the projection; cudaErrorInvalidValue: no tensor map.
 cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s);
+
+cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s);
 
 }  // namespace gdn

@@ -1,0 +1,167 @@
+// The low side of the adapters: h[t] = scale[a] A[a] x[t], a = ids[t], in float32.
+//
+// Bound by the bytes of the A in use (a decode step) or of x (prompts), so the products go where the
+// data can be used without a detour: mma.sync takes both operands from registers, and those are
+// loaded straight from global memory, 16 bytes a lane.  The order of k within a product does not
+// matter, so a lane's 16 bytes -- 8 neighbours in k -- are fed to two products as they come.
+// (These products are 3 % of a prompt's; the tensor cores that read shared memory are for the
+// projection itself.)
+//
+// A CTA takes a window of 16 * MT tokens, the adapters of which it finds by comparing the ids, and
+// 8 * NT ranks; its 8 warps split the sum over k, joined in shared memory in a fixed order.  Where
+// a window may have many adapters and there are few windows, several CTAs share it (blockIdx.y), each
+// taking every gridDim.y-th adapter.
+#include "gdn_adapt.h"
+#include "gdn_common.cuh"
+#include "gdn_kv.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kWarps = 8;
+
+__device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Elements k .. k + 7 of a row, zeros from `hidden` on (what lies behind a row is not read).
+__device__ __forceinline__ uint4 load8(const bf16 *row, int k, int hidden) {
+  if (k + 8 <= hidden) return *reinterpret_cast<const uint4 *>(row + k);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (k + j < hidden)
+      w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row)[k + j] << (16 * (j & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int MT, int NT>
+__global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) low_kernel(AdaptArgs g) {
+  constexpr int kTok = 16 * MT, kRanks = 8 * NT;
+  extern __shared__ float s_part[];  // [kWarps][kTok][kRanks]
+  __shared__ int s_id[kTok], s_lead[kTok], s_n;
+  kv::dependent_wait();
+  // the projection may start loading what no kernel before this one writes
+  kv::dependents_may_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tok0 = blockIdx.x * kTok, rank0 = blockIdx.z * kRanks;
+  if (tid < kTok) {
+    int id = tok0 + tid < g.tokens ? g.ids[tok0 + tid] : -1;
+    if (id < -1 || id >= g.n_adapters) {
+      if (blockIdx.y + blockIdx.z == 0) raise_error(g.err, GDN_DEVERR_ADAPTER);
+      id = -1;
+    }
+    s_id[tid] = id;
+  }
+  __syncthreads();
+  if (warp == 0) {  // the window's adapters, in the order of their first tokens
+    int n = 0;
+    for (int base = 0; base < kTok; base += 32) {
+      const int i = base + lane;
+      bool lead = i < kTok && s_id[i < kTok ? i : 0] >= 0;
+      for (int j = 0; j < kTok; ++j) lead = lead && !(j < i && s_id[j] == s_id[i]);
+      const uint32_t m = __ballot_sync(0xffffffffu, lead);
+      if (lead) s_lead[n + __popc(m & ((1u << lane) - 1))] = s_id[i];
+      n += __popc(m);
+    }
+    if (lane == 0) s_n = n;
+  }
+  __syncthreads();
+  const int row = lane >> 2, col = lane & 3;
+  const bf16 *x = static_cast<const bf16 *>(g.x);
+  const int ld_h = g.rank16();
+  for (int gi = blockIdx.y; gi < s_n; gi += gridDim.y) {
+    const int id = s_lead[gi];
+    const bf16 *a = static_cast<const bf16 *>(g.a) + (int64_t)id * g.rank * g.ld_a;
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
+    // 64 k a step: two loads of 16 bytes per row and lane
+#pragma unroll(MT == 1 ? 2 : 1)
+    for (int k0 = 64 * warp; k0 < g.hidden; k0 += 64 * kWarps) {
+      uint4 xv[MT][2][2], av[NT][2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int k = k0 + 32 * c + 8 * col;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int r = rank0 + 8 * n + row;
+          av[n][c] = r < g.rank ? load8(a + r * g.ld_a, k, g.hidden) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            // (a row behind the last token: any row, its result is dropped)
+            const int t = min(tok0 + 16 * m + 8 * hh + row, g.tokens - 1);
+            xv[m][hh][c] = load8(x + t * g.ld_x, k, g.hidden);
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint4 u = xv[m][0][c], v = xv[m][1][c];
+          const uint32_t f0[4] = {u.x, v.x, u.y, v.y}, f1[4] = {u.z, v.z, u.w, v.w};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816(acc[m][n], f0, av[n][c].x, av[n][c].y);
+            mma16816(acc[m][n], f1, av[n][c].z, av[n][c].w);
+          }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+          *reinterpret_cast<float2 *>(
+              &s_part[(warp * kTok + 16 * m + 8 * hh + row) * kRanks + 8 * n + 2 * col]) =
+              make_float2(acc[m][n][2 * hh], acc[m][n][2 * hh + 1]);
+    __syncthreads();
+    const float scale = g.scale[id];
+    for (int i = tid; i < kTok * kRanks; i += 32 * kWarps) {
+      const int t = i / kRanks, r = rank0 + i % kRanks;
+      if (s_id[t] != id || r >= ld_h) continue;
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += s_part[w * kTok * kRanks + i];
+      // (zeros beyond the rank, whatever the scale is)
+      g.h[(int64_t)(tok0 + t) * ld_h + r] = r < g.rank ? sum * scale : 0.f;
+    }
+    __syncthreads();
+  }
+}
+
+template <int MT, int NT>
+cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
+  constexpr int smem = kWarps * 16 * MT * 8 * NT * 4;
+  static std::atomic<uint64_t> seen{0};
+  const cudaError_t e = kv::allow_smem(low_kernel<MT, NT>, smem, g.device, seen);
+  if (e != cudaSuccess) return e;
+  const int windows = (g.tokens + 16 * MT - 1) / (16 * MT);
+  const int parts = (g.rank16() + 8 * NT - 1) / (8 * NT);
+  // CTAs that share a window: as many as it may have adapters, but no more than four waves in all
+  const int64_t room = (int64_t)4 * g.sm_count / ((int64_t)windows * parts);
+  const int share = (int)(room < 1 ? 1 : room > 16 * MT ? 16 * MT : room);
+  return kv::launch(low_kernel<MT, NT>, dim3((unsigned)windows, (unsigned)share, (unsigned)parts),
+                    32 * kWarps, smem, s, 1, g);
+}
+
+}  // namespace
+
+cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s) {
+  // few tokens: small windows, for parallel loads of A; many: large ones, that read A less often
+  return g.tokens <= 256 ? launch<1, 2>(g, s) : launch<4, 4>(g, s);
+}
+
+}  // namespace gdn
