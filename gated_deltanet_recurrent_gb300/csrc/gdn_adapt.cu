@@ -1,36 +1,36 @@
 // The input projection with a low-rank adapter per token:
 //     y[t] = W x[t] + scale[a] B[a] (A[a] x[t]),   a = ids[t]   (W x[t] alone where ids[t] = -1).
 //
-// gdn_adapt_low.cu has computed h[t] = scale[a] A[a] x[t]; here both products meet in one
-// accumulator, so that y is rounded and written once.
+// gdn_adapt_low.cu has computed h[t] = scale[a] A[a] x[t] and split it into bf16 parts whose sum it is
+// (two for a bf16 y, which leave 2^-16 of h, three for a float32 y, 2^-24); here y is formed from both
+// products and rounded and written once.
 //
-// The tile is 128 outputs x BT tokens, the transpose of the plain projection's: W and B[a] are the
-// M operand, x and h the N operand.  So few tokens make narrow tiles instead of empty rows, and the
-// tokens that share an adapter (a group) are columns: its product needs only the pieces of 16
-// columns that hold some of them, with zero rows in h for tokens that belong to others.  A unit is
-// one group's B[a] tile of KW ranks with those rows of h, split into bf16 parts (two for a bf16 y,
-// which leave 2^-16 of h, three for a float32 y, 2^-24).  The units have their own accumulator:
-// products into one place run in the order of issue only if they have one shape.
+// The tile is 128 outputs x BT tokens, the transpose of the plain projection's: W is the M operand
+// and x the N operand, so that few tokens make narrow tiles instead of empty rows.
 //
-//   warp 0      one lane: TMA of W and x tiles (a ring of k-blocks of 64) and of B tiles (a ring of
-//               units)
-//   warp 1      one lane: tcgen05.mma; the units are spread over the second half of the k-blocks,
-//               at fixed places (the order of the sum is fixed)
-//   warps 2..5  epilogue: thread = output row, from TMEM to y
-//   warps 6..9  find the groups; then a warp per unit: h rows to shared memory, and a look at the B
-//               tile: elements that are not finite would spoil other tokens of the range (0 * inf),
-//               so they are taken out, and their products added in the epilogue to the tokens
-//               that they belong to
+//   warp 0      one lane: TMA of W and x tiles, a ring of k-blocks of 64
+//   warp 1      one lane: tcgen05.mma into the tile's accumulator in TMEM
+//   warps 2..9  the adapters' part of mixed tiles, then the epilogue
+//
+// Where all tokens of a tile have one adapter (prompts), its part is a few more k-blocks: B tiles for
+// W's and the parts of h for x's.  Other tiles are mixed.  There a warp has 16 output rows and takes
+// the tokens eight at a time: for each adapter among the eight, mma.sync of its 16 rows of B, straight
+// from global memory to registers (several steps ahead), with the eight columns of h, of which it
+// keeps those of the adapter's own tokens.  So the cost goes by tokens and hardly by adapters, and
+// the work is beside the tensor core's that does W x.  The result goes to TMEM columns of its own (the
+// fragment is the 16x256b shape of tcgen05.st), where the epilogue adds it.  Either way nothing of one
+// request's adapter, be it infinite, meets another request's tokens.
 //
 // A decode step is bound by the bytes of W and of the B in use.  With fewer tiles than SMs, the CTAs
-// of a cluster split the k-blocks and the units of a tile and add their parts through
-// distributed shared memory, in a fixed order.  The kernel starts under the low side's (it
-// waits for h only), so W is on its way early.  Every wait is bounded (GDN_DEVERR_TIMEOUT).
+// of a cluster split the k-blocks and the tokens' eights of a tile and add their parts through
+// distributed shared memory, in a fixed order.  The kernel starts under the low side's: W is on its
+// way, and B asked into L2, before h is complete.  Every wait is bounded (GDN_DEVERR_TIMEOUT).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include "gdn_adapt.h"
 #include "gdn_kv.cuh"
+#include "gdn_mma.cuh"
 #include "gdn_tc.cuh"
 
 namespace gdn {
@@ -38,28 +38,21 @@ namespace {
 
 constexpr int kBM = 128, kBK = 64;
 constexpr int kThreads = 320;
-constexpr int kBuilders = 4;  // warps
 constexpr int kTileW = kBM * kBK * 2;
 
-template <int BT, int KW, typename TO>
+template <int BT, typename TO>
 struct Cfg {
   static constexpr int kParts = sizeof(TO) == 4 ? 3 : 2;
+  // The tensor core cuts its sums off: one accumulator over K = 2048 is 2e-6 off, three that take
+  // the k-blocks in turn a third of that, which a bf16 y would not show.
+  static constexpr int kAcc = sizeof(TO) == 4 ? 3 : 1;
+  static constexpr uint32_t kTmem = (kAcc + 1) * BT;  // the adapters' columns are the last
+  // two CTAs per SM where their registers (100 a thread) and columns suffice
+  static constexpr bool kTwo = sizeof(TO) == 2;
   static constexpr int kStage = kTileW + BT * kBK * 2;
-  static constexpr int kPitch = KW * 2;                  // bytes of a row of a unit's operands
-  static constexpr int kTileB = kBM * kPitch;
-  static constexpr int kTileH = BT * kPitch;             // one part
-  static constexpr int kSlot = kTileB + kParts * kTileH;
-  // two CTAs per SM, but for wide units and wide tiles
-  static constexpr bool kTwo = BT == 16 || (BT == 64 && KW == 16);
-  static constexpr int kRoom = (kTwo ? 112 : 225) * 1024 - 1024;
-  static constexpr int kSlots = BT == 16 ? (KW == 16 ? 6 : 2) : kTwo ? 3 : 4 - (BT == 64);
-  // warps that build units: a slot is always the same warp's, which then is never two rounds ahead
-  static constexpr int kTeam = kSlots % 4 == 0 ? 4 : kSlots % 3 == 0 ? 3 : 2;
-  static constexpr int kFit = (kRoom - kSlots * kSlot) / kStage;
+  static constexpr int kFit = ((kTwo ? 112 : 225) * 1024 - 1024) / kStage;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
-  static constexpr int kSmem = kStages * kStage + kSlots * kSlot + 1024;
-  static constexpr uint32_t kTmem = 2 * BT;  // the projection's columns, then the units'
-  static_assert(kStages >= 3 && kSlots % kTeam == 0, "rings");
+  static constexpr int kSmem = kStages * kStage + 1024;
   static_assert(BT * kBM * 4 <= kStages * kStage, "a cluster's parts take the ring's place");
 };
 
@@ -70,19 +63,6 @@ __device__ __forceinline__ void tma_load2(void *dst, const CUtensorMap *m, int x
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
-}
-
-// K-major operand with rows of `pitch` bytes (32, 64 or 128) in the swizzle of that width
-template <int PITCH>
-__device__ __forceinline__ uint64_t operand(uint32_t saddr) {
-  constexpr uint64_t kMode = PITCH == 128 ? 2 : PITCH == 64 ? 4 : 6;
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) |
-         ((uint64_t)((8 * PITCH) >> 4) << 32) | ((uint64_t)1 << 46) | (kMode << 61);
-}
-// where the swizzle puts byte `off` of such a tile
-template <int PITCH>
-__device__ __forceinline__ uint32_t swizzled(uint32_t off) {
-  return off ^ (((off >> 7) & (PITCH / 16 - 1)) << 4);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -109,18 +89,16 @@ __device__ __forceinline__ int ld_peer_int(uint32_t a) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
-// (try_wait may suspend the thread for a while; a producer of two rings must not)
-__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+// 16 lanes x 8 columns of TMEM from an mma.sync result (its m16n8 fragment)
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const float *d) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(__float_as_uint(d[0])), "r"(__float_as_uint(d[1])), "r"(__float_as_uint(d[2])),
+               "r"(__float_as_uint(d[3]))
+               : "memory");
 }
 
 // A bounded wait that also ends when the CTA gives up.
@@ -132,197 +110,207 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
   return false;
 }
 
-// The groups of a tile: tokens that share an adapter.
+// Elements r .. r + 3 of a row of B, zeros from `rank` on (what lies behind a row is not read).
+__device__ __forceinline__ uint2 load4(const bf16 *row, int r, int rank) {
+  if (r + 4 <= rank) return *reinterpret_cast<const uint2 *>(row + r);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (r + j < rank)
+      w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row)[r + j] << (16 * (j & 1));
+  return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ int token_id(const AdaptArgs &g, int t) {
+  const int id = t < g.tokens ? g.ids[t] : -1;
+  return id >= 0 && id < g.n_adapters ? id : -1;
+}
+
+// The adapters that each eight tokens of a mixed tile have, in order; an eight without any is one
+// entry too.
 template <int BT>
-struct Groups {
-  int id[BT];             // per token: its adapter, or -1
-  int adapter[BT];        // per group
-  unsigned short pieces[BT];  // bit p: tokens 16 p .. 16 p + 15 hold some of it
-  int n;
-  unsigned int bad[BT * 8 / 32];  // units (group * chunks + chunk) with elements that are not finite
-  int any_bad;
+struct Tasks {
+  struct {
+    int id;               // -1: none
+    unsigned char eight;  // tokens 8 eight .. of the tile
+    unsigned char mask;   // those of them that have this adapter
+    unsigned char last;   // of the eight
+  } task[BT];
+  int count[BT / 8], n;
 };
 
-// Run by the builder warps.  ids of tokens tok0 ..; kernels before this one wrote them.
+// Run by the 8 warps of the adapters' part, for the eights e = part, part + splits, ...
 template <int BT>
-__device__ __forceinline__ void find_groups(const AdaptArgs &g, int tok0, Groups<BT> &s, int *counts) {
-  const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
-  if (tid < BT) {
-    int id = tok0 + tid < g.tokens ? g.ids[tok0 + tid] : -1;
-    if (id < 0 || id >= g.n_adapters) id = -1;
-    s.id[tid] = id;
-  }
-  for (int i = tid; i < BT * 8 / 32; i += 128) s.bad[i] = 0;
-  asm volatile("bar.sync 1, 128;" ::: "memory");
-  const int id = tid < BT ? s.id[tid] : -1;
-  bool lead = id >= 0;
-  unsigned pieces = 0;
-  if (lead) {
-    for (int j = 0; j < BT; ++j) {
-      if (s.id[j] != id) continue;
-      if (j < tid) lead = false;
-      pieces |= 1u << (j >> 4);
-    }
-  }
-  const uint32_t m = __ballot_sync(0xffffffffu, lead);
-  if (lane == 0) counts[warp] = __popc(m);
-  asm volatile("bar.sync 1, 128;" ::: "memory");
-  int at = __popc(m & ((1u << lane) - 1)), n = 0;
-#pragma unroll
-  for (int w = 0; w < kBuilders; ++w) {
-    if (w < warp) at += counts[w];
-    n += counts[w];
-  }
-  if (lead) {
-    s.adapter[at] = id;
-    s.pieces[at] = (unsigned short)pieces;
-  }
-  if (tid == 0) s.n = n, s.any_bad = 0;
-  asm volatile("bar.sync 1, 128;" ::: "memory");
-}
-
-// Eight elements of h as PARTS bf16 vectors whose sum they are.
-template <int PARTS>
-__device__ __forceinline__ void split8(const float *h, uint4 *out) {
-  float rest[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) rest[e] = h[e];
-#pragma unroll
-  for (int p = 0; p < PARTS; ++p) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(rest[2 * j], rest[2 * j + 1]);
-      w[j] = *reinterpret_cast<const uint32_t *>(&b);
-      const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xffff0000u);
-      // (what is infinite or NaN is the first part alone)
-      rest[2 * j] = fabsf(lo) < INFINITY ? rest[2 * j] - lo : 0.f;
-      rest[2 * j + 1] = fabsf(hi) < INFINITY ? rest[2 * j + 1] - hi : 0.f;
-    }
-    out[p] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-
-// One warp: the rows of h of a unit, columns [k0, k0 + KW), into the operand tiles at `dst`: the
-// group's pieces, zeros for other tokens.
-template <int BT, int KW, int PARTS>
-__device__ __forceinline__ void build_rows(const AdaptArgs &g, const Groups<BT> &s, int group,
-                                           int tok0, int k0, unsigned char *dst) {
-  constexpr int kPer = KW / 8, kRows = 32 / kPer;  // lanes per row, rows per pass
-  constexpr int kPasses = BT / kRows, kAhead = kPasses < 4 ? kPasses : 4;
-  const int lane = threadIdx.x & 31, sub = lane % kPer, row = lane / kPer;
-  const int id = s.adapter[group], ld = g.rank16();
-  const unsigned pieces = s.pieces[group];
-  const bool in = k0 + 8 * sub < ld;
-  for (int p0 = 0; p0 < kPasses; p0 += kAhead) {
-    float4 u[kAhead], v[kAhead];  // the loads of several passes are on their way at once
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int r = (p0 + i) * kRows + row;
-      u[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (in && s.id[r] == id) {
-        const float4 *h =
-            reinterpret_cast<const float4 *>(g.h + (int64_t)(tok0 + r) * ld + k0 + 8 * sub);
-        u[i] = h[0], v[i] = h[1];
+__device__ __forceinline__ void list_tasks(const AdaptArgs &g, int tok0, int live, int part,
+                                           int splits, Tasks<BT> &s) {
+  const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
+  const int eights = (live + 7) / 8;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int e = warp; e < eights; e += 8) {
+      const int id = lane < 8 ? token_id(g, tok0 + 8 * e + lane) : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, id);
+      const bool lead = e % splits == part && id >= 0 && __ffs(same) - 1 == lane;
+      const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+      const int n = leads ? __popc(leads) : 1;
+      if (pass == 0) {
+        if (lane == 0) s.count[e] = n;
+        continue;
       }
+      int at = 0;
+      for (int i = 0; i < e; ++i) at += s.count[i];
+      if (e == eights - 1 && lane == 0) s.n = at + n;
+      const int mine = at + __popc(leads & ((1u << lane) - 1));
+      if (lead) s.task[mine] = {id, (unsigned char)e, (unsigned char)same, mine == at + n - 1};
+      if (!leads && lane == 0) s.task[at] = {-1, (unsigned char)e, 0, 1};
     }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+  }
+}
+
+// W bytes of a row of B from its element e on; PARTIAL: zeros from `rank` on (what lies behind a row
+// is not read).
+template <int W, bool PARTIAL>
+__device__ __forceinline__ void load_ranks(const bf16 *p, int e, int rank, uint32_t *out) {
+  if constexpr (PARTIAL) {
+    const uint2 v = load4(p, e, rank);
+    out[0] = v.x, out[1] = v.y;
+  } else if constexpr (W == 8) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p + e);
+    out[0] = v.x, out[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p + e);
+    out[0] = v.x, out[1] = v.y, out[2] = v.z, out[3] = v.w;
+  }
+}
+
+// One warp: the adapters' part of 16 output rows (`row0` .. of the tile) of all tasks, to the TMEM
+// columns at `delta`.  B rows and h columns meet in mma.sync with the rank as K; lane (r, c) of a
+// fragment has rows r and r + 8 of B and column r of h, in loads of W bytes (W / 2 neighbouring
+// ranks, those of W / 8 products: the order of K does not matter).  A step is NL such loads, up to
+// 64 ranks of a task; the loads of D steps are in flight.  PARTIAL: any rank (W = 8); otherwise
+// the rank is NL * 2 W, or with NL * 2 W = 64 also 128, and nothing is asked.
+template <int BT, int W, int NL, int D, bool PARTIAL, int PARTS>
+__device__ __forceinline__ void expand(const AdaptArgs &g, const Tasks<BT> &s, int n0, int row0,
+                                       int tok0, uint32_t delta) {
+  constexpr int kRanks = 2 * W, kWords = W / 4;  // ranks and words of a load
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int rank16 = g.rank16(), halves = NL * kRanks == 64 && rank16 > 64 ? 2 : 1;
+  const int steps = s.n * halves;
+  const int64_t stride = (int64_t)g.n_out * g.ld_b, part = (int64_t)g.tokens * rank16;
+  const bf16 *lo = static_cast<const bf16 *>(g.b) + min(n0 + row0 + r, g.n_out - 1) * g.ld_b,
+             *hi = static_cast<const bf16 *>(g.b) + min(n0 + row0 + r + 8, g.n_out - 1) * g.ld_b;
+  // (columns of other tokens, or behind the last: whatever their h holds, they are dropped)
+  const bf16 *h0 = static_cast<const bf16 *>(g.h) + (int64_t)(tok0 + r) * rank16 + c * (W / 2);
+  uint32_t b[D][NL][2][kWords], h[D][NL][PARTS][kWords];
+  auto load = [&](int d, int i) {
+    if (i >= steps) return;
+    const auto t = s.task[i >> (halves - 1)];
+    if (t.id < 0) return;
+    const int k0 = 64 * (i & (halves - 1));
+    const int64_t at = t.id * stride;
+    const bf16 *hp = h0 + 8 * t.eight * rank16 + k0;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int r = (p0 + i) * kRows + row;
-      if (!(pieces >> (r >> 4) & 1)) continue;
-      const float e[8] = {u[i].x, u[i].y, u[i].z, u[i].w, v[i].x, v[i].y, v[i].z, v[i].w};
-      uint4 part[PARTS];
-      split8<PARTS>(e, part);
-      const uint32_t off = swizzled<2 * KW>((uint32_t)(r * 2 * KW + sub * 16));
+    for (int l = 0; l < NL; ++l) {
+      if (PARTIAL && k0 + kRanks * l >= rank16) break;
+      const int e = k0 + kRanks * l + c * (W / 2);
+      load_ranks<W, PARTIAL>(lo + at, e, g.rank, b[d][l][0]);
+      load_ranks<W, PARTIAL>(hi + at, e, g.rank, b[d][l][1]);
 #pragma unroll
       for (int p = 0; p < PARTS; ++p)
-        *reinterpret_cast<uint4 *>(dst + p * BT * 2 * KW + off) = part[p];
+        load_ranks<W, false>(hp + p * part, kRanks * l, 0, h[d][l][p]);
     }
-  }
-}
-
-// One warp: takes infinities and NaN out of a B tile; true if there were any.
-template <int BYTES>
-__device__ __forceinline__ bool take_out(unsigned char *tile) {
-  const int lane = threadIdx.x & 31;
-  bool any = false;
-#pragma unroll 4
-  for (int i = lane * 16; i < BYTES; i += 512) {
-    uint4 *p = reinterpret_cast<uint4 *>(tile + i);
-    uint4 v = *p;
-    const uint32_t a = __vcmpeq2(v.x & 0x7f807f80u, 0x7f807f80u),
-                   b = __vcmpeq2(v.y & 0x7f807f80u, 0x7f807f80u),
-                   c = __vcmpeq2(v.z & 0x7f807f80u, 0x7f807f80u),
-                   d = __vcmpeq2(v.w & 0x7f807f80u, 0x7f807f80u);
-    if (a | b | c | d) {
-      any = true;
-      *p = make_uint4(v.x & ~a, v.y & ~b, v.z & ~c, v.w & ~d);
-    }
-  }
-  return __any_sync(0xffffffffu, any);
-}
-
-// The products that take_out left out, of output row n and token i of the tile.
-template <int BT, int KW>
-__device__ __noinline__ float put_back(const AdaptArgs &g, const Groups<BT> &s, int tok0, int i,
-                                       int n) {
-  float sum = 0.f;
-  const int chunks = (g.rank16() + KW - 1) / KW;
-  for (int gr = 0; gr < s.n; ++gr) {
-    if (s.adapter[gr] != s.id[i]) continue;
-    const bf16 *b = static_cast<const bf16 *>(g.b) + ((int64_t)s.id[i] * g.n_out + n) * g.ld_b;
-    const float *h = g.h + (int64_t)(tok0 + i) * g.rank16();
-    for (int c = 0; c < chunks; ++c) {
-      const int u = gr * chunks + c;
-      if (!(s.bad[u >> 5] >> (u & 31) & 1)) continue;
-      for (int r = c * KW; r < min((c + 1) * KW, g.rank); ++r) {
-        const float v = __bfloat162float(b[r]);
-        if (!(fabsf(v) < INFINITY)) sum += v * h[r];
+  };
+  float out[4], acc[PARTS][4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[e] = 0.f;
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, d);
+  for (int i0 = 0; i0 < steps; i0 += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int i = i0 + d;
+      if (i >= steps) break;
+      const auto t = s.task[i >> (halves - 1)];
+      const int half = i & (halves - 1), k0 = 64 * half;
+      if (t.id >= 0) {
+        if (half == 0)
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[p][e] = 0.f;
+#pragma unroll
+        for (int l = 0; l < NL; ++l) {
+          if (PARTIAL && k0 + kRanks * l >= rank16) break;
+#pragma unroll
+          for (int w = 0; w < kWords; w += 2) {
+            const uint32_t a[4] = {b[d][l][0][w], b[d][l][1][w], b[d][l][0][w + 1],
+                                   b[d][l][1][w + 1]};
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) mma16816(acc[p], a, h[d][l][p][w], h[d][l][p][w + 1]);
+          }
+        }
+      }
+      load(d, i + D);
+      if (half + 1 < halves) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (t.mask >> (2 * c + (e & 1)) & 1) {
+          out[e] = acc[0][e] + acc[1][e];
+          if constexpr (PARTS == 3) out[e] += acc[2][e];
+        }
+      if (t.last) {
+        tmem_st_16x8(delta + ((uint32_t)row0 << 16) + 8 * t.eight, out);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = 0.f;
       }
     }
   }
-  return sum;
 }
 
-template <int BT, int KW, typename TO>
-__global__ void __launch_bounds__(kThreads, Cfg<BT, KW, TO>::kTwo ? 2 : 1)
+// The adapter that all tokens of the tile have, -1 if none has any, -2 if it is mixed.  (A whole warp.)
+template <int BT>
+__device__ __forceinline__ int tile_adapter(const AdaptArgs &g, int tok0, int live) {
+  const int lane = threadIdx.x & 31;
+  const int one = token_id(g, tok0);
+  bool same = true;
+#pragma unroll
+  for (int i = 0; i < (BT + 31) / 32; ++i)
+    if (32 * i + lane < live) same = same && token_id(g, tok0 + 32 * i + lane) == one;
+  return __all_sync(0xffffffffu, same) ? one : -2;
+}
+
+template <int BT, typename TO>
+__global__ void __launch_bounds__(kThreads, Cfg<BT, TO>::kTwo ? 2 : 1)
     adapt_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
-                 const __grid_constant__ CUtensorMap mb, const __grid_constant__ AdaptArgs g,
-                 int splits) {
-  using C = Cfg<BT, KW, TO>;
-  constexpr int S = C::kStages, E = C::kSlots, PARTS = C::kParts;
+                 const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mh,
+                 const __grid_constant__ AdaptArgs g, int splits) {
+  using C = Cfg<BT, TO>;
+  constexpr int S = C::kStages;
   extern __shared__ unsigned char dsm_raw[];
-  __shared__ __align__(8) uint64_t full[S], empty[S], b_full[E], x_full[E], x_empty[E], list, zeroed,
-      done, drain;
+  __shared__ __align__(8) uint64_t full[S], empty[S], done, drain;
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_abort, s_counts[kBuilders];
-  __shared__ Groups<BT> s_groups;
+  __shared__ int s_abort;
+  __shared__ Tasks<BT> s_tasks;
   unsigned char *smem = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
   auto tile_w = [&](int s) { return smem + s * C::kStage; };
   auto tile_x = [&](int s) { return smem + s * C::kStage + kTileW; };
-  auto slot_b = [&](int e) { return smem + S * C::kStage + e * C::kSlot; };
-  auto slot_h = [&](int e) { return slot_b(e) + C::kTileB; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int part = (int)cluster_rank() % splits;
   const int n0 = (int)(blockIdx.x / splits) * kBM, tok0 = blockIdx.y * BT;
-  const int blocks = (g.hidden + kBK - 1) / kBK;
+  const int live = min(BT, g.tokens - tok0);
+  // k-blocks: those of W x, then, of a tile with one adapter, 64 ranks of a part of h each
+  const int one = tile_adapter<BT>(g, tok0, live);
+  const int plain = (g.hidden + kBK - 1) / kBK, chunks = (g.rank + kBK - 1) / kBK;
+  const int blocks = plain + (one >= 0 ? chunks * C::kParts : 0);
   const int kb0 = (int)((int64_t)blocks * part / splits);
   const int kbs = (int)((int64_t)blocks * (part + 1) / splits) - kb0;
-  const int chunks = (g.rank16() + KW - 1) / KW;
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int e = 0; e < E; ++e) {
-      mbar_init(&b_full[e], 1);
-      mbar_init(&x_full[e], 1);
-      mbar_init(&x_empty[e], 1);
-    }
-    mbar_init(&list, kBuilders * 32);
-    mbar_init(&zeroed, 4);
     mbar_init(&done, 1);
     mbar_init(&drain, 1);
     s_abort = 0;
@@ -338,55 +326,41 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, KW, TO>::kTwo ? 2 : 1)
     *abort_flag = 1;
     raise_error(g.err, GDN_DEVERR_TIMEOUT);
   };
-  // this CTA's units are u = part, part + splits, ... of all; the j-th of them
-  auto my_units = [&]() { return (s_groups.n * chunks - part + splits - 1) / splits; };
 
   if (warp == 0 && lane == 0) {
-    // producer: k-blocks and units as their slots get free, units as soon as the groups are known
-    int kb = 0, u = 0, units = -1;
-    bool good = true;
-    uint32_t idle = 0;
-    while (good && (kb < kbs || u < units || units < 0)) {
-      bool moved = false;
-      if (kb < kbs) {
-        const int s = kb % S;
-        if (kb < S || mbar_test_wait(&empty[s], ((kb / S) - 1) & 1)) {
-          mbar_arrive_expect_tx(&full[s], C::kStage);
-          tma_load2(tile_w(s), &mw, (kb0 + kb) * kBK, n0, &full[s]);
-          tma_load2(tile_x(s), &mx, (kb0 + kb) * kBK, tok0, &full[s]);
-          ++kb;
-          moved = true;
-        }
+    // producer
+    int issued = 0;
+    for (int kb = 0; kb < kbs; ++kb) {
+      const int s = kb % S;
+      if (kb >= S && !wait(&empty[s], ((kb / S) - 1) & 1, abort_flag)) {
+        fail();
+        break;
       }
-      if (units < 0) {
-        if (mbar_test_wait(&list, 0)) units = my_units();
-      } else if (u < units) {
-        const int e = u % E;
-        if (u < E || mbar_test_wait(&x_empty[e], ((u / E) - 1) & 1)) {
-          const int unit = part + u * splits, gr = unit / chunks, c = unit - gr * chunks;
-          mbar_arrive_expect_tx(&b_full[e], C::kTileB);
-          tma_load2(slot_b(e), &mb, c * KW, s_groups.adapter[gr] * g.n_out + n0, &b_full[e]);
-          ++u;
-          moved = true;
+      mbar_arrive_expect_tx(&full[s], C::kStage);
+      const int k = kb0 + kb, c = (k - plain) / C::kParts, p = (k - plain) % C::kParts;
+      if (k < plain) {
+        tma_load2(tile_w(s), &mw, k * kBK, n0, &full[s]);
+        tma_load2(tile_x(s), &mx, k * kBK, tok0, &full[s]);
+      } else {
+        // (rows of h behind the last token are another part's: columns that are not stored)
+        if (k == max(plain, kb0)) {
+          kv::dependent_wait();
+          asm volatile("fence.proxy.async.global;" ::: "memory");  // plain stores, read by TMA
         }
+        tma_load2(tile_w(s), &mb, c * kBK, one * g.n_out + n0, &full[s]);
+        tma_load2(tile_x(s), &mh, c * kBK, p * g.tokens + tok0, &full[s]);
       }
-      idle = moved ? 0 : idle + 1;
-      if (idle > (1u << 25)) fail();  // seconds
-      if ((idle & 15) == 15) good = *abort_flag == 0;
+      issued = kb + 1;
     }
-    if (!good) {  // let the copies still in flight land before the CTA exits
-      for (int i = kb - S < 0 ? 0 : kb - S; i < kb; ++i)
-        mbar_wait_bounded(&full[i % S], (i / S) & 1);
-      for (int i = u - E < 0 ? 0 : u - E; i < u; ++i)
-        mbar_wait_bounded(&b_full[i % E], (i / E) & 1);
+    if (*abort_flag) {  // let the copies still in flight land before the CTA exits
+      for (int kb = issued - S < 0 ? 0 : issued - S; kb < issued; ++kb)
+        mbar_wait_bounded(&full[kb % S], (kb / S) & 1);
     }
   } else if (warp == 1 && lane == 0) {
     // MMA issuer
-    constexpr uint32_t kFull = tc::idesc_bf16(kBM, BT), kPiece = tc::idesc_bf16(kBM, 16);
+    constexpr uint32_t idesc = tc::idesc_bf16(kBM, BT);
     bool good = true;
-    int u = 0, units = 0;
-    const int half = kbs / 2;
-    for (int kb = 0; kb < kbs && good; ++kb) {
+    for (int kb = 0; kb < kbs; ++kb) {
       const int s = kb % S;
       if (!wait(&full[s], (kb / S) & 1, abort_flag)) {
         good = false;
@@ -394,117 +368,86 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, KW, TO>::kTwo ? 2 : 1)
       }
       tc::fence_after_sync();
       const uint32_t a = smem_addr(tile_w(s)), b = smem_addr(tile_x(s));
+      const uint32_t acc = tmem + (uint32_t)(kb % C::kAcc) * BT;
+      const int k = kb0 + kb, c = (k - plain) / C::kParts;
+      const int steps = k < plain ? kBK / 16 : min(kBK, g.rank16() - c * kBK) / 16;
 #pragma unroll
       for (int kk = 0; kk < kBK / 16; ++kk)
-        tc::mma_ss_f16(tmem, operand<128>(a + 32 * kk), operand<128>(b + 32 * kk), kFull,
-                       (kb | kk) ? 1u : 0u);
+        if (kk < steps)
+          tc::mma_ss_f16(acc, tc::smem_desc_sw128(a + 32 * kk), tc::smem_desc_sw128(b + 32 * kk),
+                         idesc, kb >= C::kAcc || kk > 0 ? 1u : 0u);
       tc::mma_commit(&empty[s]);
-      if (kb < half) continue;
-      if (kb == half) {
-        if (!wait(&list, 0, abort_flag) || !wait(&zeroed, 0, abort_flag)) {
-          good = false;
-          break;
-        }
-        units = my_units();
-      }
-      // units up to this place: they are spread evenly over k-blocks half .. kbs - 1
-      const int upto = (int)((int64_t)units * (kb - half + 1) / (kbs - half));
-      for (; u < upto; ++u) {
-        const int e = u % E;
-        if (!wait(&b_full[e], (u / E) & 1, abort_flag) ||
-            !wait(&x_full[e], (u / E) & 1, abort_flag)) {
-          good = false;
-          break;
-        }
-        tc::fence_after_sync();
-        const int unit = part + u * splits, gr = unit / chunks, c = unit - gr * chunks;
-        const uint32_t bt = smem_addr(slot_b(e)), ht = smem_addr(slot_h(e));
-        const int steps = min(KW, g.rank16() - c * KW) / 16;
-        for (unsigned m = s_groups.pieces[gr]; m != 0; m &= m - 1) {
-          const int piece = __ffs(m) - 1;
-          for (int p = 0; p < PARTS; ++p)
-            for (int kk = 0; kk < steps; ++kk)
-              tc::mma_ss_f16(tmem + BT + 16 * piece, operand<C::kPitch>(bt + 32 * kk),
-                             operand<C::kPitch>(ht + p * C::kTileH + piece * 16 * C::kPitch +
-                                                32 * kk),
-                             kPiece, 1u);
-        }
-        tc::mma_commit(&x_empty[e]);
-      }
     }
     if (!good) fail();
     tc::mma_commit(good ? &done : &drain);
     if (!good) mbar_wait_bounded(&drain, 0);  // MMAs in flight finish before TMEM is freed
-  } else if (warp >= 6) {
-    // builders
-    find_groups<BT>(g, tok0, s_groups, s_counts);
-    mbar_arrive(&list);
-    kv::dependent_wait();  // h
-    const int units = my_units();
-    for (int u = warp - 6; warp - 6 < C::kTeam && u < units; u += C::kTeam) {
-      const int e = u % E;
-      // warp-uniform decisions
-      if (!__all_sync(0xffffffffu, u < E || wait(&x_empty[e], ((u / E) - 1) & 1, abort_flag))) {
-        fail();
-        break;
-      }
-      const int unit = part + u * splits, gr = unit / chunks, c = unit - gr * chunks;
-      build_rows<BT, KW, PARTS>(g, s_groups, gr, tok0, c * KW, slot_h(e));
-      if (!__all_sync(0xffffffffu, wait(&b_full[e], (u / E) & 1, abort_flag))) {
-        fail();
-        break;
-      }
-      if (take_out<C::kTileB>(slot_b(e)) && lane == 0) {
-        atomicOr(&s_groups.bad[unit >> 5], 1u << (unit & 31));
-        s_groups.any_bad = 1;
-      }
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&x_full[e]);
-    }
   } else if (warp >= 2) {
-    // epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31, a lane per output row
-    const int quad = warp & 3, row = 32 * quad + lane, n = n0 + row;
-    const uint32_t mine = tmem + ((uint32_t)(32 * quad) << 16);
-    {  // the units add to zeros
-      const float zero[16] = {};
-#pragma unroll
-      for (int c = 0; c < BT / 16; ++c) tc::tmem_st16(mine + BT + 16 * c, zero);
+    const int quad = warp & 3, side = (warp - 2) >> 2;  // TMEM lanes 32 quad .., two warps to each
+    // the adapters' part of rows 32 quad + 16 side .. + 15
+    const int row0 = 32 * quad + 16 * side;
+    const uint32_t delta = tmem + C::kAcc * BT;
+    if (one == -2) {
+      list_tasks<BT>(g, tok0, live, part, splits, s_tasks);
+      // B on its way to L2 meanwhile
+      const bf16 *mine = static_cast<const bf16 *>(g.b) +
+                         min(n0 + row0 + (lane & 15), g.n_out - 1) * g.ld_b + (lane >> 4) * 64;
+      for (int i = 0; i < s_tasks.n; ++i)
+        if (s_tasks.task[i].id >= 0 && (lane >> 4) * 64 < g.rank)
+          prefetch_l2(mine + (int64_t)s_tasks.task[i].id * g.n_out * g.ld_b);
+      kv::dependent_wait();  // h
+      if (g.rank == 16)
+        expand<BT, 8, 1, 8, false, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
+      else if (g.rank == 32)
+        expand<BT, 16, 1, 4, false, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
+      else if (g.rank == 64 || g.rank == 128)
+        expand<BT, 16, 2, 2, false, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
+      else
+        expand<BT, 8, 4, 2, true, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
       tc::tmem_st_wait();
       tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&zeroed);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
     }
+    // epilogue: a lane per output row, the two warps take turns in the columns
+    const int row = 32 * quad + lane, n = n0 + row;
     // warp-uniform decision: tcgen05.ld is a whole-warp instruction
     const bool got = __all_sync(0xffffffffu, wait(&done, 0, abort_flag));
     if (!got) {
       fail();
     } else {
       tc::fence_after_sync();
-      const bool bad = s_groups.any_bad != 0;
       float *parts = reinterpret_cast<float *>(smem);  // [BT][128]: the ring is empty
       TO *y = static_cast<TO *>(g.y);
+      const uint32_t mine = tmem + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
-      for (int c = 0; c < BT / 16; ++c) {
-        if (tok0 + 16 * c >= g.tokens) break;
+      for (int c = 16 * side; c < live; c += 32) {
         float v[32];
-        tc::tmem_ld32(mine + 16 * c, mine + BT + 16 * c, v);
+        if (one == -2) {
+          tc::tmem_ld32(mine + c, mine + C::kAcc * BT + c, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
-        if (bad && n < g.n_out) {
-          kv::dependent_wait();
-          for (int j = 0; j < 16; ++j)
-            if (tok0 + 16 * c + j < g.tokens)
-              v[j] += put_back<BT, KW>(g, s_groups, tok0, 16 * c + j, n);
+          for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
+        } else {
+          tc::tmem_ld16(mine + c, v);
+        }
+        if constexpr (C::kAcc == 3) {
+          float u[32];
+          if (kbs > 2) {
+            tc::tmem_ld32(mine + BT + c, mine + 2 * BT + c, u);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += u[j] + u[16 + j];
+          } else if (kbs > 1) {
+            tc::tmem_ld16(mine + BT + c, u);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += u[j];
+          }
         }
         if (splits > 1) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) parts[(16 * c + j) * kBM + row] = v[j];
+          for (int j = 0; j < 16; ++j) parts[(c + j) * kBM + row] = v[j];
         } else if (n < g.n_out) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (tok0 + 16 * c + j < g.tokens)
-              Elem<TO>::store1(y + (int64_t)(tok0 + 16 * c + j) * g.ld_y + n, v[j]);
+            if (c + j < live)
+              Elem<TO>::store1(y + (int64_t)(tok0 + c + j) * g.ld_y + n, v[j]);
         }
       }
     }
@@ -521,7 +464,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, KW, TO>::kTwo ? 2 : 1)
     cluster_sync();
     bool sound = true;
     for (int p = 0; p < splits; ++p) sound = sound && ld_peer_int(peer_addr(&s_abort, p)) == 0;
-    const int live = min(BT, g.tokens - tok0);
     const int lo = live * part / splits, hi = live * (part + 1) / splits;
     for (int i = lo * kBM + tid; sound && i < hi * kBM; i += kThreads) {
       const int t = i / kBM, n = n0 + i % kBM;
@@ -552,57 +494,54 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return encode;
 }
 
-// [rows][cols] bf16 with row stride ld elements, boxes of `box_cols` (16, 32 or 64) x box_rows in
-// the swizzle of that width
+// [rows][cols] bf16 with row stride ld elements, box {64, box_rows}, 128-byte swizzle
 bool encode_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
-                 int box_cols, int box_rows) {
+                 int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (encode == nullptr) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows};
   cuuint32_t elem[2] = {1, 1};
-  const CUtensorMapSwizzle swizzle = box_cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
-                                     : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                      : CU_TENSOR_MAP_SWIZZLE_32B;
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
-                box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
 
-template <int BT, int KW, typename TO>
+template <int BT, typename TO>
 cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
-  using C = Cfg<BT, KW, TO>;
-  CUtensorMap mw, mx, mb;
-  if (!encode_rows(&mw, g.w, g.n_out, g.hidden, g.ld_w, kBK, kBM) ||
-      !encode_rows(&mx, g.x, g.tokens, g.hidden, g.ld_x, kBK, BT) ||
-      !encode_rows(&mb, g.b, (int64_t)g.n_adapters * g.n_out, g.rank, g.ld_b, KW, kBM))
+  using C = Cfg<BT, TO>;
+  CUtensorMap mw, mx, mb, mh;
+  if (!encode_rows(&mw, g.w, g.n_out, g.hidden, g.ld_w, kBM) ||
+      !encode_rows(&mx, g.x, g.tokens, g.hidden, g.ld_x, BT) ||
+      !encode_rows(&mb, g.b, (int64_t)g.n_adapters * g.n_out, g.rank, g.ld_b, kBM) ||
+      !encode_rows(&mh, g.h, (int64_t)C::kParts * g.tokens, g.rank16(), g.rank16(), BT))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> seen{0};
-  const cudaError_t e = kv::allow_smem(adapt_kernel<BT, KW, TO>, C::kSmem, g.device, seen);
+  const cudaError_t e = kv::allow_smem(adapt_kernel<BT, TO>, C::kSmem, g.device, seen);
   if (e != cudaSuccess) return e;
   const int tiles = (g.n_out + kBM - 1) / kBM, rows = (g.tokens + BT - 1) / BT;
   const int blocks = (g.hidden + kBK - 1) / kBK;
   int splits = 1;
   while ((int64_t)tiles * rows * splits < g.sm_count && splits < 8 && blocks >= 8 * splits)
     splits *= 2;
-  return kv::launch(adapt_kernel<BT, KW, TO>, dim3((unsigned)(tiles * splits), (unsigned)rows),
-                    kThreads, C::kSmem, s, splits, mw, mx, mb, g, splits);
+  return kv::launch(adapt_kernel<BT, TO>, dim3((unsigned)(tiles * splits), (unsigned)rows), kThreads,
+                    C::kSmem, s, splits, mw, mx, mb, mh, g, splits);
 }
 
 template <typename TO>
 cudaError_t launch_t(const AdaptArgs &g, cudaStream_t s) {
-  const bool narrow = g.rank <= 16;
-  if (g.tokens <= 16) return narrow ? launch<16, 16, TO>(g, s) : launch<16, 64, TO>(g, s);
-  if (g.tokens <= 64) return narrow ? launch<64, 16, TO>(g, s) : launch<64, 64, TO>(g, s);
-  return launch<128, 16, TO>(g, s);
+  if (g.tokens <= 16) return launch<16, TO>(g, s);
+  if (g.tokens <= 64) return launch<64, TO>(g, s);
+  return launch<128, TO>(g, s);
 }
 
 }  // namespace
 
 size_t adapt_workspace_bytes(const AdaptArgs &g) {
-  return (size_t)g.tokens * g.rank16() * sizeof(float);
+  // (eight rows more: the tokens are read by eights)
+  return ((size_t)g.tokens * g.parts() + 8) * g.rank16() * 2;
 }
 
 cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s) {

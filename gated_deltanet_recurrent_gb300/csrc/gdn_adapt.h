@@ -14,9 +14,11 @@ struct AdaptArgs {
   int64_t ld_x, ld_w, ld_a, ld_b, ld_y;
   int tokens, hidden, n_out, rank, n_adapters;
   gdn_dtype y_dtype;
-  float *h;                   // workspace: [tokens][rank16] = scale * A x, zeros beyond rank
+  void *h;                    // workspace: scale * A x in bf16 parts that add up to it,
+                              // [parts][tokens][rank16], zeros beyond rank
   unsigned int *err;
   int sm_count, device;
+  GDN_HD int parts() const { return y_dtype == GDN_F32 ? 3 : 2; }
   // the rank rounded up to the tensor cores' 16
   GDN_HD int rank16() const { return (rank + 15) & ~15; }
 };

@@ -152,7 +152,7 @@ gdn_status gdn_in_proj_adapted(gdn_pool *p, gdn_adapters *ad, int64_t tokens, co
   bool temporary = false;
   e = ad->work.get(gdn::adapt_workspace_bytes(g), s, &work, &temporary);
   if (e != cudaSuccess) return cuda_fail(e, "the adapters' workspace");
-  g.h = static_cast<float *>(work);
+  g.h = work;
   e = gdn::launch_adapt(g, s);
   if (temporary) {
     const cudaError_t ef = cudaFreeAsync(work, s);

@@ -1,4 +1,5 @@
-// The low side of the adapters: h[t] = scale[a] A[a] x[t], a = ids[t], in float32.
+// The low side of the adapters: h[t] = scale[a] A[a] x[t], a = ids[t], summed in float32 and stored as
+// bf16 parts that add up to it.
 //
 // Bound by the bytes of the A in use (a decode step) or of x (prompts), so the products go where the
 // data can be used without a detour: mma.sync takes both operands from registers, and those are
@@ -14,19 +15,12 @@
 #include "gdn_adapt.h"
 #include "gdn_common.cuh"
 #include "gdn_kv.cuh"
+#include "gdn_mma.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kWarps = 8;
-
-__device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 // Elements k .. k + 7 of a row, zeros from `hidden` on (what lies behind a row is not read).
 __device__ __forceinline__ uint4 load8(const bf16 *row, int k, int hidden) {
@@ -73,7 +67,7 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) low_kernel(Adapt
   __syncthreads();
   const int row = lane >> 2, col = lane & 3;
   const bf16 *x = static_cast<const bf16 *>(g.x);
-  const int ld_h = g.rank16();
+  const int rank16 = g.rank16(), parts = g.parts();
   for (int gi = blockIdx.y; gi < s_n; gi += gridDim.y) {
     const int id = s_lead[gi];
     const bf16 *a = static_cast<const bf16 *>(g.a) + (int64_t)id * g.rank * g.ld_a;
@@ -129,14 +123,27 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) low_kernel(Adapt
               make_float2(acc[m][n][2 * hh], acc[m][n][2 * hh + 1]);
     __syncthreads();
     const float scale = g.scale[id];
-    for (int i = tid; i < kTok * kRanks; i += 32 * kWarps) {
-      const int t = i / kRanks, r = rank0 + i % kRanks;
-      if (s_id[t] != id || r >= ld_h) continue;
-      float sum = 0.f;
+    for (int i = tid; i < kTok * kRanks / 2; i += 32 * kWarps) {  // two ranks a thread
+      const int t = 2 * i / kRanks, r = rank0 + 2 * i % kRanks;
+      if (s_id[t] != id || r >= rank16) continue;
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += s_part[w * kTok * kRanks + i];
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 v = *reinterpret_cast<const float2 *>(&s_part[w * kTok * kRanks + 2 * i]);
+        sum.x += v.x, sum.y += v.y;
+      }
       // (zeros beyond the rank, whatever the scale is)
-      g.h[(int64_t)(tok0 + t) * ld_h + r] = r < g.rank ? sum * scale : 0.f;
+      float x = r < g.rank ? sum.x * scale : 0.f, y = r + 1 < g.rank ? sum.y * scale : 0.f;
+      uint32_t *h = static_cast<uint32_t *>(g.h) + ((int64_t)(tok0 + t) * rank16 + r) / 2;
+      for (int p = 0; p < parts; ++p) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
+        h[(int64_t)p * g.tokens * (rank16 / 2)] = w;
+        const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+        // (what is infinite or NaN is the first part alone)
+        x = fabsf(lo) < INFINITY ? x - lo : 0.f;
+        y = fabsf(hi) < INFINITY ? y - hi : 0.f;
+      }
     }
     __syncthreads();
   }
