@@ -40,7 +40,7 @@ constexpr int kBM = 128, kBK = 64;
 constexpr int kThreads = 320;
 constexpr int kTileW = kBM * kBK * 2;
 
-template <int BT, typename TO>
+template <int BT, typename TO, bool SPLIT>
 struct Cfg {
   static constexpr int kParts = sizeof(TO) == 4 ? 3 : 2;
   // The tensor core cuts its sums off: one accumulator over K = 2048 is 2e-6 off, three that take
@@ -50,10 +50,10 @@ struct Cfg {
   // two CTAs per SM where their registers (100 a thread) and columns suffice
   static constexpr bool kTwo = sizeof(TO) == 2;
   static constexpr int kStage = kTileW + BT * kBK * 2;
-  static constexpr int kFit = ((kTwo ? 112 : 225) * 1024 - 1024) / kStage;
+  static constexpr int kRecv = SPLIT ? BT * kBM * 4 : 0;  // the cluster's parts of a tile's share
+  static constexpr int kFit = ((kTwo ? 111 : 223) * 1024 - 1024 - kRecv) / kStage;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
-  static constexpr int kSmem = kStages * kStage + 1024;
-  static_assert(BT * kBM * 4 <= kStages * kStage, "a cluster's parts take the ring's place");
+  static constexpr int kSmem = kStages * kStage + kRecv + 1024;
 };
 
 __device__ __forceinline__ void tma_load2(void *dst, const CUtensorMap *m, int x, int y,
@@ -70,24 +70,19 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t peer_addr(const void *p, int rank) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ float ld_peer(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ int ld_peer_int(uint32_t a) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+// Store into the shared memory of CTA `rank` of the cluster, at the place of `p` in this one's.
+__device__ __forceinline__ void st_peer(const void *p, int rank, float v) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(smem_addr(p)),
+      "r"(rank), "f"(v)
+      : "memory");
 }
 __device__ __forceinline__ void prefetch_l2(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
@@ -127,15 +122,17 @@ __device__ __forceinline__ int token_id(const AdaptArgs &g, int t) {
 }
 
 // The adapters that each eight tokens of a mixed tile have, in order; an eight without any is one
-// entry too.
+// entry too, of adapter 0 with no tokens.
+struct Task {
+  int64_t b;            // elements from the first adapter's B to this one's
+  int h;                // elements from the h of the tile's first token to that of the eight's
+  unsigned char eight;  // tokens 8 eight .. of the tile
+  unsigned char mask;   // those of them that have this adapter
+  unsigned char last;   // of the eight
+};
 template <int BT>
 struct Tasks {
-  struct {
-    int id;               // -1: none
-    unsigned char eight;  // tokens 8 eight .. of the tile
-    unsigned char mask;   // those of them that have this adapter
-    unsigned char last;   // of the eight
-  } task[BT];
+  alignas(16) Task task[BT + 8];  // (the steps are rounded up to a whole number of rounds)
   int count[BT / 8], n;
 };
 
@@ -158,10 +155,15 @@ __device__ __forceinline__ void list_tasks(const AdaptArgs &g, int tok0, int liv
       }
       int at = 0;
       for (int i = 0; i < e; ++i) at += s.count[i];
-      if (e == eights - 1 && lane == 0) s.n = at + n;
-      const int mine = at + __popc(leads & ((1u << lane) - 1));
-      if (lead) s.task[mine] = {id, (unsigned char)e, (unsigned char)same, mine == at + n - 1};
-      if (!leads && lane == 0) s.task[at] = {-1, (unsigned char)e, 0, 1};
+      const int mine = at + __popc(leads & ((1u << lane) - 1)), h = 8 * e * g.rank16();
+      if (lead)
+        s.task[mine] = {(int64_t)id * g.n_out * g.ld_b, h, (unsigned char)e, (unsigned char)same,
+                        mine == at + n - 1};
+      if (!leads && lane == 0) s.task[at] = {0, h, (unsigned char)e, 0, 1};
+      if (e == eights - 1) {
+        if (lane == 0) s.n = at + n;
+        if (lane < 8) s.task[at + n + lane] = {0, 0, 0, 0, 0};
+      }
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
   }
@@ -196,25 +198,29 @@ __device__ __forceinline__ void expand(const AdaptArgs &g, const Tasks<BT> &s, i
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int rank16 = g.rank16(), halves = NL * kRanks == 64 && rank16 > 64 ? 2 : 1;
   const int steps = s.n * halves;
-  const int64_t stride = (int64_t)g.n_out * g.ld_b, part = (int64_t)g.tokens * rank16;
-  const bf16 *lo = static_cast<const bf16 *>(g.b) + min(n0 + row0 + r, g.n_out - 1) * g.ld_b,
-             *hi = static_cast<const bf16 *>(g.b) + min(n0 + row0 + r + 8, g.n_out - 1) * g.ld_b;
+  const int64_t part = (int64_t)g.tokens * rank16;
+  const bf16 *lo = static_cast<const bf16 *>(g.b) + min(n0 + row0 + r, g.n_out - 1) * g.ld_b +
+                   c * (W / 2),
+             *hi = static_cast<const bf16 *>(g.b) + min(n0 + row0 + r + 8, g.n_out - 1) * g.ld_b +
+                   c * (W / 2);
   // (columns of other tokens, or behind the last: whatever their h holds, they are dropped)
   const bf16 *h0 = static_cast<const bf16 *>(g.h) + (int64_t)(tok0 + r) * rank16 + c * (W / 2);
+  uint32_t info[D];  // eight, mask, last
   uint32_t b[D][NL][2][kWords], h[D][NL][PARTS][kWords];
+  // (no branch on the task: the loads of several steps are to be on their way together)
   auto load = [&](int d, int i) {
-    if (i >= steps) return;
-    const auto t = s.task[i >> (halves - 1)];
-    if (t.id < 0) return;
+    i = min(i, steps);  // the first step behind the last is one of nothing
+    const int4 raw = *reinterpret_cast<const int4 *>(&s.task[i >> (halves - 1)]);
     const int k0 = 64 * (i & (halves - 1));
-    const int64_t at = t.id * stride;
-    const bf16 *hp = h0 + 8 * t.eight * rank16 + k0;
+    const int64_t at = (int64_t)((uint64_t)(uint32_t)raw.y << 32 | (uint32_t)raw.x);
+    const bf16 *hp = h0 + raw.z + k0;
+    info[d] = (uint32_t)raw.w;
 #pragma unroll
     for (int l = 0; l < NL; ++l) {
       if (PARTIAL && k0 + kRanks * l >= rank16) break;
-      const int e = k0 + kRanks * l + c * (W / 2);
-      load_ranks<W, PARTIAL>(lo + at, e, g.rank, b[d][l][0]);
-      load_ranks<W, PARTIAL>(hi + at, e, g.rank, b[d][l][1]);
+      const int e = k0 + kRanks * l;
+      load_ranks<W, PARTIAL>(lo + at, e, g.rank - c * (W / 2), b[d][l][0]);
+      load_ranks<W, PARTIAL>(hi + at, e, g.rank - c * (W / 2), b[d][l][1]);
 #pragma unroll
       for (int p = 0; p < PARTS; ++p)
         load_ranks<W, false>(hp + p * part, kRanks * l, 0, h[d][l][p]);
@@ -224,42 +230,39 @@ __device__ __forceinline__ void expand(const AdaptArgs &g, const Tasks<BT> &s, i
 #pragma unroll
   for (int e = 0; e < 4; ++e) out[e] = 0.f;
 #pragma unroll
+  for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[p][e] = 0.f;
+#pragma unroll
   for (int d = 0; d < D; ++d) load(d, d);
   for (int i0 = 0; i0 < steps; i0 += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      const int i = i0 + d;
-      if (i >= steps) break;
-      const auto t = s.task[i >> (halves - 1)];
-      const int half = i & (halves - 1), k0 = 64 * half;
-      if (t.id >= 0) {
-        if (half == 0)
+      const int i = i0 + d, half = i & (halves - 1), k0 = 64 * half;
 #pragma unroll
-          for (int p = 0; p < PARTS; ++p)
+      for (int l = 0; l < NL; ++l) {
+        if (PARTIAL && k0 + kRanks * l >= rank16) break;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[p][e] = 0.f;
+        for (int w = 0; w < kWords; w += 2) {
+          const uint32_t a[4] = {b[d][l][0][w], b[d][l][1][w], b[d][l][0][w + 1],
+                                 b[d][l][1][w + 1]};
 #pragma unroll
-        for (int l = 0; l < NL; ++l) {
-          if (PARTIAL && k0 + kRanks * l >= rank16) break;
-#pragma unroll
-          for (int w = 0; w < kWords; w += 2) {
-            const uint32_t a[4] = {b[d][l][0][w], b[d][l][1][w], b[d][l][0][w + 1],
-                                   b[d][l][1][w + 1]};
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p) mma16816(acc[p], a, h[d][l][p][w], h[d][l][p][w + 1]);
-          }
+          for (int p = 0; p < PARTS; ++p) mma16816(acc[p], a, h[d][l][p][w], h[d][l][p][w + 1]);
         }
       }
+      const uint32_t mine = info[d], mask = mine >> (8 + 2 * c);
       load(d, i + D);
       if (half + 1 < halves) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (t.mask >> (2 * c + (e & 1)) & 1) {
-          out[e] = acc[0][e] + acc[1][e];
-          if constexpr (PARTS == 3) out[e] += acc[2][e];
-        }
-      if (t.last) {
-        tmem_st_16x8(delta + ((uint32_t)row0 << 16) + 8 * t.eight, out);
+      for (int e = 0; e < 4; ++e) {
+        float v = acc[0][e] + acc[1][e];
+        if constexpr (PARTS == 3) v += acc[2][e];
+        if (mask >> (e & 1) & 1) out[e] = v;
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) acc[p][e] = 0.f;
+      }
+      if (mine >> 16 & 1) {
+        tmem_st_16x8(delta + ((uint32_t)row0 << 16) + 8 * (mine & 255), out);
 #pragma unroll
         for (int e = 0; e < 4; ++e) out[e] = 0.f;
       }
@@ -279,17 +282,18 @@ __device__ __forceinline__ int tile_adapter(const AdaptArgs &g, int tok0, int li
   return __all_sync(0xffffffffu, same) ? one : -2;
 }
 
-template <int BT, typename TO>
-__global__ void __launch_bounds__(kThreads, Cfg<BT, TO>::kTwo ? 2 : 1)
+template <int BT, typename TO, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, Cfg<BT, TO, SPLIT>::kTwo ? 2 : 1)
     adapt_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
                  const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mh,
                  const __grid_constant__ AdaptArgs g, int splits) {
-  using C = Cfg<BT, TO>;
+  using C = Cfg<BT, TO, SPLIT>;
   constexpr int S = C::kStages;
   extern __shared__ unsigned char dsm_raw[];
   __shared__ __align__(8) uint64_t full[S], empty[S], done, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
+  __shared__ float s_gone;  // SPLIT: another CTA of the cluster gave up
   __shared__ Tasks<BT> s_tasks;
   unsigned char *smem = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
@@ -297,15 +301,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO>::kTwo ? 2 : 1)
   auto tile_x = [&](int s) { return smem + s * C::kStage + kTileW; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int part = (int)cluster_rank() % splits;
+  const int part = SPLIT ? (int)cluster_rank() : 0;
   const int n0 = (int)(blockIdx.x / splits) * kBM, tok0 = blockIdx.y * BT;
   const int live = min(BT, g.tokens - tok0);
-  // k-blocks: those of W x, then, of a tile with one adapter, 64 ranks of a part of h each
-  const int one = tile_adapter<BT>(g, tok0, live);
-  const int plain = (g.hidden + kBK - 1) / kBK, chunks = (g.rank + kBK - 1) / kBK;
-  const int blocks = plain + (one >= 0 ? chunks * C::kParts : 0);
-  const int kb0 = (int)((int64_t)blocks * part / splits);
-  const int kbs = (int)((int64_t)blocks * (part + 1) / splits) - kb0;
+  // this CTA's k-blocks of W x: from kb0 on
+  const int all = (g.hidden + kBK - 1) / kBK;
+  const int kb0 = (int)((int64_t)all * part / splits);
+  const int plain = (int)((int64_t)all * (part + 1) / splits) - kb0;
+  auto load_plain = [&](int kb) {
+    const int s = kb % S;
+    mbar_arrive_expect_tx(&full[s], C::kStage);
+    tma_load2(tile_w(s), &mw, (kb0 + kb) * kBK, n0, &full[s]);
+    tma_load2(tile_x(s), &mx, (kb0 + kb) * kBK, tok0, &full[s]);
+  };
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -314,13 +322,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO>::kTwo ? 2 : 1)
     mbar_init(&done, 1);
     mbar_init(&drain, 1);
     s_abort = 0;
+    s_gone = 0.f;
     mbar_fence_init();
+    for (int kb = 0; kb < S && kb < plain; ++kb) load_plain(kb);  // nothing else is needed for these
   }
+  // and, of a tile with one adapter, those of 64 ranks of a part of h each: from eb0 on
+  const int one = tile_adapter<BT>(g, tok0, live);
+  const int extra = one >= 0 ? (g.rank + kBK - 1) / kBK * C::kParts : 0;
+  const int eb0 = extra * part / splits;
+  const int kbs = plain + extra * (part + 1) / splits - eb0;
   if (warp == 1) tc::tmem_alloc(&tmem_slot, C::kTmem);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  if constexpr (SPLIT) {
+    __syncwarp();
+    cluster_arrive();  // (waited for before the first store to another CTA)
+  }
   volatile int *abort_flag = &s_abort;
   auto fail = [&]() {
     *abort_flag = 1;
@@ -329,24 +348,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO>::kTwo ? 2 : 1)
 
   if (warp == 0 && lane == 0) {
     // producer
-    int issued = 0;
-    for (int kb = 0; kb < kbs; ++kb) {
+    int issued = min(S, plain);
+    for (int kb = issued; kb < kbs; ++kb) {
       const int s = kb % S;
       if (kb >= S && !wait(&empty[s], ((kb / S) - 1) & 1, abort_flag)) {
         fail();
         break;
       }
-      mbar_arrive_expect_tx(&full[s], C::kStage);
-      const int k = kb0 + kb, c = (k - plain) / C::kParts, p = (k - plain) % C::kParts;
-      if (k < plain) {
-        tma_load2(tile_w(s), &mw, k * kBK, n0, &full[s]);
-        tma_load2(tile_x(s), &mx, k * kBK, tok0, &full[s]);
+      if (kb < plain) {
+        load_plain(kb);
       } else {
         // (rows of h behind the last token are another part's: columns that are not stored)
-        if (k == max(plain, kb0)) {
+        const int e = eb0 + kb - plain, c = e / C::kParts, p = e % C::kParts;
+        if (kb == plain) {
           kv::dependent_wait();
           asm volatile("fence.proxy.async.global;" ::: "memory");  // plain stores, read by TMA
         }
+        mbar_arrive_expect_tx(&full[s], C::kStage);
         tma_load2(tile_w(s), &mb, c * kBK, one * g.n_out + n0, &full[s]);
         tma_load2(tile_x(s), &mh, c * kBK, p * g.tokens + tok0, &full[s]);
       }
@@ -369,8 +387,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO>::kTwo ? 2 : 1)
       tc::fence_after_sync();
       const uint32_t a = smem_addr(tile_w(s)), b = smem_addr(tile_x(s));
       const uint32_t acc = tmem + (uint32_t)(kb % C::kAcc) * BT;
-      const int k = kb0 + kb, c = (k - plain) / C::kParts;
-      const int steps = k < plain ? kBK / 16 : min(kBK, g.rank16() - c * kBK) / 16;
+      const int c = (eb0 + kb - plain) / C::kParts;
+      const int steps = kb < plain ? kBK / 16 : min(kBK, g.rank16() - c * kBK) / 16;
 #pragma unroll
       for (int kk = 0; kk < kBK / 16; ++kk)
         if (kk < steps)
@@ -386,36 +404,45 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO>::kTwo ? 2 : 1)
     // the adapters' part of rows 32 quad + 16 side .. + 15
     const int row0 = 32 * quad + 16 * side;
     const uint32_t delta = tmem + C::kAcc * BT;
-    if (one == -2) {
+    if (one >= 0) {  // B on its way to L2
+      const bf16 *b = static_cast<const bf16 *>(g.b) +
+                      ((int64_t)one * g.n_out + min(n0 + row0 + (lane & 15), g.n_out - 1)) * g.ld_b +
+                      (lane >> 4) * 64;
+      if ((lane >> 4) * 64 < g.rank) prefetch_l2(b);
+    } else if (one == -2) {
       list_tasks<BT>(g, tok0, live, part, splits, s_tasks);
       // B on its way to L2 meanwhile
       const bf16 *mine = static_cast<const bf16 *>(g.b) +
                          min(n0 + row0 + (lane & 15), g.n_out - 1) * g.ld_b + (lane >> 4) * 64;
       for (int i = 0; i < s_tasks.n; ++i)
-        if (s_tasks.task[i].id >= 0 && (lane >> 4) * 64 < g.rank)
-          prefetch_l2(mine + (int64_t)s_tasks.task[i].id * g.n_out * g.ld_b);
+        if (s_tasks.task[i].mask != 0 && (lane >> 4) * 64 < g.rank)
+          prefetch_l2(mine + s_tasks.task[i].b);
       kv::dependent_wait();  // h
       if (g.rank == 16)
-        expand<BT, 8, 1, 8, false, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
+        expand<BT, 8, 1, 6, false, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
       else if (g.rank == 32)
         expand<BT, 16, 1, 4, false, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
       else if (g.rank == 64 || g.rank == 128)
         expand<BT, 16, 2, 2, false, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
       else
-        expand<BT, 8, 4, 2, true, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
+        expand<BT, 8, 4, 1, true, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       asm volatile("bar.sync 1, 256;" ::: "memory");
     }
     // epilogue: a lane per output row, the two warps take turns in the columns
     const int row = 32 * quad + lane, n = n0 + row;
+    __syncwarp();
+    if constexpr (SPLIT) cluster_wait();  // the others run
     // warp-uniform decision: tcgen05.ld is a whole-warp instruction
     const bool got = __all_sync(0xffffffffu, wait(&done, 0, abort_flag));
     if (!got) {
       fail();
     } else {
       tc::fence_after_sync();
-      float *parts = reinterpret_cast<float *>(smem);  // [BT][128]: the ring is empty
+      // SPLIT: CTA i of the cluster adds up tokens i * share ..; it receives [splits][share][128]
+      float *recv = reinterpret_cast<float *>(smem + S * C::kStage);
+      const int share = BT / splits;
       TO *y = static_cast<TO *>(g.y);
       const uint32_t mine = tmem + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
@@ -440,9 +467,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO>::kTwo ? 2 : 1)
             for (int j = 0; j < 16; ++j) v[j] += u[j];
           }
         }
-        if (splits > 1) {
+        if constexpr (SPLIT) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) parts[(c + j) * kBM + row] = v[j];
+          for (int j = 0; j < 16; ++j)
+            if (c + j < live)
+              st_peer(recv + (part * share + (c + j) % share) * kBM + row, (c + j) / share, v[j]);
         } else if (n < g.n_out) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -458,22 +487,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO>::kTwo ? 2 : 1)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::kTmem);
   }
-  if (splits > 1) {
-    // each CTA adds up its share of the tile's tokens
+  if constexpr (SPLIT) {
     __syncwarp();
-    cluster_sync();
-    bool sound = true;
-    for (int p = 0; p < splits; ++p) sound = sound && ld_peer_int(peer_addr(&s_abort, p)) == 0;
-    const int lo = live * part / splits, hi = live * (part + 1) / splits;
-    for (int i = lo * kBM + tid; sound && i < hi * kBM; i += kThreads) {
+    if (warp < 2) cluster_wait();
+    if (*abort_flag)
+      for (int p = 0; p < splits; ++p) st_peer(&s_gone, p, 1.f);
+    cluster_arrive();
+    cluster_wait();
+    const float *recv = reinterpret_cast<const float *>(smem + S * C::kStage);
+    const int share = BT / splits, mine = min(share, live - part * share);
+    for (int i = tid; s_gone == 0.f && i < mine * kBM; i += kThreads) {
       const int t = i / kBM, n = n0 + i % kBM;
       float sum = 0.f;
-      for (int p = 0; p < splits; ++p)
-        sum += ld_peer(peer_addr(reinterpret_cast<float *>(smem) + i, p));
+      for (int p = 0; p < splits; ++p) sum += recv[p * share * kBM + i];
       if (n < g.n_out)
-        Elem<TO>::store1(static_cast<TO *>(g.y) + (int64_t)(tok0 + t) * g.ld_y + n, sum);
+        Elem<TO>::store1(
+            static_cast<TO *>(g.y) + (int64_t)(tok0 + part * share + t) * g.ld_y + n, sum);
     }
-    cluster_sync();
   }
   // what follows on the stream waits for this kernel only: the low side is complete too
   kv::dependent_wait();
@@ -509,32 +539,42 @@ bool encode_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, i
          CUDA_SUCCESS;
 }
 
-template <int BT, typename TO>
-cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
-  using C = Cfg<BT, TO>;
+template <int BT, typename TO, bool SPLIT>
+cudaError_t launch(const AdaptArgs &g, int splits, cudaStream_t s) {
+  using C = Cfg<BT, TO, SPLIT>;
   CUtensorMap mw, mx, mb, mh;
   if (!encode_rows(&mw, g.w, g.n_out, g.hidden, g.ld_w, kBM) ||
       !encode_rows(&mx, g.x, g.tokens, g.hidden, g.ld_x, BT) ||
       !encode_rows(&mb, g.b, (int64_t)g.n_adapters * g.n_out, g.rank, g.ld_b, kBM) ||
       !encode_rows(&mh, g.h, (int64_t)C::kParts * g.tokens, g.rank16(), g.rank16(), BT))
-    return cudaErrorInvalidValue;
+    return cudaErrorNotSupported;
   static std::atomic<uint64_t> seen{0};
-  const cudaError_t e = kv::allow_smem(adapt_kernel<BT, TO>, C::kSmem, g.device, seen);
+  const cudaError_t e = kv::allow_smem(adapt_kernel<BT, TO, SPLIT>, C::kSmem, g.device, seen);
   if (e != cudaSuccess) return e;
   const int tiles = (g.n_out + kBM - 1) / kBM, rows = (g.tokens + BT - 1) / BT;
+  return kv::launch(adapt_kernel<BT, TO, SPLIT>, dim3((unsigned)(tiles * splits), (unsigned)rows),
+                    kThreads, C::kSmem, s, splits, mw, mx, mb, mh, g, splits);
+}
+
+template <int BT, typename TO>
+cudaError_t launch_bt(const AdaptArgs &g, cudaStream_t s) {
+  const int64_t tiles = (int64_t)((g.n_out + kBM - 1) / kBM) * ((g.tokens + BT - 1) / BT);
   const int blocks = (g.hidden + kBK - 1) / kBK;
+  // CTAs that share a tile: so many that every multiprocessor has one, with four k-blocks each at
+  // least (one token, 2048 -> 12352: 194 CTAs 15 us, 97 CTAs 17; 64 tokens with an adapter each of
+  // rank 64: 61 and 79)
   int splits = 1;
-  while ((int64_t)tiles * rows * splits < g.sm_count && splits < 8 && blocks >= 8 * splits)
-    splits *= 2;
-  return kv::launch(adapt_kernel<BT, TO>, dim3((unsigned)(tiles * splits), (unsigned)rows), kThreads,
-                    C::kSmem, s, splits, mw, mx, mb, mh, g, splits);
+  while (splits * tiles < g.sm_count && splits < 8 && blocks >= 8 * splits) splits *= 2;
+  return splits > 1 ? launch<BT, TO, true>(g, splits, s) : launch<BT, TO, false>(g, 1, s);
 }
 
 template <typename TO>
 cudaError_t launch_t(const AdaptArgs &g, cudaStream_t s) {
-  if (g.tokens <= 16) return launch<16, TO>(g, s);
-  if (g.tokens <= 64) return launch<64, TO>(g, s);
-  return launch<128, TO>(g, s);
+  if (g.tokens <= 16) return launch_bt<16, TO>(g, s);
+  // tiles of 128 tokens read W half as often, if there is one for every multiprocessor
+  const int64_t wide = (int64_t)((g.n_out + kBM - 1) / kBM) * ((g.tokens + 127) / 128);
+  if (g.tokens <= 64 || wide < g.sm_count) return launch_bt<64, TO>(g, s);
+  return launch<128, TO, false>(g, 1, s);
 }
 
 }  // namespace

@@ -24,7 +24,7 @@ struct AdaptArgs {
 };
 
 size_t adapt_workspace_bytes(const AdaptArgs &g);
-// The low side, then the projection; cudaErrorInvalidValue: no tensor map.
+// The low side, then the projection; cudaErrorNotSupported: no tensor map.
 cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s);
 
 cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s);

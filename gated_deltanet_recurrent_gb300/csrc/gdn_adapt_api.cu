@@ -158,7 +158,7 @@ gdn_status gdn_in_proj_adapted(gdn_pool *p, gdn_adapters *ad, int64_t tokens, co
     const cudaError_t ef = cudaFreeAsync(work, s);
     if (e == cudaSuccess) e = ef;
   }
-  if (e == cudaErrorInvalidValue)
+  if (e == cudaErrorNotSupported)
     return fail(GDN_ERR_UNSUPPORTED, "no tensor map for these operands (driver entry point)");
   if (e != cudaSuccess) return cuda_fail(e, "adapted projection launch");
   return ok();

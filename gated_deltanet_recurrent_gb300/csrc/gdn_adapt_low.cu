@@ -33,8 +33,9 @@ __device__ __forceinline__ uint4 load8(const bf16 *row, int k, int hidden) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int MT, int NT>
-__global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) low_kernel(AdaptArgs g) {
+// AHEAD: steps of 64 k whose loads a warp has in flight.
+template <int MT, int NT, int AHEAD>
+__global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
   constexpr int kTok = 16 * MT, kRanks = 8 * NT;
   extern __shared__ float s_part[];  // [kWarps][kTok][kRanks]
   __shared__ int s_id[kTok], s_lead[kTok], s_n;
@@ -43,33 +44,58 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) low_kernel(Adapt
   kv::dependents_may_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tok0 = blockIdx.x * kTok, rank0 = blockIdx.z * kRanks;
+  const int row = lane >> 2, col = lane & 3;
+  // (a row behind the last token: any row, its result is dropped)
+  const bf16 *xrow[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+      xrow[m][hh] = static_cast<const bf16 *>(g.x) +
+                    min(tok0 + 16 * m + 8 * hh + row, g.tokens - 1) * g.ld_x;
+  uint4 xv[AHEAD][MT][2][2];
+  auto load_x = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            xv[i][m][hh][c] = load8(xrow[m][hh], k0 + 64 * kWarps * i + 32 * c + 8 * col, g.hidden);
+  };
+  // x is on its way before the ids are known
+  load_x(64 * warp);
+  int own = -1;
   if (tid < kTok) {
-    int id = tok0 + tid < g.tokens ? g.ids[tok0 + tid] : -1;
-    if (id < -1 || id >= g.n_adapters) {
+    if (tok0 + tid < g.tokens) own = g.ids[tok0 + tid];
+    if (own < -1 || own >= g.n_adapters) {
       if (blockIdx.y + blockIdx.z == 0) raise_error(g.err, GDN_DEVERR_ADAPTER);
-      id = -1;
+      own = -1;
     }
-    s_id[tid] = id;
+    s_id[tid] = own;
   }
   __syncthreads();
   if (warp == 0) {  // the window's adapters, in the order of their first tokens
     int n = 0;
     for (int base = 0; base < kTok; base += 32) {
       const int i = base + lane;
-      bool lead = i < kTok && s_id[i < kTok ? i : 0] >= 0;
-      for (int j = 0; j < kTok; ++j) lead = lead && !(j < i && s_id[j] == s_id[i]);
+      const int id = i < kTok ? s_id[i] : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, id);
+      bool lead = id >= 0 && __ffs(same) - 1 == lane;
+      for (int j = 0; j < base; ++j) lead = lead && s_id[j] != id;
       const uint32_t m = __ballot_sync(0xffffffffu, lead);
-      if (lead) s_lead[n + __popc(m & ((1u << lane) - 1))] = s_id[i];
+      if (lead) s_lead[n + __popc(m & ((1u << lane) - 1))] = id;
       n += __popc(m);
     }
     if (lane == 0) s_n = n;
   }
   __syncthreads();
-  const int row = lane >> 2, col = lane & 3;
-  const bf16 *x = static_cast<const bf16 *>(g.x);
   const int rank16 = g.rank16(), parts = g.parts();
   for (int gi = blockIdx.y; gi < s_n; gi += gridDim.y) {
     const int id = s_lead[gi];
+    const float scale = g.scale[id];
     const bf16 *a = static_cast<const bf16 *>(g.a) + (int64_t)id * g.rank * g.ld_a;
     float acc[MT][NT][4];
 #pragma unroll
@@ -78,39 +104,33 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) low_kernel(Adapt
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
-    // 64 k a step: two loads of 16 bytes per row and lane
-#pragma unroll(MT == 1 ? 2 : 1)
-    for (int k0 = 64 * warp; k0 < g.hidden; k0 += 64 * kWarps) {
-      uint4 xv[MT][2][2], av[NT][2];
+    for (int k0 = 64 * warp; k0 < g.hidden; k0 += 64 * kWarps * AHEAD) {
+      uint4 av[AHEAD][NT][2];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int k = k0 + 32 * c + 8 * col;
+      for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int r = rank0 + 8 * n + row;
-          av[n][c] = r < g.rank ? load8(a + r * g.ld_a, k, g.hidden) : make_uint4(0, 0, 0, 0);
-        }
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            // (a row behind the last token: any row, its result is dropped)
-            const int t = min(tok0 + 16 * m + 8 * hh + row, g.tokens - 1);
-            xv[m][hh][c] = load8(x + t * g.ld_x, k, g.hidden);
+          for (int c = 0; c < 2; ++c) {
+            const int r = rank0 + 8 * n + row, k = k0 + 64 * kWarps * i + 32 * c + 8 * col;
+            av[i][n][c] = r < g.rank ? load8(a + r * g.ld_a, k, g.hidden) : make_uint4(0, 0, 0, 0);
           }
-      }
+      // (the first x of the first adapter are here already)
+      if (gi != blockIdx.y || k0 != 64 * warp) load_x(k0);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint4 u = xv[m][0][c], v = xv[m][1][c];
-          const uint32_t f0[4] = {u.x, v.x, u.y, v.y}, f1[4] = {u.z, v.z, u.w, v.w};
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816(acc[m][n], f0, av[n][c].x, av[n][c].y);
-            mma16816(acc[m][n], f1, av[n][c].z, av[n][c].w);
+          for (int m = 0; m < MT; ++m) {
+            const uint4 u = xv[i][m][0][c], v = xv[i][m][1][c];
+            const uint32_t f0[4] = {u.x, v.x, u.y, v.y}, f1[4] = {u.z, v.z, u.w, v.w};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816(acc[m][n], f0, av[i][n][c].x, av[i][n][c].y);
+              mma16816(acc[m][n], f1, av[i][n][c].z, av[i][n][c].w);
+            }
           }
-        }
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -122,7 +142,6 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) low_kernel(Adapt
               &s_part[(warp * kTok + 16 * m + 8 * hh + row) * kRanks + 8 * n + 2 * col]) =
               make_float2(acc[m][n][2 * hh], acc[m][n][2 * hh + 1]);
     __syncthreads();
-    const float scale = g.scale[id];
     for (int i = tid; i < kTok * kRanks / 2; i += 32 * kWarps) {  // two ranks a thread
       const int t = 2 * i / kRanks, r = rank0 + 2 * i % kRanks;
       if (s_id[t] != id || r >= rank16) continue;
@@ -149,18 +168,18 @@ __global__ void __launch_bounds__(32 * kWarps, MT == 1 ? 2 : 1) low_kernel(Adapt
   }
 }
 
-template <int MT, int NT>
+template <int MT, int NT, int AHEAD>
 cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
   constexpr int smem = kWarps * 16 * MT * 8 * NT * 4;
   static std::atomic<uint64_t> seen{0};
-  const cudaError_t e = kv::allow_smem(low_kernel<MT, NT>, smem, g.device, seen);
+  const cudaError_t e = kv::allow_smem(low_kernel<MT, NT, AHEAD>, smem, g.device, seen);
   if (e != cudaSuccess) return e;
   const int windows = (g.tokens + 16 * MT - 1) / (16 * MT);
   const int parts = (g.rank16() + 8 * NT - 1) / (8 * NT);
   // CTAs that share a window: as many as it may have adapters, but no more than four waves in all
   const int64_t room = (int64_t)4 * g.sm_count / ((int64_t)windows * parts);
   const int share = (int)(room < 1 ? 1 : room > 16 * MT ? 16 * MT : room);
-  return kv::launch(low_kernel<MT, NT>, dim3((unsigned)windows, (unsigned)share, (unsigned)parts),
+  return kv::launch(low_kernel<MT, NT, AHEAD>, dim3((unsigned)windows, (unsigned)share, (unsigned)parts),
                     32 * kWarps, smem, s, 1, g);
 }
 
@@ -168,7 +187,7 @@ cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
 
 cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s) {
   // few tokens: small windows, for parallel loads of A; many: large ones, that read A less often
-  return g.tokens <= 256 ? launch<1, 2>(g, s) : launch<4, 4>(g, s);
+  return g.tokens <= 256 ? launch<1, 2, 4>(g, s) : launch<4, 4, 1>(g, s);
 }
 
 }  // namespace gdn
