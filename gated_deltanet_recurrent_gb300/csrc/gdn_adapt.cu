@@ -10,21 +10,24 @@
 //
 //   warp 0      one lane: TMA of W and x tiles, a ring of k-blocks of 64
 //   warp 1      one lane: tcgen05.mma into the tile's accumulator in TMEM
-//   warps 2..9  the adapters' part of mixed tiles, then the epilogue
+//   warps 2..17 the adapters' part of mixed tiles, then the epilogue
+//   warp 18     a lane per slot: copies of the B tiles of a mixed tile
 //
 // Where all tokens of a tile have one adapter (prompts), its part is a few more k-blocks: B tiles for
-// W's and the parts of h for x's.  Other tiles are mixed.  There a warp has 16 output rows and takes
-// the tokens eight at a time: for each adapter among the eight, mma.sync of its 16 rows of B, straight
-// from global memory to registers (several steps ahead), with the eight columns of h, of which it
-// keeps those of the adapter's own tokens.  So the cost goes by tokens and hardly by adapters, and
-// the work is beside the tensor core's that does W x.  The result goes to TMEM columns of its own (the
-// fragment is the 16x256b shape of tcgen05.st), where the epilogue adds it.  Either way nothing of one
-// request's adapter, be it infinite, meets another request's tokens.
+// W's and the parts of h for x's.  Other tiles are mixed.  There the B tile of every adapter that the
+// tile has comes through a ring of its own, by TMA too: a decode step is bound by the bytes of W and of
+// the B in use, and only copies that need no registers keep enough of both on their way.  Four warps
+// with 32 output rows each take an adapter's rows of B into registers, once, and multiply them by the
+// h of the adapter's own tokens, eight at a time, wherever they are in the tile (mma.sync, with the
+// rank as K); four such teams take the adapters in turn.  So B is read once per tile and adapter, the
+// tensor core's work on W x goes on beside it, and nothing of one request's adapter, be it infinite,
+// meets another request's tokens.  The results go to shared memory, [token][row], where the epilogue
+// adds them.
 //
-// A decode step is bound by the bytes of W and of the B in use.  With fewer tiles than SMs, the CTAs
-// of a cluster split the k-blocks and the tokens' eights of a tile and add their parts through
-// distributed shared memory, in a fixed order.  The kernel starts under the low side's: W is on its
-// way, and B asked into L2, before h is complete.  Every wait is bounded (GDN_DEVERR_TIMEOUT).
+// With fewer tiles than SMs, the CTAs of a cluster split the k-blocks and the adapters of a tile and
+// push their parts into each other's shared memory, where they are added in a fixed order.  The
+// kernel starts under the low side's: W and B are on their way before h is complete.  Every wait is
+// bounded (GDN_DEVERR_TIMEOUT).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -37,23 +40,34 @@ namespace gdn {
 namespace {
 
 constexpr int kBM = 128, kBK = 64;
-constexpr int kThreads = 320;
+constexpr int kHelpers = 512;            // threads of the adapters' part and the epilogue
+constexpr int kThreads = 64 + kHelpers + 32;
+constexpr int kTeams = 4;                // of four warps
 constexpr int kTileW = kBM * kBK * 2;
 
-template <int BT, typename TO, bool SPLIT>
+constexpr int kPitch = kBM + 4;      // floats of a token's row of the adapters' part
+constexpr int kRingB = 64 * 1024;    // bytes of the ring of B tiles
+
+constexpr uint32_t pow2_at_least(uint32_t n) {
+  uint32_t p = 32;
+  while (p < n) p *= 2;
+  return p;
+}
+
+template <int BT, int PITCH, typename TO>
 struct Cfg {
   static constexpr int kParts = sizeof(TO) == 4 ? 3 : 2;
   // The tensor core cuts its sums off: one accumulator over K = 2048 is 2e-6 off, three that take
   // the k-blocks in turn a third of that, which a bf16 y would not show.
   static constexpr int kAcc = sizeof(TO) == 4 ? 3 : 1;
-  static constexpr uint32_t kTmem = (kAcc + 1) * BT;  // the adapters' columns are the last
-  // two CTAs per SM where their registers (100 a thread) and columns suffice
-  static constexpr bool kTwo = sizeof(TO) == 2;
+  static constexpr uint32_t kTmem = pow2_at_least(kAcc * BT);
   static constexpr int kStage = kTileW + BT * kBK * 2;
-  static constexpr int kRecv = SPLIT ? BT * kBM * 4 : 0;  // the cluster's parts of a tile's share
-  static constexpr int kFit = ((kTwo ? 111 : 223) * 1024 - 1024 - kRecv) / kStage;
+  static constexpr int kDelta = BT * kPitch * 4;
+  static constexpr int kH = kParts * BT * PITCH;  // h of the tile, PITCH / 2 ranks of it
+  static constexpr int kFit = (224 * 1024 - kRingB - kDelta - kH) / kStage;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
-  static constexpr int kSmem = kStages * kStage + kRecv + 1024;
+  static constexpr int kSmem = kStages * kStage + kRingB + kDelta + kH + 1024;
+  static_assert(BT * kBM * 4 <= kRingB, "a cluster's parts take the place of the B tiles");
 };
 
 __device__ __forceinline__ void tma_load2(void *dst, const CUtensorMap *m, int x, int y,
@@ -88,12 +102,17 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// 16 lanes x 8 columns of TMEM from an mma.sync result (its m16n8 fragment)
-__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const float *d) {
-  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
-               "r"(__float_as_uint(d[0])), "r"(__float_as_uint(d[1])), "r"(__float_as_uint(d[2])),
-               "r"(__float_as_uint(d[3]))
-               : "memory");
+// (try_wait may suspend the thread for a while; lanes that look after a slot each must not)
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // A bounded wait that also ends when the CTA gives up.
@@ -105,200 +124,242 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
   return false;
 }
 
-// Elements r .. r + 3 of a row of B, zeros from `rank` on (what lies behind a row is not read).
-__device__ __forceinline__ uint2 load4(const bf16 *row, int r, int rank) {
-  if (r + 4 <= rank) return *reinterpret_cast<const uint2 *>(row + r);
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (r + j < rank)
-      w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row)[r + j] << (16 * (j & 1));
-  return make_uint2(w[0], w[1]);
-}
-
 __device__ __forceinline__ int token_id(const AdaptArgs &g, int t) {
   const int id = t < g.tokens ? g.ids[t] : -1;
   return id >= 0 && id < g.n_adapters ? id : -1;
 }
 
-// The adapters that each eight tokens of a mixed tile have, in order; an eight without any is one
-// entry too, of adapter 0 with no tokens.
-struct Task {
-  int64_t b;            // elements from the first adapter's B to this one's
-  int h;                // elements from the h of the tile's first token to that of the eight's
-  unsigned char eight;  // tokens 8 eight .. of the tile
-  unsigned char mask;   // those of them that have this adapter
-  unsigned char last;   // of the eight
-};
-template <int BT>
-struct Tasks {
-  alignas(16) Task task[BT + 8];  // (the steps are rounded up to a whole number of rounds)
-  int count[BT / 8], n;
-};
-
-// Run by the 8 warps of the adapters' part, for the eights e = part, part + splits, ...
-template <int BT>
-__device__ __forceinline__ void list_tasks(const AdaptArgs &g, int tok0, int live, int part,
-                                           int splits, Tasks<BT> &s) {
-  const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
-  const int eights = (live + 7) / 8;
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int e = warp; e < eights; e += 8) {
-      const int id = lane < 8 ? token_id(g, tok0 + 8 * e + lane) : -1;
-      const uint32_t same = __match_any_sync(0xffffffffu, id);
-      const bool lead = e % splits == part && id >= 0 && __ffs(same) - 1 == lane;
-      const uint32_t leads = __ballot_sync(0xffffffffu, lead);
-      const int n = leads ? __popc(leads) : 1;
-      if (pass == 0) {
-        if (lane == 0) s.count[e] = n;
-        continue;
-      }
-      int at = 0;
-      for (int i = 0; i < e; ++i) at += s.count[i];
-      const int mine = at + __popc(leads & ((1u << lane) - 1)), h = 8 * e * g.rank16();
-      if (lead)
-        s.task[mine] = {(int64_t)id * g.n_out * g.ld_b, h, (unsigned char)e, (unsigned char)same,
-                        mine == at + n - 1};
-      if (!leads && lane == 0) s.task[at] = {0, h, (unsigned char)e, 0, 1};
-      if (e == eights - 1) {
-        if (lane == 0) s.n = at + n;
-        if (lane < 8) s.task[at + n + lane] = {0, 0, 0, 0, 0};
-      }
-    }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-  }
+__device__ __forceinline__ void helpers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kHelpers) : "memory");
 }
 
-// W bytes of a row of B from its element e on; PARTIAL: zeros from `rank` on (what lies behind a row
-// is not read).
-template <int W, bool PARTIAL>
-__device__ __forceinline__ void load_ranks(const bf16 *p, int e, int rank, uint32_t *out) {
-  if constexpr (PARTIAL) {
-    const uint2 v = load4(p, e, rank);
-    out[0] = v.x, out[1] = v.y;
-  } else if constexpr (W == 8) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p + e);
+// The groups of a mixed tile: tokens with one adapter, and the tasks, up to eight tokens of a group
+// each.  Groups are in the order of their first tokens, tasks in the order of the groups.
+template <int BT>
+struct Groups {
+  int id[BT];                   // per token: its adapter if it is this CTA's to do, or -1
+  int adapter[BT];              // per group
+  unsigned char first[BT];      // of a group: its first task, and how many there are
+  unsigned char count[BT];
+  unsigned char start[BT];      // per token that is the first of a group: the group's first task
+  unsigned char tokens[BT];     // per task: how many of the eight there are
+  alignas(8) unsigned char token[BT][8];
+  int sums[2];
+  int n;
+};
+
+// Run by the helpers, with s.id set.
+template <int BT>
+__device__ __forceinline__ void find_groups(Groups<BT> &s) {
+  const int tid = threadIdx.x - 64;
+  // eight threads per token look for the same adapter among the others
+  const int token = tid >> 3, id = token < BT ? s.id[token < BT ? token : 0] : -1;
+  int lead = BT, rank = 0, size = 0;
+  for (int j = tid & 7; j < BT; j += 8)
+    if (id >= 0 && s.id[j] == id) {
+      lead = min(lead, j);
+      rank += j < token;
+      ++size;
+    }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    lead = min(lead, __shfl_xor_sync(0xffffffffu, lead, o));
+    rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    size += __shfl_xor_sync(0xffffffffu, size, o);
+  }
+  const bool first = (tid & 7) == 0 && id >= 0;
+  if (first) s.adapter[token] = lead == token ? size : 0;  // (for now: of a group's first token, its size)
+  else if ((tid & 7) == 0 && token < BT) s.adapter[token] = 0;
+  helpers_sync();
+  // groups (upper half) and tasks (lower half) before each token
+  const int mine = tid < BT && s.adapter[tid] > 0 ? (1 << 16) + (s.adapter[tid] + 7) / 8 : 0;
+  const int own = tid < BT ? s.adapter[tid] : 0;
+  int sum = mine;
+  if (tid < 64) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if ((tid & 31) >= o) sum += y;
+    }
+    if ((tid & 31) == 31) s.sums[tid >> 5] = sum;
+  }
+  helpers_sync();
+  const int before = sum - mine + (tid >= 32 ? s.sums[0] : 0);
+  if (tid < BT && own > 0) {
+    const int at = before >> 16, tasks = (own + 7) / 8;
+    s.adapter[at] = s.id[tid];  // (at <= tid: every thread has read its place)
+    s.first[at] = s.start[tid] = (unsigned char)before;
+    s.count[at] = (unsigned char)tasks;
+    for (int i = 0; i < tasks; ++i) s.tokens[(before & 255) + i] = (unsigned char)min(8, own - 8 * i);
+  }
+  if (tid == 0) s.n = (s.sums[0] + s.sums[1]) >> 16;
+  helpers_sync();
+  if (first) {
+    s.token[s.start[lead] + rank / 8][rank % 8] = (unsigned char)token;
+    // (the last task's empty columns have the group's first token, and are dropped)
+    if (rank + 1 == size)
+      for (int i = size; i & 7; ++i) s.token[s.start[lead] + i / 8][i % 8] = (unsigned char)lead;
+  }
+  helpers_sync();
+}
+
+// A ring of B tiles of 128 rows of PITCH bytes.  Rows of just that width that follow each other come
+// as one piece (`plain`): a tensor copy takes some three cycles for each row, be it 32 bytes long
+// (64 adapters of rank 16 beside 2048 -> 12352: 33 us with it).  Others are in the swizzle of a tensor copy.
+struct RingB {
+  unsigned char *tiles;
+  uint64_t *full, *empty;
+  bool plain;
+};
+// Whether B's rows follow each other at a pitch of `pitch` bytes.
+__host__ __device__ inline bool plain_rows(const AdaptArgs &g, int pitch) {
+  return g.rank * 2 == pitch && g.ld_b == g.rank;
+}
+template <int PITCH>
+constexpr int kSlots = kRingB / (kBM * PITCH);
+
+// where the swizzle of a row's width puts byte `off` of a tile; mask 0: no swizzle
+__device__ __forceinline__ uint32_t swizzled(uint32_t off, uint32_t mask) {
+  return off ^ (((off >> 7) & mask) << 4);
+}
+
+// Where 16 bytes of h lie in shared memory, [part][token][PITCH]: two neighbouring tokens' rows take
+// different banks.
+template <int PITCH>
+__device__ __forceinline__ int h_offset(int token, int byte) {
+  return token * PITCH + (PITCH == 128 ? byte ^ ((token & 1) << 6) : byte);
+}
+
+template <int W>
+__device__ __forceinline__ void load_words(const void *p, uint32_t *out) {
+  if constexpr (W == 8) {
+    const uint2 v = *static_cast<const uint2 *>(p);
     out[0] = v.x, out[1] = v.y;
   } else {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p + e);
+    const uint4 v = *static_cast<const uint4 *>(p);
     out[0] = v.x, out[1] = v.y, out[2] = v.z, out[3] = v.w;
   }
 }
 
-// One warp: the adapters' part of 16 output rows (`row0` .. of the tile) of all tasks, to the TMEM
-// columns at `delta`.  B rows and h columns meet in mma.sync with the rank as K; lane (r, c) of a
-// fragment has rows r and r + 8 of B and column r of h, in loads of W bytes (W / 2 neighbouring
-// ranks, those of W / 8 products: the order of K does not matter).  A step is NL such loads, up to
-// 64 ranks of a task; the loads of D steps are in flight.  PARTIAL: any rank (W = 8); otherwise
-// the rank is NL * 2 W, or with NL * 2 W = 64 also 128, and nothing is asked.
-template <int BT, int W, int NL, int D, bool PARTIAL, int PARTS>
-__device__ __forceinline__ void expand(const AdaptArgs &g, const Tasks<BT> &s, int n0, int row0,
-                                       int tok0, uint32_t delta) {
-  constexpr int kRanks = 2 * W, kWords = W / 4;  // ranks and words of a load
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const int rank16 = g.rank16(), halves = NL * kRanks == 64 && rank16 > 64 ? 2 : 1;
-  const int steps = s.n * halves;
-  const int64_t part = (int64_t)g.tokens * rank16;
-  const bf16 *lo = static_cast<const bf16 *>(g.b) + min(n0 + row0 + r, g.n_out - 1) * g.ld_b +
-                   c * (W / 2),
-             *hi = static_cast<const bf16 *>(g.b) + min(n0 + row0 + r + 8, g.n_out - 1) * g.ld_b +
-                   c * (W / 2);
-  // (columns of other tokens, or behind the last: whatever their h holds, they are dropped)
-  const bf16 *h0 = static_cast<const bf16 *>(g.h) + (int64_t)(tok0 + r) * rank16 + c * (W / 2);
-  uint32_t info[D];  // eight, mask, last
-  uint32_t b[D][NL][2][kWords], h[D][NL][PARTS][kWords];
-  // (no branch on the task: the loads of several steps are to be on their way together)
-  auto load = [&](int d, int i) {
-    i = min(i, steps);  // the first step behind the last is one of nothing
-    const int4 raw = *reinterpret_cast<const int4 *>(&s.task[i >> (halves - 1)]);
-    const int k0 = 64 * (i & (halves - 1));
-    const int64_t at = (int64_t)((uint64_t)(uint32_t)raw.y << 32 | (uint32_t)raw.x);
-    const bf16 *hp = h0 + raw.z + k0;
-    info[d] = (uint32_t)raw.w;
-#pragma unroll
-    for (int l = 0; l < NL; ++l) {
-      if (PARTIAL && k0 + kRanks * l >= rank16) break;
-      const int e = k0 + kRanks * l;
-      load_ranks<W, PARTIAL>(lo + at, e, g.rank - c * (W / 2), b[d][l][0]);
-      load_ranks<W, PARTIAL>(hi + at, e, g.rank - c * (W / 2), b[d][l][1]);
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p)
-        load_ranks<W, false>(hp + p * part, kRanks * l, 0, h[d][l][p]);
+// Run by the helpers (`warp` of them): all groups of the tile.  Unit u = half * n + group is PITCH / 2
+// ranks of a group's B; it is team u % 4's, in which a warp takes 32 of its rows, as two fragments.
+// Lane (r, c) of a fragment has rows r and r + 8 of B and token r of a task, for each W bytes the same
+// ranks (W / 2 neighbours: the order of K does not matter).  False: a wait gave up.
+template <int BT, int PITCH, int PARTS>
+__device__ __forceinline__ bool expand(const AdaptArgs &g, const Groups<BT> &s, const RingB &ring,
+                                       int warp, int tok0, int live, unsigned char *hs, float *delta,
+                                       volatile int *abort_flag) {
+  constexpr int W = PITCH == 32 ? 8 : 16, NL = PITCH / (4 * W), kWords = W / 4;
+  constexpr int E = kSlots<PITCH>;
+  static_assert(E % kTeams == 0, "a slot is always the same team's, which then is never two rounds ahead");
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3, row0 = 32 * (warp & 3);
+  const int team = warp >> 2, ld = g.rank_pad(), halves = ld * 2 / PITCH;
+  const uint32_t mask = ring.plain ? 0 : PITCH / 16 - 1;
+  float *const to = delta + row0 + r;
+  bool good = true;
+  for (int half = 0; half < halves; ++half) {
+    if (half > 0) helpers_sync();  // the first half has been read
+    // h of the tokens that have an adapter here (nothing else of it is defined, nor read)
+    for (int i = 32 * warp + lane; i < PARTS * live * (PITCH / 16); i += kHelpers) {
+      const int q = i / (live * (PITCH / 16)), rest = i % (live * (PITCH / 16));
+      const int t = rest / (PITCH / 16), at = rest % (PITCH / 16) * 16;
+      if (s.id[t] < 0) continue;
+      *reinterpret_cast<uint4 *>(hs + q * (BT * PITCH) + h_offset<PITCH>(t, at)) =
+          *reinterpret_cast<const uint4 *>(
+              static_cast<const unsigned char *>(g.h) +
+              (((int64_t)q * g.tokens + tok0 + t) * ld * 2 + half * PITCH + at));
     }
-  };
-  float out[4], acc[PARTS][4];
+    helpers_sync();
+    // (units of both halves go round the teams and slots in one order)
+    for (int u = half * s.n + ((team - half * s.n) & (kTeams - 1)); good && u < (half + 1) * s.n;
+         u += kTeams) {
+      const int group = u - half * s.n, e = u % E;
+      if (!__all_sync(0xffffffffu, wait(&ring.full[e], (u / E) & 1, abort_flag))) {
+        good = false;
+        break;
+      }
+      const unsigned char *tile = ring.tiles + e * (kBM * PITCH);
+      uint32_t b[2][NL][2][kWords];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) out[e] = 0.f;
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-  for (int p = 0; p < PARTS; ++p)
+        for (int l = 0; l < NL; ++l)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[p][e] = 0.f;
+          for (int y = 0; y < 2; ++y)
+            load_words<W>(tile + swizzled((uint32_t)((row0 + 16 * m + r + 8 * y) * PITCH +
+                                                     l * 4 * W + c * W),
+                                          mask),
+                          b[m][l][y]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.empty[e]);
+      const int first = s.first[group], end = first + s.count[group];
+      for (int t = first; t < end; ++t) {
+        const int col = s.token[t][r], live_cols = s.tokens[t];
+        const uint32_t two = *reinterpret_cast<const unsigned short *>(&s.token[t][2 * c]);
+        float acc[2][PARTS][4];
 #pragma unroll
-  for (int d = 0; d < D; ++d) load(d, d);
-  for (int i0 = 0; i0 < steps; i0 += D) {
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const int i = i0 + d, half = i & (halves - 1), k0 = 64 * half;
+          for (int q = 0; q < PARTS; ++q)
 #pragma unroll
-      for (int l = 0; l < NL; ++l) {
-        if (PARTIAL && k0 + kRanks * l >= rank16) break;
+            for (int x = 0; x < 4; ++x) acc[m][q][x] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWords; w += 2) {
-          const uint32_t a[4] = {b[d][l][0][w], b[d][l][1][w], b[d][l][0][w + 1],
-                                 b[d][l][1][w + 1]};
+        for (int l = 0; l < NL; ++l) {
+          uint32_t h[PARTS][kWords];
 #pragma unroll
-          for (int p = 0; p < PARTS; ++p) mma16816(acc[p], a, h[d][l][p][w], h[d][l][p][w + 1]);
+          for (int q = 0; q < PARTS; ++q)
+            load_words<W>(hs + q * (BT * PITCH) + h_offset<PITCH>(col, l * 4 * W + c * W), h[q]);
+#pragma unroll
+          for (int w = 0; w < kWords; w += 2)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const uint32_t a[4] = {b[m][l][0][w], b[m][l][1][w], b[m][l][0][w + 1],
+                                     b[m][l][1][w + 1]};
+#pragma unroll
+              for (int q = 0; q < PARTS; ++q) mma16816(acc[m][q], a, h[q][w], h[q][w + 1]);
+            }
         }
-      }
-      const uint32_t mine = info[d], mask = mine >> (8 + 2 * c);
-      load(d, i + D);
-      if (half + 1 < halves) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float v = acc[0][e] + acc[1][e];
-        if constexpr (PARTS == 3) v += acc[2][e];
-        if (mask >> (e & 1) & 1) out[e] = v;
+        for (int y = 0; y < 2; ++y) {  // columns 2 c and 2 c + 1
+          if (2 * c + y >= live_cols) continue;
+          float *at = to + (two >> (8 * y) & 255) * kPitch;
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) acc[p][e] = 0.f;
-      }
-      if (mine >> 16 & 1) {
-        tmem_st_16x8(delta + ((uint32_t)row0 << 16) + 8 * (mine & 255), out);
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[e] = 0.f;
+            for (int x = 0; x < 2; ++x) {  // rows r and r + 8
+              float v = acc[m][0][2 * x + y] + acc[m][1][2 * x + y];
+              if constexpr (PARTS == 3) v += acc[m][2][2 * x + y];
+              if (half > 0) v += at[16 * m + 8 * x];
+              at[16 * m + 8 * x] = v;
+            }
+        }
       }
     }
   }
+  return good;
 }
 
-// The adapter that all tokens of the tile have, -1 if none has any, -2 if it is mixed.  (A whole warp.)
-template <int BT>
-__device__ __forceinline__ int tile_adapter(const AdaptArgs &g, int tok0, int live) {
-  const int lane = threadIdx.x & 31;
-  const int one = token_id(g, tok0);
-  bool same = true;
-#pragma unroll
-  for (int i = 0; i < (BT + 31) / 32; ++i)
-    if (32 * i + lane < live) same = same && token_id(g, tok0 + 32 * i + lane) == one;
-  return __all_sync(0xffffffffu, same) ? one : -2;
-}
-
-template <int BT, typename TO, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, Cfg<BT, TO, SPLIT>::kTwo ? 2 : 1)
+template <int BT, int PITCH, typename TO, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
     adapt_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
-                 const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mh,
-                 const __grid_constant__ AdaptArgs g, int splits) {
-  using C = Cfg<BT, TO, SPLIT>;
-  constexpr int S = C::kStages;
+                 const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mu,
+                 const __grid_constant__ CUtensorMap mh, const __grid_constant__ AdaptArgs g,
+                 int splits) {
+  using C = Cfg<BT, PITCH, TO>;
+  constexpr int S = C::kStages, E = kSlots<PITCH>;
   extern __shared__ unsigned char dsm_raw[];
-  __shared__ __align__(8) uint64_t full[S], empty[S], done, drain;
+  __shared__ __align__(8) uint64_t full[S], empty[S], b_full[E], b_empty[E], list, done, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
   __shared__ float s_gone;  // SPLIT: another CTA of the cluster gave up
-  __shared__ Tasks<BT> s_tasks;
+  __shared__ Groups<BT> s_groups;
   unsigned char *smem = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
   auto tile_w = [&](int s) { return smem + s * C::kStage; };
   auto tile_x = [&](int s) { return smem + s * C::kStage + kTileW; };
+  unsigned char *ring_b = smem + S * C::kStage;
+  unsigned char *hs = ring_b + kRingB;
+  float *delta = reinterpret_cast<float *>(hs + C::kH);  // [token][kPitch]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int part = SPLIT ? (int)cluster_rank() : 0;
@@ -319,6 +380,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO, SPLIT>::kTwo ? 2 : 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
+    for (int e = 0; e < E; ++e) {
+      mbar_init(&b_full[e], 1);
+      mbar_init(&b_empty[e], 4);
+    }
+    mbar_init(&list, 1);
     mbar_init(&done, 1);
     mbar_init(&drain, 1);
     s_abort = 0;
@@ -326,21 +392,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO, SPLIT>::kTwo ? 2 : 1)
     mbar_fence_init();
     for (int kb = 0; kb < S && kb < plain; ++kb) load_plain(kb);  // nothing else is needed for these
   }
-  // and, of a tile with one adapter, those of 64 ranks of a part of h each: from eb0 on
-  const int one = tile_adapter<BT>(g, tok0, live);
+  // the adapter that all tokens of the tile have, -1 if none has any, -2 if it is mixed (adapters i
+  // with i % splits == part are then this CTA's)
+  bool same = true;
+  int one = token_id(g, tok0);
+  if (tid < live) {
+    const int id = token_id(g, tok0 + tid);
+    same = id == one;
+    s_groups.id[tid] = id >= 0 && id % splits == part ? id : -1;
+  } else if (tid < BT) {
+    s_groups.id[tid] = -1;
+  }
+  __syncwarp();
+  if (warp == 1) tc::tmem_alloc(&tmem_slot, C::kTmem);
+  tc::fence_before_sync();
+  if (!__syncthreads_and(same)) one = -2;
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  // the k-blocks of a tile with one adapter: 64 ranks of a part of h each, from eb0 on
   const int extra = one >= 0 ? (g.rank + kBK - 1) / kBK * C::kParts : 0;
   const int eb0 = extra * part / splits;
   const int kbs = plain + extra * (part + 1) / splits - eb0;
-  if (warp == 1) tc::tmem_alloc(&tmem_slot, C::kTmem);
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = tmem_slot;
-  if constexpr (SPLIT) {
-    __syncwarp();
-    cluster_arrive();  // (waited for before the first store to another CTA)
-  }
+  const int halves = g.rank_pad() * 2 / PITCH;
   volatile int *abort_flag = &s_abort;
+  const RingB ring{ring_b, b_full, b_empty, plain_rows(g, PITCH)};
   auto fail = [&]() {
     *abort_flag = 1;
     raise_error(g.err, GDN_DEVERR_TIMEOUT);
@@ -360,12 +435,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO, SPLIT>::kTwo ? 2 : 1)
       } else {
         // (rows of h behind the last token are another part's: columns that are not stored)
         const int e = eb0 + kb - plain, c = e / C::kParts, p = e % C::kParts;
+        mbar_arrive_expect_tx(&full[s], C::kStage);
+        tma_load2(tile_w(s), &mb, c * kBK, one * g.n_out + n0, &full[s]);
         if (kb == plain) {
           kv::dependent_wait();
           asm volatile("fence.proxy.async.global;" ::: "memory");  // plain stores, read by TMA
         }
-        mbar_arrive_expect_tx(&full[s], C::kStage);
-        tma_load2(tile_w(s), &mb, c * kBK, one * g.n_out + n0, &full[s]);
         tma_load2(tile_x(s), &mh, c * kBK, p * g.tokens + tok0, &full[s]);
       }
       issued = kb + 1;
@@ -373,6 +448,37 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO, SPLIT>::kTwo ? 2 : 1)
     if (*abort_flag) {  // let the copies still in flight land before the CTA exits
       for (int kb = issued - S < 0 ? 0 : issued - S; kb < issued; ++kb)
         mbar_wait_bounded(&full[kb % S], (kb / S) & 1);
+    }
+  } else if (warp == 2 + kHelpers / 32) {
+    // a lane per slot of the ring of B tiles
+    if (one == -2) {
+      bool good = __all_sync(0xffffffffu, wait(&list, 0, abort_flag));
+      const int units = good ? s_groups.n * halves : 0;
+      int u = lane < E ? lane : units, issued = -1;
+      uint32_t idle = 0;
+      while (good && __any_sync(0xffffffffu, u < units)) {
+        bool moved = false;
+        if (u < units && (u < E || mbar_test_wait(&b_empty[lane], ((u / E) - 1) & 1))) {
+          const int half = u >= s_groups.n, group = u - half * s_groups.n;
+          const int row = s_groups.adapter[group] * g.n_out + n0;
+          unsigned char *tile = ring_b + lane * (kBM * PITCH);
+          if (ring.plain) {
+            const uint32_t bytes = (uint32_t)min(kBM, g.n_out - n0) * PITCH;
+            mbar_arrive_expect_tx(&b_full[lane], bytes);
+            bulk_g2s(tile, static_cast<const bf16 *>(g.b) + row * g.ld_b, bytes, &b_full[lane]);
+          } else {
+            mbar_arrive_expect_tx(&b_full[lane], kBM * PITCH);
+            tma_load2(tile, &mu, half * (PITCH / 2), row, &b_full[lane]);
+          }
+          issued = u;
+          u += E;
+          moved = true;
+        }
+        idle = __any_sync(0xffffffffu, moved) ? 0 : idle + 1;
+        if (idle > (1u << 24)) fail();  // seconds
+        if ((idle & 15) == 15) good = !__any_sync(0xffffffffu, *abort_flag != 0);
+      }
+      if (!good && issued >= 0) mbar_wait_bounded(&b_full[lane], (issued / E) & 1);
     }
   } else if (warp == 1 && lane == 0) {
     // MMA issuer
@@ -400,40 +506,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO, SPLIT>::kTwo ? 2 : 1)
     tc::mma_commit(good ? &done : &drain);
     if (!good) mbar_wait_bounded(&drain, 0);  // MMAs in flight finish before TMEM is freed
   } else if (warp >= 2) {
-    const int quad = warp & 3, side = (warp - 2) >> 2;  // TMEM lanes 32 quad .., two warps to each
-    // the adapters' part of rows 32 quad + 16 side .. + 15
-    const int row0 = 32 * quad + 16 * side;
-    const uint32_t delta = tmem + C::kAcc * BT;
     if (one >= 0) {  // B on its way to L2
       const bf16 *b = static_cast<const bf16 *>(g.b) +
-                      ((int64_t)one * g.n_out + min(n0 + row0 + (lane & 15), g.n_out - 1)) * g.ld_b +
-                      (lane >> 4) * 64;
-      if ((lane >> 4) * 64 < g.rank) prefetch_l2(b);
+                      ((int64_t)one * g.n_out + min(n0 + (tid - 64) / 4, g.n_out - 1)) * g.ld_b +
+                      (tid & 3) * 64;
+      if ((tid & 3) * 64 < g.rank) prefetch_l2(b);
     } else if (one == -2) {
-      list_tasks<BT>(g, tok0, live, part, splits, s_tasks);
-      // B on its way to L2 meanwhile
-      const bf16 *mine = static_cast<const bf16 *>(g.b) +
-                         min(n0 + row0 + (lane & 15), g.n_out - 1) * g.ld_b + (lane >> 4) * 64;
-      for (int i = 0; i < s_tasks.n; ++i)
-        if (s_tasks.task[i].mask != 0 && (lane >> 4) * 64 < g.rank)
-          prefetch_l2(mine + s_tasks.task[i].b);
+      find_groups<BT>(s_groups);
+      if (tid == 64) mbar_arrive(&list);
+      for (int t = warp - 2; t < live; t += kHelpers / 32)  // tokens that get nothing from this CTA
+        if (s_groups.id[t] < 0)
+          reinterpret_cast<float4 *>(delta + t * kPitch)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
       kv::dependent_wait();  // h
-      if (g.rank == 16)
-        expand<BT, 8, 1, 6, false, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
-      else if (g.rank == 32)
-        expand<BT, 16, 1, 4, false, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
-      else if (g.rank == 64 || g.rank == 128)
-        expand<BT, 16, 2, 2, false, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
-      else
-        expand<BT, 8, 4, 1, true, C::kParts>(g, s_tasks, n0, row0, tok0, delta);
-      tc::tmem_st_wait();
-      tc::fence_before_sync();
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (!expand<BT, PITCH, C::kParts>(g, s_groups, ring, warp - 2, tok0, live, hs, delta,
+                                        abort_flag))
+        fail();
+      helpers_sync();
     }
-    // epilogue: a lane per output row, the two warps take turns in the columns
-    const int row = 32 * quad + lane, n = n0 + row;
-    __syncwarp();
-    if constexpr (SPLIT) cluster_wait();  // the others run
+    if constexpr (SPLIT) {
+      __syncwarp();
+      cluster_arrive();  // the B tiles' place may be written by the others
+      cluster_wait();
+    }
+    // epilogue: a lane per output row, the four warps of TMEM lanes 32 quad .. take turns in the columns
+    const int quad = warp & 3, side = (warp - 2) >> 2, row = 32 * quad + lane, n = n0 + row;
     // warp-uniform decision: tcgen05.ld is a whole-warp instruction
     const bool got = __all_sync(0xffffffffu, wait(&done, 0, abort_flag));
     if (!got) {
@@ -441,20 +537,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO, SPLIT>::kTwo ? 2 : 1)
     } else {
       tc::fence_after_sync();
       // SPLIT: CTA i of the cluster adds up tokens i * share ..; it receives [splits][share][128]
-      float *recv = reinterpret_cast<float *>(smem + S * C::kStage);
-      const int share = BT / splits;
+      float *recv = reinterpret_cast<float *>(ring_b);
+      const int share = (BT + splits - 1) / splits;
       TO *y = static_cast<TO *>(g.y);
       const uint32_t mine = tmem + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
-      for (int c = 16 * side; c < live; c += 32) {
-        float v[32];
-        if (one == -2) {
-          tc::tmem_ld32(mine + c, mine + C::kAcc * BT + c, v);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
-        } else {
-          tc::tmem_ld16(mine + c, v);
-        }
+      for (int c = 16 * side; c < live; c += 64) {
+        float v[16];
+        tc::tmem_ld16(mine + c, v);
         if constexpr (C::kAcc == 3) {
           float u[32];
           if (kbs > 2) {
@@ -466,6 +556,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO, SPLIT>::kTwo ? 2 : 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] += u[j];
           }
+        }
+        if (one == -2) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < live) v[j] += delta[(c + j) * kPitch + row];
         }
         if constexpr (SPLIT) {
 #pragma unroll
@@ -481,6 +576,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO, SPLIT>::kTwo ? 2 : 1)
       }
     }
   }
+  if constexpr (SPLIT) {
+    __syncwarp();
+    if (warp < 2 || warp >= 2 + kHelpers / 32) cluster_arrive();
+  }
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 1) {
@@ -489,13 +588,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT, TO, SPLIT>::kTwo ? 2 : 1)
   }
   if constexpr (SPLIT) {
     __syncwarp();
-    if (warp < 2) cluster_wait();
+    if (warp < 2 || warp >= 2 + kHelpers / 32) cluster_wait();
     if (*abort_flag)
       for (int p = 0; p < splits; ++p) st_peer(&s_gone, p, 1.f);
     cluster_arrive();
     cluster_wait();
-    const float *recv = reinterpret_cast<const float *>(smem + S * C::kStage);
-    const int share = BT / splits, mine = min(share, live - part * share);
+    const float *recv = reinterpret_cast<const float *>(ring_b);
+    const int share = (BT + splits - 1) / splits, mine = min(share, live - part * share);
     for (int i = tid; s_gone == 0.f && i < mine * kBM; i += kThreads) {
       const int t = i / kBM, n = n0 + i % kBM;
       float sum = 0.f;
@@ -524,64 +623,73 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return encode;
 }
 
-// [rows][cols] bf16 with row stride ld elements, box {64, box_rows}, 128-byte swizzle
+// [rows][cols] bf16 with row stride ld elements, boxes of box_cols (16, 32 or 64) x box_rows in the
+// swizzle of that width
 bool encode_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
-                 int box_rows) {
+                 int box_rows, int box_cols = kBK) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (encode == nullptr) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t elem[2] = {1, 1};
+  const CUtensorMapSwizzle swizzle = box_cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                      : CU_TENSOR_MAP_SWIZZLE_32B;
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
-                box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
 
-template <int BT, typename TO, bool SPLIT>
+template <int BT, int PITCH, typename TO, bool SPLIT>
 cudaError_t launch(const AdaptArgs &g, int splits, cudaStream_t s) {
-  using C = Cfg<BT, TO, SPLIT>;
-  CUtensorMap mw, mx, mb, mh;
+  using C = Cfg<BT, PITCH, TO>;
+  CUtensorMap mw, mx, mb, mu, mh;
+  const int64_t rows_b = (int64_t)g.n_adapters * g.n_out, ld = g.rank_pad();
   if (!encode_rows(&mw, g.w, g.n_out, g.hidden, g.ld_w, kBM) ||
       !encode_rows(&mx, g.x, g.tokens, g.hidden, g.ld_x, BT) ||
-      !encode_rows(&mb, g.b, (int64_t)g.n_adapters * g.n_out, g.rank, g.ld_b, kBM) ||
-      !encode_rows(&mh, g.h, (int64_t)C::kParts * g.tokens, g.rank16(), g.rank16(), BT))
+      !encode_rows(&mb, g.b, rows_b, g.rank, g.ld_b, kBM) ||
+      !encode_rows(&mu, g.b, rows_b, g.rank, g.ld_b, kBM, PITCH / 2) ||
+      !encode_rows(&mh, g.h, (int64_t)C::kParts * g.tokens, ld, ld, BT))
     return cudaErrorNotSupported;
   static std::atomic<uint64_t> seen{0};
-  const cudaError_t e = kv::allow_smem(adapt_kernel<BT, TO, SPLIT>, C::kSmem, g.device, seen);
+  const cudaError_t e =
+      kv::allow_smem(adapt_kernel<BT, PITCH, TO, SPLIT>, C::kSmem, g.device, seen);
   if (e != cudaSuccess) return e;
   const int tiles = (g.n_out + kBM - 1) / kBM, rows = (g.tokens + BT - 1) / BT;
-  return kv::launch(adapt_kernel<BT, TO, SPLIT>, dim3((unsigned)(tiles * splits), (unsigned)rows),
-                    kThreads, C::kSmem, s, splits, mw, mx, mb, mh, g, splits);
+  return kv::launch(adapt_kernel<BT, PITCH, TO, SPLIT>,
+                    dim3((unsigned)(tiles * splits), (unsigned)rows), kThreads, C::kSmem, s, splits,
+                    mw, mx, mb, mu, mh, g, splits);
+}
+
+template <int BT, int PITCH, typename TO>
+cudaError_t launch_split(const AdaptArgs &g, cudaStream_t s) {
+  const int64_t tiles = (int64_t)((g.n_out + kBM - 1) / kBM) * ((g.tokens + BT - 1) / BT);
+  const int blocks = (g.hidden + kBK - 1) / kBK;
+  // CTAs that share a tile: as many as fit on the device at once, with four k-blocks each at least
+  const int64_t most = g.sm_count / tiles < blocks / 4 ? g.sm_count / tiles : blocks / 4;
+  const int splits = most > 8 ? 8 : (int)most;
+  return splits > 1 ? launch<BT, PITCH, TO, true>(g, splits, s)
+                    : launch<BT, PITCH, TO, false>(g, 1, s);
 }
 
 template <int BT, typename TO>
 cudaError_t launch_bt(const AdaptArgs &g, cudaStream_t s) {
-  const int64_t tiles = (int64_t)((g.n_out + kBM - 1) / kBM) * ((g.tokens + BT - 1) / BT);
-  const int blocks = (g.hidden + kBK - 1) / kBK;
-  // CTAs that share a tile: so many that every multiprocessor has one, with four k-blocks each at
-  // least (one token, 2048 -> 12352: 194 CTAs 15 us, 97 CTAs 17; 64 tokens with an adapter each of
-  // rank 64: 61 and 79)
-  int splits = 1;
-  while (splits * tiles < g.sm_count && splits < 8 && blocks >= 8 * splits) splits *= 2;
-  return splits > 1 ? launch<BT, TO, true>(g, splits, s) : launch<BT, TO, false>(g, 1, s);
+  return g.rank <= 16   ? launch_split<BT, 32, TO>(g, s)
+         : g.rank <= 32 ? launch_split<BT, 64, TO>(g, s)
+                        : launch_split<BT, 128, TO>(g, s);
 }
 
 template <typename TO>
 cudaError_t launch_t(const AdaptArgs &g, cudaStream_t s) {
-  if (g.tokens <= 16) return launch_bt<16, TO>(g, s);
-  // tiles of 128 tokens read W half as often, if there is one for every multiprocessor
-  const int64_t wide = (int64_t)((g.n_out + kBM - 1) / kBM) * ((g.tokens + 127) / 128);
-  if (g.tokens <= 64 || wide < g.sm_count) return launch_bt<64, TO>(g, s);
-  return launch<128, TO, false>(g, 1, s);
+  return g.tokens <= 16 ? launch_bt<16, TO>(g, s) : launch_bt<64, TO>(g, s);
 }
 
 }  // namespace
 
 size_t adapt_workspace_bytes(const AdaptArgs &g) {
-  // (eight rows more: the tokens are read by eights)
-  return ((size_t)g.tokens * g.parts() + 8) * g.rank16() * 2;
+  return (size_t)g.tokens * g.parts() * g.rank_pad() * 2;
 }
 
 cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s) {

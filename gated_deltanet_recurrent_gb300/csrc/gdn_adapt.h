@@ -15,12 +15,14 @@ struct AdaptArgs {
   int tokens, hidden, n_out, rank, n_adapters;
   gdn_dtype y_dtype;
   void *h;                    // workspace: scale * A x in bf16 parts that add up to it,
-                              // [parts][tokens][rank16], zeros beyond rank
+                              // [parts][tokens][rank_pad], zeros beyond rank
   unsigned int *err;
   int sm_count, device;
   GDN_HD int parts() const { return y_dtype == GDN_F32 ? 3 : 2; }
   // the rank rounded up to the tensor cores' 16
   GDN_HD int rank16() const { return (rank + 15) & ~15; }
+  // and to the width of the rows that the projection reads
+  GDN_HD int rank_pad() const { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 };
 
 size_t adapt_workspace_bytes(const AdaptArgs &g);

@@ -22,8 +22,11 @@ namespace {
 
 constexpr int kWarps = 8;
 
-// Elements k .. k + 7 of a row, zeros from `hidden` on (what lies behind a row is not read).
+// Elements k .. k + 7 of a row, zeros from `hidden` on (what lies behind a row is not read).  WHOLE:
+// hidden is a multiple of 8.
+template <bool WHOLE>
 __device__ __forceinline__ uint4 load8(const bf16 *row, int k, int hidden) {
+  if (WHOLE) return k < hidden ? *reinterpret_cast<const uint4 *>(row + k) : make_uint4(0, 0, 0, 0);
   if (k + 8 <= hidden) return *reinterpret_cast<const uint4 *>(row + k);
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -33,8 +36,9 @@ __device__ __forceinline__ uint4 load8(const bf16 *row, int k, int hidden) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// AHEAD: steps of 64 k whose loads a warp has in flight.
-template <int MT, int NT, int AHEAD>
+// AHEAD: steps of 64 k whose loads a warp has in flight.  (With the ends of odd rows looked at in
+// every load the code was so long that fetching it took longer than the work.)
+template <int MT, int NT, int AHEAD, bool WHOLE>
 __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
   constexpr int kTok = 16 * MT, kRanks = 8 * NT;
   extern __shared__ float s_part[];  // [kWarps][kTok][kRanks]
@@ -63,7 +67,7 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
         for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            xv[i][m][hh][c] = load8(xrow[m][hh], k0 + 64 * kWarps * i + 32 * c + 8 * col, g.hidden);
+            xv[i][m][hh][c] = load8<WHOLE>(xrow[m][hh], k0 + 64 * kWarps * i + 32 * c + 8 * col, g.hidden);
   };
   // x is on its way before the ids are known
   load_x(64 * warp);
@@ -92,7 +96,7 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
     if (lane == 0) s_n = n;
   }
   __syncthreads();
-  const int rank16 = g.rank16(), parts = g.parts();
+  const int rank_pad = g.rank_pad(), parts = g.parts();
   for (int gi = blockIdx.y; gi < s_n; gi += gridDim.y) {
     const int id = s_lead[gi];
     const float scale = g.scale[id];
@@ -113,7 +117,7 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int r = rank0 + 8 * n + row, k = k0 + 64 * kWarps * i + 32 * c + 8 * col;
-            av[i][n][c] = r < g.rank ? load8(a + r * g.ld_a, k, g.hidden) : make_uint4(0, 0, 0, 0);
+            av[i][n][c] = r < g.rank ? load8<WHOLE>(a + r * g.ld_a, k, g.hidden) : make_uint4(0, 0, 0, 0);
           }
       // (the first x of the first adapter are here already)
       if (gi != blockIdx.y || k0 != 64 * warp) load_x(k0);
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
     __syncthreads();
     for (int i = tid; i < kTok * kRanks / 2; i += 32 * kWarps) {  // two ranks a thread
       const int t = 2 * i / kRanks, r = rank0 + 2 * i % kRanks;
-      if (s_id[t] != id || r >= rank16) continue;
+      if (s_id[t] != id || r >= rank_pad) continue;
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -153,11 +157,11 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
       }
       // (zeros beyond the rank, whatever the scale is)
       float x = r < g.rank ? sum.x * scale : 0.f, y = r + 1 < g.rank ? sum.y * scale : 0.f;
-      uint32_t *h = static_cast<uint32_t *>(g.h) + ((int64_t)(tok0 + t) * rank16 + r) / 2;
+      uint32_t *h = static_cast<uint32_t *>(g.h) + ((int64_t)(tok0 + t) * rank_pad + r) / 2;
       for (int p = 0; p < parts; ++p) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
         const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
-        h[(int64_t)p * g.tokens * (rank16 / 2)] = w;
+        h[(int64_t)p * g.tokens * (rank_pad / 2)] = w;
         const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
         // (what is infinite or NaN is the first part alone)
         x = fabsf(lo) < INFINITY ? x - lo : 0.f;
@@ -168,18 +172,18 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
   }
 }
 
-template <int MT, int NT, int AHEAD>
+template <int MT, int NT, int AHEAD, bool WHOLE>
 cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
   constexpr int smem = kWarps * 16 * MT * 8 * NT * 4;
   static std::atomic<uint64_t> seen{0};
-  const cudaError_t e = kv::allow_smem(low_kernel<MT, NT, AHEAD>, smem, g.device, seen);
+  const cudaError_t e = kv::allow_smem(low_kernel<MT, NT, AHEAD, WHOLE>, smem, g.device, seen);
   if (e != cudaSuccess) return e;
   const int windows = (g.tokens + 16 * MT - 1) / (16 * MT);
-  const int parts = (g.rank16() + 8 * NT - 1) / (8 * NT);
+  const int parts = (g.rank_pad() + 8 * NT - 1) / (8 * NT);
   // CTAs that share a window: as many as it may have adapters, but no more than four waves in all
   const int64_t room = (int64_t)4 * g.sm_count / ((int64_t)windows * parts);
   const int share = (int)(room < 1 ? 1 : room > 16 * MT ? 16 * MT : room);
-  return kv::launch(low_kernel<MT, NT, AHEAD>, dim3((unsigned)windows, (unsigned)share, (unsigned)parts),
+  return kv::launch(low_kernel<MT, NT, AHEAD, WHOLE>, dim3((unsigned)windows, (unsigned)share, (unsigned)parts),
                     32 * kWarps, smem, s, 1, g);
 }
 
@@ -187,7 +191,8 @@ cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
 
 cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s) {
   // few tokens: small windows, for parallel loads of A; many: large ones, that read A less often
-  return g.tokens <= 256 ? launch<1, 2, 4>(g, s) : launch<4, 4, 1>(g, s);
+  if (g.hidden % 8 != 0) return launch<1, 2, 1, false>(g, s);
+  return g.tokens <= 256 ? launch<1, 2, 4, true>(g, s) : launch<4, 4, 1, true>(g, s);
 }
 
 }  // namespace gdn
