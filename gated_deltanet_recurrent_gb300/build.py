@@ -26,6 +26,7 @@ SOURCES = ["gdn_api.cu", "gdn_conv.cu", "gdn_decode.cu", "gdn_verify.cu", "gdn_p
            "gdn_prefill_split.cu", "gdn_norm.cu", "gdn_in_proj.cu", "gdn_kv_api.cu", "gdn_kv_cache.cu",
            "gdn_kv_attend.cu", "gdn_kv_prompt.cu", "gdn_kv_pages.cu",
            "gdn_rope.cu", "gdn_adapt.cu", "gdn_adapt_low.cu",
+           "gdn_adapt_pair.cu",
            "gdn_adapt_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",

@@ -28,23 +28,16 @@
 // push their parts into each other's shared memory, where they are added in a fixed order.  The
 // kernel starts under the low side's: W and B are on their way before h is complete.  Every wait is
 // bounded (GDN_DEVERR_TIMEOUT).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include "gdn_adapt.h"
-#include "gdn_kv.cuh"
-#include "gdn_mma.cuh"
-#include "gdn_tc.cuh"
+#include "gdn_adapt.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kBM = 128, kBK = 64;
-constexpr int kHelpers = 512;            // threads of the adapters' part and the epilogue
+using namespace adapt;
+
+constexpr int kHelpers = 512;            // threads: warps 2 .. 17
 constexpr int kThreads = 64 + kHelpers + 32;
 constexpr int kTeams = 4;                // of four warps
-constexpr int kTileW = kBM * kBK * 2;
-
 constexpr int kPitch = kBM + 4;      // floats of a token's row of the adapters' part
 constexpr int kRingB = 64 * 1024;    // bytes of the ring of B tiles
 
@@ -69,139 +62,6 @@ struct Cfg {
   static constexpr int kSmem = kStages * kStage + kRingB + kDelta + kH + 1024;
   static_assert(BT * kBM * 4 <= kRingB, "a cluster's parts take the place of the B tiles");
 };
-
-__device__ __forceinline__ void tma_load2(void *dst, const CUtensorMap *m, int x, int y,
-                                          uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_addr(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Store into the shared memory of CTA `rank` of the cluster, at the place of `p` in this one's.
-__device__ __forceinline__ void st_peer(const void *p, int rank, float v) {
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(smem_addr(p)),
-      "r"(rank), "f"(v)
-      : "memory");
-}
-__device__ __forceinline__ void prefetch_l2(const void *p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
-// (try_wait may suspend the thread for a while; lanes that look after a slot each must not)
-__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// A bounded wait that also ends when the CTA gives up.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-  for (uint32_t it = 0; it < (1u << 20); ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 15) == 15 && *abort_flag) return false;
-  }
-  return false;
-}
-
-__device__ __forceinline__ int token_id(const AdaptArgs &g, int t) {
-  const int id = t < g.tokens ? g.ids[t] : -1;
-  return id >= 0 && id < g.n_adapters ? id : -1;
-}
-
-__device__ __forceinline__ void helpers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kHelpers) : "memory");
-}
-
-// The groups of a mixed tile: tokens with one adapter, and the tasks, up to eight tokens of a group
-// each.  Groups are in the order of their first tokens, tasks in the order of the groups.
-template <int BT>
-struct Groups {
-  int id[BT];                   // per token: its adapter if it is this CTA's to do, or -1
-  int adapter[BT];              // per group
-  unsigned char first[BT];      // of a group: its first task, and how many there are
-  unsigned char count[BT];
-  unsigned char start[BT];      // per token that is the first of a group: the group's first task
-  unsigned char tokens[BT];     // per task: how many of the eight there are
-  alignas(8) unsigned char token[BT][8];
-  int sums[2];
-  int n;
-};
-
-// Run by the helpers, with s.id set.
-template <int BT>
-__device__ __forceinline__ void find_groups(Groups<BT> &s) {
-  const int tid = threadIdx.x - 64;
-  // eight threads per token look for the same adapter among the others
-  const int token = tid >> 3, id = token < BT ? s.id[token < BT ? token : 0] : -1;
-  int lead = BT, rank = 0, size = 0;
-  for (int j = tid & 7; j < BT; j += 8)
-    if (id >= 0 && s.id[j] == id) {
-      lead = min(lead, j);
-      rank += j < token;
-      ++size;
-    }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    lead = min(lead, __shfl_xor_sync(0xffffffffu, lead, o));
-    rank += __shfl_xor_sync(0xffffffffu, rank, o);
-    size += __shfl_xor_sync(0xffffffffu, size, o);
-  }
-  const bool first = (tid & 7) == 0 && id >= 0;
-  if (first) s.adapter[token] = lead == token ? size : 0;  // (for now: of a group's first token, its size)
-  else if ((tid & 7) == 0 && token < BT) s.adapter[token] = 0;
-  helpers_sync();
-  // groups (upper half) and tasks (lower half) before each token
-  const int mine = tid < BT && s.adapter[tid] > 0 ? (1 << 16) + (s.adapter[tid] + 7) / 8 : 0;
-  const int own = tid < BT ? s.adapter[tid] : 0;
-  int sum = mine;
-  if (tid < 64) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, sum, o);
-      if ((tid & 31) >= o) sum += y;
-    }
-    if ((tid & 31) == 31) s.sums[tid >> 5] = sum;
-  }
-  helpers_sync();
-  const int before = sum - mine + (tid >= 32 ? s.sums[0] : 0);
-  if (tid < BT && own > 0) {
-    const int at = before >> 16, tasks = (own + 7) / 8;
-    s.adapter[at] = s.id[tid];  // (at <= tid: every thread has read its place)
-    s.first[at] = s.start[tid] = (unsigned char)before;
-    s.count[at] = (unsigned char)tasks;
-    for (int i = 0; i < tasks; ++i) s.tokens[(before & 255) + i] = (unsigned char)min(8, own - 8 * i);
-  }
-  if (tid == 0) s.n = (s.sums[0] + s.sums[1]) >> 16;
-  helpers_sync();
-  if (first) {
-    s.token[s.start[lead] + rank / 8][rank % 8] = (unsigned char)token;
-    // (the last task's empty columns have the group's first token, and are dropped)
-    if (rank + 1 == size)
-      for (int i = size; i & 7; ++i) s.token[s.start[lead] + i / 8][i % 8] = (unsigned char)lead;
-  }
-  helpers_sync();
-}
 
 // A ring of B tiles of 128 rows of PITCH bytes.  Rows of just that width that follow each other come
 // as one piece (`plain`): a tensor copy takes some three cycles for each row, be it 32 bytes long
@@ -230,17 +90,6 @@ __device__ __forceinline__ int h_offset(int token, int byte) {
   return token * PITCH + (PITCH == 128 ? byte ^ ((token & 1) << 6) : byte);
 }
 
-template <int W>
-__device__ __forceinline__ void load_words(const void *p, uint32_t *out) {
-  if constexpr (W == 8) {
-    const uint2 v = *static_cast<const uint2 *>(p);
-    out[0] = v.x, out[1] = v.y;
-  } else {
-    const uint4 v = *static_cast<const uint4 *>(p);
-    out[0] = v.x, out[1] = v.y, out[2] = v.z, out[3] = v.w;
-  }
-}
-
 // Run by the helpers (`warp` of them): all groups of the tile.  Unit u = half * n + group is PITCH / 2
 // ranks of a group's B; it is team u % 4's, in which a warp takes 32 of its rows, as two fragments.
 // Lane (r, c) of a fragment has rows r and r + 8 of B and token r of a task, for each W bytes the same
@@ -258,7 +107,7 @@ __device__ __forceinline__ bool expand(const AdaptArgs &g, const Groups<BT> &s, 
   float *const to = delta + row0 + r;
   bool good = true;
   for (int half = 0; half < halves; ++half) {
-    if (half > 0) helpers_sync();  // the first half has been read
+    if (half > 0) helpers_sync<kHelpers>();  // the first half has been read
     // h of the tokens that have an adapter here (nothing else of it is defined, nor read)
     for (int i = 32 * warp + lane; i < PARTS * live * (PITCH / 16); i += kHelpers) {
       const int q = i / (live * (PITCH / 16)), rest = i % (live * (PITCH / 16));
@@ -269,7 +118,7 @@ __device__ __forceinline__ bool expand(const AdaptArgs &g, const Groups<BT> &s, 
               static_cast<const unsigned char *>(g.h) +
               (((int64_t)q * g.tokens + tok0 + t) * ld * 2 + half * PITCH + at));
     }
-    helpers_sync();
+    helpers_sync<kHelpers>();
     // (units of both halves go round the teams and slots in one order)
     for (int u = half * s.n + ((team - half * s.n) & (kTeams - 1)); good && u < (half + 1) * s.n;
          u += kTeams) {
@@ -512,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       (tid & 3) * 64;
       if ((tid & 3) * 64 < g.rank) prefetch_l2(b);
     } else if (one == -2) {
-      find_groups<BT>(s_groups);
+      find_groups<BT, kHelpers>(s_groups);
       if (tid == 64) mbar_arrive(&list);
       for (int t = warp - 2; t < live; t += kHelpers / 32)  // tokens that get nothing from this CTA
         if (s_groups.id[t] < 0)
@@ -521,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!expand<BT, PITCH, C::kParts>(g, s_groups, ring, warp - 2, tok0, live, hs, delta,
                                         abort_flag))
         fail();
-      helpers_sync();
+      helpers_sync<kHelpers>();
     }
     if constexpr (SPLIT) {
       __syncwarp();
@@ -608,40 +457,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   kv::dependent_wait();
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      fn = nullptr;
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }();
-  return encode;
-}
-
-// [rows][cols] bf16 with row stride ld elements, boxes of box_cols (16, 32 or 64) x box_rows in the
-// swizzle of that width
-bool encode_rows(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld,
-                 int box_rows, int box_cols = kBK) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  if (encode == nullptr) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-  cuuint32_t elem[2] = {1, 1};
-  const CUtensorMapSwizzle swizzle = box_cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
-                                     : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                      : CU_TENSOR_MAP_SWIZZLE_32B;
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides,
-                box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
-}
-
 template <int BT, int PITCH, typename TO, bool SPLIT>
 cudaError_t launch(const AdaptArgs &g, int splits, cudaStream_t s) {
   using C = Cfg<BT, PITCH, TO>;
@@ -681,6 +496,8 @@ cudaError_t launch_bt(const AdaptArgs &g, cudaStream_t s) {
                         : launch_split<BT, 128, TO>(g, s);
 }
 
+constexpr int kFewTokens = 128;
+
 template <typename TO>
 cudaError_t launch_t(const AdaptArgs &g, cudaStream_t s) {
   return g.tokens <= 16 ? launch_bt<16, TO>(g, s) : launch_bt<64, TO>(g, s);
@@ -695,6 +512,7 @@ size_t adapt_workspace_bytes(const AdaptArgs &g) {
 cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s) {
   const cudaError_t e = launch_adapt_low(g, s);
   if (e != cudaSuccess) return e;
+  if (g.tokens > kFewTokens) return launch_adapt_pair(g, s);
   return g.y_dtype == GDN_F32 ? launch_t<float>(g, s) : launch_t<bf16>(g, s);
 }
 

@@ -29,6 +29,9 @@ size_t adapt_workspace_bytes(const AdaptArgs &g);
 // The low side, then the projection; cudaErrorNotSupported: no tensor map.
 cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s);
 
+// The projection of many tokens, on pairs of CTAs.
+cudaError_t launch_adapt_pair(const AdaptArgs &g, cudaStream_t s);
+
 cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s);
 
 }  // namespace gdn

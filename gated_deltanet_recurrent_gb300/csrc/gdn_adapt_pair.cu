@@ -1,0 +1,496 @@
+// The projection with adapters for many tokens (see gdn_adapt.cu for the mathematics and for calls of
+// few): pairs of CTAs on the 5th-generation tensor cores, tcgen05.mma cta_group::2.
+//
+// A pair's tile is 256 outputs x BT tokens.  Each CTA holds 128 rows of W and half of the tokens of x,
+// and both halves of the products: 32 KiB of operands per k-block and CTA for 256 x 256 x 64, two thirds
+// of what a CTA alone needs for as much work, so that a ring of six covers the copies' latency.  The
+// pairs walk the tiles, output blocks fastest (W stays in L2).
+//
+//   warp 0      one lane: TMA into this CTA's ring, reported to CTA 0's barriers
+//   warp 1      one lane of CTA 0: tcgen05.mma for both, commits to both
+//   warps 2..13 the adapters' part of mixed tiles, then the epilogue
+//   warp 14     looks a few tiles ahead: which have one adapter, or none
+//
+// A tile whose tokens have one adapter (most of a prompt) takes it as further k-blocks: B tiles for W's
+// and the parts of h for x's.  In a mixed tile the helpers multiply B and h with mma.sync while the
+// tensor core computes W x: four warps with 32 output rows each take the tasks (up to eight tokens of
+// one adapter) in turn, with B and h from global memory, and store them to TMEM columns [token][row] of
+// their own, which the epilogue adds.  For a bf16 y these are the columns of the next tile's accumulator,
+// which then starts after the epilogue; for a float32 y, of 128 tokens, there are columns for the three
+// accumulators (see gdn_adapt.cu) and these.
+#include "gdn_adapt.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace adapt;
+
+constexpr int kTeams = 3;      // of four warps (with four, a thread has 96 registers, which do not suffice)
+constexpr int kWarps = 4 * kTeams;
+constexpr int kHelpers = 32 * kWarps;
+constexpr int kThreads = 64 + kHelpers + 32;
+constexpr int kInfo = 8;  // tiles looked ahead
+
+template <typename TO>
+struct Cfg {
+  static constexpr bool kF32 = sizeof(TO) == 4;
+  static constexpr int kParts = kF32 ? 3 : 2;
+  static constexpr int BT = kF32 ? 128 : 256;
+  static constexpr int kAcc = kF32 ? 3 : 1;
+  static constexpr int kStage = kTileW + BT / 2 * kBK * 2;
+  static constexpr int kStages = 6;
+  static constexpr int kScratch = kWarps * 8 * 33 * 4;
+  static constexpr int kSmem = kStages * kStage + kScratch + 1024;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+}
+__device__ __forceinline__ uint32_t leader_addr(const void *p) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(p)));
+  return a;
+}
+// to this CTA's shared memory, reported to a barrier of CTA 0
+__device__ __forceinline__ void tma_load2_pair(void *dst, const CUtensorMap *m, int x, int y,
+                                               uint32_t leader_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(leader_bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_leader(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_addr(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr),
+               "r"(__float_as_uint(v))
+               : "memory");
+}
+
+// Ranks e .. e + W / 2 - 1 of a row of B, zeros from `rank` on (what lies behind a row is not read).
+template <int W>
+__device__ __forceinline__ void load_b(const bf16 *row, int e, int rank, uint32_t *out) {
+#pragma unroll
+  for (int w = 0; w < W / 4; ++w) out[w] = 0;
+  if (e + W / 2 <= rank) {
+    load_words<W>(row + e, out);
+  } else if (e < rank) {
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j)
+      if (e + j < rank)
+        out[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row)[e + j] << (16 * (j & 1));
+  }
+}
+
+// Run by the helpers (`warp` of them; `quad`: the TMEM lanes it may write, 32 quad ..): every third
+// task.  Lane (r, c) of a fragment has rows r and r + 8 of B and token r of the task, for each W bytes
+// the same ranks (W / 2 neighbours: the order of K does not matter); NL such loads at a time, HALVES
+// times.  B stays in registers while the group does, and the h of the team's next task is on its way
+// under a task's results, unless there are two halves.
+template <int BT, int W, int NL, int HALVES, int PARTS>
+__device__ __forceinline__ void expand(const AdaptArgs &g, const Groups<BT> &s, int warp, int quad,
+                                       int n0, int tok0, float *scratch, uint32_t delta) {
+  constexpr int kWords = W / 4;
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3, team = warp >> 2;
+  const int ld = g.rank_pad();
+  const int64_t part = (int64_t)g.tokens * ld;
+  const bf16 *h0 = static_cast<const bf16 *>(g.h) + (int64_t)tok0 * ld + c * (W / 2);
+  uint32_t b[2][NL][2][kWords], h[NL][PARTS][kWords];
+  auto load_h = [&](int t, int half) {
+    const bf16 *p = h0 + s.token[t][r] * ld + half * (NL * 2 * W);
+#pragma unroll
+    for (int l = 0; l < NL; ++l)
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) load_words<W>(p + q * part + l * 2 * W, h[l][q]);
+  };
+  auto load_rows = [&](int group, int half) {
+    const bf16 *b0 = static_cast<const bf16 *>(g.b) + (int64_t)s.adapter[group] * g.n_out * g.ld_b;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const bf16 *row = b0 + min(n0 + 32 * quad + 16 * m + 8 * y + r, g.n_out - 1) * g.ld_b;
+#pragma unroll
+        for (int l = 0; l < NL; ++l)
+          load_b<W>(row, (half * NL + l) * 2 * W + c * (W / 2), g.rank, b[m][l][y]);
+      }
+  };
+  int group = -1;
+  if (HALVES == 1 && team < s.tasks) load_h(team, 0);
+  for (int t = team; t < s.tasks; t += kTeams) {
+    float acc[2][PARTS][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[m][q][x] = 0.f;
+    if (HALVES == 1 && s.group[t] != group) load_rows(group = s.group[t], 0);
+#pragma unroll 1
+    for (int half = 0; half < HALVES; ++half) {
+      if (HALVES > 1) {
+        load_rows(s.group[t], half);
+        load_h(t, half);
+      }
+#pragma unroll
+      for (int l = 0; l < NL; ++l)
+#pragma unroll
+        for (int w = 0; w < kWords; w += 2)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint32_t a[4] = {b[m][l][0][w], b[m][l][1][w], b[m][l][0][w + 1],
+                                   b[m][l][1][w + 1]};
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) mma16816(acc[m][q], a, h[l][q][w], h[l][q][w + 1]);
+          }
+    }
+    if (HALVES == 1 && t + kTeams < s.tasks) load_h(t + kTeams, 0);
+    // from fragments to a row a lane
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float v = acc[m][0][x] + acc[m][1][x];
+        if constexpr (PARTS == 3) v += acc[m][2][x];
+        scratch[(2 * c + (x & 1)) * 33 + 16 * m + 8 * (x >> 1) + r] = v;
+      }
+    __syncwarp();
+    const int cols = s.tokens[t];
+    for (int j = 0; j < cols; ++j) tmem_st1(delta + s.token[t][j], scratch[j * 33 + lane]);
+  }
+}
+
+// Among the helpers: whether all say so.
+__device__ __forceinline__ bool helpers_and(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "n"(kHelpers)
+      : "memory");
+  return r != 0;
+}
+
+template <typename TO>
+__global__ void __launch_bounds__(kThreads, 1)
+    adapt_pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
+                      const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mh,
+                      const __grid_constant__ AdaptArgs g) {
+  using C = Cfg<TO>;
+  constexpr int S = C::kStages, BT = C::BT;
+  extern __shared__ unsigned char dsm_raw[];
+  __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], info_full[kInfo],
+      info_empty[kInfo], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_abort, s_info[kInfo];
+  __shared__ Groups<BT> s_groups;
+  unsigned char *smem = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
+  auto tile_w = [&](int s) { return smem + s * C::kStage; };
+  auto tile_x = [&](int s) { return smem + s * C::kStage + kTileW; };
+  float *scratch = reinterpret_cast<float *>(smem + S * C::kStage);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int n_tiles = (g.n_out + 2 * kBM - 1) / (2 * kBM), t_tiles = (g.tokens + BT - 1) / BT;
+  const int64_t tiles = (int64_t)n_tiles * t_tiles;
+  const int plain = (g.hidden + kBK - 1) / kBK, chunks = (g.rank + kBK - 1) / kBK;
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kWarps);
+    }
+    for (int i = 0; i < kInfo; ++i) {
+      mbar_init(&info_full[i], 1);
+      mbar_init(&info_empty[i], kWarps);
+    }
+    mbar_init(&drain, 1);
+    s_abort = 0;
+    mbar_fence_init();
+  }
+  __syncwarp();
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // the other CTA's barriers are there
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  volatile int *abort_flag = &s_abort;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    raise_error(g.err, GDN_DEVERR_TIMEOUT);
+  };
+  // the adapter that all tokens of the pair's i-th tile have, -1: none has any, -2: it is mixed, -3: a
+  // wait gave up
+  auto tile_info = [&](int i) {
+    if (!wait(&info_full[i % kInfo], (i / kInfo) & 1, abort_flag)) return -3;
+    return *reinterpret_cast<volatile int *>(&s_info[i % kInfo]);
+  };
+
+  if (warp == 0 && lane == 0) {
+    // producer
+    int64_t u = 0;
+    bool good = true, waited = false;
+    int i = 0;
+    for (int64_t t = pair; t < tiles && good; t += pairs, ++i) {
+      const int tok0 = (int)(t / n_tiles) * BT + rank * (BT / 2);
+      const int n0 = (int)(t % n_tiles) * 2 * kBM + rank * kBM;
+      const int one = tile_info(i);
+      if (one == -3) {
+        good = false;
+        break;
+      }
+      const int kbs = plain + (one >= 0 ? chunks * C::kParts : 0);
+      for (int kb = 0; kb < kbs; ++kb, ++u) {
+        const int s = (int)(u % S);
+        const int64_t round = u / S;
+        if (round > 0 && !wait(&empty[s], (uint32_t)((round - 1) & 1), abort_flag)) {
+          good = false;
+          break;
+        }
+        const uint32_t bar = leader_addr(&full[s]);
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
+        if (kb < plain) {
+          tma_load2_pair(tile_w(s), &mw, kb * kBK, n0, bar);
+          tma_load2_pair(tile_x(s), &mx, kb * kBK, tok0, bar);
+        } else {
+          // (rows of h behind the last token are another part's: columns that are not stored)
+          const int c = (kb - plain) / C::kParts, p = (kb - plain) % C::kParts;
+          tma_load2_pair(tile_w(s), &mb, c * kBK, one * g.n_out + n0, bar);
+          if (!waited) {
+            kv::dependent_wait();
+            asm volatile("fence.proxy.async.global;" ::: "memory");  // plain stores, read by TMA
+            waited = true;
+          }
+          tma_load2_pair(tile_x(s), &mh, c * kBK, p * g.tokens + tok0, bar);
+        }
+      }
+    }
+    if (!good) {
+      fail();
+      if (rank == 0)  // let the copies still in flight land before the pair exits
+        for (int64_t q = u - S < 0 ? 0 : u - S; q < u; ++q)
+          mbar_wait_bounded(&full[q % S], (uint32_t)((q / S) & 1));
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // MMA issuer
+    constexpr uint32_t idesc = tc::idesc_bf16(2 * kBM, BT);
+    int64_t u = 0;
+    bool good = true;
+    int i = 0, before = -1;  // the tile before
+    for (int64_t t = pair; t < tiles && good; t += pairs, ++i) {
+      const int one = tile_info(i);
+      // The accumulators' columns are free once the epilogue of tile i - 2 is done, or of tile i - 1
+      // where they are the same or held its adapters' part.
+      const int last = C::kF32 || before == -2 ? i - 1 : i - 2;
+      if (one == -3 ||
+          (last >= 0 && !wait(&acc_empty[last & 1], (uint32_t)((last >> 1) & 1), abort_flag))) {
+        good = false;
+        break;
+      }
+      before = one;
+      tc::fence_after_sync();
+      const uint32_t base = C::kF32 ? tmem : tmem + (uint32_t)(i & 1) * BT;
+      const int kbs = plain + (one >= 0 ? chunks * C::kParts : 0);
+      for (int kb = 0; kb < kbs; ++kb, ++u) {
+        const int s = (int)(u % S);
+        if (!wait(&full[s], (uint32_t)((u / S) & 1), abort_flag)) {
+          good = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const uint32_t a = smem_addr(tile_w(s)), b = smem_addr(tile_x(s));
+        const uint32_t acc = base + (uint32_t)(kb % C::kAcc) * BT;
+        const int c = (kb - plain) / C::kParts;
+        const int steps = kb < plain ? kBK / 16 : min(kBK, g.rank16() - c * kBK) / 16;
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk)
+          if (kk < steps)
+            mma_pair(acc, tc::smem_desc_sw128(a + 32 * kk), tc::smem_desc_sw128(b + 32 * kk), idesc,
+                     kb >= C::kAcc || kk > 0 ? 1u : 0u);
+        commit_pair(&empty[s]);
+      }
+      if (good) commit_pair(&acc_full[i & 1]);
+    }
+    if (!good) {
+      fail();
+      commit_pair(&drain);
+      mbar_wait_bounded(&drain, 0);  // MMAs in flight finish before TMEM is freed
+    }
+  } else if (warp == 2 + kWarps) {
+    // scout
+    int i = 0;
+    bool good = true;
+    for (int64_t t = pair; t < tiles && good; t += pairs, ++i) {
+      const int tok0 = (int)(t / n_tiles) * BT, live = min(BT, g.tokens - tok0);
+      const int one = token_id(g, tok0);
+      bool same = true;
+#pragma unroll
+      for (int j = 0; j < BT / 32; ++j)
+        if (32 * j + lane < live) same = same && token_id(g, tok0 + 32 * j + lane) == one;
+      same = __all_sync(0xffffffffu, same);
+      if (i >= kInfo)
+        good = __all_sync(0xffffffffu,
+                          wait(&info_empty[i % kInfo], ((i / kInfo) - 1) & 1, abort_flag));
+      if (good && lane == 0) {
+        *reinterpret_cast<volatile int *>(&s_info[i % kInfo]) = same ? one : -2;
+        mbar_arrive(&info_full[i % kInfo]);
+      }
+    }
+    if (!good) fail();
+  } else if (warp >= 2 && warp < 2 + kWarps) {
+    const int quad = warp & 3, side = (warp - 2) >> 2;
+    const uint32_t mine = tmem + ((uint32_t)(32 * quad) << 16);
+    TO *y = static_cast<TO *>(g.y);
+    int i = 0;
+    bool good = true;
+    for (int64_t t = pair; t < tiles; t += pairs, ++i) {
+      const int tok0 = (int)(t / n_tiles) * BT, live = min(BT, g.tokens - tok0);
+      const int n0 = (int)(t % n_tiles) * 2 * kBM + rank * kBM, n = n0 + 32 * quad + lane;
+      // (the helpers meet in barriers: they give up together, or not yet)
+      const int one = good ? tile_info(i) : -3;
+      if (!helpers_and(one != -3)) {
+        fail();
+        break;
+      }
+      tc::fence_after_sync();  // all have read the tile before
+      const uint32_t acc = mine + (C::kF32 ? 0u : (uint32_t)(i & 1) * BT);
+      const uint32_t delta = mine + (C::kF32 ? 3u * BT : (uint32_t)((i & 1) ^ 1) * BT);
+      if (one == -2) {
+        if (tid - 64 < BT) s_groups.id[tid - 64] = token_id(g, tok0 + tid - 64);
+        helpers_sync<kHelpers>();
+        find_groups<BT, kHelpers>(s_groups);
+        kv::dependent_wait();  // h
+        float *sc = scratch + (warp - 2) * 8 * 33;
+        if (n0 < g.n_out) {
+          if (g.rank <= 16)
+            expand<BT, 8, 1, 1, C::kParts>(g, s_groups, warp - 2, quad, n0, tok0, sc, delta);
+          else if (g.rank <= 32)
+            expand<BT, 16, 1, 1, C::kParts>(g, s_groups, warp - 2, quad, n0, tok0, sc, delta);
+          else if (g.rank <= 64)
+            expand<BT, 16, 2, 1, C::kParts>(g, s_groups, warp - 2, quad, n0, tok0, sc, delta);
+          else
+            expand<BT, 16, 2, 2, C::kParts>(g, s_groups, warp - 2, quad, n0, tok0, sc, delta);
+        }
+        for (int j = side; j < live; j += kTeams)
+          if (s_groups.id[j] < 0) tmem_st1(delta + j, 0.f);
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        helpers_sync<kHelpers>();
+      }
+      good = __all_sync(0xffffffffu, wait(&acc_full[i & 1], (i >> 1) & 1, abort_flag));
+      if (!good) {
+        fail();
+        continue;
+      }
+      tc::fence_after_sync();
+#pragma unroll 1
+      for (int c = 16 * side; c < live; c += 16 * kTeams) {
+        float v[32];
+        if constexpr (C::kF32) {
+          float u[32];
+          tc::tmem_ld32(acc + c, acc + BT + c, v);
+          if (one == -2) {
+            tc::tmem_ld32(acc + 2 * BT + c, delta + c, u);
+          } else {
+            tc::tmem_ld16(acc + 2 * BT + c, u);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) u[16 + j] = 0.f;
+          }
+          const int kbs = plain + (one >= 0 ? chunks * C::kParts : 0);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)  // (accumulators that no k-block has come to hold anything)
+            v[j] = v[j] + (kbs > 1 ? v[16 + j] : 0.f) + ((kbs > 2 ? u[j] : 0.f) + u[16 + j]);
+        } else if (one == -2) {
+          tc::tmem_ld32(acc + c, delta + c, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
+        } else {
+          tc::tmem_ld16(acc + c, v);
+        }
+        if (n < g.n_out) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < live) Elem<TO>::store1(y + (int64_t)(tok0 + c + j) * g.ld_y + n, v[j]);
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&info_empty[i % kInfo]);
+        arrive_leader(&acc_empty[i & 1]);
+      }
+    }
+  }
+  // (the leader's products read the other CTA's shared memory, and its commits arrive there)
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+  }
+  // what follows on the stream waits for this kernel only: the low side is complete too
+  kv::dependent_wait();
+}
+
+template <typename TO>
+cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
+  using C = Cfg<TO>;
+  CUtensorMap mw, mx, mb, mh;
+  const int64_t ld = g.rank_pad();
+  if (!encode_rows(&mw, g.w, g.n_out, g.hidden, g.ld_w, kBM) ||
+      !encode_rows(&mx, g.x, g.tokens, g.hidden, g.ld_x, C::BT / 2) ||
+      !encode_rows(&mb, g.b, (int64_t)g.n_adapters * g.n_out, g.rank, g.ld_b, kBM) ||
+      !encode_rows(&mh, g.h, (int64_t)C::kParts * g.tokens, ld, ld, C::BT / 2))
+    return cudaErrorNotSupported;
+  static std::atomic<uint64_t> seen{0};
+  const cudaError_t e = kv::allow_smem(adapt_pair_kernel<TO>, C::kSmem, g.device, seen);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles =
+      (int64_t)((g.n_out + 2 * kBM - 1) / (2 * kBM)) * ((g.tokens + C::BT - 1) / C::BT);
+  const int pairs = (int)(tiles < g.sm_count / 2 ? tiles : g.sm_count / 2);
+  return kv::launch(adapt_pair_kernel<TO>, dim3((unsigned)(2 * pairs)), kThreads, C::kSmem, s, 2, mw,
+                    mx, mb, mh, g);
+}
+
+}  // namespace
+
+cudaError_t launch_adapt_pair(const AdaptArgs &g, cudaStream_t s) {
+  return g.y_dtype == GDN_F32 ? launch<float>(g, s) : launch<bf16>(g, s);
+}
+
+}  // namespace gdn
