@@ -96,7 +96,7 @@ __device__ __forceinline__ void load_words(const void *p, uint32_t *out) {
 // each.  Groups are in the order of their first tokens, tasks in the order of the groups.
 template <int BT>
 struct Groups {
-  int id[BT];               // per token: its adapter if it is this CTA's to do, or -1
+  alignas(16) int id[BT];   // per token: its adapter if it is this CTA's to do, or -1
   int adapter[BT];          // per group
   short first[BT];          // of a group: its first task, and how many there are
   short count[BT];
@@ -112,17 +112,23 @@ struct Groups {
 template <int BT, int HELPERS>
 __device__ __forceinline__ void find_groups(Groups<BT> &s) {
   // threads that look for a token's others
-  constexpr int kPer = HELPERS >= 8 * BT ? 8 : HELPERS >= 2 * BT ? 2 : 1;
+  constexpr int kPer = HELPERS >= 8 * BT ? (BT >= 64 ? 8 : 4) : HELPERS >= 2 * BT ? 2 : 1;
   static_assert(HELPERS > 256 && HELPERS >= BT, "a thread per token, and one behind the last");
   const int tid = threadIdx.x - 64;
   const int token = tid / kPer, sub = tid % kPer, id = token < BT ? s.id[token < BT ? token : 0] : -1;
   int lead = BT, rank = 0, size = 0;
-  for (int j = sub; j < BT; j += kPer)
-    if (id >= 0 && s.id[j] == id) {
-      lead = min(lead, j);
-      rank += j < token;
-      ++size;
-    }
+#pragma unroll 4
+  for (int j = 4 * sub; j < BT; j += 4 * kPer) {
+    const int4 other = *reinterpret_cast<const int4 *>(&s.id[j]);
+    const int o[4] = {other.x, other.y, other.z, other.w};
+#pragma unroll
+    for (int x = 3; x >= 0; --x)
+      if (o[x] == id) {
+        lead = min(lead, j + x);
+        rank += j + x < token;
+        ++size;
+      }
+  }
 #pragma unroll
   for (int o = 1; o < kPer; o <<= 1) {
     lead = min(lead, __shfl_xor_sync(0xffffffffu, lead, o));

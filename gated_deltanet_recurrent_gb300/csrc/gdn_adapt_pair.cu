@@ -88,13 +88,17 @@ __device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
 }
 
 // Ranks e .. e + W / 2 - 1 of a row of B, zeros from `rank` on (what lies behind a row is not read).
-template <int W>
+// WHOLE: the rank is a multiple of W / 2.
+template <int W, bool WHOLE>
 __device__ __forceinline__ void load_b(const bf16 *row, int e, int rank, uint32_t *out) {
+  if constexpr (WHOLE) {
+    load_words<W>(row + (e < rank ? e : 0), out);
+    if (e >= rank)
 #pragma unroll
-  for (int w = 0; w < W / 4; ++w) out[w] = 0;
-  if (e + W / 2 <= rank) {
-    load_words<W>(row + e, out);
-  } else if (e < rank) {
+      for (int w = 0; w < W / 4; ++w) out[w] = 0;
+  } else {
+#pragma unroll
+    for (int w = 0; w < W / 4; ++w) out[w] = 0;
 #pragma unroll
     for (int j = 0; j < W / 2; ++j)
       if (e + j < rank)
@@ -105,9 +109,9 @@ __device__ __forceinline__ void load_b(const bf16 *row, int e, int rank, uint32_
 // Run by the helpers (`warp` of them; `quad`: the TMEM lanes it may write, 32 quad ..): every third
 // task.  Lane (r, c) of a fragment has rows r and r + 8 of B and token r of the task, for each W bytes
 // the same ranks (W / 2 neighbours: the order of K does not matter); NL such loads at a time, HALVES
-// times.  B stays in registers while the group does, and the h of the team's next task is on its way
+// times.  B stays in registers while the group does, and what the team's next task needs is on its way
 // under a task's results, unless there are two halves.
-template <int BT, int W, int NL, int HALVES, int PARTS>
+template <int BT, int W, int NL, int HALVES, bool WHOLE, int PARTS>
 __device__ __forceinline__ void expand(const AdaptArgs &g, const Groups<BT> &s, int warp, int quad,
                                        int n0, int tok0, float *scratch, uint32_t delta) {
   constexpr int kWords = W / 4;
@@ -132,11 +136,15 @@ __device__ __forceinline__ void expand(const AdaptArgs &g, const Groups<BT> &s, 
         const bf16 *row = b0 + min(n0 + 32 * quad + 16 * m + 8 * y + r, g.n_out - 1) * g.ld_b;
 #pragma unroll
         for (int l = 0; l < NL; ++l)
-          load_b<W>(row, (half * NL + l) * 2 * W + c * (W / 2), g.rank, b[m][l][y]);
+          load_b<W, WHOLE>(row, (half * NL + l) * 2 * W + c * (W / 2), g.rank, b[m][l][y]);
       }
   };
   int group = -1;
-  if (HALVES == 1 && team < s.tasks) load_h(team, 0);
+  auto load = [&](int t) {
+    if (s.group[t] != group) load_rows(group = s.group[t], 0);
+    load_h(t, 0);
+  };
+  if (HALVES == 1 && team < s.tasks) load(team);
   for (int t = team; t < s.tasks; t += kTeams) {
     float acc[2][PARTS][4];
 #pragma unroll
@@ -145,7 +153,6 @@ __device__ __forceinline__ void expand(const AdaptArgs &g, const Groups<BT> &s, 
       for (int q = 0; q < PARTS; ++q)
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[m][q][x] = 0.f;
-    if (HALVES == 1 && s.group[t] != group) load_rows(group = s.group[t], 0);
 #pragma unroll 1
     for (int half = 0; half < HALVES; ++half) {
       if (HALVES > 1) {
@@ -164,7 +171,7 @@ __device__ __forceinline__ void expand(const AdaptArgs &g, const Groups<BT> &s, 
             for (int q = 0; q < PARTS; ++q) mma16816(acc[m][q], a, h[l][q][w], h[l][q][w + 1]);
           }
     }
-    if (HALVES == 1 && t + kTeams < s.tasks) load_h(t + kTeams, 0);
+    if (HALVES == 1 && t + kTeams < s.tasks) load(t + kTeams);
     // from fragments to a row a lane
     __syncwarp();
 #pragma unroll
@@ -179,6 +186,19 @@ __device__ __forceinline__ void expand(const AdaptArgs &g, const Groups<BT> &s, 
     const int cols = s.tokens[t];
     for (int j = 0; j < cols; ++j) tmem_st1(delta + s.token[t][j], scratch[j * 33 + lane]);
   }
+}
+
+template <int BT, bool WHOLE, int PARTS>
+__device__ __forceinline__ void expand_rank(const AdaptArgs &g, const Groups<BT> &s, int warp, int quad,
+                                            int n0, int tok0, float *scratch, uint32_t delta) {
+  if (g.rank <= 16)
+    expand<BT, 8, 1, 1, WHOLE, PARTS>(g, s, warp, quad, n0, tok0, scratch, delta);
+  else if (g.rank <= 32)
+    expand<BT, 16, 1, 1, WHOLE, PARTS>(g, s, warp, quad, n0, tok0, scratch, delta);
+  else if (g.rank <= 64)
+    expand<BT, 16, 2, 1, WHOLE, PARTS>(g, s, warp, quad, n0, tok0, scratch, delta);
+  else
+    expand<BT, 16, 2, 2, WHOLE, PARTS>(g, s, warp, quad, n0, tok0, scratch, delta);
 }
 
 // Among the helpers: whether all say so.
@@ -389,23 +409,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t acc = mine + (C::kF32 ? 0u : (uint32_t)(i & 1) * BT);
       const uint32_t delta = mine + (C::kF32 ? 3u * BT : (uint32_t)((i & 1) ^ 1) * BT);
       if (one == -2) {
+        const float zero[16] = {};  // what tokens without an adapter get
+#pragma unroll 1
+        for (int c = 16 * side; c < BT; c += 16 * kTeams) tc::tmem_st16(delta + c, zero);
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
         if (tid - 64 < BT) s_groups.id[tid - 64] = token_id(g, tok0 + tid - 64);
         helpers_sync<kHelpers>();
         find_groups<BT, kHelpers>(s_groups);
+        tc::fence_after_sync();
         kv::dependent_wait();  // h
         float *sc = scratch + (warp - 2) * 8 * 33;
         if (n0 < g.n_out) {
-          if (g.rank <= 16)
-            expand<BT, 8, 1, 1, C::kParts>(g, s_groups, warp - 2, quad, n0, tok0, sc, delta);
-          else if (g.rank <= 32)
-            expand<BT, 16, 1, 1, C::kParts>(g, s_groups, warp - 2, quad, n0, tok0, sc, delta);
-          else if (g.rank <= 64)
-            expand<BT, 16, 2, 1, C::kParts>(g, s_groups, warp - 2, quad, n0, tok0, sc, delta);
+          if (g.rank % 8 == 0)
+            expand_rank<BT, true, C::kParts>(g, s_groups, warp - 2, quad, n0, tok0, sc, delta);
           else
-            expand<BT, 16, 2, 2, C::kParts>(g, s_groups, warp - 2, quad, n0, tok0, sc, delta);
+            expand_rank<BT, false, C::kParts>(g, s_groups, warp - 2, quad, n0, tok0, sc, delta);
         }
-        for (int j = side; j < live; j += kTeams)
-          if (s_groups.id[j] < 0) tmem_st1(delta + j, 0.f);
         tc::tmem_st_wait();
         tc::fence_before_sync();
         helpers_sync<kHelpers>();
