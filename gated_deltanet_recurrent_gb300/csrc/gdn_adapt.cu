@@ -496,7 +496,7 @@ cudaError_t launch_bt(const AdaptArgs &g, cudaStream_t s) {
                         : launch_split<BT, 128, TO>(g, s);
 }
 
-constexpr int kFewTokens = 128;
+constexpr int kFewTokens = 256;
 
 template <typename TO>
 cudaError_t launch_t(const AdaptArgs &g, cudaStream_t s) {
@@ -506,13 +506,17 @@ cudaError_t launch_t(const AdaptArgs &g, cudaStream_t s) {
 }  // namespace
 
 size_t adapt_workspace_bytes(const AdaptArgs &g) {
-  return (size_t)g.tokens * g.parts() * g.rank_pad() * 2;
+  return (size_t)g.tokens * g.parts() * g.rank_pad() * 2 * (g.tile > 0 ? kPlanes : 1);
+}
+
+int adapt_tile(const AdaptArgs &g) {
+  return g.tokens <= kFewTokens ? 0 : g.y_dtype == GDN_F32 ? 128 : 256;
 }
 
 cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s) {
   const cudaError_t e = launch_adapt_low(g, s);
   if (e != cudaSuccess) return e;
-  if (g.tokens > kFewTokens) return launch_adapt_pair(g, s);
+  if (g.tile > 0) return launch_adapt_pair(g, s);
   return g.y_dtype == GDN_F32 ? launch_t<float>(g, s) : launch_t<bf16>(g, s);
 }
 

@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include "gdn_adapt.h"
+#include "gdn_adapt_tile.cuh"
 #include "gdn_kv.cuh"
 #include "gdn_mma.cuh"
 #include "gdn_tc.cuh"
@@ -68,11 +69,6 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
     if ((it & 15) == 15 && *abort_flag) return false;
   }
   return false;
-}
-
-__device__ __forceinline__ int token_id(const AdaptArgs &g, int t) {
-  const int id = t < g.tokens ? g.ids[t] : -1;
-  return id >= 0 && id < g.n_adapters ? id : -1;
 }
 
 // The helpers, HELPERS threads from warp 2 on, do the adapters' part of mixed tiles and the epilogue.

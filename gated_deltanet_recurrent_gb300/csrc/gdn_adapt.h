@@ -14,8 +14,12 @@ struct AdaptArgs {
   int64_t ld_x, ld_w, ld_a, ld_b, ld_y;
   int tokens, hidden, n_out, rank, n_adapters;
   gdn_dtype y_dtype;
-  void *h;                    // workspace: scale * A x in bf16 parts that add up to it,
-                              // [parts][tokens][rank_pad], zeros beyond rank
+  // workspace: scale * A x in bf16 parts that add up to it, [parts][tokens][rank_pad], zeros beyond
+  // rank; with tile > 0 [kPlanes][parts][tokens][rank_pad]: of a tile of `tile` tokens with n <=
+  // kPlanes adapters, plane j < n has the h of the j-th adapter's tokens (in the order of their
+  // first ones) and zeros for the others; with more, plane 0 has all h there is
+  void *h;
+  int tile;
   unsigned int *err;
   int sm_count, device;
   GDN_HD int parts() const { return y_dtype == GDN_F32 ? 3 : 2; }
@@ -25,7 +29,11 @@ struct AdaptArgs {
   GDN_HD int rank_pad() const { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 };
 
+constexpr int kPlanes = 8;
+
 size_t adapt_workspace_bytes(const AdaptArgs &g);
+// What the kernels that the call takes need of `tile`.
+int adapt_tile(const AdaptArgs &g);
 // The low side, then the projection; cudaErrorNotSupported: no tensor map.
 cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s);
 

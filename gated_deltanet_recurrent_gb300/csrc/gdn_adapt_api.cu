@@ -128,8 +128,7 @@ gdn_status gdn_in_proj_adapted(gdn_pool *p, gdn_adapters *ad, int64_t tokens, co
   if (tokens < 0) return fail(GDN_ERR_ARG, "tokens = %lld", (long long)tokens);
   if (!dtype_ok(y_dtype)) return fail(GDN_ERR_DTYPE, "y dtype must be F32 or BF16");
   if (tokens == 0) return ok();
-  // (token tiles are a grid's second dimension)
-  if (tokens > 1 << 20) return fail(GDN_ERR_SIZE, "tokens = %lld > 2^20", (long long)tokens);
+  if (tokens > 1 << 18) return fail(GDN_ERR_SIZE, "tokens = %lld > 2^18", (long long)tokens);
   if (!x || !w || !ids || !y) return fail(GDN_ERR_ARG, "x, w, ids and y must be non-NULL");
   const gdn_adapters_desc &d = ad->desc;
   gdn_status st;
@@ -146,8 +145,9 @@ gdn_status gdn_in_proj_adapted(gdn_pool *p, gdn_adapters *ad, int64_t tokens, co
        (st = check_device_ptr(y, "y")) || (st = check_ids(ad, ids, (int32_t)tokens, s))))
     return st;
   gdn::AdaptArgs g = {x, w, ad->a, ad->b, ad->scale, ids, y, ld_x, ld_w, ad->ld_a, ad->ld_b, ld_y,
-                      (int)tokens, d.hidden, d.n_out, d.rank, d.n_adapters, y_dtype, nullptr,
+                      (int)tokens, d.hidden, d.n_out, d.rank, d.n_adapters, y_dtype, nullptr, 0,
                       p->view.err, ad->sm_count, dev};
+  g.tile = gdn::adapt_tile(g);
   void *work = nullptr;
   bool temporary = false;
   e = ad->work.get(gdn::adapt_workspace_bytes(g), s, &work, &temporary);

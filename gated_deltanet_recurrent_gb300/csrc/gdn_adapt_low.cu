@@ -17,6 +17,8 @@
 #include "gdn_kv.cuh"
 #include "gdn_mma.cuh"
 
+#include "gdn_adapt_tile.cuh"
+
 namespace gdn {
 namespace {
 
@@ -38,11 +40,12 @@ __device__ __forceinline__ uint4 load8(const bf16 *row, int k, int hidden) {
 
 // AHEAD: steps of 64 k whose loads a warp has in flight.  (With the ends of odd rows looked at in
 // every load the code was so long that fetching it took longer than the work.)
-template <int MT, int NT, int AHEAD, bool WHOLE>
+template <int MT, int NT, int AHEAD, bool WHOLE, bool PLANES>
 __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
   constexpr int kTok = 16 * MT, kRanks = 8 * NT;
   extern __shared__ float s_part[];  // [kWarps][kTok][kRanks]
   __shared__ int s_id[kTok], s_lead[kTok], s_n;
+  __shared__ int s_tile[kPlanes], s_tile_n;  // PLANES: the adapters of the window's tile
   kv::dependent_wait();
   // the projection may start loading what no kernel before this one writes
   kv::dependents_may_launch();
@@ -95,11 +98,34 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
     }
     if (lane == 0) s_n = n;
   }
+  if (PLANES && warp == 1) {
+    int list[kPlanes];
+    const int t0 = tok0 / g.tile * g.tile;
+    const int n = tile_groups(g, t0, min(g.tile, g.tokens - t0), list);
+    if (lane == 0) {
+      s_tile_n = n;
+#pragma unroll
+      for (int j = 0; j < kPlanes; ++j) s_tile[j] = list[j];
+    }
+  }
   __syncthreads();
+  // planes that a token has a row in, and the words from one to the next
+  const int planes = !PLANES || s_tile_n > kPlanes ? 1 : s_tile_n;
+  const int64_t part_words = (int64_t)g.tokens * (g.rank_pad() / 2);
+  if (PLANES && blockIdx.y == 0 && s_tile_n <= kPlanes)  // zeros for tokens without an adapter
+    for (int i = tid; i < kTok * kRanks / 2; i += 32 * kWarps) {
+      const int t = 2 * i / kRanks, r = rank0 + 2 * i % kRanks;
+      if (s_id[t] >= 0 || tok0 + t >= g.tokens || r >= g.rank_pad()) continue;
+      uint32_t *h = static_cast<uint32_t *>(g.h) + ((int64_t)(tok0 + t) * g.rank_pad() + r) / 2;
+      for (int p = 0; p < planes * g.parts(); ++p) h[p * part_words] = 0;
+    }
   const int rank_pad = g.rank_pad(), parts = g.parts();
   for (int gi = blockIdx.y; gi < s_n; gi += gridDim.y) {
     const int id = s_lead[gi];
     const float scale = g.scale[id];
+    int plane = 0;
+    if (PLANES && s_tile_n <= kPlanes)
+      while (s_tile[plane] != id) ++plane;
     const bf16 *a = static_cast<const bf16 *>(g.a) + (int64_t)id * g.rank * g.ld_a;
     float acc[MT][NT][4];
 #pragma unroll
@@ -161,7 +187,7 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
       for (int p = 0; p < parts; ++p) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
         const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
-        h[(int64_t)p * g.tokens * (rank_pad / 2)] = w;
+        for (int j = 0; j < planes; ++j) h[(j * parts + p) * part_words] = j == plane ? w : 0;
         const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
         // (what is infinite or NaN is the first part alone)
         x = fabsf(lo) < INFINITY ? x - lo : 0.f;
@@ -172,18 +198,18 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
   }
 }
 
-template <int MT, int NT, int AHEAD, bool WHOLE>
+template <int MT, int NT, int AHEAD, bool WHOLE, bool PLANES>
 cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
   constexpr int smem = kWarps * 16 * MT * 8 * NT * 4;
   static std::atomic<uint64_t> seen{0};
-  const cudaError_t e = kv::allow_smem(low_kernel<MT, NT, AHEAD, WHOLE>, smem, g.device, seen);
+  const cudaError_t e = kv::allow_smem(low_kernel<MT, NT, AHEAD, WHOLE, PLANES>, smem, g.device, seen);
   if (e != cudaSuccess) return e;
   const int windows = (g.tokens + 16 * MT - 1) / (16 * MT);
   const int parts = (g.rank_pad() + 8 * NT - 1) / (8 * NT);
   // CTAs that share a window: as many as it may have adapters, but no more than four waves in all
   const int64_t room = (int64_t)4 * g.sm_count / ((int64_t)windows * parts);
   const int share = (int)(room < 1 ? 1 : room > 16 * MT ? 16 * MT : room);
-  return kv::launch(low_kernel<MT, NT, AHEAD, WHOLE>, dim3((unsigned)windows, (unsigned)share, (unsigned)parts),
+  return kv::launch(low_kernel<MT, NT, AHEAD, WHOLE, PLANES>, dim3((unsigned)windows, (unsigned)share, (unsigned)parts),
                     32 * kWarps, smem, s, 1, g);
 }
 
@@ -191,8 +217,10 @@ cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
 
 cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s) {
   // few tokens: small windows, for parallel loads of A; many: large ones, that read A less often
-  if (g.hidden % 8 != 0) return launch<1, 2, 1, false>(g, s);
-  return g.tokens <= 256 ? launch<1, 2, 4, true>(g, s) : launch<4, 4, 1, true>(g, s);
+  if (g.tile > 0)
+    return g.hidden % 8 == 0 ? launch<4, 4, 1, true, true>(g, s) : launch<1, 2, 1, false, true>(g, s);
+  return g.hidden % 8 == 0 ? launch<1, 2, 4, true, false>(g, s)
+                           : launch<1, 2, 1, false, false>(g, s);
 }
 
 }  // namespace gdn

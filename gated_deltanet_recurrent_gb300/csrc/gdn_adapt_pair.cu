@@ -11,13 +11,18 @@
 //   warps 2..13 the adapters' part of mixed tiles, then the epilogue
 //   warp 14     looks a few tiles ahead: which have one adapter, or none
 //
-// A tile whose tokens have one adapter (most of a prompt) takes it as further k-blocks: B tiles for W's
-// and the parts of h for x's.  In a mixed tile the helpers multiply B and h with mma.sync while the
-// tensor core computes W x: four warps with 32 output rows each take the tasks (up to eight tokens of
-// one adapter) in turn, with B and h from global memory, and store them to TMEM columns [token][row] of
-// their own, which the epilogue adds.  For a bf16 y these are the columns of the next tile's accumulator,
-// which then starts after the epilogue; for a float32 y, of 128 tokens, there are columns for the three
-// accumulators (see gdn_adapt.cu) and these.
+// The adapters are further k-blocks: B tiles for W's and the parts of h for x's.  Where all tokens of a
+// tile have one adapter (most of a prompt) they add to the tile's accumulator.  In a mixed tile every
+// adapter has its own k-blocks, with a plane of h that has zeros for the other tokens, and they add to
+// columns of their own: what is not finite there may come from another request's adapter (0 * inf), and
+// is then computed again by itself, so that nothing of one adapter reaches another's tokens.  For a
+// bf16 y these are the columns of the next tile's accumulator, which then starts after the epilogue;
+// for a float32 y, of 128 tokens, there are columns for the three accumulators (see gdn_adapt.cu) and
+// these.  For more than eight adapters in a tile there are no planes.  Then the helpers multiply B and
+// h with mma.sync: four warps with 32 output rows each take the tasks (up to eight tokens of one
+// adapter) in turn, with B and h from global memory, and store them to those columns, [token][row].
+// (That is slow beside the tensor core, whose operands take all of the shared memory's bandwidth: 15 us
+// for a tile of 256 tokens with two adapters, whose k-blocks take 4.)
 #include "gdn_adapt.cuh"
 
 namespace gdn {
@@ -42,6 +47,14 @@ struct Cfg {
   static constexpr int kScratch = kWarps * 8 * 33 * 4;
   static constexpr int kSmem = kStages * kStage + kScratch + 1024;
 };
+
+constexpr int kMany = -2, kGaveUp = -3, kMixed = -4;
+// The adapters of a tile that are k-blocks of it.
+__device__ __forceinline__ int adapters_of(int one) {
+  return one >= 0 ? 1 : one <= kMixed ? kMixed - one : 0;
+}
+// Whether a tile's adapters add to columns of their own.
+__device__ __forceinline__ bool apart(int one) { return one == kMany || one <= kMixed; }
 
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
@@ -201,6 +214,44 @@ __device__ __forceinline__ void expand_rank(const AdaptArgs &g, const Groups<BT>
     expand<BT, 16, 2, 2, WHOLE, PARTS>(g, s, warp, quad, n0, tok0, scratch, delta);
 }
 
+// The adapters' part of one output: row n, token t of a tile with the adapters list[0 .. count).
+template <int PARTS>
+__device__ __noinline__ float one_by_one(const AdaptArgs &g, const int *list, int count, int t, int n) {
+  const int id = token_id(g, t), ld = g.rank_pad();
+  if (id < 0) return 0.f;
+  int plane = 0;
+  while (plane + 1 < count && list[plane] != id) ++plane;
+  kv::dependent_wait();
+  const bf16 *b = static_cast<const bf16 *>(g.b) + ((int64_t)id * g.n_out + n) * g.ld_b;
+  const bf16 *h = static_cast<const bf16 *>(g.h) + ((int64_t)plane * PARTS * g.tokens + t) * ld;
+  float sum = 0.f;
+  for (int r = 0; r < g.rank; ++r) {
+    float x = __bfloat162float(h[r]);
+    for (int p = 1; p < PARTS; ++p) x += __bfloat162float(h[(int64_t)p * g.tokens * ld + r]);
+    sum += __bfloat162float(b[r]) * x;
+  }
+  return sum;
+}
+
+// 16 tokens' outputs n, a lane per output: two neighbouring lanes exchange, so that each stores two
+// outputs of every other token.
+__device__ __forceinline__ void store_rows(bf16 *y, int64_t ld, int n, int n_out, int live,
+                                           const float *v) {
+  const int odd = n & 1;
+  bf16 *p = y + odd * ld + (n - odd);
+#pragma unroll
+  for (int j = 0; j < 16; j += 2, p += 2 * ld) {
+    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+    const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(other, v[j + 1])
+                                 : __floats2bfloat162_rn(v[j], other);
+    if (j + odd >= live) continue;
+    if (n - odd + 1 < n_out)
+      *reinterpret_cast<__nv_bfloat162 *>(p) = w;
+    else if (n - odd < n_out)
+      *p = w.x;
+  }
+}
+
 // Among the helpers: whether all say so.
 __device__ __forceinline__ bool helpers_and(bool x) {
   uint32_t r;
@@ -224,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], info_full[kInfo],
       info_empty[kInfo], drain;
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_abort, s_info[kInfo];
+  __shared__ int s_abort, s_info[kInfo], s_list[kInfo][kPlanes];
   __shared__ Groups<BT> s_groups;
   unsigned char *smem = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
@@ -272,15 +323,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
     raise_error(g.err, GDN_DEVERR_TIMEOUT);
   };
-  // the adapter that all tokens of the pair's i-th tile have, -1: none has any, -2: it is mixed, -3: a
-  // wait gave up
+  // the adapter that all tokens of the pair's i-th tile have, or -1: none has any, kMany: more than there
+  // are planes for, kGaveUp: a wait did, kMixed - n: n (s_list)
   auto tile_info = [&](int i) {
-    if (!wait(&info_full[i % kInfo], (i / kInfo) & 1, abort_flag)) return -3;
+    if (!wait(&info_full[i % kInfo], (i / kInfo) & 1, abort_flag)) return kGaveUp;
     return *reinterpret_cast<volatile int *>(&s_info[i % kInfo]);
   };
 
   if (warp == 0 && lane == 0) {
     // producer
+    int s = 0;
+    uint32_t round = 0;
     int64_t u = 0;
     bool good = true, waited = false;
     int i = 0;
@@ -288,15 +341,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok0 = (int)(t / n_tiles) * BT + rank * (BT / 2);
       const int n0 = (int)(t % n_tiles) * 2 * kBM + rank * kBM;
       const int one = tile_info(i);
-      if (one == -3) {
+      if (one == kGaveUp) {
         good = false;
         break;
       }
-      const int kbs = plain + (one >= 0 ? chunks * C::kParts : 0);
-      for (int kb = 0; kb < kbs; ++kb, ++u) {
-        const int s = (int)(u % S);
-        const int64_t round = u / S;
-        if (round > 0 && !wait(&empty[s], (uint32_t)((round - 1) & 1), abort_flag)) {
+      const int kbs = plain + adapters_of(one) * chunks * C::kParts;
+      for (int kb = 0; kb < kbs; ++kb, ++u, s = s + 1 == S ? 0 : s + 1) {
+        if (s == 0 && u > S) round ^= 1;  // (the first round waits for nothing, the second for phase 0)
+        if (u >= S && !wait(&empty[s], round, abort_flag)) {
           good = false;
           break;
         }
@@ -307,14 +359,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load2_pair(tile_x(s), &mx, kb * kBK, tok0, bar);
         } else {
           // (rows of h behind the last token are another part's: columns that are not stored)
-          const int c = (kb - plain) / C::kParts, p = (kb - plain) % C::kParts;
-          tma_load2_pair(tile_w(s), &mb, c * kBK, one * g.n_out + n0, bar);
+          const int e = kb - plain, p = e % C::kParts, c = e / C::kParts % chunks,
+                    j = e / C::kParts / chunks;
+          const int id = one >= 0 ? one : s_list[i % kInfo][j];
+          tma_load2_pair(tile_w(s), &mb, c * kBK, id * g.n_out + n0, bar);
           if (!waited) {
             kv::dependent_wait();
             asm volatile("fence.proxy.async.global;" ::: "memory");  // plain stores, read by TMA
             waited = true;
           }
-          tma_load2_pair(tile_x(s), &mh, c * kBK, p * g.tokens + tok0, bar);
+          tma_load2_pair(tile_x(s), &mh, c * kBK, (j * C::kParts + p) * g.tokens + tok0, bar);
         }
       }
     }
@@ -327,41 +381,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // MMA issuer
     constexpr uint32_t idesc = tc::idesc_bf16(2 * kBM, BT);
-    int64_t u = 0;
+    int s = 0;
+    uint32_t round = 0;
     bool good = true;
-    int i = 0, before = -1;  // the tile before
+    int i = 0, before = -1;  // the tile before: it has no adapters
     for (int64_t t = pair; t < tiles && good; t += pairs, ++i) {
       const int one = tile_info(i);
       // The accumulators' columns are free once the epilogue of tile i - 2 is done, or of tile i - 1
       // where they are the same or held its adapters' part.
-      const int last = C::kF32 || before == -2 ? i - 1 : i - 2;
-      if (one == -3 ||
-          (last >= 0 && !wait(&acc_empty[last & 1], (uint32_t)((last >> 1) & 1), abort_flag))) {
+      auto free_after = [&](int last) {
+        return last < 0 || wait(&acc_empty[last & 1], (uint32_t)((last >> 1) & 1), abort_flag);
+      };
+      if (one == kGaveUp || !free_after(C::kF32 || apart(before) ? i - 1 : i - 2)) {
         good = false;
         break;
       }
       before = one;
       tc::fence_after_sync();
       const uint32_t base = C::kF32 ? tmem : tmem + (uint32_t)(i & 1) * BT;
-      const int kbs = plain + (one >= 0 ? chunks * C::kParts : 0);
-      for (int kb = 0; kb < kbs; ++kb, ++u) {
-        const int s = (int)(u % S);
-        if (!wait(&full[s], (uint32_t)((u / S) & 1), abort_flag)) {
-          good = false;
-          break;
-        }
+      const uint32_t delta = C::kF32 ? tmem + 3 * BT : tmem + (uint32_t)((i & 1) ^ 1) * BT;
+      // the next k-block's products; a loop round it has 256 cycles
+      auto block = [&](uint32_t acc, int steps, bool fresh) {
+        if (!wait(&full[s], round, abort_flag)) return false;
         tc::fence_after_sync();
         const uint32_t a = smem_addr(tile_w(s)), b = smem_addr(tile_x(s));
-        const uint32_t acc = base + (uint32_t)(kb % C::kAcc) * BT;
-        const int c = (kb - plain) / C::kParts;
-        const int steps = kb < plain ? kBK / 16 : min(kBK, g.rank16() - c * kBK) / 16;
 #pragma unroll
         for (int kk = 0; kk < kBK / 16; ++kk)
           if (kk < steps)
             mma_pair(acc, tc::smem_desc_sw128(a + 32 * kk), tc::smem_desc_sw128(b + 32 * kk), idesc,
-                     kb >= C::kAcc || kk > 0 ? 1u : 0u);
+                     !fresh || kk > 0 ? 1u : 0u);
         commit_pair(&empty[s]);
+        if (++s == S) s = 0, round ^= 1;
+        return true;
+      };
+      int turn = 0;  // of the accumulators
+      for (int kb = 0; kb < plain && good; ++kb) {
+        good = block(base + (uint32_t)turn * BT, kBK / 16, kb < C::kAcc);
+        turn = turn + 1 == C::kAcc ? 0 : turn + 1;
       }
+      // the adapters, to the same place, or (the last tile's accumulator, which has to be read) apart
+      const int count = adapters_of(one);
+      if (good && one <= kMixed) good = free_after(i - 1);
+      tc::fence_after_sync();
+      for (int j = 0, kb = plain; j < count; ++j)
+        for (int c = 0; c < chunks; ++c)
+          for (int p = 0; p < C::kParts && good; ++p, ++kb) {
+            const int steps = min(kBK, g.rank16() - c * kBK) / 16;
+            if (one <= kMixed) {
+              good = block(delta, steps, kb == plain);
+            } else {
+              good = block(base + (uint32_t)turn * BT, steps, kb < C::kAcc);
+              turn = turn + 1 == C::kAcc ? 0 : turn + 1;
+            }
+          }
       if (good) commit_pair(&acc_full[i & 1]);
     }
     if (!good) {
@@ -375,17 +447,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool good = true;
     for (int64_t t = pair; t < tiles && good; t += pairs, ++i) {
       const int tok0 = (int)(t / n_tiles) * BT, live = min(BT, g.tokens - tok0);
-      const int one = token_id(g, tok0);
-      bool same = true;
+      int list[kPlanes];
+      const int n = tile_groups(g, tok0, live, list);
+      bool whole = true;  // no token without an adapter
 #pragma unroll
       for (int j = 0; j < BT / 32; ++j)
-        if (32 * j + lane < live) same = same && token_id(g, tok0 + 32 * j + lane) == one;
-      same = __all_sync(0xffffffffu, same);
+        if (32 * j + lane < live) whole = whole && token_id(g, tok0 + 32 * j + lane) >= 0;
+      whole = __all_sync(0xffffffffu, whole);
       if (i >= kInfo)
         good = __all_sync(0xffffffffu,
                           wait(&info_empty[i % kInfo], ((i / kInfo) - 1) & 1, abort_flag));
       if (good && lane == 0) {
-        *reinterpret_cast<volatile int *>(&s_info[i % kInfo]) = same ? one : -2;
+#pragma unroll
+        for (int j = 0; j < kPlanes; ++j) s_list[i % kInfo][j] = list[j];
+        *reinterpret_cast<volatile int *>(&s_info[i % kInfo]) =
+            n == 0 ? -1 : n == 1 && whole ? list[0] : n > kPlanes ? kMany : kMixed - n;
         mbar_arrive(&info_full[i % kInfo]);
       }
     }
@@ -400,15 +476,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok0 = (int)(t / n_tiles) * BT, live = min(BT, g.tokens - tok0);
       const int n0 = (int)(t % n_tiles) * 2 * kBM + rank * kBM, n = n0 + 32 * quad + lane;
       // (the helpers meet in barriers: they give up together, or not yet)
-      const int one = good ? tile_info(i) : -3;
-      if (!helpers_and(one != -3)) {
+      const int one = good ? tile_info(i) : kGaveUp;
+      if (!helpers_and(one != kGaveUp)) {
         fail();
         break;
       }
       tc::fence_after_sync();  // all have read the tile before
       const uint32_t acc = mine + (C::kF32 ? 0u : (uint32_t)(i & 1) * BT);
       const uint32_t delta = mine + (C::kF32 ? 3u * BT : (uint32_t)((i & 1) ^ 1) * BT);
-      if (one == -2) {
+      if (one == kMany) {
         const float zero[16] = {};  // what tokens without an adapter get
 #pragma unroll 1
         for (int c = 16 * side; c < BT; c += 16 * kTeams) tc::tmem_st16(delta + c, zero);
@@ -438,32 +514,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
 #pragma unroll 1
       for (int c = 16 * side; c < live; c += 16 * kTeams) {
-        float v[32];
+        float v[32];  // W x, and the adapters' part
         if constexpr (C::kF32) {
           float u[32];
           tc::tmem_ld32(acc + c, acc + BT + c, v);
-          if (one == -2) {
+          const int kbs = plain + (one >= 0 ? chunks * C::kParts : 0);
+          if (kbs > 1)  // (an accumulator that no k-block has come to holds anything)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
+          if (apart(one))
             tc::tmem_ld32(acc + 2 * BT + c, delta + c, u);
-          } else {
+          else
             tc::tmem_ld16(acc + 2 * BT + c, u);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) u[16 + j] = 0.f;
+          for (int j = 0; j < 16; ++j) {
+            if (kbs > 2) v[j] += u[j];
+            v[16 + j] = u[16 + j];
           }
-          const int kbs = plain + (one >= 0 ? chunks * C::kParts : 0);
-#pragma unroll
-          for (int j = 0; j < 16; ++j)  // (accumulators that no k-block has come to hold anything)
-            v[j] = v[j] + (kbs > 1 ? v[16 + j] : 0.f) + ((kbs > 2 ? u[j] : 0.f) + u[16 + j]);
-        } else if (one == -2) {
+        } else if (apart(one)) {
           tc::tmem_ld32(acc + c, delta + c, v);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
         } else {
           tc::tmem_ld16(acc + c, v);
         }
-        if (n < g.n_out) {
+        if (apart(one)) {
+          if (one <= kMixed) {
+            bool odd = false;
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < live) Elem<TO>::store1(y + (int64_t)(tok0 + c + j) * g.ld_y + n, v[j]);
+            for (int j = 0; j < 16; ++j) odd = odd || !(fabsf(v[16 + j]) < INFINITY);
+            if (odd && n < g.n_out)
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (c + j < live && !(fabsf(v[16 + j]) < INFINITY))
+                  v[16 + j] = one_by_one<C::kParts>(g, s_list[i % kInfo], kMixed - one,
+                                                    tok0 + c + j, n);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
+        }
+        if constexpr (C::kF32) {
+          if (n < g.n_out)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < live) y[(int64_t)(tok0 + c + j) * g.ld_y + n] = v[j];
+        } else {
+          store_rows(y + (int64_t)(tok0 + c) * g.ld_y, g.ld_y, n, g.n_out, live - c, v);
         }
       }
       tc::fence_before_sync();
@@ -495,7 +589,7 @@ cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
   if (!encode_rows(&mw, g.w, g.n_out, g.hidden, g.ld_w, kBM) ||
       !encode_rows(&mx, g.x, g.tokens, g.hidden, g.ld_x, C::BT / 2) ||
       !encode_rows(&mb, g.b, (int64_t)g.n_adapters * g.n_out, g.rank, g.ld_b, kBM) ||
-      !encode_rows(&mh, g.h, (int64_t)C::kParts * g.tokens, ld, ld, C::BT / 2))
+      !encode_rows(&mh, g.h, (int64_t)kPlanes * C::kParts * g.tokens, ld, ld, C::BT / 2))
     return cudaErrorNotSupported;
   static std::atomic<uint64_t> seen{0};
   const cudaError_t e = kv::allow_smem(adapt_pair_kernel<TO>, C::kSmem, g.device, seen);

@@ -676,7 +676,8 @@ typedef struct {
 typedef struct gdn_adapters gdn_adapters;
 
 /* The handle owns a memory pool with a workspace for each of the first 16 streams that
- * it is used on, as the KV cache does (tokens * rank * 12 bytes, at most). */
+ * it is used on, as the KV cache does: 4 bytes (bf16 y) or 6 per token and rank, the rank
+ * rounded up to a power of two, in calls of more than 256 tokens eight times that. */
 gdn_status gdn_adapters_create(const gdn_adapters_desc *desc, const void *a, int64_t ld_a,
                                const void *b, int64_t ld_b, const float *scale,
                                gdn_adapters **out);
@@ -691,7 +692,7 @@ gdn_status gdn_adapters_destroy(gdn_adapters *adapters);
  * itself) for bf16 y and in three (2^-24) for float32 y; y is rounded once.  An adapter
  * with values that are not finite spoils its own tokens only.  An id outside
  * [-1, n_adapters) counts as -1 (GDN_DEVERR_ADAPTER).  The pool supplies the error
- * word.  tokens <= 2^20.  Calls from several host threads on one handle must be
+ * word.  tokens <= 2^18.  Calls from several host threads on one handle must be
  * serialised by the caller. */
 gdn_status gdn_in_proj_adapted(gdn_pool *pool, gdn_adapters *adapters, int64_t tokens,
                                const void *x, int64_t ld_x, const void *w, int64_t ld_w,
