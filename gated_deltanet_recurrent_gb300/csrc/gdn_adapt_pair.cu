@@ -12,17 +12,17 @@
 //   warp 14     looks a few tiles ahead: which have one adapter, or none
 //
 // The adapters are further k-blocks: B tiles for W's and the parts of h for x's.  Where all tokens of a
-// tile have one adapter (most of a prompt) they add to the tile's accumulator.  In a mixed tile every
-// adapter has its own k-blocks, with a plane of h that has zeros for the other tokens, and they add to
-// columns of their own: what is not finite there may come from another request's adapter (0 * inf), and
-// is then computed again by itself, so that nothing of one adapter reaches another's tokens.  For a
-// bf16 y these are the columns of the next tile's accumulator, which then starts after the epilogue;
-// for a float32 y, of 128 tokens, there are columns for the three accumulators (see gdn_adapt.cu) and
-// these.  For more than eight adapters in a tile there are no planes.  Then the helpers multiply B and
-// h with mma.sync: four warps with 32 output rows each take the tasks (up to eight tokens of one
-// adapter) in turn, with B and h from global memory, and store them to those columns, [token][row].
-// (That is slow beside the tensor core, whose operands take all of the shared memory's bandwidth: 15 us
-// for a tile of 256 tokens with two adapters, whose k-blocks take 4.)
+// tile have one adapter (most of a prompt) that is all.  In a mixed tile every adapter has its own
+// k-blocks, with a plane of h that has zeros for the other tokens.  A result that is not finite may then
+// come from another request's adapter (0 * inf), and is computed again by itself, so that nothing of
+// one adapter reaches another's tokens.  For more than eight adapters in a tile there are no planes.
+// Then the helpers multiply B and h with mma.sync: four warps with 32 output rows each take the tasks
+// (up to eight tokens of one adapter) in turn, with B and h from global memory, and store them to TMEM
+// columns of their own, [token][row], which the epilogue adds.  For a bf16 y these are the columns of
+// the next tile's accumulator, which then starts after the epilogue; for a float32 y, of 128 tokens,
+// there are columns for the three accumulators (see gdn_adapt.cu) and these.  (That is slow beside the
+// tensor core, whose operands take all of the shared memory's bandwidth: 15 us for a tile of 256 tokens
+// with two adapters, whose k-blocks take 4.)
 #include "gdn_adapt.cuh"
 
 namespace gdn {
@@ -53,8 +53,6 @@ constexpr int kMany = -2, kGaveUp = -3, kMixed = -4;
 __device__ __forceinline__ int adapters_of(int one) {
   return one >= 0 ? 1 : one <= kMixed ? kMixed - one : 0;
 }
-// Whether a tile's adapters add to columns of their own.
-__device__ __forceinline__ bool apart(int one) { return one == kMany || one <= kMixed; }
 
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
@@ -214,21 +212,24 @@ __device__ __forceinline__ void expand_rank(const AdaptArgs &g, const Groups<BT>
     expand<BT, 16, 2, 2, WHOLE, PARTS>(g, s, warp, quad, n0, tok0, scratch, delta);
 }
 
-// The adapters' part of one output: row n, token t of a tile with the adapters list[0 .. count).
+// One output by itself: row n, token t of a tile with the adapters list[0 .. count).
 template <int PARTS>
 __device__ __noinline__ float one_by_one(const AdaptArgs &g, const int *list, int count, int t, int n) {
+  const bf16 *x = static_cast<const bf16 *>(g.x) + t * g.ld_x;
+  const bf16 *w = static_cast<const bf16 *>(g.w) + n * g.ld_w;
+  float sum = 0.f;
+  for (int k = 0; k < g.hidden; ++k) sum += __bfloat162float(w[k]) * __bfloat162float(x[k]);
   const int id = token_id(g, t), ld = g.rank_pad();
-  if (id < 0) return 0.f;
+  if (id < 0) return sum;
   int plane = 0;
   while (plane + 1 < count && list[plane] != id) ++plane;
   kv::dependent_wait();
   const bf16 *b = static_cast<const bf16 *>(g.b) + ((int64_t)id * g.n_out + n) * g.ld_b;
   const bf16 *h = static_cast<const bf16 *>(g.h) + ((int64_t)plane * PARTS * g.tokens + t) * ld;
-  float sum = 0.f;
   for (int r = 0; r < g.rank; ++r) {
-    float x = __bfloat162float(h[r]);
-    for (int p = 1; p < PARTS; ++p) x += __bfloat162float(h[(int64_t)p * g.tokens * ld + r]);
-    sum += __bfloat162float(b[r]) * x;
+    float low = __bfloat162float(h[r]);
+    for (int p = 1; p < PARTS; ++p) low += __bfloat162float(h[(int64_t)p * g.tokens * ld + r]);
+    sum += __bfloat162float(b[r]) * low;
   }
   return sum;
 }
@@ -392,14 +393,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto free_after = [&](int last) {
         return last < 0 || wait(&acc_empty[last & 1], (uint32_t)((last >> 1) & 1), abort_flag);
       };
-      if (one == kGaveUp || !free_after(C::kF32 || apart(before) ? i - 1 : i - 2)) {
+      if (one == kGaveUp || !free_after(C::kF32 || before == kMany ? i - 1 : i - 2)) {
         good = false;
         break;
       }
       before = one;
       tc::fence_after_sync();
       const uint32_t base = C::kF32 ? tmem : tmem + (uint32_t)(i & 1) * BT;
-      const uint32_t delta = C::kF32 ? tmem + 3 * BT : tmem + (uint32_t)((i & 1) ^ 1) * BT;
       // the next k-block's products; a loop round it has 256 cycles
       auto block = [&](uint32_t acc, int steps, bool fresh) {
         if (!wait(&full[s], round, abort_flag)) return false;
@@ -419,20 +419,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         good = block(base + (uint32_t)turn * BT, kBK / 16, kb < C::kAcc);
         turn = turn + 1 == C::kAcc ? 0 : turn + 1;
       }
-      // the adapters, to the same place, or (the last tile's accumulator, which has to be read) apart
-      const int count = adapters_of(one);
-      if (good && one <= kMixed) good = free_after(i - 1);
-      tc::fence_after_sync();
-      for (int j = 0, kb = plain; j < count; ++j)
+      for (int j = adapters_of(one), kb = plain; j > 0; --j)
         for (int c = 0; c < chunks; ++c)
           for (int p = 0; p < C::kParts && good; ++p, ++kb) {
-            const int steps = min(kBK, g.rank16() - c * kBK) / 16;
-            if (one <= kMixed) {
-              good = block(delta, steps, kb == plain);
-            } else {
-              good = block(base + (uint32_t)turn * BT, steps, kb < C::kAcc);
-              turn = turn + 1 == C::kAcc ? 0 : turn + 1;
-            }
+            good = block(base + (uint32_t)turn * BT, min(kBK, g.rank16() - c * kBK) / 16,
+                         kb < C::kAcc);
+            turn = turn + 1 == C::kAcc ? 0 : turn + 1;
           }
       if (good) commit_pair(&acc_full[i & 1]);
     }
@@ -514,42 +506,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
 #pragma unroll 1
       for (int c = 16 * side; c < live; c += 16 * kTeams) {
-        float v[32];  // W x, and the adapters' part
+        float v[32];
         if constexpr (C::kF32) {
           float u[32];
           tc::tmem_ld32(acc + c, acc + BT + c, v);
-          const int kbs = plain + (one >= 0 ? chunks * C::kParts : 0);
+          const int kbs = plain + adapters_of(one) * chunks * C::kParts;
           if (kbs > 1)  // (an accumulator that no k-block has come to holds anything)
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
-          if (apart(one))
+          if (one == kMany)
             tc::tmem_ld32(acc + 2 * BT + c, delta + c, u);
           else
             tc::tmem_ld16(acc + 2 * BT + c, u);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             if (kbs > 2) v[j] += u[j];
-            v[16 + j] = u[16 + j];
+            if (one == kMany) v[j] += u[16 + j];
           }
-        } else if (apart(one)) {
+        } else if (one == kMany) {
           tc::tmem_ld32(acc + c, delta + c, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
         } else {
           tc::tmem_ld16(acc + c, v);
         }
-        if (apart(one)) {
-          if (one <= kMixed) {
-            bool odd = false;
+        if (one <= kMixed) {
+          bool odd = false;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) odd = odd || !(fabsf(v[16 + j]) < INFINITY);
-            if (odd && n < g.n_out)
+          for (int j = 0; j < 16; ++j) odd = odd || !(fabsf(v[j]) < INFINITY);
+          if (odd && n < g.n_out)
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (c + j < live && !(fabsf(v[16 + j]) < INFINITY))
-                  v[16 + j] = one_by_one<C::kParts>(g, s_list[i % kInfo], kMixed - one,
-                                                    tok0 + c + j, n);
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
+            for (int j = 0; j < 16; ++j)
+              if (c + j < live && !(fabsf(v[j]) < INFINITY))
+                v[j] = one_by_one<C::kParts>(g, s_list[i % kInfo], kMixed - one, tok0 + c + j, n);
+          __syncwarp();
         }
         if constexpr (C::kF32) {
           if (n < g.n_out)
