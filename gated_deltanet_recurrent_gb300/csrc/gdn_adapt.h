@@ -29,10 +29,11 @@ struct AdaptArgs {
   GDN_HD int rank_pad() const { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 };
 
+// (With 64, 512 tokens with 64 adapters, 2048 -> 5120 at rank 64, took 140 us, with eight 112.)
 constexpr int kPlanes = 8;
 
 size_t adapt_workspace_bytes(const AdaptArgs &g);
-// What the kernels that the call takes need of `tile`.
+// The `tile` that the kernels of this call go by.
 int adapt_tile(const AdaptArgs &g);
 // The low side, then the projection; cudaErrorNotSupported: no tensor map.
 cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s);

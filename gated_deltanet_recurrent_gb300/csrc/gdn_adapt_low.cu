@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
   constexpr int kTok = 16 * MT, kRanks = 8 * NT;
   extern __shared__ float s_part[];  // [kWarps][kTok][kRanks]
   __shared__ int s_id[kTok], s_lead[kTok], s_n;
+  __shared__ int s_plane[PLANES ? kTok : 1];
   __shared__ int s_tile[kPlanes], s_tile_n;  // PLANES: the adapters of the window's tile
   kv::dependent_wait();
   // the projection may start loading what no kernel before this one writes
@@ -99,33 +100,40 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
     if (lane == 0) s_n = n;
   }
   if (PLANES && warp == 1) {
-    int list[kPlanes];
     const int t0 = tok0 / g.tile * g.tile;
-    const int n = tile_groups(g, t0, min(g.tile, g.tokens - t0), list);
-    if (lane == 0) {
-      s_tile_n = n;
-#pragma unroll
-      for (int j = 0; j < kPlanes; ++j) s_tile[j] = list[j];
-    }
+    const int n = tile_groups(g, t0, min(g.tile, g.tokens - t0), s_tile);
+    if (lane == 0) s_tile_n = n;
   }
   __syncthreads();
-  // planes that a token has a row in, and the words from one to the next
-  const int planes = !PLANES || s_tile_n > kPlanes ? 1 : s_tile_n;
   const int64_t part_words = (int64_t)g.tokens * (g.rank_pad() / 2);
-  if (PLANES && blockIdx.y == 0 && s_tile_n <= kPlanes)  // zeros for tokens without an adapter
-    for (int i = tid; i < kTok * kRanks / 2; i += 32 * kWarps) {
-      const int t = 2 * i / kRanks, r = rank0 + 2 * i % kRanks;
-      if (s_id[t] >= 0 || tok0 + t >= g.tokens || r >= g.rank_pad()) continue;
-      uint32_t *h = static_cast<uint32_t *>(g.h) + ((int64_t)(tok0 + t) * g.rank_pad() + r) / 2;
-      for (int p = 0; p < planes * g.parts(); ++p) h[p * part_words] = 0;
+  if (PLANES) {
+    if (tid < kTok) {
+      int plane = 0;
+      if (s_id[tid] < 0)
+        plane = -1;
+      else if (s_tile_n <= kPlanes)
+        while (s_tile[plane] != s_id[tid]) ++plane;
+      s_plane[tid] = plane;
     }
+    __syncthreads();
+    // zeros in the planes of the tile's other adapters, shared by the CTAs of a window
+    if (s_tile_n <= kPlanes) {
+      constexpr int kVecs = kRanks / 8;
+      const int rows = kTok * g.parts() * kVecs;
+      for (int j = blockIdx.y; j < s_tile_n; j += gridDim.y)
+        for (int i = tid; i < rows; i += 32 * kWarps) {
+          const int v = i % kVecs, t = i / kVecs % kTok, p = i / (kVecs * kTok), r = rank0 + 8 * v;
+          if (s_plane[t] == j || tok0 + t >= g.tokens || r >= g.rank_pad()) continue;
+          reinterpret_cast<uint4 *>(static_cast<uint32_t *>(g.h) +
+                                    (j * g.parts() + p) * part_words)[
+              ((int64_t)(tok0 + t) * g.rank_pad() + r) / 8] = make_uint4(0, 0, 0, 0);
+        }
+    }
+  }
   const int rank_pad = g.rank_pad(), parts = g.parts();
   for (int gi = blockIdx.y; gi < s_n; gi += gridDim.y) {
     const int id = s_lead[gi];
     const float scale = g.scale[id];
-    int plane = 0;
-    if (PLANES && s_tile_n <= kPlanes)
-      while (s_tile[plane] != id) ++plane;
     const bf16 *a = static_cast<const bf16 *>(g.a) + (int64_t)id * g.rank * g.ld_a;
     float acc[MT][NT][4];
 #pragma unroll
@@ -183,11 +191,12 @@ __global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
       }
       // (zeros beyond the rank, whatever the scale is)
       float x = r < g.rank ? sum.x * scale : 0.f, y = r + 1 < g.rank ? sum.y * scale : 0.f;
-      uint32_t *h = static_cast<uint32_t *>(g.h) + ((int64_t)(tok0 + t) * rank_pad + r) / 2;
+      uint32_t *h = static_cast<uint32_t *>(g.h) + ((int64_t)(tok0 + t) * rank_pad + r) / 2 +
+                    (PLANES ? s_plane[t] * parts * part_words : 0);
       for (int p = 0; p < parts; ++p) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
         const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
-        for (int j = 0; j < planes; ++j) h[(j * parts + p) * part_words] = j == plane ? w : 0;
+        h[p * part_words] = w;
         const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
         // (what is infinite or NaN is the first part alone)
         x = fabsf(lo) < INFINITY ? x - lo : 0.f;
@@ -215,10 +224,15 @@ cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
 
 }  // namespace
 
+// Few tokens: small windows, for parallel loads of A; many: large ones, that read A less often (512 with
+// 64 adapters of rank 64: 112 and 123 us with the projection, 1024 in prompts 63 and 61).
+constexpr int kFewWindows = 512;
+
 cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s) {
-  // few tokens: small windows, for parallel loads of A; many: large ones, that read A less often
   if (g.tile > 0)
-    return g.hidden % 8 == 0 ? launch<4, 4, 1, true, true>(g, s) : launch<1, 2, 1, false, true>(g, s);
+    return g.hidden % 8 != 0     ? launch<1, 2, 1, false, true>(g, s)
+           : g.tokens <= kFewWindows ? launch<1, 2, 4, true, true>(g, s)
+                                 : launch<4, 4, 1, true, true>(g, s);
   return g.hidden % 8 == 0 ? launch<1, 2, 4, true, false>(g, s)
                            : launch<1, 2, 1, false, false>(g, s);
 }

@@ -15,8 +15,8 @@
 // tile have one adapter (most of a prompt) that is all.  In a mixed tile every adapter has its own
 // k-blocks, with a plane of h that has zeros for the other tokens.  A result that is not finite may then
 // come from another request's adapter (0 * inf), and is computed again by itself, so that nothing of
-// one adapter reaches another's tokens.  For more than eight adapters in a tile there are no planes.
-// Then the helpers multiply B and h with mma.sync: four warps with 32 output rows each take the tasks
+// one adapter reaches another's tokens.  For more than eight adapters in a tile
+// the helpers multiply B and h with mma.sync: four warps with 32 output rows each take the tasks
 // (up to eight tokens of one adapter) in turn, with B and h from global memory, and store them to TMEM
 // columns of their own, [token][row], which the epilogue adds.  For a bf16 y these are the columns of
 // the next tile's accumulator, which then starts after the epilogue; for a float32 y, of 128 tokens,
@@ -439,21 +439,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool good = true;
     for (int64_t t = pair; t < tiles && good; t += pairs, ++i) {
       const int tok0 = (int)(t / n_tiles) * BT, live = min(BT, g.tokens - tok0);
-      int list[kPlanes];
-      const int n = tile_groups(g, tok0, live, list);
+      if (i >= kInfo)
+        good = __all_sync(0xffffffffu,
+                          wait(&info_empty[i % kInfo], ((i / kInfo) - 1) & 1, abort_flag));
+      if (!good) break;
+      const int n = tile_groups(g, tok0, live, s_list[i % kInfo]);
       bool whole = true;  // no token without an adapter
 #pragma unroll
       for (int j = 0; j < BT / 32; ++j)
         if (32 * j + lane < live) whole = whole && token_id(g, tok0 + 32 * j + lane) >= 0;
       whole = __all_sync(0xffffffffu, whole);
-      if (i >= kInfo)
-        good = __all_sync(0xffffffffu,
-                          wait(&info_empty[i % kInfo], ((i / kInfo) - 1) & 1, abort_flag));
-      if (good && lane == 0) {
-#pragma unroll
-        for (int j = 0; j < kPlanes; ++j) s_list[i % kInfo][j] = list[j];
+      if (lane == 0) {
         *reinterpret_cast<volatile int *>(&s_info[i % kInfo]) =
-            n == 0 ? -1 : n == 1 && whole ? list[0] : n > kPlanes ? kMany : kMixed - n;
+            n == 0 ? -1 : n == 1 && whole ? s_list[i % kInfo][0] : n > kPlanes ? kMany : kMixed - n;
         mbar_arrive(&info_full[i % kInfo]);
       }
     }
