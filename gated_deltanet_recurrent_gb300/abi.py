@@ -758,6 +758,12 @@ def gdn_kv_attend(kv: KVCache, layer: int, slot_ids: torch.Tensor, kv_lens: torc
     return o
 
 
+def _elsewhere(t, device):
+    """Whether t is not on the GPU of that index (-1: the host's memory)."""
+    d = t.get_device()
+    return d != device or (d < 0 and t.is_meta)
+
+
 # ----------------------------------------- pages of the KV cache, on the GPU
 
 class KVPages:
@@ -781,16 +787,17 @@ class KVPages:
                 raise GDNError(5, f"{name} must have {size} entries")
         self.page_table, self.held, self.free_pages, self.n_free = \
             kv.page_table, held, free_pages, n_free
+        self.device = held.get_device()
         self.desc = gdn_kv_pages(kv.page_table.data_ptr(), held.data_ptr(),
                                  free_pages.data_ptr(), n_free.data_ptr())
         self.desc_ptr = ctypes.addressof(self.desc)
 
 
 def _like(t, name, dtype, size, device):
-    """Pointer of an optional output array."""
+    """Pointer of an optional output array; device: an index."""
     if t is None:
         return None
-    if t.dtype != dtype or not t.is_contiguous() or t.device != device:
+    if t.dtype != dtype or _elsewhere(t, device) or not t.is_contiguous():
         raise GDNError(1, f"{name} must be a contiguous {dtype} tensor on slot_ids' device")
     if t.numel() != size:
         raise GDNError(5, f"{name} must have {size} entries")
@@ -806,7 +813,6 @@ def gdn_kv_pages_grow(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, pos: 
     packed by cu_seqlens).  positions (int32), rows (int64): [total_tokens], where each token
     goes; granted (int32): [n_seqs], 0 where the free pages did not suffice; each is written if
     given.  total_tokens is needed where neither positions nor rows says it."""
-    n, device = slot_ids.numel(), slot_ids.device
     tokens = rows.numel() if rows is not None else \
         positions.numel() if positions is not None else total_tokens
     if total_tokens not in (-1, tokens):
@@ -814,16 +820,18 @@ def gdn_kv_pages_grow(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, pos: 
     if tokens < 0:
         if cu_seqlens is not None:
             raise GDNError(1, "total_tokens is needed with cu_seqlens")
-        tokens = n
-    if device != pages.held.device or pos.device != device or \
-            (cu_seqlens is not None and cu_seqlens.device != device):
+        tokens = slot_ids.numel()
+    device = pages.device
+    if _elsewhere(slot_ids, device) or _elsewhere(pos, device) or \
+            (cu_seqlens is not None and _elsewhere(cu_seqlens, device)):
         raise GDNError(1, "slot_ids, pos and cu_seqlens must be on the cache's device")
     slots, starts, cu, n = _kv_index(slot_ids, pos, cu_seqlens, tokens, "pos")
     status = _lib.gdn_kv_pages_grow(
         kv.handle, pages.desc_ptr, slots, starts, cu, n, tokens,
         _like(positions, "positions", torch.int32, tokens, device),
         _like(rows, "rows", torch.int64, tokens, device),
-        _like(granted, "granted", torch.int32, n, device), _kv_stream(stream, slot_ids))
+        _like(granted, "granted", torch.int32, n, device),
+        stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device))
     if status:
         _check(status)
 
@@ -831,12 +839,13 @@ def gdn_kv_pages_grow(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, pos: 
 def gdn_kv_pages_trim(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, lens: torch.Tensor,
                       stream=None):
     """Give back the pages that the first lens[i] tokens of slot slot_ids[i] do not use."""
-    n, device = slot_ids.numel(), slot_ids.device
-    if device != pages.held.device or lens.device != device:
+    device = pages.device
+    if _elsewhere(slot_ids, device) or _elsewhere(lens, device):
         raise GDNError(1, "slot_ids and lens must be on the cache's device")
-    slots, starts, _, n = _kv_index(slot_ids, lens, None, n, "lens")
-    status = _lib.gdn_kv_pages_trim(kv.handle, pages.desc_ptr, slots, starts, n,
-                                    _kv_stream(stream, slot_ids))
+    slots, starts, _, n = _kv_index(slot_ids, lens, None, slot_ids.numel(), "lens")
+    status = _lib.gdn_kv_pages_trim(
+        kv.handle, pages.desc_ptr, slots, starts, n,
+        stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device))
     if status:
         _check(status)
 
@@ -885,23 +894,29 @@ def gdn_rope_destroy(rope: Rope):
 
 def _rope_rows(x, out, d, tokens, dtype, device, name):
     """Pointer, token stride and heads of x [tokens, heads, d], and pointer and stride of out
-    (None: x itself)."""
+    (None: x itself); device: an index."""
     shape = x.shape
     if len(shape) != 3 or shape[0] != tokens:
         raise GDNError(5, f"{name} must be [{tokens}, heads, {d}], got {tuple(shape)}")
     heads = shape[1]
     ld = _kv_token_rows(shape, x.stride(), heads, d, name)
+    ptr = x.data_ptr()
+    if x.dtype != dtype or x.get_device() != device:
+        _rope_refuse(x, dtype, name)
     if out is None or out is x:
-        out, ld_out = x, ld
-    else:
-        if out.shape != shape:
-            raise GDNError(5, f"{name}_out must have {name}'s shape {tuple(shape)}")
-        ld_out = _kv_token_rows(shape, out.stride(), heads, d, f"{name}_out")
-    if x.dtype != dtype or out.dtype != dtype:
+        return ptr, ld, heads, ptr, ld
+    if out.shape != shape:
+        raise GDNError(5, f"{name}_out must have {name}'s shape {tuple(shape)}")
+    if out.dtype != dtype or out.get_device() != device:
+        _rope_refuse(out, dtype, name)
+    return ptr, ld, heads, out.data_ptr(), _kv_token_rows(shape, out.stride(), heads, d,
+                                                          f"{name}_out")
+
+
+def _rope_refuse(t, dtype, name):
+    if t.dtype != dtype:
         raise GDNError(4, "q, k and their outputs must share one dtype")
-    if x.device != device or out.device != device:
-        raise GDNError(1, f"{name} must be on the positions' device")
-    return x.data_ptr(), ld, heads, out.data_ptr(), ld_out
+    raise GDNError(1, f"{name} must be on the positions' device")
 
 
 def gdn_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor],
@@ -913,23 +928,27 @@ def gdn_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor],
     first = k if q is None else q
     if first is None:
         raise GDNError(1, "q or k is needed")
-    tokens, dtype, device = positions.numel(), first.dtype, positions.device
-    code = _kv_dtype(first)
-    if positions.dtype != torch.int32 or not positions.is_contiguous() or \
-            device.type != "cuda":
+    tokens, dtype, device = positions.numel(), first.dtype, positions.get_device()
+    code = _KV_DTYPES.get(dtype)
+    if code is None:
+        raise GDNError(4, f"unsupported dtype {dtype}")
+    if positions.dtype != torch.int32 or device < 0 or not positions.is_contiguous():
         raise GDNError(1, "positions must be a contiguous int32 tensor on the GPU")
-    if tokens == 0:
-        return q if q_out is None else q_out, k if k_out is None else k_out
-    q_ptr = q_to = k_ptr = k_to = None
-    ld_q = h_q = ld_q_to = ld_k = h_k = ld_k_to = 0
-    if q is not None:
-        q_ptr, ld_q, h_q, q_to, ld_q_to = _rope_rows(q, q_out, rope.d, tokens, dtype, device, "q")
-    if k is not None:
-        k_ptr, ld_k, h_k, k_to, ld_k_to = _rope_rows(k, k_out, rope.d, tokens, dtype, device, "k")
-    status = _lib.gdn_rope(rope.handle, tokens, positions.data_ptr(), q_ptr, ld_q, h_q, k_ptr, ld_k,
-                           h_k, q_to, ld_q_to, k_to, ld_k_to, code, _kv_stream(stream, positions))
-    if status:
-        _check(status)
+    if tokens:
+        q_ptr = q_to = k_ptr = k_to = None
+        ld_q = h_q = ld_q_to = ld_k = h_k = ld_k_to = 0
+        if q is not None:
+            q_ptr, ld_q, h_q, q_to, ld_q_to = _rope_rows(q, q_out, rope.d, tokens, dtype, device,
+                                                         "q")
+        if k is not None:
+            k_ptr, ld_k, h_k, k_to, ld_k_to = _rope_rows(k, k_out, rope.d, tokens, dtype, device,
+                                                         "k")
+        status = _lib.gdn_rope(
+            rope.handle, tokens, positions.data_ptr(), q_ptr, ld_q, h_q, k_ptr, ld_k, h_k, q_to,
+            ld_q_to, k_to, ld_k_to, code, stream.cuda_stream if stream is not None else
+            torch._C._cuda_getCurrentRawStream(device))
+        if status:
+            _check(status)
     return q if q_out is None else q_out, k if k_out is None else k_out
 
 
@@ -963,6 +982,7 @@ class Adapters:
                                   f"stride (strides {t.stride()})")
             lds.append(ld)
         self.a, self.b, self.scale = a, b, scale
+        self.device = a.get_device()
         self.desc = gdn_adapters_desc(n, self.rank, self.hidden, self.n_out,
                                       1 if host_checks else 0)
         self.handle = gdn_adapters_create(self.desc, a, lds[0], b, lds[1], scale)
@@ -992,20 +1012,20 @@ def gdn_adapters_destroy(adapters: Adapters):
 
 def _proj_rows(t, rows, width, device, name):
     """Row stride of t [rows, width] with unit column stride (0: one row or none)."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] != rows or shape[1] != width:
-        raise GDNError(5, f"{name} must be [{rows}, {width}], got {tuple(shape)}")
-    if t.device != device:
+    if t.shape != (rows, width):
+        raise GDNError(5, f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
+    if _elsewhere(t, device):
         raise GDNError(1, f"{name} must be on the adapters' device")
     if rows == 0:
         return 0
-    if stride[1] != 1 and width > 1:
-        raise GDNError(1, f"{name} must have a unit column stride (strides {stride})")
-    if rows <= 1:
+    ld, unit = t.stride()
+    if unit != 1 and width > 1:
+        raise GDNError(1, f"{name} must have a unit column stride (strides {t.stride()})")
+    if rows == 1:
         return 0
-    if stride[0] < width:  # an expanded row (stride 0) is not the library's "packed" (0)
-        raise GDNError(1, f"{name}: row stride {stride[0]} smaller than a row of {width}")
-    return stride[0]
+    if ld < width:  # an expanded row (stride 0) is not the library's "packed" (0)
+        raise GDNError(1, f"{name}: row stride {ld} smaller than a row of {width}")
+    return ld
 
 
 def gdn_in_proj_adapted(pool: Pool, adapters: Adapters, x: torch.Tensor, w: torch.Tensor,
@@ -1013,22 +1033,25 @@ def gdn_in_proj_adapted(pool: Pool, adapters: Adapters, x: torch.Tensor, w: torc
     """y[t] = W x[t] + scale[a] B[a] (A[a] x[t]) with a = ids[t] (-1: none): x [tokens, hidden]
     and w [n_out, hidden] bf16, ids [tokens] int32, y [tokens, n_out] float32 or bf16 (default
     float32)."""
-    tokens, device = ids.numel(), adapters.a.device
-    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+    tokens, device = ids.numel(), adapters.device
+    hidden, n_out = adapters.hidden, adapters.n_out
+    bf16 = torch.bfloat16
+    if x.dtype != bf16 or w.dtype != bf16:
         raise GDNError(4, "x and w must be bf16")
-    if ids.dtype != torch.int32 or not ids.is_contiguous() or ids.device != device:
+    if ids.dtype != torch.int32 or _elsewhere(ids, device) or not ids.is_contiguous():
         raise GDNError(1, "ids must be a contiguous int32 tensor on the adapters' device")
-    ld_x = _proj_rows(x, tokens, adapters.hidden, device, "x")
-    ld_w = _proj_rows(w, adapters.n_out, adapters.hidden, device, "w")
+    ld_x = _proj_rows(x, tokens, hidden, device, "x")
+    ld_w = _proj_rows(w, n_out, hidden, device, "w")
     if y is None:
-        y = torch.empty(tokens, adapters.n_out, dtype=torch.float32, device=device)
-    ld_y = _proj_rows(y, tokens, adapters.n_out, device, "y")
+        y = torch.empty(tokens, n_out, dtype=torch.float32, device=ids.device)
+    ld_y = _proj_rows(y, tokens, n_out, device, "y")
     if tokens <= 1:  # the stride of a single row says nothing, and has to be aligned
-        ld_y = -(-adapters.n_out // 8) * 8
-        ld_x = -(-adapters.hidden // 8) * 8
-    status = _lib.gdn_in_proj_adapted(pool.handle, adapters.handle, tokens, x.data_ptr(), ld_x,
-                                      w.data_ptr(), ld_w, ids.data_ptr(), y.data_ptr(), ld_y,
-                                      _kv_dtype(y), _kv_stream(stream, ids))
+        ld_y = -(-n_out // 8) * 8
+        ld_x = -(-hidden // 8) * 8
+    status = _lib.gdn_in_proj_adapted(
+        pool.handle, adapters.handle, tokens, x.data_ptr(), ld_x, w.data_ptr(), ld_w,
+        ids.data_ptr(), y.data_ptr(), ld_y, _kv_dtype(y), stream.cuda_stream if stream is not None
+        else torch._C._cuda_getCurrentRawStream(device))
     if status:
         _check(status)
     return y

@@ -84,7 +84,7 @@ def test_the_binding_refuses(monkeypatch):
     refused("GDN_ERR_ARG", at, None)
     refused("GDN_ERR_ARG", at, q)          # a CPU tensor
     refused("GDN_ERR_DTYPE", at, q.half())
-    rows = lambda x, out=None, n=3: abi._rope_rows(x, out, 64, n, torch.float32, at.device, "q")
+    rows = lambda x, out=None, n=3: abi._rope_rows(x, out, 64, n, torch.float32, at.get_device(), "q")
     for x, out in ((q[:2], None), (q[..., :32], None), (q, q[:, :1]), (q[:, 0], None)):
         with pytest.raises(abi.GDNError) as e:
             rows(x, out)
