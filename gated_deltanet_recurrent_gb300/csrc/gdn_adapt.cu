@@ -63,24 +63,18 @@ struct Cfg {
   static_assert(BT * kBM * 4 <= kRingB, "a cluster's parts take the place of the B tiles");
 };
 
-// A ring of B tiles of 128 rows of PITCH bytes.  Rows of just that width that follow each other come
-// as one piece (`plain`): a tensor copy takes some three cycles for each row, be it 32 bytes long
-// (64 adapters of rank 16 beside 2048 -> 12352: 33 us with it).  Others are in the swizzle of a tensor copy.
+// A ring of B tiles of 128 rows of PITCH bytes, in the swizzle of that width.
 struct RingB {
   unsigned char *tiles;
   uint64_t *full, *empty;
-  bool plain;
 };
-// Whether B's rows follow each other at a pitch of `pitch` bytes.
-__host__ __device__ inline bool plain_rows(const AdaptArgs &g, int pitch) {
-  return g.rank * 2 == pitch && g.ld_b == g.rank;
-}
 template <int PITCH>
 constexpr int kSlots = kRingB / (kBM * PITCH);
 
-// where the swizzle of a row's width puts byte `off` of a tile; mask 0: no swizzle
-__device__ __forceinline__ uint32_t swizzled(uint32_t off, uint32_t mask) {
-  return off ^ (((off >> 7) & mask) << 4);
+// where that puts byte `off` of a tile
+template <int PITCH>
+__device__ __forceinline__ uint32_t swizzled(uint32_t off) {
+  return off ^ (((off >> 7) & (PITCH / 16 - 1)) << 4);
 }
 
 // Where 16 bytes of h lie in shared memory, [part][token][PITCH]: two neighbouring tokens' rows take
@@ -103,7 +97,6 @@ __device__ __forceinline__ bool expand(const AdaptArgs &g, const Groups<BT> &s, 
   static_assert(E % kTeams == 0, "a slot is always the same team's, which then is never two rounds ahead");
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3, row0 = 32 * (warp & 3);
   const int team = warp >> 2, ld = g.rank_pad(), halves = ld * 2 / PITCH;
-  const uint32_t mask = ring.plain ? 0 : PITCH / 16 - 1;
   float *const to = delta + row0 + r;
   bool good = true;
   for (int half = 0; half < halves; ++half) {
@@ -135,9 +128,8 @@ __device__ __forceinline__ bool expand(const AdaptArgs &g, const Groups<BT> &s, 
         for (int l = 0; l < NL; ++l)
 #pragma unroll
           for (int y = 0; y < 2; ++y)
-            load_words<W>(tile + swizzled((uint32_t)((row0 + 16 * m + r + 8 * y) * PITCH +
-                                                     l * 4 * W + c * W),
-                                          mask),
+            load_words<W>(tile + swizzled<PITCH>((uint32_t)((row0 + 16 * m + r + 8 * y) * PITCH +
+                                                            l * 4 * W + c * W)),
                           b[m][l][y]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[e]);
@@ -264,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kbs = plain + extra * (part + 1) / splits - eb0;
   const int halves = g.rank_pad() * 2 / PITCH;
   volatile int *abort_flag = &s_abort;
-  const RingB ring{ring_b, b_full, b_empty, plain_rows(g, PITCH)};
+  const RingB ring{ring_b, b_full, b_empty};
   auto fail = [&]() {
     *abort_flag = 1;
     raise_error(g.err, GDN_DEVERR_TIMEOUT);
@@ -311,14 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int half = u >= s_groups.n, group = u - half * s_groups.n;
           const int row = s_groups.adapter[group] * g.n_out + n0;
           unsigned char *tile = ring_b + lane * (kBM * PITCH);
-          if (ring.plain) {
-            const uint32_t bytes = (uint32_t)min(kBM, g.n_out - n0) * PITCH;
-            mbar_arrive_expect_tx(&b_full[lane], bytes);
-            bulk_g2s(tile, static_cast<const bf16 *>(g.b) + row * g.ld_b, bytes, &b_full[lane]);
-          } else {
-            mbar_arrive_expect_tx(&b_full[lane], kBM * PITCH);
-            tma_load2(tile, &mu, half * (PITCH / 2), row, &b_full[lane]);
-          }
+          mbar_arrive_expect_tx(&b_full[lane], kBM * PITCH);
+          tma_load2(tile, &mu, half * (PITCH / 2), row, &b_full[lane]);
           issued = u;
           u += E;
           moved = true;
@@ -482,9 +468,11 @@ template <int BT, int PITCH, typename TO>
 cudaError_t launch_split(const AdaptArgs &g, cudaStream_t s) {
   const int64_t tiles = (int64_t)((g.n_out + kBM - 1) / kBM) * ((g.tokens + BT - 1) / BT);
   const int blocks = (g.hidden + kBK - 1) / kBK;
-  // CTAs that share a tile: as many as fit on the device at once, with four k-blocks each at least
+  // CTAs that share a tile: as many as fit on the device at once, with four k-blocks each at least, and
+  // four at most (one token, 2048 -> 5120: one CTA a tile 16.6 us, two 13.0, three 11.6; 64 tokens with an
+  // adapter each, 2048 -> 2048: two 17.1 us, four 13.8, eight 21.6)
   const int64_t most = g.sm_count / tiles < blocks / 4 ? g.sm_count / tiles : blocks / 4;
-  const int splits = most > 8 ? 8 : (int)most;
+  const int splits = most > 4 ? 4 : (int)most;
   return splits > 1 ? launch<BT, PITCH, TO, true>(g, splits, s)
                     : launch<BT, PITCH, TO, false>(g, 1, s);
 }

@@ -58,8 +58,10 @@ gdn_status gdn_adapters_create(const gdn_adapters_desc *d, const void *a, int64_
   if (d->n_adapters < 1 || d->rank < 1 || d->hidden < 1 || d->n_out < 1)
     return fail(GDN_ERR_ARG, "adapter dimensions must be positive");
   if (d->rank > 128) return fail(GDN_ERR_UNSUPPORTED, "rank = %d (at most 128)", d->rank);
-  if ((int64_t)d->n_adapters * d->n_out > INT32_MAX || (int64_t)d->n_adapters * d->rank > INT32_MAX)
-    return fail(GDN_ERR_UNSUPPORTED, "n_adapters * n_out and * rank must stay below 2^31");
+  // (rows of a and b are int32, and a tile's may lie up to 255 behind the last)
+  if ((int64_t)d->n_adapters * d->n_out > INT32_MAX - 256 ||
+      (int64_t)d->n_adapters * d->rank > INT32_MAX - 256)
+    return fail(GDN_ERR_UNSUPPORTED, "n_adapters * n_out and * rank must stay below 2^31 - 256");
   if (!a || !b || !scale) return fail(GDN_ERR_ARG, "a, b and scale must be non-NULL");
   gdn_status st;
   if ((st = check_rows(a, &ld_a, d->hidden, "a")) || (st = check_rows(b, &ld_b, d->rank, "b")))

@@ -79,7 +79,7 @@ SHAPES = [(256, 384, 16), (64, 128, 8), (2048, 2048, 64), (512, 1040, 32), (72, 
 
 
 @pytest.mark.parametrize("hidden,n_out,rank", SHAPES)
-@pytest.mark.parametrize("tokens", [1, 2, 17, 64, 100, 129, 300])
+@pytest.mark.parametrize("tokens", [1, 2, 3, 4, 5, 17, 64, 100, 129, 300])
 def test_whole_numbers(pool, hidden, n_out, rank, tokens):
     rng = np.random.default_rng(hidden + rank + tokens)
     n = 5 if tokens < 100 else 37
@@ -116,6 +116,47 @@ def test_whole_numbers_of_many_tokens(pool, tokens, hidden, n_out, rank, n):
     assert abi.gdn_pool_get_error(pool) == 0
 
 
+@pytest.mark.parametrize("n_out", [5120, 6400, 2600, 1000])
+@pytest.mark.parametrize("tokens", [1, 33, 64])
+def test_tiles_that_several_blocks_share(pool, tokens, n_out):
+    """Long sums and few outputs: a tile is split over 3 or 4 blocks."""
+    hidden, rank, n = 2048, 64, 12
+    rng = np.random.default_rng(n_out + tokens)
+    w, a, b, scale = make(rng, hidden, n_out, rank, n)
+    x = whole(rng, 2, tokens, hidden)
+    ad = abi.Adapters(bf(a), bf(b), torch.tensor(scale, dtype=torch.float32, device="cuda"))
+    gx, gw = bf(x), bf(w)
+    for name, ids in patterns(tokens, n).items():
+        want, _, _ = adapted(x, w, a, b, scale, ids)
+        for dtype in (torch.float32, torch.bfloat16):
+            y = torch.full((tokens, n_out), 77.0, dtype=dtype, device="cuda")
+            abi.gdn_in_proj_adapted(pool, ad, gx, gw, i32(ids), y)
+            same(y, want)
+    assert abi.gdn_pool_get_error(pool) == 0
+
+
+def test_the_most_tokens(pool):
+    """2^18 tokens with runs, mixed tiles and scattered adapters among them."""
+    tokens, hidden, n_out, rank, n = 1 << 18, 64, 72, 16, 300
+    rng = np.random.default_rng(11)
+    w, a, b, scale = make(rng, hidden, n_out, rank, n)
+    x = whole(rng, 2, tokens, hidden)
+    ids = np.arange(tokens) // 700 % n
+    ids[5000:6000] = rng.integers(-1, n, 1000)
+    ids[-3:] = [7, -1, 299]
+    ad = abi.Adapters(bf(a), bf(b), torch.tensor(scale, dtype=torch.float32, device="cuda"))
+    want, _, _ = adapted(x, w, a, b, scale, ids)
+    for dtype in (torch.float32, torch.bfloat16):
+        y = torch.full((tokens, n_out), 77.0, dtype=dtype, device="cuda")
+        abi.gdn_in_proj_adapted(pool, ad, bf(x), bf(w), i32(ids), y)
+        same(y, want)
+    assert abi.gdn_pool_get_error(pool) == 0
+    with pytest.raises(abi.GDNError) as e:
+        abi.gdn_in_proj_adapted(pool, ad, torch.empty(tokens + 1, 64, device="cuda").bfloat16(), bf(w),
+                                i32([-1] * (tokens + 1)))
+    assert e.value.name == "GDN_ERR_SIZE"
+
+
 @pytest.mark.parametrize("tokens", [1, 40, 600, 4000])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_real_numbers(pool, tokens, dtype):
@@ -142,9 +183,10 @@ def test_real_numbers(pool, tokens, dtype):
         assert rel <= (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -18)
 
 
-@pytest.mark.parametrize("tokens", [3, 64, 200, 5000])
-def test_adapters_that_are_not_finite_spoil_their_own_tokens_only(pool, tokens):
-    hidden, n_out, rank, n = 256, 1300 // 8 * 8, 32, 8
+@pytest.mark.parametrize("tokens,n", [(1, 8), (3, 8), (4, 8), (5, 8), (64, 8), (200, 8), (5000, 8), (600, 8), (600, 40)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_adapters_that_are_not_finite_spoil_their_own_tokens_only(pool, tokens, n, dtype):
+    hidden, n_out, rank = 256, 1300 // 8 * 8, 32
     rng = np.random.default_rng(3)
     w, a, b, scale = make(rng, hidden, n_out, rank, n)
     x = whole(rng, 2, tokens, hidden)
@@ -157,12 +199,13 @@ def test_adapters_that_are_not_finite_spoil_their_own_tokens_only(pool, tokens):
         ids[0] = 3
         with np.errstate(invalid="ignore"):
             want, _, _ = adapted(x, w, a, b, scale, ids)
-        y = torch.empty(tokens, n_out, device="cuda")
+        y = torch.empty(tokens, n_out, dtype=dtype, device="cuda")
         ad = abi.Adapters(bf(a), bf(b), torch.tensor(scale, dtype=torch.float32, device="cuda"))
         abi.gdn_in_proj_adapted(pool, ad, bf(x), bf(w), i32(ids), y)
         y = y.double().cpu().numpy()
         good = np.isfinite(want)
         assert good[:-1].any() or tokens == 1
+        want = torch.from_numpy(want).to(dtype).double().numpy()
         assert np.array_equal(y[good], want[good])
         assert not np.isfinite(y[~good]).any()
 

@@ -259,6 +259,12 @@ def test_every_output_may_be_missing():
     b.same()
 
 
+def test_a_call_without_any_token():
+    b = Both(3, 12, 4, 16)
+    b.grow([0, 1], [0, 0], [20, 20])
+    assert b.grow([1, 0, 2], [20, 3, 0], [0, 0, 0]) == [1, 1, 1]
+
+
 def test_host_checks_refuse_before_anything_moves():
     b = Both(4, 12, 4, 16, host_checks=True)
     b.grow([0, 1], [0, 0], [20, 20])

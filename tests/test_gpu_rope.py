@@ -105,6 +105,18 @@ def test_many_tokens(layout, dtype):
     check(out, *rotated(q, p, 32, layout))
 
 
+@pytest.mark.parametrize("d,rot,start", [(4096, 64, 0), (4096, 512, 0), (2048, 510, 0), (1024, 512, 1)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tokens", [3, 4100])
+def test_heads_with_more_places_than_a_block_has_threads(d, rot, start, layout, dtype, tokens):
+    x = torch.randn(tokens * d + 8, device="cuda").to(dtype)[start:start + tokens * d]
+    x = x.view(tokens, 1, d)
+    p = positions_of(tokens, 9000)
+    out, _ = abi.gdn_rope(abi.Rope(d, rot, layout), i32(p), x, q_out=torch.empty_like(x))
+    check(out, *rotated(x, p, rot, layout))
+
+
 @pytest.mark.parametrize("shift", [1, 2, 3, 4])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
