@@ -464,9 +464,26 @@ cudaError_t launch(const AdaptArgs &g, int splits, cudaStream_t s) {
                     mw, mx, mb, mu, mh, g, splits);
 }
 
+int64_t tiles_of(const AdaptArgs &g, int bt) {
+  return (int64_t)((g.n_out + kBM - 1) / kBM) * ((g.tokens + bt - 1) / bt);
+}
+
+// How often tiles of bt tokens fill the device.
+int64_t rounds_of(const AdaptArgs &g, int bt) {
+  return (tiles_of(g, bt) + g.sm_count - 1) / g.sm_count;
+}
+
+// Tiles of 96 tokens where they take fewer rounds than tiles of 64: 256 tokens with 64 adapters of rank
+// 16, 2048 -> 5120: 26.6 and 41.3 us, 96 tokens, 2048 -> 12352: 25.9 and 36.5; 192 tokens, 2048 -> 5120, in
+// one round either way: 64 is faster.
+bool wide_tiles(const AdaptArgs &g) {
+  return rounds_of(g, 96) < rounds_of(g, 64);
+}
+
 template <int BT, int PITCH, typename TO>
 cudaError_t launch_split(const AdaptArgs &g, cudaStream_t s) {
-  const int64_t tiles = (int64_t)((g.n_out + kBM - 1) / kBM) * ((g.tokens + BT - 1) / BT);
+  const int64_t tiles = tiles_of(g, BT);
+  if constexpr (BT == 96) return launch<BT, PITCH, TO, false>(g, 1, s);  // (too many tiles to share any)
   const int blocks = (g.hidden + kBK - 1) / kBK;
   // CTAs that share a tile: as many as fit on the device at once, with four k-blocks each at least, and
   // four at most (one token, 2048 -> 5120: one CTA a tile 16.6 us, two 13.0, three 11.6; 64 tokens with an
@@ -484,13 +501,17 @@ cudaError_t launch_bt(const AdaptArgs &g, cudaStream_t s) {
                         : launch_split<BT, 128, TO>(g, s);
 }
 
-// Up to here tiles of 64 tokens, above pairs of CTAs.  256 tokens with 64 adapters, 2048 -> 5120: 41 and 63
-// us; 777 float32 tokens in runs of 50: 75 and 54; 1024 in prompts, 2048 -> 12352: 184 and 62.
-constexpr int kFewTokens = 256;
+// These kernels take calls of one tile's tokens, and others that fill the device at most twice;
+// pairs of CTAs take what is longer.  With 64 adapters of rank 64 in any order and with none (us, here
+// and pairs): 384 tokens, 2048 -> 5120: 65 and 104, 38 and 31; 256, 2048 -> 12352: 75 and 105, 41 and 33;
+// three rounds, 384, 2048 -> 12352: 107 and 166, 57 and 41, 777 float32 tokens in runs of 50, 2048 -> 5120:
+// 75 and 54.  (Up to 2048 tokens: the low side's windows are made for few.)
+constexpr int kOneTile = 64, kMostTokens = 2048, kRounds = 2;
 
 template <typename TO>
 cudaError_t launch_t(const AdaptArgs &g, cudaStream_t s) {
-  return g.tokens <= 16 ? launch_bt<16, TO>(g, s) : launch_bt<64, TO>(g, s);
+  if (g.tokens <= 16) return launch_bt<16, TO>(g, s);
+  return wide_tiles(g) ? launch_bt<96, TO>(g, s) : launch_bt<64, TO>(g, s);
 }
 
 }  // namespace
@@ -500,7 +521,9 @@ size_t adapt_workspace_bytes(const AdaptArgs &g) {
 }
 
 int adapt_tile(const AdaptArgs &g) {
-  return g.tokens <= kFewTokens ? 0 : g.y_dtype == GDN_F32 ? 128 : 256;
+  const bool few = g.tokens <= kOneTile ||
+                   (g.tokens <= kMostTokens && rounds_of(g, wide_tiles(g) ? 96 : 64) <= kRounds);
+  return few ? 0 : g.y_dtype == GDN_F32 ? 128 : 256;
 }
 
 cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s) {

@@ -677,8 +677,8 @@ typedef struct gdn_adapters gdn_adapters;
 
 /* The handle owns a memory pool with a workspace for each of the first 16 streams that
  * it is used on, as the KV cache does: 4 bytes (bf16 y) or 6 per token and rank, the rank
- * rounded up to a power of two (16 at least); in calls of more than 256 tokens eight times
- * that. */
+ * rounded up to a power of two (16 at least); in calls of more than 64 tokens up to eight
+ * times that. */
 gdn_status gdn_adapters_create(const gdn_adapters_desc *desc, const void *a, int64_t ld_a,
                                const void *b, int64_t ld_b, const float *scale,
                                gdn_adapters **out);

@@ -99,6 +99,29 @@ def test_whole_numbers(pool, hidden, n_out, rank, tokens):
     assert abi.gdn_pool_get_error(pool) == 0
 
 
+@pytest.mark.parametrize("hidden,n_out,rank", [
+    (2048, 12352, 16), (512, 10000, 64), (512, 10000, 128), (192, 24576, 32), (256, 130, 48)])
+@pytest.mark.parametrize("tokens", [65, 96, 97, 192, 260, 2048, 2049])
+def test_tiles_that_fill_the_device_more_than_once(pool, tokens, hidden, n_out, rank):
+    """Where wider tiles of tokens, and then pairs of blocks, take over."""
+    rng = np.random.default_rng(tokens + n_out)
+    n = 70
+    w, a, b, scale = make(rng, hidden, n_out, rank, n)
+    x = whole(rng, 2, tokens, hidden)
+    ad = abi.Adapters(bf(a), bf(b), torch.tensor(scale, dtype=torch.float32, device="cuda"))
+    gx, gw = bf(x), bf(w)
+    for name, ids in patterns(tokens, n).items():
+        if tokens * n_out > 4e6 and name not in ("some", "runs"):
+            continue
+        want, _, _ = adapted(x, w, a, b, scale, ids)
+        for dtype in (torch.float32, torch.bfloat16):
+            y = torch.full((tokens + 1, -(-n_out // 8) * 8), 77.0, dtype=dtype, device="cuda")
+            abi.gdn_in_proj_adapted(pool, ad, gx, gw, i32(ids), y[:tokens, :n_out])
+            same(y[:tokens, :n_out], want)
+            assert (y[tokens] == 77).all(), name
+    assert abi.gdn_pool_get_error(pool) == 0
+
+
 @pytest.mark.parametrize("tokens,hidden,n_out,rank,n", [
     (1500, 512, 1040, 64, 200), (4097, 256, 640, 16, 9), (777, 2048, 5120, 32, 24),
     (2500, 192, 12352, 128, 3), (16384, 128, 2560, 24, 40)])
