@@ -41,7 +41,7 @@ __device__ __forceinline__ uint4 load8(const bf16 *row, int k, int hidden) {
 // AHEAD: steps of 64 k whose loads a warp has in flight.  (With the ends of odd rows looked at in
 // every load the code was so long that fetching it took longer than the work.)
 template <int MT, int NT, int AHEAD, bool WHOLE, bool PLANES>
-__global__ void __launch_bounds__(32 * kWarps) low_kernel(AdaptArgs g) {
+__global__ void __launch_bounds__(32 * kWarps, MT * NT == 8 ? 2 : 1) low_kernel(AdaptArgs g) {
   constexpr int kTok = 16 * MT, kRanks = 8 * NT;
   extern __shared__ float s_part[];  // [kWarps][kTok][kRanks]
   __shared__ int s_id[kTok], s_lead[kTok], s_n;
@@ -224,15 +224,16 @@ cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
 
 }  // namespace
 
-// Few tokens: small windows, for parallel loads of A; many: large ones, that read A less often (512 with
-// 64 adapters of rank 64: 112 and 123 us with the projection, 1024 in prompts 63 and 61).
+// Few tokens: windows of 16, for parallel loads of A; many: windows of 32, that read A less often, two
+// CTAs an SM, so that one's loads cover the other's sums (with the projection, 1024 in prompts, 2048 ->
+// 12352: windows of 16 59.0 us, of 32 56.2, of 64 and one CTA 61.8; 16384: 625, 563, 572).
 constexpr int kFewWindows = 512;
 
 cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s) {
   if (g.tile > 0)
     return g.hidden % 8 != 0     ? launch<1, 2, 1, false, true>(g, s)
            : g.tokens <= kFewWindows ? launch<1, 2, 4, true, true>(g, s)
-                                 : launch<4, 4, 1, true, true>(g, s);
+                                 : launch<2, 4, 1, true, true>(g, s);
   return g.hidden % 8 == 0 ? launch<1, 2, 4, true, false>(g, s)
                            : launch<1, 2, 1, false, false>(g, s);
 }
