@@ -6,7 +6,7 @@
 // loaded straight from global memory, 16 bytes a lane.  The order of k within a product does not
 // matter, so a lane's 16 bytes -- 8 neighbours in k -- are fed to two products as they come.
 // (These products are 3 % of a prompt's; the tensor cores that read shared memory are for the
-// projection itself.)
+// projection itself.)  16384 tokens, rank 64, take 54 us, for 268 MB through L2.
 //
 // A CTA takes a window of 16 * MT tokens, the adapters of which it finds by comparing the ids, and
 // 8 * NT ranks; its 8 warps split the sum over k, joined in shared memory in a fixed order.  Where
