@@ -166,6 +166,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+def _released(owner):
+    """The owner's handle, which it no longer has: a destroy call frees it even where it reports
+    an error, so that it must not be made again."""
+    handle, owner.handle = owner.handle, None
+    return handle
+
+
 def _check(status: int):
     if status != 0:
         msg = load_library().gdn_last_error_message().decode()
@@ -275,7 +282,6 @@ class Pool:
     def close(self):
         if getattr(self, "handle", None):
             gdn_pool_destroy(self)
-            self.handle = None
 
     def __del__(self):
         try:
@@ -304,7 +310,7 @@ def gdn_pool_create(desc: gdn_pool_desc, state: torch.Tensor, conv: torch.Tensor
 
 
 def gdn_pool_destroy(pool: Pool):
-    _check(load_library().gdn_pool_destroy(pool.handle))
+    _check(load_library().gdn_pool_destroy(_released(pool)))
 
 
 def gdn_pool_reset(pool: Pool, slot_ids: torch.Tensor, stream=None):
@@ -582,7 +588,6 @@ class KVCache:
     def close(self):
         if getattr(self, "handle", None):
             gdn_kv_destroy(self)
-            self.handle = None
 
     def __del__(self):
         try:
@@ -608,7 +613,7 @@ def gdn_kv_create(desc: gdn_kv_desc, k, v, k_scale, v_scale, page_table):
 
 
 def gdn_kv_destroy(kv: KVCache):
-    _check(load_library().gdn_kv_destroy(kv.handle))
+    _check(load_library().gdn_kv_destroy(_released(kv)))
 
 
 def gdn_kv_get_error(kv: KVCache) -> int:
@@ -873,7 +878,6 @@ class Rope:
     def close(self):
         if getattr(self, "handle", None):
             gdn_rope_destroy(self)
-            self.handle = None
 
     def __del__(self):
         try:
@@ -889,7 +893,7 @@ def gdn_rope_create(desc: gdn_rope_desc):
 
 
 def gdn_rope_destroy(rope: Rope):
-    _check(load_library().gdn_rope_destroy(rope.handle))
+    _check(load_library().gdn_rope_destroy(_released(rope)))
 
 
 def _rope_rows(x, out, d, tokens, dtype, device, name):
@@ -990,7 +994,6 @@ class Adapters:
     def close(self):
         if getattr(self, "handle", None):
             gdn_adapters_destroy(self)
-            self.handle = None
 
     def __del__(self):
         try:
@@ -1007,7 +1010,7 @@ def gdn_adapters_create(desc: gdn_adapters_desc, a, ld_a, b, ld_b, scale):
 
 
 def gdn_adapters_destroy(adapters: Adapters):
-    _check(load_library().gdn_adapters_destroy(adapters.handle))
+    _check(load_library().gdn_adapters_destroy(_released(adapters)))
 
 
 def _proj_rows(t, rows, width, device, name):

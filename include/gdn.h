@@ -554,7 +554,7 @@ gdn_status gdn_kv_attend(gdn_kv *kv, int32_t layer, const int32_t *slot_ids,
  * All four are plain caller memory, to be set before the first call: held 0, every
  * page id once in free_pages, *n_free = n_pages (or fewer, with pages that
  * the caller gave to slots itself counted in held).  The two calls below change
- * them in the order of their stream; calls on different streams on one set must be
+ * them in the order of their stream; calls on different streams on one cache must be
  * ordered by the caller (events).  Pages that several slots share (a common
  * prefix) are the caller's: trim those slots to no less than the shared pages, and
  * take these out of table and held by itself. */
@@ -582,10 +582,10 @@ typedef struct {
  * each of them NULL if not wanted.  Tokens before cu_seqlens[0], after the last
  * sequence or of a malformed range are not written (where cu_seqlens decreases, it
  * is not specified which of the tokens that two sequences claim are).  Skipped as
- * never asked for, with granted 0, positions and rows -1: entries with a slot out of range or named twice in the call
- * (GDN_DEVERR_SLOT), with a malformed token range or one that does not fit
- * [0, max_pages * page_tokens) (GDN_DEVERR_SEQ), or whose held is outside
- * [0, max_pages] (GDN_DEVERR_PAGE).  An impossible *n_free counts as 0
+ * never asked for, with granted 0, positions and rows -1: entries with a slot out of
+ * range or named twice in the call (GDN_DEVERR_SLOT), with a malformed token range or
+ * one that does not fit [0, max_pages * page_tokens) (GDN_DEVERR_SEQ), or whose held is
+ * outside [0, max_pages] (GDN_DEVERR_PAGE).  An impossible *n_free counts as 0
  * (GDN_DEVERR_PAGE).  Needs no workspace; one launch. */
 gdn_status gdn_kv_pages_grow(gdn_kv *kv, const gdn_kv_pages *pages, const int32_t *slot_ids,
                              const int32_t *pos, const int32_t *cu_seqlens, int32_t n_seqs,

@@ -109,3 +109,30 @@ def test_calls_the_binding_refuses(made, monkeypatch):
     refused("GDN_ERR_ARG", x, w, ids, y[:1].expand(5, 32))
     refused("GDN_ERR_ARG", x, z(64, 32).T, ids, y)
     refused("GDN_ERR_ARG", torch.zeros(5, 64, dtype=torch.bfloat16, device="meta"), w, ids, y)
+
+
+@pytest.mark.parametrize("cls,call", [
+    (abi.Adapters, "gdn_adapters_destroy"), (abi.Rope, "gdn_rope_destroy"),
+    (abi.Pool, "gdn_pool_destroy"), (abi.KVCache, "gdn_kv_destroy")])
+def test_a_destroy_call_that_reports_an_error_is_not_made_again(monkeypatch, cls, call):
+    """The library frees a handle even where the device has failed."""
+    freed = []
+
+    def destroy(handle):
+        freed.append(handle)
+        return 7 if handle else 0
+
+    fake = types.SimpleNamespace(**{call: destroy, "gdn_last_error_message": lambda: b"no device"})
+    monkeypatch.setattr(abi, "load_library", lambda: fake)
+    owner = cls.__new__(cls)
+    owner.handle = 1234
+    with pytest.raises(abi.GDNError):
+        owner.close()
+    owner.close()
+    owner.__del__()
+    assert freed == [1234]
+    owner.handle = 5678  # by the function itself
+    with pytest.raises(abi.GDNError):
+        getattr(abi, call)(owner)
+    owner.__del__()
+    assert freed == [1234, 5678]
