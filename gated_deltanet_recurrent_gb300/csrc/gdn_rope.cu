@@ -304,6 +304,10 @@ gdn_status gdn_rope_create(const gdn_rope_desc *desc, gdn_rope_plan **out) {
     } else {
       theta /= desc->factor;
     }
+    if (!std::isfinite(theta)) {
+      delete p;
+      return fail(GDN_ERR_ARG, "the frequency of pair %d is not finite", j);
+    }
     p->turns.f[j] = fraction(theta / (2 * kPi));
   }
   *out = p;

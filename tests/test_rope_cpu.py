@@ -33,6 +33,15 @@ def test_plans_that_cannot_be(kw, name):
     assert e.value.name == name
 
 
+@pytest.mark.parametrize("kw", [
+    dict(base=1e-320), dict(factor=1e-320), dict(base=1e-300, factor=1e-300),
+    dict(base=1e-300, factor=1e-300, original_len=8, low_turns=0.5, high_turns=1e308)])
+def test_frequencies_that_are_not_finite(kw):
+    with pytest.raises(abi.GDNError) as e:
+        abi.Rope(**{"d": 64, "rot": 64, **kw})
+    assert e.value.name == "GDN_ERR_ARG"
+
+
 def test_a_plan_needs_no_device():
     rope = abi.Rope(256, 64)
     rope.close()
