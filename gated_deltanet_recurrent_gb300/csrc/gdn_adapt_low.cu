@@ -215,8 +215,9 @@ cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int windows = (g.tokens + 16 * MT - 1) / (16 * MT);
   const int parts = (g.rank_pad() + 8 * NT - 1) / (8 * NT);
-  // CTAs that share a window: as many as it may have adapters, but no more than four waves in all
-  const int64_t room = (int64_t)4 * g.sm_count / ((int64_t)windows * parts);
+  // CTAs that share a window: as many as it may have adapters, but no more than two an SM in all (with
+  // four, of which most find nothing to do, 1024 tokens in prompts took 56.6 us instead of 51.3)
+  const int64_t room = (int64_t)2 * g.sm_count / ((int64_t)windows * parts);
   const int share = (int)(room < 1 ? 1 : room > 16 * MT ? 16 * MT : room);
   return kv::launch(low_kernel<MT, NT, AHEAD, WHOLE, PLANES>, dim3((unsigned)windows, (unsigned)share, (unsigned)parts),
                     32 * kWarps, smem, s, 1, g);
@@ -225,8 +226,8 @@ cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
 }  // namespace
 
 // Few tokens: windows of 16, for parallel loads of A; many: windows of 32, that read A less often, two
-// CTAs an SM, so that one's loads cover the other's sums (with the projection, 1024 in prompts, 2048 ->
-// 12352: windows of 16 59.0 us, of 32 56.2, of 64 and one CTA 61.8; 16384: 625, 563, 572).
+// CTAs an SM, so that one's loads cover the other's sums (with the projection and four CTAs an SM in
+// all, 1024 in prompts, 2048 -> 12352: windows of 16 59.0 us, of 32 56.2, of 64 61.8; 16384: 625, 563, 572).
 constexpr int kFewWindows = 512;
 
 cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s) {

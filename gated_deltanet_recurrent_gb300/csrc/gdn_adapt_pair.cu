@@ -26,7 +26,7 @@
 //
 // Bound by the tensor pipe, 78 % active: 16384 tokens, 2048 -> 12352, in 487 us without adapters (1.70
 // PFLOP/s), 558 in prompts of 1100 with adapters of rank 64 (of which the low side some 50), 708 in runs of
-// 50.  777 float32 tokens in runs of 50, 2048 -> 5120: 47.8 us, a tile and its epilogue one after the other.
+// 50.  777 float32 tokens in runs of 50, 2048 -> 5120: 46.0 us, a tile and its epilogue one after the other.
 #include "gdn_adapt.cuh"
 
 namespace gdn {
