@@ -30,8 +30,8 @@
 // bounded (GDN_DEVERR_TIMEOUT).
 //
 // Measured with the low side: one token, 2048 -> 5120, rank 16, 10.7 us (latency; its bytes take 3.1);
-// 64 tokens with an adapter each, 2048 -> 12352, rank 16, 20.5 us on warm and 24.4 on cold weights (82 MB:
-// 12.1), rank 64 40.6 (25.1), without adapters 18.1 (7.7).  Narrower tiles, one for each SM, take as long.
+// 64 tokens with an adapter each, 2048 -> 12352, rank 16, 19.5 us on warm and 21.7 on cold weights (82 MB:
+// 12.1), rank 64 39.5 (25.1), without adapters 17.5 (7.7).  Narrower tiles, one for each SM, take as long.
 #include "gdn_adapt.cuh"
 
 namespace gdn {
@@ -478,22 +478,30 @@ int64_t rounds_of(const AdaptArgs &g, int bt) {
 }
 
 // Tiles of 96 tokens where they take fewer rounds than tiles of 64: 256 tokens with 64 adapters of rank
-// 16, 2048 -> 5120: 26.6 and 41.3 us, 96 tokens, 2048 -> 12352: 25.9 and 36.5; 192 tokens, 2048 -> 5120, in
+// 16, 2048 -> 5120: 25.6 and 41.3 us, 96 tokens, 2048 -> 12352: 23.4 and 36.5; 192 tokens, 2048 -> 5120, in
 // one round either way: 64 is faster.
 bool wide_tiles(const AdaptArgs &g) {
   return rounds_of(g, 96) < rounds_of(g, 64);
 }
 
+// CTAs that share a tile: as many as fit on the device at once, with four k-blocks each at least, and
+// four at most (one token, 2048 -> 5120: one CTA a tile 16.6 us, two 13.0, three 11.6; 64 tokens with an
+// adapter each, 2048 -> 2048: two 17.1 us, four 13.8, eight 21.6)
+int splits_of(const AdaptArgs &g, int bt) {
+  const int64_t fit = g.sm_count / tiles_of(g, bt), blocks = (g.hidden + kBK - 1) / kBK;
+  const int64_t most = fit < blocks / 4 ? fit : blocks / 4;
+  return most < 1 ? 1 : most > 4 ? 4 : (int)most;
+}
+
+// The tile's tokens.
+int tokens_of_tile(const AdaptArgs &g) {
+  return g.tokens <= 16 ? 16 : wide_tiles(g) ? 96 : 64;
+}
+
 template <int BT, int PITCH, typename TO>
 cudaError_t launch_split(const AdaptArgs &g, cudaStream_t s) {
-  const int64_t tiles = tiles_of(g, BT);
   if constexpr (BT == 96) return launch<BT, PITCH, TO, false>(g, 1, s);  // (too many tiles to share any)
-  const int blocks = (g.hidden + kBK - 1) / kBK;
-  // CTAs that share a tile: as many as fit on the device at once, with four k-blocks each at least, and
-  // four at most (one token, 2048 -> 5120: one CTA a tile 16.6 us, two 13.0, three 11.6; 64 tokens with an
-  // adapter each, 2048 -> 2048: two 17.1 us, four 13.8, eight 21.6)
-  const int64_t most = g.sm_count / tiles < blocks / 4 ? g.sm_count / tiles : blocks / 4;
-  const int splits = most > 4 ? 4 : (int)most;
+  const int splits = splits_of(g, BT);
   return splits > 1 ? launch<BT, PITCH, TO, true>(g, splits, s)
                     : launch<BT, PITCH, TO, false>(g, 1, s);
 }
@@ -507,15 +515,15 @@ cudaError_t launch_bt(const AdaptArgs &g, cudaStream_t s) {
 
 // These kernels take calls of one tile's tokens, and others that fill the device at most twice;
 // pairs of CTAs take what is longer.  With 64 adapters of rank 64 in any order and with none (us, here
-// and pairs): 384 tokens, 2048 -> 5120: 65 and 104, 38 and 31; 256, 2048 -> 12352: 75 and 105, 41 and 33;
-// three rounds, 384, 2048 -> 12352: 107 and 166, 57 and 41, 777 float32 tokens in runs of 50, 2048 -> 5120:
-// 75 and 54.  (Up to 2048 tokens: the low side's windows are made for few.)
+// and pairs): 384 tokens, 2048 -> 5120: 65 and 104, 34 and 31; 256, 2048 -> 12352: 73 and 105, 38 and 33;
+// three rounds, 384, 2048 -> 12352: 107 and 160, 57 and 37, 777 float32 tokens in runs of 50, 2048 -> 5120:
+// 75 and 46.  (Up to 2048 tokens: the low side's windows are made for few.)
 constexpr int kOneTile = 64, kMostTokens = 2048, kRounds = 2;
 
 template <typename TO>
 cudaError_t launch_t(const AdaptArgs &g, cudaStream_t s) {
-  if (g.tokens <= 16) return launch_bt<16, TO>(g, s);
-  return wide_tiles(g) ? launch_bt<96, TO>(g, s) : launch_bt<64, TO>(g, s);
+  const int bt = tokens_of_tile(g);
+  return bt == 16 ? launch_bt<16, TO>(g, s) : bt == 96 ? launch_bt<96, TO>(g, s) : launch_bt<64, TO>(g, s);
 }
 
 }  // namespace
@@ -526,12 +534,16 @@ size_t adapt_workspace_bytes(const AdaptArgs &g) {
 
 int adapt_tile(const AdaptArgs &g) {
   const bool few = g.tokens <= kOneTile ||
-                   (g.tokens <= kMostTokens && rounds_of(g, wide_tiles(g) ? 96 : 64) <= kRounds);
+                   (g.tokens <= kMostTokens && rounds_of(g, tokens_of_tile(g)) <= kRounds);
   return few ? 0 : g.y_dtype == GDN_F32 ? 128 : 256;
 }
 
 cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s) {
-  const cudaError_t e = launch_adapt_low(g, s);
+  // (CTAs that share a tile have so little of W each that h is what they wait for: 64 tokens with an adapter
+  // each, 2048 -> 5120, 19.0 us without regard to them and 20.8 with)
+  const int bt = tokens_of_tile(g);
+  const int64_t tiles = tiles_of(g, bt) < g.sm_count ? tiles_of(g, bt) : g.sm_count;
+  const cudaError_t e = launch_adapt_low(g, splits_of(g, bt) > 1 ? 0 : (int)tiles, s);
   if (e != cudaSuccess) return e;
   if (g.tile > 0) return launch_adapt_pair(g, s);
   return g.y_dtype == GDN_F32 ? launch_t<float>(g, s) : launch_t<bf16>(g, s);

@@ -41,6 +41,7 @@ cudaError_t launch_adapt(const AdaptArgs &g, cudaStream_t s);
 // The projection of many tokens, on pairs of CTAs.
 cudaError_t launch_adapt_pair(const AdaptArgs &g, cudaStream_t s);
 
-cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s);
+// others: CTAs of the projection that want an SM while the low side has its own.
+cudaError_t launch_adapt_low(const AdaptArgs &g, int others, cudaStream_t s);
 
 }  // namespace gdn

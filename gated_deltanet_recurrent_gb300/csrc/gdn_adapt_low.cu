@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(32 * kWarps, MT * NT == 8 ? 2 : 1) low_kernel(
 }
 
 template <int MT, int NT, int AHEAD, bool WHOLE, bool PLANES>
-cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
+cudaError_t launch(const AdaptArgs &g, int others, cudaStream_t s) {
   constexpr int smem = kWarps * 16 * MT * 8 * NT * 4;
   static std::atomic<uint64_t> seen{0};
   const cudaError_t e = kv::allow_smem(low_kernel<MT, NT, AHEAD, WHOLE, PLANES>, smem, g.device, seen);
@@ -218,7 +218,18 @@ cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
   // CTAs that share a window: as many as it may have adapters, but no more than two an SM in all (with
   // four, of which most find nothing to do, 1024 tokens in prompts took 56.6 us instead of 51.3)
   const int64_t room = (int64_t)2 * g.sm_count / ((int64_t)windows * parts);
-  const int share = (int)(room < 1 ? 1 : room > 16 * MT ? 16 * MT : room);
+  int share = (int)(room < 1 ? 1 : room > 16 * MT ? 16 * MT : room);
+  // A CTA of the projection finds no room beside one of these.  So these take the SMs that it leaves, if
+  // that is kLeast for a window at least (fewer, and a window's adapters take too long one after the
+  // other), else one an SM: 64 tokens with an adapter each, 2048 -> 12352, 16 for a window 24.5 us, 13
+  // 21.7; 128 with 64 adapters, 2048 -> 5120, 16 22.7, 8 19.7; 64 of rank 64, 16 40.8, 8 39.5, 4 42.0.
+  constexpr int kLeast = 8;
+  if (!PLANES && share > kLeast) {
+    const int64_t spare = (g.sm_count - others) / ((int64_t)windows * parts);
+    const int64_t all = g.sm_count / ((int64_t)windows * parts);
+    const int64_t fit = spare >= kLeast ? spare : all >= kLeast ? all : kLeast;
+    if (fit < share) share = (int)fit;
+  }
   return kv::launch(low_kernel<MT, NT, AHEAD, WHOLE, PLANES>, dim3((unsigned)windows, (unsigned)share, (unsigned)parts),
                     32 * kWarps, smem, s, 1, g);
 }
@@ -230,13 +241,13 @@ cudaError_t launch(const AdaptArgs &g, cudaStream_t s) {
 // all, 1024 in prompts, 2048 -> 12352: windows of 16 59.0 us, of 32 56.2, of 64 61.8; 16384: 625, 563, 572).
 constexpr int kFewWindows = 512;
 
-cudaError_t launch_adapt_low(const AdaptArgs &g, cudaStream_t s) {
+cudaError_t launch_adapt_low(const AdaptArgs &g, int others, cudaStream_t s) {
   if (g.tile > 0)
-    return g.hidden % 8 != 0     ? launch<1, 2, 1, false, true>(g, s)
-           : g.tokens <= kFewWindows ? launch<1, 2, 4, true, true>(g, s)
-                                 : launch<2, 4, 1, true, true>(g, s);
-  return g.hidden % 8 == 0 ? launch<1, 2, 4, true, false>(g, s)
-                           : launch<1, 2, 1, false, false>(g, s);
+    return g.hidden % 8 != 0         ? launch<1, 2, 1, false, true>(g, others, s)
+           : g.tokens <= kFewWindows ? launch<1, 2, 4, true, true>(g, others, s)
+                                     : launch<2, 4, 1, true, true>(g, others, s);
+  return g.hidden % 8 == 0 ? launch<1, 2, 4, true, false>(g, others, s)
+                           : launch<1, 2, 1, false, false>(g, others, s);
 }
 
 }  // namespace gdn
