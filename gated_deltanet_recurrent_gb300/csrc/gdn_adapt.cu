@@ -45,6 +45,25 @@ constexpr int kTeams = 4;                // of four warps
 constexpr int kPitch = kBM + 4;      // floats of a token's row of the adapters' part
 constexpr int kRingB = 64 * 1024;    // bytes of the ring of B tiles
 
+// The sums of one output: column at (+ BT, + 2 BT ...) of the first `used` of ACC accumulators.
+template <int BT, int ACC>
+__device__ __forceinline__ void add_accumulators(uint32_t at, int used, float *v) {
+  tc::tmem_ld16(at, v);
+#pragma unroll
+  for (int a = 1; a < ACC; a += 2) {
+    float u[32];
+    if (a + 1 < ACC && a + 1 < used) {
+      tc::tmem_ld32(at + a * BT, at + (a + 1) * BT, u);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] += u[j] + u[16 + j];
+    } else if (a < used) {
+      tc::tmem_ld16(at + a * BT, u);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] += u[j];
+    }
+  }
+}
+
 constexpr uint32_t pow2_at_least(uint32_t n) {
   uint32_t p = 32;
   while (p < n) p *= 2;
@@ -54,9 +73,13 @@ constexpr uint32_t pow2_at_least(uint32_t n) {
 template <int BT, int PITCH, typename TO>
 struct Cfg {
   static constexpr int kParts = sizeof(TO) == 4 ? 3 : 2;
-  // The tensor core cuts its sums off: one accumulator over K = 2048 is 2e-6 off, three that take
-  // the k-blocks in turn a third of that, which a bf16 y would not show.
-  static constexpr int kAcc = sizeof(TO) == 4 ? 3 : 1;
+  // The tensor core cuts its sums off: one accumulator over K = 2048 is 2e-6 off, and several that
+  // take the k-blocks in turn that much less each.  A bf16 y has four, so that its roundings are nearly
+  // always those of the exact sum; a float32 y has as many as there is room for, and where one would get
+  // more than kChain k-blocks they are taken out before (`delta`) and start anew.
+  static constexpr bool kLong = sizeof(TO) == 4;
+  static constexpr int kAcc = !kLong ? 4 : BT == 96 ? 5 : 8;
+  static constexpr int kRound = kAcc * kChain;
   static constexpr uint32_t kTmem = pow2_at_least(kAcc * BT);
   static constexpr int kStage = kTileW + BT * kBK * 2;
   static constexpr int kDelta = BT * kPitch * 4;
@@ -193,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<BT, PITCH, TO>;
   constexpr int S = C::kStages, E = kSlots<PITCH>;
   extern __shared__ unsigned char dsm_raw[];
-  __shared__ __align__(8) uint64_t full[S], empty[S], b_full[E], b_empty[E], list, done, drain;
+  __shared__ __align__(8) uint64_t full[S], empty[S], b_full[E], b_empty[E], list, done, taken,
+      drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
   __shared__ float s_gone;  // SPLIT: another CTA of the cluster gave up
@@ -231,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&list, 1);
     mbar_init(&done, 1);
+    mbar_init(&taken, kHelpers / 32);
     mbar_init(&drain, 1);
     s_abort = 0;
     s_gone = 0.f;
@@ -258,6 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int extra = one >= 0 ? (g.rank + kBK - 1) / kBK * C::kParts : 0;
   const int eb0 = extra * part / splits;
   const int kbs = plain + extra * (part + 1) / splits - eb0;
+  // k-blocks before the last round of the accumulators, and in it
+  const int rounds_before = C::kLong ? (kbs - 1) / C::kRound : 0, last = kbs - rounds_before * C::kRound;
   const int halves = g.rank_pad() * 2 / PITCH;
   volatile int *abort_flag = &s_abort;
   const RingB ring{ring_b, b_full, b_empty};
@@ -323,22 +350,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     // MMA issuer
     constexpr uint32_t idesc = tc::idesc_bf16(kBM, BT);
     bool good = true;
-    for (int kb = 0; kb < kbs; ++kb) {
+    int in = 0, round = 0;  // k-blocks of the round
+    for (int kb = 0; kb < kbs; ++kb, ++in) {
+      if (C::kLong && in == C::kRound) {
+        tc::mma_commit(&done);
+        good = wait(&taken, round & 1, abort_flag);
+        tc::fence_after_sync();
+        in = 0, ++round;
+      }
       const int s = kb % S;
-      if (!wait(&full[s], (kb / S) & 1, abort_flag)) {
+      if (!good || !wait(&full[s], (kb / S) & 1, abort_flag)) {
         good = false;
         break;
       }
       tc::fence_after_sync();
       const uint32_t a = smem_addr(tile_w(s)), b = smem_addr(tile_x(s));
-      const uint32_t acc = tmem + (uint32_t)(kb % C::kAcc) * BT;
+      const uint32_t acc = tmem + (uint32_t)(in % C::kAcc) * BT;
       const int c = (eb0 + kb - plain) / C::kParts;
       const int steps = kb < plain ? kBK / 16 : min(kBK, g.rank16() - c * kBK) / 16;
 #pragma unroll
       for (int kk = 0; kk < kBK / 16; ++kk)
         if (kk < steps)
           tc::mma_ss_f16(acc, tc::smem_desc_sw128(a + 32 * kk), tc::smem_desc_sw128(b + 32 * kk),
-                         idesc, kb >= C::kAcc || kk > 0 ? 1u : 0u);
+                         idesc, in >= C::kAcc || kk > 0 ? 1u : 0u);
       tc::mma_commit(&empty[s]);
     }
     if (!good) fail();
@@ -362,15 +396,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         fail();
       helpers_sync<kHelpers>();
     }
+    // a lane per output row, the four warps of TMEM lanes 32 quad .. take turns in the columns
+    const int quad = warp & 3, side = (warp - 2) >> 2, row = 32 * quad + lane, n = n0 + row;
+    const uint32_t mine = tmem + ((uint32_t)(32 * quad) << 16);
+    // the accumulators of a long sum, taken out
+    for (int r = 0; C::kLong && r < rounds_before; ++r) {
+      if (!__all_sync(0xffffffffu, wait(&done, r & 1, abort_flag))) {
+        fail();
+        break;
+      }
+      tc::fence_after_sync();
+#pragma unroll 1
+      for (int c = 16 * side; c < live; c += 64) {
+        float v[16];
+        add_accumulators<BT, C::kAcc>(mine + c, C::kAcc, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (c + j < live) {
+            float *at = &delta[(c + j) * kPitch + row];
+            *at = one == -2 || r > 0 ? *at + v[j] : v[j];
+          }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&taken);
+    }
     if constexpr (SPLIT) {
       __syncwarp();
       cluster_arrive();  // the B tiles' place may be written by the others
       cluster_wait();
     }
-    // epilogue: a lane per output row, the four warps of TMEM lanes 32 quad .. take turns in the columns
-    const int quad = warp & 3, side = (warp - 2) >> 2, row = 32 * quad + lane, n = n0 + row;
     // warp-uniform decision: tcgen05.ld is a whole-warp instruction
-    const bool got = __all_sync(0xffffffffu, wait(&done, 0, abort_flag));
+    const bool got = __all_sync(0xffffffffu, wait(&done, rounds_before & 1, abort_flag));
     if (!got) {
       fail();
     } else {
@@ -379,24 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float *recv = reinterpret_cast<float *>(ring_b);
       const int share = (BT + splits - 1) / splits;
       TO *y = static_cast<TO *>(g.y);
-      const uint32_t mine = tmem + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
       for (int c = 16 * side; c < live; c += 64) {
         float v[16];
-        tc::tmem_ld16(mine + c, v);
-        if constexpr (C::kAcc == 3) {
-          float u[32];
-          if (kbs > 2) {
-            tc::tmem_ld32(mine + BT + c, mine + 2 * BT + c, u);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] += u[j] + u[16 + j];
-          } else if (kbs > 1) {
-            tc::tmem_ld16(mine + BT + c, u);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] += u[j];
-          }
-        }
-        if (one == -2) {
+        add_accumulators<BT, C::kAcc>(mine + c, last, v);
+        if (one == -2 || rounds_before > 0) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             if (c + j < live) v[j] += delta[(c + j) * kPitch + row];

@@ -17,6 +17,10 @@ namespace adapt {
 constexpr int kBM = 128, kBK = 64;
 constexpr int kTileW = kBM * kBK * 2;
 
+// k-blocks that one accumulator of a float32 y gets: the tensor core cuts its sums off, and K = 960 so
+// added is 1e-6 off, whatever hidden is.
+constexpr int kChain = 15;
+
 __device__ __forceinline__ void tma_load2(void *dst, const CUtensorMap *m, int x, int y,
                                           uint64_t *bar) {
   asm volatile(

@@ -20,7 +20,8 @@
 // (up to eight tokens of one adapter) in turn, with B and h from global memory, and store them to TMEM
 // columns of their own, [token][row], which the epilogue adds.  For a bf16 y these are the columns of
 // the next tile's accumulator, which then starts after the epilogue; for a float32 y, of 128 tokens,
-// there are columns for the three accumulators (see gdn_adapt.cu) and these.  (That is slow beside the
+// there are columns for the three accumulators (see gdn_adapt.cu) and these, to which the accumulators of
+// long sums are added too.  (That is slow beside the
 // tensor core, whose operands take all of the shared memory's bandwidth: 15 us for a tile of 256 tokens
 // with two adapters, whose k-blocks take 4.)
 //
@@ -46,6 +47,7 @@ struct Cfg {
   static constexpr int kParts = kF32 ? 3 : 2;
   static constexpr int BT = kF32 ? 128 : 256;
   static constexpr int kAcc = kF32 ? 3 : 1;
+  static constexpr int kRound = kAcc * kChain;  // k-blocks after which a float32 y's are taken out
   static constexpr int kStage = kTileW + BT / 2 * kBK * 2;
   static constexpr int kStages = 6;
   static constexpr int kScratch = kWarps * 8 * 33 * 4;
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int S = C::kStages, BT = C::BT;
   extern __shared__ unsigned char dsm_raw[];
   __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], info_full[kInfo],
-      info_empty[kInfo], drain;
+      info_empty[kInfo], round_full, round_taken, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort, s_info[kInfo], s_list[kInfo][kPlanes];
   __shared__ Groups<BT> s_groups;
@@ -306,6 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&info_full[i], 1);
       mbar_init(&info_empty[i], kWarps);
     }
+    mbar_init(&round_full, 1);
+    mbar_init(&round_taken, 2 * kWarps);
     mbar_init(&drain, 1);
     s_abort = 0;
     mbar_fence_init();
@@ -390,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t round = 0;
     bool good = true;
     int i = 0, before = -1;  // the tile before: it has no adapters
+    uint32_t rounds = 0;     // of the accumulators, that were taken out
     for (int64_t t = pair; t < tiles && good; t += pairs, ++i) {
       const int one = tile_info(i);
       // The accumulators' columns are free once the epilogue of tile i - 2 is done, or of tile i - 1
@@ -404,8 +409,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       before = one;
       tc::fence_after_sync();
       const uint32_t base = C::kF32 ? tmem : tmem + (uint32_t)(i & 1) * BT;
+      int turn = 0, in = 0;  // of the accumulators; k-blocks of the round
       // the next k-block's products; a loop round it has 256 cycles
-      auto block = [&](uint32_t acc, int steps, bool fresh) {
+      auto block = [&](int steps) {
+        if (C::kF32 && in == C::kRound) {
+          commit_pair(&round_full);
+          if (!wait(&round_taken, rounds++ & 1, abort_flag)) return false;
+          tc::fence_after_sync();
+          turn = in = 0;
+        }
+        const uint32_t acc = base + (uint32_t)turn * BT;
+        const bool fresh = in++ < C::kAcc;
+        turn = turn + 1 == C::kAcc ? 0 : turn + 1;
         if (!wait(&full[s], round, abort_flag)) return false;
         tc::fence_after_sync();
         const uint32_t a = smem_addr(tile_w(s)), b = smem_addr(tile_x(s));
@@ -418,18 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++s == S) s = 0, round ^= 1;
         return true;
       };
-      int turn = 0;  // of the accumulators
-      for (int kb = 0; kb < plain && good; ++kb) {
-        good = block(base + (uint32_t)turn * BT, kBK / 16, kb < C::kAcc);
-        turn = turn + 1 == C::kAcc ? 0 : turn + 1;
-      }
-      for (int j = adapters_of(one), kb = plain; j > 0; --j)
+      for (int kb = 0; kb < plain && good; ++kb) good = block(kBK / 16);
+      for (int j = adapters_of(one); j > 0; --j)
         for (int c = 0; c < chunks; ++c)
-          for (int p = 0; p < C::kParts && good; ++p, ++kb) {
-            good = block(base + (uint32_t)turn * BT, min(kBK, g.rank16() - c * kBK) / 16,
-                         kb < C::kAcc);
-            turn = turn + 1 == C::kAcc ? 0 : turn + 1;
-          }
+          for (int p = 0; p < C::kParts && good; ++p)
+            good = block(min(kBK, g.rank16() - c * kBK) / 16);
       if (good) commit_pair(&acc_full[i & 1]);
     }
     if (!good) {
@@ -465,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t mine = tmem + ((uint32_t)(32 * quad) << 16);
     TO *y = static_cast<TO *>(g.y);
     int i = 0;
+    uint32_t rounds = 0;
     bool good = true;
     for (int64_t t = pair; t < tiles; t += pairs, ++i) {
       const int tok0 = (int)(t / n_tiles) * BT, live = min(BT, g.tokens - tok0);
@@ -500,7 +509,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before_sync();
         helpers_sync<kHelpers>();
       }
-      good = __all_sync(0xffffffffu, wait(&acc_full[i & 1], (i >> 1) & 1, abort_flag));
+      // the accumulators of a long sum, taken out into the columns of `delta`
+      const int kbs = plain + adapters_of(one) * chunks * C::kParts;
+      if constexpr (C::kF32)
+        for (int k = C::kRound; k < kbs && good; k += C::kRound, ++rounds) {
+          good = __all_sync(0xffffffffu, wait(&round_full, rounds & 1, abort_flag));
+          if (!good) break;
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int c = 16 * side; c < live; c += 16 * kTeams) {
+            float v[32], u[32];
+            tc::tmem_ld32(acc + c, acc + BT + c, v);
+            if (one == kMany || k > C::kRound) {
+              tc::tmem_ld32(acc + 2 * BT + c, delta + c, u);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) u[j] += u[16 + j];
+            } else {
+              tc::tmem_ld16(acc + 2 * BT + c, u);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += v[16 + j] + u[j];
+            tc::tmem_st16(delta + c, v);
+          }
+          tc::tmem_st_wait();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) arrive_leader(&round_taken);
+        }
+      good = good &&
+             __all_sync(0xffffffffu, wait(&acc_full[i & 1], (i >> 1) & 1, abort_flag));
       if (!good) {
         fail();
         continue;
@@ -512,18 +549,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (C::kF32) {
           float u[32];
           tc::tmem_ld32(acc + c, acc + BT + c, v);
-          const int kbs = plain + adapters_of(one) * chunks * C::kParts;
-          if (kbs > 1)  // (an accumulator that no k-block has come to holds anything)
+          const bool summed = one == kMany || kbs > C::kRound;
+          const int last = (kbs - 1) % C::kRound + 1;
+          if (last > 1)  // (an accumulator that no k-block of the round has come to holds anything)
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
-          if (one == kMany)
+          if (summed)
             tc::tmem_ld32(acc + 2 * BT + c, delta + c, u);
           else
             tc::tmem_ld16(acc + 2 * BT + c, u);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            if (kbs > 2) v[j] += u[j];
-            if (one == kMany) v[j] += u[16 + j];
+            if (last > 2) v[j] += u[j];
+            if (summed) v[j] += u[16 + j];
           }
         } else if (one == kMany) {
           tc::tmem_ld32(acc + c, delta + c, v);
