@@ -118,7 +118,7 @@ __device__ __forceinline__ int h_offset(int token, int byte) {
 template <int BT, int PITCH, int PARTS>
 __device__ __forceinline__ bool expand(const AdaptArgs &g, const Groups<BT> &s, const RingB &ring,
                                        int warp, int tok0, int live, unsigned char *hs, float *delta,
-                                       volatile int *abort_flag) {
+                                       volatile int *abort_flag, uint32_t polls) {
   constexpr int W = PITCH == 32 ? 8 : 16, NL = PITCH / (4 * W), kWords = W / 4;
   constexpr int E = kSlots<PITCH>;
   static_assert(E % kTeams == 0, "a slot is always the same team's, which then is never two rounds ahead");
@@ -143,7 +143,7 @@ __device__ __forceinline__ bool expand(const AdaptArgs &g, const Groups<BT> &s, 
     for (int u = half * s.n + ((team - half * s.n) & (kTeams - 1)); good && u < (half + 1) * s.n;
          u += kTeams) {
       const int group = u - half * s.n, e = u % E;
-      if (!__all_sync(0xffffffffu, wait(&ring.full[e], (u / E) & 1, abort_flag))) {
+      if (!__all_sync(0xffffffffu, wait(&ring.full[e], (u / E) & 1, abort_flag, polls))) {
         good = false;
         break;
       }
@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rounds_before = C::kLong ? (kbs - 1) / C::kRound : 0, last = kbs - rounds_before * C::kRound;
   const int halves = g.rank_pad() * 2 / PITCH;
   volatile int *abort_flag = &s_abort;
+  const uint32_t polls = patience(g);
   const RingB ring{ring_b, b_full, b_empty};
   auto fail = [&]() {
     *abort_flag = 1;
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int issued = min(S, plain);
     for (int kb = issued; kb < kbs; ++kb) {
       const int s = kb % S;
-      if (kb >= S && !wait(&empty[s], ((kb / S) - 1) & 1, abort_flag)) {
+      if (kb >= S && !wait(&empty[s], ((kb / S) - 1) & 1, abort_flag, polls)) {
         fail();
         break;
       }
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2 + kHelpers / 32) {
     // a lane per slot of the ring of B tiles
     if (one == -2) {
-      bool good = __all_sync(0xffffffffu, wait(&list, 0, abort_flag));
+      bool good = __all_sync(0xffffffffu, wait(&list, 0, abort_flag, polls));
       const int units = good ? s_groups.n * halves : 0;
       int u = lane < E ? lane : units, issued = -1;
       uint32_t idle = 0;
@@ -354,12 +355,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int kb = 0; kb < kbs; ++kb, ++in) {
       if (C::kLong && in == C::kRound) {
         tc::mma_commit(&done);
-        good = wait(&taken, round & 1, abort_flag);
+        good = wait(&taken, round & 1, abort_flag, polls);
         tc::fence_after_sync();
         in = 0, ++round;
       }
       const int s = kb % S;
-      if (!good || !wait(&full[s], (kb / S) & 1, abort_flag)) {
+      if (!good || !wait(&full[s], (kb / S) & 1, abort_flag, polls)) {
         good = false;
         break;
       }
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           reinterpret_cast<float4 *>(delta + t * kPitch)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
       kv::dependent_wait();  // h
       if (!expand<BT, PITCH, C::kParts>(g, s_groups, ring, warp - 2, tok0, live, hs, delta,
-                                        abort_flag))
+                                        abort_flag, polls))
         fail();
       helpers_sync<kHelpers>();
     }
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t mine = tmem + ((uint32_t)(32 * quad) << 16);
     // the accumulators of a long sum, taken out
     for (int r = 0; C::kLong && r < rounds_before; ++r) {
-      if (!__all_sync(0xffffffffu, wait(&done, r & 1, abort_flag))) {
+      if (!__all_sync(0xffffffffu, wait(&done, r & 1, abort_flag, polls))) {
         fail();
         break;
       }
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_wait();
     }
     // warp-uniform decision: tcgen05.ld is a whole-warp instruction
-    const bool got = __all_sync(0xffffffffu, wait(&done, rounds_before & 1, abort_flag));
+    const bool got = __all_sync(0xffffffffu, wait(&done, rounds_before & 1, abort_flag, polls));
     if (!got) {
       fail();
     } else {

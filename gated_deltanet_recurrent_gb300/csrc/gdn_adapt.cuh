@@ -66,9 +66,16 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Polls of a bounded wait (of up to a microsecond or two each): what one step of any role may take grows
+// with hidden, and is some 50 ns for each of it where a tile's results are all computed again.
+__device__ __forceinline__ uint32_t patience(const AdaptArgs &g) {
+  return (1u << 20) + 64u * (uint32_t)min(g.hidden, 1 << 24);
+}
+
 // A bounded wait that also ends when the CTA gives up.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-  for (uint32_t it = 0; it < (1u << 20); ++it) {
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                     uint32_t polls) {
+  for (uint32_t it = 0; it < polls; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 15) == 15 && *abort_flag) return false;
   }

@@ -24,20 +24,6 @@ namespace {
 
 constexpr int kWarps = 8;
 
-// Elements k .. k + 7 of a row, zeros from `hidden` on (what lies behind a row is not read).  WHOLE:
-// hidden is a multiple of 8.
-template <bool WHOLE>
-__device__ __forceinline__ uint4 load8(const bf16 *row, int k, int hidden) {
-  if (WHOLE) return k < hidden ? *reinterpret_cast<const uint4 *>(row + k) : make_uint4(0, 0, 0, 0);
-  if (k + 8 <= hidden) return *reinterpret_cast<const uint4 *>(row + k);
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (k + j < hidden)
-      w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row)[k + j] << (16 * (j & 1));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // AHEAD: steps of 64 k whose loads a warp has in flight.  (With the ends of odd rows looked at in
 // every load the code was so long that fetching it took longer than the work.)
 template <int MT, int NT, int AHEAD, bool WHOLE, bool PLANES>

@@ -14,8 +14,10 @@
 // The adapters are further k-blocks: B tiles for W's and the parts of h for x's.  Where all tokens of a
 // tile have one adapter (most of a prompt) that is all.  In a mixed tile every adapter has its own
 // k-blocks, with a plane of h that has zeros for the other tokens.  A result that is not finite may then
-// come from another request's adapter (0 * inf), and is computed again by itself, so that nothing of
-// one adapter reaches another's tokens.  For more than eight adapters in a tile
+// come from another request's adapter (0 * inf), and is computed again from its own, so that nothing of
+// one adapter reaches another's tokens: 32 outputs of 16 tokens at a time, by mma.sync.  (Where every result
+// of every tile is: 5000 bf16 tokens, eight adapters of rank 32, 2048 -> 1296, 108 -> 650 us; 600 tokens ->
+// 40960 161 -> 2040; these are loads of W from L2, once per 16 tokens.)  For more than eight adapters in a tile
 // the helpers multiply B and h with mma.sync: four warps with 32 output rows each take the tasks
 // (up to eight tokens of one adapter) in turn, with B and h from global memory, and store them to TMEM
 // columns of their own, [token][row], which the epilogue adds.  For a bf16 y these are the columns of
@@ -50,7 +52,7 @@ struct Cfg {
   static constexpr int kRound = kAcc * kChain;  // k-blocks after which a float32 y's are taken out
   static constexpr int kStage = kTileW + BT / 2 * kBK * 2;
   static constexpr int kStages = 6;
-  static constexpr int kScratch = kWarps * 8 * 33 * 4;
+  static constexpr int kScratch = kWarps * 16 * 33 * 4;
   static constexpr int kSmem = kStages * kStage + kScratch + 1024;
 };
 
@@ -218,26 +220,103 @@ __device__ __forceinline__ void expand_rank(const AdaptArgs &g, const Groups<BT>
     expand<BT, 16, 2, 2, WHOLE, PARTS>(g, s, warp, quad, n0, tok0, scratch, delta);
 }
 
-// One output by itself: row n, token t of a tile with the adapters list[0 .. count).
+// Outputs row0 .. row0 + 31 of tokens tok .. tok + live - 1 (at most 16) by themselves, a warp: W x with
+// mma.sync (see gdn_adapt_low.cu for the loads), and what each token's own adapter adds.  The tile's
+// adapters are list[0 .. count).  Into out [token][33].
 template <int PARTS>
-__device__ __noinline__ float one_by_one(const AdaptArgs &g, const int *list, int count, int t, int n) {
-  const bf16 *x = static_cast<const bf16 *>(g.x) + t * g.ld_x;
-  const bf16 *w = static_cast<const bf16 *>(g.w) + n * g.ld_w;
-  float sum = 0.f;
-  for (int k = 0; k < g.hidden; ++k) sum += __bfloat162float(w[k]) * __bfloat162float(x[k]);
-  const int id = token_id(g, t), ld = g.rank_pad();
-  if (id < 0) return sum;
-  int plane = 0;
-  while (plane + 1 < count && list[plane] != id) ++plane;
-  kv::dependent_wait();
-  const bf16 *b = static_cast<const bf16 *>(g.b) + ((int64_t)id * g.n_out + n) * g.ld_b;
-  const bf16 *h = static_cast<const bf16 *>(g.h) + ((int64_t)plane * PARTS * g.tokens + t) * ld;
-  for (int r = 0; r < g.rank; ++r) {
-    float low = __bfloat162float(h[r]);
-    for (int p = 1; p < PARTS; ++p) low += __bfloat162float(h[(int64_t)p * g.tokens * ld + r]);
-    sum += __bfloat162float(b[r]) * low;
+__device__ __forceinline__ void again(const AdaptArgs &g, const int *list, int count, int row0, int tok,
+                                   int live, float *out) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const bf16 *x[2], *w[2][2];  // (rows that are not there: any, their results are dropped)
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[i] = static_cast<const bf16 *>(g.x) + (tok + min(8 * i + r, live - 1)) * g.ld_x;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      w[i][y] = static_cast<const bf16 *>(g.w) + min(row0 + 16 * i + 8 * y + r, g.n_out - 1) * g.ld_w;
   }
-  return sum;
+  float sum[2][2][4] = {};
+  for (int k0 = 0; k0 < g.hidden; k0 += 256) {  // (short chains: these sums are cut off too)
+    float acc[2][2][4] = {};
+    const int end = min(k0 + 256, g.hidden);
+#pragma unroll 2
+    for (int k = k0; k < end; k += 32) {
+      uint4 a[2][2], b[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        b[i] = load8<false>(x[i], k + 8 * c, g.hidden);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) a[i][y] = load8<false>(w[i][y], k + 8 * c, g.hidden);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t f0[4] = {a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y};
+        const uint32_t f1[4] = {a[m][0].z, a[m][1].z, a[m][0].w, a[m][1].w};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mma16816(acc[m][i], f0, b[i].x, b[i].y);
+          mma16816(acc[m][i], f1, b[i].z, b[i].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[m][i][e] += acc[m][i][e];
+  }
+  kv::dependent_wait();  // h
+  // what the adapters add: all of one to every token, and kept where it is the token's own
+  const int ld = g.rank_pad(), id = lane < live ? token_id(g, tok + lane) : -1;
+  const int64_t part = (int64_t)g.tokens * ld;
+  for (int j = 0; j < count; ++j) {
+    const uint32_t own = __ballot_sync(0xffffffffu, id >= 0 && id == list[j]);
+    if (own == 0) continue;
+    float acc[2][2][4] = {};
+    for (int k = 8 * c; k - 8 * c < g.rank; k += 32) {
+      uint4 a[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int n = min(row0 + 16 * i + 8 * y + r, g.n_out - 1);
+          a[i][y] = load8<false>(
+              static_cast<const bf16 *>(g.b) + ((int64_t)list[j] * g.n_out + n) * g.ld_b, k, g.rank);
+        }
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bf16 *h = static_cast<const bf16 *>(g.h) + (j * PARTS + p) * part +
+                          (int64_t)(tok + min(8 * i + r, live - 1)) * ld;
+          const uint4 b = load8<true>(h, k, ld);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint32_t f0[4] = {a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y};
+            const uint32_t f1[4] = {a[m][0].z, a[m][1].z, a[m][0].w, a[m][1].w};
+            mma16816(acc[m][i], f0, b.x, b.y);
+            mma16816(acc[m][i], f1, b.z, b.w);
+          }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (own >> (8 * i + 2 * c + (e & 1)) & 1) sum[m][i][e] += acc[m][i][e];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        out[(8 * i + 2 * c + (e & 1)) * 33 + 16 * m + 8 * (e >> 1) + r] = sum[m][i][e];
+  __syncwarp();
 }
 
 // 16 tokens' outputs n, a lane per output: two neighbouring lanes exchange, so that each stores two
@@ -256,6 +335,73 @@ __device__ __forceinline__ void store_rows(bf16 *y, int64_t ld, int n, int n_out
       *reinterpret_cast<__nv_bfloat162 *>(p) = w;
     else if (n - odd < n_out)
       *p = w.x;
+  }
+}
+
+// 16 tokens' results of this lane's row, from column c of the accumulators on; `delta`: what is to be
+// added, if `summed`.  kbs: the tile's k-blocks.
+template <typename TO>
+__device__ __forceinline__ void load_results(uint32_t acc, uint32_t delta, bool summed, int kbs, int c,
+                                             float *v) {
+  using C = Cfg<TO>;
+  constexpr int BT = C::BT;
+  if constexpr (C::kF32) {
+    float u[32];
+    tc::tmem_ld32(acc + c, acc + BT + c, v);
+    const int last = (kbs - 1) % C::kRound + 1;
+    if (last > 1)  // (an accumulator that no k-block of the round has come to holds anything)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
+    if (summed)
+      tc::tmem_ld32(acc + 2 * BT + c, delta + c, u);
+    else
+      tc::tmem_ld16(acc + 2 * BT + c, u);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (last > 2) v[j] += u[j];
+      if (summed) v[j] += u[16 + j];
+    }
+  } else if (summed) {
+    tc::tmem_ld32(acc + c, delta + c, v);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
+  } else {
+    tc::tmem_ld16(acc + c, v);
+  }
+}
+
+// Outputs n of tokens tok .. tok + min(live, 16) - 1.
+__device__ __forceinline__ void store_results(const AdaptArgs &g, float *y, int tok, int live, int n,
+                                              const float *v) {
+  if (n >= g.n_out) return;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j < live) y[(int64_t)(tok + j) * g.ld_y + n] = v[j];
+}
+__device__ __forceinline__ void store_results(const AdaptArgs &g, bf16 *y, int tok, int live, int n,
+                                              const float *v) {
+  store_rows(y + (int64_t)tok * g.ld_y, g.ld_y, n, g.n_out, live, v);
+}
+
+// Steps `odd` of a tile's results, some of which are not finite: those are computed again, and all stored
+// again.  (By itself: what is kept over the calls would cost the kernel registers.)
+template <typename TO>
+__device__ __noinline__ void results_again(const AdaptArgs &g, const int *list, int count, int row0,
+                                           int tok0, int live, uint32_t odd, uint32_t acc,
+                                           uint32_t delta, float *own) {
+  using C = Cfg<TO>;
+  const int lane = threadIdx.x & 31;
+  const int kbs = (g.hidden + kBK - 1) / kBK + count * ((g.rank + kBK - 1) / kBK) * C::kParts;
+  for (; odd != 0; odd &= odd - 1) {
+    const int c = 16 * (__ffs(odd) - 1);
+    again<C::kParts>(g, list, count, row0, tok0 + c, min(16, live - c), own);
+    float v[32];
+    load_results<TO>(acc, delta, C::kF32 && kbs > C::kRound, kbs, c, v);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (c + j < live && !(fabsf(v[j]) < INFINITY)) v[j] = own[j * 33 + lane];
+    store_results(g, static_cast<TO *>(g.y), tok0 + c, live - c, row0 + lane, v);
+    __syncwarp();
   }
 }
 
@@ -335,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the adapter that all tokens of the pair's i-th tile have, or -1: none has any, kMany: more than there
   // are planes for, kGaveUp: a wait did, kMixed - n: n (s_list)
   auto tile_info = [&](int i) {
-    if (!wait(&info_full[i % kInfo], (i / kInfo) & 1, abort_flag)) return kGaveUp;
+    if (!wait(&info_full[i % kInfo], (i / kInfo) & 1, abort_flag, patience(g))) return kGaveUp;
     return *reinterpret_cast<volatile int *>(&s_info[i % kInfo]);
   };
 
@@ -357,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kbs = plain + adapters_of(one) * chunks * C::kParts;
       for (int kb = 0; kb < kbs; ++kb, ++u, s = s + 1 == S ? 0 : s + 1) {
         if (s == 0 && u > S) round ^= 1;  // (the first round waits for nothing, the second for phase 0)
-        if (u >= S && !wait(&empty[s], round, abort_flag)) {
+        if (u >= S && !wait(&empty[s], round, abort_flag, patience(g))) {
           good = false;
           break;
         }
@@ -400,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The accumulators' columns are free once the epilogue of tile i - 2 is done, or of tile i - 1
       // where they are the same or held its adapters' part.
       auto free_after = [&](int last) {
-        return last < 0 || wait(&acc_empty[last & 1], (uint32_t)((last >> 1) & 1), abort_flag);
+        return last < 0 || wait(&acc_empty[last & 1], (uint32_t)((last >> 1) & 1), abort_flag, patience(g));
       };
       if (one == kGaveUp || !free_after(C::kF32 || before == kMany ? i - 1 : i - 2)) {
         good = false;
@@ -414,14 +560,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto block = [&](int steps) {
         if (C::kF32 && in == C::kRound) {
           commit_pair(&round_full);
-          if (!wait(&round_taken, rounds++ & 1, abort_flag)) return false;
+          if (!wait(&round_taken, rounds++ & 1, abort_flag, patience(g))) return false;
           tc::fence_after_sync();
           turn = in = 0;
         }
         const uint32_t acc = base + (uint32_t)turn * BT;
         const bool fresh = in++ < C::kAcc;
         turn = turn + 1 == C::kAcc ? 0 : turn + 1;
-        if (!wait(&full[s], round, abort_flag)) return false;
+        if (!wait(&full[s], round, abort_flag, patience(g))) return false;
         tc::fence_after_sync();
         const uint32_t a = smem_addr(tile_w(s)), b = smem_addr(tile_x(s));
 #pragma unroll
@@ -453,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok0 = (int)(t / n_tiles) * BT, live = min(BT, g.tokens - tok0);
       if (i >= kInfo)
         good = __all_sync(0xffffffffu,
-                          wait(&info_empty[i % kInfo], ((i / kInfo) - 1) & 1, abort_flag));
+                          wait(&info_empty[i % kInfo], ((i / kInfo) - 1) & 1, abort_flag, patience(g)));
       if (!good) break;
       const int n = tile_groups(g, tok0, live, s_list[i % kInfo]);
       bool whole = true;  // no token without an adapter
@@ -498,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         find_groups<BT, kHelpers>(s_groups);
         tc::fence_after_sync();
         kv::dependent_wait();  // h
-        float *sc = scratch + (warp - 2) * 8 * 33;
+        float *sc = scratch + (warp - 2) * 16 * 33;
         if (n0 < g.n_out) {
           if (g.rank % 8 == 0)
             expand_rank<BT, true, C::kParts>(g, s_groups, warp - 2, quad, n0, tok0, sc, delta);
@@ -513,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kbs = plain + adapters_of(one) * chunks * C::kParts;
       if constexpr (C::kF32)
         for (int k = C::kRound; k < kbs && good; k += C::kRound, ++rounds) {
-          good = __all_sync(0xffffffffu, wait(&round_full, rounds & 1, abort_flag));
+          good = __all_sync(0xffffffffu, wait(&round_full, rounds & 1, abort_flag, patience(g)));
           if (!good) break;
           tc::fence_after_sync();
 #pragma unroll 1
@@ -537,59 +683,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive_leader(&round_taken);
         }
       good = good &&
-             __all_sync(0xffffffffu, wait(&acc_full[i & 1], (i >> 1) & 1, abort_flag));
+             __all_sync(0xffffffffu, wait(&acc_full[i & 1], (i >> 1) & 1, abort_flag, patience(g)));
       if (!good) {
         fail();
         continue;
       }
       tc::fence_after_sync();
+      const bool summed = one == kMany || (C::kF32 && kbs > C::kRound);
+      uint32_t odd = 0;  // steps with results that are not finite
 #pragma unroll 1
       for (int c = 16 * side; c < live; c += 16 * kTeams) {
         float v[32];
-        if constexpr (C::kF32) {
-          float u[32];
-          tc::tmem_ld32(acc + c, acc + BT + c, v);
-          const bool summed = one == kMany || kbs > C::kRound;
-          const int last = (kbs - 1) % C::kRound + 1;
-          if (last > 1)  // (an accumulator that no k-block of the round has come to holds anything)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
-          if (summed)
-            tc::tmem_ld32(acc + 2 * BT + c, delta + c, u);
-          else
-            tc::tmem_ld16(acc + 2 * BT + c, u);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (last > 2) v[j] += u[j];
-            if (summed) v[j] += u[16 + j];
-          }
-        } else if (one == kMany) {
-          tc::tmem_ld32(acc + c, delta + c, v);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] += v[16 + j];
-        } else {
-          tc::tmem_ld16(acc + c, v);
-        }
+        load_results<TO>(acc, delta, summed, kbs, c, v);
         if (one <= kMixed) {
-          bool odd = false;
+          bool finite = true;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) odd = odd || !(fabsf(v[j]) < INFINITY);
-          if (odd && n < g.n_out)
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c + j < live && !(fabsf(v[j]) < INFINITY))
-                v[j] = one_by_one<C::kParts>(g, s_list[i % kInfo], kMixed - one, tok0 + c + j, n);
-          __syncwarp();
+          for (int j = 0; j < 16; ++j) finite = finite && (c + j >= live || fabsf(v[j]) < INFINITY);
+          if (!__all_sync(0xffffffffu, finite || n >= g.n_out)) odd |= 1u << (c / 16);
         }
-        if constexpr (C::kF32) {
-          if (n < g.n_out)
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c + j < live) y[(int64_t)(tok0 + c + j) * g.ld_y + n] = v[j];
-        } else {
-          store_rows(y + (int64_t)(tok0 + c) * g.ld_y, g.ld_y, n, g.n_out, live - c, v);
-        }
+        store_results(g, y, tok0 + c, live - c, n, v);
       }
+      if (odd != 0)
+        results_again<TO>(g, s_list[i % kInfo], kMixed - one, n0 + 32 * quad, tok0, live, odd, acc, delta,
+                          scratch + (warp - 2) * 16 * 33);
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) {

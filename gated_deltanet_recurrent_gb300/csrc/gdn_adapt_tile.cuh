@@ -1,13 +1,28 @@
-// The adapters of a tile of tokens.
+// The adapters of a tile of tokens, and rows of bf16 elements.
 #pragma once
 
 #include "gdn_adapt.h"
+#include "gdn_common.cuh"
 
 namespace gdn {
 
 __device__ __forceinline__ int token_id(const AdaptArgs &g, int t) {
   const int id = t < g.tokens ? g.ids[t] : -1;
   return id >= 0 && id < g.n_adapters ? id : -1;
+}
+
+// Elements k .. k + 7 of a row, zeros from `hidden` on (what lies behind a row is not read).  WHOLE:
+// hidden is a multiple of 8.
+template <bool WHOLE>
+__device__ __forceinline__ uint4 load8(const bf16 *row, int k, int hidden) {
+  if (WHOLE) return k < hidden ? *reinterpret_cast<const uint4 *>(row + k) : make_uint4(0, 0, 0, 0);
+  if (k + 8 <= hidden) return *reinterpret_cast<const uint4 *>(row + k);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (k + j < hidden)
+      w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row)[k + j] << (16 * (j & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // One warp: the adapters of tokens tok0 .. tok0 + live - 1 (live <= 256) in the order of their first
