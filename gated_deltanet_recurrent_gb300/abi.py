@@ -24,6 +24,7 @@ DEVERR_PAGE, DEVERR_VALUE, DEVERR_ADAPTER = 16, 32, 64
 GDN_KV_I8, GDN_KV_E4M3 = 0, 1
 GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
 TEST_DECODE_WAIT_TIMEOUT = 1
+TEST_ADAPT_WAIT_TIMEOUT, TEST_ADAPT_SIDE_TIMEOUT = 4, 8
 TEST_KV_WAIT_TIMEOUT = 1
 
 EXPORTED = ("gdn_pool_state_bytes", "gdn_pool_conv_bytes", "gdn_pool_create", "gdn_pool_reset",

@@ -238,9 +238,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int all = (g.hidden + kBK - 1) / kBK;
   const int kb0 = (int)((int64_t)all * part / splits);
   const int plain = (int)((int64_t)all * (part + 1) / splits) - kb0;
+  // (test hooks: a barrier of one CTA waits for 16 bytes that no one sends)
+  const bool short_of = (blockIdx.x / splits + blockIdx.y) & 1 && part == splits - 1;
+  const uint32_t short_w = short_of && g.test_flags & GDN_TEST_ADAPT_WAIT_TIMEOUT ? 16 : 0;
+  const uint32_t short_b = short_of && g.test_flags & GDN_TEST_ADAPT_SIDE_TIMEOUT ? 16 : 0;
+  int issued = 0, issued_b = -1;  // k-blocks whose copies the producer has started; a lane's last B tile
   auto load_plain = [&](int kb) {
     const int s = kb % S;
-    mbar_arrive_expect_tx(&full[s], C::kStage);
+    mbar_arrive_expect_tx(&full[s], C::kStage + (kb == 0 ? short_w : 0));
     tma_load2(tile_w(s), &mw, (kb0 + kb) * kBK, n0, &full[s]);
     tma_load2(tile_x(s), &mx, (kb0 + kb) * kBK, tok0, &full[s]);
   };
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0 && lane == 0) {
     // producer
-    int issued = min(S, plain);
+    issued = min(S, plain);
     for (int kb = issued; kb < kbs; ++kb) {
       const int s = kb % S;
       if (kb >= S && !wait(&empty[s], ((kb / S) - 1) & 1, abort_flag, polls)) {
@@ -318,16 +323,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       issued = kb + 1;
     }
-    if (*abort_flag) {  // let the copies still in flight land before the CTA exits
-      for (int kb = issued - S < 0 ? 0 : issued - S; kb < issued; ++kb)
-        mbar_wait_bounded(&full[kb % S], (kb / S) & 1);
-    }
   } else if (warp == 2 + kHelpers / 32) {
     // a lane per slot of the ring of B tiles
     if (one == -2) {
       bool good = __all_sync(0xffffffffu, wait(&list, 0, abort_flag, polls));
       const int units = good ? s_groups.n * halves : 0;
-      int u = lane < E ? lane : units, issued = -1;
+      int u = lane < E ? lane : units;
       uint32_t idle = 0;
       while (good && __any_sync(0xffffffffu, u < units)) {
         bool moved = false;
@@ -335,9 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int half = u >= s_groups.n, group = u - half * s_groups.n;
           const int row = s_groups.adapter[group] * g.n_out + n0;
           unsigned char *tile = ring_b + lane * (kBM * PITCH);
-          mbar_arrive_expect_tx(&b_full[lane], kBM * PITCH);
+          mbar_arrive_expect_tx(&b_full[lane], kBM * PITCH + (u == 0 ? short_b : 0));
           tma_load2(tile, &mu, half * (PITCH / 2), row, &b_full[lane]);
-          issued = u;
+          issued_b = u;
           u += E;
           moved = true;
         }
@@ -345,7 +346,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (idle > (1u << 24)) fail();  // seconds
         if ((idle & 15) == 15) good = !__any_sync(0xffffffffu, *abort_flag != 0);
       }
-      if (!good && issued >= 0) mbar_wait_bounded(&b_full[lane], (issued / E) & 1);
     }
   } else if (warp == 1 && lane == 0) {
     // MMA issuer
@@ -376,10 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                          idesc, in >= C::kAcc || kk > 0 ? 1u : 0u);
       tc::mma_commit(&empty[s]);
     }
-    if (!good) fail();
-    tc::mma_commit(good ? &done : &drain);
-    if (!good) mbar_wait_bounded(&drain, 0);  // MMAs in flight finish before TMEM is freed
+    if (good)
+      tc::mma_commit(&done);
+    else
+      fail();
   } else if (warp >= 2) {
+    bool whole = true;  // nothing was given up
     if (one >= 0) {  // B on its way to L2
       const bf16 *b = static_cast<const bf16 *>(g.b) +
                       ((int64_t)one * g.n_out + min(n0 + (tid - 64) / 4, g.n_out - 1)) * g.ld_b +
@@ -396,13 +398,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         abort_flag, polls))
         fail();
       helpers_sync<kHelpers>();
+      whole = *abort_flag == 0;
     }
     // a lane per output row, the four warps of TMEM lanes 32 quad .. take turns in the columns
     const int quad = warp & 3, side = (warp - 2) >> 2, row = 32 * quad + lane, n = n0 + row;
     const uint32_t mine = tmem + ((uint32_t)(32 * quad) << 16);
     // the accumulators of a long sum, taken out
-    for (int r = 0; C::kLong && r < rounds_before; ++r) {
-      if (!__all_sync(0xffffffffu, wait(&done, r & 1, abort_flag, polls))) {
+    for (int r = 0; C::kLong && whole && r < rounds_before; ++r) {
+      whole = __all_sync(0xffffffffu, wait(&done, r & 1, abort_flag, polls));
+      if (!whole) {
         fail();
         break;
       }
@@ -428,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_wait();
     }
     // warp-uniform decision: tcgen05.ld is a whole-warp instruction
-    const bool got = __all_sync(0xffffffffu, wait(&done, rounds_before & 1, abort_flag, polls));
+    const bool got =
+        __all_sync(0xffffffffu, whole && wait(&done, rounds_before & 1, abort_flag, polls));
     if (!got) {
       fail();
     } else {
@@ -466,6 +471,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (*abort_flag) {  // copies and products still in flight end before the CTA does
+    if (tid == 0)
+      for (int kb = max(0, issued - S); kb < issued; ++kb)
+        mbar_wait_bounded(&full[kb % S], (kb / S) & 1, polls);
+    if (tid == 32) {
+      tc::mma_commit(&drain);
+      mbar_wait_bounded(&drain, 0, polls);
+    }
+    if (issued_b >= 0) mbar_wait_bounded(&b_full[lane], (issued_b / E) & 1, polls);
+    __syncthreads();
+  }
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::kTmem);

@@ -69,6 +69,7 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
 // Polls of a bounded wait (of up to a microsecond or two each): what one step of any role may take grows
 // with hidden, and is some 50 ns for each of it where a tile's results are all computed again.
 __device__ __forceinline__ uint32_t patience(const AdaptArgs &g) {
+  if (g.test_flags & (GDN_TEST_ADAPT_WAIT_TIMEOUT | GDN_TEST_ADAPT_SIDE_TIMEOUT)) return 1u << 11;
   return (1u << 20) + 64u * (uint32_t)min(g.hidden, 1 << 24);
 }
 

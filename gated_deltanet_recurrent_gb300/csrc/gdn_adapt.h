@@ -22,6 +22,7 @@ struct AdaptArgs {
   int tile;
   unsigned int *err;
   int sm_count, device;
+  uint32_t test_flags;  // GDN_TEST_ADAPT_* bits of the pool; 0 in normal use
   GDN_HD int parts() const { return y_dtype == GDN_F32 ? 3 : 2; }
   // the rank rounded up to the tensor cores' 16
   GDN_HD int rank16() const { return (rank + 15) & ~15; }

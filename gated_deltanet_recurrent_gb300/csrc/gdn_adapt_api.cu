@@ -148,7 +148,7 @@ gdn_status gdn_in_proj_adapted(gdn_pool *p, gdn_adapters *ad, int64_t tokens, co
     return st;
   gdn::AdaptArgs g = {x, w, ad->a, ad->b, ad->scale, ids, y, ld_x, ld_w, ad->ld_a, ad->ld_b, ld_y,
                       (int)tokens, d.hidden, d.n_out, d.rank, d.n_adapters, y_dtype, nullptr, 0,
-                      p->view.err, ad->sm_count, dev};
+                      p->view.err, ad->sm_count, dev, p->view.test_flags};
   g.tile = gdn::adapt_tile(g);
   void *work = nullptr;
   bool temporary = false;

@@ -100,6 +100,19 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// As if a copy of `bytes` had reported to the barrier.
+__device__ __forceinline__ void complete_tx(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void st_peer64(const void *p, int rank, int64_t v) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "st.shared::cluster.b64 [a], %2;\n\t}" ::"r"(smem_addr(p)),
+      "r"(rank), "l"(v)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr),
                "r"(__float_as_uint(v))
@@ -429,6 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       info_empty[kInfo], round_full, round_taken, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort, s_info[kInfo], s_list[kInfo][kPlanes];
+  __shared__ float s_gone;      // one of the two gave up
+  __shared__ int64_t s_issued;  // in CTA 0: k-blocks whose copies the other has started
   __shared__ Groups<BT> s_groups;
   unsigned char *smem = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
@@ -441,6 +456,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_tiles = (g.n_out + 2 * kBM - 1) / (2 * kBM), t_tiles = (g.tokens + BT - 1) / BT;
   const int64_t tiles = (int64_t)n_tiles * t_tiles;
   const int plain = (g.hidden + kBK - 1) / kBK, chunks = (g.rank + kBK - 1) / kBK;
+  // (test hooks: in every other pair a barrier waits for what no one sends, CTA 0's first copies', or that
+  // of the first tile's adapters in CTA 0 or 1)
+  const bool short_w = g.test_flags & GDN_TEST_ADAPT_WAIT_TIMEOUT && pair & 1;
+  const bool short_side = g.test_flags & GDN_TEST_ADAPT_SIDE_TIMEOUT && pair & 1 && (pair >> 1 & 1) == rank;
+  int64_t issued = 0;  // k-blocks whose copies this CTA's producer has started
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -451,13 +471,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_empty[b], 2 * kWarps);
     }
     for (int i = 0; i < kInfo; ++i) {
-      mbar_init(&info_full[i], 1);
+      mbar_init(&info_full[i], short_side && i == 0 ? 2 : 1);
       mbar_init(&info_empty[i], kWarps);
     }
     mbar_init(&round_full, 1);
     mbar_init(&round_taken, 2 * kWarps);
     mbar_init(&drain, 1);
     s_abort = 0;
+    s_gone = 0.f;
     mbar_fence_init();
   }
   __syncwarp();
@@ -474,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
   volatile int *abort_flag = &s_abort;
+  const uint32_t polls = patience(g);
   auto fail = [&]() {
     *abort_flag = 1;
     raise_error(g.err, GDN_DEVERR_TIMEOUT);
@@ -481,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the adapter that all tokens of the pair's i-th tile have, or -1: none has any, kMany: more than there
   // are planes for, kGaveUp: a wait did, kMixed - n: n (s_list)
   auto tile_info = [&](int i) {
-    if (!wait(&info_full[i % kInfo], (i / kInfo) & 1, abort_flag, patience(g))) return kGaveUp;
+    if (!wait(&info_full[i % kInfo], (i / kInfo) & 1, abort_flag, polls)) return kGaveUp;
     return *reinterpret_cast<volatile int *>(&s_info[i % kInfo]);
   };
 
@@ -489,7 +511,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // producer
     int s = 0;
     uint32_t round = 0;
-    int64_t u = 0;
     bool good = true, waited = false;
     int i = 0;
     for (int64_t t = pair; t < tiles && good; t += pairs, ++i) {
@@ -501,14 +522,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       const int kbs = plain + adapters_of(one) * chunks * C::kParts;
-      for (int kb = 0; kb < kbs; ++kb, ++u, s = s + 1 == S ? 0 : s + 1) {
-        if (s == 0 && u > S) round ^= 1;  // (the first round waits for nothing, the second for phase 0)
-        if (u >= S && !wait(&empty[s], round, abort_flag, patience(g))) {
+      for (int kb = 0; kb < kbs; ++kb, ++issued, s = s + 1 == S ? 0 : s + 1) {
+        if (s == 0 && issued > S) round ^= 1;  // (the first round waits for nothing, the second for phase 0)
+        if (issued >= S && !wait(&empty[s], round, abort_flag, polls)) {
           good = false;
           break;
         }
         const uint32_t bar = leader_addr(&full[s]);
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
+        if (rank == 0)
+          mbar_arrive_expect_tx(&full[s], 2 * C::kStage + (short_w && issued == 0 ? 16 : 0));
         if (kb < plain) {
           tma_load2_pair(tile_w(s), &mw, kb * kBK, n0, bar);
           tma_load2_pair(tile_x(s), &mx, kb * kBK, tok0, bar);
@@ -527,12 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!good) {
-      fail();
-      if (rank == 0)  // let the copies still in flight land before the pair exits
-        for (int64_t q = u - S < 0 ? 0 : u - S; q < u; ++q)
-          mbar_wait_bounded(&full[q % S], (uint32_t)((q / S) & 1));
-    }
+    if (!good) fail();
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // MMA issuer
     constexpr uint32_t idesc = tc::idesc_bf16(2 * kBM, BT);
@@ -546,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The accumulators' columns are free once the epilogue of tile i - 2 is done, or of tile i - 1
       // where they are the same or held its adapters' part.
       auto free_after = [&](int last) {
-        return last < 0 || wait(&acc_empty[last & 1], (uint32_t)((last >> 1) & 1), abort_flag, patience(g));
+        return last < 0 || wait(&acc_empty[last & 1], (uint32_t)((last >> 1) & 1), abort_flag, polls);
       };
       if (one == kGaveUp || !free_after(C::kF32 || before == kMany ? i - 1 : i - 2)) {
         good = false;
@@ -560,14 +577,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto block = [&](int steps) {
         if (C::kF32 && in == C::kRound) {
           commit_pair(&round_full);
-          if (!wait(&round_taken, rounds++ & 1, abort_flag, patience(g))) return false;
+          if (!wait(&round_taken, rounds++ & 1, abort_flag, polls)) return false;
           tc::fence_after_sync();
           turn = in = 0;
         }
         const uint32_t acc = base + (uint32_t)turn * BT;
         const bool fresh = in++ < C::kAcc;
         turn = turn + 1 == C::kAcc ? 0 : turn + 1;
-        if (!wait(&full[s], round, abort_flag, patience(g))) return false;
+        if (!wait(&full[s], round, abort_flag, polls)) return false;
         tc::fence_after_sync();
         const uint32_t a = smem_addr(tile_w(s)), b = smem_addr(tile_x(s));
 #pragma unroll
@@ -586,11 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             good = block(min(kBK, g.rank16() - c * kBK) / 16);
       if (good) commit_pair(&acc_full[i & 1]);
     }
-    if (!good) {
-      fail();
-      commit_pair(&drain);
-      mbar_wait_bounded(&drain, 0);  // MMAs in flight finish before TMEM is freed
-    }
+    if (!good) fail();
   } else if (warp == 2 + kWarps) {
     // scout
     int i = 0;
@@ -599,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok0 = (int)(t / n_tiles) * BT, live = min(BT, g.tokens - tok0);
       if (i >= kInfo)
         good = __all_sync(0xffffffffu,
-                          wait(&info_empty[i % kInfo], ((i / kInfo) - 1) & 1, abort_flag, patience(g)));
+                          wait(&info_empty[i % kInfo], ((i / kInfo) - 1) & 1, abort_flag, polls));
       if (!good) break;
       const int n = tile_groups(g, tok0, live, s_list[i % kInfo]);
       bool whole = true;  // no token without an adapter
@@ -659,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kbs = plain + adapters_of(one) * chunks * C::kParts;
       if constexpr (C::kF32)
         for (int k = C::kRound; k < kbs && good; k += C::kRound, ++rounds) {
-          good = __all_sync(0xffffffffu, wait(&round_full, rounds & 1, abort_flag, patience(g)));
+          good = __all_sync(0xffffffffu, wait(&round_full, rounds & 1, abort_flag, polls));
           if (!good) break;
           tc::fence_after_sync();
 #pragma unroll 1
@@ -683,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive_leader(&round_taken);
         }
       good = good &&
-             __all_sync(0xffffffffu, wait(&acc_full[i & 1], (i >> 1) & 1, abort_flag, patience(g)));
+             __all_sync(0xffffffffu, wait(&acc_full[i & 1], (i >> 1) & 1, abort_flag, polls));
       if (!good) {
         fail();
         continue;
@@ -717,7 +730,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (the leader's products read the other CTA's shared memory, and its commits arrive there)
   tc::fence_before_sync();
   __syncthreads();
+  if (tid == 0) {
+    if (rank == 1) st_peer64(&s_issued, 0, issued);
+    if (*abort_flag)
+      for (int p = 0; p < 2; ++p) st_peer(&s_gone, p, 1.f);
+  }
   cluster_sync();
+  if (s_gone != 0.f) {  // copies and products still in flight end before the pair does
+    if (tid == 32) {
+      if (rank == 0) commit_pair(&drain);
+      mbar_wait_bounded(&drain, 0, polls);
+    }
+    if (rank == 0 && tid == 0) {
+      // The two may have stopped at different k-blocks.  Of what both started, CTA 0's barriers await both;
+      // of what only one did, its half: CTA 0 awaits the other's too, or nothing yet.
+      const int64_t both = min(issued, s_issued), any = max(issued, s_issued);
+      for (int64_t q = max((int64_t)0, both - S); q < any; ++q) {
+        uint64_t *bar = &full[q % S];
+        if (q >= both && issued > both) complete_tx(bar, C::kStage);
+        if (q >= both && issued == both) mbar_arrive_expect_tx(bar, C::kStage);
+        mbar_wait_bounded(bar, (uint32_t)((q / S) & 1), polls);
+      }
+    }
+    cluster_sync();
+  }
   if (warp == 1) {
     tc::fence_after_sync();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)

@@ -309,7 +309,8 @@ gdn_status gdn_pool_destroy(gdn_pool *p) {
 
 gdn_status gdn_pool_set_test_flags(gdn_pool *p, uint32_t flags) {
   if (!p) return fail(GDN_ERR_ARG, "pool is NULL");
-  if (flags & ~(uint32_t)GDN_TEST_DECODE_WAIT_TIMEOUT)
+  if (flags & ~(GDN_TEST_DECODE_WAIT_TIMEOUT | GDN_TEST_ADAPT_WAIT_TIMEOUT |
+                GDN_TEST_ADAPT_SIDE_TIMEOUT))
     return fail(GDN_ERR_ARG, "unknown test flags 0x%x", flags);
   p->view.test_flags = flags;
   return ok();

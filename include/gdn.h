@@ -184,9 +184,15 @@ gdn_status gdn_pool_get_error(gdn_pool *pool, uint32_t *dev_err);
  * 16 bytes more than its state-tile copy delivers: the copy lands, the
  * bounded wait runs out (a second or two), the CTA sets GDN_DEVERR_TIMEOUT,
  * leaves its state rows and its rows of o unwritten and exits with no copy
- * in flight.  It exercises the error path of the waits without a fault; flags
- * other than that bit are GDN_ERR_ARG. */
+ * in flight.  It exercises the error path of the waits without a fault.  The
+ * next two do the same in gdn_in_proj_adapted, with short limits (milliseconds):
+ * in every other tile of outputs the products wait for more than their copies
+ * deliver, or what goes on beside the products does (in calls of few tokens with several
+ * adapters a tile, the copies of B; in calls of many, what tells a tile's
+ * adapters); those tiles of y keep what they held.  Other flags are GDN_ERR_ARG. */
 #define GDN_TEST_DECODE_WAIT_TIMEOUT 1u
+#define GDN_TEST_ADAPT_WAIT_TIMEOUT 4u
+#define GDN_TEST_ADAPT_SIDE_TIMEOUT 8u
 gdn_status gdn_pool_set_test_flags(gdn_pool *pool, uint32_t flags);
 
 /* Causal depthwise conv of width conv_k followed by SiLU (baseRT issue #31,
