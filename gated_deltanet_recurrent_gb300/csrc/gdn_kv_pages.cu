@@ -204,8 +204,9 @@ __global__ void __launch_bounds__(kThreads)
     // the table entries of this round's pages
     for (int k = taken + me; k < s_taken; k += step) {
       const int j = last_at_most(r.first, cnt, k);
-      b.table[(int64_t)r.slot[j] * c.max_pages + r.have[j] + (k - r.first[j])] =
-          b.free_pages[top - 1 - k];
+      const int id = b.free_pages[top - 1 - k];
+      if (id < 0 || id >= c.n_pages) raise_error(c.err, GDN_DEVERR_PAGE);
+      b.table[(int64_t)r.slot[j] * c.max_pages + r.have[j] + (k - r.first[j])] = id;
     }
     // the tokens, each once: those of no sequence are left as they are
     if (positions != nullptr || rows != nullptr) {
@@ -320,7 +321,9 @@ __global__ void __launch_bounds__(kThreads)
     for (int64_t k = before + me; k < upto; k += step) {
       const int j = last_at_most(r.first, cnt, (int)k);
       int32_t *entry = b.table + (int64_t)r.slot[j] * c.max_pages + r.have[j] + ((int)k - r.first[j]);
-      b.free_pages[top + all - 1 - k] = *entry;
+      const int id = *entry;
+      if (id < 0 || id >= c.n_pages) raise_error(c.err, GDN_DEVERR_PAGE);
+      b.free_pages[top + all - 1 - k] = id;
       *entry = -1;
     }
     if (gridDim.x == 1 && drop > 0) b.held[r.slot[tid]] = r.have[tid];
@@ -374,19 +377,23 @@ gdn_status check_book(const gdn_kv *c, const gdn_kv_pages *b) {
   return GDN_OK;
 }
 
-// Host checks: slots in range and distinct, the book's counts possible, and
-// the lengths (cu: of positions starts[i], ... within a slot) in range.
+// Host checks: slots in range and distinct, the book's counts possible, the
+// lengths (cu: of positions starts[i], ... within a slot) in range, and so the
+// pages that change hands.
 gdn_status check_arrays(const gdn_kv *c, const gdn_kv_pages *b, const int32_t *slot_ids,
                         const int32_t *starts, const char *name, bool growing,
                         const int32_t *cu_seqlens, int n, int total, cudaStream_t s) {
   const gdn_kv_desc &d = c->desc;
-  std::vector<int32_t> slots, from, cu, held, count;
+  std::vector<int32_t> slots, from, cu, held, count, pages;
   gdn_status st;
   if ((st = fetch(slots, slot_ids, (size_t)n, s, "slot_ids")) ||
       (st = fetch(from, starts, (size_t)n, s, name)) ||
       (st = fetch(held, b->held, (size_t)d.n_slots, s, "held")) ||
-      (st = fetch(count, b->n_free, 1, s, "n_free")))
+      (st = fetch(count, b->n_free, 1, s, "n_free")) ||
+      (st = growing ? fetch(pages, b->free_pages, (size_t)d.n_pages, s, "free_pages")
+                    : fetch(pages, b->page_table, (size_t)d.n_slots * d.max_pages, s, "page_table")))
     return st;
+  const auto valid = [&](int32_t id) { return id >= 0 && id < d.n_pages; };
   if (count[0] < 0 || count[0] > d.n_pages)
     return fail(GDN_ERR_SIZE, "n_free = %d outside [0, %d]", count[0], d.n_pages);
   if (cu_seqlens) {
@@ -398,7 +405,7 @@ gdn_status check_arrays(const gdn_kv *c, const gdn_kv_pages *b, const int32_t *s
       return fail(GDN_ERR_SIZE, "cu_seqlens[%d] = %d, expected total_tokens %d", n, cu[n], total);
   }
   std::vector<unsigned char> seen((size_t)d.n_slots, 0);
-  int64_t back = count[0];
+  int64_t back = count[0], asked = 0, given = 0;
   for (int i = 0; i < n; ++i) {
     const int slot = slots[i];
     if (slot < 0 || slot >= d.n_slots)
@@ -411,8 +418,18 @@ gdn_status check_arrays(const gdn_kv *c, const gdn_kv_pages *b, const int32_t *s
     if (from[i] < 0 || (growing && from[i] + len > c->view.capacity()))
       return fail(GDN_ERR_SIZE, "%s[%d] = %d: outside the slot's %lld positions", name, i, from[i],
                   (long long)c->view.capacity());
-    const int64_t keep = ((int64_t)from[i] + d.page_tokens - 1) / d.page_tokens;
-    if (!growing && held[slot] > keep) back += held[slot] - keep;
+    const int64_t keep = ((int64_t)from[i] + len + d.page_tokens - 1) / d.page_tokens;
+    if (growing && len > 0 && keep > held[slot]) {
+      asked += keep - held[slot];
+      for (; asked <= count[0] && given < asked; ++given)
+        if (!valid(pages[count[0] - 1 - given]))
+          return fail(GDN_ERR_SIZE, "free_pages[%lld] = %d outside [0, %d)",
+                      (long long)(count[0] - 1 - given), pages[count[0] - 1 - given], d.n_pages);
+    }
+    for (int64_t col = keep; !growing && col < held[slot]; ++col, ++back)
+      if (!valid(pages[(size_t)slot * d.max_pages + col]))
+        return fail(GDN_ERR_SIZE, "page_table[%d][%lld] = %d outside [0, %d)", slot, (long long)col,
+                    pages[(size_t)slot * d.max_pages + col], d.n_pages);
   }
   if (back > d.n_pages)
     return fail(GDN_ERR_SIZE, "%lld pages would be free of %d", (long long)back, d.n_pages);

@@ -592,7 +592,9 @@ typedef struct {
  * range or named twice in the call (GDN_DEVERR_SLOT), with a malformed token range or
  * one that does not fit [0, max_pages * page_tokens) (GDN_DEVERR_SEQ), or whose held is
  * outside [0, max_pages] (GDN_DEVERR_PAGE).  An impossible *n_free counts as 0
- * (GDN_DEVERR_PAGE).  Needs no workspace; one launch. */
+ * (GDN_DEVERR_PAGE).  What free_pages holds is handed out as it is: an id outside
+ * [0, n_pages) gets its sequence an invalid page, and GDN_DEVERR_PAGE.  The outputs must
+ * not overlap the inputs.  Needs no workspace; one launch. */
 gdn_status gdn_kv_pages_grow(gdn_kv *kv, const gdn_kv_pages *pages, const int32_t *slot_ids,
                              const int32_t *pos, const int32_t *cu_seqlens, int32_t n_seqs,
                              int32_t total_tokens, int32_t *positions, int64_t *rows,
@@ -602,7 +604,9 @@ gdn_status gdn_kv_pages_grow(gdn_kv *kv, const gdn_kv_pages *pages, const int32_
  * use: 0 when a request ends, less than before when drafts were rejected.  Their
  * table entries become -1.  The pages go to the end of free_pages such that a
  * gdn_kv_pages_grow of the same sequences finds the same pages in the same
- * places.  Skipped: as above, and negative lengths (GDN_DEVERR_SEQ).  A call after
+ * places.  Skipped: as above, and negative lengths (GDN_DEVERR_SEQ).  A table entry that
+ * is no page goes to free_pages too, with GDN_DEVERR_PAGE: the caller takes it out
+ * before the next grow (with host_checks the call is refused).  A call after
  * which more than n_pages pages were free changes nothing (GDN_DEVERR_PAGE). */
 gdn_status gdn_kv_pages_trim(gdn_kv *kv, const gdn_kv_pages *pages, const int32_t *slot_ids,
                              const int32_t *lens, int32_t n_seqs, gdn_stream stream);

@@ -20,6 +20,10 @@ class PagesOracle:
             return None
         return slot
 
+    def _page(self, page):
+        if not 0 <= page < len(self.free):
+            self.err |= PAGE
+
     def grow(self, slot_ids, pos, cu, total, positions, rows):
         """positions, rows: arrays that are changed where a token belongs to a sequence.  Returns
         granted."""
@@ -53,6 +57,7 @@ class PagesOracle:
             granted.append(int(ok))
             for _ in range(need if ok else 0):
                 left -= 1
+                self._page(self.free[left])
                 self.table[slot, self.held[slot]] = self.free[left]
                 self.held[slot] += 1
             for t in range(t0, t1):
@@ -92,6 +97,7 @@ class PagesOracle:
         for slot, keep in drops:
             for col in range(keep, self.held[slot]):
                 at -= 1
+                self._page(self.table[slot, col])
                 self.free[at] = int(self.table[slot, col])
                 self.table[slot, col] = -1
             self.held[slot] = keep
