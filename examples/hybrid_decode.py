@@ -127,8 +127,21 @@ class Hybrid:
                           max_kv_len=longest_context)
         return o.view(n, nq) @ p["out"].T
 
+    def reserve(self, slots, pos, new):
+        """Pages for new[i] more tokens of slots[i], which holds pos[i]: True where there were
+        enough.  Where there were not, the request must not go into forward(): it would attend to
+        less than it was given.  It waits until others end, or ends itself."""
+        if self.pages is None:
+            return [True] * len(new)
+        cu = torch.tensor([0] + new, dtype=torch.int32).cumsum(0, dtype=torch.int32)
+        granted = torch.empty(len(new), dtype=torch.int32, device=self.device)
+        abi.gdn_kv_pages_grow(self.kv, self.pages, slots, pos, cu.to(self.device), sum(new),
+                              granted=granted)
+        return [bool(x) for x in granted.tolist()]
+
     def _positions(self, n, slots, pos, cu):
-        """Each new token's position; with pages of its own, the cache gets those the tokens need."""
+        """Each new token's position; with pages of its own, the cache gets those the tokens need
+        (reserve() has done that already where they may not suffice)."""
         if self.pages is not None:
             at = torch.empty(n, dtype=torch.int32, device=self.device)
             abi.gdn_kv_pages_grow(self.kv, self.pages, slots, pos, cu, positions=at)
@@ -165,32 +178,50 @@ class Hybrid:
         return abi.gdn_pool_get_error(self.pool) | abi.gdn_kv_get_error(self.kv)
 
 
-def serve(model, adapters=None):
-    """Three prompts and eight steps; adapters: the one of each request."""
+def serve(model, adapters=None, prompts=(100, 17, 64), steps=8):
+    """Three prompts, and `steps` more tokens of each; adapters: the one of each request.  Returns the
+    lengths that were reached, and prints them."""
     torch.manual_seed(0)
-    prompts = [100, 17, 64]
-    slots = torch.tensor([2, 0, 3], dtype=torch.int32, device="cuda")
-    abi.gdn_pool_reset(model.pool, slots)
-    cu = torch.tensor([0, 100, 117, 181], dtype=torch.int32, device="cuda")
-    pos = torch.zeros(3, dtype=torch.int32, device="cuda")
-    x = torch.randn(sum(prompts), HIDDEN, device="cuda").to(torch.bfloat16)
-    ids = packed = None
-    if adapters is not None:
-        ids = torch.tensor(adapters, dtype=torch.int32, device="cuda")
-        packed = torch.repeat_interleave(ids, torch.tensor(prompts, device="cuda"))
-    h = model.forward(x, slots, pos, cu, longest=max(prompts), longest_context=max(prompts),
-                      ids=packed)
-    h = h[cu[1:].long() - 1]
-    pos = pos + torch.tensor(prompts, dtype=torch.int32, device="cuda")
-    for step in range(8):
-        # a model would sample a token and embed it; here the state itself is fed back
-        h = torch.nn.functional.normalize(h.float(), dim=-1).mul(HIDDEN ** 0.5).to(torch.bfloat16)
-        h = model.forward(h, slots, pos, longest_context=max(prompts) + step + 1, ids=ids)
-        pos = pos + 1
-    model.release(slots, torch.zeros_like(pos))
-    torch.cuda.synchronize()
-    print("lengths", pos.tolist(), "norms", [round(float(v), 3) for v in h.float().norm(dim=-1)],
-          "errors", model.errors())
+    x = torch.randn(sum(prompts), HIDDEN, device="cuda").to(torch.bfloat16).split(list(prompts))
+    slots, adapters = [2, 0, 3], adapters or [None] * 3
+    lens, norms, waiting = [0] * 3, [0.0] * 3, [0, 1, 2]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    while waiting:
+        # the first of the waiting requests for which there are pages; the others come when these have ended
+        here = i32([slots[i] for i in waiting])
+        fits = model.reserve(here, torch.zeros_like(here), [prompts[i] for i in waiting])
+        batch = [i for i, ok in zip(waiting, fits) if ok]
+        if not batch:
+            raise RuntimeError("a prompt needs more pages than there are")
+        waiting = [i for i in waiting if i not in batch]
+        new = [prompts[i] for i in batch]
+        here, pos, ids, packed = i32([slots[i] for i in batch]), i32([0] * len(batch)), None, None
+        abi.gdn_pool_reset(model.pool, here)
+        cu = i32([sum(new[:k]) for k in range(len(new) + 1)])
+        if adapters[0] is not None:
+            ids = i32([adapters[i] for i in batch])
+            packed = torch.repeat_interleave(ids, i32(new))
+        h = model.forward(torch.cat([x[i] for i in batch]), here, pos, cu, longest=max(new),
+                          longest_context=max(new), ids=packed)
+        h, pos = h[cu[1:].long() - 1], i32(new)
+        for step in range(steps + 1):
+            fits = [False] * len(batch) if step == steps else model.reserve(here, pos, [1] * len(batch))
+            ended = [k for k, ok in enumerate(fits) if not ok]
+            if ended:  # at their full length, or because there is no page left
+                for k in ended:
+                    lens[batch[k]], norms[batch[k]] = int(pos[k]), float(h[k].float().norm())
+                model.release(here[ended], torch.zeros_like(pos[ended]))
+                rest = [k for k, ok in enumerate(fits) if ok]
+                batch, here, pos, h = [batch[k] for k in rest], here[rest], pos[rest], h[rest]
+                ids = None if ids is None else ids[rest]
+            if not batch:
+                break
+            # a model would sample a token and embed it; here the state itself is fed back
+            h = torch.nn.functional.normalize(h.float(), dim=-1).mul(HIDDEN ** 0.5).to(torch.bfloat16)
+            h = model.forward(h, here, pos, longest_context=max(prompts) + step + 1, ids=ids)
+            pos = pos + 1
+    print("lengths", lens, "norms", [round(v, 3) for v in norms], "errors", model.errors())
+    return lens
 
 
 def main():
