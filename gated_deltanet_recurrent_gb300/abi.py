@@ -1049,9 +1049,6 @@ def gdn_in_proj_adapted(pool: Pool, adapters: Adapters, x: torch.Tensor, w: torc
     if y is None:
         y = torch.empty(tokens, n_out, dtype=torch.float32, device=ids.device)
     ld_y = _proj_rows(y, tokens, n_out, device, "y")
-    if tokens <= 1:  # the stride of a single row says nothing, and has to be aligned
-        ld_y = -(-n_out // 8) * 8
-        ld_x = -(-hidden // 8) * 8
     status = _lib.gdn_in_proj_adapted(
         pool.handle, adapters.handle, tokens, x.data_ptr(), ld_x, w.data_ptr(), ld_w,
         ids.data_ptr(), y.data_ptr(), ld_y, _kv_dtype(y), stream.cuda_stream if stream is not None

@@ -20,9 +20,12 @@ namespace {
 
 using namespace gdn::host;
 
-// Rows of bf16 elements whose starts are 16-byte aligned.
-gdn_status check_rows(const void *p, int64_t *ld, int64_t width, const char *name) {
-  if (*ld == 0) *ld = width;
+// Rows of bf16 elements whose starts are 16-byte aligned.  (A single row has no stride.)
+gdn_status check_rows(const void *p, int64_t *ld, int64_t width, int64_t rows, const char *name) {
+  if (rows == 1)
+    *ld = (width + 7) / 8 * 8;
+  else if (*ld == 0)
+    *ld = width;
   if (*ld < width)
     return fail(GDN_ERR_ARG, "%s: row stride %lld smaller than a row of %lld", name,
                 (long long)*ld, (long long)width);
@@ -64,7 +67,8 @@ gdn_status gdn_adapters_create(const gdn_adapters_desc *d, const void *a, int64_
     return fail(GDN_ERR_UNSUPPORTED, "n_adapters * n_out and * rank must stay below 2^31 - 256");
   if (!a || !b || !scale) return fail(GDN_ERR_ARG, "a, b and scale must be non-NULL");
   gdn_status st;
-  if ((st = check_rows(a, &ld_a, d->hidden, "a")) || (st = check_rows(b, &ld_b, d->rank, "b")))
+  if ((st = check_rows(a, &ld_a, d->hidden, (int64_t)d->n_adapters * d->rank, "a")) ||
+      (st = check_rows(b, &ld_b, d->rank, (int64_t)d->n_adapters * d->n_out, "b")))
     return st;
   if ((uintptr_t)scale % 4) return fail(GDN_ERR_ARG, "scale must be 4-byte aligned");
   int dev = -1, sm_count = 0;
@@ -134,8 +138,10 @@ gdn_status gdn_in_proj_adapted(gdn_pool *p, gdn_adapters *ad, int64_t tokens, co
   if (!x || !w || !ids || !y) return fail(GDN_ERR_ARG, "x, w, ids and y must be non-NULL");
   const gdn_adapters_desc &d = ad->desc;
   gdn_status st;
-  if ((st = check_rows(x, &ld_x, d.hidden, "x")) || (st = check_rows(w, &ld_w, d.hidden, "w")))
+  if ((st = check_rows(x, &ld_x, d.hidden, tokens, "x")) ||
+      (st = check_rows(w, &ld_w, d.hidden, d.n_out, "w")))
     return st;
+  if (tokens == 1) ld_y = ((int64_t)d.n_out + 7) / 8 * 8;
   if (ld_y == 0) ld_y = d.n_out;
   if (ld_y < d.n_out) return fail(GDN_ERR_ARG, "y: row stride smaller than a row");
   if ((uintptr_t)y % 16 || (ld_y * (int64_t)dtype_size(y_dtype)) % 16)
