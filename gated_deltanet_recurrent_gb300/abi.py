@@ -939,6 +939,8 @@ def gdn_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor],
         raise GDNError(4, f"unsupported dtype {dtype}")
     if positions.dtype != torch.int32 or device < 0 or not positions.is_contiguous():
         raise GDNError(1, "positions must be a contiguous int32 tensor on the GPU")
+    if device != torch._C._cuda_getDevice():  # (the plan belongs to none: the launch goes there)
+        raise GDNError(1, f"the tensors are on GPU {device}, which is not the current one")
     if tokens:
         q_ptr = q_to = k_ptr = k_to = None
         ld_q = h_q = ld_q_to = ld_k = h_k = ld_k_to = 0
@@ -1004,6 +1006,9 @@ class Adapters:
 
 
 def gdn_adapters_create(desc: gdn_adapters_desc, a, ld_a, b, ld_b, scale):
+    # (the handle belongs to the current device, and its calls read a and b there)
+    if a.get_device() < 0 or a.get_device() != torch.cuda.current_device():
+        raise GDNError(1, "a, b and scale must be on the current GPU")
     out = ctypes.c_void_p()
     _check(load_library().gdn_adapters_create(ctypes.byref(desc), _ptr(a), ld_a, _ptr(b), ld_b,
                                               _ptr(scale), ctypes.byref(out)))
