@@ -794,9 +794,19 @@ class KVPages:
         self.page_table, self.held, self.free_pages, self.n_free = \
             kv.page_table, held, free_pages, n_free
         self.device = held.get_device()
+        self.sizes = d.n_slots, d.n_pages
         self.desc = gdn_kv_pages(kv.page_table.data_ptr(), held.data_ptr(),
                                  free_pages.data_ptr(), n_free.data_ptr())
         self.desc_ptr = ctypes.addressof(self.desc)
+
+
+def _book_of(kv, pages):
+    """The arrays' sizes are those of the cache that they were made for: another on the same page
+    table may have more slots or pages."""
+    d = kv.desc
+    if pages.sizes != (d.n_slots, d.n_pages):
+        raise GDNError(5, f"held and free_pages have {pages.sizes} entries, the cache has "
+                          f"{d.n_slots} slots and {d.n_pages} pages")
 
 
 def _like(t, name, dtype, size, device):
@@ -828,6 +838,7 @@ def gdn_kv_pages_grow(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, pos: 
             raise GDNError(1, "total_tokens is needed with cu_seqlens")
         tokens = slot_ids.numel()
     device = pages.device
+    _book_of(kv, pages)
     if _elsewhere(slot_ids, device) or _elsewhere(pos, device) or \
             (cu_seqlens is not None and _elsewhere(cu_seqlens, device)):
         raise GDNError(1, "slot_ids, pos and cu_seqlens must be on the cache's device")
@@ -846,6 +857,7 @@ def gdn_kv_pages_trim(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, lens:
                       stream=None):
     """Give back the pages that the first lens[i] tokens of slot slot_ids[i] do not use."""
     device = pages.device
+    _book_of(kv, pages)
     if _elsewhere(slot_ids, device) or _elsewhere(lens, device):
         raise GDNError(1, "slot_ids and lens must be on the cache's device")
     slots, starts, _, n = _kv_index(slot_ids, lens, None, slot_ids.numel(), "lens")
