@@ -465,6 +465,8 @@ gdn_status gdn_kv_pages_grow(gdn_kv *c, const gdn_kv_pages *b, const int32_t *sl
     return fail(GDN_ERR_ARG, "rows must be 8-byte aligned, positions and granted 4-byte");
   if (n_seqs == 0) return ok();
   if (!slot_ids || !pos) return fail(GDN_ERR_ARG, "slot_ids and pos must be non-NULL");
+  if (((uintptr_t)slot_ids | (uintptr_t)pos | (uintptr_t)cu_seqlens) % 4)
+    return fail(GDN_ERR_ARG, "slot_ids, pos and cu_seqlens must be 4-byte aligned");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (c->desc.host_checks &&
       ((st = check_host(c, b, slot_ids, pos, "pos", true, cu_seqlens, n_seqs, total_tokens, s)) ||
@@ -490,6 +492,8 @@ gdn_status gdn_kv_pages_trim(gdn_kv *c, const gdn_kv_pages *b, const int32_t *sl
   if (n_seqs > 65535) return fail(GDN_ERR_SIZE, "n_seqs = %d > 65535", n_seqs);
   if (n_seqs == 0) return ok();
   if (!slot_ids || !lens) return fail(GDN_ERR_ARG, "slot_ids and lens must be non-NULL");
+  if (((uintptr_t)slot_ids | (uintptr_t)lens) % 4)
+    return fail(GDN_ERR_ARG, "slot_ids and lens must be 4-byte aligned");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (c->desc.host_checks &&
       (st = check_host(c, b, slot_ids, lens, "lens", false, nullptr, n_seqs, 0, s)))

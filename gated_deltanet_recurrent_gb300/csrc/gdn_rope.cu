@@ -331,6 +331,7 @@ gdn_status gdn_rope(const gdn_rope_plan *p, int32_t tokens, const int32_t *posit
   const size_t es = dtype_size(dtype);
   if (tokens == 0 || h_q + h_k == 0) return ok();
   if (!positions) return fail(GDN_ERR_ARG, "positions is NULL");
+  if ((uintptr_t)positions % 4) return fail(GDN_ERR_ARG, "positions must be 4-byte aligned");
   gdn::RopeArgs a = {positions, {q, k}, {q_out, k_out}, {ld_q, ld_k}, {ld_q_out, ld_k_out},
                      {h_q, h_k}, tokens, r.d, r.rot / 2, 0, r.out_scale};
   gdn_status st;
