@@ -3,9 +3,9 @@
 //     a' = s (a cos - b sin),   b' = s (b cos + a sin).
 //
 // The angle is formed in turns and in whole numbers: theta_j / 2 pi is held as a 64-bit binary
-// fraction f_j, and p * f_j modulo 2^64 -- one wrapping product -- is the angle modulo a turn, exact
-// to 2^-65 p.  Far positions thus cost no precision and no 64-bit floats (whose rate here is a
-// sixtieth of the 32-bit one).  Its upper 24 bits go to sincospi, the rest is a first-order
+// fraction f_j, and p * f_j modulo 2^64 -- one wrapping product -- is the angle modulo a turn, off by
+// 2^-65 p and by p times what theta_j, a 64-bit float, is off by (2^-53 of it and a few more).  So the
+// product takes no 64-bit floats, whose rate here is a sixtieth of the 32-bit one.  Its upper 24 bits go to sincospi, the rest is a first-order
 // correction, so that sine and cosine are as good as their rounding to float32.
 //
 // HBM-bound: each head is read once and written once.  A CTA takes up to four tokens: it asks for the
