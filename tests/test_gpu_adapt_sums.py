@@ -14,10 +14,12 @@ squares add up to E[|e| u].  Normally distributed results of RMS 1 have E[u] = s
 2^(k+1)) 2^(k-7) = 4.5e-3."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
 from gated_deltanet_recurrent_gb300 import abi
+from oracle.adapt_oracle import adapted
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +83,30 @@ def test_bf16_roundings_of_few_tokens_are_those_of_the_exact_sum(pool, tokens, n
     y = torch.empty(tokens, n_out, device="cuda", dtype=torch.bfloat16)
     abi.gdn_in_proj_adapted(pool, ad, x, w, ids, y)
     assert off(y, want.bfloat16().double()) <= math.sqrt(4.5e-3 * cut_off(hidden / 16 / 4))
+
+
+@pytest.mark.parametrize("tokens", [3, 64, 200, 2100])
+@pytest.mark.parametrize("pattern", ["one", "two", "own"])
+def test_the_low_side_of_a_float32_result_keeps_24_bits(pool, tokens, pattern):
+    """Sums A x of up to 2^22 whole numbers, of which two bf16 parts hold 16 or 17 bits; everything is
+    exact: |w| <= 1 and x <= 32 over 2048 are 2^16 at most, and 3 B (A x) of 2^22 stay below 2^24."""
+    hidden, n_out, rank, n = 2048, 264, 3, 20
+    rng = np.random.default_rng(tokens)
+    x = rng.integers(0, 33, (tokens, hidden)).astype(np.float64)
+    a = rng.integers(0, 65, (n, rank, hidden)).astype(np.float64)
+    w = rng.integers(-1, 2, (n_out, hidden)).astype(np.float64)
+    b = rng.integers(-1, 2, (n, n_out, rank)).astype(np.float64)
+    ids = {"one": [4] * tokens, "two": [t % 2 for t in range(tokens)],
+           "own": [t % n for t in range(tokens)]}[pattern]
+    bf = lambda v: torch.from_numpy(v).float().cuda().bfloat16()
+    want, _, _ = adapted(x, w, a, b, np.ones(n), ids)
+    h = torch.from_numpy((x[0] @ a[ids[0]].T)).float()
+    rest = h - h.bfloat16().float()
+    assert (rest - rest.bfloat16().float()).abs().max() >= 1, "no third part"
+    assert np.abs(want).max() < 2 ** 24 and h.max() <= 2 ** 22
+    wide = torch.zeros(n, n_out, 8, device="cuda", dtype=torch.bfloat16)
+    wide[:, :, :rank] = bf(b)
+    y = torch.empty(tokens, n_out, device="cuda")
+    abi.gdn_in_proj_adapted(pool, abi.Adapters(bf(a), wide[:, :, :rank]), bf(x), bf(w),
+                            torch.tensor(ids, dtype=torch.int32, device="cuda"), y)
+    assert np.array_equal(y.double().cpu().numpy(), want)
