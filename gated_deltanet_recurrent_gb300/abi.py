@@ -764,6 +764,9 @@ def gdn_kv_attend(kv: KVCache, layer: int, slot_ids: torch.Tensor, kv_lens: torc
     return o
 
 
+_INT32 = 2 ** 31 - 1  # (larger sizes would be cut to 32 bits on their way to the library)
+
+
 def _elsewhere(t, device):
     """Whether t is not on the GPU of that index (-1: the host's memory)."""
     d = t.get_device()
@@ -837,6 +840,8 @@ def gdn_kv_pages_grow(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, pos: 
         if cu_seqlens is not None:
             raise GDNError(1, "total_tokens is needed with cu_seqlens")
         tokens = slot_ids.numel()
+    if tokens > _INT32:
+        raise GDNError(5, f"{tokens} tokens: more than 2^31 - 1")
     device = pages.device
     _book_of(kv, pages)
     if _elsewhere(slot_ids, device) or _elsewhere(pos, device) or \
@@ -949,6 +954,8 @@ def gdn_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor],
     code = _KV_DTYPES.get(dtype)
     if code is None:
         raise GDNError(4, f"unsupported dtype {dtype}")
+    if tokens > _INT32:
+        raise GDNError(5, f"{tokens} tokens: more than 2^31 - 1")
     if positions.dtype != torch.int32 or device < 0 or not positions.is_contiguous():
         raise GDNError(1, "positions must be a contiguous int32 tensor on the GPU")
     if device != torch._C._cuda_getDevice():  # (the plan belongs to none: the launch goes there)
@@ -985,6 +992,8 @@ class Adapters:
             raise GDNError(5, "a must be [n, rank, hidden] and b [n, n_out, rank]")
         n, self.rank, self.hidden = a.shape
         self.n_out = b.shape[1]
+        if max(n, self.rank, self.hidden, self.n_out) > _INT32:
+            raise GDNError(6, "a and b have sizes of 2^31 and more")
         if scale is None:
             scale = torch.ones(n, dtype=torch.float32, device=a.device)
         if scale.dtype != torch.float32 or scale.shape != (n,) or not scale.is_contiguous():

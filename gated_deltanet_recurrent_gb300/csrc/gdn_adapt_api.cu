@@ -61,6 +61,8 @@ gdn_status gdn_adapters_create(const gdn_adapters_desc *d, const void *a, int64_
   if (d->n_adapters < 1 || d->rank < 1 || d->hidden < 1 || d->n_out < 1)
     return fail(GDN_ERR_ARG, "adapter dimensions must be positive");
   if (d->rank > 128) return fail(GDN_ERR_UNSUPPORTED, "rank = %d (at most 128)", d->rank);
+  // (k runs up to some thousands behind hidden)
+  if (d->hidden > 1 << 30) return fail(GDN_ERR_UNSUPPORTED, "hidden = %d (at most 2^30)", d->hidden);
   // (rows of a and b are int32, and a tile's may lie up to 255 behind the last)
   if ((int64_t)d->n_adapters * d->n_out > INT32_MAX - 256 ||
       (int64_t)d->n_adapters * d->rank > INT32_MAX - 256)

@@ -196,7 +196,7 @@ cudaError_t launch(const Turns &f, const RopeArgs &a, cudaStream_t s) {
   // (few tokens: a CTA each, for the latency)
   const int per_cta = a.tokens >= 1024 * kRopeTokens ? kRopeTokens : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.tokens + per_cta - 1) / per_cta));
+  cfg.gridDim = dim3((unsigned)(((int64_t)a.tokens + per_cta - 1) / per_cta));
   cfg.blockDim = dim3((unsigned)x, (unsigned)(kRopeThreads / x));
   cfg.dynamicSmemBytes = sizeof(float2) * per_cta * a.pairs;
   cfg.stream = s;

@@ -679,7 +679,7 @@ gdn_status gdn_rope(const gdn_rope_plan *plan, int32_t tokens, const int32_t *po
  *   scale  [n_adapters]                 float32
  * the rows of one adapter following those of the other.  Rows start 16-byte aligned
  * (so ld_b is a multiple of 8; the stride of a single row is not looked at, here nor in
- * gdn_in_proj_adapted).  1 <= rank <= 128. */
+ * gdn_in_proj_adapted).  1 <= rank <= 128, hidden <= 2^30. */
 typedef struct {
   int32_t n_adapters;
   int32_t rank;
