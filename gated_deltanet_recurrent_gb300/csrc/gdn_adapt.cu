@@ -118,7 +118,7 @@ __device__ __forceinline__ int h_offset(int token, int byte) {
 template <int BT, int PITCH, int PARTS>
 __device__ __forceinline__ bool expand(const AdaptArgs &g, const Groups<BT> &s, const RingB &ring,
                                        int warp, int tok0, int live, unsigned char *hs, float *delta,
-                                       volatile int *abort_flag, uint32_t polls) {
+                                       volatile uint32_t *limit) {
   constexpr int W = PITCH == 32 ? 8 : 16, NL = PITCH / (4 * W), kWords = W / 4;
   constexpr int E = kSlots<PITCH>;
   static_assert(E % kTeams == 0, "a slot is always the same team's, which then is never two rounds ahead");
@@ -143,7 +143,7 @@ __device__ __forceinline__ bool expand(const AdaptArgs &g, const Groups<BT> &s, 
     for (int u = half * s.n + ((team - half * s.n) & (kTeams - 1)); good && u < (half + 1) * s.n;
          u += kTeams) {
       const int group = u - half * s.n, e = u % E;
-      if (!__all_sync(0xffffffffu, wait(&ring.full[e], (u / E) & 1, abort_flag, polls))) {
+      if (!__all_sync(0xffffffffu, wait(&ring.full[e], (u / E) & 1, limit))) {
         good = false;
         break;
       }
@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t full[S], empty[S], b_full[E], b_empty[E], list, done, taken,
       drain;
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_abort;
+  __shared__ uint32_t s_limit;  // of the waits
+  __shared__ int s_issued, s_issued_b[E];  // k-blocks and B tiles whose copies were started
   __shared__ float s_gone;  // SPLIT: another CTA of the cluster gave up
   __shared__ Groups<BT> s_groups;
   unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -238,14 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int all = (g.hidden + kBK - 1) / kBK;
   const int kb0 = (int)((int64_t)all * part / splits);
   const int plain = (int)((int64_t)all * (part + 1) / splits) - kb0;
-  // (test hooks: a barrier of one CTA waits for 16 bytes that no one sends)
-  const bool short_of = (blockIdx.x / splits + blockIdx.y) & 1 && part == splits - 1;
-  const uint32_t short_w = short_of && g.test_flags & GDN_TEST_ADAPT_WAIT_TIMEOUT ? 16 : 0;
-  const uint32_t short_b = short_of && g.test_flags & GDN_TEST_ADAPT_SIDE_TIMEOUT ? 16 : 0;
-  int issued = 0, issued_b = -1;  // k-blocks whose copies the producer has started; a lane's last B tile
   auto load_plain = [&](int kb) {
     const int s = kb % S;
-    mbar_arrive_expect_tx(&full[s], C::kStage + (kb == 0 ? short_w : 0));
+    mbar_arrive_expect_tx(&full[s], C::kStage);
     tma_load2(tile_w(s), &mw, (kb0 + kb) * kBK, n0, &full[s]);
     tma_load2(tile_x(s), &mx, (kb0 + kb) * kBK, tok0, &full[s]);
   };
@@ -262,9 +258,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&done, 1);
     mbar_init(&taken, kHelpers / 32);
     mbar_init(&drain, 1);
-    s_abort = 0;
+    s_limit = patience(g);
+    for (int e = 0; e < E; ++e) s_issued_b[e] = 0;
     s_gone = 0.f;
     mbar_fence_init();
+    // (test hooks: a barrier of one CTA waits for 16 bytes that no one sends)
+    if (g.test_flags != 0 && (blockIdx.x / splits + blockIdx.y) & 1 && part == splits - 1) {
+      if (g.test_flags & GDN_TEST_ADAPT_WAIT_TIMEOUT) mbar_expect_tx(&full[0], 16);
+      if (g.test_flags & GDN_TEST_ADAPT_SIDE_TIMEOUT) mbar_expect_tx(&b_full[0], 16);
+    }
     for (int kb = 0; kb < S && kb < plain; ++kb) load_plain(kb);  // nothing else is needed for these
   }
   // the adapter that all tokens of the tile have, -1 if none has any, -2 if it is mixed (adapters i
@@ -291,20 +293,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   // k-blocks before the last round of the accumulators, and in it
   const int rounds_before = C::kLong ? (kbs - 1) / C::kRound : 0, last = kbs - rounds_before * C::kRound;
   const int halves = g.rank_pad() * 2 / PITCH;
-  volatile int *abort_flag = &s_abort;
-  const uint32_t polls = patience(g);
+  volatile uint32_t *limit = &s_limit;
   const RingB ring{ring_b, b_full, b_empty};
   auto fail = [&]() {
-    *abort_flag = 1;
+    *limit = 0;
     raise_error(g.err, GDN_DEVERR_TIMEOUT);
   };
 
   if (warp == 0 && lane == 0) {
     // producer
-    issued = min(S, plain);
+    int issued = min(S, plain);
     for (int kb = issued; kb < kbs; ++kb) {
       const int s = kb % S;
-      if (kb >= S && !wait(&empty[s], ((kb / S) - 1) & 1, abort_flag, polls)) {
+      if (kb >= S && !wait(&empty[s], ((kb / S) - 1) & 1, limit)) {
         fail();
         break;
       }
@@ -323,10 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       issued = kb + 1;
     }
+    s_issued = issued;
   } else if (warp == 2 + kHelpers / 32) {
     // a lane per slot of the ring of B tiles
     if (one == -2) {
-      bool good = __all_sync(0xffffffffu, wait(&list, 0, abort_flag, polls));
+      bool good = __all_sync(0xffffffffu, wait(&list, 0, limit));
       const int units = good ? s_groups.n * halves : 0;
       int u = lane < E ? lane : units;
       uint32_t idle = 0;
@@ -336,16 +338,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int half = u >= s_groups.n, group = u - half * s_groups.n;
           const int row = s_groups.adapter[group] * g.n_out + n0;
           unsigned char *tile = ring_b + lane * (kBM * PITCH);
-          mbar_arrive_expect_tx(&b_full[lane], kBM * PITCH + (u == 0 ? short_b : 0));
+          mbar_arrive_expect_tx(&b_full[lane], kBM * PITCH);
           tma_load2(tile, &mu, half * (PITCH / 2), row, &b_full[lane]);
-          issued_b = u;
           u += E;
           moved = true;
         }
         idle = __any_sync(0xffffffffu, moved) ? 0 : idle + 1;
         if (idle > (1u << 24)) fail();  // seconds
-        if ((idle & 15) == 15) good = !__any_sync(0xffffffffu, *abort_flag != 0);
+        if ((idle & 15) == 15) good = !__any_sync(0xffffffffu, *limit == 0);
       }
+      if (lane < E) s_issued_b[lane] = u / E;
     }
   } else if (warp == 1 && lane == 0) {
     // MMA issuer
@@ -355,12 +357,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int kb = 0; kb < kbs; ++kb, ++in) {
       if (C::kLong && in == C::kRound) {
         tc::mma_commit(&done);
-        good = wait(&taken, round & 1, abort_flag, polls);
+        good = wait(&taken, round & 1, limit);
         tc::fence_after_sync();
         in = 0, ++round;
       }
       const int s = kb % S;
-      if (!good || !wait(&full[s], (kb / S) & 1, abort_flag, polls)) {
+      if (!good || !wait(&full[s], (kb / S) & 1, limit)) {
         good = false;
         break;
       }
@@ -395,17 +397,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           reinterpret_cast<float4 *>(delta + t * kPitch)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
       kv::dependent_wait();  // h
       if (!expand<BT, PITCH, C::kParts>(g, s_groups, ring, warp - 2, tok0, live, hs, delta,
-                                        abort_flag, polls))
+                                        limit))
         fail();
       helpers_sync<kHelpers>();
-      whole = *abort_flag == 0;
+      whole = *limit != 0;
     }
     // a lane per output row, the four warps of TMEM lanes 32 quad .. take turns in the columns
     const int quad = warp & 3, side = (warp - 2) >> 2, row = 32 * quad + lane, n = n0 + row;
     const uint32_t mine = tmem + ((uint32_t)(32 * quad) << 16);
     // the accumulators of a long sum, taken out
     for (int r = 0; C::kLong && whole && r < rounds_before; ++r) {
-      whole = __all_sync(0xffffffffu, wait(&done, r & 1, abort_flag, polls));
+      whole = __all_sync(0xffffffffu, wait(&done, r & 1, limit));
       if (!whole) {
         fail();
         break;
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // warp-uniform decision: tcgen05.ld is a whole-warp instruction
     const bool got =
-        __all_sync(0xffffffffu, whole && wait(&done, rounds_before & 1, abort_flag, polls));
+        __all_sync(0xffffffffu, whole && wait(&done, rounds_before & 1, limit));
     if (!got) {
       fail();
     } else {
@@ -471,15 +473,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (*abort_flag) {  // copies and products still in flight end before the CTA does
+  if (*limit == 0) {  // copies and products still in flight end before the CTA does
     if (tid == 0)
-      for (int kb = max(0, issued - S); kb < issued; ++kb)
-        mbar_wait_bounded(&full[kb % S], (kb / S) & 1, polls);
+      for (int kb = max(0, s_issued - S); kb < s_issued; ++kb)
+        mbar_wait_bounded(&full[kb % S], (kb / S) & 1, patience(g));
     if (tid == 32) {
       tc::mma_commit(&drain);
-      mbar_wait_bounded(&drain, 0, polls);
+      mbar_wait_bounded(&drain, 0, patience(g));
     }
-    if (issued_b >= 0) mbar_wait_bounded(&b_full[lane], (issued_b / E) & 1, polls);
+    if (warp == 2 + kHelpers / 32 && lane < E && s_issued_b[lane] > 0)
+      mbar_wait_bounded(&b_full[lane], (s_issued_b[lane] - 1) & 1, patience(g));
     __syncthreads();
   }
   if (warp == 1) {
@@ -489,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (SPLIT) {
     __syncwarp();
     if (warp < 2 || warp >= 2 + kHelpers / 32) cluster_wait();
-    if (*abort_flag)
+    if (*limit == 0)
       for (int p = 0; p < splits; ++p) st_peer(&s_gone, p, 1.f);
     cluster_arrive();
     cluster_wait();

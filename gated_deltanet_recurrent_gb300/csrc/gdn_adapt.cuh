@@ -67,20 +67,18 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
 }
 
 // Polls of a bounded wait (of up to a microsecond or two each): what one step of any role may take grows
-// with hidden, and is some 50 ns for each of it where a tile's results are all computed again.
+// with hidden.
 __device__ __forceinline__ uint32_t patience(const AdaptArgs &g) {
   if (g.test_flags & (GDN_TEST_ADAPT_WAIT_TIMEOUT | GDN_TEST_ADAPT_SIDE_TIMEOUT)) return 1u << 11;
   return (1u << 20) + 64u * (uint32_t)min(g.hidden, 1 << 24);
 }
 
-// A bounded wait that also ends when the CTA gives up.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                     uint32_t polls) {
-  for (uint32_t it = 0; it < polls; ++it) {
+// A bounded wait that also ends when the CTA gives up, which sets its limit to 0.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile uint32_t *limit) {
+  for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 15) == 15 && *abort_flag) return false;
+    if ((it & 15) == 0 && it >= *limit) return false;
   }
-  return false;
 }
 
 // The helpers, HELPERS threads from warp 2 on, do the adapters' part of mixed tiles and the epilogue.

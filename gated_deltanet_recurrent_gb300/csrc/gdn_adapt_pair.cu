@@ -15,9 +15,9 @@
 // tile have one adapter (most of a prompt) that is all.  In a mixed tile every adapter has its own
 // k-blocks, with a plane of h that has zeros for the other tokens.  A result that is not finite may then
 // come from another request's adapter (0 * inf), and is computed again from its own, so that nothing of
-// one adapter reaches another's tokens: 32 outputs of 16 tokens at a time, by mma.sync.  (Where every result
-// of every tile is: 5000 bf16 tokens, eight adapters of rank 32, 2048 -> 1296, 108 -> 650 us; 600 tokens ->
-// 40960 161 -> 2040; these are loads of W from L2, once per 16 tokens.)  For more than eight adapters in a tile
+// one adapter reaches another's tokens: after a warp's last tile, 32 outputs of 16 tokens at a time, by
+// mma.sync.  (Where every result of every tile is: 5000 bf16 tokens, eight adapters of rank 32, 2048 -> 1296,
+// 110 -> 633 us; 600 tokens -> 40960 161 -> 2180; these are loads of W from L2, once per 16 tokens.)  For more than eight adapters in a tile
 // the helpers multiply B and h with mma.sync: four warps with 32 output rows each take the tasks
 // (up to eight tokens of one adapter) in turn, with B and h from global memory, and store them to TMEM
 // columns of their own, [token][row], which the epilogue adds.  For a bf16 y these are the columns of
@@ -396,25 +396,42 @@ __device__ __forceinline__ void store_results(const AdaptArgs &g, bf16 *y, int t
   store_rows(y + (int64_t)tok * g.ld_y, g.ld_y, n, g.n_out, live, v);
 }
 
-// Steps `odd` of a tile's results, some of which are not finite: those are computed again, and all stored
-// again.  (By itself: what is kept over the calls would cost the kernel registers.)
+__device__ __forceinline__ float result(float v) { return v; }
+__device__ __forceinline__ float result(bf16 v) { return __bfloat162float(v); }
+
+// After a warp's last tile, if there were results that are not finite in mixed tiles: they are computed
+// again, of the `stored` tiles.  (Within the loop over the tiles the call would cost it registers, and the
+// products would wait.)
 template <typename TO>
-__device__ __noinline__ void results_again(const AdaptArgs &g, const int *list, int count, int row0,
-                                           int tok0, int live, uint32_t odd, uint32_t acc,
-                                           uint32_t delta, float *own) {
+__device__ __noinline__ void results_again(const AdaptArgs &g, int stored, int *list, float *own) {
   using C = Cfg<TO>;
-  const int lane = threadIdx.x & 31;
-  const int kbs = (g.hidden + kBK - 1) / kBK + count * ((g.rank + kBK - 1) / kBK) * C::kParts;
-  for (; odd != 0; odd &= odd - 1) {
-    const int c = 16 * (__ffs(odd) - 1);
-    again<C::kParts>(g, list, count, row0, tok0 + c, min(16, live - c), own);
-    float v[32];
-    load_results<TO>(acc, delta, C::kF32 && kbs > C::kRound, kbs, c, v);
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (c + j < live && !(fabsf(v[j]) < INFINITY)) v[j] = own[j * 33 + lane];
-    store_results(g, static_cast<TO *>(g.y), tok0 + c, live - c, row0 + lane, v);
+  const int lane = threadIdx.x & 31, quad = threadIdx.x >> 5 & 3, side = ((int)(threadIdx.x >> 5) - 2) >> 2;
+  const int n_tiles = (g.n_out + 2 * kBM - 1) / (2 * kBM);
+  TO *y = static_cast<TO *>(g.y);
+  int64_t t = blockIdx.x >> 1;
+  for (int i = 0; i < stored; ++i, t += gridDim.x >> 1) {
+    const int tok0 = (int)(t / n_tiles) * C::BT, live = min(C::BT, g.tokens - tok0);
+    const int row0 = (int)(t % n_tiles) * 2 * kBM + (int)cluster_rank() * kBM + 32 * quad;
     __syncwarp();
+    const int count = tile_groups(g, tok0, live, list);
+    __syncwarp();
+    if (row0 >= g.n_out || count == 0 || count > kPlanes) continue;
+    bool whole = true;  // no token without an adapter
+    for (int j = lane; j < live; j += 32) whole = whole && token_id(g, tok0 + j) >= 0;
+    if (count == 1 && __all_sync(0xffffffffu, whole)) continue;
+    for (int c = 16 * side; c < live; c += 16 * kTeams) {
+      TO *at = y + (int64_t)(tok0 + c) * g.ld_y + min(row0 + lane, g.n_out - 1);
+      const int steps = min(16, live - c);
+      bool finite = true;
+      for (int j = 0; j < steps; ++j) finite = finite && fabsf(result(at[j * g.ld_y])) < INFINITY;
+      if (__all_sync(0xffffffffu, finite)) continue;
+      again<C::kParts>(g, list, count, row0, tok0 + c, steps, own);
+      if (row0 + lane < g.n_out)
+        for (int j = 0; j < steps; ++j)
+          if (!(fabsf(result(at[j * g.ld_y])) < INFINITY))
+            Elem<TO>::store1(at + j * g.ld_y, own[j * 33 + lane]);
+      __syncwarp();
+    }
   }
 }
 
@@ -441,9 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], info_full[kInfo],
       info_empty[kInfo], round_full, round_taken, drain;
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_abort, s_info[kInfo], s_list[kInfo][kPlanes];
+  __shared__ uint32_t s_limit;  // of the waits
+  __shared__ int s_info[kInfo], s_list[kInfo][kPlanes], s_again[kWarps][kPlanes];
   __shared__ float s_gone;      // one of the two gave up
-  __shared__ int64_t s_issued;  // in CTA 0: k-blocks whose copies the other has started
+  __shared__ int64_t s_issued, s_other;  // k-blocks whose copies were started, here and (CTA 0) by the other
   __shared__ Groups<BT> s_groups;
   unsigned char *smem = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~uintptr_t(1023));
@@ -458,9 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int plain = (g.hidden + kBK - 1) / kBK, chunks = (g.rank + kBK - 1) / kBK;
   // (test hooks: in every other pair a barrier waits for what no one sends, CTA 0's first copies', or that
   // of the first tile's adapters in CTA 0 or 1)
-  const bool short_w = g.test_flags & GDN_TEST_ADAPT_WAIT_TIMEOUT && pair & 1;
-  const bool short_side = g.test_flags & GDN_TEST_ADAPT_SIDE_TIMEOUT && pair & 1 && (pair >> 1 & 1) == rank;
-  int64_t issued = 0;  // k-blocks whose copies this CTA's producer has started
+  const uint32_t hook = pair & 1 ? g.test_flags : 0;
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -471,15 +487,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_empty[b], 2 * kWarps);
     }
     for (int i = 0; i < kInfo; ++i) {
-      mbar_init(&info_full[i], short_side && i == 0 ? 2 : 1);
+      mbar_init(&info_full[i], i == 0 && hook & GDN_TEST_ADAPT_SIDE_TIMEOUT && (pair >> 1 & 1) == rank ? 2 : 1);
       mbar_init(&info_empty[i], kWarps);
     }
     mbar_init(&round_full, 1);
     mbar_init(&round_taken, 2 * kWarps);
     mbar_init(&drain, 1);
-    s_abort = 0;
+    s_limit = patience(g);
     s_gone = 0.f;
     mbar_fence_init();
+    if (hook & GDN_TEST_ADAPT_WAIT_TIMEOUT) mbar_expect_tx(&full[0], 16);
   }
   __syncwarp();
   if (warp == 1) {
@@ -494,16 +511,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // the other CTA's barriers are there
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  volatile int *abort_flag = &s_abort;
-  const uint32_t polls = patience(g);
+  volatile uint32_t *limit = &s_limit;
   auto fail = [&]() {
-    *abort_flag = 1;
+    *limit = 0;
     raise_error(g.err, GDN_DEVERR_TIMEOUT);
   };
   // the adapter that all tokens of the pair's i-th tile have, or -1: none has any, kMany: more than there
   // are planes for, kGaveUp: a wait did, kMixed - n: n (s_list)
   auto tile_info = [&](int i) {
-    if (!wait(&info_full[i % kInfo], (i / kInfo) & 1, abort_flag, polls)) return kGaveUp;
+    if (!wait(&info_full[i % kInfo], (i / kInfo) & 1, limit)) return kGaveUp;
     return *reinterpret_cast<volatile int *>(&s_info[i % kInfo]);
   };
 
@@ -511,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // producer
     int s = 0;
     uint32_t round = 0;
+    int64_t u = 0;
     bool good = true, waited = false;
     int i = 0;
     for (int64_t t = pair; t < tiles && good; t += pairs, ++i) {
@@ -522,15 +539,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       const int kbs = plain + adapters_of(one) * chunks * C::kParts;
-      for (int kb = 0; kb < kbs; ++kb, ++issued, s = s + 1 == S ? 0 : s + 1) {
-        if (s == 0 && issued > S) round ^= 1;  // (the first round waits for nothing, the second for phase 0)
-        if (issued >= S && !wait(&empty[s], round, abort_flag, polls)) {
+      for (int kb = 0; kb < kbs; ++kb, ++u, s = s + 1 == S ? 0 : s + 1) {
+        if (s == 0 && u > S) round ^= 1;  // (the first round waits for nothing, the second for phase 0)
+        if (u >= S && !wait(&empty[s], round, limit)) {
           good = false;
           break;
         }
         const uint32_t bar = leader_addr(&full[s]);
-        if (rank == 0)
-          mbar_arrive_expect_tx(&full[s], 2 * C::kStage + (short_w && issued == 0 ? 16 : 0));
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
         if (kb < plain) {
           tma_load2_pair(tile_w(s), &mw, kb * kBK, n0, bar);
           tma_load2_pair(tile_x(s), &mx, kb * kBK, tok0, bar);
@@ -549,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    s_issued = u;
     if (!good) fail();
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // MMA issuer
@@ -563,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The accumulators' columns are free once the epilogue of tile i - 2 is done, or of tile i - 1
       // where they are the same or held its adapters' part.
       auto free_after = [&](int last) {
-        return last < 0 || wait(&acc_empty[last & 1], (uint32_t)((last >> 1) & 1), abort_flag, polls);
+        return last < 0 || wait(&acc_empty[last & 1], (uint32_t)((last >> 1) & 1), limit);
       };
       if (one == kGaveUp || !free_after(C::kF32 || before == kMany ? i - 1 : i - 2)) {
         good = false;
@@ -577,14 +594,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto block = [&](int steps) {
         if (C::kF32 && in == C::kRound) {
           commit_pair(&round_full);
-          if (!wait(&round_taken, rounds++ & 1, abort_flag, polls)) return false;
+          if (!wait(&round_taken, rounds++ & 1, limit)) return false;
           tc::fence_after_sync();
           turn = in = 0;
         }
         const uint32_t acc = base + (uint32_t)turn * BT;
         const bool fresh = in++ < C::kAcc;
         turn = turn + 1 == C::kAcc ? 0 : turn + 1;
-        if (!wait(&full[s], round, abort_flag, polls)) return false;
+        if (!wait(&full[s], round, limit)) return false;
         tc::fence_after_sync();
         const uint32_t a = smem_addr(tile_w(s)), b = smem_addr(tile_x(s));
 #pragma unroll
@@ -612,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok0 = (int)(t / n_tiles) * BT, live = min(BT, g.tokens - tok0);
       if (i >= kInfo)
         good = __all_sync(0xffffffffu,
-                          wait(&info_empty[i % kInfo], ((i / kInfo) - 1) & 1, abort_flag, polls));
+                          wait(&info_empty[i % kInfo], ((i / kInfo) - 1) & 1, limit));
       if (!good) break;
       const int n = tile_groups(g, tok0, live, s_list[i % kInfo]);
       bool whole = true;  // no token without an adapter
@@ -633,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     TO *y = static_cast<TO *>(g.y);
     int i = 0;
     uint32_t rounds = 0;
-    bool good = true;
+    bool good = true, odd = false;  // odd: mixed tiles had results that are not finite
+    int stored = 0;
     for (int64_t t = pair; t < tiles; t += pairs, ++i) {
       const int tok0 = (int)(t / n_tiles) * BT, live = min(BT, g.tokens - tok0);
       const int n0 = (int)(t % n_tiles) * 2 * kBM + rank * kBM, n = n0 + 32 * quad + lane;
@@ -672,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kbs = plain + adapters_of(one) * chunks * C::kParts;
       if constexpr (C::kF32)
         for (int k = C::kRound; k < kbs && good; k += C::kRound, ++rounds) {
-          good = __all_sync(0xffffffffu, wait(&round_full, rounds & 1, abort_flag, polls));
+          good = __all_sync(0xffffffffu, wait(&round_full, rounds & 1, limit));
           if (!good) break;
           tc::fence_after_sync();
 #pragma unroll 1
@@ -696,29 +714,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive_leader(&round_taken);
         }
       good = good &&
-             __all_sync(0xffffffffu, wait(&acc_full[i & 1], (i >> 1) & 1, abort_flag, polls));
+             __all_sync(0xffffffffu, wait(&acc_full[i & 1], (i >> 1) & 1, limit));
       if (!good) {
         fail();
         continue;
       }
       tc::fence_after_sync();
       const bool summed = one == kMany || (C::kF32 && kbs > C::kRound);
-      uint32_t odd = 0;  // steps with results that are not finite
 #pragma unroll 1
       for (int c = 16 * side; c < live; c += 16 * kTeams) {
         float v[32];
         load_results<TO>(acc, delta, summed, kbs, c, v);
         if (one <= kMixed) {
-          bool finite = true;
+          // (rows and columns that are not there count too: there is only more looked at again)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) finite = finite && (c + j >= live || fabsf(v[j]) < INFINITY);
-          if (!__all_sync(0xffffffffu, finite || n >= g.n_out)) odd |= 1u << (c / 16);
+          for (int j = 0; j < 16; ++j) odd = odd || !(fabsf(v[j]) < INFINITY);
         }
         store_results(g, y, tok0 + c, live - c, n, v);
       }
-      if (odd != 0)
-        results_again<TO>(g, s_list[i % kInfo], kMixed - one, n0 + 32 * quad, tok0, live, odd, acc, delta,
-                          scratch + (warp - 2) * 16 * 33);
+      ++stored;
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) {
@@ -726,30 +740,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive_leader(&acc_empty[i & 1]);
       }
     }
+    if (__any_sync(0xffffffffu, odd))
+      results_again<TO>(g, stored, s_again[warp - 2], scratch + (warp - 2) * 16 * 33);
   }
   // (the leader's products read the other CTA's shared memory, and its commits arrive there)
   tc::fence_before_sync();
   __syncthreads();
-  if (tid == 0) {
-    if (rank == 1) st_peer64(&s_issued, 0, issued);
-    if (*abort_flag)
-      for (int p = 0; p < 2; ++p) st_peer(&s_gone, p, 1.f);
-  }
+  if (tid == 0 && *limit == 0)
+    for (int p = 0; p < 2; ++p) st_peer(&s_gone, p, 1.f);
   cluster_sync();
   if (s_gone != 0.f) {  // copies and products still in flight end before the pair does
+    if (rank == 1 && tid == 0) st_peer64(&s_other, 0, s_issued);
+    cluster_sync();
     if (tid == 32) {
       if (rank == 0) commit_pair(&drain);
-      mbar_wait_bounded(&drain, 0, polls);
+      mbar_wait_bounded(&drain, 0, patience(g));
     }
     if (rank == 0 && tid == 0) {
       // The two may have stopped at different k-blocks.  Of what both started, CTA 0's barriers await both;
       // of what only one did, its half: CTA 0 awaits the other's too, or nothing yet.
-      const int64_t both = min(issued, s_issued), any = max(issued, s_issued);
+      const int64_t both = min(s_issued, s_other), any = max(s_issued, s_other);
       for (int64_t q = max((int64_t)0, both - S); q < any; ++q) {
         uint64_t *bar = &full[q % S];
-        if (q >= both && issued > both) complete_tx(bar, C::kStage);
-        if (q >= both && issued == both) mbar_arrive_expect_tx(bar, C::kStage);
-        mbar_wait_bounded(bar, (uint32_t)((q / S) & 1), polls);
+        if (q >= both && s_issued > both) complete_tx(bar, C::kStage);
+        if (q >= both && s_issued == both) mbar_arrive_expect_tx(bar, C::kStage);
+        mbar_wait_bounded(bar, (uint32_t)((q / S) & 1), patience(g));
       }
     }
     cluster_sync();

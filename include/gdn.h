@@ -710,7 +710,7 @@ gdn_status gdn_adapters_destroy(gdn_adapters *adapters);
  * 960 products, so that it is some 1e-6 off at most at any hidden size; a bf16 y, that is 2e-6
  * off over 2048 before its rounding (5e-7 in calls of few tokens), shows none of it.  An adapter
  * with values that are not finite spoils its own tokens only; in calls of many tokens others near
- * them are then summed up in another order, and the call takes up to some 13 times as long.  An id outside
+ * them are then summed up in another order, and the call takes up to some 14 times as long.  An id outside
  * [-1, n_adapters) counts as -1 (GDN_DEVERR_ADAPTER).  The pool supplies the error
  * word.  tokens <= 2^18.  Calls from several host threads on one handle must be
  * serialised by the caller. */
