@@ -797,7 +797,7 @@ class KVPages:
         self.page_table, self.held, self.free_pages, self.n_free = \
             kv.page_table, held, free_pages, n_free
         self.device = held.get_device()
-        self.sizes = d.n_slots, d.n_pages
+        self.kv, self.sizes = kv, (d.n_slots, d.n_pages)
         self.desc = gdn_kv_pages(kv.page_table.data_ptr(), held.data_ptr(),
                                  free_pages.data_ptr(), n_free.data_ptr())
         self.desc_ptr = ctypes.addressof(self.desc)
@@ -806,6 +806,8 @@ class KVPages:
 def _book_of(kv, pages):
     """The arrays' sizes are those of the cache that they were made for: another on the same page
     table may have more slots or pages."""
+    if kv is pages.kv:
+        return
     d = kv.desc
     if pages.sizes != (d.n_slots, d.n_pages):
         raise GDNError(5, f"held and free_pages have {pages.sizes} entries, the cache has "
@@ -874,6 +876,17 @@ def gdn_kv_pages_trim(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, lens:
 
 
 # ------------------------------------------------------------ rotary positions
+
+_devices = 0
+
+
+def _current(device):
+    """Whether that GPU is the current one.  (Where there is only one it is; asking takes longer.)"""
+    global _devices
+    if not _devices:
+        _devices = torch.cuda.device_count()
+    return _devices == 1 or torch._C._cuda_getDevice() == device
+
 
 _ROPE_LAYOUTS = {"half": GDN_ROPE_HALF, "interleaved": GDN_ROPE_INTERLEAVED}
 
@@ -958,7 +971,7 @@ def gdn_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor],
         raise GDNError(5, f"{tokens} tokens: more than 2^31 - 1")
     if positions.dtype != torch.int32 or device < 0 or not positions.is_contiguous():
         raise GDNError(1, "positions must be a contiguous int32 tensor on the GPU")
-    if device != torch._C._cuda_getDevice():  # (the plan belongs to none: the launch goes there)
+    if not _current(device):  # (the plan belongs to none: the launch goes there)
         raise GDNError(1, f"the tensors are on GPU {device}, which is not the current one")
     if tokens:
         q_ptr = q_to = k_ptr = k_to = None

@@ -61,7 +61,7 @@ CALLS = [(1, 5120), (64, 12352), (64, 2048), (256, 5120), (96, 12352), (2049, 10
 @pytest.mark.parametrize("hidden", [512, 960, 2048, 8192, 16384, 32768])
 @pytest.mark.parametrize("pattern", ["none", "one", "three", "own"])
 def test_float32_sums_of_any_length(pool, tokens, n_out, hidden, pattern):
-    if pattern in ("three", "own") and hidden not in (2048, 16384):
+    if pattern in ("three", "own") and hidden not in (2048, 16384, 32768):
         return
     n = 12
     t = torch.arange(tokens, device="cuda", dtype=torch.int32)
