@@ -806,8 +806,6 @@ class KVPages:
 def _book_of(kv, pages):
     """The arrays' sizes are those of the cache that they were made for: another on the same page
     table may have more slots or pages."""
-    if kv is pages.kv:
-        return
     d = kv.desc
     if pages.sizes != (d.n_slots, d.n_pages):
         raise GDNError(5, f"held and free_pages have {pages.sizes} entries, the cache has "
@@ -845,7 +843,8 @@ def gdn_kv_pages_grow(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, pos: 
     if tokens > _INT32:
         raise GDNError(5, f"{tokens} tokens: more than 2^31 - 1")
     device = pages.device
-    _book_of(kv, pages)
+    if kv is not pages.kv:
+        _book_of(kv, pages)
     if _elsewhere(slot_ids, device) or _elsewhere(pos, device) or \
             (cu_seqlens is not None and _elsewhere(cu_seqlens, device)):
         raise GDNError(1, "slot_ids, pos and cu_seqlens must be on the cache's device")
@@ -864,7 +863,8 @@ def gdn_kv_pages_trim(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, lens:
                       stream=None):
     """Give back the pages that the first lens[i] tokens of slot slot_ids[i] do not use."""
     device = pages.device
-    _book_of(kv, pages)
+    if kv is not pages.kv:
+        _book_of(kv, pages)
     if _elsewhere(slot_ids, device) or _elsewhere(lens, device):
         raise GDNError(1, "slot_ids and lens must be on the cache's device")
     slots, starts, _, n = _kv_index(slot_ids, lens, None, slot_ids.numel(), "lens")
@@ -877,15 +877,21 @@ def gdn_kv_pages_trim(kv: KVCache, pages: KVPages, slot_ids: torch.Tensor, lens:
 
 # ------------------------------------------------------------ rotary positions
 
-_devices = 0
+_only = None  # the GPU's index where there is one only, as soon as that is known
 
 
-def _current(device):
-    """Whether that GPU is the current one.  (Where there is only one it is; asking takes longer.)"""
-    global _devices
-    if not _devices:
-        _devices = torch.cuda.device_count()
-    return _devices == 1 or torch._C._cuda_getDevice() == device
+def _rope_positions(positions, tokens, device):
+    """Refuses positions that cannot be.  The plan belongs to no device: the launch goes to the
+    current one, on which they have to be."""
+    global _only
+    if positions.dtype != torch.int32 or device < 0 or not positions.is_contiguous():
+        raise GDNError(1, "positions must be a contiguous int32 tensor on the GPU")
+    if tokens > _INT32:
+        raise GDNError(5, f"{tokens} tokens: more than 2^31 - 1")
+    if device != torch._C._cuda_getDevice():
+        raise GDNError(1, f"the tensors are on GPU {device}, which is not the current one")
+    if torch.cuda.device_count() == 1:
+        _only = device
 
 
 _ROPE_LAYOUTS = {"half": GDN_ROPE_HALF, "interleaved": GDN_ROPE_INTERLEAVED}
@@ -967,12 +973,9 @@ def gdn_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor],
     code = _KV_DTYPES.get(dtype)
     if code is None:
         raise GDNError(4, f"unsupported dtype {dtype}")
-    if tokens > _INT32:
-        raise GDNError(5, f"{tokens} tokens: more than 2^31 - 1")
-    if positions.dtype != torch.int32 or device < 0 or not positions.is_contiguous():
-        raise GDNError(1, "positions must be a contiguous int32 tensor on the GPU")
-    if not _current(device):  # (the plan belongs to none: the launch goes there)
-        raise GDNError(1, f"the tensors are on GPU {device}, which is not the current one")
+    if positions.dtype != torch.int32 or device != _only or not positions.is_contiguous() or \
+            tokens > 0x7fffffff:
+        _rope_positions(positions, tokens, device)
     if tokens:
         q_ptr = q_to = k_ptr = k_to = None
         ld_q = h_q = ld_q_to = ld_k = h_k = ld_k_to = 0

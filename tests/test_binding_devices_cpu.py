@@ -32,7 +32,8 @@ def current(monkeypatch):
     """GPU 1 is the current one, and the library fails the test."""
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    monkeypatch.setattr(abi, "_devices", 3)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 3)
+    monkeypatch.setattr(abi, "_only", None)
     lib = types.SimpleNamespace(gdn_rope=launched, gdn_adapters_create=launched)
     monkeypatch.setattr(abi, "_lib", lib)
     monkeypatch.setattr(abi, "load_library", lambda: lib)

@@ -58,7 +58,7 @@ def nothing_launched(monkeypatch):
     monkeypatch.setattr(abi, "load_library", lambda: lib)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(abi, "_devices", 1)
+    monkeypatch.setattr(abi, "_only", 0)
 
 
 @pytest.mark.parametrize("a,b", [((2 ** 32 + 1, 8, 64), (2 ** 32 + 1, 16, 8)),
