@@ -29,9 +29,9 @@
 // kernel starts under the low side's: W and B are on their way before h is complete.  Every wait is
 // bounded (GDN_DEVERR_TIMEOUT).
 //
-// Measured with the low side: one token, 2048 -> 5120, rank 16, 10.7 us (latency; its bytes take 3.1);
-// 64 tokens with an adapter each, 2048 -> 12352, rank 16, 19.5 us on warm and 21.7 on cold weights (82 MB:
-// 12.1), rank 64 39.5 (25.1), without adapters 17.5 (7.7).  Narrower tiles, one for each SM, take as long.
+// Measured with the low side: one token, 2048 -> 5120, rank 16, 10.9 us (latency; its bytes take 3.1);
+// 64 tokens with an adapter each, 2048 -> 12352, rank 16, 20.9 us on warm and 22.1 on cold weights (82 MB:
+// 12.1), rank 64 39.9 (25.1), without adapters 18.0 (7.7).  Narrower tiles, one for each SM, take as long.
 #include "gdn_adapt.cuh"
 
 namespace gdn {

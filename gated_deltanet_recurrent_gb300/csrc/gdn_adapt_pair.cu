@@ -27,9 +27,9 @@
 // tensor core, whose operands take all of the shared memory's bandwidth: 15 us for a tile of 256 tokens
 // with two adapters, whose k-blocks take 4.)
 //
-// Bound by the tensor pipe, 78 % active: 16384 tokens, 2048 -> 12352, in 487 us without adapters (1.70
-// PFLOP/s), 558 in prompts of 1100 with adapters of rank 64 (of which the low side some 50), 708 in runs of
-// 50.  777 float32 tokens in runs of 50, 2048 -> 5120: 46.0 us, a tile and its epilogue one after the other.
+// Bound by the tensor pipe, 79 % active: 16384 tokens, 2048 -> 12352, in 488 us without adapters (1.70
+// PFLOP/s), 555 in prompts of 1100 with adapters of rank 64 (of which the low side some 50), 706 in runs of
+// 50.  777 float32 tokens in runs of 50, 2048 -> 5120: 47.0 us, a tile and its epilogue one after the other.
 #include "gdn_adapt.cuh"
 
 namespace gdn {

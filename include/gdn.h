@@ -707,8 +707,8 @@ gdn_status gdn_adapters_destroy(gdn_adapters *adapters);
  * multiplied by scale; it enters the second product in two bf16 parts (to 2^-16 of
  * itself) for bf16 y and in three (2^-24) for float32 y; y is rounded once.  The tensor
  * cores' float32 sums are cut off, not rounded: those of a float32 y are begun anew every
- * 960 products, so that it is some 1e-6 off at most at any hidden size; a bf16 y, that is 2e-6
- * off over 2048 before its rounding (5e-7 in calls of few tokens), shows none of it.  An adapter
+ * 960 products, so that it is some 1e-6 off at most at any hidden size; a bf16 y is 2e-6 off
+ * over 2048 before its rounding of 2^-9 (5e-7 in calls of few tokens), more with more.  An adapter
  * with values that are not finite spoils its own tokens only; in calls of many tokens others near
  * them are then summed up in another order, and the call takes up to some 14 times as long.  An id outside
  * [-1, n_adapters) counts as -1 (GDN_DEVERR_ADAPTER).  The pool supplies the error
