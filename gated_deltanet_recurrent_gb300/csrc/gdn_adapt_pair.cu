@@ -726,9 +726,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[32];
         load_results<TO>(acc, delta, summed, kbs, c, v);
         if (one <= kMixed) {
-          // (rows and columns that are not there count too: there is only more looked at again)
+          bool finite = true;
+          if (live - c >= 16) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) odd = odd || !(fabsf(v[j]) < INFINITY);
+            for (int j = 0; j < 16; ++j) finite = finite && fabsf(v[j]) < INFINITY;
+          } else {  // (columns behind the last token hold anything)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) finite = finite && (c + j >= live || fabsf(v[j]) < INFINITY);
+          }
+          odd = odd || (!finite && n < g.n_out);
         }
         store_results(g, y, tok0 + c, live - c, n, v);
       }
